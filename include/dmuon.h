@@ -54,7 +54,8 @@ typedef enum dmuon_status {
   DMUON_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (text in dmuon_last_error)  */
   DMUON_ERR_TIMEOUT = 5,     /* a device-side bounded wait gave up (reported by check_status)  */
   DMUON_ERR_NONFINITE = 6,   /* an fp16 intermediate overflowed or became NaN (check_status)   */
-  DMUON_ERR_RANGE = 7        /* checked build only: a device-side range check failed (check_status) */
+  DMUON_ERR_RANGE = 7,       /* checked build only: a device-side range check failed (check_status) */
+  DMUON_ERR_INDEX = 8        /* a token id outside its table or vocabulary (check_status)      */
 } dmuon_status;
 
 typedef enum dmuon_ns_backend {
@@ -64,7 +65,8 @@ typedef enum dmuon_ns_backend {
                           (direct 15 m^2 n + 5 m^3 against Gram 6 m^2 n + 17 m^3), else Gram      */
 } dmuon_ns_backend;
 
-typedef enum dmuon_dtype { DMUON_F32 = 0, DMUON_BF16 = 1 } dmuon_dtype;
+/* DMUON_E4M3 (8-bit floating point, 448 at most) is an output type of dmuon_add_rmsnorm only. */
+typedef enum dmuon_dtype { DMUON_F32 = 0, DMUON_BF16 = 1, DMUON_E4M3 = 2 } dmuon_dtype;
 
 /* Largest number of Newton-Schulz steps accepted (coefficient triples per call). */
 #define DMUON_MAX_STEPS 16
@@ -299,6 +301,91 @@ DMUON_API int dmuon_check_status(void* cuda_stream);
 DMUON_API int dmuon_set_graph_replay(int on);
 
 /*
+ * Token operators: what a training step of a language model runs beside its matrix products, on the
+ * parameters that AdamW updates (embedding table, norm gains, output head). No counterpart on the pages.
+ *
+ * Arrays are row-major with `ld` elements from one row to the next (ld >= the row length; rows of fp32 or
+ * bf16 as the dtype says). Unlike the entry points above they need no more than their elements'
+ * alignment; rows that are 16-byte aligned run faster. Token ids are int32 (id_bytes 4) or int64
+ * (id_bytes 8). n == 0 is a call without tokens. Sums are held in fp32, in an order that depends on the
+ * sizes alone: the same call gives the same bits. Offsets are 64-bit.
+ */
+
+/*
+ * dmuon_embedding -- out[i, :] = scale * table[ids[i], :], i in [0, n).
+ *   table  device, rows x dim, fp32 or bf16          out  device, n x dim, fp32 or bf16
+ * An id outside [0, rows) gives a row of zeros and DMUON_ERR_INDEX at the next dmuon_check_status.
+ */
+DMUON_API int dmuon_embedding(const void* table, int table_dtype, int64_t rows, int64_t dim, int64_t ld_table,
+                              const void* ids, int id_bytes, int64_t n, float scale, void* out, int out_dtype,
+                              int64_t ld_out, void* cuda_stream);
+
+/*
+ * dmuon_embedding_grad -- grad[v, :] (+)= scale * sum over the i with ids[i] == v of grad_out[i, :], the
+ * dense gradient of dmuon_embedding's table.
+ *   grad_out     device, n x dim, fp32 or bf16
+ *   padding_idx  an id whose tokens add nothing (negative: none)
+ *   grad         device, rows x dim, fp32. accumulate == 0: every row is written (zeros where no token
+ *                falls); otherwise the sums are added and the other rows are left alone.
+ * An id outside [0, rows) adds nothing and gives DMUON_ERR_INDEX at the next dmuon_check_status.
+ */
+DMUON_API int dmuon_embedding_grad(const void* grad_out, int grad_dtype, int64_t ld_grad_out, const void* ids,
+                                   int id_bytes, int64_t n, int64_t rows, int64_t dim, float scale,
+                                   int64_t padding_idx, float* grad, int64_t ld_grad, int accumulate,
+                                   void* cuda_stream);
+
+/*
+ * dmuon_add_rmsnorm -- h = x + residual; y = h * (mean over the row of h^2 + eps)^(-1/2) * gain.
+ *   x, residual, h  device, n x dim, `dtype` (fp32 or bf16). residual NULL: h = x. h NULL: not stored. h may
+ *                   be x or residual. The norm is formed from h before its rounding to `dtype`.
+ *   gain            device, dim, fp32; NULL: ones
+ *   y               device, n x dim, y_dtype: `dtype`, or DMUON_E4M3 with scales
+ *   scales          device, n x ceil(dim / group) fp32, or NULL. Columns [k group, (k + 1) group) of a row hold
+ *                   e4m3(y / scales[k]) with scales[k] = max |y| / 448 over them (at least 2^-126; 1 where y
+ *                   is all zeros). group is 32, 64, 128, 256, or 0 for one scale per row.
+ */
+DMUON_API int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype,
+                                const float* gain, int64_t n, int64_t dim, float eps, void* h, int64_t ldh, void* y,
+                                int y_dtype, int64_t ldy, float* scales, int64_t group, void* cuda_stream);
+
+/*
+ * dmuon_add_rmsnorm_grad -- the backward pass at the stored h: with rho = (mean h^2 + eps)^(-1/2) and
+ * d = dy * gain,
+ *   dx = dh + rho d - h rho^3 / dim * sum over the row of d h   (the gradient of x and of residual alike)
+ *   dgain (+)= sum over the rows of dy h rho
+ *   dy, h, dh, dx  device, n x dim, `dtype`; dh (the gradient of the stored h) may be NULL; dx may be dy or dh
+ *   gain, dgain    device, dim, fp32; either may be NULL (ones; not wanted). accumulate != 0 adds to dgain.
+ */
+DMUON_API int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,
+                                     int64_t lddh, int dtype, const float* gain, int64_t n, int64_t dim, float eps,
+                                     void* dx, int64_t lddx, float* dgain, int accumulate, void* cuda_stream);
+
+/*
+ * dmuon_policy_loss -- the clipped policy loss with a KL term, and its gradient, from a model's logits.
+ * Per row t: lp = log softmax(logits / temperature)[targets[t]], r = exp(lp - old_logp[t]),
+ * d = ref_logp[t] - lp,
+ *   l = -min(r A, clip(r, 1 - clip_low, 1 + clip_high) A) + kl_coef (exp(d) - d - 1),   A = advantages[t]
+ *   loss = sum of weights[t] l,    dlogits = d loss / d logits.
+ *   logits, dlogits  device, n x vocab, fp32 or bf16; dlogits may be NULL (loss only) or be logits (ldd == ld)
+ *   old_logp, ref_logp, advantages, weights  device, n, fp32; ref_logp may be NULL when kl_coef is 0
+ *   loss             device, one fp32          logp  device, n, fp32: lp, or NULL
+ * The weights hold the mask and the mean (1 / tokens, say). A row of weight 0, or whose target is negative,
+ * is not read: it adds nothing, its lp is given as 0 and its gradient is zeros. A target >= vocab counts
+ * as one, and gives DMUON_ERR_INDEX at the next dmuon_check_status. Logits of -infinity are tokens of
+ * probability 0; a row that holds NaN or +infinity, or nothing but -infinity, gives NaN.
+ */
+DMUON_API int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab,
+                                const void* targets, int id_bytes, const float* old_logp, const float* ref_logp,
+                                const float* advantages, const float* weights, float clip_low, float clip_high,
+                                float kl_coef, float temperature, float* loss, float* logp, void* dlogits, int64_t ldd,
+                                void* cuda_stream);
+
+/* dmuon_token_logprobs -- logp[t] as in dmuon_policy_loss, alone: old_logp and ref_logp of a policy. */
+DMUON_API int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab,
+                                   const void* targets, int id_bytes, float temperature, float* logp,
+                                   void* cuda_stream);
+
+/*
  * Per-kernel CUDA-event timing (off by default; used by benchmarks). While enabled, the library records
  * a pair of CUDA events on the caller's stream around every kernel it launches. dmuon_timing_read
  * waits for the recorded events, writes per kernel class the summed elapsed milliseconds and the
@@ -309,6 +396,9 @@ DMUON_API int dmuon_set_graph_replay(int on);
  * ms_out and launches_out must each hold DMUON_TIMING_CLASSES entries (host memory).
  */
 #define DMUON_TIMING_CLASSES 6
+/* dmuon_timing_read_launches also reports the token operators, as classes 6 embedding, 7 RMS norm and
+ * 8 policy loss: one record per call. dmuon_timing_read leaves them out. */
+#define DMUON_LAUNCH_CLASSES 9
 DMUON_API int dmuon_timing_enable(int on);
 DMUON_API int dmuon_timing_read(double* ms_out, int64_t* launches_out);
 

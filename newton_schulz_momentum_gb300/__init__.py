@@ -9,7 +9,8 @@ call raises ``LibraryNotBuilt``.
     dm.muon_step(params, grads, momenta, lr=0.02, beta=0.95, coeffs=dm.POLAR_EXPRESS)
 
 The pages' own names -- newton_schulz, NewtonSchulz and the Muon optimizer -- live in
-newton_schulz_momentum_gb300.optim (imports torch) and are reachable here as attributes.
+newton_schulz_momentum_gb300.optim, and the token operators (embedding, residual RMS norm, policy loss) in
+newton_schulz_momentum_gb300.token_ops; both import torch and are reachable here as attributes.
 """
 
 from __future__ import annotations
@@ -41,10 +42,11 @@ YOU = (
 )
 DEFAULT_RESTARTS = (2,)
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OOM, ERR_CUDA, ERR_TIMEOUT, ERR_NONFINITE, ERR_RANGE = range(8)
-_STATUS_NAMES = {1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "OOM", 4: "CUDA", 5: "TIMEOUT", 6: "NONFINITE", 7: "RANGE"}
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OOM, ERR_CUDA, ERR_TIMEOUT, ERR_NONFINITE, ERR_RANGE, ERR_INDEX = range(9)
+_STATUS_NAMES = {1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "OOM", 4: "CUDA", 5: "TIMEOUT", 6: "NONFINITE", 7: "RANGE",
+                 8: "INDEX"}
 BACKENDS = {"direct": 0, "gram": 1, "auto": 2}
-F32, BF16 = 0, 1
+F32, BF16, E4M3 = 0, 1, 2
 
 EXPORTS = (
     "dmuon_ns", "dmuon_muon_step", "dmuon_momentum_normalize", "dmuon_gemm_f16", "dmuon_check_status",
@@ -52,11 +54,13 @@ EXPORTS = (
     "dmuon_release_workspace", "dmuon_timing_enable", "dmuon_timing_read", "dmuon_momentum_normalize_noalloc",
     "dmuon_assign_owners", "dmuon_adamw_step", "dmuon_ns_tp", "dmuon_muon_step_host",
     "dmuon_timing_read_launches", "dmuon_plan_info", "dmuon_selftest_bounded_wait", "dmuon_selftest_range_check",
-    "dmuon_set_graph_replay",
+    "dmuon_set_graph_replay", "dmuon_embedding", "dmuon_embedding_grad", "dmuon_add_rmsnorm",
+    "dmuon_add_rmsnorm_grad", "dmuon_policy_loss", "dmuon_token_logprobs",
 )
 COST_MODELS = {"elements": 0, "gram_flops": 1, "direct_flops": 2}
 NOALLOC_MAX_ELEMS = 268435456
 TIMING_CLASSES = ("momentum_sumsq", "finalize_norms", "normalize_cast", "gemm_tc", "adamw", "tp_reduce")
+LAUNCH_CLASSES = TIMING_CLASSES + ("embedding", "rmsnorm", "policy_loss")
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -110,6 +114,13 @@ def lib():
     L.dmuon_plan_info.argtypes = [ctypes.POINTER(ctypes.c_double), _c_i64p, _c_ip]
     L.dmuon_selftest_bounded_wait.argtypes = [i64, vp]
     L.dmuon_selftest_range_check.argtypes = [vp]
+    L.dmuon_embedding.argtypes = [vp, i32, i64, i64, i64, vp, i32, i64, f32, vp, i32, i64, vp]
+    L.dmuon_embedding_grad.argtypes = [vp, i32, i64, vp, i32, i64, i64, i64, f32, i64, vp, i64, i32, vp]
+    L.dmuon_add_rmsnorm.argtypes = [vp, i64, vp, i64, i32, vp, i64, i64, f32, vp, i64, vp, i32, i64, vp, i64, vp]
+    L.dmuon_add_rmsnorm_grad.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, i64, f32, vp, i64, vp, i32, vp]
+    L.dmuon_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp,
+                                    i64, vp]
+    L.dmuon_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i32, f32, vp, vp]
     for name in EXPORTS:
         if name not in ("dmuon_last_error", "dmuon_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -395,7 +406,7 @@ def timing_read_launches(max_launches=4096):
     cls = (ctypes.c_int * max_launches)()
     n = ctypes.c_int()
     _check(lib().dmuon_timing_read_launches(max_launches, ms, cls, ctypes.byref(n)))
-    return [(TIMING_CLASSES[cls[i]] if 0 <= cls[i] < len(TIMING_CLASSES) else str(cls[i]), ms[i])
+    return [(LAUNCH_CLASSES[cls[i]] if 0 <= cls[i] < len(LAUNCH_CLASSES) else str(cls[i]), ms[i])
             for i in range(min(n.value, max_launches))]
 
 
@@ -476,10 +487,18 @@ def direct_flops(m, n, steps=5, dense=False):
     return steps * ((h + 2) * m * m * n + h * m ** 3)
 
 
+_TOKEN_OPS = ("embedding", "embedding_grad", "add_rmsnorm", "add_rmsnorm_fp8", "add_rmsnorm_grad", "policy_loss",
+              "token_logprobs")
+
+
 def __getattr__(name):
-    """newton_schulz, NewtonSchulz, Muon and default_muon_filter load from .optim on first use (it imports
-    torch; this module does not)."""
+    """newton_schulz, NewtonSchulz, Muon and default_muon_filter load from .optim, and the token operators from
+    .token_ops, on first use (they import torch; this module does not)."""
     if name in ("newton_schulz", "NewtonSchulz", "Muon", "default_muon_filter"):
         from . import optim
         return getattr(optim, name)
+    if name in _TOKEN_OPS:
+        from . import token_ops
+        globals().update((op, getattr(token_ops, op)) for op in _TOKEN_OPS)
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdmuon.so")
 CHECKED_LIB = os.path.join(PKG, "libdmuon_checked.so")
-SOURCES = ("api.cu", "gemm_tc.cu", "ns_small.cu", "rowwise.cu", "adamw.cu", "noalloc.cu", "partition.cpp")
+SOURCES = ("api.cu", "gemm_tc.cu", "ns_small.cu", "rowwise.cu", "adamw.cu", "noalloc.cu", "embedding.cu", "rmsnorm.cu",
+           "policy_loss.cu", "partition.cpp")
 ARCH = ("-gencode", "arch=compute_103a,code=sm_103a")
 # (library, object directory, extra flags)
 VARIANTS = ((LIB, BUILD_DIR, ()), (CHECKED_LIB, os.path.join(BUILD_DIR, "checked"), ("-DDMUON_DEVICE_CHECKS=1",)))

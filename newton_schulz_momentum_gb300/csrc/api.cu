@@ -210,6 +210,8 @@ struct DeviceState {
   char* gather_buf = nullptr;
   size_t gather_bytes = 0;
   int64_t gather_chunks = 0;
+  char* token_buf = nullptr;  // scratch of the token operators
+  size_t token_bytes = 0;
 };
 
 std::mutex g_mu;
@@ -239,10 +241,13 @@ cudaEvent_t take_event() {
   return e;
 }
 
-// Names of the timing classes (dmuon.h), also the NVTX range names of their launches.
-const char* const kClassNames[DMUON_TIMING_CLASSES] = {"dmuon momentum_sumsq", "dmuon finalize_norms",
+// Names of the launch classes (dmuon.h), also the NVTX range names of their launches.
+enum { kClsEmbedding = 6, kClsRmsNorm = 7, kClsPolicy = 8 };
+const char* const kClassNames[DMUON_LAUNCH_CLASSES] = {"dmuon momentum_sumsq", "dmuon finalize_norms",
                                                         "dmuon normalize_cast", "dmuon gemm_tc",
-                                                        "dmuon adamw",          "dmuon tp_reduce"};
+                                                        "dmuon adamw",          "dmuon tp_reduce",
+                                                        "dmuon embedding",      "dmuon rmsnorm",
+                                                        "dmuon policy_loss"};
 
 // Records events around one launch when timing is on (and an NVTX range around its host-side enqueue, for
 // a profiler's timeline); otherwise just launches.
@@ -1203,6 +1208,85 @@ int check_matrix_list(int count, const int64_t* rows, const int64_t* cols) {
   return DMUON_OK;
 }
 
+// ---------------------------------------------------------------------------- token operators: shared checks
+
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 1;
+
+bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+int check_token_sizes(int64_t n, int64_t dim, const char* dim_name) {
+  if (n < 0 || n > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "n must be in [0, 2^31 - 1], got %lld", (long long)n);
+  if (dim < 1) return fail(DMUON_ERR_INVALID_ARG, "%s must be >= 1, got %lld", dim_name, (long long)dim);
+  if (dim > kMaxDim) return fail(DMUON_ERR_UNSUPPORTED, "%s is larger than %lld", dim_name, (long long)kMaxDim);
+  return DMUON_OK;
+}
+
+int check_ids(const void* ids, int id_bytes, int64_t n) {
+  if (id_bytes != 4 && id_bytes != 8) return fail(DMUON_ERR_INVALID_ARG, "id_bytes must be 4 or 8, got %d", id_bytes);
+  if (n > 0 && !ids) return fail(DMUON_ERR_INVALID_ARG, "the token ids are NULL");
+  if (!aligned_to(ids, static_cast<uintptr_t>(id_bytes)))
+    return fail(DMUON_ERR_INVALID_ARG, "the token ids must be aligned to their type");
+  return DMUON_OK;
+}
+
+// A row-major fp32 or bf16 array of n rows of `dim` elements, `ld` elements apart.
+int check_elements(const char* name, const void* ptr, int dtype, int64_t ld, int64_t dim, int64_t n) {
+  if (dtype != DMUON_F32 && dtype != DMUON_BF16)
+    return fail(DMUON_ERR_INVALID_ARG, "the dtype of %s must be DMUON_F32 (0) or DMUON_BF16 (1), got %d", name, dtype);
+  if (n > 0 && !ptr) return fail(DMUON_ERR_INVALID_ARG, "%s must not be NULL", name);
+  if (!aligned_to(ptr, dtype == DMUON_F32 ? 4 : 2))
+    return fail(DMUON_ERR_INVALID_ARG, "%s must be aligned to its elements", name);
+  if (ld < dim)
+    return fail(DMUON_ERR_INVALID_ARG, "the leading dimension of %s is smaller than its row length", name);
+  return DMUON_OK;
+}
+
+// The token operators' scratch, `bytes` long, grown when a call needs more.
+int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** out) {
+  const size_t need = static_cast<size_t>(bytes);
+  if (g_ws_limit && need > g_ws_limit)
+    return fail(DMUON_ERR_OOM, "workspace of %zu bytes exceeds the limit of %zu", need, g_ws_limit);
+  if (need > ds.token_bytes) {
+    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+    DM_CUDA(cudaStreamIsCapturing(stream, &capturing), "cudaStreamIsCapturing");
+    if (capturing != cudaStreamCaptureStatusNone)
+      return fail(DMUON_ERR_OOM, "the workspace must grow to %zu bytes, which a capture cannot hold: make this call "
+                                 "once before capturing it", need);
+    DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize before growing the workspace");
+    if (ds.token_buf) cudaFree(ds.token_buf);
+    ds.token_buf = nullptr;
+    ds.token_bytes = 0;
+    // Half as much again, so that a slowly growing batch does not reallocate at every call.
+    size_t get = std::max<size_t>(need + need / 2, size_t(1) << 20);
+    if (g_ws_limit) get = std::min(get, g_ws_limit);
+    if (cudaMalloc(&ds.token_buf, get) != cudaSuccess) {
+      cudaGetLastError();
+      ds.token_buf = nullptr;
+      return fail(DMUON_ERR_OOM, "cudaMalloc of %zu bytes of workspace failed", get);
+    }
+    ds.token_bytes = get;
+  }
+  *out = ds.token_buf;
+  return DMUON_OK;
+}
+
+// The launches of dmuon_policy_loss and dmuon_token_logprobs (p.loss null). Called with g_mu held.
+int run_policy(PolicyLaunch& p, cudaStream_t stream) {
+  DeviceState* ds = nullptr;
+  int st = current_device(&ds);
+  if (st != DMUON_OK || (p.n == 0 && !p.loss)) return st;
+  p.row_loss = nullptr;
+  if (p.loss) {
+    char* ws = nullptr;
+    st = token_workspace(*ds, p.n * static_cast<int64_t>(sizeof(float)), stream, &ws);
+    if (st != DMUON_OK) return st;
+    p.row_loss = reinterpret_cast<float*>(ws);
+  }
+  p.status = ds->status;
+  DM_CUDA(timed(kClsPolicy, stream, [&] { return launch_policy(p, stream); }), "policy loss launch");
+  return DMUON_OK;
+}
+
 }  // namespace
 
 int set_error(int status, const char* message) { return fail(status, "%s", message); }
@@ -1473,6 +1557,8 @@ int dmuon_check_status(void* cuda_stream) {
   if (word & kDevRange)
     return fail(DMUON_ERR_RANGE, "a device-side range check failed (checked build): an index or tile outside its "
                                  "table or matrix was skipped; results are invalid");
+  if (word & kDevIndex)
+    return fail(DMUON_ERR_INDEX, "a token id lies outside its table or vocabulary; its row was skipped");
   if (word & kDevNonfinite) return fail(DMUON_ERR_NONFINITE, "an fp16 intermediate overflowed or was NaN");
   return DMUON_OK;
 }
@@ -1568,6 +1654,187 @@ int dmuon_adamw_step(int count, float* const* params, const void* const* grads, 
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
   }
+}
+
+// ---------------------------------------------------------------------------- token operators
+
+int dmuon_embedding(const void* table, int table_dtype, int64_t rows, int64_t dim, int64_t ld_table, const void* ids,
+                    int id_bytes, int64_t n, float scale, void* out, int out_dtype, int64_t ld_out, void* cuda_stream) {
+  int st = check_token_sizes(n, dim, "dim");
+  if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
+  if (st == DMUON_OK) st = check_elements("table", table, table_dtype, ld_table, dim, rows);
+  if (st == DMUON_OK) st = check_elements("out", out, out_dtype, ld_out, dim, n);
+  if (st != DMUON_OK) return st;
+  if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
+  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* ds = nullptr;
+  st = current_device(&ds);
+  if (st != DMUON_OK || n == 0) return st;
+  EmbeddingLaunch p;
+  p.table = table, p.table_dtype = table_dtype, p.out_dtype = out_dtype;
+  p.rows = rows, p.dim = dim, p.ld_table = ld_table;
+  p.ids = ids, p.id_bytes = id_bytes, p.n = n;
+  p.scale = scale, p.out = out, p.ld_out = ld_out;
+  p.status = ds->status;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding(p, stream); }), "embedding launch");
+  return DMUON_OK;
+}
+
+int dmuon_embedding_grad(const void* grad_out, int grad_dtype, int64_t ld_grad_out, const void* ids, int id_bytes,
+                         int64_t n, int64_t rows, int64_t dim, float scale, int64_t padding_idx, float* grad,
+                         int64_t ld_grad, int accumulate, void* cuda_stream) {
+  int st = check_token_sizes(n, dim, "dim");
+  if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
+  if (st == DMUON_OK) st = check_elements("grad_out", grad_out, grad_dtype, ld_grad_out, dim, n);
+  if (st == DMUON_OK) st = check_elements("grad", grad, DMUON_F32, ld_grad, dim, rows);
+  if (st != DMUON_OK) return st;
+  if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
+  if (padding_idx >= rows) return fail(DMUON_ERR_INVALID_ARG, "padding_idx must be below rows (negative: none)");
+  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* ds = nullptr;
+  st = current_device(&ds);
+  if (st != DMUON_OK || (n == 0 && accumulate)) return st;
+  EmbeddingGradLaunch p;
+  p.grad_out = grad_out, p.grad_dtype = grad_dtype, p.ld_grad_out = ld_grad_out;
+  p.ids = ids, p.id_bytes = id_bytes;
+  p.n = n, p.rows = rows, p.dim = dim;
+  p.scale = scale, p.padding_idx = padding_idx;
+  p.grad = grad, p.ld_grad = ld_grad, p.accumulate = accumulate != 0;
+  p.status = ds->status;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding_grad(p, stream); }), "embedding gradient launch");
+  return DMUON_OK;
+}
+
+int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, const float* gain,
+                      int64_t n, int64_t dim, float eps, void* h, int64_t ldh, void* y, int y_dtype, int64_t ldy,
+                      float* scales, int64_t group, void* cuda_stream) {
+  int st = check_token_sizes(n, dim, "dim");
+  if (st == DMUON_OK) st = check_elements("x", x, dtype, ldx, dim, n);
+  if (st == DMUON_OK && residual) st = check_elements("residual", residual, dtype, ldr, dim, n);
+  if (st == DMUON_OK && h) st = check_elements("h", h, dtype, ldh, dim, n);
+  if (st != DMUON_OK) return st;
+  if (y_dtype == DMUON_E4M3) {
+    if (n > 0 && (!y || !scales)) return fail(DMUON_ERR_INVALID_ARG, "y and scales must not be NULL");
+    if (ldy < dim) return fail(DMUON_ERR_INVALID_ARG, "the leading dimension of y is smaller than its row length");
+    if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+      return fail(DMUON_ERR_INVALID_ARG, "group must be 32, 64, 128, 256 or 0 (one scale per row), got %lld",
+                  (long long)group);
+    if (!aligned_to(scales, 4)) return fail(DMUON_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+  } else {
+    if (y_dtype != dtype) return fail(DMUON_ERR_INVALID_ARG, "y_dtype must be dtype or DMUON_E4M3 (2)");
+    if (scales) return fail(DMUON_ERR_INVALID_ARG, "scales must be NULL unless y_dtype is DMUON_E4M3 (2)");
+    st = check_elements("y", y, dtype, ldy, dim, n);
+    if (st != DMUON_OK) return st;
+  }
+  if (!aligned_to(gain, 4)) return fail(DMUON_ERR_INVALID_ARG, "gain must be 4-byte aligned");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DMUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState* ds = nullptr;
+  st = current_device(&ds);
+  if (st != DMUON_OK || n == 0) return st;
+  RmsNormLaunch p;
+  p.x = x, p.residual = residual, p.dtype = dtype, p.ldx = ldx, p.ldr = ldr;
+  p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
+  p.h = h, p.ldh = ldh, p.y = y, p.ldy = ldy;
+  p.scales = y_dtype == DMUON_E4M3 ? scales : nullptr, p.group = group;
+  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+  DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm(p, stream); }), "RMS norm launch");
+  return DMUON_OK;
+}
+
+int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh, int64_t lddh,
+                           int dtype, const float* gain, int64_t n, int64_t dim, float eps, void* dx, int64_t lddx,
+                           float* dgain, int accumulate, void* cuda_stream) {
+  try {
+    int st = check_token_sizes(n, dim, "dim");
+    if (st == DMUON_OK) st = check_elements("dy", dy, dtype, lddy, dim, n);
+    if (st == DMUON_OK) st = check_elements("h", h, dtype, ldh, dim, n);
+    if (st == DMUON_OK && dh) st = check_elements("dh", dh, dtype, lddh, dim, n);
+    if (st == DMUON_OK) st = check_elements("dx", dx, dtype, lddx, dim, n);
+    if (st != DMUON_OK) return st;
+    if (!aligned_to(gain, 4) || !aligned_to(dgain, 4))
+      return fail(DMUON_ERR_INVALID_ARG, "gain and dgain must be 4-byte aligned");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DMUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    if (n == 0) {
+      if (dgain && !accumulate)
+        DM_CUDA(cudaMemsetAsync(dgain, 0, static_cast<size_t>(dim) * sizeof(float), stream), "zero dgain");
+      return DMUON_OK;
+    }
+    RmsNormGradLaunch p;
+    p.dy = dy, p.h = h, p.dh = dh, p.dtype = dtype;
+    p.lddy = lddy, p.ldh = ldh, p.lddh = lddh;
+    p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
+    p.dx = dx, p.lddx = lddx, p.dgain = dgain, p.accumulate = accumulate != 0;
+    char* ws = nullptr;
+    st = token_workspace(*ds, rmsnorm_grad_workspace(n, dim), stream, &ws);
+    if (st != DMUON_OK) return st;
+    p.rho = reinterpret_cast<float*>(ws);
+    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm_grad(p, stream); }), "RMS norm gradient launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab, const void* targets,
+                      int id_bytes, const float* old_logp, const float* ref_logp, const float* advantages,
+                      const float* weights, float clip_low, float clip_high, float kl_coef, float temperature,
+                      float* loss, float* logp, void* dlogits, int64_t ldd, void* cuda_stream) {
+  int st = check_token_sizes(n, vocab, "vocab");
+  if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
+  if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+  if (st == DMUON_OK && dlogits) st = check_elements("dlogits", dlogits, dtype, ldd, vocab, n);
+  if (st != DMUON_OK) return st;
+  if (!loss || (n > 0 && (!old_logp || !advantages || !weights)))
+    return fail(DMUON_ERR_INVALID_ARG, "old_logp, advantages, weights and loss must not be NULL");
+  for (const void* v : {static_cast<const void*>(old_logp), static_cast<const void*>(ref_logp),
+                        static_cast<const void*>(advantages), static_cast<const void*>(weights),
+                        static_cast<const void*>(loss), static_cast<const void*>(logp)})
+    if (!aligned_to(v, 4)) return fail(DMUON_ERR_INVALID_ARG, "fp32 vectors must be 4-byte aligned");
+  if (!(clip_low >= 0.f) || !(clip_high >= 0.f) || !std::isfinite(clip_low) || !std::isfinite(clip_high))
+    return fail(DMUON_ERR_INVALID_ARG, "clip_low and clip_high must be finite and >= 0");
+  if (!std::isfinite(kl_coef)) return fail(DMUON_ERR_INVALID_ARG, "kl_coef must be finite");
+  if (kl_coef != 0.f && n > 0 && !ref_logp)
+    return fail(DMUON_ERR_INVALID_ARG, "ref_logp must not be NULL with a kl_coef other than 0");
+  if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
+    return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
+  std::lock_guard<std::mutex> lock(g_mu);
+  PolicyLaunch p;
+  p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+  p.targets = targets, p.id_bytes = id_bytes;
+  p.old_logp = old_logp, p.ref_logp = kl_coef != 0.f ? ref_logp : nullptr;
+  p.advantages = advantages, p.weights = weights;
+  p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.temperature = temperature;
+  p.loss = loss, p.logp = logp, p.dlogits = dlogits, p.ldd = ldd;
+  return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+}
+
+int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab, const void* targets,
+                         int id_bytes, float temperature, float* logp, void* cuda_stream) {
+  int st = check_token_sizes(n, vocab, "vocab");
+  if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
+  if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+  if (st != DMUON_OK) return st;
+  if (n > 0 && (!logp || !aligned_to(logp, 4)))
+    return fail(DMUON_ERR_INVALID_ARG, "logp must not be NULL and must be 4-byte aligned");
+  if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
+    return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
+  std::lock_guard<std::mutex> lock(g_mu);
+  PolicyLaunch p;
+  std::memset(&p, 0, sizeof(p));
+  p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+  p.targets = targets, p.id_bytes = id_bytes;
+  p.temperature = temperature, p.logp = logp;
+  return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
 }
 
 int dmuon_set_graph_replay(int on) {
@@ -1754,6 +2021,12 @@ int dmuon_release_workspace(void) {
   ds.gather_bytes = 0;
   ds.gather_key.clear();
   ds.gather_ok = false;
+  if (ds.token_buf) {
+    DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
+    DM_CUDA(cudaFree(ds.token_buf), "cudaFree(token workspace)");
+  }
+  ds.token_buf = nullptr;
+  ds.token_bytes = 0;
   return DMUON_OK;
 }
 

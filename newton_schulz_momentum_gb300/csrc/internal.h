@@ -15,6 +15,7 @@ enum : unsigned {
   kDevTimeout = 1u,    // a bounded mbarrier wait gave up; the launch's results are invalid
   kDevNonfinite = 2u,  // an fp16 store overflowed or was NaN
   kDevRange = 4u,      // checked build: an index or tile outside its table or matrix was skipped
+  kDevIndex = 8u,      // a token id outside its table or vocabulary was skipped
 };
 
 // Device-side range checks: compiled in with -DDMUON_DEVICE_CHECKS=1 (the checked build,
@@ -297,6 +298,93 @@ cudaError_t launch_momentum_sumsq(const RowLaunch& p, int64_t nchunks, cudaStrea
 // the preceding grid themselves). The bulk momentum kernel (RowLaunch.status set) always is.
 cudaError_t launch_finalize_norms(const RowLaunch& p, cudaStream_t stream, bool programmatic = false);
 cudaError_t launch_normalize_cast(const RowLaunch& p, int64_t ntiles, cudaStream_t stream, bool programmatic = false);
+
+// ------------------------------------------------------------------------------------------------
+// Token operators: embedding lookup and gradient (embedding.cu), residual addition with RMS norm
+// (rmsnorm.cu), policy loss from logits (policy_loss.cu). Element types: 0 fp32, 1 bf16, 2 e4m3. Leading
+// dimensions count elements. Buffers need their element type's alignment only.
+// ------------------------------------------------------------------------------------------------
+
+struct EmbeddingLaunch {
+  const void* table;
+  int table_dtype, out_dtype;
+  int64_t rows, dim, ld_table;
+  const void* ids;
+  int id_bytes;
+  int64_t n;
+  float scale;
+  void* out;
+  int64_t ld_out;
+  unsigned* status;
+};
+cudaError_t launch_embedding(const EmbeddingLaunch& p, cudaStream_t stream);
+
+struct EmbeddingGradLaunch {
+  const void* grad_out;
+  int grad_dtype;
+  int64_t ld_grad_out;
+  const void* ids;
+  int id_bytes;
+  int64_t n, rows, dim;
+  float scale;
+  int64_t padding_idx;  // negative: none
+  float* grad;
+  int64_t ld_grad;
+  int accumulate;
+  unsigned* status;
+};
+cudaError_t launch_embedding_grad(const EmbeddingGradLaunch& p, cudaStream_t stream);
+
+struct RmsNormLaunch {
+  const void* x;
+  const void* residual;  // may be null
+  int dtype;             // of x, residual and h (and of y without scales)
+  int64_t ldx, ldr;
+  const float* gain;  // may be null
+  int64_t n, dim;
+  float eps;
+  void* h;  // may be null
+  int64_t ldh;
+  void* y;
+  int64_t ldy;
+  float* scales;  // e4m3 output: n x ceil(dim / group), null otherwise
+  int64_t group;  // columns per scale; 0: the whole row
+};
+cudaError_t launch_add_rmsnorm(const RmsNormLaunch& p, cudaStream_t stream);
+
+struct RmsNormGradLaunch {
+  const void *dy, *h, *dh;  // dh may be null
+  int dtype;                // of dy, h, dh and dx
+  int64_t lddy, ldh, lddh;
+  const float* gain;  // may be null
+  int64_t n, dim;
+  float eps;
+  void* dx;
+  int64_t lddx;
+  float* dgain;  // may be null
+  int accumulate;
+  float* rho;  // workspace: rmsnorm_grad_workspace(n, dim) bytes
+};
+int64_t rmsnorm_grad_workspace(int64_t n, int64_t dim);
+cudaError_t launch_add_rmsnorm_grad(const RmsNormGradLaunch& p, cudaStream_t stream);
+
+struct PolicyLaunch {
+  const void* logits;
+  int dtype;  // of logits and dlogits
+  int64_t ld, n, vocab;
+  const void* targets;
+  int id_bytes;
+  const float *old_logp, *ref_logp, *advantages;  // ref_logp may be null: no KL term
+  const float* weights;                           // null: log-probabilities only
+  float clip_low, clip_high, kl_coef, temperature;
+  float* loss;      // null: log-probabilities only
+  float* row_loss;  // workspace, n entries
+  float* logp;      // may be null
+  void* dlogits;    // may be null
+  int64_t ldd;
+  unsigned* status;
+};
+cudaError_t launch_policy(const PolicyLaunch& p, cudaStream_t stream);
 
 // Record `message` as the calling thread's last error (returned by dmuon_last_error) and return status.
 int set_error(int status, const char* message);
