@@ -1705,7 +1705,12 @@ int dmuon_embedding_grad(const void* grad_out, int grad_dtype, int64_t ld_grad_o
   p.grad = grad, p.ld_grad = ld_grad, p.accumulate = accumulate != 0;
   p.status = ds->status;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding_grad(p, stream); }), "embedding gradient launch");
+  char* ws = nullptr;
+  st = token_workspace(*ds, embedding_grad_workspace(p, nullptr), stream, &ws);
+  if (st != DMUON_OK) return st;
+  embedding_grad_workspace(p, ws);
+  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding_grad(p, ds->sms, stream); }),
+          "embedding gradient launch");
   return DMUON_OK;
 }
 

@@ -332,8 +332,20 @@ struct EmbeddingGradLaunch {
   int64_t ld_grad;
   int accumulate;
   unsigned* status;
+  // Set by embedding_grad_workspace.
+  int64_t chunk_len, chunks;  // the sorted tokens are summed in `chunks` runs of chunk_len
+  uint2* sorted[2];           // (id, position) of every token by id; the sort ends in sorted[0]
+  int* chunk_state;
+  float* partials;            // two rows of ld_partials per chunk
+  int64_t ld_partials;
+  uint2* crossing;            // (first chunk, id) of the rows that cross chunks
+  unsigned* crossing_count;
+  // Set by launch_embedding_grad.
+  int passes, digit_bits, vec_grad, tpr;
 };
-cudaError_t launch_embedding_grad(const EmbeddingGradLaunch& p, cudaStream_t stream);
+// Workspace bytes; with `ws` it also places the buffers there.
+int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws);
+cudaError_t launch_embedding_grad(EmbeddingGradLaunch& p, int sms, cudaStream_t stream);
 
 struct RmsNormLaunch {
   const void* x;

@@ -19,6 +19,21 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// 16 bytes of elements as floats (4 fp32 or 8 bf16), read past L1.
+__device__ __forceinline__ void load16(float (&v)[4], const float* src) {
+  const float4 u = __ldcs(reinterpret_cast<const float4*>(src));
+  v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+}
+__device__ __forceinline__ void load16(float (&v)[8], const __nv_bfloat16* src) {
+  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+  }
+}
+
 // Token id `i` of an int32 or int64 list.
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<int64_t>(static_cast<const int*>(ids)[i]);
@@ -35,6 +50,23 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   v = (threadIdx.x & 31) < nwarps ? red[threadIdx.x & 31] : 0.f;
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Launches `kernel`, which waits for the preceding grid itself (griddepcontrol.wait), with programmatic stream
+// serialisation: its CTAs may be set up while that grid drains.
+template <typename P>
+cudaError_t launch(void (*kernel)(const P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace row
