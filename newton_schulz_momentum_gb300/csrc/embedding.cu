@@ -3,8 +3,8 @@
 //
 // The gradient takes four launches:
 //   1. one cluster sorts the tokens by id (stable);
-//   2. meanwhile, on the other SMs, the table rows that no token falls on are written with zeros, which at a
-//      language model's sizes is most of the bytes (not run where the caller adds to the gradient);
+//   2. meanwhile, on the other SMs, the table is filled with zeros, which at a language model's sizes is most
+//      of the bytes (not run where the caller adds to the gradient);
 //   3. the sorted list is cut into chunks of equal length, whatever the ids' frequencies: a CTA adds a
 //      chunk's rows and writes each table row that begins and ends inside it; a row that crosses a chunk's
 //      border leaves its sum over the chunk in the workspace;
@@ -19,16 +19,62 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename TI, typename TO>
+// ---------------------------------------------------------------------------- lookup
+
+constexpr int kLookup = 8;  // columns of a thread at a time: consecutive (VEC), or tpr apart
+
+// Eight consecutive elements by 16-byte loads and stores.
+__device__ __forceinline__ void load8(float (&v)[8], const float* src) {
+  float lo[4], hi[4];
+  row::unpack16<float>(lo, __ldg(reinterpret_cast<const uint4*>(src)));
+  row::unpack16<float>(hi, __ldg(reinterpret_cast<const uint4*>(src) + 1));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = lo[k], v[k + 4] = hi[k];
+}
+__device__ __forceinline__ void load8(float (&v)[8], const __nv_bfloat16* src) {
+  row::unpack16<__nv_bfloat16>(v, __ldg(reinterpret_cast<const uint4*>(src)));
+}
+__device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
+  __stcs(reinterpret_cast<float4*>(dst), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(dst) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) {
+  __stcs(reinterpret_cast<uint4*>(dst), row::pack16(v));
+}
+
+// `tpr` threads per token. Bound by memory: each row is read once (a row that several tokens name comes from
+// L2 again) and the output is written once.
+template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaunch p) {
-  const int64_t i = blockIdx.x;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tpr = p.tpr, t = threadIdx.x % tpr;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr;
+  if (i >= p.n) return;
   const int64_t id = row::load_id(p.ids, p.id_bytes, i);
   const bool ok = id >= 0 && id < p.rows;
-  if (!ok && threadIdx.x == 0) atomicOr(p.status, kDevIndex);
+  if (!ok && t == 0) atomicOr(p.status, kDevIndex);
   const TI* src = static_cast<const TI*>(p.table) + (ok ? id : 0) * p.ld_table;
   TO* dst = static_cast<TO*>(p.out) + i * p.ld_out;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads)
-    dst[c] = row::from_f<TO>(ok ? p.scale * row::to_f(src[c]) : 0.f);
+  const float scale = p.scale;
+  for (int64_t c0 = 0; c0 < p.dim; c0 += tpr * kLookup) {
+    float v[kLookup];
+    const int64_t c = c0 + (VEC ? t * kLookup : t);
+    if constexpr (VEC) {
+      if (c < p.dim) {
+        load8(v, src + c);
+#pragma unroll
+        for (int k = 0; k < kLookup; ++k) v[k] = ok ? scale * v[k] : 0.f;
+        store8(dst + c, v);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kLookup; ++k) v[k] = c + k * tpr < p.dim ? row::to_f(__ldg(src + c + k * tpr)) : 0.f;
+#pragma unroll
+      for (int k = 0; k < kLookup; ++k)
+        if (c + k * tpr < p.dim) dst[c + k * tpr] = row::from_f<TO>(ok ? scale * v[k] : 0.f);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------- 1. sort
@@ -151,37 +197,33 @@ __global__ void __cluster_dims__(kSortCtas) __launch_bounds__(kSortThreads, 1)
   sort_tokens(p, smem);
 }
 
-// ---------------------------------------------------------------------------- 2. rows without tokens
+// ---------------------------------------------------------------------------- 2. zeros
 
 constexpr int kZeroThreads = 512;
-constexpr int kMarkWords = 8192;  // a CTA marks the rows with tokens in a bitmap over 2^18 of its rows at a time
+constexpr int kZeroPer = 2;  // 16-byte stores of a thread
+constexpr int64_t kZeroBlock = int64_t(kZeroThreads) * kZeroPer * 4;  // elements of a CTA
 
+// One short CTA per 16 KB of the table. They start in the order of the addresses, so the stores in flight stay
+// close together: 2.1 GB take 270 us (7.8 TB/s), against 312-323 us for CTAs that stay and walk over it.
 __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const EmbeddingGradLaunch p) {
-  __shared__ uint32_t marks[kMarkWords];
   ptx::griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t begin = p.rows * blockIdx.x / gridDim.x, end = p.rows * (blockIdx.x + 1) / gridDim.x;
-  for (int64_t r0 = begin; r0 < end; r0 += kMarkWords * 32) {
-    const int here = static_cast<int>(min(static_cast<int64_t>(kMarkWords) * 32, end - r0));
-    for (int k = threadIdx.x; k < (here + 31) / 32; k += kZeroThreads) marks[k] = 0;
-    __syncthreads();
-    for (int64_t i = threadIdx.x; i < p.n; i += kZeroThreads) {
-      const int64_t at = static_cast<int64_t>(sort_key(p, i)) - r0;
-      if (at >= 0 && at < here) atomicOr(marks + (at >> 5), 1u << (at & 31));
+  // Rows that follow one another are one long row.
+  const bool flat = p.ld_grad == p.dim;
+  const int64_t len = flat ? p.rows * p.dim : p.dim;
+  const int64_t blocks = (len + kZeroBlock - 1) / kZeroBlock;
+  const int64_t begin = blockIdx.x % blocks * kZeroBlock, end = min(begin + kZeroBlock, len);
+  float* dst = p.grad + blockIdx.x / blocks * p.ld_grad;
+  if (p.vec_grad) {
+#pragma unroll
+    for (int k = 0; k < kZeroPer; ++k) {
+      const int64_t c = begin + (k * kZeroThreads + threadIdx.x) * 4;
+      if (c + 4 <= end)
+        __stcs(reinterpret_cast<float4*>(dst + c), make_float4(0.f, 0.f, 0.f, 0.f));
+      else
+        for (int64_t e = c; e < end; ++e) dst[e] = 0.f;
     }
-    __syncthreads();
-    for (int r = warp; r < here; r += kZeroThreads / 32) {
-      if (marks[r >> 5] >> (r & 31) & 1) continue;
-      float* dst = p.grad + (r0 + r) * p.ld_grad;
-      int64_t c = lane;
-      if (p.vec_grad) {
-        float4* dst4 = reinterpret_cast<float4*>(dst);
-        for (; c < p.dim / 4; c += 32) __stcs(dst4 + c, make_float4(0.f, 0.f, 0.f, 0.f));
-        c = p.dim / 4 * 4 + lane;
-      }
-      for (; c < p.dim; c += 32) __stcs(dst + c, 0.f);
-    }
-    __syncthreads();
+  } else {
+    for (int64_t c = begin + threadIdx.x; c < end; c += kZeroThreads) __stcs(dst + c, 0.f);
   }
   // The next launch waits for this one, and needs the sort's result.
   ptx::griddep_wait();
@@ -189,22 +231,39 @@ __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const Embe
 
 // ---------------------------------------------------------------------------- 3. sums by chunk
 
-// A group of `tpr` threads adds the rows of one chunk over tpr * COLS consecutive columns.
-// VEC: a thread's COLS columns are one 16-byte load; otherwise they lie tpr apart.
+// A group of `tpr` threads adds the rows of one chunk over tpr * kCols consecutive columns. With 16-byte rows
+// (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise its columns lie tpr apart.
 template <typename TG, bool VEC>
-struct ChunkColumns {
-  static constexpr int kCols = VEC ? 16 / sizeof(TG) : 4;
+struct Columns;
+
+template <typename TG>
+struct Columns<TG, true> {
+  static constexpr int kCols = 16 / sizeof(TG);
+  uint4 raw;
+  __device__ __forceinline__ void load(const TG* src, int64_t col, int, int64_t) {
+    raw = __ldcs(reinterpret_cast<const uint4*>(src + col));
+  }
+  __device__ __forceinline__ void add_to(float (&acc)[kCols]) const {
+    float v[kCols];
+    row::unpack16<TG>(v, raw);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] += v[k];
+  }
 };
 
-template <typename TG, bool VEC, int COLS>
-__device__ __forceinline__ void load_columns(float (&v)[COLS], const TG* src, int64_t col, int tpr, int64_t dim) {
-  if constexpr (VEC) {
-    row::load16(v, src + col);
-  } else {
+template <typename TG>
+struct Columns<TG, false> {
+  static constexpr int kCols = 8;
+  TG raw[kCols];
+  __device__ __forceinline__ void load(const TG* src, int64_t col, int tpr, int64_t dim) {
 #pragma unroll
-    for (int k = 0; k < COLS; ++k) v[k] = col + k * tpr < dim ? row::to_f(__ldcs(src + col + k * tpr)) : 0.f;
+    for (int k = 0; k < kCols; ++k) raw[k] = col + k * tpr < dim ? __ldcs(src + col + k * tpr) : row::from_f<TG>(0.f);
   }
-}
+  __device__ __forceinline__ void add_to(float (&acc)[kCols]) const {
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) acc[k] += row::to_f(raw[k]);
+  }
+};
 
 // dst = scale * acc, or dst += scale * acc.
 template <bool VEC, int COLS>
@@ -230,11 +289,12 @@ __device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COL
   }
 }
 
-constexpr int kAhead = 4;  // rows in flight per thread
+constexpr int kAhead = 4;  // rows in flight per thread, while as many are added
 
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const EmbeddingGradLaunch p) {
-  constexpr int COLS = ChunkColumns<TG, VEC>::kCols;
+  using Cols = Columns<TG, VEC>;
+  constexpr int COLS = Cols::kCols;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tpr = p.tpr, groups = kThreads / tpr;
@@ -242,29 +302,40 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
   if (chunk >= p.chunks) return;
   const int t = threadIdx.x % tpr;
   const int64_t col = static_cast<int64_t>(blockIdx.y) * tpr * COLS + (VEC ? t * COLS : t);
+  const bool active = col < p.dim;
   const bool first_slice = blockIdx.y == 0 && t == 0;
   const uint2* tokens = p.sorted[0];
   const int64_t begin = chunk * p.chunk_len, end = min(begin + p.chunk_len, p.n);
   const uint32_t none = static_cast<uint32_t>(p.rows);
+  const TG* src = static_cast<const TG*>(p.grad_out);
+  // Two batches of rows: one is on its way while the other is added. Tokens that add nothing sort behind
+  // every row; their rows are not read.
+  uint2 tok[2][kAhead];
+  Cols val[2][kAhead];
+  auto fetch_tokens = [&](uint2 (&to)[kAhead], int64_t i) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) to[a] = i + a < end ? __ldcg(tokens + i + a) : make_uint2(none, 0);
+  };
+  auto fetch_rows = [&](Cols (&v)[kAhead], const uint2 (&of)[kAhead]) {
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (active && of[a].x != none) v[a].load(src + of[a].y * p.ld_grad_out, col, tpr, p.dim);
+  };
+  fetch_tokens(tok[0], begin);
+  fetch_tokens(tok[1], begin + kAhead);
   const uint32_t key_before = begin > 0 ? __ldcg(&tokens[begin - 1].x) : none;
   const uint32_t key_after = end < p.n ? __ldcg(&tokens[end].x) : none;
-  uint32_t key = __ldcg(&tokens[begin].x);
-  const bool head_comes_in = key == key_before && key != none;
+  fetch_rows(val[0], tok[0]);
+  uint32_t key = tok[0][0].x;
+  bool from_before = key == key_before && key != none;
   // Bit 0: the chunk begins inside a row; bit 1: that row also fills the chunk and goes on.
-  if (first_slice) {
-    const bool through = head_comes_in && key == key_after;
-    p.chunk_state[chunk] = (head_comes_in ? 1 : 0) | (through ? 2 : 0);
-  }
-  if (key == none) return;  // padding sorts behind every row
-  const TG* src = static_cast<const TG*>(p.grad_out);
-  const bool active = col < p.dim;
+  if (first_slice) p.chunk_state[chunk] = (from_before ? 1 : 0) | (from_before && key == key_after ? 2 : 0);
   float acc[COLS];
 #pragma unroll
   for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
-  bool from_before = head_comes_in;
   auto flush = [&](bool goes_on) {
     if (from_before || goes_on) {
-      // Head sums lie in the even slots of the workspace, tail sums in the odd ones.
+      // Head sums lie in the even rows of the workspace, tail sums in the odd ones.
       float* part = p.partials + (chunk * 2 + (from_before ? 0 : 1)) * p.ld_partials;
       if (active) store_columns<VEC>(part, acc, 1.f, false, col, tpr, p.dim);
       if (!from_before && first_slice) {
@@ -275,100 +346,121 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
       store_columns<VEC>(p.grad + static_cast<int64_t>(key) * p.ld_grad, acc, p.scale, p.accumulate != 0, col, tpr, p.dim);
     }
   };
-  for (int64_t i = begin; i < end; i += kAhead) {
-    uint2 tok[kAhead];
-    float v[kAhead][COLS];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) tok[a] = i + a < end ? __ldcg(tokens + i + a) : make_uint2(none, 0);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (active && tok[a].x != none) load_columns<TG, VEC>(v[a], src + tok[a].y * p.ld_grad_out, col, tpr, p.dim);
+  auto add = [&](const Cols (&v)[kAhead], const uint2 (&of)[kAhead]) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (tok[a].x == none) {
+      if (of[a].x != key) {
         if (key != none) flush(false);
-        key = none;
-        continue;
-      }
-      if (tok[a].x != key) {
-        flush(false);
-        key = tok[a].x;
+        key = of[a].x;
         from_before = false;
 #pragma unroll
         for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
       }
-      if (active) {
-#pragma unroll
-        for (int k = 0; k < COLS; ++k) acc[k] += v[a][k];
-      }
+      if (key != none) v[a].add_to(acc);
     }
-    if (key == none) return;
+  };
+  // A chunk's length is a multiple of two batches: only the list's last chunk has places without tokens.
+  for (int64_t i = begin; i < end && key != none; i += 2 * kAhead) {
+    fetch_rows(val[1], tok[1]);
+    uint2 next[kAhead];
+    fetch_tokens(next, i + 2 * kAhead);
+    add(val[0], tok[0]);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) tok[0][a] = next[a];
+    fetch_rows(val[0], tok[0]);
+    fetch_tokens(next, i + 3 * kAhead);
+    add(val[1], tok[1]);
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) tok[1][a] = next[a];
   }
-  flush(key == key_after);
+  if (key != none) flush(key == key_after);
 }
 
 // ---------------------------------------------------------------------------- 4. rows across chunks
 
-constexpr int kJoinCols = 64;                       // columns of a CTA, one per thread of a group
-constexpr int kJoinGroups = kThreads / kJoinCols;   // a row's chunks are split over the groups
+constexpr int kJoinWarps = kThreads / 32;
+constexpr int kJoinCols = 128;  // columns of a warp, four per lane
+constexpr int64_t kJoinBlock = kJoinWarps * kJoinCols;
+// A row of this many chunks' sums or more is split over the CTA's warps; below, each warp adds all of them for
+// columns of its own.
+constexpr int kJoinSplit = 16;
+
+__device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const EmbeddingGradLaunch p) {
-  __shared__ float sums[kJoinGroups][kJoinCols];
+  __shared__ float4 sums[kJoinWarps][32];
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31, group = threadIdx.x / kJoinCols, t = threadIdx.x % kJoinCols;
-  const int64_t slices = (p.dim + kJoinCols - 1) / kJoinCols;
-  const int64_t items = static_cast<int64_t>(*p.crossing_count) * slices;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t blocks = (p.dim + kJoinBlock - 1) / kJoinBlock;
+  const int64_t items = static_cast<int64_t>(*p.crossing_count) * blocks;
+  auto add_heads = [&](float4& acc, int64_t lo, int64_t hi, int64_t col) {
+    const float* part = p.partials + col;
+    int64_t c = lo;
+    for (; c + 8 <= hi; c += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part + (c + k) * 2 * p.ld_partials));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add4(acc, v[k]);
+    }
+    for (; c < hi; ++c) add4(acc, __ldcg(reinterpret_cast<const float4*>(part + c * 2 * p.ld_partials)));
+  };
+  auto store = [&](uint32_t key, int64_t col, const float4& acc) {
+    float* dst = p.grad + static_cast<int64_t>(key) * p.ld_grad + col;
+    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k < p.dim) dst[k] = fmaf(p.scale, v[k], p.accumulate ? dst[k] : 0.f);
+  };
   for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const uint2 row = p.crossing[item / slices];
-    const int64_t col = item % slices * kJoinCols + t;
-    // The last chunk that the row reaches into: the first one behind row.x that it does not fill.
-    int64_t last = row.x;
+    const uint2 row = p.crossing[item / blocks];
+    const int64_t first = row.x, block = item % blocks * kJoinBlock;
+    // The last chunk that the row reaches into: the first one behind its own that it does not fill.
+    int64_t last = first;
     for (;;) {
       const int64_t c = last + 1 + lane;
       const unsigned ends = __ballot_sync(0xffffffffu, c >= p.chunks || p.chunk_state[c] != 3);
       if (ends) {
-        const int64_t stop = last + __ffs(ends);
-        last = stop < p.chunks && (p.chunk_state[stop] & 1) ? stop : stop - 1;
+        last += __ffs(ends);
         break;
       }
       last += 32;
     }
-    const int64_t span = last - row.x;  // heads to add
-    const int64_t lo = row.x + 1 + span * group / kJoinGroups, hi = row.x + 1 + span * (group + 1) / kJoinGroups;
-    float acc = 0.f;
-    if (col < p.dim) {
-      const float* part = p.partials + col;
-      if (group == 0) acc = __ldcg(part + (static_cast<int64_t>(row.x) * 2 + 1) * p.ld_partials);
-      int64_t c = lo;
-      for (; c + 8 <= hi; c += 8) {
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __ldcg(part + (c + k) * 2 * p.ld_partials);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc += v[k];
+    if (last >= p.chunks || !(p.chunk_state[last] & 1)) --last;
+    const int64_t span = last - first;
+    const float* tail = p.partials + (first * 2 + 1) * p.ld_partials;
+    if (span < kJoinSplit) {
+      const int64_t col = block + warp * kJoinCols + lane * 4;
+      if (col < p.dim) {
+        float4 acc = __ldcg(reinterpret_cast<const float4*>(tail + col));
+        add_heads(acc, first + 1, last + 1, col);
+        store(row.y, col, acc);
       }
-      for (; c < hi; ++c) acc += __ldcg(part + c * 2 * p.ld_partials);
+      continue;
     }
-    sums[group][t] = acc;
-    __syncthreads();
-    if (group == 0 && col < p.dim) {
-#pragma unroll
-      for (int g = 1; g < kJoinGroups; ++g) acc += sums[g][t];
-      float* dst = p.grad + static_cast<int64_t>(row.y) * p.ld_grad + col;
-      *dst = fmaf(p.scale, acc, p.accumulate ? *dst : 0.f);
+    for (int64_t c0 = block; c0 < min(block + kJoinBlock, p.dim); c0 += kJoinCols) {
+      const int64_t col = c0 + lane * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (col < p.dim) {
+        if (warp == 0) acc = __ldcg(reinterpret_cast<const float4*>(tail + col));
+        add_heads(acc, first + 1 + span * warp / kJoinWarps, first + 1 + span * (warp + 1) / kJoinWarps, col);
+      }
+      sums[warp][lane] = acc;
+      __syncthreads();
+      if (warp == 0 && col < p.dim) {
+        for (int w = 1; w < kJoinWarps; ++w) add4(acc, sums[w][lane]);
+        store(row.y, col, acc);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
 template <typename TG, bool VEC>
-cudaError_t launch_chunks(EmbeddingGradLaunch& p, cudaStream_t stream) {
-  constexpr int COLS = ChunkColumns<TG, VEC>::kCols;
-  p.tpr = 1;
-  while (p.tpr < kThreads && p.tpr * COLS < p.dim) p.tpr *= 2;
-  const int groups = kThreads / p.tpr;
+cudaError_t launch_chunks(const EmbeddingGradLaunch& p, cudaStream_t stream) {
+  const int64_t slice = int64_t(p.tpr) * Columns<TG, VEC>::kCols, groups = kThreads / p.tpr;
   const dim3 grid(static_cast<unsigned>((p.chunks + groups - 1) / groups),
-                  static_cast<unsigned>((p.dim + p.tpr * COLS - 1) / (p.tpr * COLS)));
+                  static_cast<unsigned>((p.dim + slice - 1) / slice));
   return row::launch(embedding_chunk_kernel<TG, VEC>, grid, kThreads, 0, stream, p);
 }
 
@@ -376,34 +468,45 @@ bool aligned16(const void* p, int64_t ld, size_t elem) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && static_cast<size_t>(ld) * elem % 16 == 0;
 }
 
-// Tokens per chunk: at least 16, so that the sums over chunks stay well under the tokens' own rows (two fp32
-// rows of sums for 16 rows read, at worst), and about a thousand chunks from there on.
-int64_t chunk_length(int64_t n) {
-  int64_t len = 16;
-  while (len * 1024 < n) len *= 2;
-  return len;
+// How the sums by chunk are split: threads per row, and tokens per chunk. Short chunks spread few tokens over
+// many SMs; long ones leave fewer sums in the workspace (a chunk writes two fp32 rows of them at worst). So
+// chunks are 16 tokens long, and longer once that still leaves a CTA for each of 1024 places (about 7 per SM).
+void split_tokens(EmbeddingGradLaunch& p) {
+  const int cols = p.vec ? (p.grad_dtype == 1 ? Columns<__nv_bfloat16, true>::kCols : Columns<float, true>::kCols)
+                         : Columns<float, false>::kCols;
+  p.tpr = 1;
+  while (p.tpr < kThreads && p.tpr * cols < p.dim) p.tpr *= 2;
+  const int64_t slices = (p.dim + p.tpr * cols - 1) / (p.tpr * cols), groups = kThreads / p.tpr;
+  p.chunk_len = 16;
+  while (p.n / (2 * p.chunk_len) * slices >= 1024 * groups) p.chunk_len *= 2;
+  p.chunks = (p.n + p.chunk_len - 1) / p.chunk_len;
 }
 
 int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
 
-cudaError_t launch_embedding(const EmbeddingLaunch& p, cudaStream_t stream) {
-  const unsigned grid = static_cast<unsigned>(p.n);
+cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream) {
+  const size_t ti = p.table_dtype == 0 ? 4 : 2, to = p.out_dtype == 0 ? 4 : 2;
+  const bool vec = p.dim % kLookup == 0 && aligned16(p.table, p.ld_table, ti) && aligned16(p.out, p.ld_out, to);
+  p.tpr = 1;
+  while (p.tpr < kThreads && p.tpr * kLookup < p.dim) p.tpr *= 2;
+  const int64_t groups = kThreads / p.tpr;
+  const dim3 grid(static_cast<unsigned>((p.n + groups - 1) / groups));
+  auto run = [&](auto kernel) { return row::launch(kernel, grid, kThreads, 0, stream, const_cast<const EmbeddingLaunch&>(p)); };
+  using B = __nv_bfloat16;
   if (p.table_dtype == 0 && p.out_dtype == 0)
-    embedding_kernel<float, float><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.table_dtype == 0)
-    embedding_kernel<float, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-  else if (p.out_dtype == 0)
-    embedding_kernel<__nv_bfloat16, float><<<grid, kThreads, 0, stream>>>(p);
-  else
-    embedding_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+    return vec ? run(embedding_kernel<float, float, true>) : run(embedding_kernel<float, float, false>);
+  if (p.table_dtype == 0) return vec ? run(embedding_kernel<float, B, true>) : run(embedding_kernel<float, B, false>);
+  if (p.out_dtype == 0) return vec ? run(embedding_kernel<B, float, true>) : run(embedding_kernel<B, float, false>);
+  return vec ? run(embedding_kernel<B, B, true>) : run(embedding_kernel<B, B, false>);
 }
 
 int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws) {
-  p.chunk_len = chunk_length(p.n);
-  p.chunks = (p.n + p.chunk_len - 1) / p.chunk_len;
+  p.vec_grad = aligned16(p.grad, p.ld_grad, sizeof(float));
+  p.vec = p.vec_grad && p.dim % (p.grad_dtype == 1 ? 8 : 4) == 0 &&
+          aligned16(p.grad_out, p.ld_grad_out, p.grad_dtype == 1 ? 2 : 4);
+  split_tokens(p);
   p.ld_partials = (p.dim + 3) / 4 * 4;
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
@@ -424,22 +527,25 @@ cudaError_t launch_embedding_grad(EmbeddingGradLaunch& p, int sms, cudaStream_t 
   while ((int64_t(1) << bits) <= p.rows) ++bits;  // keys go up to `rows`
   p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   p.digit_bits = (bits + p.passes - 1) / p.passes;
-  p.vec_grad = aligned16(p.grad, p.ld_grad, sizeof(float));
-  const bool vec = p.vec_grad && p.dim % (p.grad_dtype == 1 ? 8 : 4) == 0 &&
-                   aligned16(p.grad_out, p.ld_grad_out, p.grad_dtype == 1 ? 2 : 4);
   cudaError_t e = cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kSortSmem));
   if (e != cudaSuccess) return e;
   e = row::launch(embedding_sort_kernel, dim3(kSortCtas), kSortThreads, kSortSmem, stream, p);
   if (e != cudaSuccess) return e;
-  if (!p.accumulate) e = row::launch(embedding_zero_kernel, dim3(2 * sms), kZeroThreads, 0, stream, p);
+  if (!p.accumulate) {
+    const bool flat = p.ld_grad == p.dim;
+    const int64_t len = flat ? p.rows * p.dim : p.dim;
+    const int64_t blocks = (len + kZeroBlock - 1) / kZeroBlock * (flat ? 1 : p.rows);
+    if (blocks >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;
+    e = row::launch(embedding_zero_kernel, dim3(static_cast<unsigned>(blocks)), kZeroThreads, 0, stream, p);
+  }
   if (e != cudaSuccess || p.n == 0) return e;
   if (p.grad_dtype == 0)
-    e = vec ? launch_chunks<float, true>(p, stream) : launch_chunks<float, false>(p, stream);
+    e = p.vec ? launch_chunks<float, true>(p, stream) : launch_chunks<float, false>(p, stream);
   else
-    e = vec ? launch_chunks<__nv_bfloat16, true>(p, stream) : launch_chunks<__nv_bfloat16, false>(p, stream);
+    e = p.vec ? launch_chunks<__nv_bfloat16, true>(p, stream) : launch_chunks<__nv_bfloat16, false>(p, stream);
   if (e != cudaSuccess) return e;
-  const int64_t items = p.chunks * ((p.dim + kJoinCols - 1) / kJoinCols);
+  const int64_t items = p.chunks * ((p.dim + kJoinBlock - 1) / kJoinBlock);
   return row::launch(embedding_join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 4 * sms))), kThreads, 0,
                      stream, p);
 }

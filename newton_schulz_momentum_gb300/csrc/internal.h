@@ -316,8 +316,9 @@ struct EmbeddingLaunch {
   void* out;
   int64_t ld_out;
   unsigned* status;
+  int tpr;  // threads per token, set by launch_embedding
 };
-cudaError_t launch_embedding(const EmbeddingLaunch& p, cudaStream_t stream);
+cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream);
 
 struct EmbeddingGradLaunch {
   const void* grad_out;
@@ -340,8 +341,10 @@ struct EmbeddingGradLaunch {
   int64_t ld_partials;
   uint2* crossing;            // (first chunk, id) of the rows that cross chunks
   unsigned* crossing_count;
+  int tpr;                    // threads per row of grad_out
+  int vec_grad, vec;          // 16-byte access to grad; to grad and grad_out
   // Set by launch_embedding_grad.
-  int passes, digit_bits, vec_grad, tpr;
+  int passes, digit_bits;
 };
 // Workspace bytes; with `ws` it also places the buffers there.
 int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws);

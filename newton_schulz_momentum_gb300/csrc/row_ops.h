@@ -19,19 +19,30 @@ __device__ __forceinline__ float from_f<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// 16 bytes of elements as floats (4 fp32 or 8 bf16), read past L1.
-__device__ __forceinline__ void load16(float (&v)[4], const float* src) {
-  const float4 u = __ldcs(reinterpret_cast<const float4*>(src));
-  v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-}
-__device__ __forceinline__ void load16(float (&v)[8], const __nv_bfloat16* src) {
-  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(src));
+// 16 bytes of elements as floats: 4 fp32 or 8 bf16.
+template <typename T>
+__device__ __forceinline__ void unpack16(float (&v)[16 / sizeof(T)], const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    v[2 * k] = __uint_as_float(w[k] << 16);
-    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    if constexpr (sizeof(T) == 4) {
+      v[k] = __uint_as_float(w[k]);
+    } else {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
   }
+}
+
+// Eight floats rounded to bf16, in 16 bytes.
+__device__ __forceinline__ uint4 pack16(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Token id `i` of an int32 or int64 list.
@@ -55,7 +66,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // Launches `kernel`, which waits for the preceding grid itself (griddepcontrol.wait), with programmatic stream
 // serialisation: its CTAs may be set up while that grid drains.
 template <typename P>
-cudaError_t launch(void (*kernel)(const P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
