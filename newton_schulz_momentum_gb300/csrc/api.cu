@@ -1747,7 +1747,7 @@ int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
   p.h = h, p.ldh = ldh, p.y = y, p.ldy = ldy;
   p.scales = y_dtype == DMUON_E4M3 ? scales : nullptr, p.group = group;
   cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm(p, stream); }), "RMS norm launch");
+  DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm(p, ds->sms, stream); }), "RMS norm launch");
   return DMUON_OK;
 }
 
@@ -1780,10 +1780,10 @@ int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t 
     p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
     p.dx = dx, p.lddx = lddx, p.dgain = dgain, p.accumulate = accumulate != 0;
     char* ws = nullptr;
-    st = token_workspace(*ds, rmsnorm_grad_workspace(n, dim), stream, &ws);
+    st = token_workspace(*ds, rmsnorm_grad_workspace(p, ds->sms, nullptr), stream, &ws);
     if (st != DMUON_OK) return st;
-    p.rho = reinterpret_cast<float*>(ws);
-    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm_grad(p, stream); }), "RMS norm gradient launch");
+    rmsnorm_grad_workspace(p, ds->sms, ws);
+    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm_grad(p, ds->sms, stream); }), "RMS norm gradient launch");
     return DMUON_OK;
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());

@@ -364,8 +364,13 @@ struct RmsNormLaunch {
   int64_t ldy;
   float* scales;  // e4m3 output: n x ceil(dim / group), null otherwise
   int64_t group;  // columns per scale; 0: the whole row
+  // Set by launch_add_rmsnorm: threads per row, scales per row, shared memory for a row of bytes, and whether
+  // every row of x starts on 16 bytes.
+  int tpr, parts, stage, aligned;
+  // Threads that form a row's sum; shared memory words of a row that passes through it for that (0: does not).
+  int sum_threads, line;
 };
-cudaError_t launch_add_rmsnorm(const RmsNormLaunch& p, cudaStream_t stream);
+cudaError_t launch_add_rmsnorm(RmsNormLaunch& p, int sms, cudaStream_t stream);
 
 struct RmsNormGradLaunch {
   const void *dy, *h, *dh;  // dh may be null
@@ -378,10 +383,12 @@ struct RmsNormGradLaunch {
   int64_t lddx;
   float* dgain;  // may be null
   int accumulate;
-  float* rho;  // workspace: rmsnorm_grad_workspace(n, dim) bytes
+  float *partials, *rho;  // workspace, set by rmsnorm_grad_workspace
+  int tpr, npartials;     // set by launch_add_rmsnorm_grad: threads per row, rows of partials
 };
-int64_t rmsnorm_grad_workspace(int64_t n, int64_t dim);
-cudaError_t launch_add_rmsnorm_grad(const RmsNormGradLaunch& p, cudaStream_t stream);
+// Workspace bytes; also places the buffers at `ws` (null when asked for the size alone).
+int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, int sms, char* ws);
+cudaError_t launch_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream);
 
 struct PolicyLaunch {
   const void* logits;

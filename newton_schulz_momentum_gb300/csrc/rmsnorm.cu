@@ -7,14 +7,30 @@
 //
 // Backward, for the stored h: with d = dy * gain,
 //   dx = dh + rho d - h rho^3 / dim * sum(d h),   dgain = sum over rows of dy h rho.
+//
+// Both are bound by memory: each element is read once and written once. A row is held in the registers of
+// `tpr` threads, K 16-byte granules of it in each, so one read serves the sums and the outputs. Rows need
+// not start on 16 bytes: the granules are cut where the addresses are aligned, the row's first and last one
+// may be partial, and those are read and written element by element. CTAs stay and take every
+// (gridDim.x * rows per CTA)-th row, a multiple of 8, so all rows of a thread start at the same offset from
+// 16 bytes whatever their length: its columns, and with them its gains and its sums for dgain, stay the
+// same. The next row is on its way while the current one is reduced and written.
+//
+// The forward sum has one order for every layout, that of rows that start on 16 bytes: thread t of sum_threads
+// adds granules t, t + sum_threads, ... counted from the row's first element, then the threads join. Rows that
+// start elsewhere pass through shared memory for it, so a value's bits do not depend on where it lies.
+#include <algorithm>
+
 #include <cuda_fp8.h>
 
 #include "row_ops.h"
+#include "tc_ptx.h"
 
 namespace dmuon {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // of a CTA that holds short rows, and of the kernels for the longest ones
+constexpr int kMaxThreads = 1024;
 constexpr float kFp8Max = 448.f;  // largest finite e4m3
 constexpr float kMinScale = 1.17549435e-38f;
 
@@ -32,28 +48,441 @@ __device__ __forceinline__ unsigned block_top(unsigned v, unsigned* red) {
   return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < (blockDim.x >> 5) ? red[threadIdx.x & 31] : 0u);
 }
 
+// ---------------------------------------------------------------------------- granules
+
+// The elements [e0, e0 + E) of a row of `dim` elements, 16 bytes at an aligned address; elements outside the
+// row are neither read nor written, and count as 0.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const RmsNormLaunch p) {
-  __shared__ float red[32];
+struct Granule {
+  static constexpr int E = 16 / sizeof(T);
+
+  static __device__ __forceinline__ uint4 load(const T* row, int e0, int dim) {
+    if (e0 >= 0 && e0 + E <= dim) return __ldcs(reinterpret_cast<const uint4*>(row + e0));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      const int e = e0 + j;
+      if (e < 0 || e >= dim) continue;
+      if constexpr (sizeof(T) == 4)
+        w[j] = __float_as_uint(row[e]);
+      else
+        w[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(row[e])) << (j % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+
+  static __device__ __forceinline__ void store(T* row, int e0, int dim, const float (&v)[E]) {
+    if (e0 >= 0 && e0 + E <= dim) {
+      if constexpr (sizeof(T) == 4)
+        __stcs(reinterpret_cast<float4*>(row + e0), make_float4(v[0], v[1], v[2], v[3]));
+      else
+        __stcs(reinterpret_cast<uint4*>(row + e0), row::pack16(v));
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (e0 + j >= 0 && e0 + j < dim) row[e0 + j] = row::from_f<T>(v[j]);
+  }
+};
+
+template <int E>
+__device__ __forceinline__ void load_gain(float (&g)[E], const float* gain, int e0, int dim) {
+  if (gain && e0 >= 0 && e0 + E <= dim && (reinterpret_cast<uintptr_t>(gain + e0) & 15) == 0) {
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(gain + e0 + j));
+      g[j] = u.x, g[j + 1] = u.y, g[j + 2] = u.z, g[j + 3] = u.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < E; ++j) g[j] = gain && e0 + j >= 0 && e0 + j < dim ? __ldg(gain + e0 + j) : 1.f;
+}
+
+// Sums over the `tpr` threads of a row. `red` alternates between two halves from row to row, so one barrier
+// per row is enough. All threads of the CTA call it.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[32][N], int half) {
+  for (int o = min(tpr, 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  if (tpr <= 32) {
+    __syncwarp();  // as the barrier below does for wider rows: what a row left in shared memory is there for the next
+    return;
+  }
+  const int warp = threadIdx.x >> 5, warps = tpr >> 5, first = warp / warps * warps;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[half][warp][k] = s[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = 0.f;
+  for (int w = first; w < first + warps; ++w)
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] += red[half][w][k];
+}
+
+// ---------------------------------------------------------------------------- forward
+
+// THREADS: the most of a CTA. REGS: gains stay in registers. AHEAD: the next row is loaded early.
+template <typename T, int K, bool FP8, int THREADS, bool REGS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
+  using G = Granule<T>;
+  constexpr int E = G::E;
+  __shared__ float red[2][32][1];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int dim = static_cast<int>(p.dim);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  const T* x = static_cast<const T*>(p.x) + (first + slot) * p.ldx;
+  const T* r = p.residual ? static_cast<const T*>(p.residual) + (first + slot) * p.ldr : nullptr;
+  T* h = p.h ? static_cast<T*>(p.h) + (first + slot) * p.ldh : nullptr;
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  auto start = [&](int k) { return (t + k * tpr) * E - shift; };
+  float gain[REGS ? K : 1][E];
+  if (REGS)
+#pragma unroll
+    for (int k = 0; k < K; ++k) load_gain(gain[k], p.gain, start(k), dim);
+
+  // 8-bit output: the largest |y| of each group, alternating between two halves; then a row of bytes.
+  const int parts = FP8 ? p.parts : 0;
+  unsigned* tops = reinterpret_cast<unsigned*>(dyn);
+  uint8_t* bytes = dyn + (2 * rows * parts * 4 + 15) / 16 * 16 + slot * p.stage;
+  // Rows that do not start on 16 bytes: h in the order of its elements, a word left out after every 32, so that
+  // lanes eight elements apart use different banks.
+  float* line = reinterpret_cast<float*>(dyn + (2 * rows * parts * 4 + 15) / 16 * 16 + rows * p.stage) + slot * p.line;
+  if (FP8) {
+    for (int k = threadIdx.x; k < 2 * rows * parts; k += blockDim.x) tops[k] = 0;
+    __syncthreads();
+  }
+
+  uint4 xr[K], rr[K];
+  auto fetch = [&](int64_t i) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool in = i < p.n && start(k) < dim;
+      xr[k] = in ? G::load(x, start(k), dim) : make_uint4(0, 0, 0, 0);
+      rr[k] = in && r ? G::load(r, start(k), dim) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (AHEAD) fetch(first + slot);
+  int half = 0;
+  for (int64_t base = first; base < p.n; base += step, half ^= 1) {
+    const int64_t i = base + slot;
+    if (!AHEAD) fetch(i);
+    float v[K][E];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float a[E], b[E];
+      row::unpack16<T>(a, xr[k]);
+      row::unpack16<T>(b, rr[k]);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        v[k][j] = a[j] + b[j];
+        if (p.line == 0) s[0] = fmaf(v[k][j], v[k][j], s[0]);
+      }
+    }
+    x += step * p.ldx;
+    if (r) r += step * p.ldr;
+    if (AHEAD && base + step < p.n) fetch(i + step);
+    if (h && i < p.n)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (start(k) < dim) G::store(h, start(k), dim, v[k]);
+    if (h) h += step * p.ldh;
+    if (p.line) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const int e = start(k) + j;
+          if (e >= 0 && e < dim) line[e + (e >> 5)] = v[k][j];
+        }
+      __syncthreads();
+      if (t < p.sum_threads)
+        for (int e0 = t * E; e0 < dim; e0 += p.sum_threads * E)
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (e0 + j < dim) {
+              const float a = line[e0 + j + ((e0 + j) >> 5)];
+              s[0] = fmaf(a, a, s[0]);
+            }
+    }
+    row_sum(s, tpr, red, half);
+    const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[k][j] = v[k][j] * rho * gain[REGS ? k : 0][j];
+    }
+    if constexpr (!FP8) {
+      T* y = static_cast<T*>(p.y) + i * p.ldy;
+      if (i < p.n)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (start(k) < dim) G::store(y, start(k), dim, v[k]);
+    } else {
+      unsigned* top = tops + (half * rows + slot) * parts;
+      const int group = p.group ? static_cast<int>(p.group) : 1 << 30;
+      // Lanes that share a group where granules do not straddle two: the largest of theirs goes to one lane.
+      const int lanes = p.aligned || p.group == 0 ? min(min(group / E, 32), tpr) : 1;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int e0 = start(k);
+        unsigned low = 0, high = 0;  // of the granule's first group, and of the next one
+        const int border = (max(e0, 0) / group + 1) * group;
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const unsigned b = e0 + j >= 0 && e0 + j < dim ? __float_as_uint(fabsf(v[k][j])) : 0u;
+          if (e0 + j < border) low = max(low, b); else high = max(high, b);
+        }
+        for (int o = lanes / 2; o > 0; o >>= 1) low = max(low, __shfl_xor_sync(0xffffffffu, low, o));
+        if (i < p.n && e0 < dim) {
+          if (t % lanes == 0 && low) atomicMax(top + max(e0, 0) / group, low);
+          if (high) atomicMax(top + border / group, high);
+        }
+      }
+      __syncthreads();
+      for (int k = t; k < parts; k += tpr) {
+        if (i < p.n) p.scales[i * parts + k] = scale_of(top[k]);
+        tops[((half ^ 1) * rows + slot) * parts + k] = 0;  // for the next row; its readers are a barrier behind
+      }
+      uint8_t* q = static_cast<uint8_t*>(p.y) + i * p.ldy;
+      const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int e0 = start(k);
+        if (i >= p.n || e0 >= dim) continue;
+        const int part = max(e0, 0) / group, border = (part + 1) * group;
+        const float inv = 1.f / scale_of(top[part]);
+        const float inv_next = border < e0 + E && border < dim ? 1.f / scale_of(top[part + 1]) : inv;
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int j = 0; j < E; j += 2) {
+          const float lo = v[k][j] * (e0 + j < border ? inv : inv_next);
+          const float hi = v[k][j + 1] * (e0 + j + 1 < border ? inv : inv_next);
+          const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+          if (j % 4 == 0) w[j / 4] = two; else w[j / 4] |= two << 16;
+        }
+        if (p.stage == 0) {
+          if constexpr (E == 8)
+            *reinterpret_cast<uint2*>(q + e0) = make_uint2(w[0], w[1]);
+          else
+            *reinterpret_cast<uint32_t*>(q + e0) = w[0];
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (e0 + j >= 0 && e0 + j < dim) bytes[at + e0 + j] = static_cast<uint8_t>(w[j / 4] >> (j % 4 * 8));
+        }
+      }
+      if (p.stage) {
+        // The row lies in shared memory as its bytes lie around 16-byte addresses; whole sixteens go out as such.
+        __syncthreads();
+        if (i < p.n)
+          for (int c = t * 16; c < at + dim; c += tpr * 16) {
+            if (c >= at && c + 16 <= at + dim)
+              __stcs(reinterpret_cast<uint4*>(q - at + c), *reinterpret_cast<const uint4*>(bytes + c));
+            else
+              for (int b = max(c, at); b < min(c + 16, at + dim); ++b) q[b - at] = bytes[b];
+          }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- backward
+
+// The sums for dgain of a thread's columns stay in registers (REGS) or, for long rows, in shared memory.
+template <typename T, int K, int THREADS, bool REGS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const RmsNormGradLaunch p) {
+  using G = Granule<T>;
+  constexpr int E = G::E;
+  __shared__ float red[2][32][2];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int dim = static_cast<int>(p.dim);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  const T* dy = static_cast<const T*>(p.dy) + (first + slot) * p.lddy;
+  const T* h = static_cast<const T*>(p.h) + (first + slot) * p.ldh;
+  const T* dh = p.dh ? static_cast<const T*>(p.dh) + (first + slot) * p.lddh : nullptr;
+  T* dx = static_cast<T*>(p.dx) + (first + slot) * p.lddx;
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(dy) & 15) / sizeof(T));
+  auto start = [&](int k) { return (t + k * tpr) * E - shift; };
+  float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E];
+  // Without REGS a thread's sums: four columns at [quarter][granule], so that a warp's accesses do not conflict.
+  float4* sums = reinterpret_cast<float4*>(dyn);
+  const int granules = K * tpr;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (REGS) {
+      load_gain(gain[k], p.gain, start(k), dim);
+#pragma unroll
+      for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
+    } else {
+#pragma unroll
+      for (int j = 0; j < E / 4; ++j) sums[j * granules + t + k * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  uint4 yr[2][K], hr[2][K], tr[2][K];  // of the current row and the next
+  auto fetch = [&](uint4 (&a)[K], uint4 (&b)[K], uint4 (&c)[K], int64_t i) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const bool in = i < p.n && start(k) < dim;
+      a[k] = in ? G::load(dy, start(k), dim) : make_uint4(0, 0, 0, 0);
+      b[k] = in ? G::load(h, start(k), dim) : make_uint4(0, 0, 0, 0);
+      c[k] = in && dh ? G::load(dh, start(k), dim) : make_uint4(0, 0, 0, 0);
+    }
+    dy += step * p.lddy;
+    h += step * p.ldh;
+    if (dh) dh += step * p.lddh;
+  };
+  if (AHEAD) fetch(yr[1], hr[1], tr[1], first + slot);
+  int half = 0;
+  for (int64_t base = first; base < p.n; base += step, half ^= 1) {
+    const int64_t i = base + slot;
+    if (AHEAD) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) yr[0][k] = yr[1][k], hr[0][k] = hr[1][k], tr[0][k] = tr[1][k];
+      if (base + step < p.n) fetch(yr[1], hr[1], tr[1], i + step);
+    } else {
+      fetch(yr[0], hr[0], tr[0], i);
+    }
+    float s[2] = {0.f, 0.f};  // sum of h^2, sum of d h
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float a[E], b[E];
+      row::unpack16<T>(a, yr[0][k]);
+      row::unpack16<T>(b, hr[0][k]);
+      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        s[0] = fmaf(b[j], b[j], s[0]);
+        s[1] = fmaf(a[j] * gain[REGS ? k : 0][j], b[j], s[1]);
+      }
+    }
+    row_sum(s, tpr, red, half);
+    const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
+    const float back = s[1] / static_cast<float>(dim) * rho * rho * rho;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float a[E], b[E], c[E];
+      row::unpack16<T>(a, yr[0][k]);
+      row::unpack16<T>(b, hr[0][k]);
+      row::unpack16<T>(c, tr[0][k]);
+      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+      float4 sum;
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const float term = i < p.n ? a[j] * (b[j] * rho) : 0.f;
+        if (REGS) {
+          acc[k][j] += term;
+        } else {
+          if (j % 4 == 0) sum = sums[j / 4 * granules + t + k * tpr];
+          (j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w) += term;
+          if (j % 4 == 3) sums[j / 4 * granules + t + k * tpr] = sum;
+        }
+        c[j] = fmaf(rho, a[j] * gain[REGS ? k : 0][j], fmaf(-back, b[j], c[j]));
+      }
+      if (i < p.n && start(k) < dim) G::store(dx, start(k), dim, c);
+    }
+    dx += step * p.lddx;
+  }
+  if (!p.dgain) return;
+  // This CTA's sums, one row of the workspace. The row slots of a CTA start at different offsets, so they join
+  // by column, in their order.
+  float* out = p.partials + static_cast<int64_t>(blockIdx.x) * p.dim;
+  float* line = reinterpret_cast<float*>(dyn);
+  for (int turn = 0; turn < rows; ++turn) {
+    if (rows > 1) __syncthreads();
+    if (turn != slot) continue;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        const int e = start(k) + j;
+        if (e < 0 || e >= dim) continue;
+        float v;
+        if (REGS) {
+          v = acc[k][j];
+        } else {
+          const float4 sum = sums[j / 4 * granules + t + k * tpr];
+          v = j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w;
+        }
+        if (rows > 1) {
+          if (turn > 0) v += line[e];
+          line[e] = v;
+        }
+        if (turn == rows - 1) out[e] = v;
+      }
+  }
+}
+
+// dgain from the CTAs' sums: a CTA takes 32 columns, its warps every eighth row of the workspace.
+__global__ void __launch_bounds__(kThreads) rmsnorm_dgain_kernel(const RmsNormGradLaunch p) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float sums[kWarps][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float acc = 0.f;
+  if (c < p.dim) {
+    int i = warp;
+    for (; i + 7 * kWarps < p.npartials; i += 8 * kWarps) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = __ldcg(p.partials + (i + k * kWarps) * p.dim + c);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc += v[k];
+    }
+    for (; i < p.npartials; i += kWarps) acc += __ldcg(p.partials + i * p.dim + c);
+  }
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp == 0 && c < p.dim) {
+    for (int w = 1; w < kWarps; ++w) acc += sums[w][lane];
+    p.dgain[c] = p.accumulate ? p.dgain[c] + acc : acc;
+  }
+}
+
+// ---------------------------------------------------------------------------- the longest rows
+
+// One CTA per row, each element read again for every use: rows beyond what registers hold, and arrays that
+// start at different offsets from 16 bytes.
+template <typename T>
+__global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormLaunch p) {
+  __shared__ float red[2][32][1];
   __shared__ unsigned redu[32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  constexpr int E = Granule<T>::E;
+  const int threads = blockDim.x;
   const int64_t i = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + i * p.ldx;
   const T* r = p.residual ? static_cast<const T*>(p.residual) + i * p.ldr : nullptr;
   T* h = p.h ? static_cast<T*>(p.h) + i * p.ldh : nullptr;
-  float sq = 0.f;
-  for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
-    const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
-    sq = fmaf(v, v, sq);
-  }
-  sq = row::block_sum(sq, red);
-  const float rho = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
+  float sq[1] = {0.f};
+  if (threadIdx.x < p.sum_threads)
+    for (int64_t c0 = threadIdx.x * E; c0 < p.dim; c0 += p.sum_threads * E)
+      for (int64_t c = c0; c < min(c0 + E, p.dim); ++c) {
+        const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
+        sq[0] = fmaf(v, v, sq[0]);
+      }
+  row_sum(sq, threads, red, 0);
+  const float rho = rsqrtf(sq[0] / static_cast<float>(p.dim) + p.eps);
   auto value = [&](int64_t c) {
     const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
     return v * rho * (p.gain ? p.gain[c] : 1.f);
   };
   if (!p.scales) {
     T* y = static_cast<T*>(p.y) + i * p.ldy;
-    for (int64_t c = threadIdx.x; c < p.dim; c += kThreads) {
+    for (int64_t c = threadIdx.x; c < p.dim; c += threads) {
       const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
       const float yv = v * rho * (p.gain ? p.gain[c] : 1.f);
       if (h) h[c] = row::from_f<T>(v);
@@ -67,11 +496,11 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const RmsNormLaun
   for (int64_t k = 0; k < parts; ++k) {
     const int64_t begin = k * group, end = min(begin + group, p.dim);
     unsigned top = 0;
-    for (int64_t c = begin + threadIdx.x; c < end; c += kThreads) top = max(top, __float_as_uint(fabsf(value(c))));
+    for (int64_t c = begin + threadIdx.x; c < end; c += threads) top = max(top, __float_as_uint(fabsf(value(c))));
     const float scale = scale_of(block_top(top, redu));
     const float inv = 1.f / scale;
     if (threadIdx.x == 0) p.scales[i * parts + k] = scale;
-    for (int64_t c = begin + threadIdx.x; c < end; c += kThreads) {
+    for (int64_t c = begin + threadIdx.x; c < end; c += threads) {
       const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
       q[c] = __nv_cvt_float_to_fp8(value(c) * inv, __NV_SATFINITE, __NV_E4M3);
       if (h) h[c] = row::from_f<T>(v);
@@ -82,6 +511,8 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_kernel(const RmsNormLaun
 template <typename T>
 __global__ void __launch_bounds__(kThreads) add_rmsnorm_grad_kernel(const RmsNormGradLaunch p) {
   __shared__ float red[32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   const int64_t i = blockIdx.x;
   const T* dy = static_cast<const T*>(p.dy) + i * p.lddy;
   const T* h = static_cast<const T*>(p.h) + i * p.ldh;
@@ -106,51 +537,208 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_grad_kernel(const RmsNor
   }
 }
 
-// One thread per column, rows in order.
+// dgain for them: a CTA takes 32 columns over a stretch of rows, its warps every eighth row of it, and leaves
+// their sums in the workspace.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rmsnorm_dgain_kernel(const RmsNormGradLaunch p) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (c >= p.dim) return;
-  const T* dy = static_cast<const T*>(p.dy) + c;
-  const T* h = static_cast<const T*>(p.h) + c;
+__global__ void __launch_bounds__(kThreads) rmsnorm_columns_kernel(const RmsNormGradLaunch p) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float sums[kWarps][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t begin = p.n * blockIdx.y / gridDim.y, end = p.n * (blockIdx.y + 1) / gridDim.y;
   float acc = 0.f;
-  for (int64_t i = 0; i < p.n; ++i) acc = fmaf(row::to_f(dy[i * p.lddy]) * p.rho[i], row::to_f(h[i * p.ldh]), acc);
-  p.dgain[c] = p.accumulate ? p.dgain[c] + acc : acc;
+  if (c < p.dim)
+    for (int64_t i = begin + warp; i < end; i += kWarps)
+      acc = fmaf(row::to_f(static_cast<const T*>(p.dy)[i * p.lddy + c]) * p.rho[i],
+                 row::to_f(static_cast<const T*>(p.h)[i * p.ldh + c]), acc);
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp == 0 && c < p.dim) {
+    for (int w = 1; w < kWarps; ++w) acc += sums[w][lane];
+    p.partials[blockIdx.y * p.dim + c] = acc;
+  }
+}
+
+// ---------------------------------------------------------------------------- launches
+
+constexpr int kMaxHeld = 16384;  // elements of a row held in registers
+constexpr int kColumnSplits = 32;  // stretches of rows of rmsnorm_columns_kernel
+
+// A row's arrays and their strides, to see whether their granules coincide.
+struct Array {
+  const void* ptr;
+  int64_t ld;
+};
+
+// Granules of a row where every array starts rows at the same offsets from 16 bytes; 0 where they differ.
+int row_granules(std::initializer_list<Array> arrays, int64_t n, int64_t dim, size_t elem) {
+  const Array& a = *arrays.begin();
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.ptr) % 16;
+  const size_t step = n > 1 ? static_cast<size_t>(a.ld) * elem % 16 : 0;
+  for (const Array& b : arrays)
+    if (b.ptr && (reinterpret_cast<uintptr_t>(b.ptr) % 16 != at ||
+                  (n > 1 && static_cast<size_t>(b.ld) * elem % 16 != step)))
+      return 0;
+  const int per = static_cast<int>(16 / elem);
+  if (dim > kMaxHeld) return 0;
+  const int64_t offset = at == 0 && step == 0 ? 0 : per - 1;
+  const int64_t granules = (dim + offset + per - 1) / per;
+  return granules * per <= kMaxHeld ? static_cast<int>(granules) : 0;
+}
+
+// Threads of a row for K granules each: whole warps, or a power of two below one.
+int row_threads(int granules, int k) {
+  const int need = (granules + k - 1) / k;
+  if (need > 16) return (need + 31) / 32 * 32;
+  int t = 1;
+  while (t < need) t *= 2;
+  return t;
+}
+
+constexpr int kMaxPerSm = 16;  // CTAs (of 160 threads at least)
+
+struct RowGrid {
+  int tpr, threads, rows;
+  unsigned ctas;
+};
+
+// Resident CTAs of a kernel, all over the GPU and a multiple of 8 (152 SMs are), or fewer where the rows run out.
+template <typename P>
+cudaError_t row_grid(RowGrid& g, void (*kernel)(P), int tpr, int64_t n, size_t smem, int sms) {
+  g.tpr = tpr;
+  g.rows = g.tpr >= kThreads ? 1 : kThreads / g.tpr;
+  g.threads = g.tpr * g.rows;
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, g.threads, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = std::max<int64_t>(8, static_cast<int64_t>(sms) * std::min(per_sm, kMaxPerSm) / 8 * 8);
+  g.ctas = static_cast<unsigned>(std::min<int64_t>(most, (n + g.rows - 1) / g.rows));
+  return cudaSuccess;
+}
+
+template <typename T, int K, bool FP8, int THREADS, bool REGS, bool AHEAD>
+cudaError_t launch_rows(RmsNormLaunch& p, int granules, int sms, cudaStream_t stream) {
+  auto* kernel = add_rmsnorm_rows_kernel<T, K, FP8, THREADS, REGS, AHEAD>;
+  constexpr int E = Granule<T>::E;
+  size_t per_row = 0;
+  p.parts = 0, p.stage = 0;
+  p.aligned = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && (p.n == 1 || static_cast<size_t>(p.ldx) * sizeof(T) % 16 == 0);
+  if (FP8) {
+    p.parts = p.group ? static_cast<int>((p.dim + p.group - 1) / p.group) : 1;
+    // A granule's bytes are stored as such where they are aligned in every row.
+    const bool whole = p.aligned && (reinterpret_cast<uintptr_t>(p.y) | static_cast<uintptr_t>(p.n == 1 ? 0 : p.ldy)) % E == 0 &&
+                       p.dim % E == 0;
+    p.stage = whole ? 0 : static_cast<int>((p.dim + 15 + 15) / 16 * 16);
+    per_row = static_cast<size_t>(2 * p.parts * 4 + 16 + p.stage);
+  }
+  p.line = 0;
+  if (!p.aligned) {
+    p.line = static_cast<int>(p.dim + p.dim / 32 + 1);
+    per_row += static_cast<size_t>(p.line) * 4;
+  }
+  const int tpr = std::max(row_threads(granules, K), p.sum_threads);
+  const size_t smem = per_row * (tpr >= kThreads ? 1 : kThreads / tpr);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  RowGrid g;
+  const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
+  if (e != cudaSuccess) return e;
+  p.tpr = g.tpr;
+  return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
+}
+
+template <typename T, bool FP8>
+cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
+  const int granules = row_granules({{p.x, p.ldx}, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n,
+                                    p.dim, sizeof(T));
+  // CTAs of 256 threads as long as a row's gains fit their registers beside it, then of up to 512, then 1024.
+  // The order of the sum is that of the kernel that takes aligned rows of this length.
+  const int whole = static_cast<int>((p.dim + Granule<T>::E - 1) / Granule<T>::E);
+  p.sum_threads = std::min(whole <= 256 ? row_threads(whole, 1)
+                           : whole <= 512 ? row_threads(whole, 2) : row_threads(whole, 4), kMaxThreads);
+  if (granules == 0)
+    return row::launch(add_rmsnorm_kernel<T>, dim3(static_cast<unsigned>(p.n)), std::max(32, p.sum_threads), 0, stream, p);
+  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true, true>(p, granules, sms, stream);
+  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true, true>(p, granules, sms, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (granules <= 1024) return launch_rows<T, 4, FP8, 256, true, true>(p, granules, sms, stream);
+    if (granules > 2048) return launch_rows<T, 4, FP8, 1024, false, false>(p, granules, sms, stream);
+  }
+  return launch_rows<T, 4, FP8, 512, false, true>(p, granules, sms, stream);
+}
+
+template <typename T, int K, int THREADS, bool REGS, bool AHEAD>
+cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
+  auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, REGS, AHEAD>;
+  // Sums of long rows, or the line in which a CTA's short rows join.
+  const int tpr = row_threads(granules, K), rows = tpr >= kThreads ? 1 : kThreads / tpr;
+  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * 16 / sizeof(T) * 4;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  RowGrid g;
+  const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
+  if (e != cudaSuccess) return e;
+  p.tpr = g.tpr;
+  p.npartials = static_cast<int>(g.ctas);
+  return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
+  const int granules = row_granules({{p.dy, p.lddy}, {p.h, p.ldh}, {p.dh, p.lddh}, {p.dx, p.lddx}}, p.n, p.dim, sizeof(T));
+  cudaError_t e;
+  if (granules == 0) {
+    const dim3 grid(static_cast<unsigned>(p.n));
+    if (p.dgain) {  // before dx, which may be written over dy
+      RmsNormGradLaunch only_rho = p;
+      only_rho.dx = nullptr;
+      e = row::launch(add_rmsnorm_grad_kernel<T>, grid, kThreads, 0, stream, only_rho);
+      if (e != cudaSuccess) return e;
+      p.npartials = kColumnSplits;
+      e = row::launch(rmsnorm_columns_kernel<T>, dim3(static_cast<unsigned>((p.dim + 31) / 32), kColumnSplits), kThreads, 0,
+                      stream, p);
+      if (e != cudaSuccess) return e;
+    }
+    e = row::launch(add_rmsnorm_grad_kernel<T>, grid, kThreads, 0, stream, p);
+  } else if (granules <= 256) {
+    e = launch_grad_rows<T, 1, 256, true, true>(p, granules, sms, stream);
+  } else if (granules <= 512) {
+    e = launch_grad_rows<T, 2, 256, true, true>(p, granules, sms, stream);
+  } else if (granules > 2048) {
+    if constexpr (sizeof(T) == 4) e = launch_grad_rows<T, 4, 1024, false, false>(p, granules, sms, stream);
+    else e = cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
+  } else {
+    e = launch_grad_rows<T, 4, 512, false, true>(p, granules, sms, stream);
+  }
+  if (e != cudaSuccess || !p.dgain) return e;
+  return row::launch(rmsnorm_dgain_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), kThreads, 0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_add_rmsnorm(const RmsNormLaunch& p, cudaStream_t stream) {
-  if (p.dtype == 0)
-    add_rmsnorm_kernel<float><<<static_cast<unsigned>(p.n), kThreads, 0, stream>>>(p);
-  else
-    add_rmsnorm_kernel<__nv_bfloat16><<<static_cast<unsigned>(p.n), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_add_rmsnorm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
+  if (p.scales)
+    return p.dtype == 0 ? launch_norm<float, true>(p, sms, stream) : launch_norm<__nv_bfloat16, true>(p, sms, stream);
+  return p.dtype == 0 ? launch_norm<float, false>(p, sms, stream) : launch_norm<__nv_bfloat16, false>(p, sms, stream);
 }
 
-int64_t rmsnorm_grad_workspace(int64_t n, int64_t dim) {
-  (void)dim;
-  return n * static_cast<int64_t>(sizeof(float));
+// Rows of sums, one per resident CTA or kColumnSplits; then a rho per row for the longest rows.
+int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, int sms, char* ws) {
+  const int64_t rows = std::max<int64_t>(kColumnSplits, std::min<int64_t>(p.n, std::max(8, sms * kMaxPerSm)));
+  const int64_t sums = (rows * p.dim * 4 + 255) / 256 * 256;
+  p.partials = reinterpret_cast<float*>(ws);
+  p.rho = reinterpret_cast<float*>(ws + sums);
+  return sums + p.n * 4;
 }
 
-cudaError_t launch_add_rmsnorm_grad(const RmsNormGradLaunch& p, cudaStream_t stream) {
-  const unsigned rows = static_cast<unsigned>(p.n), cols = static_cast<unsigned>((p.dim + kThreads - 1) / kThreads);
-  if (p.dgain) {  // before dx, which may be written over dy
-    RmsNormGradLaunch only_rho = p;
-    only_rho.dx = nullptr;
-    if (p.dtype == 0) {
-      add_rmsnorm_grad_kernel<float><<<rows, kThreads, 0, stream>>>(only_rho);
-      rmsnorm_dgain_kernel<float><<<cols, kThreads, 0, stream>>>(p);
-    } else {
-      add_rmsnorm_grad_kernel<__nv_bfloat16><<<rows, kThreads, 0, stream>>>(only_rho);
-      rmsnorm_dgain_kernel<__nv_bfloat16><<<cols, kThreads, 0, stream>>>(p);
-    }
-  }
-  if (p.dtype == 0)
-    add_rmsnorm_grad_kernel<float><<<rows, kThreads, 0, stream>>>(p);
-  else
-    add_rmsnorm_grad_kernel<__nv_bfloat16><<<rows, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
+  return p.dtype == 0 ? launch_grad<float>(p, sms, stream) : launch_grad<__nv_bfloat16>(p, sms, stream);
 }
 
 }  // namespace dmuon
