@@ -1283,7 +1283,7 @@ int run_policy(PolicyLaunch& p, cudaStream_t stream) {
     p.row_loss = reinterpret_cast<float*>(ws);
   }
   p.status = ds->status;
-  DM_CUDA(timed(kClsPolicy, stream, [&] { return launch_policy(p, stream); }), "policy loss launch");
+  DM_CUDA(timed(kClsPolicy, stream, [&] { return launch_policy(p, ds->sms, stream); }), "policy loss launch");
   return DMUON_OK;
 }
 
@@ -1818,7 +1818,7 @@ int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int6
   p.targets = targets, p.id_bytes = id_bytes;
   p.old_logp = old_logp, p.ref_logp = kl_coef != 0.f ? ref_logp : nullptr;
   p.advantages = advantages, p.weights = weights;
-  p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.temperature = temperature;
+  p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.inv_temperature = 1.f / temperature;
   p.loss = loss, p.logp = logp, p.dlogits = dlogits, p.ldd = ldd;
   return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
 }
@@ -1838,7 +1838,7 @@ int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, i
   std::memset(&p, 0, sizeof(p));
   p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
   p.targets = targets, p.id_bytes = id_bytes;
-  p.temperature = temperature, p.logp = logp;
+  p.inv_temperature = 1.f / temperature, p.logp = logp;
   return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
 }
 

@@ -398,15 +398,18 @@ struct PolicyLaunch {
   int id_bytes;
   const float *old_logp, *ref_logp, *advantages;  // ref_logp may be null: no KL term
   const float* weights;                           // null: log-probabilities only
-  float clip_low, clip_high, kl_coef, temperature;
+  float clip_low, clip_high, kl_coef, inv_temperature;
   float* loss;      // null: log-probabilities only
   float* row_loss;  // workspace, n entries
   float* logp;      // may be null
   void* dlogits;    // may be null
   int64_t ldd;
   unsigned* status;
+  // Set by launch_policy: threads per row, CTAs per row, whether logits and dlogits start their rows at the same
+  // offsets from 16 bytes, and whether every row of logits starts on 16 bytes.
+  int tpr, cluster, same_cut, aligned;
 };
-cudaError_t launch_policy(const PolicyLaunch& p, cudaStream_t stream);
+cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream);
 
 // Record `message` as the calling thread's last error (returned by dmuon_last_error) and return status.
 int set_error(int status, const char* message);

@@ -6,18 +6,43 @@
 //   c = d(loss)/d(lp) = w (-A r [r A <= clip(r) A] + k (1 - exp(d))),
 //   d(loss)/dx = c / T (onehot(a) - softmax(z)).
 // A row of weight 0 or with a negative token is not read: its terms and gradient are 0.
+//
+// Bound by memory: c needs the whole row's sum before the first element of the gradient, and a row of a large
+// vocabulary is more than an SM holds (128256 bf16: 257 KB), so the row is split over the CTAs of a cluster. It
+// waits in their shared memory while they join their sums, and is read and written once. Rows of up to 16384
+// elements are held in the registers of a CTA's threads instead; beyond the cluster's memory a row is read twice.
+//
+// Memory is read and written in 16-byte granules at aligned addresses, wherever a row starts; the sum runs over
+// groups of as many elements counted from the row's first one. So its order goes by the vocabulary alone: a row
+// gives the same bits whatever the other rows are, and wherever it and its gradient lie.
+#include <algorithm>
+
 #include "row_ops.h"
+#include "tc_ptx.h"
 
 namespace dmuon {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// 2^x, within 2 units of the last place; below 2^-126 it is 0.
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Within 2^-22 of itself, and of 1 for arguments around 1.
+__device__ __forceinline__ float log2_of(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // The largest logit m and s = sum of 2^((x - m) k), k = log2(e) / T. The difference is formed before the
 // product: it is exact for the largest logit, and small where the terms are large. Against a maximum of
 // -infinity (masked logits so far) terms are taken from 0, so that -infinity adds 0 and not NaN.
-struct MaxSum {
+struct alignas(8) MaxSum {
   float m, s;
 };
 
@@ -25,94 +50,680 @@ __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY
 
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m), base = finite_or_zero(m);
-  return {m, a.s * exp2f((a.m - base) * k) + b.s * exp2f((b.m - base) * k)};
+  return {m, a.s * pow2((a.m - base) * k) + b.s * pow2((b.m - base) * k)};
 }
 
-struct RowTerms {
-  float loss, coef;
+// Over `lanes` (a power of two) neighbouring lanes.
+__device__ __forceinline__ MaxSum join_lanes(MaxSum t, int lanes, float k) {
+  for (int o = lanes / 2; o > 0; o >>= 1)
+    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o)}, k);
+  return t;
+}
+
+// Over a warp: the maximum as one integer reduction (of bits that order as the floats do), then the sums.
+__device__ __forceinline__ MaxSum join_warp(MaxSum t, float k) {
+  const uint32_t bits = __float_as_uint(t.m);
+  const uint32_t top = __reduce_max_sync(0xffffffffu, bits & 0x80000000u ? ~bits : bits | 0x80000000u);
+  const float m = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+  float s = t.s * pow2((t.m - finite_or_zero(m)) * k);
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return {m, s};
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(c))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return c;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 c;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(c))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return c;
+}
+
+// A granule's largest element: of bf16, two at a time.
+template <typename T>
+__device__ __forceinline__ float top_of(const uint4& raw) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+  } else {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(two(raw.x), two(raw.y)), __hmax2(two(raw.z), two(raw.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+}
+
+// The sum over a thread's granules, with base = finite_or_zero(m).
+struct RunningSum {
+  float m = -INFINITY, s = 0.f, base = 0.f;
+
+  template <typename T>
+  __device__ __forceinline__ void add(const uint4& raw, float k) {
+    constexpr int E = 16 / sizeof(T);
+    const float top = top_of<T>(raw);
+    if (top > m) {
+      s *= pow2((m - top) * k);
+      m = base = top;
+    }
+    float v[E];
+    row::unpack16<T>(v, raw);
+    const float2 less = make_float2(-base, -base), kk = make_float2(k, k);
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < E; j += 2) {
+      const float2 z = mul2(add2(make_float2(v[j], v[j + 1]), less), kk);
+      acc = add2(acc, make_float2(pow2(z.x), pow2(z.y)));
+    }
+    s += acc.x + acc.y;
+  }
+
+  __device__ __forceinline__ MaxSum get() const { return {m, s}; }
 };
 
-__device__ __forceinline__ RowTerms row_terms(const PolicyLaunch& p, int64_t i, float logp) {
-  const float w = p.weights[i], adv = p.advantages[i];
-  const float r = expf(logp - p.old_logp[i]);
-  const float whole = r * adv, cut = fminf(fmaxf(r, 1.f - p.clip_low), 1.f + p.clip_high) * adv;
-  float each = -fminf(whole, cut);
-  if (isnan(whole)) each = whole;
-  float c = whole <= cut || isnan(whole) ? -whole : 0.f;
-  if (p.ref_logp) {
-    const float d = p.ref_logp[i] - logp, e = expm1f(d);
-    each = fmaf(p.kl_coef, e - d, each);
-    c = fmaf(-p.kl_coef, e, c);
-  }
-  return {each * w, c * w};
+// The 16 bytes that start `bytes` (a multiple of 4, or of 2 with HALVES) into a and b.
+template <bool HALVES>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int bytes) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (bytes & 8)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  if (bytes & 4)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  if (HALVES && (bytes & 2))
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// The elements of a granule from `left` on become -infinity.
+template <typename T>
+__device__ __forceinline__ uint4 cut_behind(const uint4& raw, int left) {
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int j = 0; j < 16 / static_cast<int>(sizeof(T)); ++j) {
+    if (j < left) continue;
+    if constexpr (sizeof(T) == 4)
+      w[j] = 0xff800000u;
+    else
+      w[j / 2] = j % 2 ? (w[j / 2] & 0xffffu) | 0xff800000u : (w[j / 2] & 0xffff0000u) | 0xff80u;
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What a row needs beside its logits; a < 0: the row is not read.
+struct RowMeta {
+  int a;
+  float w, old, ref, adv;
+};
+
+__device__ __forceinline__ RowMeta row_meta(const PolicyLaunch& p, int64_t i) {
+  RowMeta r{-1, 0.f, 0.f, 0.f, 0.f};
+  if (i >= p.n) return r;
+  const int64_t a = row::load_id(p.targets, p.id_bytes, i);
+  if (p.weights) {
+    r.w = __ldg(p.weights + i);
+    r.old = __ldg(p.old_logp + i);
+    r.adv = __ldg(p.advantages + i);
+    if (p.ref_logp) r.ref = __ldg(p.ref_logp + i);
+    if (r.w == 0.f) return r;
+  }
+  if (a >= p.vocab) atomicOr(p.status, kDevIndex);
+  r.a = a < 0 || a >= p.vocab ? -1 : static_cast<int>(a);
+  return r;
+}
+
+// Writes the row's log-probability and term (one thread), and gives its gradient's scale c / T.
+__device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const RowMeta& r, float xa, MaxSum t,
+                                         bool writes) {
+  // The token's distance from the maximum is exact in many cases, and log2 of a sum of 1 is 0.
+  const float logp = (xa - t.m) * p.inv_temperature - log2_of(t.s) * kLn2;
+  float each = 0.f, c = 0.f;
+  if (p.weights) {
+    const float ratio = pow2((logp - r.old) * kLog2e);
+    const float whole = ratio * r.adv, cut = fminf(fmaxf(ratio, 1.f - p.clip_low), 1.f + p.clip_high) * r.adv;
+    // Not "whole <= cut": a NaN stays one.
+    each = whole > cut ? -cut : -whole;
+    c = whole > cut ? 0.f : -whole;
+    if (p.ref_logp) {
+      const float d = r.ref - logp, e = expm1f(d);
+      each = fmaf(p.kl_coef, e - d, each);
+      c = fmaf(-p.kl_coef, e, c);
+    }
+  }
+  if (writes) {
+    if (p.logp) p.logp[i] = logp;
+    if (p.row_loss) p.row_loss[i] = each * r.w;
+  }
+  return c * r.w * p.inv_temperature;
+}
+
+__device__ __forceinline__ void row_skipped(const PolicyLaunch& p, int64_t i) {
+  if (p.logp) p.logp[i] = 0.f;
+  if (p.row_loss) p.row_loss[i] = 0.f;
+}
+
+// The gradient of a granule's logits: scale (onehot - 2^((x - base) k) / s), with per = -scale / s.
+template <int E>
+__device__ __forceinline__ void gradient(float (&v)[E], float base, float k, float per) {
+  const float2 less = make_float2(-base, -base), kk = make_float2(k, k), pp = make_float2(per, per);
+#pragma unroll
+  for (int j = 0; j < E; j += 2) {
+    const float2 z = mul2(add2(make_float2(v[j], v[j + 1]), less), kk);
+    const float2 g = mul2(make_float2(pow2(z.x), pow2(z.y)), pp);
+    v[j] = g.x, v[j + 1] = g.y;
+  }
+}
+
+// Where a row lies: `head` elements before the first 16-byte address, `full` whole granules, `tail` elements.
+struct Cut {
+  int head, full, tail;
+};
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) policy_row_kernel(const PolicyLaunch p) {
-  __shared__ MaxSum part[kThreads / 32];
-  const int64_t i = blockIdx.x;
-  const int64_t a = row::load_id(p.targets, p.id_bytes, i);
-  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
-  T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd : nullptr;
-  bool live = a >= 0 && (!p.weights || p.weights[i] != 0.f);
-  if (live && a >= p.vocab) {
-    if (threadIdx.x == 0) atomicOr(p.status, kDevIndex);
-    live = false;
-  }
-  if (!live) {
-    if (threadIdx.x == 0) {
-      if (p.logp) p.logp[i] = 0.f;
-      if (p.row_loss) p.row_loss[i] = 0.f;
+__device__ __forceinline__ Cut cut_row(const T* x, int vocab) {
+  constexpr int E = 16 / sizeof(T);
+  const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  Cut c;
+  c.head = min((E - off) & (E - 1), vocab);
+  c.full = (vocab - c.head) / E;
+  c.tail = vocab - c.head - c.full * E;
+  return c;
+}
+
+// ---------------------------------------------------------------------------- rows in registers
+
+// As many rows per CTA as `tpr` threads leave room for, K granules per thread; granule 0 is the partial one
+// at the row's head where there is one. CTAs stay: the next row is on its way while this one is worked on.
+template <typename T, int K, int THREADS>
+__global__ void __launch_bounds__(THREADS) policy_held_kernel(const PolicyLaunch p) {
+  constexpr int E = 16 / sizeof(T);
+  __shared__ MaxSum part[2][THREADS / 32];
+  extern __shared__ uint4 image[];  // rows that do not start on 16 bytes, granule by granule
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
+  const int vocab = static_cast<int>(p.vocab);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  const T* logits = static_cast<const T*>(p.logits);
+  const float k = kLog2e * p.inv_temperature;
+  // The first element of this thread's granule `g` in a row at x, which may lie before the row.
+  auto start = [&](const T* x, int g) {
+    return (t + g * tpr) * E - static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+  };
+  auto fetch = [&](uint4 (&raw)[K], float& xa, int64_t i, const RowMeta& r) {
+    xa = 0.f;
+    if (r.a < 0) return;
+    const T* x = logits + i * p.ld;
+    xa = row::to_f(x[r.a]);
+#pragma unroll
+    for (int g = 0; g < K; ++g) {
+      const int e0 = start(x, g);
+      if (e0 >= 0 && e0 + E <= vocab) {
+        raw[g] = __ldcs(reinterpret_cast<const uint4*>(x + e0));
+      } else {
+        // Elements outside the row count as -infinity.
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          const bool in = e0 + j >= 0 && e0 + j < vocab;
+          if constexpr (sizeof(T) == 4) {
+            w[j] = in ? __float_as_uint(x[e0 + j]) : 0xff800000u;
+          } else {
+            const uint32_t b = in ? __bfloat16_as_ushort(x[e0 + j]) : 0xff80u;
+            w[j / 2] = j % 2 ? w[j / 2] | b << 16 : b;
+          }
+        }
+        raw[g] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
-    if (dx)
-      for (int64_t c = threadIdx.x; c < p.vocab; c += kThreads) dx[c] = row::from_f<T>(0.f);
-    return;
-  }
-  const float k = kLog2e / p.temperature;
-  MaxSum t{-INFINITY, 0.f};
-  for (int64_t c = threadIdx.x; c < p.vocab; c += kThreads) t = join(t, {row::to_f(x[c]), 1.f}, k);
-  for (int o = 16; o > 0; o >>= 1)
-    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o)}, k);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
-  const float xa = row::to_f(x[a]);  // read before any thread writes a gradient over it
-  __syncthreads();
-  t = part[0];
-  for (int w = 1; w < kThreads / 32; ++w) t = join(t, part[w], k);
-  const float logp = (xa - t.m) / p.temperature - logf(t.s);  // exactly 0 for the only token left
-  float coef = 0.f;
-  if (p.weights) {
-    const RowTerms rt = row_terms(p, i, logp);
-    coef = rt.coef;
-    if (threadIdx.x == 0) p.row_loss[i] = rt.loss;
-  }
-  if (threadIdx.x == 0 && p.logp) p.logp[i] = logp;
-  if (!dx) return;
-  const float scale = coef / p.temperature, per = -scale / t.s;
-  for (int64_t c = threadIdx.x; c < p.vocab; c += kThreads) {
-    const float e = per * exp2f((row::to_f(x[c]) - finite_or_zero(t.m)) * k);
-    dx[c] = row::from_f<T>(c == a ? e + scale : e);
+  };
+  RowMeta now = row_meta(p, first + slot), next = row_meta(p, first + step + slot);
+  uint4 raw[K], ahead[K];
+  float xa, xa_ahead;
+  fetch(raw, xa, first + slot, now);
+  int half = 0;
+  for (int64_t base_row = first; base_row < p.n; base_row += step, half ^= 1) {
+    const int64_t i = base_row + slot;
+    const RowMeta later = row_meta(p, i + 2 * step);
+    fetch(ahead, xa_ahead, i + step, next);
+    RunningSum run;
+    uint4* line = image + slot * (K * tpr + 1);
+    if (!p.aligned) {
+      if (now.a >= 0)
+#pragma unroll
+        for (int g = 0; g < K; ++g) line[t + g * tpr] = raw[g];
+      __syncthreads();
+    }
+    if (now.a >= 0) {
+      const int bytes = static_cast<int>(reinterpret_cast<uintptr_t>(logits + i * p.ld) & 15);
+#pragma unroll
+      for (int g = 0; g < K; ++g) {
+        const int q = t + g * tpr;
+        if (q * E >= vocab) continue;
+        uint4 group = p.aligned ? raw[g] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
+        if ((q + 1) * E > vocab) group = cut_behind<T>(group, vocab - q * E);
+        run.template add<T>(group, k);
+      }
+    }
+    MaxSum sum = tpr >= 32 ? join_warp(run.get(), k) : join_lanes(run.get(), tpr, k);
+    // Here every thread of the row has read the token's logit, which the gradient may be written over.
+    if (tpr <= 32) {
+      __syncwarp();
+    } else {
+      const int warp = threadIdx.x >> 5, warps = tpr >> 5, from = warp / warps * warps;
+      if ((threadIdx.x & 31) == 0) part[half][warp] = sum;
+      __syncthreads();
+      sum = part[half][from];
+      for (int w = 1; w < warps; ++w) sum = join(sum, part[half][from + w], k);
+    }
+    float scale = 0.f;
+    if (now.a >= 0)
+      scale = row_end(p, i, now, xa, sum, t == 0);
+    else if (i < p.n && t == 0)
+      row_skipped(p, i);
+    if (p.dlogits && i < p.n) {
+      T* dx = static_cast<T*>(p.dlogits) + i * p.ldd;
+      const T* x = logits + i * p.ld;
+      const float base = finite_or_zero(sum.m), per = -scale * __frcp_rn(sum.s);
+#pragma unroll
+      for (int g = 0; g < K; ++g) {
+        const int e0 = start(x, g);
+        if (e0 >= vocab) continue;
+        float v[E];
+        if (now.a >= 0) {
+          row::unpack16<T>(v, raw[g]);
+          gradient(v, base, k, per);
+          if (now.a >= e0 && now.a < e0 + E)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              if (now.a == e0 + j) v[j] += scale;
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) v[j] = 0.f;
+        }
+        if (p.same_cut && e0 >= 0 && e0 + E <= vocab) {
+          __stcs(reinterpret_cast<uint4*>(dx + e0), row::pack16(v));
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j)
+            if (e0 + j >= 0 && e0 + j < vocab) dx[e0 + j] = row::from_f<T>(v[j]);
+        }
+      }
+    }
+    now = next, next = later, xa = xa_ahead;
+#pragma unroll
+    for (int g = 0; g < K; ++g) raw[g] = ahead[g];
   }
 }
 
-__global__ void __launch_bounds__(kThreads) policy_sum_kernel(const PolicyLaunch p) {
+// ---------------------------------------------------------------------------- rows in a cluster's shared memory
+
+constexpr int kRingSlots = 3;          // of a warp: one being loaded, one worked on, one being written
+constexpr int kSlotBytes = 4608;
+constexpr int kWarpGroups = kSlotBytes / 16 - 2;  // beside the rest of the first granule, and the one read past the last
+constexpr int kMaxCluster = 16;
+
+// Two CTAs per SM, in clusters of a portable size; or, for rows beyond eight of those, CTAs of twice the size.
+template <bool WIDE>
+struct Ring {
+  static constexpr int kThreads = WIDE ? 512 : 256;
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kSmem = kWarps * kRingSlots * kSlotBytes + 128;
+  static constexpr int kCluster = WIDE ? kMaxCluster : 8;  // CTAs per row at most
+};
+
+// Writes v into a CTA of the cluster and counts its 8 bytes at that CTA's barrier (shared::cluster addresses).
+__device__ __forceinline__ void send(uint32_t addr, MaxSum v, uint32_t barrier) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(v.m),
+               "f"(v.s), "r"(barrier)
+               : "memory");
+}
+
+// A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it. The warps work on
+// their own: bulk copies bring a share's whole granules into the warp's slots and take their gradients, formed
+// in place, out; up to E - 1 elements on either side of them go through registers. Where they meet is the
+// row's sum: every warp sends its own to every CTA of the cluster, and goes on when all have arrived. (With
+// barriers over the cluster and the CTA in their place, a third of the warps' time went into those and the
+// fences they imply.)
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_ring_kernel(const PolicyLaunch p) {
+  using R = Ring<WIDE>;
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ uint8_t dyn[];
+  __shared__ MaxSum joined[2][R::kCluster * R::kWarps];  // the warps' sums of a row and the next
+  __shared__ uint64_t joined_full[2];
+  __shared__ uint64_t slot_full[R::kWarps][kRingSlots];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* slots = dyn + (128 - (ptx::smem_u32(dyn) & 127)) % 128 + warp * kRingSlots * kSlotBytes;
+  uint64_t* full = slot_full[warp];
+  const int C = p.cluster, unit = static_cast<int>(ptx::cluster_ctarank()) * R::kWarps + warp;
+  const int64_t step = gridDim.x / C, first = blockIdx.x / C;
+  const int vocab = static_cast<int>(p.vocab);
+  const int groups_each = (vocab + C * R::kWarps * E - 1) / (C * R::kWarps * E);
+  const int from = min(unit * groups_each * E, vocab), length = min(groups_each * E, vocab - from);
+  const T* logits = static_cast<const T*>(p.logits) + from;
+  const float k = kLog2e * p.inv_temperature;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < R::kWarps; ++w)
+      for (int s = 0; s < kRingSlots; ++s) ptx::mbar_init(&slot_full[w][s], 1);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&joined_full[s], 1);
+    abort_word = 0;
+    ptx::fence_barrier_init();
+  }
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  __syncthreads();
+  ptx::cluster_sync_all();  // the barriers are set up, and every CTA runs before another writes into it
+
+  uint64_t policy = 0;
+  if (lane == 0) policy = ptx::l2_policy_evict_first();
+  auto load = [&](int64_t i, const RowMeta& r, int s) {  // lane 0: this warp's share of row i into slot s
+    if (r.a < 0) return;
+    const T* x = logits + i * p.ld;
+    const Cut c = cut_row(x, length);
+    ptx::mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(c.full) * 16u);
+    if (c.full > 0)
+      ptx::bulk_load_hint(ptx::smem_u32(slots + s * kSlotBytes + (c.head ? 16 : 0)), x + c.head,
+                          static_cast<uint32_t>(c.full) * 16u, &full[s], policy);
+  };
+  // The element outside the granules that this lane holds, or -1.
+  auto edge_of = [&](const Cut& c) {
+    if (lane < c.head) return lane;
+    if (lane >= 16 && lane - 16 < c.tail) return c.head + c.full * E + lane - 16;
+    return -1;
+  };
+  auto fetch = [&](float& xa, float& xe, int64_t i, const RowMeta& r) {  // the token's logit and the edge's
+    xa = xe = 0.f;
+    if (r.a < 0) return;
+    const T* x = logits + i * p.ld;
+    xa = row::to_f(x[r.a - from]);
+    const int e = edge_of(cut_row(x, length));
+    if (e >= 0) xe = row::to_f(x[e]);
+  };
+
+  RowMeta now = row_meta(p, first), next = row_meta(p, first + step), third = row_meta(p, first + 2 * step);
+  float xa, xe, xa_next, xe_next;
+  fetch(xa, xe, first, now);
+  if (lane == 0) {
+    load(first, now, 0);
+    load(first + step, next, 1);
+  }
+  uint32_t parity = 0, joined_parity = 0;  // bit s: of the next phase of a slot, of a half, to wait for
+  int s = 0, half = 0;
+  for (int64_t i = first; i < p.n; i += step) {
+    const RowMeta fourth = row_meta(p, i + 3 * step);
+    fetch(xa_next, xe_next, i + step, next);
+    const Cut c = cut_row(logits + i * p.ld, length);
+    // The share lies in the slot as it does around 16-byte addresses; `data` are its whole granules.
+    uint4* line = reinterpret_cast<uint4*>(slots + s * kSlotBytes);
+    uint4* data = line + (c.head ? 1 : 0);
+    const int edge = edge_of(c);
+    T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd + from : nullptr;
+    if (now.a >= 0) {
+      // A wait that runs out is recorded; the launch goes on to its end on whatever has come, so that no warp of
+      // the cluster is left waiting.
+      ptx::wait_fast(&full[s], (parity >> s) & 1u, abort_flag, p.status);
+      parity ^= 1u << s;
+      const int bytes = c.head ? 16 - c.head * static_cast<int>(sizeof(T)) : 0;
+      if (c.head || c.tail) {
+        if (edge >= 0) reinterpret_cast<T*>(line)[bytes / static_cast<int>(sizeof(T)) + edge] = row::from_f<T>(xe);
+        __syncwarp();
+      }
+      // Whole groups first, then the last one where it is not.
+      RunningSum run;
+      const int whole = length / E;
+      if (bytes == 0) {
+#pragma unroll 4
+        for (int q = lane; q < whole; q += 32) run.template add<T>(line[q], k);
+      } else {
+#pragma unroll 4
+        for (int q = lane; q < whole; q += 32) run.template add<T>(shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes), k);
+      }
+      if (whole * E < length && lane == 31)
+        run.template add<T>(cut_behind<T>(shifted<sizeof(T) == 2>(line[whole], line[whole + 1], bytes), length - whole * E), k);
+      MaxSum sum = join_warp(run.get(), k);
+      // A half is written again two rows on, when every warp has sent its sum of the row between, and so has read
+      // this one's.
+      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[half], static_cast<uint32_t>(C * R::kWarps * sizeof(MaxSum)));
+      if (lane < C)
+        send(ptx::map_shared(ptx::smem_u32(&joined[half][unit]), lane), sum,
+             ptx::map_shared(ptx::smem_u32(&joined_full[half]), lane));
+      ptx::wait_fast(&joined_full[half], (joined_parity >> half) & 1u, abort_flag, p.status);
+      joined_parity ^= 1u << half;
+      sum = {-INFINITY, 0.f};
+      for (int w = lane; w < C * R::kWarps; w += 32) sum = join(sum, joined[half][w], k);
+      sum = join_warp(sum, k);
+      half ^= 1;
+      const float scale = row_end(p, i, now, xa, sum, unit == 0 && lane == 0);
+      if (dx) {
+        const float base = finite_or_zero(sum.m), per = -scale * __frcp_rn(sum.s);
+        const int inside = now.a - from - c.head;  // the token's place in this share, if it has one
+        const int token_q = inside >= 0 ? inside / E : -1, token_j = inside & (E - 1);
+#pragma unroll 4
+        for (int q = lane; q < c.full; q += 32) {
+          float v[E];
+          row::unpack16<T>(v, data[q]);
+          gradient(v, base, k, per);
+          if (q == token_q)
+#pragma unroll
+            for (int j = 0; j < E; ++j)
+              if (j == token_j) v[j] += scale;
+          data[q] = row::pack16(v);
+        }
+        if (edge >= 0) {
+          const float g = per * pow2((xe - base) * k);
+          dx[edge] = row::from_f<T>(from + edge == now.a ? g + scale : g);
+        }
+      }
+    } else {
+      if (unit == 0 && lane == 0) row_skipped(p, i);
+      if (dx) {
+        for (int q = lane; q < c.full; q += 32) data[q] = make_uint4(0, 0, 0, 0);
+        if (edge >= 0) dx[edge] = row::from_f<T>(0.f);
+      }
+    }
+    if (dx && p.same_cut) ptx::fence_async_smem();
+    __syncwarp();  // every lane is done with the slot
+    if (dx && p.same_cut) {
+      if (lane == 0) {
+        if (c.full > 0) ptx::bulk_store(dx + c.head, ptx::smem_u32(data), static_cast<uint32_t>(c.full) * 16u);
+        ptx::bulk_commit();
+      }
+    } else if (dx) {
+      const T* from_smem = reinterpret_cast<const T*>(data);
+      for (int e = lane; e < c.full * E; e += 32) dx[c.head + e] = from_smem[e];
+      __syncwarp();
+    }
+    // The slot of the row before takes the row after next, once its gradient has left it.
+    const int spare = s == 0 ? 2 : s - 1;
+    if (lane == 0) {
+      ptx::bulk_wait_read_allow<1>();
+      ptx::fence_async_smem();
+      load(i + 2 * step, third, spare);
+    }
+    s = s == 2 ? 0 : s + 1;
+    now = next, next = third, third = fourth, xa = xa_next, xe = xe_next;
+  }
+  // Rows behind the last are never loaded, so no load is on its way here, unless a wait ran out.
+  if (lane == 0) {
+    if (*abort_flag)
+      for (int q = 0; q < kRingSlots; ++q)
+        ptx::wait_bounded(&full[q], (parity >> q) & 1u, abort_flag, p.status, ptx::kDrainLimitNs, false);
+    ptx::bulk_wait0();
+  }
+  __syncwarp();
+  ptx::cluster_sync_all();  // nobody writes into a CTA that has ended
+}
+
+// ---------------------------------------------------------------------------- rows read twice
+
+constexpr int kTwiceThreads = 512;
+
+// One CTA per row: rows beyond a cluster's shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const PolicyLaunch p) {
+  __shared__ MaxSum part[kTwiceThreads / 32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t i = blockIdx.x;
+  const RowMeta r = row_meta(p, i);
+  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
+  T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd : nullptr;
+  if (r.a < 0) {
+    if (threadIdx.x == 0) row_skipped(p, i);
+    if (dx)
+      for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) dx[c] = row::from_f<T>(0.f);
+    return;
+  }
+  const float k = kLog2e * p.inv_temperature;
+  MaxSum t{-INFINITY, 0.f};
+  float base = 0.f;
+  for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) {
+    const float v = row::to_f(x[c]);
+    if (v > t.m) {
+      t.s *= pow2((t.m - v) * k);
+      t.m = base = v;
+    }
+    t.s += pow2((v - base) * k);
+  }
+  t = join_warp(t, k);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = t;
+  const float xa = row::to_f(x[r.a]);  // read before any thread writes a gradient over it
+  __syncthreads();
+  t = part[0];
+  for (int w = 1; w < kTwiceThreads / 32; ++w) t = join(t, part[w], k);
+  const float scale = row_end(p, i, r, xa, t, threadIdx.x == 0);
+  if (!dx) return;
+  base = finite_or_zero(t.m);
+  const float per = -scale * __frcp_rn(t.s);
+  for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) {
+    const float e = per * pow2((row::to_f(x[c]) - base) * k);
+    dx[c] = row::from_f<T>(c == r.a ? e + scale : e);
+  }
+}
+
+// ---------------------------------------------------------------------------- the loss
+
+constexpr int kSumThreads = 1024;
+
+__global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const PolicyLaunch p) {
   __shared__ float red[32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
   float acc = 0.f;
-  for (int64_t i = threadIdx.x; i < p.n; i += kThreads) acc += p.row_loss[i];
+  for (int64_t i = threadIdx.x; i < p.n; i += kSumThreads) acc += __ldcg(p.row_loss + i);
   acc = row::block_sum(acc, red);
   if (threadIdx.x == 0) *p.loss = acc;
 }
 
+template <typename T, int K, int THREADS>
+cudaError_t launch_held(PolicyLaunch& p, int granules, int sms, cudaStream_t stream) {
+  auto* kernel = policy_held_kernel<T, K, THREADS>;
+  const int need = (granules + K - 1) / K;
+  p.tpr = need > 16 ? (need + 31) / 32 * 32 : 1;
+  while (p.tpr < need) p.tpr *= 2;
+  const int rows = p.tpr >= 256 ? 1 : 256 / p.tpr, threads = p.tpr * rows;
+  int per_sm = 0;
+  const size_t smem = p.aligned ? 0 : static_cast<size_t>(rows) * (K * p.tpr + 1) * 16;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * std::max(per_sm, 1), (p.n + rows - 1) / rows);
+  return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), threads, smem, stream, p);
+}
+
+// How many clusters of `size` CTAs of the ring kernel fit on the GPU at once. A property of the device: asked for
+// once (the caller holds the library's lock).
+template <typename T, bool WIDE>
+cudaError_t resident_clusters(int size, int* clusters) {
+  constexpr int kMaxDevices = 64;
+  static int known[kMaxDevices][kMaxCluster + 1];  // 1 + the number
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < kMaxDevices ? known[dev][size] - 1 : -1;
+  if (n < 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(Ring<WIDE>::kThreads);
+    cfg.dynamicSmemBytes = Ring<WIDE>::kSmem;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(size);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, WIDE>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) known[dev][size] = n + 1;
+  }
+  *clusters = n;
+  return cudaSuccess;
+}
+
+// Whether a row fits the shared memory of a cluster that fits the GPU; if so, launches. Of the cluster sizes
+// that hold a row, the one with the most CTAs on the GPU at once, so that few SMs are left over.
+template <typename T, bool WIDE>
+cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
+  using R = Ring<WIDE>;
+  constexpr int E = 16 / sizeof(T);
+  *launched = false;
+  constexpr int64_t per_cta = R::kWarps * kWarpGroups;
+  // Two CTAs at least: the sums travel by asynchronous stores, which only a cluster launch has.
+  const int64_t groups = (p.vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
+  if (least > R::kCluster) return cudaSuccess;
+  cudaError_t e =
+      cudaFuncSetAttribute(policy_ring_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+  if (e == cudaSuccess && WIDE)
+    e = cudaFuncSetAttribute(policy_ring_kernel<T, WIDE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int best = 0;
+  for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
+    int n = 0;
+    e = resident_clusters<T, WIDE>(size, &n);
+    if (e == cudaSuccess && n * size > best * p.cluster) best = n, p.cluster = size;
+  }
+  if (e != cudaSuccess || best == 0) return e;
+  *launched = true;
+  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(p.n, best) * p.cluster);
+  return row::launch(policy_ring_kernel<T, WIDE>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
+}
+
+template <typename T>
+cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T);
+  const size_t step = static_cast<size_t>(p.ld) * sizeof(T) % 16;
+  p.aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (p.n == 1 || step == 0);
+  p.same_cut = p.dlogits && (reinterpret_cast<uintptr_t>(p.dlogits) - reinterpret_cast<uintptr_t>(p.logits)) % 16 == 0 &&
+               (p.n == 1 || static_cast<size_t>(p.ldd) * sizeof(T) % 16 == step);
+  // Granules of a row that starts anywhere.
+  const int64_t granules = (p.vocab + 2 * (E - 1)) / E;
+  if (granules <= 256) return launch_held<T, 1, 256>(p, static_cast<int>(granules), sms, stream);
+  if (granules <= 512) return launch_held<T, 2, 256>(p, static_cast<int>(granules), sms, stream);
+  if (granules <= 1024) return launch_held<T, 4, 256>(p, static_cast<int>(granules), sms, stream);
+  if (granules <= 2048) return launch_held<T, 4, 512>(p, static_cast<int>(granules), sms, stream);
+  bool launched = false;
+  p.cluster = 0;
+  cudaError_t e = launch_ring<T, false>(p, stream, &launched);
+  if (e == cudaSuccess && !launched) e = launch_ring<T, true>(p, stream, &launched);
+  if (e != cudaSuccess || launched) return e;
+  return row::launch(policy_twice_kernel<T>, dim3(static_cast<unsigned>(p.n)), kTwiceThreads, 0, stream, p);
+}
+
 }  // namespace
 
-cudaError_t launch_policy(const PolicyLaunch& p, cudaStream_t stream) {
+cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream) {
   if (p.n > 0) {
-    if (p.dtype == 0)
-      policy_row_kernel<float><<<static_cast<unsigned>(p.n), kThreads, 0, stream>>>(p);
-    else
-      policy_row_kernel<__nv_bfloat16><<<static_cast<unsigned>(p.n), kThreads, 0, stream>>>(p);
+    const cudaError_t e = p.dtype == 0 ? launch_rows<float>(p, sms, stream) : launch_rows<__nv_bfloat16>(p, sms, stream);
+    if (e != cudaSuccess) return e;
   }
-  if (p.loss) policy_sum_kernel<<<1, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.loss ? row::launch(policy_sum_kernel, dim3(1), kSumThreads, 0, stream, p) : cudaSuccess;
 }
 
 }  // namespace dmuon

@@ -36,7 +36,7 @@ constexpr float kMinScale = 1.17549435e-38f;
 
 __device__ __forceinline__ float scale_of(unsigned top_bits) {
   const float top = __uint_as_float(top_bits);
-  return top == 0.f ? 1.f : (top < kFp8Max * kMinScale ? kMinScale : top / kFp8Max);
+  return top == 0.f ? 1.f : (top < kFp8Max * kMinScale ? kMinScale : top * (1.f / kFp8Max));
 }
 
 // Largest |y| of the block as the bits of a non-negative float; a NaN is larger than every number.
@@ -124,9 +124,10 @@ __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[32]
 
 // ---------------------------------------------------------------------------- forward
 
-// THREADS: the most of a CTA. REGS: gains stay in registers. AHEAD: the next row is loaded early.
-template <typename T, int K, bool FP8, int THREADS, bool REGS, bool AHEAD>
-__global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
+// THREADS: the most of a CTA. HELD: gains stay in registers and the next row is loaded early; without it, for
+// longer rows, a thread has fewer registers and more CTAs overlap.
+template <typename T, int K, bool FP8, int THREADS, bool HELD>
+__global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   using G = Granule<T>;
   constexpr int E = G::E;
   __shared__ float red[2][32][1];
@@ -141,8 +142,8 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNorm
   T* h = p.h ? static_cast<T*>(p.h) + (first + slot) * p.ldh : nullptr;
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
   auto start = [&](int k) { return (t + k * tpr) * E - shift; };
-  float gain[REGS ? K : 1][E];
-  if (REGS)
+  float gain[HELD ? K : 1][E];
+  if (HELD)
 #pragma unroll
     for (int k = 0; k < K; ++k) load_gain(gain[k], p.gain, start(k), dim);
 
@@ -167,11 +168,11 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNorm
       rr[k] = in && r ? G::load(r, start(k), dim) : make_uint4(0, 0, 0, 0);
     }
   };
-  if (AHEAD) fetch(first + slot);
+  if (HELD) fetch(first + slot);
   int half = 0;
   for (int64_t base = first; base < p.n; base += step, half ^= 1) {
     const int64_t i = base + slot;
-    if (!AHEAD) fetch(i);
+    if (!HELD) fetch(i);
     float v[K][E];
     float s[1] = {0.f};
 #pragma unroll
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNorm
     }
     x += step * p.ldx;
     if (r) r += step * p.ldr;
-    if (AHEAD && base + step < p.n) fetch(i + step);
+    if (HELD && base + step < p.n) fetch(i + step);
     if (h && i < p.n)
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -215,9 +216,9 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNorm
     const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+      if (!HELD) load_gain(gain[0], p.gain, start(k), dim);
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[k][j] = v[k][j] * rho * gain[REGS ? k : 0][j];
+      for (int j = 0; j < E; ++j) v[k][j] = v[k][j] * rho * gain[HELD ? k : 0][j];
     }
     if constexpr (!FP8) {
       T* y = static_cast<T*>(p.y) + i * p.ldy;
@@ -258,8 +259,8 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_rows_kernel(const RmsNorm
         const int e0 = start(k);
         if (i >= p.n || e0 >= dim) continue;
         const int part = max(e0, 0) / group, border = (part + 1) * group;
-        const float inv = 1.f / scale_of(top[part]);
-        const float inv_next = border < e0 + E && border < dim ? 1.f / scale_of(top[part + 1]) : inv;
+        const float inv = __frcp_rn(scale_of(top[part]));
+        const float inv_next = border < e0 + E && border < dim ? __frcp_rn(scale_of(top[part + 1])) : inv;
         uint32_t w[E / 4];
 #pragma unroll
         for (int j = 0; j < E; j += 2) {
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormL
     unsigned top = 0;
     for (int64_t c = begin + threadIdx.x; c < end; c += threads) top = max(top, __float_as_uint(fabsf(value(c))));
     const float scale = scale_of(block_top(top, redu));
-    const float inv = 1.f / scale;
+    const float inv = __frcp_rn(scale);
     if (threadIdx.x == 0) p.scales[i * parts + k] = scale;
     for (int64_t c = begin + threadIdx.x; c < end; c += threads) {
       const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
@@ -597,6 +598,7 @@ int row_threads(int granules, int k) {
   return t;
 }
 
+constexpr size_t kPlainSmem = 40 * 1024;  // dynamic shared memory that needs no opt-in, beside the static one
 constexpr int kMaxPerSm = 16;  // CTAs (of 160 threads at least)
 
 struct RowGrid {
@@ -618,9 +620,9 @@ cudaError_t row_grid(RowGrid& g, void (*kernel)(P), int tpr, int64_t n, size_t s
   return cudaSuccess;
 }
 
-template <typename T, int K, bool FP8, int THREADS, bool REGS, bool AHEAD>
+template <typename T, int K, bool FP8, int THREADS, bool HELD>
 cudaError_t launch_rows(RmsNormLaunch& p, int granules, int sms, cudaStream_t stream) {
-  auto* kernel = add_rmsnorm_rows_kernel<T, K, FP8, THREADS, REGS, AHEAD>;
+  auto* kernel = add_rmsnorm_rows_kernel<T, K, FP8, THREADS, HELD>;
   constexpr int E = Granule<T>::E;
   size_t per_row = 0;
   p.parts = 0, p.stage = 0;
@@ -640,7 +642,7 @@ cudaError_t launch_rows(RmsNormLaunch& p, int granules, int sms, cudaStream_t st
   }
   const int tpr = std::max(row_threads(granules, K), p.sum_threads);
   const size_t smem = per_row * (tpr >= kThreads ? 1 : kThreads / tpr);
-  if (smem > 48 * 1024) {
+  if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
@@ -655,20 +657,19 @@ template <typename T, bool FP8>
 cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   const int granules = row_granules({{p.x, p.ldx}, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n,
                                     p.dim, sizeof(T));
-  // CTAs of 256 threads as long as a row's gains fit their registers beside it, then of up to 512, then 1024.
   // The order of the sum is that of the kernel that takes aligned rows of this length.
   const int whole = static_cast<int>((p.dim + Granule<T>::E - 1) / Granule<T>::E);
-  p.sum_threads = std::min(whole <= 256 ? row_threads(whole, 1)
-                           : whole <= 512 ? row_threads(whole, 2) : row_threads(whole, 4), kMaxThreads);
+  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;  // 16 and 32 elements per thread
+  p.sum_threads = std::min(
+      row_threads(whole, whole <= 256 ? 1 : whole <= 512 ? 2 : whole <= 256 * kHeld ? kHeld : kLong), kMaxThreads);
   if (granules == 0)
     return row::launch(add_rmsnorm_kernel<T>, dim3(static_cast<unsigned>(p.n)), std::max(32, p.sum_threads), 0, stream, p);
-  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true, true>(p, granules, sms, stream);
-  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true, true>(p, granules, sms, stream);
-  if constexpr (sizeof(T) == 4) {
-    if (granules <= 1024) return launch_rows<T, 4, FP8, 256, true, true>(p, granules, sms, stream);
-    if (granules > 2048) return launch_rows<T, 4, FP8, 1024, false, false>(p, granules, sms, stream);
-  }
-  return launch_rows<T, 4, FP8, 512, false, true>(p, granules, sms, stream);
+  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true>(p, granules, sms, stream);
+  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true>(p, granules, sms, stream);
+  if (granules <= 256 * kHeld) return launch_rows<T, kHeld, FP8, 256, true>(p, granules, sms, stream);
+  if (std::max(row_threads(granules, kLong), p.sum_threads) <= 320)
+    return launch_rows<T, kLong, FP8, 320, false>(p, granules, sms, stream);
+  return launch_rows<T, kLong, FP8, 512, false>(p, granules, sms, stream);
 }
 
 template <typename T, int K, int THREADS, bool REGS, bool AHEAD>
@@ -677,7 +678,7 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   // Sums of long rows, or the line in which a CTA's short rows join.
   const int tpr = row_threads(granules, K), rows = tpr >= kThreads ? 1 : kThreads / tpr;
   const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * 16 / sizeof(T) * 4;
-  if (smem > 48 * 1024) {
+  if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }

@@ -45,6 +45,10 @@ __device__ __forceinline__ uint4 pack16(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ uint4 pack16(const float (&v)[4]) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+
 // Token id `i` of an int32 or int64 list.
 __device__ __forceinline__ int64_t load_id(const void* ids, int id_bytes, int64_t i) {
   return id_bytes == 8 ? static_cast<const int64_t*>(ids)[i] : static_cast<int64_t>(static_cast<const int*>(ids)[i]);
@@ -64,19 +68,23 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 }
 
 // Launches `kernel`, which waits for the preceding grid itself (griddepcontrol.wait), with programmatic stream
-// serialisation: its CTAs may be set up while that grid drains.
+// serialisation: its CTAs may be set up while that grid drains. `cluster` CTAs form a cluster.
 template <typename P>
-cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p,
+                   int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2] = {};
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

@@ -345,6 +345,11 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t smem_dst, const void* sr
       : "memory");
 }
 
+// `bytes` (a multiple of 16) of shared memory to 16-byte aligned global memory, in the current bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_src), "r"(bytes)
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read0() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 // Wait until at most N of this thread's most recent bulk groups are still reading shared memory.
