@@ -61,13 +61,32 @@ __device__ __forceinline__ MaxSum join_lanes(MaxSum t, int lanes, float k) {
 }
 
 // Over a warp: the maximum as one integer reduction (of bits that order as the floats do), then the sums.
-__device__ __forceinline__ MaxSum join_warp(MaxSum t, float k) {
-  const uint32_t bits = __float_as_uint(t.m);
+__device__ __forceinline__ float warp_max(float m) {
+  const uint32_t bits = __float_as_uint(m);
   const uint32_t top = __reduce_max_sync(0xffffffffu, bits & 0x80000000u ? ~bits : bits | 0x80000000u);
-  const float m = __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
-  float s = t.s * pow2((t.m - finite_or_zero(m)) * k);
+  return __uint_as_float(top & 0x80000000u ? top & 0x7fffffffu : ~top);
+}
+
+__device__ __forceinline__ float warp_sum(float s) {
+#pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return {m, s};
+  return s;
+}
+
+__device__ __forceinline__ MaxSum join_warp(MaxSum t, float k) {
+  const float m = warp_max(t.m);
+  return {m, warp_sum(t.s * pow2((t.m - finite_or_zero(m)) * k))};
+}
+
+// Of n sums in shared memory, by a warp.
+__device__ __forceinline__ MaxSum join_list(const MaxSum* list, int n, float k) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, s = 0.f;
+  for (int w = lane; w < n; w += 32) m = fmaxf(m, list[w].m);
+  m = warp_max(m);
+  const float base = finite_or_zero(m);
+  for (int w = lane; w < n; w += 32) s = fmaf(list[w].s, pow2((list[w].m - base) * k), s);
+  return {m, warp_sum(s)};
 }
 
 // Two fp32 operations in one instruction.
@@ -86,43 +105,60 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return c;
 }
 
-// A granule's largest element: of bf16, two at a time.
+// The largest element of granules; of bf16, two at a time. (NaN is left to the sum.)
 template <typename T>
-__device__ __forceinline__ float top_of(const uint4& raw) {
-  if constexpr (sizeof(T) == 4) {
-    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
-  } else {
-    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(two(raw.x), two(raw.y)), __hmax2(two(raw.z), two(raw.w)));
-    return fmaxf(__low2float(m), __high2float(m));
+struct Largest;
+
+template <>
+struct Largest<float> {
+  float m = -INFINITY;
+  __device__ __forceinline__ void add(const uint4& raw) {
+    m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)),
+                       fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w))));
   }
+  __device__ __forceinline__ float get() const { return m; }
+};
+
+template <>
+struct Largest<__nv_bfloat16> {
+  uint32_t m = 0xff80ff80u;
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  __device__ __forceinline__ void add(const uint4& raw) {
+    const __nv_bfloat162 t = __hmax2(__hmax2(two(raw.x), two(raw.y)), __hmax2(two(raw.z), two(raw.w)));
+    const __nv_bfloat162 n = __hmax2(two(m), t);
+    m = *reinterpret_cast<const uint32_t*>(&n);
+  }
+  __device__ __forceinline__ float get() const {
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+
+// A granule of -infinity.
+template <typename T>
+__device__ __forceinline__ uint4 lowest() {
+  const uint32_t w = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(w, w, w, w);
 }
 
-// The sum over a thread's granules, with base = finite_or_zero(m).
-struct RunningSum {
-  float m = -INFINITY, s = 0.f, base = 0.f;
+// The sum of 2^((x - base) k) over granules.
+struct Terms {
+  float2 less, kk, acc;
+
+  __device__ __forceinline__ Terms(float base, float k)
+      : less(make_float2(-base, -base)), kk(make_float2(k, k)), acc(make_float2(0.f, 0.f)) {}
 
   template <typename T>
-  __device__ __forceinline__ void add(const uint4& raw, float k) {
+  __device__ __forceinline__ void add(const uint4& raw) {
     constexpr int E = 16 / sizeof(T);
-    const float top = top_of<T>(raw);
-    if (top > m) {
-      s *= pow2((m - top) * k);
-      m = base = top;
-    }
     float v[E];
     row::unpack16<T>(v, raw);
-    const float2 less = make_float2(-base, -base), kk = make_float2(k, k);
-    float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < E; j += 2) {
       const float2 z = mul2(add2(make_float2(v[j], v[j + 1]), less), kk);
       acc = add2(acc, make_float2(pow2(z.x), pow2(z.y)));
     }
-    s += acc.x + acc.y;
   }
-
-  __device__ __forceinline__ MaxSum get() const { return {m, s}; }
+  __device__ __forceinline__ float get() const { return acc.x + acc.y; }
 };
 
 // The 16 bytes that start `bytes` (a multiple of 4, or of 2 with HALVES) into a and b.
@@ -178,6 +214,18 @@ __device__ __forceinline__ RowMeta row_meta(const PolicyLaunch& p, int64_t i) {
   return r;
 }
 
+// exp(d) - 1: near 0 by its series up to d^7 / 7!, 1e-8 off at 1/4.
+__device__ __forceinline__ float exp_less_1(float d) {
+  float r = 1.f / 5040.f;
+  r = fmaf(r, d, 1.f / 720.f);
+  r = fmaf(r, d, 1.f / 120.f);
+  r = fmaf(r, d, 1.f / 24.f);
+  r = fmaf(r, d, 1.f / 6.f);
+  r = fmaf(r, d, 0.5f);
+  r = fmaf(r * d, d, d);
+  return fabsf(d) < 0.25f ? r : pow2(d * kLog2e) - 1.f;
+}
+
 // Writes the row's log-probability and term (one thread), and gives its gradient's scale c / T.
 __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const RowMeta& r, float xa, MaxSum t,
                                          bool writes) {
@@ -191,7 +239,7 @@ __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const
     each = whole > cut ? -cut : -whole;
     c = whole > cut ? 0.f : -whole;
     if (p.ref_logp) {
-      const float d = r.ref - logp, e = expm1f(d);
+      const float d = r.ref - logp, e = exp_less_1(d);
       each = fmaf(p.kl_coef, e - d, each);
       c = fmaf(-p.kl_coef, e, c);
     }
@@ -292,7 +340,7 @@ __global__ void __launch_bounds__(THREADS) policy_held_kernel(const PolicyLaunch
     const int64_t i = base_row + slot;
     const RowMeta later = row_meta(p, i + 2 * step);
     fetch(ahead, xa_ahead, i + step, next);
-    RunningSum run;
+    MaxSum sum{-INFINITY, 0.f};
     uint4* line = image + slot * (K * tpr + 1);
     if (!p.aligned) {
       if (now.a >= 0)
@@ -302,16 +350,23 @@ __global__ void __launch_bounds__(THREADS) policy_held_kernel(const PolicyLaunch
     }
     if (now.a >= 0) {
       const int bytes = static_cast<int>(reinterpret_cast<uintptr_t>(logits + i * p.ld) & 15);
+      uint4 group[K];
+      Largest<T> top;
 #pragma unroll
       for (int g = 0; g < K; ++g) {
         const int q = t + g * tpr;
-        if (q * E >= vocab) continue;
-        uint4 group = p.aligned ? raw[g] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
-        if ((q + 1) * E > vocab) group = cut_behind<T>(group, vocab - q * E);
-        run.template add<T>(group, k);
+        group[g] = p.aligned || q * E >= vocab ? raw[g] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
+        if ((q + 1) * E > vocab) group[g] = cut_behind<T>(group[g], vocab - q * E);
+        top.add(group[g]);
       }
+      sum.m = top.get();
+      Terms terms(finite_or_zero(sum.m), k);
+#pragma unroll
+      for (int g = 0; g < K; ++g)
+        if ((t + g * tpr) * E < vocab) terms.template add<T>(group[g]);
+      sum.s = terms.get();
     }
-    MaxSum sum = tpr >= 32 ? join_warp(run.get(), k) : join_lanes(run.get(), tpr, k);
+    sum = tpr >= 32 ? join_warp(sum, k) : join_lanes(sum, tpr, k);
     // Here every thread of the row has read the token's logit, which the gradient may be written over.
     if (tpr <= 32) {
       __syncwarp();
@@ -366,8 +421,13 @@ __global__ void __launch_bounds__(THREADS) policy_held_kernel(const PolicyLaunch
 
 constexpr int kRingSlots = 3;          // of a warp: one being loaded, one worked on, one being written
 constexpr int kSlotBytes = 4608;
+constexpr int kBatch = 4;
 constexpr int kWarpGroups = kSlotBytes / 16 - 2;  // beside the rest of the first granule, and the one read past the last
 constexpr int kMaxCluster = 16;
+// Rows whose sums are on their way or being read, of those that are read at all. A warp sends its sum of the
+// n-th when it has joined the (n - 2)-th: then every warp has sent that one, and before it has read the
+// (n - 4)-th, whose place the n-th takes.
+constexpr int kJoins = 4;
 
 // Two CTAs per SM, in clusters of a portable size; or, for rows beyond eight of those, CTAs of twice the size.
 template <bool WIDE>
@@ -385,19 +445,54 @@ __device__ __forceinline__ void send(uint32_t addr, MaxSum v, uint32_t barrier) 
                : "memory");
 }
 
+// What a row needs beside its logits, one word per lane, so that one load per warp brings all of it and nothing
+// waits for it until its row is near: lanes 0 and 1 the token's low and high word, then weight, old
+// log-probability, advantage and reference.
+struct LaneMeta {
+  const char* at = nullptr;
+  int64_t stride = 4;
+
+  __device__ __forceinline__ LaneMeta(const PolicyLaunch& p, int lane) {
+    if (lane < 2 && 4 * lane < p.id_bytes) {
+      at = static_cast<const char*>(p.targets) + 4 * lane;
+      stride = p.id_bytes;
+    } else if (lane >= 2 && lane < 6) {
+      const float* from = lane == 2 ? p.weights : lane == 3 ? p.old_logp : lane == 4 ? p.advantages : p.ref_logp;
+      at = reinterpret_cast<const char*>(from);
+    }
+  }
+  __device__ __forceinline__ uint32_t load(int64_t i, int64_t n) const {
+    return at && i < n ? __ldg(reinterpret_cast<const uint32_t*>(at + i * stride)) : 0u;
+  }
+};
+
+// The row's token, or -1: the row is not read.
+__device__ __forceinline__ int token_of(const PolicyLaunch& p, uint32_t word, int64_t i) {
+  const uint32_t lo = __shfl_sync(0xffffffffu, word, 0);
+  const int hi = p.id_bytes == 8 ? static_cast<int>(__shfl_sync(0xffffffffu, word, 1)) : static_cast<int>(lo) >> 31;
+  const float w = __uint_as_float(__shfl_sync(0xffffffffu, word, 2));
+  if (i >= p.n || hi < 0 || (p.weights && w == 0.f)) return -1;
+  if (hi > 0 || lo >= static_cast<uint32_t>(p.vocab)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(p.status, kDevIndex);
+    return -1;
+  }
+  return static_cast<int>(lo);
+}
+
 // A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it. The warps work on
 // their own: bulk copies bring a share's whole granules into the warp's slots and take their gradients, formed
 // in place, out; up to E - 1 elements on either side of them go through registers. Where they meet is the
 // row's sum: every warp sends its own to every CTA of the cluster, and goes on when all have arrived. (With
 // barriers over the cluster and the CTA in their place, a third of the warps' time went into those and the
 // fences they imply.)
-template <typename T, bool WIDE>
+// EDGES: shares that are not whole granules.
+template <typename T, bool WIDE, bool EDGES>
 __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_ring_kernel(const PolicyLaunch p) {
   using R = Ring<WIDE>;
   constexpr int E = 16 / sizeof(T);
   extern __shared__ uint8_t dyn[];
-  __shared__ MaxSum joined[2][R::kCluster * R::kWarps];  // the warps' sums of a row and the next
-  __shared__ uint64_t joined_full[2];
+  __shared__ MaxSum joined[kJoins][R::kCluster * R::kWarps];
+  __shared__ uint64_t joined_full[kJoins];
   __shared__ uint64_t slot_full[R::kWarps][kRingSlots];
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
@@ -414,7 +509,7 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
   if (threadIdx.x == 0) {
     for (int w = 0; w < R::kWarps; ++w)
       for (int s = 0; s < kRingSlots; ++s) ptx::mbar_init(&slot_full[w][s], 1);
-    for (int s = 0; s < 2; ++s) ptx::mbar_init(&joined_full[s], 1);
+    for (int s = 0; s < kJoins; ++s) ptx::mbar_init(&joined_full[s], 1);
     abort_word = 0;
     ptx::fence_barrier_init();
   }
@@ -425,102 +520,152 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
 
   uint64_t policy = 0;
   if (lane == 0) policy = ptx::l2_policy_evict_first();
-  auto load = [&](int64_t i, const RowMeta& r, int s) {  // lane 0: this warp's share of row i into slot s
-    if (r.a < 0) return;
-    const T* x = logits + i * p.ld;
-    const Cut c = cut_row(x, length);
+  auto cut = [&](int64_t i) { return EDGES ? cut_row(logits + i * p.ld, length) : Cut{0, length / E, 0}; };
+  auto load = [&](int64_t i, int a, int s) {  // lane 0: this warp's share of row i into slot s
+    if (a < 0) return;
+    const Cut c = cut(i);
     ptx::mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(c.full) * 16u);
     if (c.full > 0)
-      ptx::bulk_load_hint(ptx::smem_u32(slots + s * kSlotBytes + (c.head ? 16 : 0)), x + c.head,
+      ptx::bulk_load_hint(ptx::smem_u32(slots + s * kSlotBytes + (c.head ? 16 : 0)), logits + i * p.ld + c.head,
                           static_cast<uint32_t>(c.full) * 16u, &full[s], policy);
   };
   // The element outside the granules that this lane holds, or -1.
   auto edge_of = [&](const Cut& c) {
+    if (!EDGES) return -1;
     if (lane < c.head) return lane;
     if (lane >= 16 && lane - 16 < c.tail) return c.head + c.full * E + lane - 16;
     return -1;
   };
-  auto fetch = [&](float& xa, float& xe, int64_t i, const RowMeta& r) {  // the token's logit and the edge's
-    xa = xe = 0.f;
-    if (r.a < 0) return;
+  // The token's logit and the edge's, as they lie in memory.
+  auto fetch = [&](T& xa, T& xe, int64_t i, int a) {
+    if (a < 0) return;
     const T* x = logits + i * p.ld;
-    xa = row::to_f(x[r.a - from]);
-    const int e = edge_of(cut_row(x, length));
-    if (e >= 0) xe = row::to_f(x[e]);
+    xa = x[a - from];
+    const int e = EDGES ? edge_of(cut(i)) : -1;
+    if (e >= 0) xe = x[e];
+  };
+  uint32_t parity = 0;  // bit s: of the next phase of slot s to wait for
+  uint32_t sent = 0, read = 0;  // rows whose sums this warp has sent, has joined
+  // This warp's sum of row i, in slot s, to every CTA of the cluster; gives the token's logit.
+  auto sum_row = [&](int64_t i, int s, T xa, T xe) {
+    const Cut c = cut(i);
+    uint4* line = reinterpret_cast<uint4*>(slots + s * kSlotBytes);
+    const uint4* data = line + (c.head ? 1 : 0);
+    const int edge = edge_of(c), bytes = c.head ? 16 - c.head * static_cast<int>(sizeof(T)) : 0;
+    // A wait that runs out is recorded; the launch goes on to its end on whatever has come, so that no warp of
+    // the cluster is left waiting.
+    ptx::wait_fast(&full[s], (parity >> s) & 1u, abort_flag, p.status);
+    parity ^= 1u << s;
+    if (EDGES && (c.head || c.tail)) {
+      if (edge >= 0) reinterpret_cast<T*>(line)[bytes / static_cast<int>(sizeof(T)) + edge] = xe;
+      __syncwarp();
+    }
+    // Granules in batches of kBatch per lane, loaded together: a lane has under ten of them, and one at a time
+    // each would wait for its load and its chain of operations.
+    const uint4 none = lowest<T>();
+    Largest<T> top;
+    for (int q0 = lane; q0 < c.full; q0 += 32 * kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) raw[b] = q0 + 32 * b < c.full ? data[q0 + 32 * b] : none;
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) top.add(raw[b]);
+    }
+    MaxSum sum;
+    sum.m = warp_max(EDGES && edge >= 0 ? fmaxf(top.get(), row::to_f(xe)) : top.get());
+    // Whole groups first, then the last one where it is not.
+    Terms terms(finite_or_zero(sum.m), k);
+    const int whole = length / E;
+    for (int q0 = lane; q0 < whole; q0 += 32 * kBatch) {
+      uint4 raw[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int q = q0 + 32 * b;
+        raw[b] = none;
+        if (q < whole) raw[b] = !EDGES || bytes == 0 ? line[q] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) terms.template add<T>(raw[b]);
+    }
+    if (EDGES && whole * E < length && lane == 31)
+      terms.template add<T>(cut_behind<T>(shifted<sizeof(T) == 2>(line[whole], line[whole + 1], bytes), length - whole * E));
+    sum.s = warp_sum(terms.get());
+    // The token's logit has been read before this warp's sum lets the others write the row's gradient, which may
+    // go over it.
+    const float token_logit = row::to_f(xa);
+    asm volatile("" ::"f"(token_logit) : "memory");
+    const int j = sent++ % kJoins;
+    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[j], static_cast<uint32_t>(C * R::kWarps * sizeof(MaxSum)));
+    if (lane < C)
+      send(ptx::map_shared(ptx::smem_u32(&joined[j][unit]), lane), sum, ptx::map_shared(ptx::smem_u32(&joined_full[j]), lane));
+    return token_logit;
   };
 
-  RowMeta now = row_meta(p, first), next = row_meta(p, first + step), third = row_meta(p, first + 2 * step);
-  float xa, xe, xa_next, xe_next;
-  fetch(xa, xe, first, now);
+  const LaneMeta meta(p, lane);
+  uint32_t word = meta.load(first, p.n), word1 = meta.load(first + step, p.n), word2 = meta.load(first + 2 * step, p.n);
+  int a = token_of(p, word, first), a1 = token_of(p, word1, first + step);
+  T xa{}, xe{}, xa1{}, xe1{};
+  fetch(xa, xe, first, a);
+  fetch(xa1, xe1, first + step, a1);
   if (lane == 0) {
-    load(first, now, 0);
-    load(first + step, next, 1);
+    load(first, a, 0);
+    load(first + step, a1, 1);
   }
-  uint32_t parity = 0, joined_parity = 0;  // bit s: of the next phase of a slot, of a half, to wait for
-  int s = 0, half = 0;
+  float token_logit = 0.f, token_logit1 = 0.f;
+  if (a >= 0) token_logit = sum_row(first, 0, xa, xe);
+  int s = 0;
   for (int64_t i = first; i < p.n; i += step) {
-    const RowMeta fourth = row_meta(p, i + 3 * step);
-    fetch(xa_next, xe_next, i + step, next);
-    const Cut c = cut_row(logits + i * p.ld, length);
+    const uint32_t word3 = meta.load(i + 3 * step, p.n);
+    const int s1 = s == 2 ? 0 : s + 1, s2 = s == 0 ? 2 : s - 1;
+    if (a1 >= 0) token_logit1 = sum_row(i + step, s1, xa1, xe1);
+    // The slot of the row before takes the row after next, once its gradient has left it.
+    const int a2 = token_of(p, word2, i + 2 * step);
+    T xa2{}, xe2{};
+    fetch(xa2, xe2, i + 2 * step, a2);
+    if (lane == 0) {
+      ptx::bulk_wait_read0();
+      ptx::fence_async_smem();
+      load(i + 2 * step, a2, s2);
+    }
+    const Cut c = cut(i);
     // The share lies in the slot as it does around 16-byte addresses; `data` are its whole granules.
-    uint4* line = reinterpret_cast<uint4*>(slots + s * kSlotBytes);
-    uint4* data = line + (c.head ? 1 : 0);
+    uint4* data = reinterpret_cast<uint4*>(slots + s * kSlotBytes) + (c.head ? 1 : 0);
     const int edge = edge_of(c);
     T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd + from : nullptr;
-    if (now.a >= 0) {
-      // A wait that runs out is recorded; the launch goes on to its end on whatever has come, so that no warp of
-      // the cluster is left waiting.
-      ptx::wait_fast(&full[s], (parity >> s) & 1u, abort_flag, p.status);
-      parity ^= 1u << s;
-      const int bytes = c.head ? 16 - c.head * static_cast<int>(sizeof(T)) : 0;
-      if (c.head || c.tail) {
-        if (edge >= 0) reinterpret_cast<T*>(line)[bytes / static_cast<int>(sizeof(T)) + edge] = row::from_f<T>(xe);
-        __syncwarp();
-      }
-      // Whole groups first, then the last one where it is not.
-      RunningSum run;
-      const int whole = length / E;
-      if (bytes == 0) {
-#pragma unroll 4
-        for (int q = lane; q < whole; q += 32) run.template add<T>(line[q], k);
-      } else {
-#pragma unroll 4
-        for (int q = lane; q < whole; q += 32) run.template add<T>(shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes), k);
-      }
-      if (whole * E < length && lane == 31)
-        run.template add<T>(cut_behind<T>(shifted<sizeof(T) == 2>(line[whole], line[whole + 1], bytes), length - whole * E), k);
-      MaxSum sum = join_warp(run.get(), k);
-      // A half is written again two rows on, when every warp has sent its sum of the row between, and so has read
-      // this one's.
-      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[half], static_cast<uint32_t>(C * R::kWarps * sizeof(MaxSum)));
-      if (lane < C)
-        send(ptx::map_shared(ptx::smem_u32(&joined[half][unit]), lane), sum,
-             ptx::map_shared(ptx::smem_u32(&joined_full[half]), lane));
-      ptx::wait_fast(&joined_full[half], (joined_parity >> half) & 1u, abort_flag, p.status);
-      joined_parity ^= 1u << half;
-      sum = {-INFINITY, 0.f};
-      for (int w = lane; w < C * R::kWarps; w += 32) sum = join(sum, joined[half][w], k);
-      sum = join_warp(sum, k);
-      half ^= 1;
-      const float scale = row_end(p, i, now, xa, sum, unit == 0 && lane == 0);
+    if (a >= 0) {
+      const int j = read % kJoins;
+      ptx::wait_fast(&joined_full[j], (read++ / kJoins) & 1u, abort_flag, p.status);
+      const MaxSum sum = join_list(joined[j], C * R::kWarps, k);
+      RowMeta now;
+      now.w = __uint_as_float(__shfl_sync(0xffffffffu, word, 2));
+      now.old = __uint_as_float(__shfl_sync(0xffffffffu, word, 3));
+      now.adv = __uint_as_float(__shfl_sync(0xffffffffu, word, 4));
+      now.ref = __uint_as_float(__shfl_sync(0xffffffffu, word, 5));
+      const float scale = row_end(p, i, now, token_logit, sum, unit == 0 && lane == 0);
       if (dx) {
         const float base = finite_or_zero(sum.m), per = -scale * __frcp_rn(sum.s);
-        const int inside = now.a - from - c.head;  // the token's place in this share, if it has one
+        const int inside = a - from - c.head;  // the token's place in this share, if it has one
         const int token_q = inside >= 0 ? inside / E : -1, token_j = inside & (E - 1);
-#pragma unroll 4
-        for (int q = lane; q < c.full; q += 32) {
-          float v[E];
-          row::unpack16<T>(v, data[q]);
-          gradient(v, base, k, per);
-          if (q == token_q)
+        for (int q0 = lane; q0 < c.full; q0 += 32 * kBatch) {
+          uint4 raw[kBatch];
 #pragma unroll
-            for (int j = 0; j < E; ++j)
-              if (j == token_j) v[j] += scale;
-          data[q] = row::pack16(v);
+          for (int b = 0; b < kBatch; ++b) raw[b] = q0 + 32 * b < c.full ? data[q0 + 32 * b] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int q = q0 + 32 * b;
+            float v[E];
+            row::unpack16<T>(v, raw[b]);
+            gradient(v, base, k, per);
+            if (q == token_q)
+#pragma unroll
+              for (int e = 0; e < E; ++e)
+                if (e == token_j) v[e] += scale;
+            if (q < c.full) data[q] = row::pack16(v);
+          }
         }
         if (edge >= 0) {
-          const float g = per * pow2((xe - base) * k);
-          dx[edge] = row::from_f<T>(from + edge == now.a ? g + scale : g);
+          const float g = per * pow2((row::to_f(xe) - base) * k);
+          dx[edge] = row::from_f<T>(from + edge == a ? g + scale : g);
         }
       }
     } else {
@@ -542,15 +687,9 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
       for (int e = lane; e < c.full * E; e += 32) dx[c.head + e] = from_smem[e];
       __syncwarp();
     }
-    // The slot of the row before takes the row after next, once its gradient has left it.
-    const int spare = s == 0 ? 2 : s - 1;
-    if (lane == 0) {
-      ptx::bulk_wait_read_allow<1>();
-      ptx::fence_async_smem();
-      load(i + 2 * step, third, spare);
-    }
-    s = s == 2 ? 0 : s + 1;
-    now = next, next = third, third = fourth, xa = xa_next, xe = xe_next;
+    s = s1;
+    word = word1, word1 = word2, word2 = word3, a = a1, a1 = a2;
+    token_logit = token_logit1, xe = xe1, xa1 = xa2, xe1 = xe2;
   }
   // Rows behind the last are never loaded, so no load is on its way here, unless a wait ran out.
   if (lane == 0) {
@@ -641,7 +780,7 @@ cudaError_t launch_held(PolicyLaunch& p, int granules, int sms, cudaStream_t str
 
 // How many clusters of `size` CTAs of the ring kernel fit on the GPU at once. A property of the device: asked for
 // once (the caller holds the library's lock).
-template <typename T, bool WIDE>
+template <typename T, bool WIDE, bool EDGES>
 cudaError_t resident_clusters(int size, int* clusters) {
   constexpr int kMaxDevices = 64;
   static int known[kMaxDevices][kMaxCluster + 1];  // 1 + the number
@@ -660,7 +799,7 @@ cudaError_t resident_clusters(int size, int* clusters) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, WIDE>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, WIDE, EDGES>, &cfg);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) known[dev][size] = n + 1;
   }
@@ -670,7 +809,7 @@ cudaError_t resident_clusters(int size, int* clusters) {
 
 // Whether a row fits the shared memory of a cluster that fits the GPU; if so, launches. Of the cluster sizes
 // that hold a row, the one with the most CTAs on the GPU at once, so that few SMs are left over.
-template <typename T, bool WIDE>
+template <typename T, bool WIDE, bool EDGES>
 cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   using R = Ring<WIDE>;
   constexpr int E = 16 / sizeof(T);
@@ -680,19 +819,19 @@ cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   const int64_t groups = (p.vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
   if (least > R::kCluster) return cudaSuccess;
   cudaError_t e =
-      cudaFuncSetAttribute(policy_ring_kernel<T, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+      cudaFuncSetAttribute(policy_ring_kernel<T, WIDE, EDGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
   if (e == cudaSuccess && WIDE)
-    e = cudaFuncSetAttribute(policy_ring_kernel<T, WIDE>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(policy_ring_kernel<T, WIDE, EDGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   int best = 0;
   for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
     int n = 0;
-    e = resident_clusters<T, WIDE>(size, &n);
+    e = resident_clusters<T, WIDE, EDGES>(size, &n);
     if (e == cudaSuccess && n * size > best * p.cluster) best = n, p.cluster = size;
   }
   if (e != cudaSuccess || best == 0) return e;
   *launched = true;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(p.n, best) * p.cluster);
-  return row::launch(policy_ring_kernel<T, WIDE>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
+  return row::launch(policy_ring_kernel<T, WIDE, EDGES>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
 }
 
 template <typename T>
@@ -710,8 +849,10 @@ cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
   if (granules <= 2048) return launch_held<T, 4, 512>(p, static_cast<int>(granules), sms, stream);
   bool launched = false;
   p.cluster = 0;
-  cudaError_t e = launch_ring<T, false>(p, stream, &launched);
-  if (e == cudaSuccess && !launched) e = launch_ring<T, true>(p, stream, &launched);
+  const bool edges = !p.aligned || p.vocab % E != 0;
+  cudaError_t e = edges ? launch_ring<T, false, true>(p, stream, &launched) : launch_ring<T, false, false>(p, stream, &launched);
+  if (e == cudaSuccess && !launched)
+    e = edges ? launch_ring<T, true, true>(p, stream, &launched) : launch_ring<T, true, false>(p, stream, &launched);
   if (e != cudaSuccess || launched) return e;
   return row::launch(policy_twice_kernel<T>, dim3(static_cast<unsigned>(p.n)), kTwiceThreads, 0, stream, p);
 }
