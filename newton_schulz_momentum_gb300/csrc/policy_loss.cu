@@ -153,10 +153,11 @@ struct Terms {
     float v[E];
     row::unpack16<T>(v, raw);
 #pragma unroll
-    for (int j = 0; j < E; j += 2) {
-      const float2 z = mul2(add2(make_float2(v[j], v[j + 1]), less), kk);
-      acc = add2(acc, make_float2(pow2(z.x), pow2(z.y)));
-    }
+    for (int j = 0; j < E; j += 2) add_pair(v[j], v[j + 1]);
+  }
+  __device__ __forceinline__ void add_pair(float x, float y) {
+    const float2 z = mul2(add2(make_float2(x, y), less), kk);
+    acc = add2(acc, make_float2(pow2(z.x), pow2(z.y)));
   }
   __device__ __forceinline__ float get() const { return acc.x + acc.y; }
 };
@@ -573,22 +574,34 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
     }
     MaxSum sum;
     sum.m = warp_max(EDGES && edge >= 0 ? fmaxf(top.get(), row::to_f(xe)) : top.get());
-    // Whole groups first, then the last one where it is not.
     Terms terms(finite_or_zero(sum.m), k);
-    const int whole = length / E;
-    for (int q0 = lane; q0 < whole; q0 += 32 * kBatch) {
-      uint4 raw[kBatch];
+    if constexpr (sizeof(T) == 4) {
+      // Single elements, at any offset: the memory traffic of fp32 leaves time for their loads.
+      const float* x = reinterpret_cast<const float*>(line) + bytes / 4;
+      for (int e0 = lane; e0 < length; e0 += 32 * 4 * kBatch) {
+        float v[4 * kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int q = q0 + 32 * b;
-        raw[b] = none;
-        if (q < whole) raw[b] = !EDGES || bytes == 0 ? line[q] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
+        for (int b = 0; b < 4 * kBatch; ++b) v[b] = e0 + 32 * b < length ? x[e0 + 32 * b] : -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 4 * kBatch; b += 2) terms.add_pair(v[b], v[b + 1]);
       }
+    } else {
+      // Whole groups first, then the last one where it is not.
+      const int whole = length / E;
+      for (int q0 = lane; q0 < whole; q0 += 32 * kBatch) {
+        uint4 raw[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) terms.template add<T>(raw[b]);
+        for (int b = 0; b < kBatch; ++b) {
+          const int q = q0 + 32 * b;
+          raw[b] = none;
+          if (q < whole) raw[b] = !EDGES || bytes == 0 ? line[q] : shifted<true>(line[q], line[q + 1], bytes);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) terms.template add<T>(raw[b]);
+      }
+      if (EDGES && whole * E < length && lane == 31)
+        terms.template add<T>(cut_behind<T>(shifted<true>(line[whole], line[whole + 1], bytes), length - whole * E));
     }
-    if (EDGES && whole * E < length && lane == 31)
-      terms.template add<T>(cut_behind<T>(shifted<sizeof(T) == 2>(line[whole], line[whole + 1], bytes), length - whole * E));
     sum.s = warp_sum(terms.get());
     // The token's logit has been read before this warp's sum lets the others write the row's gradient, which may
     // go over it.
@@ -807,8 +820,12 @@ cudaError_t resident_clusters(int size, int* clusters) {
   return cudaSuccess;
 }
 
+// A warp's time for a row beside its granules, in granules (about 500 instructions to 65 for 32 of them).
+constexpr int kRowCost = 256;
+
 // Whether a row fits the shared memory of a cluster that fits the GPU; if so, launches. Of the cluster sizes
-// that hold a row, the one with the most CTAs on the GPU at once, so that few SMs are left over.
+// that hold a row, the one that brings the most rows through: clusters at once over time per row. (Larger ones
+// leave fewer SMs over at times, but each of their warps pays for the row again.)
 template <typename T, bool WIDE, bool EDGES>
 cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   using R = Ring<WIDE>;
@@ -823,10 +840,12 @@ cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   if (e == cudaSuccess && WIDE)
     e = cudaFuncSetAttribute(policy_ring_kernel<T, WIDE, EDGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   int best = 0;
+  double most = 0.0;
   for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
     int n = 0;
     e = resident_clusters<T, WIDE, EDGES>(size, &n);
-    if (e == cudaSuccess && n * size > best * p.cluster) best = n, p.cluster = size;
+    const double rate = n / (kRowCost + static_cast<double>(groups) / (size * R::kWarps));
+    if (e == cudaSuccess && rate > most) most = rate, best = n, p.cluster = size;
   }
   if (e != cudaSuccess || best == 0) return e;
   *launched = true;
