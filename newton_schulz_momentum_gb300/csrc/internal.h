@@ -405,9 +405,9 @@ struct PolicyLaunch {
   void* dlogits;    // may be null
   int64_t ldd;
   unsigned* status;
-  // Set by launch_policy: threads per row, CTAs per row, whether logits and dlogits start their rows at the same
-  // offsets from 16 bytes, and whether every row of logits starts on 16 bytes.
-  int tpr, cluster, same_cut, aligned;
+  // Set by launch_policy: CTAs per row, bytes of a warp's shared memory slot, and whether logits and dlogits
+  // start their rows at the same offsets from 16 bytes.
+  int cluster, slot_bytes, same_cut;
 };
 cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream);
 

@@ -9,8 +9,8 @@
 //
 // Bound by memory: c needs the whole row's sum before the first element of the gradient, and a row of a large
 // vocabulary is more than an SM holds (128256 bf16: 257 KB), so the row is split over the CTAs of a cluster. It
-// waits in their shared memory while they join their sums, and is read and written once. Rows of up to 16384
-// elements are held in the registers of a CTA's threads instead; beyond the cluster's memory a row is read twice.
+// waits in their shared memory while they join their sums, and is read and written once. A row of up to 18 KB is
+// one warp's; beyond the cluster's memory a row is read twice.
 //
 // Memory is read and written in 16-byte granules at aligned addresses, wherever a row starts; the sum runs over
 // groups of as many elements counted from the row's first one. So its order goes by the vocabulary alone: a row
@@ -51,13 +51,6 @@ __device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY
 __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float k) {
   const float m = fmaxf(a.m, b.m), base = finite_or_zero(m);
   return {m, a.s * pow2((a.m - base) * k) + b.s * pow2((b.m - base) * k)};
-}
-
-// Over `lanes` (a power of two) neighbouring lanes.
-__device__ __forceinline__ MaxSum join_lanes(MaxSum t, int lanes, float k) {
-  for (int o = lanes / 2; o > 0; o >>= 1)
-    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o)}, k);
-  return t;
 }
 
 // Over a warp: the maximum as one integer reduction (of bits that order as the floats do), then the sums.
@@ -285,144 +278,11 @@ __device__ __forceinline__ Cut cut_row(const T* x, int vocab) {
   return c;
 }
 
-// ---------------------------------------------------------------------------- rows in registers
-
-// As many rows per CTA as `tpr` threads leave room for, K granules per thread; granule 0 is the partial one
-// at the row's head where there is one. CTAs stay: the next row is on its way while this one is worked on.
-template <typename T, int K, int THREADS>
-__global__ void __launch_bounds__(THREADS) policy_held_kernel(const PolicyLaunch p) {
-  constexpr int E = 16 / sizeof(T);
-  __shared__ MaxSum part[2][THREADS / 32];
-  extern __shared__ uint4 image[];  // rows that do not start on 16 bytes, granule by granule
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
-  const int vocab = static_cast<int>(p.vocab);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
-  const T* logits = static_cast<const T*>(p.logits);
-  const float k = kLog2e * p.inv_temperature;
-  // The first element of this thread's granule `g` in a row at x, which may lie before the row.
-  auto start = [&](const T* x, int g) {
-    return (t + g * tpr) * E - static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  };
-  auto fetch = [&](uint4 (&raw)[K], float& xa, int64_t i, const RowMeta& r) {
-    xa = 0.f;
-    if (r.a < 0) return;
-    const T* x = logits + i * p.ld;
-    xa = row::to_f(x[r.a]);
-#pragma unroll
-    for (int g = 0; g < K; ++g) {
-      const int e0 = start(x, g);
-      if (e0 >= 0 && e0 + E <= vocab) {
-        raw[g] = __ldcs(reinterpret_cast<const uint4*>(x + e0));
-      } else {
-        // Elements outside the row count as -infinity.
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const bool in = e0 + j >= 0 && e0 + j < vocab;
-          if constexpr (sizeof(T) == 4) {
-            w[j] = in ? __float_as_uint(x[e0 + j]) : 0xff800000u;
-          } else {
-            const uint32_t b = in ? __bfloat16_as_ushort(x[e0 + j]) : 0xff80u;
-            w[j / 2] = j % 2 ? w[j / 2] | b << 16 : b;
-          }
-        }
-        raw[g] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  };
-  RowMeta now = row_meta(p, first + slot), next = row_meta(p, first + step + slot);
-  uint4 raw[K], ahead[K];
-  float xa, xa_ahead;
-  fetch(raw, xa, first + slot, now);
-  int half = 0;
-  for (int64_t base_row = first; base_row < p.n; base_row += step, half ^= 1) {
-    const int64_t i = base_row + slot;
-    const RowMeta later = row_meta(p, i + 2 * step);
-    fetch(ahead, xa_ahead, i + step, next);
-    MaxSum sum{-INFINITY, 0.f};
-    uint4* line = image + slot * (K * tpr + 1);
-    if (!p.aligned) {
-      if (now.a >= 0)
-#pragma unroll
-        for (int g = 0; g < K; ++g) line[t + g * tpr] = raw[g];
-      __syncthreads();
-    }
-    if (now.a >= 0) {
-      const int bytes = static_cast<int>(reinterpret_cast<uintptr_t>(logits + i * p.ld) & 15);
-      uint4 group[K];
-      Largest<T> top;
-#pragma unroll
-      for (int g = 0; g < K; ++g) {
-        const int q = t + g * tpr;
-        group[g] = p.aligned || q * E >= vocab ? raw[g] : shifted<sizeof(T) == 2>(line[q], line[q + 1], bytes);
-        if ((q + 1) * E > vocab) group[g] = cut_behind<T>(group[g], vocab - q * E);
-        top.add(group[g]);
-      }
-      sum.m = top.get();
-      Terms terms(finite_or_zero(sum.m), k);
-#pragma unroll
-      for (int g = 0; g < K; ++g)
-        if ((t + g * tpr) * E < vocab) terms.template add<T>(group[g]);
-      sum.s = terms.get();
-    }
-    sum = tpr >= 32 ? join_warp(sum, k) : join_lanes(sum, tpr, k);
-    // Here every thread of the row has read the token's logit, which the gradient may be written over.
-    if (tpr <= 32) {
-      __syncwarp();
-    } else {
-      const int warp = threadIdx.x >> 5, warps = tpr >> 5, from = warp / warps * warps;
-      if ((threadIdx.x & 31) == 0) part[half][warp] = sum;
-      __syncthreads();
-      sum = part[half][from];
-      for (int w = 1; w < warps; ++w) sum = join(sum, part[half][from + w], k);
-    }
-    float scale = 0.f;
-    if (now.a >= 0)
-      scale = row_end(p, i, now, xa, sum, t == 0);
-    else if (i < p.n && t == 0)
-      row_skipped(p, i);
-    if (p.dlogits && i < p.n) {
-      T* dx = static_cast<T*>(p.dlogits) + i * p.ldd;
-      const T* x = logits + i * p.ld;
-      const float base = finite_or_zero(sum.m), per = -scale * __frcp_rn(sum.s);
-#pragma unroll
-      for (int g = 0; g < K; ++g) {
-        const int e0 = start(x, g);
-        if (e0 >= vocab) continue;
-        float v[E];
-        if (now.a >= 0) {
-          row::unpack16<T>(v, raw[g]);
-          gradient(v, base, k, per);
-          if (now.a >= e0 && now.a < e0 + E)
-#pragma unroll
-            for (int j = 0; j < E; ++j)
-              if (now.a == e0 + j) v[j] += scale;
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j) v[j] = 0.f;
-        }
-        if (p.same_cut && e0 >= 0 && e0 + E <= vocab) {
-          __stcs(reinterpret_cast<uint4*>(dx + e0), row::pack16(v));
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j)
-            if (e0 + j >= 0 && e0 + j < vocab) dx[e0 + j] = row::from_f<T>(v[j]);
-        }
-      }
-    }
-    now = next, next = later, xa = xa_ahead;
-#pragma unroll
-    for (int g = 0; g < K; ++g) raw[g] = ahead[g];
-  }
-}
-
-// ---------------------------------------------------------------------------- rows in a cluster's shared memory
+// ---------------------------------------------------------------------------- rows in shared memory
 
 constexpr int kRingSlots = 3;          // of a warp: one being loaded, one worked on, one being written
-constexpr int kSlotBytes = 4608;
 constexpr int kBatch = 4;
+constexpr int kSlotBytes = 4608;       // of a warp that shares a row
 constexpr int kWarpGroups = kSlotBytes / 16 - 2;  // beside the rest of the first granule, and the one read past the last
 constexpr int kMaxCluster = 16;
 // Rows whose sums are on their way or being read, of those that are read at all. A warp sends its sum of the
@@ -430,14 +290,19 @@ constexpr int kMaxCluster = 16;
 // (n - 4)-th, whose place the n-th takes.
 constexpr int kJoins = 4;
 
-// Two CTAs per SM, in clusters of a portable size; or, for rows beyond eight of those, CTAs of twice the size.
-template <bool WIDE>
+// Who takes a row: one warp; a cluster of a portable size, two CTAs per SM; or, for rows beyond eight of
+// those, a cluster of CTAs twice as large.
+enum RingMode { kSolo, kShared, kWide };
+
+template <int MODE>
 struct Ring {
-  static constexpr int kThreads = WIDE ? 512 : 256;
+  static constexpr int kThreads = MODE == kSolo ? 128 : MODE == kShared ? 256 : 512;
+  static constexpr int kPerSm = MODE == kSolo ? 4 : MODE == kShared ? 2 : 1;
   static constexpr int kWarps = kThreads / 32;
   static constexpr int kSmem = kWarps * kRingSlots * kSlotBytes + 128;
-  static constexpr int kCluster = WIDE ? kMaxCluster : 8;  // CTAs per row at most
+  static constexpr int kCluster = MODE == kSolo ? 1 : MODE == kShared ? 8 : kMaxCluster;  // CTAs per row at most
 };
+constexpr int kSoloSlotBytes = 18432;  // the most for which four warps' slots fit an SM
 
 // Writes v into a CTA of the cluster and counts its 8 bytes at that CTA's barrier (shared::cluster addresses).
 __device__ __forceinline__ void send(uint32_t addr, MaxSum v, uint32_t barrier) {
@@ -480,17 +345,18 @@ __device__ __forceinline__ int token_of(const PolicyLaunch& p, uint32_t word, in
   return static_cast<int>(lo);
 }
 
-// A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it. The warps work on
-// their own: bulk copies bring a share's whole granules into the warp's slots and take their gradients, formed
+// A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it (kSolo: every warp rows
+// of its own). The warps work by themselves: bulk copies bring a share's whole granules into the warp's slots and take their gradients, formed
 // in place, out; up to E - 1 elements on either side of them go through registers. Where they meet is the
 // row's sum: every warp sends its own to every CTA of the cluster, and goes on when all have arrived. (With
 // barriers over the cluster and the CTA in their place, a third of the warps' time went into those and the
 // fences they imply.)
 // EDGES: shares that are not whole granules.
-template <typename T, bool WIDE, bool EDGES>
-__global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_ring_kernel(const PolicyLaunch p) {
-  using R = Ring<WIDE>;
+template <typename T, int MODE, bool EDGES>
+__global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) policy_ring_kernel(const PolicyLaunch p) {
+  using R = Ring<MODE>;
   constexpr int E = 16 / sizeof(T);
+  constexpr bool SOLO = MODE == kSolo;
   extern __shared__ uint8_t dyn[];
   __shared__ MaxSum joined[kJoins][R::kCluster * R::kWarps];
   __shared__ uint64_t joined_full[kJoins];
@@ -498,12 +364,13 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
   __shared__ int abort_word;
   volatile int* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* slots = dyn + (128 - (ptx::smem_u32(dyn) & 127)) % 128 + warp * kRingSlots * kSlotBytes;
+  uint8_t* slots = dyn + (128 - (ptx::smem_u32(dyn) & 127)) % 128 + warp * kRingSlots * p.slot_bytes;
   uint64_t* full = slot_full[warp];
-  const int C = p.cluster, unit = static_cast<int>(ptx::cluster_ctarank()) * R::kWarps + warp;
-  const int64_t step = gridDim.x / C, first = blockIdx.x / C;
+  const int C = p.cluster, unit = SOLO ? 0 : static_cast<int>(ptx::cluster_ctarank()) * R::kWarps + warp;
+  const int64_t step = SOLO ? gridDim.x * R::kWarps : gridDim.x / C;
+  const int64_t first = SOLO ? blockIdx.x * R::kWarps + warp : blockIdx.x / C;
   const int vocab = static_cast<int>(p.vocab);
-  const int groups_each = (vocab + C * R::kWarps * E - 1) / (C * R::kWarps * E);
+  const int units = SOLO ? 1 : C * R::kWarps, groups_each = (vocab + units * E - 1) / (units * E);
   const int from = min(unit * groups_each * E, vocab), length = min(groups_each * E, vocab - from);
   const T* logits = static_cast<const T*>(p.logits) + from;
   const float k = kLog2e * p.inv_temperature;
@@ -517,7 +384,7 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   __syncthreads();
-  ptx::cluster_sync_all();  // the barriers are set up, and every CTA runs before another writes into it
+  if (!SOLO) ptx::cluster_sync_all();  // every CTA has set up its barriers before another writes into it
 
   uint64_t policy = 0;
   if (lane == 0) policy = ptx::l2_policy_evict_first();
@@ -527,7 +394,7 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
     const Cut c = cut(i);
     ptx::mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(c.full) * 16u);
     if (c.full > 0)
-      ptx::bulk_load_hint(ptx::smem_u32(slots + s * kSlotBytes + (c.head ? 16 : 0)), logits + i * p.ld + c.head,
+      ptx::bulk_load_hint(ptx::smem_u32(slots + s * p.slot_bytes + (c.head ? 16 : 0)), logits + i * p.ld + c.head,
                           static_cast<uint32_t>(c.full) * 16u, &full[s], policy);
   };
   // The element outside the granules that this lane holds, or -1.
@@ -547,10 +414,11 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
   };
   uint32_t parity = 0;  // bit s: of the next phase of slot s to wait for
   uint32_t sent = 0, read = 0;  // rows whose sums this warp has sent, has joined
+  MaxSum ready{};  // kSolo: the sum of the row last summed
   // This warp's sum of row i, in slot s, to every CTA of the cluster; gives the token's logit.
   auto sum_row = [&](int64_t i, int s, T xa, T xe) {
     const Cut c = cut(i);
-    uint4* line = reinterpret_cast<uint4*>(slots + s * kSlotBytes);
+    uint4* line = reinterpret_cast<uint4*>(slots + s * p.slot_bytes);
     const uint4* data = line + (c.head ? 1 : 0);
     const int edge = edge_of(c), bytes = c.head ? 16 - c.head * static_cast<int>(sizeof(T)) : 0;
     // A wait that runs out is recorded; the launch goes on to its end on whatever has come, so that no warp of
@@ -607,8 +475,12 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
     // go over it.
     const float token_logit = row::to_f(xa);
     asm volatile("" ::"f"(token_logit) : "memory");
+    if (SOLO) {
+      ready = sum;
+      return token_logit;
+    }
     const int j = sent++ % kJoins;
-    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[j], static_cast<uint32_t>(C * R::kWarps * sizeof(MaxSum)));
+    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[j], static_cast<uint32_t>(units * sizeof(MaxSum)));
     if (lane < C)
       send(ptx::map_shared(ptx::smem_u32(&joined[j][unit]), lane), sum, ptx::map_shared(ptx::smem_u32(&joined_full[j]), lane));
     return token_logit;
@@ -630,6 +502,7 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
   for (int64_t i = first; i < p.n; i += step) {
     const uint32_t word3 = meta.load(i + 3 * step, p.n);
     const int s1 = s == 2 ? 0 : s + 1, s2 = s == 0 ? 2 : s - 1;
+    MaxSum sum = ready;
     if (a1 >= 0) token_logit1 = sum_row(i + step, s1, xa1, xe1);
     // The slot of the row before takes the row after next, once its gradient has left it.
     const int a2 = token_of(p, word2, i + 2 * step);
@@ -642,13 +515,15 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
     }
     const Cut c = cut(i);
     // The share lies in the slot as it does around 16-byte addresses; `data` are its whole granules.
-    uint4* data = reinterpret_cast<uint4*>(slots + s * kSlotBytes) + (c.head ? 1 : 0);
+    uint4* data = reinterpret_cast<uint4*>(slots + s * p.slot_bytes) + (c.head ? 1 : 0);
     const int edge = edge_of(c);
     T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd + from : nullptr;
     if (a >= 0) {
-      const int j = read % kJoins;
-      ptx::wait_fast(&joined_full[j], (read++ / kJoins) & 1u, abort_flag, p.status);
-      const MaxSum sum = join_list(joined[j], C * R::kWarps, k);
+      if (!SOLO) {
+        const int j = read % kJoins;
+        ptx::wait_fast(&joined_full[j], (read++ / kJoins) & 1u, abort_flag, p.status);
+        sum = join_list(joined[j], units, k);
+      }
       RowMeta now;
       now.w = __uint_as_float(__shfl_sync(0xffffffffu, word, 2));
       now.old = __uint_as_float(__shfl_sync(0xffffffffu, word, 3));
@@ -712,7 +587,7 @@ __global__ void __launch_bounds__(Ring<WIDE>::kThreads, WIDE ? 1 : 2) policy_rin
     ptx::bulk_wait0();
   }
   __syncwarp();
-  ptx::cluster_sync_all();  // nobody writes into a CTA that has ended
+  if (!SOLO) ptx::cluster_sync_all();  // nobody writes into a CTA that has ended
 }
 
 // ---------------------------------------------------------------------------- rows read twice
@@ -776,24 +651,9 @@ __global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const PolicyLau
   if (threadIdx.x == 0) *p.loss = acc;
 }
 
-template <typename T, int K, int THREADS>
-cudaError_t launch_held(PolicyLaunch& p, int granules, int sms, cudaStream_t stream) {
-  auto* kernel = policy_held_kernel<T, K, THREADS>;
-  const int need = (granules + K - 1) / K;
-  p.tpr = need > 16 ? (need + 31) / 32 * 32 : 1;
-  while (p.tpr < need) p.tpr *= 2;
-  const int rows = p.tpr >= 256 ? 1 : 256 / p.tpr, threads = p.tpr * rows;
-  int per_sm = 0;
-  const size_t smem = p.aligned ? 0 : static_cast<size_t>(rows) * (K * p.tpr + 1) * 16;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * std::max(per_sm, 1), (p.n + rows - 1) / rows);
-  return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), threads, smem, stream, p);
-}
-
 // How many clusters of `size` CTAs of the ring kernel fit on the GPU at once. A property of the device: asked for
 // once (the caller holds the library's lock).
-template <typename T, bool WIDE, bool EDGES>
+template <typename T, int MODE, bool EDGES>
 cudaError_t resident_clusters(int size, int* clusters) {
   constexpr int kMaxDevices = 64;
   static int known[kMaxDevices][kMaxCluster + 1];  // 1 + the number
@@ -804,15 +664,15 @@ cudaError_t resident_clusters(int size, int* clusters) {
   if (n < 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
-    cfg.blockDim = dim3(Ring<WIDE>::kThreads);
-    cfg.dynamicSmemBytes = Ring<WIDE>::kSmem;
+    cfg.blockDim = dim3(Ring<MODE>::kThreads);
+    cfg.dynamicSmemBytes = Ring<MODE>::kSmem;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = static_cast<unsigned>(size);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, WIDE, EDGES>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, MODE, EDGES>, &cfg);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) known[dev][size] = n + 1;
   }
@@ -826,9 +686,9 @@ constexpr int kRowCost = 256;
 // Whether a row fits the shared memory of a cluster that fits the GPU; if so, launches. Of the cluster sizes
 // that hold a row, the one that brings the most rows through: clusters at once over time per row. (Larger ones
 // leave fewer SMs over at times, but each of their warps pays for the row again.)
-template <typename T, bool WIDE, bool EDGES>
+template <typename T, int MODE, bool EDGES>
 cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
-  using R = Ring<WIDE>;
+  using R = Ring<MODE>;
   constexpr int E = 16 / sizeof(T);
   *launched = false;
   constexpr int64_t per_cta = R::kWarps * kWarpGroups;
@@ -836,42 +696,57 @@ cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   const int64_t groups = (p.vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
   if (least > R::kCluster) return cudaSuccess;
   cudaError_t e =
-      cudaFuncSetAttribute(policy_ring_kernel<T, WIDE, EDGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
-  if (e == cudaSuccess && WIDE)
-    e = cudaFuncSetAttribute(policy_ring_kernel<T, WIDE, EDGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      cudaFuncSetAttribute(policy_ring_kernel<T, MODE, EDGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
+  if (e == cudaSuccess && MODE == kWide)
+    e = cudaFuncSetAttribute(policy_ring_kernel<T, MODE, EDGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   int best = 0;
   double most = 0.0;
   for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
     int n = 0;
-    e = resident_clusters<T, WIDE, EDGES>(size, &n);
+    e = resident_clusters<T, MODE, EDGES>(size, &n);
     const double rate = n / (kRowCost + static_cast<double>(groups) / (size * R::kWarps));
     if (e == cudaSuccess && rate > most) most = rate, best = n, p.cluster = size;
   }
   if (e != cudaSuccess || best == 0) return e;
   *launched = true;
+  p.slot_bytes = kSlotBytes;
   const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(p.n, best) * p.cluster);
-  return row::launch(policy_ring_kernel<T, WIDE, EDGES>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
+  return row::launch(policy_ring_kernel<T, MODE, EDGES>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
+}
+
+template <typename T, bool EDGES>
+cudaError_t launch_solo(PolicyLaunch& p, int sms, cudaStream_t stream) {
+  using R = Ring<kSolo>;
+  auto* kernel = policy_ring_kernel<T, kSolo, EDGES>;
+  const size_t smem = static_cast<size_t>(R::kWarps) * kRingSlots * p.slot_bytes + 128;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       R::kWarps * kRingSlots * kSoloSlotBytes + 128);
+  int per_sm = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, R::kThreads, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * std::max(per_sm, 1), (p.n + R::kWarps - 1) / R::kWarps);
+  return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), R::kThreads, smem, stream, p);
 }
 
 template <typename T>
 cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(T);
   const size_t step = static_cast<size_t>(p.ld) * sizeof(T) % 16;
-  p.aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (p.n == 1 || step == 0);
+  const bool aligned = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 && (p.n == 1 || step == 0);
   p.same_cut = p.dlogits && (reinterpret_cast<uintptr_t>(p.dlogits) - reinterpret_cast<uintptr_t>(p.logits)) % 16 == 0 &&
                (p.n == 1 || static_cast<size_t>(p.ldd) * sizeof(T) % 16 == step);
-  // Granules of a row that starts anywhere.
-  const int64_t granules = (p.vocab + 2 * (E - 1)) / E;
-  if (granules <= 256) return launch_held<T, 1, 256>(p, static_cast<int>(granules), sms, stream);
-  if (granules <= 512) return launch_held<T, 2, 256>(p, static_cast<int>(granules), sms, stream);
-  if (granules <= 1024) return launch_held<T, 4, 256>(p, static_cast<int>(granules), sms, stream);
-  if (granules <= 2048) return launch_held<T, 4, 512>(p, static_cast<int>(granules), sms, stream);
+  const bool edges = !aligned || p.vocab % E != 0;
+  p.cluster = 1;
+  // As a shared row's slot: beside the groups, the rest of the first granule and the one read past the last.
+  const int64_t slot = ((p.vocab + E - 1) / E + 2) * 16;
+  if (slot <= kSoloSlotBytes) {
+    p.slot_bytes = static_cast<int>(slot);
+    return edges ? launch_solo<T, true>(p, sms, stream) : launch_solo<T, false>(p, sms, stream);
+  }
   bool launched = false;
-  p.cluster = 0;
-  const bool edges = !p.aligned || p.vocab % E != 0;
-  cudaError_t e = edges ? launch_ring<T, false, true>(p, stream, &launched) : launch_ring<T, false, false>(p, stream, &launched);
+  cudaError_t e = edges ? launch_ring<T, kShared, true>(p, stream, &launched) : launch_ring<T, kShared, false>(p, stream, &launched);
   if (e == cudaSuccess && !launched)
-    e = edges ? launch_ring<T, true, true>(p, stream, &launched) : launch_ring<T, true, false>(p, stream, &launched);
+    e = edges ? launch_ring<T, kWide, true>(p, stream, &launched) : launch_ring<T, kWide, false>(p, stream, &launched);
   if (e != cudaSuccess || launched) return e;
   return row::launch(policy_twice_kernel<T>, dim3(static_cast<unsigned>(p.n)), kTwiceThreads, 0, stream, p);
 }
