@@ -1275,12 +1275,12 @@ int run_policy(PolicyLaunch& p, cudaStream_t stream) {
   DeviceState* ds = nullptr;
   int st = current_device(&ds);
   if (st != DMUON_OK || (p.n == 0 && !p.loss)) return st;
-  p.row_loss = nullptr;
+  p.loss_terms = nullptr;
   if (p.loss) {
     char* ws = nullptr;
-    st = token_workspace(*ds, p.n * static_cast<int64_t>(sizeof(float)), stream, &ws);
+    st = token_workspace(*ds, policy_workspace(p.n), stream, &ws);
     if (st != DMUON_OK) return st;
-    p.row_loss = reinterpret_cast<float*>(ws);
+    p.loss_terms = reinterpret_cast<float*>(ws);
   }
   p.status = ds->status;
   DM_CUDA(timed(kClsPolicy, stream, [&] { return launch_policy(p, ds->sms, stream); }), "policy loss launch");

@@ -400,7 +400,8 @@ struct PolicyLaunch {
   const float* weights;                           // null: log-probabilities only
   float clip_low, clip_high, kl_coef, inv_temperature;
   float* loss;      // null: log-probabilities only
-  float* row_loss;  // workspace, n entries
+  float* loss_terms;  // workspace of policy_workspace(n) bytes: `terms` summands of the loss, set by launch_policy
+  int64_t terms;
   float* logp;      // may be null
   void* dlogits;    // may be null
   int64_t ldd;
@@ -409,6 +410,7 @@ struct PolicyLaunch {
   // start their rows at the same offsets from 16 bytes.
   int cluster, slot_bytes, same_cut;
 };
+int64_t policy_workspace(int64_t n);
 cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream);
 
 // Record `message` as the calling thread's last error (returned by dmuon_last_error) and return status.

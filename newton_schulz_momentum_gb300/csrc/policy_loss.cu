@@ -16,6 +16,7 @@
 // groups of as many elements counted from the row's first one. So its order goes by the vocabulary alone: a row
 // gives the same bits whatever the other rows are, and wherever it and its gradient lie.
 #include <algorithm>
+#include <type_traits>
 
 #include "row_ops.h"
 #include "tc_ptx.h"
@@ -155,20 +156,14 @@ struct Terms {
   __device__ __forceinline__ float get() const { return acc.x + acc.y; }
 };
 
-// The 16 bytes that start `bytes` (a multiple of 4, or of 2 with HALVES) into a and b.
-template <bool HALVES>
-__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int bytes) {
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (bytes & 8)
+// The 16 bytes that start WORDS words, and with HALF two more bytes, into a and b.
+template <int WORDS, bool HALF>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b) {
+  const uint32_t w[9] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, 0};
+  uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  if (bytes & 4)
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  if (HALVES && (bytes & 2))
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) o[i] = HALF ? __funnelshift_r(w[i + WORDS], w[i + WORDS + 1], 16) : w[i + WORDS];
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The elements of a granule from `left` on become -infinity.
@@ -220,9 +215,9 @@ __device__ __forceinline__ float exp_less_1(float d) {
   return fabsf(d) < 0.25f ? r : pow2(d * kLog2e) - 1.f;
 }
 
-// Writes the row's log-probability and term (one thread), and gives its gradient's scale c / T.
+// Writes the row's log-probability (one thread), adds its term to `loss` and gives its gradient's scale c / T.
 __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const RowMeta& r, float xa, MaxSum t,
-                                         bool writes) {
+                                         bool writes, float& loss) {
   // The token's distance from the maximum is exact in many cases, and log2 of a sum of 1 is 0.
   const float logp = (xa - t.m) * p.inv_temperature - log2_of(t.s) * kLn2;
   float each = 0.f, c = 0.f;
@@ -238,16 +233,13 @@ __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const
       c = fmaf(-p.kl_coef, e, c);
     }
   }
-  if (writes) {
-    if (p.logp) p.logp[i] = logp;
-    if (p.row_loss) p.row_loss[i] = each * r.w;
-  }
+  if (writes && p.logp) p.logp[i] = logp;
+  loss = fmaf(each, r.w, loss);
   return c * r.w * p.inv_temperature;
 }
 
 __device__ __forceinline__ void row_skipped(const PolicyLaunch& p, int64_t i) {
   if (p.logp) p.logp[i] = 0.f;
-  if (p.row_loss) p.row_loss[i] = 0.f;
 }
 
 // The gradient of a granule's logits: scale (onehot - 2^((x - base) k) / s), with per = -scale / s.
@@ -454,21 +446,39 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
         for (int b = 0; b < 4 * kBatch; b += 2) terms.add_pair(v[b], v[b + 1]);
       }
     } else {
-      // Whole groups first, then the last one where it is not.
+      // Whole groups first, then the last one where it is not; one copy of the loop for each offset from 16 bytes.
       const int whole = length / E;
-      for (int q0 = lane; q0 < whole; q0 += 32 * kBatch) {
-        uint4 raw[kBatch];
+      auto pass = [&](auto words, auto half) {
+        constexpr int W = decltype(words)::value;
+        constexpr bool H = decltype(half)::value;
+        for (int q0 = lane; q0 < whole; q0 += 32 * kBatch) {
+          uint4 raw[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int q = q0 + 32 * b;
-          raw[b] = none;
-          if (q < whole) raw[b] = !EDGES || bytes == 0 ? line[q] : shifted<true>(line[q], line[q + 1], bytes);
+          for (int b = 0; b < kBatch; ++b) {
+            const int q = q0 + 32 * b;
+            raw[b] = none;
+            if (q < whole) raw[b] = W == 0 && !H ? line[q] : shifted<W, H>(line[q], line[q + 1]);
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) terms.template add<T>(raw[b]);
         }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) terms.template add<T>(raw[b]);
+        if (EDGES && whole * E < length && lane == 31)
+          terms.template add<T>(cut_behind<T>(shifted<W, H>(line[whole], line[whole + 1]), length - whole * E));
+      };
+      if constexpr (!EDGES) {
+        pass(std::integral_constant<int, 0>(), std::false_type());
+      } else {
+        switch (bytes >> 1) {
+          case 0: pass(std::integral_constant<int, 0>(), std::false_type()); break;
+          case 1: pass(std::integral_constant<int, 0>(), std::true_type()); break;
+          case 2: pass(std::integral_constant<int, 1>(), std::false_type()); break;
+          case 3: pass(std::integral_constant<int, 1>(), std::true_type()); break;
+          case 4: pass(std::integral_constant<int, 2>(), std::false_type()); break;
+          case 5: pass(std::integral_constant<int, 2>(), std::true_type()); break;
+          case 6: pass(std::integral_constant<int, 3>(), std::false_type()); break;
+          default: pass(std::integral_constant<int, 3>(), std::true_type()); break;
+        }
       }
-      if (EDGES && whole * E < length && lane == 31)
-        terms.template add<T>(cut_behind<T>(shifted<true>(line[whole], line[whole + 1], bytes), length - whole * E));
     }
     sum.s = warp_sum(terms.get());
     // The token's logit has been read before this warp's sum lets the others write the row's gradient, which may
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
     load(first, a, 0);
     load(first + step, a1, 1);
   }
-  float token_logit = 0.f, token_logit1 = 0.f;
+  float token_logit = 0.f, token_logit1 = 0.f, loss = 0.f;
   if (a >= 0) token_logit = sum_row(first, 0, xa, xe);
   int s = 0;
   for (int64_t i = first; i < p.n; i += step) {
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
       now.old = __uint_as_float(__shfl_sync(0xffffffffu, word, 3));
       now.adv = __uint_as_float(__shfl_sync(0xffffffffu, word, 4));
       now.ref = __uint_as_float(__shfl_sync(0xffffffffu, word, 5));
-      const float scale = row_end(p, i, now, token_logit, sum, unit == 0 && lane == 0);
+      const float scale = row_end(p, i, now, token_logit, sum, unit == 0 && lane == 0, loss);
       if (dx) {
         const float base = finite_or_zero(sum.m), per = -scale * __frcp_rn(sum.s);
         const int inside = a - from - c.head;  // the token's place in this share, if it has one
@@ -579,6 +589,8 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
     word = word1, word1 = word2, word2 = word3, a = a1, a1 = a2;
     token_logit = token_logit1, xe = xe1, xa1 = xa2, xe1 = xe2;
   }
+  // One term per cluster or warp: its rows' in their order.
+  if (p.loss_terms && unit == 0 && lane == 0) p.loss_terms[first] = loss;
   // Rows behind the last are never loaded, so no load is on its way here, unless a wait ran out.
   if (lane == 0) {
     if (*abort_flag)
@@ -605,7 +617,10 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
   const T* x = static_cast<const T*>(p.logits) + i * p.ld;
   T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd : nullptr;
   if (r.a < 0) {
-    if (threadIdx.x == 0) row_skipped(p, i);
+    if (threadIdx.x == 0) {
+      row_skipped(p, i);
+      if (p.loss_terms) p.loss_terms[i] = 0.f;
+    }
     if (dx)
       for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) dx[c] = row::from_f<T>(0.f);
     return;
@@ -627,7 +642,9 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
   __syncthreads();
   t = part[0];
   for (int w = 1; w < kTwiceThreads / 32; ++w) t = join(t, part[w], k);
-  const float scale = row_end(p, i, r, xa, t, threadIdx.x == 0);
+  float loss = 0.f;
+  const float scale = row_end(p, i, r, xa, t, threadIdx.x == 0, loss);
+  if (threadIdx.x == 0 && p.loss_terms) p.loss_terms[i] = loss;
   if (!dx) return;
   base = finite_or_zero(t.m);
   const float per = -scale * __frcp_rn(t.s);
@@ -646,7 +663,7 @@ __global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const PolicyLau
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   float acc = 0.f;
-  for (int64_t i = threadIdx.x; i < p.n; i += kSumThreads) acc += __ldcg(p.row_loss + i);
+  for (int64_t i = threadIdx.x; i < p.terms; i += kSumThreads) acc += __ldcg(p.loss_terms + i);
   acc = row::block_sum(acc, red);
   if (threadIdx.x == 0) *p.loss = acc;
 }
@@ -710,7 +727,8 @@ cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   if (e != cudaSuccess || best == 0) return e;
   *launched = true;
   p.slot_bytes = kSlotBytes;
-  const unsigned ctas = static_cast<unsigned>(std::min<int64_t>(p.n, best) * p.cluster);
+  p.terms = std::min<int64_t>(p.n, best);
+  const unsigned ctas = static_cast<unsigned>(p.terms * p.cluster);
   return row::launch(policy_ring_kernel<T, MODE, EDGES>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
 }
 
@@ -725,6 +743,7 @@ cudaError_t launch_solo(PolicyLaunch& p, int sms, cudaStream_t stream) {
   if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, R::kThreads, smem);
   if (e != cudaSuccess) return e;
   const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * std::max(per_sm, 1), (p.n + R::kWarps - 1) / R::kWarps);
+  p.terms = ctas * R::kWarps;
   return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), R::kThreads, smem, stream, p);
 }
 
@@ -748,12 +767,16 @@ cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
   if (e == cudaSuccess && !launched)
     e = edges ? launch_ring<T, kWide, true>(p, stream, &launched) : launch_ring<T, kWide, false>(p, stream, &launched);
   if (e != cudaSuccess || launched) return e;
+  p.terms = p.n;
   return row::launch(policy_twice_kernel<T>, dim3(static_cast<unsigned>(p.n)), kTwiceThreads, 0, stream, p);
 }
 
 }  // namespace
 
+int64_t policy_workspace(int64_t n) { return (n + Ring<kSolo>::kWarps) * static_cast<int64_t>(sizeof(float)); }
+
 cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream) {
+  p.terms = 0;
   if (p.n > 0) {
     const cudaError_t e = p.dtype == 0 ? launch_rows<float>(p, sms, stream) : launch_rows<__nv_bfloat16>(p, sms, stream);
     if (e != cudaSuccess) return e;
