@@ -364,11 +364,9 @@ struct RmsNormLaunch {
   int64_t ldy;
   float* scales;  // e4m3 output: n x ceil(dim / group), null otherwise
   int64_t group;  // columns per scale; 0: the whole row
-  // Set by launch_add_rmsnorm: threads per row, scales per row, shared memory for a row of bytes, and whether
-  // every row of x starts on 16 bytes.
-  int tpr, parts, stage, aligned;
-  // Threads that form a row's sum; shared memory words of a row that passes through it for that (0: does not).
-  int sum_threads, line;
+  // Set by launch_add_rmsnorm: threads per row and those that form its sum; scales per row and the lanes that
+  // share one (0: more than a warp); shared memory bytes for a row of bytes and words for a row of h (0: none).
+  int tpr, sum_threads, parts, lanes, stage, line;
 };
 cudaError_t launch_add_rmsnorm(RmsNormLaunch& p, int sms, cudaStream_t stream);
 

@@ -9,16 +9,15 @@
 //   dx = dh + rho d - h rho^3 / dim * sum(d h),   dgain = sum over rows of dy h rho.
 //
 // Both are bound by memory: each element is read once and written once. A row is held in the registers of
-// `tpr` threads, K 16-byte granules of it in each, so one read serves the sums and the outputs. Rows need
-// not start on 16 bytes: the granules are cut where the addresses are aligned, the row's first and last one
-// may be partial, and those are read and written element by element. CTAs stay and take every
-// (gridDim.x * rows per CTA)-th row, a multiple of 8, so all rows of a thread start at the same offset from
-// 16 bytes whatever their length: its columns, and with them its gains and its sums for dgain, stay the
-// same. The next row is on its way while the current one is reduced and written.
+// `tpr` threads, K 16-byte granules of it in each, so one read serves the sums and the outputs. Rows need not
+// start on 16 bytes: granules are cut where the addresses are aligned, and the up to 2 (E - 1) elements before
+// and behind them are held one per thread. CTAs stay and take every (gridDim.x * rows per CTA)-th row, a multiple
+// of 8, so all rows of a thread start at the same offset from 16 bytes whatever their length: its columns, and
+// with them its gains and its sums for dgain, stay the same.
 //
-// The forward sum has one order for every layout, that of rows that start on 16 bytes: thread t of sum_threads
-// adds granules t, t + sum_threads, ... counted from the row's first element, then the threads join. Rows that
-// start elsewhere pass through shared memory for it, so a value's bits do not depend on where it lies.
+// The forward sum has one order for every layout: thread t of sum_threads adds groups of E elements t,
+// t + sum_threads, ... counted from the row's first element, then the threads join. Rows that are not whole
+// granules pass through shared memory for it, so a value's bits do not depend on where it lies.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -50,44 +49,36 @@ __device__ __forceinline__ unsigned block_top(unsigned v, unsigned* red) {
 
 // ---------------------------------------------------------------------------- granules
 
-// The elements [e0, e0 + E) of a row of `dim` elements, 16 bytes at an aligned address; elements outside the
-// row are neither read nor written, and count as 0.
 template <typename T>
-struct Granule {
-  static constexpr int E = 16 / sizeof(T);
+constexpr int kPer = 16 / sizeof(T);  // elements of a granule
 
-  static __device__ __forceinline__ uint4 load(const T* row, int e0, int dim) {
-    if (e0 >= 0 && e0 + E <= dim) return __ldcs(reinterpret_cast<const uint4*>(row + e0));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const int e = e0 + j;
-      if (e < 0 || e >= dim) continue;
-      if constexpr (sizeof(T) == 4)
-        w[j] = __float_as_uint(row[e]);
-      else
-        w[j / 2] |= static_cast<uint32_t>(__bfloat16_as_ushort(row[e])) << (j % 2 * 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+template <typename T>
+__device__ __forceinline__ void store_granule(T* dst, const float (&v)[kPer<T>]) {
+  __stcs(reinterpret_cast<uint4*>(dst), row::pack16(v));
+}
+
+// Where a row lies: `head` elements before the first 16-byte address, `full` granules, `tail` elements.
+template <typename T>
+struct Cut {
+  int head, full, tail;
+  __device__ __forceinline__ Cut(const T* x, int dim) {
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    head = min((kPer<T> - off) & (kPer<T> - 1), dim);
+    full = (dim - head) / kPer<T>;
+    tail = dim - head - full * kPer<T>;
   }
-
-  static __device__ __forceinline__ void store(T* row, int e0, int dim, const float (&v)[E]) {
-    if (e0 >= 0 && e0 + E <= dim) {
-      if constexpr (sizeof(T) == 4)
-        __stcs(reinterpret_cast<float4*>(row + e0), make_float4(v[0], v[1], v[2], v[3]));
-      else
-        __stcs(reinterpret_cast<uint4*>(row + e0), row::pack16(v));
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (e0 + j >= 0 && e0 + j < dim) row[e0 + j] = row::from_f<T>(v[j]);
+  // The element outside the granules that thread t of a row (16 threads at least) holds, or -1.
+  __device__ __forceinline__ int edge(int t) const {
+    if (t < head) return t;
+    if (t >= 8 && t - 8 < tail) return head + full * kPer<T> + t - 8;
+    return -1;
   }
 };
 
+// Gains [e0, e0 + E), ones outside the row or without gains.
 template <int E>
 __device__ __forceinline__ void load_gain(float (&g)[E], const float* gain, int e0, int dim) {
-  if (gain && e0 >= 0 && e0 + E <= dim && (reinterpret_cast<uintptr_t>(gain + e0) & 15) == 0) {
+  if (gain && e0 + E <= dim && (reinterpret_cast<uintptr_t>(gain + e0) & 15) == 0) {
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
       const float4 u = __ldg(reinterpret_cast<const float4*>(gain + e0 + j));
@@ -96,7 +87,7 @@ __device__ __forceinline__ void load_gain(float (&g)[E], const float* gain, int 
     return;
   }
 #pragma unroll
-  for (int j = 0; j < E; ++j) g[j] = gain && e0 + j >= 0 && e0 + j < dim ? __ldg(gain + e0 + j) : 1.f;
+  for (int j = 0; j < E; ++j) g[j] = gain && e0 + j < dim ? __ldg(gain + e0 + j) : 1.f;
 }
 
 // Sums over the `tpr` threads of a row. `red` alternates between two halves from row to row, so one barrier
@@ -124,12 +115,30 @@ __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[32]
 
 // ---------------------------------------------------------------------------- forward
 
+// max that gives NaN for NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
+// E elements as e4m3 bytes.
+template <int E>
+__device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[E], float inv) {
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[j] * inv, v[j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[j + 2] * inv, v[j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[j / 4] = lo | hi << 16;
+  }
+}
+
 // THREADS: the most of a CTA. HELD: gains stay in registers and the next row is loaded early; without it, for
-// longer rows, a thread has fewer registers and more CTAs overlap.
-template <typename T, int K, bool FP8, int THREADS, bool HELD>
-__global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
-  using G = Granule<T>;
-  constexpr int E = G::E;
+// longer rows, a thread has fewer registers and more CTAs overlap. EDGES: rows that are not whole granules.
+template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
+__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREADS <= 320 ? 2 : 1)
+    add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
+  constexpr int E = kPer<T>;
   __shared__ float red[2][32][1];
   extern __shared__ __align__(16) uint8_t dyn[];
   ptx::griddep_launch_dependents();
@@ -140,32 +149,43 @@ __global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) ad
   const T* x = static_cast<const T*>(p.x) + (first + slot) * p.ldx;
   const T* r = p.residual ? static_cast<const T*>(p.residual) + (first + slot) * p.ldr : nullptr;
   T* h = p.h ? static_cast<T*>(p.h) + (first + slot) * p.ldh : nullptr;
-  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  auto start = [&](int k) { return (t + k * tpr) * E - shift; };
+  const Cut<T> cut(x, dim);
+  const int full = EDGES ? cut.full : dim / E, edge = EDGES ? cut.edge(t) : -1;
+  auto start = [&](int k) { return (EDGES ? cut.head : 0) + (t + k * tpr) * E; };
+  auto holds = [&](int k) { return t + k * tpr < full; };
+  // 8-bit outputs of such rows are formed from the line below, by groups of elements from the row's first one.
+  constexpr bool LINED = FP8 && EDGES;
+  auto first_out = [&](int k) { return LINED ? (t + k * tpr) * E : start(k); };
   float gain[HELD ? K : 1][E];
   if (HELD)
 #pragma unroll
-    for (int k = 0; k < K; ++k) load_gain(gain[k], p.gain, start(k), dim);
+    for (int k = 0; k < K; ++k) load_gain(gain[k], p.gain, first_out(k), dim);
+  const float gain_edge = EDGES && !FP8 && edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
 
-  // 8-bit output: the largest |y| of each group, alternating between two halves; then a row of bytes.
-  const int parts = FP8 ? p.parts : 0;
+  // For a group that is not within a warp, the largest |y| of each (as bits, which order as the values do),
+  // alternating between two halves. Then a row of bytes. Then h in the order of its elements, a word left out
+  // after every 32, so that lanes E elements apart use different banks.
+  const int parts = FP8 ? p.parts : 0, top_bytes = FP8 && p.lanes == 0 ? (2 * rows * parts * 4 + 15) / 16 * 16 : 0;
   unsigned* tops = reinterpret_cast<unsigned*>(dyn);
-  uint8_t* bytes = dyn + (2 * rows * parts * 4 + 15) / 16 * 16 + slot * p.stage;
-  // Rows that do not start on 16 bytes: h in the order of its elements, a word left out after every 32, so that
-  // lanes eight elements apart use different banks.
-  float* line = reinterpret_cast<float*>(dyn + (2 * rows * parts * 4 + 15) / 16 * 16 + rows * p.stage) + slot * p.line;
-  if (FP8) {
+  uint8_t* bytes = dyn + top_bytes + slot * p.stage;
+  float* line = reinterpret_cast<float*>(dyn + top_bytes + rows * p.stage) + slot * p.line;
+  if (top_bytes) {
     for (int k = threadIdx.x; k < 2 * rows * parts; k += blockDim.x) tops[k] = 0;
     __syncthreads();
   }
 
   uint4 xr[K], rr[K];
+  T xe{}, re{};
   auto fetch = [&](int64_t i) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const bool in = i < p.n && start(k) < dim;
-      xr[k] = in ? G::load(x, start(k), dim) : make_uint4(0, 0, 0, 0);
-      rr[k] = in && r ? G::load(r, start(k), dim) : make_uint4(0, 0, 0, 0);
+      const bool in = i < p.n && holds(k);
+      xr[k] = in ? __ldcs(reinterpret_cast<const uint4*>(x + start(k))) : make_uint4(0, 0, 0, 0);
+      rr[k] = in && r ? __ldcs(reinterpret_cast<const uint4*>(r + start(k))) : make_uint4(0, 0, 0, 0);
+    }
+    if (EDGES && i < p.n && edge >= 0) {
+      xe = x[edge];
+      if (r) re = r[edge];
     }
   };
   if (HELD) fetch(first + slot);
@@ -173,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) ad
   for (int64_t base = first; base < p.n; base += step, half ^= 1) {
     const int64_t i = base + slot;
     if (!HELD) fetch(i);
-    float v[K][E];
+    float v[K][E], ve = 0.f;
     float s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -183,25 +203,27 @@ __global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) ad
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         v[k][j] = a[j] + b[j];
-        if (p.line == 0) s[0] = fmaf(v[k][j], v[k][j], s[0]);
+        if (!EDGES) s[0] = fmaf(v[k][j], v[k][j], s[0]);
       }
     }
+    if (EDGES) ve = row::to_f(xe) + row::to_f(re);
     x += step * p.ldx;
     if (r) r += step * p.ldr;
     if (HELD && base + step < p.n) fetch(i + step);
-    if (h && i < p.n)
+    if (h && i < p.n) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (start(k) < dim) G::store(h, start(k), dim, v[k]);
+        if (holds(k)) store_granule(h + start(k), v[k]);
+      if (edge >= 0) h[edge] = row::from_f<T>(ve);
+    }
     if (h) h += step * p.ldh;
-    if (p.line) {
+    if (EDGES) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
+        if (holds(k))
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const int e = start(k) + j;
-          if (e >= 0 && e < dim) line[e + (e >> 5)] = v[k][j];
-        }
+          for (int j = 0; j < E; ++j) line[start(k) + j + ((start(k) + j) >> 5)] = v[k][j];
+      if (edge >= 0) line[edge + (edge >> 5)] = ve;
       __syncthreads();
       if (t < p.sum_threads)
         for (int e0 = t * E; e0 < dim; e0 += p.sum_threads * E)
@@ -216,79 +238,77 @@ __global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) ad
     const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (!HELD) load_gain(gain[0], p.gain, start(k), dim);
+      if (!HELD) load_gain(gain[0], p.gain, first_out(k), dim);
 #pragma unroll
-      for (int j = 0; j < E; ++j) v[k][j] = v[k][j] * rho * gain[HELD ? k : 0][j];
+      for (int j = 0; j < E; ++j) {
+        const int e = first_out(k) + j;
+        if (LINED) v[k][j] = e < dim ? line[e + (e >> 5)] : 0.f;
+        v[k][j] = v[k][j] * rho * gain[HELD ? k : 0][j];
+      }
     }
     if constexpr (!FP8) {
       T* y = static_cast<T*>(p.y) + i * p.ldy;
-      if (i < p.n)
+      if (i < p.n) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          if (start(k) < dim) G::store(y, start(k), dim, v[k]);
+          if (holds(k)) store_granule(y + start(k), v[k]);
+        if (edge >= 0) y[edge] = row::from_f<T>(ve * rho * gain_edge);
+      }
     } else {
-      unsigned* top = tops + (half * rows + slot) * parts;
       const int group = p.group ? static_cast<int>(p.group) : 1 << 30;
-      // Lanes that share a group where granules do not straddle two: the largest of theirs goes to one lane.
-      const int lanes = p.aligned || p.group == 0 ? min(min(group / E, 32), tpr) : 1;
+      unsigned* top = tops + (half * rows + slot) * parts;
+      float most[K];  // of the granule, then of its group
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int e0 = start(k);
-        unsigned low = 0, high = 0;  // of the granule's first group, and of the next one
-        const int border = (max(e0, 0) / group + 1) * group;
+        most[k] = 0.f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          const unsigned b = e0 + j >= 0 && e0 + j < dim ? __float_as_uint(fabsf(v[k][j])) : 0u;
-          if (e0 + j < border) low = max(low, b); else high = max(high, b);
-        }
-        for (int o = lanes / 2; o > 0; o >>= 1) low = max(low, __shfl_xor_sync(0xffffffffu, low, o));
-        if (i < p.n && e0 < dim) {
-          if (t % lanes == 0 && low) atomicMax(top + max(e0, 0) / group, low);
-          if (high) atomicMax(top + border / group, high);
-        }
+        for (int j = 0; j < E; ++j) most[k] = max_nan(most[k], fabsf(v[k][j]));
+        const int lanes = p.lanes ? p.lanes : 32;  // a group's, or a part of it
+        for (int o = lanes / 2; o > 0; o >>= 1) most[k] = max_nan(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+        if (p.lanes == 0 && i < p.n && first_out(k) < dim && (threadIdx.x & 31) == 0)
+          atomicMax(top + first_out(k) / group, __float_as_uint(most[k]));
       }
-      __syncthreads();
-      for (int k = t; k < parts; k += tpr) {
-        if (i < p.n) p.scales[i * parts + k] = scale_of(top[k]);
-        tops[((half ^ 1) * rows + slot) * parts + k] = 0;  // for the next row; its readers are a barrier behind
+      if (p.lanes == 0) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (first_out(k) < dim) most[k] = __uint_as_float(top[first_out(k) / group]);
+        for (int k = t; k < parts; k += tpr) {
+          if (i < p.n) p.scales[i * parts + k] = scale_of(top[k]);
+          tops[((half ^ 1) * rows + slot) * parts + k] = 0;  // for the next row; its readers are a barrier behind
+        }
       }
       uint8_t* q = static_cast<uint8_t*>(p.y) + i * p.ldy;
-      const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int e0 = start(k);
+        const int e0 = first_out(k);
         if (i >= p.n || e0 >= dim) continue;
-        const int part = max(e0, 0) / group, border = (part + 1) * group;
-        const float inv = __frcp_rn(scale_of(top[part]));
-        const float inv_next = border < e0 + E && border < dim ? __frcp_rn(scale_of(top[part + 1])) : inv;
+        const float scale = scale_of(__float_as_uint(most[k]));
+        if (p.lanes && t % p.lanes == 0) p.scales[i * parts + e0 / group] = scale;
         uint32_t w[E / 4];
-#pragma unroll
-        for (int j = 0; j < E; j += 2) {
-          const float lo = v[k][j] * (e0 + j < border ? inv : inv_next);
-          const float hi = v[k][j + 1] * (e0 + j + 1 < border ? inv : inv_next);
-          const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-          if (j % 4 == 0) w[j / 4] = two; else w[j / 4] |= two << 16;
-        }
-        if (p.stage == 0) {
-          if constexpr (E == 8)
-            *reinterpret_cast<uint2*>(q + e0) = make_uint2(w[0], w[1]);
-          else
-            *reinterpret_cast<uint32_t*>(q + e0) = w[0];
-        } else {
-#pragma unroll
-          for (int j = 0; j < E; ++j)
-            if (e0 + j >= 0 && e0 + j < dim) bytes[at + e0 + j] = static_cast<uint8_t>(w[j / 4] >> (j % 4 * 8));
-        }
+        pack_fp8(w, v[k], __frcp_rn(scale));
+        uint8_t* to = p.stage ? bytes + e0 : q + e0;
+        if constexpr (E == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(to) = w[0];
       }
       if (p.stage) {
-        // The row lies in shared memory as its bytes lie around 16-byte addresses; whole sixteens go out as such.
         __syncthreads();
+        // The row goes out by 16-byte addresses; what lies there begins between words of the bytes.
+        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
         if (i < p.n)
-          for (int c = t * 16; c < at + dim; c += tpr * 16) {
-            if (c >= at && c + 16 <= at + dim)
-              __stcs(reinterpret_cast<uint4*>(q - at + c), *reinterpret_cast<const uint4*>(bytes + c));
-            else
-              for (int b = max(c, at); b < min(c + 16, at + dim); ++b) q[b - at] = bytes[b];
+          for (int lo = t * 16 - at; lo < dim; lo += tpr * 16) {
+            if (lo >= 0 && lo + 16 <= dim) {
+              const uint32_t* from = reinterpret_cast<const uint32_t*>(bytes) + (lo >> 2);
+              const int bits = (lo & 3) * 8;
+              uint4 o;
+              o.x = __funnelshift_r(from[0], from[1], bits), o.y = __funnelshift_r(from[1], from[2], bits);
+              o.z = __funnelshift_r(from[2], from[3], bits), o.w = __funnelshift_r(from[3], from[4], bits);
+              __stcs(reinterpret_cast<uint4*>(q + lo), o);
+            } else {
+              for (int b = max(lo, 0); b < min(lo + 16, dim); ++b) q[b] = bytes[b];
+            }
           }
       }
     }
@@ -297,11 +317,11 @@ __global__ void __launch_bounds__(THREADS, HELD ? 3 : THREADS <= 320 ? 2 : 1) ad
 
 // ---------------------------------------------------------------------------- backward
 
-// The sums for dgain of a thread's columns stay in registers (REGS) or, for long rows, in shared memory.
-template <typename T, int K, int THREADS, bool REGS, bool AHEAD>
-__global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const RmsNormGradLaunch p) {
-  using G = Granule<T>;
-  constexpr int E = G::E;
+// The sums for dgain of a thread's columns, and its gains, stay in registers (REGS) or, for long rows, the sums in
+// shared memory. AHEAD: the next row is loaded early. PER_SM: CTAs that registers are to leave room for.
+template <typename T, int K, int THREADS, int PER_SM, bool REGS, bool AHEAD, bool EDGES>
+__global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(const RmsNormGradLaunch p) {
+  constexpr int E = kPer<T>;
   __shared__ float red[2][32][2];
   extern __shared__ __align__(16) uint8_t dyn[];
   ptx::griddep_launch_dependents();
@@ -313,9 +333,12 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const Rm
   const T* h = static_cast<const T*>(p.h) + (first + slot) * p.ldh;
   const T* dh = p.dh ? static_cast<const T*>(p.dh) + (first + slot) * p.lddh : nullptr;
   T* dx = static_cast<T*>(p.dx) + (first + slot) * p.lddx;
-  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(dy) & 15) / sizeof(T));
-  auto start = [&](int k) { return (t + k * tpr) * E - shift; };
-  float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E];
+  const Cut<T> cut(dy, dim);
+  const int full = EDGES ? cut.full : dim / E, edge = EDGES ? cut.edge(t) : -1;
+  auto start = [&](int k) { return (EDGES ? cut.head : 0) + (t + k * tpr) * E; };
+  auto holds = [&](int k) { return t + k * tpr < full; };
+  float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E], acc_edge = 0.f;
+  const float gain_edge = edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
   // Without REGS a thread's sums: four columns at [quarter][granule], so that a warp's accesses do not conflict.
   float4* sums = reinterpret_cast<float4*>(dyn);
   const int granules = K * tpr;
@@ -330,36 +353,47 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const Rm
       for (int j = 0; j < E / 4; ++j) sums[j * granules + t + k * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
-  uint4 yr[2][K], hr[2][K], tr[2][K];  // of the current row and the next
-  auto fetch = [&](uint4 (&a)[K], uint4 (&b)[K], uint4 (&c)[K], int64_t i) {
+  struct Row {
+    uint4 y[K], h[K], t[K];
+    T ye, he, te;
+  };
+  Row now{}, next{};
+  auto fetch = [&](Row& to, int64_t i) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const bool in = i < p.n && start(k) < dim;
-      a[k] = in ? G::load(dy, start(k), dim) : make_uint4(0, 0, 0, 0);
-      b[k] = in ? G::load(h, start(k), dim) : make_uint4(0, 0, 0, 0);
-      c[k] = in && dh ? G::load(dh, start(k), dim) : make_uint4(0, 0, 0, 0);
+      const bool in = i < p.n && holds(k);
+      to.y[k] = in ? __ldcs(reinterpret_cast<const uint4*>(dy + start(k))) : make_uint4(0, 0, 0, 0);
+      to.h[k] = in ? __ldcs(reinterpret_cast<const uint4*>(h + start(k))) : make_uint4(0, 0, 0, 0);
+      to.t[k] = in && dh ? __ldcs(reinterpret_cast<const uint4*>(dh + start(k))) : make_uint4(0, 0, 0, 0);
+    }
+    if (EDGES) {
+      to.ye = to.he = to.te = row::from_f<T>(0.f);
+      if (i < p.n && edge >= 0) {
+        to.ye = dy[edge];
+        to.he = h[edge];
+        if (dh) to.te = dh[edge];
+      }
     }
     dy += step * p.lddy;
     h += step * p.ldh;
     if (dh) dh += step * p.lddh;
   };
-  if (AHEAD) fetch(yr[1], hr[1], tr[1], first + slot);
+  if (AHEAD) fetch(next, first + slot);
   int half = 0;
   for (int64_t base = first; base < p.n; base += step, half ^= 1) {
     const int64_t i = base + slot;
     if (AHEAD) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) yr[0][k] = yr[1][k], hr[0][k] = hr[1][k], tr[0][k] = tr[1][k];
-      if (base + step < p.n) fetch(yr[1], hr[1], tr[1], i + step);
+      now = next;
+      if (base + step < p.n) fetch(next, i + step);
     } else {
-      fetch(yr[0], hr[0], tr[0], i);
+      fetch(now, i);
     }
     float s[2] = {0.f, 0.f};  // sum of h^2, sum of d h
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float a[E], b[E];
-      row::unpack16<T>(a, yr[0][k]);
-      row::unpack16<T>(b, hr[0][k]);
+      row::unpack16<T>(a, now.y[k]);
+      row::unpack16<T>(b, now.h[k]);
       if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -367,15 +401,20 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const Rm
         s[1] = fmaf(a[j] * gain[REGS ? k : 0][j], b[j], s[1]);
       }
     }
+    const float he = EDGES ? row::to_f(now.he) : 0.f, de = EDGES ? row::to_f(now.ye) * gain_edge : 0.f;
+    if (EDGES) {
+      s[0] = fmaf(he, he, s[0]);
+      s[1] = fmaf(de, he, s[1]);
+    }
     row_sum(s, tpr, red, half);
     const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
     const float back = s[1] / static_cast<float>(dim) * rho * rho * rho;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float a[E], b[E], c[E];
-      row::unpack16<T>(a, yr[0][k]);
-      row::unpack16<T>(b, hr[0][k]);
-      row::unpack16<T>(c, tr[0][k]);
+      row::unpack16<T>(a, now.y[k]);
+      row::unpack16<T>(b, now.h[k]);
+      row::unpack16<T>(c, now.t[k]);
       if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
       float4 sum;
 #pragma unroll
@@ -390,7 +429,11 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const Rm
         }
         c[j] = fmaf(rho, a[j] * gain[REGS ? k : 0][j], fmaf(-back, b[j], c[j]));
       }
-      if (i < p.n && start(k) < dim) G::store(dx, start(k), dim, c);
+      if (i < p.n && holds(k)) store_granule(dx + start(k), c);
+    }
+    if (EDGES && i < p.n && edge >= 0) {
+      acc_edge = fmaf(row::to_f(now.ye), he * rho, acc_edge);
+      dx[edge] = row::from_f<T>(fmaf(rho, de, fmaf(-back, he, row::to_f(now.te))));
     }
     dx += step * p.lddx;
   }
@@ -402,25 +445,26 @@ __global__ void __launch_bounds__(THREADS) add_rmsnorm_grad_rows_kernel(const Rm
   for (int turn = 0; turn < rows; ++turn) {
     if (rows > 1) __syncthreads();
     if (turn != slot) continue;
+    auto put = [&](int e, float v) {
+      if (rows > 1) {
+        if (turn > 0) v += line[e];
+        line[e] = v;
+      }
+      if (turn == rows - 1) out[e] = v;
+    };
 #pragma unroll
     for (int k = 0; k < K; ++k)
+      if (holds(k))
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int e = start(k) + j;
-        if (e < 0 || e >= dim) continue;
-        float v;
-        if (REGS) {
-          v = acc[k][j];
-        } else {
-          const float4 sum = sums[j / 4 * granules + t + k * tpr];
-          v = j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w;
+        for (int j = 0; j < E; ++j) {
+          if (REGS) {
+            put(start(k) + j, acc[k][j]);
+          } else {
+            const float4 sum = sums[j / 4 * granules + t + k * tpr];
+            put(start(k) + j, j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w);
+          }
         }
-        if (rows > 1) {
-          if (turn > 0) v += line[e];
-          line[e] = v;
-        }
-        if (turn == rows - 1) out[e] = v;
-      }
+    if (edge >= 0) put(edge, acc_edge);
   }
 }
 
@@ -462,7 +506,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormL
   __shared__ unsigned redu[32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  constexpr int E = Granule<T>::E;
+  constexpr int E = kPer<T>;
   const int threads = blockDim.x;
   const int64_t i = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + i * p.ldx;
@@ -573,20 +617,20 @@ struct Array {
   int64_t ld;
 };
 
-// Granules of a row where every array starts rows at the same offsets from 16 bytes; 0 where they differ.
-int row_granules(std::initializer_list<Array> arrays, int64_t n, int64_t dim, size_t elem) {
+// Whether every array starts its rows at the same offsets from 16 bytes as the first one.
+bool same_offsets(std::initializer_list<Array> arrays, int64_t n, size_t elem) {
   const Array& a = *arrays.begin();
-  const uintptr_t at = reinterpret_cast<uintptr_t>(a.ptr) % 16;
-  const size_t step = n > 1 ? static_cast<size_t>(a.ld) * elem % 16 : 0;
   for (const Array& b : arrays)
-    if (b.ptr && (reinterpret_cast<uintptr_t>(b.ptr) % 16 != at ||
-                  (n > 1 && static_cast<size_t>(b.ld) * elem % 16 != step)))
-      return 0;
-  const int per = static_cast<int>(16 / elem);
-  if (dim > kMaxHeld) return 0;
-  const int64_t offset = at == 0 && step == 0 ? 0 : per - 1;
-  const int64_t granules = (dim + offset + per - 1) / per;
-  return granules * per <= kMaxHeld ? static_cast<int>(granules) : 0;
+    if (b.ptr && ((reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr)) % 16 != 0 ||
+                  (n > 1 && (static_cast<size_t>(b.ld) - static_cast<size_t>(a.ld)) * elem % 16 != 0)))
+      return false;
+  return true;
+}
+
+// Whether rows are not whole granules.
+bool has_edges(const Array& a, int64_t n, int64_t dim, size_t elem) {
+  return reinterpret_cast<uintptr_t>(a.ptr) % 16 != 0 || (n > 1 && static_cast<size_t>(a.ld) * elem % 16 != 0) ||
+         static_cast<size_t>(dim) * elem % 16 != 0;
 }
 
 // Threads of a row for K granules each: whole warps, or a power of two below one.
@@ -620,27 +664,26 @@ cudaError_t row_grid(RowGrid& g, void (*kernel)(P), int tpr, int64_t n, size_t s
   return cudaSuccess;
 }
 
-template <typename T, int K, bool FP8, int THREADS, bool HELD>
-cudaError_t launch_rows(RmsNormLaunch& p, int granules, int sms, cudaStream_t stream) {
-  auto* kernel = add_rmsnorm_rows_kernel<T, K, FP8, THREADS, HELD>;
-  constexpr int E = Granule<T>::E;
+template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
+cudaError_t launch_rows(RmsNormLaunch& p, int sms, cudaStream_t stream) {
+  auto* kernel = add_rmsnorm_rows_kernel<T, K, FP8, THREADS, HELD, EDGES>;
+  constexpr int E = kPer<T>;
+  const int tpr = std::max(p.sum_threads, EDGES ? 16 : 1);
   size_t per_row = 0;
-  p.parts = 0, p.stage = 0;
-  p.aligned = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && (p.n == 1 || static_cast<size_t>(p.ldx) * sizeof(T) % 16 == 0);
+  p.parts = 0, p.stage = 0, p.lanes = 0;
   if (FP8) {
     p.parts = p.group ? static_cast<int>((p.dim + p.group - 1) / p.group) : 1;
+    // Lanes that share a scale, where that is a part of a warp; a group may be longer than the row.
+    const int lanes = p.group ? std::min(static_cast<int>(p.group) / E, tpr < 32 ? tpr : 1 << 30) : tpr;
+    p.lanes = lanes <= 32 ? lanes : 0;
+    if (p.lanes == 0) per_row += static_cast<size_t>(2 * p.parts * 4 + 16);
     // A granule's bytes are stored as such where they are aligned in every row.
-    const bool whole = p.aligned && (reinterpret_cast<uintptr_t>(p.y) | static_cast<uintptr_t>(p.n == 1 ? 0 : p.ldy)) % E == 0 &&
-                       p.dim % E == 0;
-    p.stage = whole ? 0 : static_cast<int>((p.dim + 15 + 15) / 16 * 16);
-    per_row = static_cast<size_t>(2 * p.parts * 4 + 16 + p.stage);
+    const bool direct = !EDGES && (reinterpret_cast<uintptr_t>(p.y) | static_cast<uintptr_t>(p.n == 1 ? 0 : p.ldy)) % E == 0;
+    p.stage = direct ? 0 : static_cast<int>((p.dim + 15) / 16 * 16 + 32);
+    per_row += static_cast<size_t>(p.stage);
   }
-  p.line = 0;
-  if (!p.aligned) {
-    p.line = static_cast<int>(p.dim + p.dim / 32 + 1);
-    per_row += static_cast<size_t>(p.line) * 4;
-  }
-  const int tpr = std::max(row_threads(granules, K), p.sum_threads);
+  p.line = EDGES ? static_cast<int>(p.dim + p.dim / 32 + 1) : 0;
+  per_row += static_cast<size_t>(p.line) * 4;
   const size_t smem = per_row * (tpr >= kThreads ? 1 : kThreads / tpr);
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -653,31 +696,39 @@ cudaError_t launch_rows(RmsNormLaunch& p, int granules, int sms, cudaStream_t st
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
-template <typename T, bool FP8>
-cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
-  const int granules = row_granules({{p.x, p.ldx}, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n,
-                                    p.dim, sizeof(T));
-  // The order of the sum is that of the kernel that takes aligned rows of this length.
-  const int whole = static_cast<int>((p.dim + Granule<T>::E - 1) / Granule<T>::E);
+template <typename T, bool FP8, bool EDGES>
+cudaError_t launch_held_norm(RmsNormLaunch& p, int granules, int sms, cudaStream_t stream) {
   constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;  // 16 and 32 elements per thread
-  p.sum_threads = std::min(
-      row_threads(whole, whole <= 256 ? 1 : whole <= 512 ? 2 : whole <= 256 * kHeld ? kHeld : kLong), kMaxThreads);
-  if (granules == 0)
-    return row::launch(add_rmsnorm_kernel<T>, dim3(static_cast<unsigned>(p.n)), std::max(32, p.sum_threads), 0, stream, p);
-  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true>(p, granules, sms, stream);
-  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true>(p, granules, sms, stream);
-  if (granules <= 256 * kHeld) return launch_rows<T, kHeld, FP8, 256, true>(p, granules, sms, stream);
-  if (std::max(row_threads(granules, kLong), p.sum_threads) <= 320)
-    return launch_rows<T, kLong, FP8, 320, false>(p, granules, sms, stream);
-  return launch_rows<T, kLong, FP8, 512, false>(p, granules, sms, stream);
+  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true, EDGES>(p, sms, stream);
+  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true, EDGES>(p, sms, stream);
+  if (granules <= 256 * kHeld) return launch_rows<T, kHeld, FP8, 256, true, EDGES>(p, sms, stream);
+  if (p.sum_threads <= 320) return launch_rows<T, kLong, FP8, 320, false, EDGES>(p, sms, stream);
+  return launch_rows<T, kLong, FP8, 512, false, EDGES>(p, sms, stream);
 }
 
-template <typename T, int K, int THREADS, bool REGS, bool AHEAD>
+template <typename T, bool FP8>
+cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
+  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
+  const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>);
+  p.sum_threads = std::min(row_threads(granules, granules <= 256           ? 1
+                                                 : granules <= 512         ? 2
+                                                 : granules <= 256 * kHeld ? kHeld
+                                                                           : kLong),
+                           kMaxThreads);
+  const Array x{p.x, p.ldx};
+  if (p.dim > kMaxHeld ||
+      !same_offsets({x, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n, sizeof(T)))
+    return row::launch(add_rmsnorm_kernel<T>, dim3(static_cast<unsigned>(p.n)), std::max(32, p.sum_threads), 0, stream, p);
+  return has_edges(x, p.n, p.dim, sizeof(T)) ? launch_held_norm<T, FP8, true>(p, granules, sms, stream)
+                                             : launch_held_norm<T, FP8, false>(p, granules, sms, stream);
+}
+
+template <typename T, int K, int THREADS, int PER_SM, bool REGS, bool AHEAD, bool EDGES>
 cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
-  auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, REGS, AHEAD>;
+  auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, PER_SM, REGS, AHEAD, EDGES>;
   // Sums of long rows, or the line in which a CTA's short rows join.
-  const int tpr = row_threads(granules, K), rows = tpr >= kThreads ? 1 : kThreads / tpr;
-  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * 16 / sizeof(T) * 4;
+  const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
+  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * kPer<T> * 4;
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -690,11 +741,23 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
+template <typename T, bool EDGES>
+cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
+  if (granules <= 256) return launch_grad_rows<T, 1, 256, 3, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 1024) return launch_grad_rows<T, 4, 256, 3, false, false, EDGES>(p, granules, sms, stream);
+  if (granules <= 2048) return launch_grad_rows<T, 4, 512, 1, false, false, EDGES>(p, granules, sms, stream);
+  if constexpr (sizeof(T) == 4)
+    return launch_grad_rows<T, 4, 1024, 1, false, false, EDGES>(p, granules, sms, stream);
+  else
+    return cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
+}
+
 template <typename T>
 cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
-  const int granules = row_granules({{p.dy, p.lddy}, {p.h, p.ldh}, {p.dh, p.lddh}, {p.dx, p.lddx}}, p.n, p.dim, sizeof(T));
+  const Array dy{p.dy, p.lddy};
   cudaError_t e;
-  if (granules == 0) {
+  if (p.dim > kMaxHeld || !same_offsets({dy, {p.h, p.ldh}, {p.dh, p.lddh}, {p.dx, p.lddx}}, p.n, sizeof(T))) {
     const dim3 grid(static_cast<unsigned>(p.n));
     if (p.dgain) {  // before dx, which may be written over dy
       RmsNormGradLaunch only_rho = p;
@@ -707,15 +770,10 @@ cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
     e = row::launch(add_rmsnorm_grad_kernel<T>, grid, kThreads, 0, stream, p);
-  } else if (granules <= 256) {
-    e = launch_grad_rows<T, 1, 256, true, true>(p, granules, sms, stream);
-  } else if (granules <= 512) {
-    e = launch_grad_rows<T, 2, 256, true, true>(p, granules, sms, stream);
-  } else if (granules > 2048) {
-    if constexpr (sizeof(T) == 4) e = launch_grad_rows<T, 4, 1024, false, false>(p, granules, sms, stream);
-    else e = cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
   } else {
-    e = launch_grad_rows<T, 4, 512, false, true>(p, granules, sms, stream);
+    const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>);
+    e = has_edges(dy, p.n, p.dim, sizeof(T)) ? launch_held_grad<T, true>(p, granules, sms, stream)
+                                             : launch_held_grad<T, false>(p, granules, sms, stream);
   }
   if (e != cudaSuccess || !p.dgain) return e;
   return row::launch(rmsnorm_dgain_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), kThreads, 0, stream, p);
