@@ -231,14 +231,15 @@ __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const Embe
 
 // ---------------------------------------------------------------------------- 3. sums by chunk
 
-// A group of `tpr` threads adds the rows of one chunk over tpr * kCols consecutive columns. With 16-byte rows
-// (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise its columns lie tpr apart.
+// A group of `tpr` threads adds the rows of one chunk over tpr * kCols consecutive columns, kAhead rows loaded at a
+// time. With 16-byte rows (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise its
+// columns lie tpr apart.
 template <typename TG, bool VEC>
 struct Columns;
 
 template <typename TG>
 struct Columns<TG, true> {
-  static constexpr int kCols = 16 / sizeof(TG);
+  static constexpr int kCols = 16 / sizeof(TG), kAhead = 8;
   uint4 raw;
   __device__ __forceinline__ void load(const TG* src, int64_t col, int, int64_t) {
     raw = __ldcs(reinterpret_cast<const uint4*>(src + col));
@@ -253,7 +254,7 @@ struct Columns<TG, true> {
 
 template <typename TG>
 struct Columns<TG, false> {
-  static constexpr int kCols = 8;
+  static constexpr int kCols = 8, kAhead = 4;
   TG raw[kCols];
   __device__ __forceinline__ void load(const TG* src, int64_t col, int tpr, int64_t dim) {
 #pragma unroll
@@ -289,12 +290,13 @@ __device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COL
   }
 }
 
-constexpr int kAhead = 4;  // rows in flight per thread, while as many are added
+// Rows of this many chunks' heads or more are listed, to be joined by more threads.
+constexpr int kLongSpan = 32;
 
 template <typename TG, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const EmbeddingGradLaunch p) {
   using Cols = Columns<TG, VEC>;
-  constexpr int COLS = Cols::kCols;
+  constexpr int COLS = Cols::kCols, kAhead = Cols::kAhead;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tpr = p.tpr, groups = kThreads / tpr;
@@ -308,25 +310,18 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
   const int64_t begin = chunk * p.chunk_len, end = min(begin + p.chunk_len, p.n);
   const uint32_t none = static_cast<uint32_t>(p.rows);
   const TG* src = static_cast<const TG*>(p.grad_out);
-  // Two batches of rows: one is on its way while the other is added. Tokens that add nothing sort behind
-  // every row; their rows are not read.
-  uint2 tok[2][kAhead];
-  Cols val[2][kAhead];
+  // Tokens that add nothing sort behind every row; their rows are not read.
+  uint2 tok[kAhead];
   auto fetch_tokens = [&](uint2 (&to)[kAhead], int64_t i) {
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) to[a] = i + a < end ? __ldcg(tokens + i + a) : make_uint2(none, 0);
   };
-  auto fetch_rows = [&](Cols (&v)[kAhead], const uint2 (&of)[kAhead]) {
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a)
-      if (active && of[a].x != none) v[a].load(src + of[a].y * p.ld_grad_out, col, tpr, p.dim);
-  };
-  fetch_tokens(tok[0], begin);
-  fetch_tokens(tok[1], begin + kAhead);
+  fetch_tokens(tok, begin);
   const uint32_t key_before = begin > 0 ? __ldcg(&tokens[begin - 1].x) : none;
   const uint32_t key_after = end < p.n ? __ldcg(&tokens[end].x) : none;
-  fetch_rows(val[0], tok[0]);
-  uint32_t key = tok[0][0].x;
+  const int64_t far = (chunk + kLongSpan) * p.chunk_len;
+  const uint32_t key_far = far < p.n ? __ldcg(&tokens[far].x) : none;
+  uint32_t key = tok[0].x;
   bool from_before = key == key_before && key != none;
   // Bit 0: the chunk begins inside a row; bit 1: that row also fills the chunk and goes on.
   if (first_slice) p.chunk_state[chunk] = (from_before ? 1 : 0) | (from_before && key == key_after ? 2 : 0);
@@ -338,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
       // Head sums lie in the even rows of the workspace, tail sums in the odd ones.
       float* part = p.partials + (chunk * 2 + (from_before ? 0 : 1)) * p.ld_partials;
       if (active) store_columns<VEC>(part, acc, 1.f, false, col, tpr, p.dim);
-      if (!from_before && first_slice) {
+      if (!from_before && key == key_far && first_slice) {
         const unsigned at = atomicAdd(p.crossing_count, 1u);
         if (dev_check(at < p.chunks, p.status)) p.crossing[at] = make_uint2(static_cast<uint32_t>(chunk), key);
       }
@@ -346,32 +341,27 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
       store_columns<VEC>(p.grad + static_cast<int64_t>(key) * p.ld_grad, acc, p.scale, p.accumulate != 0, col, tpr, p.dim);
     }
   };
-  auto add = [&](const Cols (&v)[kAhead], const uint2 (&of)[kAhead]) {
+  // A chunk's length is a multiple of kAhead: only the list's last chunk has places without tokens.
+  for (int64_t i = begin; i < end && key != none; i += kAhead) {
+    Cols val[kAhead];
+    uint2 next[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+      if (active && tok[a].x != none) val[a].load(src + tok[a].y * p.ld_grad_out, col, tpr, p.dim);
+    fetch_tokens(next, i + kAhead);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      if (of[a].x != key) {
+      if (tok[a].x != key) {
         if (key != none) flush(false);
-        key = of[a].x;
+        key = tok[a].x;
         from_before = false;
 #pragma unroll
         for (int k = 0; k < COLS; ++k) acc[k] = 0.f;
       }
-      if (key != none) v[a].add_to(acc);
+      if (key != none) val[a].add_to(acc);
     }
-  };
-  // A chunk's length is a multiple of two batches: only the list's last chunk has places without tokens.
-  for (int64_t i = begin; i < end && key != none; i += 2 * kAhead) {
-    fetch_rows(val[1], tok[1]);
-    uint2 next[kAhead];
-    fetch_tokens(next, i + 2 * kAhead);
-    add(val[0], tok[0]);
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) tok[0][a] = next[a];
-    fetch_rows(val[0], tok[0]);
-    fetch_tokens(next, i + 3 * kAhead);
-    add(val[1], tok[1]);
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) tok[1][a] = next[a];
+    for (int a = 0; a < kAhead; ++a) tok[a] = next[a];
   }
   if (key != none) flush(key == key_after);
 }
@@ -380,79 +370,88 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
 
 constexpr int kJoinWarps = kThreads / 32;
 constexpr int kJoinCols = 128;  // columns of a warp, four per lane
-constexpr int64_t kJoinBlock = kJoinWarps * kJoinCols;
-// A row of this many chunks' sums or more is split over the CTA's warps; below, each warp adds all of them for
-// columns of its own.
-constexpr int kJoinSplit = 16;
+constexpr int kLongCtas = 304;  // that join listed rows, beside those that look at the chunks
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) { a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w; }
 
+// Adds the heads of chunks [lo, hi) at a column.
+__device__ __forceinline__ void add_heads(float4& acc, const EmbeddingGradLaunch& p, int64_t lo, int64_t hi, int64_t col) {
+  const float* part = p.partials + col;
+  int64_t c = lo;
+  for (; c + 8 <= hi; c += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part + (c + k) * 2 * p.ld_partials));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add4(acc, v[k]);
+  }
+  for (; c < hi; ++c) add4(acc, __ldcg(reinterpret_cast<const float4*>(part + c * 2 * p.ld_partials)));
+}
+
+__device__ __forceinline__ void store_joined(const EmbeddingGradLaunch& p, uint32_t key, int64_t col, const float4& acc) {
+  float* dst = p.grad + static_cast<int64_t>(key) * p.ld_grad + col;
+  const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (col + k < p.dim) dst[k] = fmaf(p.scale, v[k], p.accumulate ? dst[k] : 0.f);
+}
+
+// The last chunk that the row which `first` leaves open reaches into: the first one behind it that the row does
+// not fill. Called by whole warps.
+__device__ __forceinline__ int64_t last_chunk(const EmbeddingGradLaunch& p, int64_t first) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t last = first;; last += 32) {
+    const int64_t c = last + 1 + lane;
+    const unsigned ends = __ballot_sync(0xffffffffu, c >= p.chunks || __ldcg(p.chunk_state + c) != 3);
+    if (ends) {
+      const int64_t stop = last + __ffs(ends);
+      return stop < p.chunks && (__ldcg(p.chunk_state + stop) & 1) ? stop : stop - 1;
+    }
+  }
+}
+
+// The first CTAs take the chunks, p.join_warps warps for each: where a chunk leaves a row open that it does not
+// begin inside of, they add the row's heads to its tail, a warp for 128 columns at a time. The last kLongCtas
+// take the listed rows, 128 columns of one at a time, the heads split over the CTA's warps.
 __global__ void __launch_bounds__(kThreads) embedding_join_kernel(const EmbeddingGradLaunch p) {
   __shared__ float4 sums[kJoinWarps][32];
+  ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t blocks = (p.dim + kJoinBlock - 1) / kJoinBlock;
-  const int64_t items = static_cast<int64_t>(*p.crossing_count) * blocks;
-  auto add_heads = [&](float4& acc, int64_t lo, int64_t hi, int64_t col) {
-    const float* part = p.partials + col;
-    int64_t c = lo;
-    for (; c + 8 <= hi; c += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(part + (c + k) * 2 * p.ld_partials));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) add4(acc, v[k]);
+  const int64_t per_cta = kJoinWarps / p.join_warps, short_ctas = (p.chunks + per_cta - 1) / per_cta;
+  if (blockIdx.x < short_ctas) {
+    const int64_t c = blockIdx.x * per_cta + warp / p.join_warps;
+    if (c + 1 >= p.chunks) return;
+    const int here = __ldcg(p.chunk_state + c), next = __ldcg(p.chunk_state + c + 1);
+    const uint32_t key = __ldcg(&p.sorted[0][(c + 1) * p.chunk_len].x);
+    if (!(next & 1) || here == 3) return;
+    const int64_t last = last_chunk(p, c);
+    if (last - c >= kLongSpan) return;
+    const float* tail = p.partials + (c * 2 + 1) * p.ld_partials;
+    for (int64_t col = (warp % p.join_warps) * kJoinCols + lane * 4; col < p.dim; col += p.join_warps * kJoinCols) {
+      float4 acc = __ldcg(reinterpret_cast<const float4*>(tail + col));
+      add_heads(acc, p, c + 1, last + 1, col);
+      store_joined(p, key, col, acc);
     }
-    for (; c < hi; ++c) add4(acc, __ldcg(reinterpret_cast<const float4*>(part + c * 2 * p.ld_partials)));
-  };
-  auto store = [&](uint32_t key, int64_t col, const float4& acc) {
-    float* dst = p.grad + static_cast<int64_t>(key) * p.ld_grad + col;
-    const float v[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (col + k < p.dim) dst[k] = fmaf(p.scale, v[k], p.accumulate ? dst[k] : 0.f);
-  };
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    return;
+  }
+  const int64_t blocks = (p.dim + kJoinCols - 1) / kJoinCols;
+  const int64_t items = static_cast<int64_t>(__ldcg(p.crossing_count)) * blocks;
+  for (int64_t item = blockIdx.x - short_ctas; item < items; item += kLongCtas) {
     const uint2 row = p.crossing[item / blocks];
-    const int64_t first = row.x, block = item % blocks * kJoinBlock;
-    // The last chunk that the row reaches into: the first one behind its own that it does not fill.
-    int64_t last = first;
-    for (;;) {
-      const int64_t c = last + 1 + lane;
-      const unsigned ends = __ballot_sync(0xffffffffu, c >= p.chunks || p.chunk_state[c] != 3);
-      if (ends) {
-        last += __ffs(ends);
-        break;
-      }
-      last += 32;
+    const int64_t first = row.x, col = item % blocks * kJoinCols + lane * 4, span = last_chunk(p, first) - first;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (col < p.dim) {
+      if (warp == 0) acc = __ldcg(reinterpret_cast<const float4*>(p.partials + (first * 2 + 1) * p.ld_partials + col));
+      add_heads(acc, p, first + 1 + span * warp / kJoinWarps, first + 1 + span * (warp + 1) / kJoinWarps, col);
     }
-    if (last >= p.chunks || !(p.chunk_state[last] & 1)) --last;
-    const int64_t span = last - first;
-    const float* tail = p.partials + (first * 2 + 1) * p.ld_partials;
-    if (span < kJoinSplit) {
-      const int64_t col = block + warp * kJoinCols + lane * 4;
-      if (col < p.dim) {
-        float4 acc = __ldcg(reinterpret_cast<const float4*>(tail + col));
-        add_heads(acc, first + 1, last + 1, col);
-        store(row.y, col, acc);
-      }
-      continue;
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && col < p.dim) {
+      for (int w = 1; w < kJoinWarps; ++w) add4(acc, sums[w][lane]);
+      store_joined(p, row.y, col, acc);
     }
-    for (int64_t c0 = block; c0 < min(block + kJoinBlock, p.dim); c0 += kJoinCols) {
-      const int64_t col = c0 + lane * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (col < p.dim) {
-        if (warp == 0) acc = __ldcg(reinterpret_cast<const float4*>(tail + col));
-        add_heads(acc, first + 1 + span * warp / kJoinWarps, first + 1 + span * (warp + 1) / kJoinWarps, col);
-      }
-      sums[warp][lane] = acc;
-      __syncthreads();
-      if (warp == 0 && col < p.dim) {
-        for (int w = 1; w < kJoinWarps; ++w) add4(acc, sums[w][lane]);
-        store(row.y, col, acc);
-      }
-      __syncthreads();
-    }
+    __syncthreads();
   }
 }
 
@@ -489,8 +488,9 @@ int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream) {
   const size_t ti = p.table_dtype == 0 ? 4 : 2, to = p.out_dtype == 0 ? 4 : 2;
   const bool vec = p.dim % kLookup == 0 && aligned16(p.table, p.ld_table, ti) && aligned16(p.out, p.ld_out, to);
+  // Eight columns of a row per thread, or a little more: fewer threads per row are more rows on their way.
   p.tpr = 1;
-  while (p.tpr < kThreads && p.tpr * kLookup < p.dim) p.tpr *= 2;
+  while (p.tpr < kThreads && 2 * p.tpr * kLookup <= p.dim + 7) p.tpr *= 2;
   const int64_t groups = kThreads / p.tpr;
   const dim3 grid(static_cast<unsigned>((p.n + groups - 1) / groups));
   auto run = [&](auto kernel) { return row::launch(kernel, grid, kThreads, 0, stream, const_cast<const EmbeddingLaunch&>(p)); };
@@ -545,9 +545,11 @@ cudaError_t launch_embedding_grad(EmbeddingGradLaunch& p, int sms, cudaStream_t 
   else
     e = p.vec ? launch_chunks<__nv_bfloat16, true>(p, stream) : launch_chunks<__nv_bfloat16, false>(p, stream);
   if (e != cudaSuccess) return e;
-  const int64_t items = p.chunks * ((p.dim + kJoinBlock - 1) / kJoinBlock);
-  return row::launch(embedding_join_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(items, 4 * sms))), kThreads, 0,
-                     stream, p);
+  p.join_warps = 1;
+  while (p.join_warps < kJoinWarps && p.join_warps * kJoinCols < p.dim) p.join_warps *= 2;
+  const int64_t per_cta = kJoinWarps / p.join_warps;
+  const int64_t ctas = (p.chunks + per_cta - 1) / per_cta + (p.chunks > kLongSpan ? kLongCtas : 0);
+  return row::launch(embedding_join_kernel, dim3(static_cast<unsigned>(ctas)), kThreads, 0, stream, p);
 }
 
 }  // namespace dmuon

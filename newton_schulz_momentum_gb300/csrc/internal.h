@@ -339,12 +339,12 @@ struct EmbeddingGradLaunch {
   int* chunk_state;
   float* partials;            // two rows of ld_partials per chunk
   int64_t ld_partials;
-  uint2* crossing;            // (first chunk, id) of the rows that cross chunks
+  uint2* crossing;            // (first chunk, id) of the rows that cross many chunks
   unsigned* crossing_count;
   int tpr;                    // threads per row of grad_out
   int vec_grad, vec;          // 16-byte access to grad; to grad and grad_out
-  // Set by launch_embedding_grad.
-  int passes, digit_bits;
+  // Set by launch_embedding_grad; join_warps: warps that join a chunk's open row.
+  int passes, digit_bits, join_warps;
 };
 // Workspace bytes; with `ws` it also places the buffers there.
 int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws);

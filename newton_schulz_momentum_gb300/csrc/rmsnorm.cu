@@ -263,7 +263,16 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREA
         most[k] = 0.f;
 #pragma unroll
         for (int j = 0; j < E; ++j) most[k] = max_nan(most[k], fabsf(v[k][j]));
-        const int lanes = p.lanes ? p.lanes : 32;  // a group's, or a part of it
+      }
+      if (p.group == 0) {
+#pragma unroll
+        for (int k = 1; k < K; ++k) most[0] = max_nan(most[0], most[k]);
+#pragma unroll
+        for (int k = 1; k < K; ++k) most[k] = most[0];
+      }
+      const int lanes = p.lanes ? p.lanes : 32;  // a group's, or a part of it
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
         for (int o = lanes / 2; o > 0; o >>= 1) most[k] = max_nan(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
         if (p.lanes == 0 && i < p.n && first_out(k) < dim && (threadIdx.x & 31) == 0)
           atomicMax(top + first_out(k) / group, __float_as_uint(most[k]));
@@ -317,8 +326,8 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREA
 
 // ---------------------------------------------------------------------------- backward
 
-// The sums for dgain of a thread's columns, and its gains, stay in registers (REGS) or, for long rows, the sums in
-// shared memory. AHEAD: the next row is loaded early. PER_SM: CTAs that registers are to leave room for.
+// The sums for dgain of a thread's columns, and its gains, stay in registers (REGS) or, for long rows, in shared
+// memory. AHEAD: the next row is loaded early. PER_SM: CTAs that registers are to leave room for.
 template <typename T, int K, int THREADS, int PER_SM, bool REGS, bool AHEAD, bool EDGES>
 __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(const RmsNormGradLaunch p) {
   constexpr int E = kPer<T>;
@@ -339,20 +348,39 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   auto holds = [&](int k) { return t + k * tpr < full; };
   float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E], acc_edge = 0.f;
   const float gain_edge = edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
-  // Without REGS a thread's sums: four columns at [quarter][granule], so that a warp's accesses do not conflict.
-  float4* sums = reinterpret_cast<float4*>(dyn);
+  // Without REGS a thread's sums, then its gains: four columns at [quarter][granule], so that a warp's accesses do
+  // not conflict. Aligned gains of a small CTA are LOADED from memory at each use, which leaves L1 its space.
+  constexpr bool LOADED = !EDGES && THREADS <= 256;
   const int granules = K * tpr;
+  float4* sums = reinterpret_cast<float4*>(dyn);
+  float4* gains = sums + E / 4 * granules;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    if (REGS) {
-      load_gain(gain[k], p.gain, start(k), dim);
+    float g[E];
+    load_gain(g, p.gain, start(k), dim);
 #pragma unroll
-      for (int j = 0; j < E; ++j) acc[k][j] = 0.f;
-    } else {
-#pragma unroll
-      for (int j = 0; j < E / 4; ++j) sums[j * granules + t + k * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < E; ++j) {
+      if (REGS) {
+        gain[k][j] = g[j];
+        acc[k][j] = 0.f;
+      } else if (j % 4 == 0) {
+        sums[j / 4 * granules + t + k * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!LOADED) gains[j / 4 * granules + t + k * tpr] = make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
+      }
     }
   }
+  // Into gain[0], without REGS.
+  auto gains_of = [&](int k) {
+    if (LOADED) {
+      load_gain(gain[0], p.gain, start(k), dim);
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < E; j += 4) {
+      const float4 u = gains[j / 4 * granules + t + k * tpr];
+      gain[0][j] = u.x, gain[0][j + 1] = u.y, gain[0][j + 2] = u.z, gain[0][j + 3] = u.w;
+    }
+  };
   struct Row {
     uint4 y[K], h[K], t[K];
     T ye, he, te;
@@ -394,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
       float a[E], b[E];
       row::unpack16<T>(a, now.y[k]);
       row::unpack16<T>(b, now.h[k]);
-      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+      if (!REGS) gains_of(k);
 #pragma unroll
       for (int j = 0; j < E; ++j) {
         s[0] = fmaf(b[j], b[j], s[0]);
@@ -415,7 +443,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
       row::unpack16<T>(a, now.y[k]);
       row::unpack16<T>(b, now.h[k]);
       row::unpack16<T>(c, now.t[k]);
-      if (!REGS) load_gain(gain[0], p.gain, start(k), dim);
+      if (!REGS) gains_of(k);
       float4 sum;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -696,31 +724,35 @@ cudaError_t launch_rows(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
+// Granules per thread: up to 64 granules a row is one warp's, so that it needs no barrier of the CTA; then CTAs of
+// 256 threads as long as that is 16 elements per thread, and 32 elements from there on.
+template <typename T>
+int granules_each(int granules) {
+  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
+  return granules <= 32 ? 1 : granules <= 64 ? 2 : granules <= 256 ? 1 : granules <= 512 ? 2
+       : granules <= 256 * kHeld ? kHeld : kLong;
+}
+
 template <typename T, bool FP8, bool EDGES>
-cudaError_t launch_held_norm(RmsNormLaunch& p, int granules, int sms, cudaStream_t stream) {
-  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;  // 16 and 32 elements per thread
-  if (granules <= 256) return launch_rows<T, 1, FP8, 256, true, EDGES>(p, sms, stream);
-  if (granules <= 512) return launch_rows<T, 2, FP8, 256, true, EDGES>(p, sms, stream);
-  if (granules <= 256 * kHeld) return launch_rows<T, kHeld, FP8, 256, true, EDGES>(p, sms, stream);
+cudaError_t launch_held_norm(RmsNormLaunch& p, int each, int sms, cudaStream_t stream) {
+  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
+  if (each == 1) return launch_rows<T, 1, FP8, 256, true, EDGES>(p, sms, stream);
+  if (each == 2) return launch_rows<T, 2, FP8, 256, true, EDGES>(p, sms, stream);
+  if (each == kHeld) return launch_rows<T, kHeld, FP8, 256, true, EDGES>(p, sms, stream);
   if (p.sum_threads <= 320) return launch_rows<T, kLong, FP8, 320, false, EDGES>(p, sms, stream);
   return launch_rows<T, kLong, FP8, 512, false, EDGES>(p, sms, stream);
 }
 
 template <typename T, bool FP8>
 cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
-  constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
-  const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>);
-  p.sum_threads = std::min(row_threads(granules, granules <= 256           ? 1
-                                                 : granules <= 512         ? 2
-                                                 : granules <= 256 * kHeld ? kHeld
-                                                                           : kLong),
-                           kMaxThreads);
+  const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T>(granules);
+  p.sum_threads = std::min(row_threads(granules, each), kMaxThreads);
   const Array x{p.x, p.ldx};
   if (p.dim > kMaxHeld ||
       !same_offsets({x, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n, sizeof(T)))
     return row::launch(add_rmsnorm_kernel<T>, dim3(static_cast<unsigned>(p.n)), std::max(32, p.sum_threads), 0, stream, p);
-  return has_edges(x, p.n, p.dim, sizeof(T)) ? launch_held_norm<T, FP8, true>(p, granules, sms, stream)
-                                             : launch_held_norm<T, FP8, false>(p, granules, sms, stream);
+  return has_edges(x, p.n, p.dim, sizeof(T)) ? launch_held_norm<T, FP8, true>(p, each, sms, stream)
+                                             : launch_held_norm<T, FP8, false>(p, each, sms, stream);
 }
 
 template <typename T, int K, int THREADS, int PER_SM, bool REGS, bool AHEAD, bool EDGES>
@@ -728,7 +760,7 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, PER_SM, REGS, AHEAD, EDGES>;
   // Sums of long rows, or the line in which a CTA's short rows join.
   const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
-  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * kPer<T> * 4;
+  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2);
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -743,9 +775,11 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 
 template <typename T, bool EDGES>
 cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
-  if (granules <= 256) return launch_grad_rows<T, 1, 256, 3, true, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, true, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 1024) return launch_grad_rows<T, 4, 256, 3, false, false, EDGES>(p, granules, sms, stream);
+  if (granules <= 32) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 256) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 1024) return launch_grad_rows<T, 4, 256, 2, false, false, EDGES>(p, granules, sms, stream);
   if (granules <= 2048) return launch_grad_rows<T, 4, 512, 1, false, false, EDGES>(p, granules, sms, stream);
   if constexpr (sizeof(T) == 4)
     return launch_grad_rows<T, 4, 1024, 1, false, false, EDGES>(p, granules, sms, stream);
