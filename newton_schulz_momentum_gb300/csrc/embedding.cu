@@ -42,37 +42,53 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) 
   __stcs(reinterpret_cast<uint4*>(dst), row::pack16(v));
 }
 
-// `tpr` threads per token. Bound by memory: each row is read once (a row that several tokens name comes from
-// L2 again) and the output is written once.
+// `tpr` threads take two tokens, so that twice as much is on its way. Bound by memory: each row is read once (a
+// row that several tokens name comes from L2 again) and the output is written once.
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaunch p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int tpr = p.tpr, t = threadIdx.x % tpr;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr;
-  if (i >= p.n) return;
-  const int64_t id = row::load_id(p.ids, p.id_bytes, i);
-  const bool ok = id >= 0 && id < p.rows;
-  if (!ok && t == 0) atomicOr(p.status, kDevIndex);
-  const TI* src = static_cast<const TI*>(p.table) + (ok ? id : 0) * p.ld_table;
-  TO* dst = static_cast<TO*>(p.out) + i * p.ld_out;
-  const float scale = p.scale;
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr) * 2;
+  const TI* src[2];
+  TO* dst[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int64_t i = i0 + r;
+    const int64_t id = i < p.n ? row::load_id(p.ids, p.id_bytes, i) : 0;
+    const bool ok = id >= 0 && id < p.rows;
+    if (!ok && t == 0) atomicOr(p.status, kDevIndex);
+    src[r] = ok && i < p.n ? static_cast<const TI*>(p.table) + id * p.ld_table : nullptr;
+    dst[r] = i < p.n ? static_cast<TO*>(p.out) + i * p.ld_out : nullptr;
+  }
   for (int64_t c0 = 0; c0 < p.dim; c0 += tpr * kLookup) {
-    float v[kLookup];
+    float v[2][kLookup];
     const int64_t c = c0 + (VEC ? t * kLookup : t);
-    if constexpr (VEC) {
-      if (c < p.dim) {
-        load8(v, src + c);
 #pragma unroll
-        for (int k = 0; k < kLookup; ++k) v[k] = ok ? scale * v[k] : 0.f;
-        store8(dst + c, v);
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int k = 0; k < kLookup; ++k) v[r][k] = 0.f;
+      if constexpr (VEC) {
+        if (src[r] && c < p.dim) load8(v[r], src[r] + c);
+      } else {
+        if (src[r])
+#pragma unroll
+          for (int k = 0; k < kLookup; ++k)
+            if (c + k * tpr < p.dim) v[r][k] = row::to_f(__ldg(src[r] + c + k * tpr));
       }
-    } else {
+    }
 #pragma unroll
-      for (int k = 0; k < kLookup; ++k) v[k] = c + k * tpr < p.dim ? row::to_f(__ldg(src + c + k * tpr)) : 0.f;
+    for (int r = 0; r < 2; ++r) {
+      if (!dst[r]) continue;
 #pragma unroll
-      for (int k = 0; k < kLookup; ++k)
-        if (c + k * tpr < p.dim) dst[c + k * tpr] = row::from_f<TO>(ok ? scale * v[k] : 0.f);
+      for (int k = 0; k < kLookup; ++k) v[r][k] = src[r] ? p.scale * v[r][k] : 0.f;
+      if constexpr (VEC) {
+        if (c < p.dim) store8(dst[r] + c, v[r]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kLookup; ++k)
+          if (c + k * tpr < p.dim) dst[r][c + k * tpr] = row::from_f<TO>(v[r][k]);
+      }
     }
   }
 }
@@ -83,12 +99,14 @@ constexpr int kSortCtas = 8;  // one portable cluster
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxDigitBits = 9;
+constexpr int kHeldTokens = 4;  // per lane: all of them up to 32768
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
 constexpr size_t kSortSmem = sizeof(uint32_t) * (kSortWarps + 2) * kMaxDigits;
 
 // Token i's sort key: its id, or `rows` (behind every row) for padding and ids outside the table.
 __device__ __forceinline__ uint32_t sort_key(const EmbeddingGradLaunch& p, int64_t i) {
   const int64_t id = row::load_id(p.ids, p.id_bytes, i);
+  if (id < 0 || id >= p.rows) atomicOr(p.status, kDevIndex);
   return id >= 0 && id < p.rows && id != p.padding_idx ? static_cast<uint32_t>(id) : static_cast<uint32_t>(p.rows);
 }
 
@@ -121,13 +139,20 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
       if (i >= p.n) return make_uint2(0xffffffffu, 0);
       return pass == 0 ? make_uint2(sort_key(p, i), static_cast<uint32_t>(i)) : __ldcg(in + i);
     };
-    for (int64_t s = 0; s < steps; ++s) {
-      const int64_t i = first + s * 32 + lane;
-      const uint32_t d = i < p.n ? (token(i).x >> shift) & (digits - 1) : 0xffffffffu;
+    // The first tokens stay in registers for the second look at them.
+    uint2 held[kHeldTokens];
+#pragma unroll
+    for (int s = 0; s < kHeldTokens; ++s) held[s] = s < steps ? token(first + s * 32 + lane) : make_uint2(0, 0);
+    auto count_one = [&](int64_t i, const uint2& t) {
+      const uint32_t d = i < p.n ? (t.x >> shift) & (digits - 1) : 0xffffffffu;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (d != 0xffffffffu && lane == __ffs(same) - 1) mine[d] += __popc(same);
       __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int s = 0; s < kHeldTokens; ++s)
+      if (s < steps) count_one(first + s * 32 + lane, held[s]);
+    for (int64_t s = kHeldTokens; s < steps; ++s) count_one(first + s * 32 + lane, token(first + s * 32 + lane));
     __syncthreads();
     if (threadIdx.x < digits) {
       uint32_t sum = 0;
@@ -164,9 +189,7 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
       base[threadIdx.x] = start + upto - all + before;
     }
     __syncthreads();
-    for (int64_t s = 0; s < steps; ++s) {
-      const int64_t i = first + s * 32 + lane;
-      const uint2 t = token(i);
+    auto place_one = [&](int64_t i, const uint2& t) {
       const uint32_t d = i < p.n ? (t.x >> shift) & (digits - 1) : 0xffffffffu;
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (d != 0xffffffffu) {
@@ -176,7 +199,11 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
       __syncwarp();
       if (d != 0xffffffffu && lane == __ffs(same) - 1) mine[d] += __popc(same);
       __syncwarp();
-    }
+    };
+#pragma unroll
+    for (int s = 0; s < kHeldTokens; ++s)
+      if (s < steps) place_one(first + s * 32 + lane, held[s]);
+    for (int64_t s = kHeldTokens; s < steps; ++s) place_one(first + s * 32 + lane, token(first + s * 32 + lane));
     // The next pass reads what the whole cluster wrote, and reuses the counts others have read.
     ptx::cluster_sync_all();
   }
@@ -190,10 +217,6 @@ __global__ void __cluster_dims__(kSortCtas) __launch_bounds__(kSortThreads, 1)
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.crossing_count = 0;
-  for (int64_t i = blockIdx.x * kSortThreads + threadIdx.x; i < p.n; i += kSortCtas * kSortThreads) {
-    const int64_t id = row::load_id(p.ids, p.id_bytes, i);
-    if (id < 0 || id >= p.rows) atomicOr(p.status, kDevIndex);
-  }
   sort_tokens(p, smem);
 }
 
@@ -254,7 +277,7 @@ struct Columns<TG, true> {
 
 template <typename TG>
 struct Columns<TG, false> {
-  static constexpr int kCols = 8, kAhead = 4;
+  static constexpr int kCols = 4, kAhead = 4;
   TG raw[kCols];
   __device__ __forceinline__ void load(const TG* src, int64_t col, int tpr, int64_t dim) {
 #pragma unroll
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
   constexpr int COLS = Cols::kCols, kAhead = Cols::kAhead;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int tpr = p.tpr, groups = kThreads / tpr;
+  const int tpr = p.tpr, groups = blockDim.x / tpr;
   const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
   if (chunk >= p.chunks) return;
   const int t = threadIdx.x % tpr;
@@ -460,7 +483,7 @@ cudaError_t launch_chunks(const EmbeddingGradLaunch& p, cudaStream_t stream) {
   const int64_t slice = int64_t(p.tpr) * Columns<TG, VEC>::kCols, groups = kThreads / p.tpr;
   const dim3 grid(static_cast<unsigned>((p.chunks + groups - 1) / groups),
                   static_cast<unsigned>((p.dim + slice - 1) / slice));
-  return row::launch(embedding_chunk_kernel<TG, VEC>, grid, kThreads, 0, stream, p);
+  return row::launch(embedding_chunk_kernel<TG, VEC>, grid, static_cast<int>(groups * p.tpr), 0, stream, p);
 }
 
 bool aligned16(const void* p, int64_t ld, size_t elem) {
@@ -473,9 +496,13 @@ bool aligned16(const void* p, int64_t ld, size_t elem) {
 void split_tokens(EmbeddingGradLaunch& p) {
   const int cols = p.vec ? (p.grad_dtype == 1 ? Columns<__nv_bfloat16, true>::kCols : Columns<float, true>::kCols)
                          : Columns<float, false>::kCols;
-  p.tpr = 1;
-  while (p.tpr < kThreads && p.tpr * cols < p.dim) p.tpr *= 2;
-  const int64_t slices = (p.dim + p.tpr * cols - 1) / (p.tpr * cols), groups = kThreads / p.tpr;
+  // Slices of equal length: whole warps, or a power of two below one.
+  const int64_t slices = (p.dim + kThreads * cols - 1) / (kThreads * cols);
+  const int need = static_cast<int>(((p.dim + slices - 1) / slices + cols - 1) / cols);
+  p.tpr = (need + 31) / 32 * 32;
+  if (need <= 16)
+    for (p.tpr = 1; p.tpr < need;) p.tpr *= 2;
+  const int64_t groups = kThreads / p.tpr;
   p.chunk_len = 16;
   while (p.n / (2 * p.chunk_len) * slices >= 1024 * groups) p.chunk_len *= 2;
   p.chunks = (p.n + p.chunk_len - 1) / p.chunk_len;
@@ -488,11 +515,10 @@ int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream) {
   const size_t ti = p.table_dtype == 0 ? 4 : 2, to = p.out_dtype == 0 ? 4 : 2;
   const bool vec = p.dim % kLookup == 0 && aligned16(p.table, p.ld_table, ti) && aligned16(p.out, p.ld_out, to);
-  // Eight columns of a row per thread, or a little more: fewer threads per row are more rows on their way.
   p.tpr = 1;
-  while (p.tpr < kThreads && 2 * p.tpr * kLookup <= p.dim + 7) p.tpr *= 2;
-  const int64_t groups = kThreads / p.tpr;
-  const dim3 grid(static_cast<unsigned>((p.n + groups - 1) / groups));
+  while (p.tpr < kThreads && p.tpr * kLookup < p.dim) p.tpr *= 2;
+  const int64_t tokens = kThreads / p.tpr * 2;  // of a CTA
+  const dim3 grid(static_cast<unsigned>((p.n + tokens - 1) / tokens));
   auto run = [&](auto kernel) { return row::launch(kernel, grid, kThreads, 0, stream, const_cast<const EmbeddingLaunch&>(p)); };
   using B = __nv_bfloat16;
   if (p.table_dtype == 0 && p.out_dtype == 0)
