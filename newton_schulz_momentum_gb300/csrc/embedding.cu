@@ -21,7 +21,7 @@ constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------------------- lookup
 
-constexpr int kLookup = 8;  // columns of a thread at a time: consecutive (VEC), or tpr apart
+constexpr int kLookup = 8;  // consecutive columns of a thread at a time
 
 // Eight consecutive elements by 16-byte loads and stores.
 __device__ __forceinline__ void load8(float (&v)[8], const float* src) {
@@ -42,9 +42,23 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&v)[8]) 
   __stcs(reinterpret_cast<uint4*>(dst), row::pack16(v));
 }
 
+// Token i's row of the table (null for an id outside it, which is recorded) and of the output (null beyond the
+// last token).
+template <typename TI, typename TO>
+__device__ __forceinline__ void source_row(const EmbeddingLaunch& p, int64_t i, int t, const TI*& src, TO*& dst) {
+  src = nullptr, dst = nullptr;
+  if (i >= p.n) return;
+  const int64_t id = row::load_id(p.ids, p.id_bytes, i);
+  if (id >= 0 && id < p.rows)
+    src = static_cast<const TI*>(p.table) + id * p.ld_table;
+  else if (t == 0)
+    atomicOr(p.status, kDevIndex);
+  dst = static_cast<TO*>(p.out) + i * p.ld_out;
+}
+
 // `tpr` threads take two tokens, so that twice as much is on its way. Bound by memory: each row is read once (a
 // row that several tokens name comes from L2 again) and the output is written once.
-template <typename TI, typename TO, bool VEC>
+template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaunch p) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -53,42 +67,82 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaun
   const TI* src[2];
   TO* dst[2];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int64_t i = i0 + r;
-    const int64_t id = i < p.n ? row::load_id(p.ids, p.id_bytes, i) : 0;
-    const bool ok = id >= 0 && id < p.rows;
-    if (!ok && t == 0) atomicOr(p.status, kDevIndex);
-    src[r] = ok && i < p.n ? static_cast<const TI*>(p.table) + id * p.ld_table : nullptr;
-    dst[r] = i < p.n ? static_cast<TO*>(p.out) + i * p.ld_out : nullptr;
-  }
-  for (int64_t c0 = 0; c0 < p.dim; c0 += tpr * kLookup) {
+  for (int r = 0; r < 2; ++r) source_row(p, i0 + r, t, src[r], dst[r]);
+  for (int64_t c = t * kLookup; c < p.dim; c += tpr * kLookup) {
     float v[2][kLookup];
-    const int64_t c = c0 + (VEC ? t * kLookup : t);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
 #pragma unroll
       for (int k = 0; k < kLookup; ++k) v[r][k] = 0.f;
-      if constexpr (VEC) {
-        if (src[r] && c < p.dim) load8(v[r], src[r] + c);
-      } else {
-        if (src[r])
-#pragma unroll
-          for (int k = 0; k < kLookup; ++k)
-            if (c + k * tpr < p.dim) v[r][k] = row::to_f(__ldg(src[r] + c + k * tpr));
-      }
+      if (src[r]) load8(v[r], src[r] + c);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (!dst[r]) continue;
 #pragma unroll
       for (int k = 0; k < kLookup; ++k) v[r][k] = src[r] ? p.scale * v[r][k] : 0.f;
-      if constexpr (VEC) {
-        if (c < p.dim) store8(dst[r] + c, v[r]);
-      } else {
+      store8(dst[r] + c, v[r]);
+    }
+  }
+}
+
+// Rows that do not start on 16 bytes, or are not whole granules. The output is written in 16-byte granules at
+// aligned addresses; a granule's elements begin anywhere in the table's row, so the aligned 16-byte words
+// around them are read and shifted. Where those would reach beyond the row, and in the up to 2 (E - 1) elements
+// beside the granules, single elements are read.
+template <typename TI, typename TO>
+__global__ void __launch_bounds__(kThreads) embedding_shift_kernel(const EmbeddingLaunch p) {
+  constexpr int E = 16 / sizeof(TO), BYTES = E * sizeof(TI), LOADS = (BYTES + 15) / 16 + 1, WORDS = LOADS * 4;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int tpr = p.tpr, t = threadIdx.x % tpr, dim = static_cast<int>(p.dim);
+  const int64_t i0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / tpr) + threadIdx.x / tpr) * 2;
 #pragma unroll
-        for (int k = 0; k < kLookup; ++k)
-          if (c + k * tpr < p.dim) dst[r][c + k * tpr] = row::from_f<TO>(v[r][k]);
+  for (int r = 0; r < 2; ++r) {
+    const TI* src;
+    TO* dst;
+    source_row(p, i0 + r, t, src, dst);
+    if (!dst) continue;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(dst) & 15) / sizeof(TO));
+    const int head = min((E - off) & (E - 1), dim), full = (dim - head) / E, tail = dim - head - full * E;
+    const int edge = t < head ? t : t >= 8 && t - 8 < tail ? head + full * E + t - 8 : -1;
+    if (edge >= 0) dst[edge] = row::from_f<TO>(src ? p.scale * row::to_f(__ldg(src + edge)) : 0.f);
+    const char* begin = reinterpret_cast<const char*>(src);
+    const char* end = begin + static_cast<int64_t>(dim) * sizeof(TI);
+    for (int q = t; q < full; q += tpr) {
+      float v[E];
+#pragma unroll
+      for (int k = 0; k < E; ++k) v[k] = 0.f;
+      if (src) {
+        const TI* at = src + head + q * E;
+        const int a = static_cast<int>(reinterpret_cast<uintptr_t>(at) & 15);
+        const char* base = reinterpret_cast<const char*>(at) - a;
+        if (base >= begin && base + LOADS * 16 <= end) {
+          uint32_t w[WORDS];
+#pragma unroll
+          for (int l = 0; l < LOADS; ++l) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(base) + l);
+            w[4 * l] = u.x, w[4 * l + 1] = u.y, w[4 * l + 2] = u.z, w[4 * l + 3] = u.w;
+          }
+          if (a & 8)
+#pragma unroll
+            for (int k = 0; k + 2 < WORDS; ++k) w[k] = w[k + 2];
+          if (a & 4)
+#pragma unroll
+            for (int k = 0; k + 1 < WORDS; ++k) w[k] = w[k + 1];
+          if (sizeof(TI) == 2 && (a & 2))
+#pragma unroll
+            for (int k = 0; k + 1 < WORDS; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            v[k] = p.scale * (sizeof(TI) == 4 ? __uint_as_float(w[k])
+                                              : __uint_as_float(k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16));
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k) v[k] = p.scale * row::to_f(__ldg(at + k));
+        }
       }
+      __stcs(reinterpret_cast<uint4*>(dst + head + q * E), row::pack16(v));
     }
   }
 }
@@ -515,17 +569,17 @@ int64_t padded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream) {
   const size_t ti = p.table_dtype == 0 ? 4 : 2, to = p.out_dtype == 0 ? 4 : 2;
   const bool vec = p.dim % kLookup == 0 && aligned16(p.table, p.ld_table, ti) && aligned16(p.out, p.ld_out, to);
-  p.tpr = 1;
-  while (p.tpr < kThreads && p.tpr * kLookup < p.dim) p.tpr *= 2;
+  const int each = vec ? kLookup : static_cast<int>(16 / to);
+  p.tpr = vec ? 1 : 16;
+  while (p.tpr < kThreads && p.tpr * each < p.dim) p.tpr *= 2;
   const int64_t tokens = kThreads / p.tpr * 2;  // of a CTA
   const dim3 grid(static_cast<unsigned>((p.n + tokens - 1) / tokens));
   auto run = [&](auto kernel) { return row::launch(kernel, grid, kThreads, 0, stream, const_cast<const EmbeddingLaunch&>(p)); };
   using B = __nv_bfloat16;
-  if (p.table_dtype == 0 && p.out_dtype == 0)
-    return vec ? run(embedding_kernel<float, float, true>) : run(embedding_kernel<float, float, false>);
-  if (p.table_dtype == 0) return vec ? run(embedding_kernel<float, B, true>) : run(embedding_kernel<float, B, false>);
-  if (p.out_dtype == 0) return vec ? run(embedding_kernel<B, float, true>) : run(embedding_kernel<B, float, false>);
-  return vec ? run(embedding_kernel<B, B, true>) : run(embedding_kernel<B, B, false>);
+  if (p.table_dtype == 0 && p.out_dtype == 0) return run(vec ? embedding_kernel<float, float> : embedding_shift_kernel<float, float>);
+  if (p.table_dtype == 0) return run(vec ? embedding_kernel<float, B> : embedding_shift_kernel<float, B>);
+  if (p.out_dtype == 0) return run(vec ? embedding_kernel<B, float> : embedding_shift_kernel<B, float>);
+  return run(vec ? embedding_kernel<B, B> : embedding_shift_kernel<B, B>);
 }
 
 int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws) {
