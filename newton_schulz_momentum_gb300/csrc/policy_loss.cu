@@ -737,12 +737,16 @@ cudaError_t launch_solo(PolicyLaunch& p, int sms, cudaStream_t stream) {
   using R = Ring<kSolo>;
   auto* kernel = policy_ring_kernel<T, kSolo, EDGES>;
   const size_t smem = static_cast<size_t>(R::kWarps) * kRingSlots * p.slot_bytes + 128;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       R::kWarps * kRingSlots * kSoloSlotBytes + 128);
-  int per_sm = 0;
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, R::kThreads, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024)  // beside the static shared memory, what needs no opt-in
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  int64_t ctas = (p.n + R::kWarps - 1) / R::kWarps;
+  if (e == cudaSuccess && ctas > sms) {
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, R::kThreads, smem);
+    ctas = std::min<int64_t>(ctas, static_cast<int64_t>(sms) * std::max(per_sm, 1));
+  }
   if (e != cudaSuccess) return e;
-  const int64_t ctas = std::min<int64_t>(static_cast<int64_t>(sms) * std::max(per_sm, 1), (p.n + R::kWarps - 1) / R::kWarps);
   p.terms = ctas * R::kWarps;
   return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), R::kThreads, smem, stream, p);
 }

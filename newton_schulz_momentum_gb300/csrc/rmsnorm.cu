@@ -684,11 +684,16 @@ cudaError_t row_grid(RowGrid& g, void (*kernel)(P), int tpr, int64_t n, size_t s
   g.tpr = tpr;
   g.rows = g.tpr >= kThreads ? 1 : kThreads / g.tpr;
   g.threads = g.tpr * g.rows;
+  const int64_t turns = (n + g.rows - 1) / g.rows;
+  if (turns <= sms) {
+    g.ctas = static_cast<unsigned>(turns);
+    return cudaSuccess;
+  }
   int per_sm = 0;
   const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, g.threads, smem);
   if (e != cudaSuccess) return e;
   const int64_t most = std::max<int64_t>(8, static_cast<int64_t>(sms) * std::min(per_sm, kMaxPerSm) / 8 * 8);
-  g.ctas = static_cast<unsigned>(std::min<int64_t>(most, (n + g.rows - 1) / g.rows));
+  g.ctas = static_cast<unsigned>(std::min<int64_t>(most, turns));
   return cudaSuccess;
 }
 

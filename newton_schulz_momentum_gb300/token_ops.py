@@ -18,10 +18,19 @@ from __future__ import annotations
 
 import torch
 
-from . import BF16, E4M3, F32, _check, _stream, lib
+from . import BF16, E4M3, F32, _check, lib
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
+# The current stream's address without a Stream object around it (a third of a small call's time), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, t):
+    """Address of `stream`, by default the current one of t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _code(t, name):
@@ -35,18 +44,19 @@ def _rows(t, name, shape=None, dtype=None):
     """(rows, row length, row stride) of a CUDA tensor, given its expected shape and dtype."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() == 0:
+    if not size:
         raise ValueError(f"{name} must have at least one dimension")
-    dim = t.shape[-1]
+    dim = size[-1]
     if t.is_contiguous():
         return (t.numel() // dim if dim else 0), dim, dim
-    if t.dim() != 2 or t.stride(1) != 1 or t.stride(0) < dim:
+    if len(size) != 2 or t.stride(1) != 1 or t.stride(0) < dim:
         raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
-    return t.shape[0], dim, t.stride(0)
+    return size[0], dim, t.stride(0)
 
 
 def _vector(t, name, n, dtype=torch.float32):
@@ -74,12 +84,14 @@ def embedding(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     if table.dim() != 2:
         raise ValueError("table must be a 2-D tensor")
     rows, dim, ld = _rows(table, "table")
+    ptr, size = _ids(ids, "ids")
     if out is None:
         out = torch.empty(ids.shape + (dim,), dtype=dtype or table.dtype, device=table.device)
-    n, _, ldo = _rows(out, "out", ids.shape + (dim,), dtype)
-    ptr, size = _ids(ids, "ids")
+        n, ldo = ids.numel(), dim
+    else:
+        n, _, ldo = _rows(out, "out", ids.shape + (dim,), dtype)
     _check(lib().dmuon_embedding(table.data_ptr(), _code(table, "table"), rows, dim, ld, ptr, size, n, scale,
-                                 out.data_ptr(), _code(out, "out"), ldo, _stream(stream)))
+                                 out.data_ptr(), _code(out, "out"), ldo, _stream(stream, table)))
     return out
 
 
@@ -92,10 +104,12 @@ def embedding_grad(grad_out, ids, rows, scale=1.0, padding_idx=None, grad=None, 
         if accumulate:
             raise ValueError("accumulate needs a grad to add to")
         grad = torch.empty((rows, dim), dtype=torch.float32, device=grad_out.device)
-    _, _, ldg = _rows(grad, "grad", (rows, dim), torch.float32)
+        ldg = dim
+    else:
+        _, _, ldg = _rows(grad, "grad", (rows, dim), torch.float32)
     _check(lib().dmuon_embedding_grad(grad_out.data_ptr(), _code(grad_out, "grad_out"), ld, ptr, size, n, rows, dim,
                                       scale, -1 if padding_idx is None else padding_idx, grad.data_ptr(), ldg,
-                                      1 if accumulate else 0, _stream(stream)))
+                                      1 if accumulate else 0, _stream(stream, grad_out)))
     return grad
 
 
@@ -105,8 +119,9 @@ def _norm_args(x, residual, gain, h):
     if residual is not None:
         _, _, ldr = _rows(residual, "residual", x.shape, x.dtype)
         if h is None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if h is not None:
+            h, ldh = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
+            hp = h.data_ptr()
+    if hp is None and h is not None:
         _, _, ldh = _rows(h, "h", x.shape, x.dtype)
         hp = h.data_ptr()
     return (n, dim, h, (x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, _code(x, "x"),
@@ -118,9 +133,10 @@ def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, y=None, h=None, stream=No
     dtype. Without a residual h is x itself. `h` may be x or residual, to update the residual stream in place."""
     n, dim, h, head, tail = _norm_args(x, residual, gain, h)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _, _, ldy = _rows(y, "y", x.shape, x.dtype)
-    _check(lib().dmuon_add_rmsnorm(*head, eps, *tail, y.data_ptr(), head[4], ldy, None, 0, _stream(stream)))
+        y, ldy = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
+    else:
+        _, _, ldy = _rows(y, "y", x.shape, x.dtype)
+    _check(lib().dmuon_add_rmsnorm(*head, eps, *tail, y.data_ptr(), head[4], ldy, None, 0, _stream(stream, x)))
     return y, (x if h is None else h)
 
 
@@ -131,7 +147,7 @@ def add_rmsnorm_fp8(x, residual=None, gain=None, eps=1e-6, group=128, h=None, st
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(x.shape[:-1] + (-(-dim // group) if group else 1,), dtype=torch.float32, device=x.device)
     _check(lib().dmuon_add_rmsnorm(*head, eps, *tail, q.data_ptr(), E4M3, dim, scales.data_ptr(), group,
-                                   _stream(stream)))
+                                   _stream(stream, x)))
     return q, scales, (x if h is None else h)
 
 
@@ -143,15 +159,16 @@ def add_rmsnorm_grad(dy, h, gain=None, dh=None, eps=1e-6, dx=None, dgain=None, a
     _, _, ldh = _rows(h, "h", dy.shape, dy.dtype)
     lddh = 0 if dh is None else _rows(dh, "dh", dy.shape, dy.dtype)[2]
     if dx is None:
-        dx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-    _, _, lddx = _rows(dx, "dx", dy.shape, dy.dtype)
+        dx, lddx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device), dim
+    else:
+        _, _, lddx = _rows(dx, "dx", dy.shape, dy.dtype)
     if dgain is None and gain is not None:
         if accumulate:
             raise ValueError("accumulate needs a dgain to add to")
         dgain = torch.empty(dim, dtype=torch.float32, device=dy.device)
     _check(lib().dmuon_add_rmsnorm_grad(dy.data_ptr(), ldy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(),
                                         lddh, _code(dy, "dy"), _vector(gain, "gain", dim), n, dim, eps, dx.data_ptr(),
-                                        lddx, _vector(dgain, "dgain", dim), 1 if accumulate else 0, _stream(stream)))
+                                        lddx, _vector(dgain, "dgain", dim), 1 if accumulate else 0, _stream(stream, dy)))
     return dx, dgain
 
 
@@ -167,10 +184,11 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
     ptr, size = _ids(targets, "targets", n)
     ldd, dptr = 0, None
     if dlogits is None:
-        dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        dlogits, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), vocab
+        dptr = dlogits.data_ptr()
     elif dlogits is False:
         dlogits = None
-    if dlogits is not None:
+    else:
         _, _, ldd = _rows(dlogits, "dlogits", logits.shape, logits.dtype)
         dptr = dlogits.data_ptr()
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
@@ -179,7 +197,7 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
                                    _vector(old_logp, "old_logp", n), _vector(ref_logp, "ref_logp", n),
                                    _vector(advantages, "advantages", n), _vector(weights, "weights", n), clip_low,
                                    clip_high, kl_coef, temperature, loss.data_ptr(), logp.data_ptr(), dptr, ldd,
-                                   _stream(stream)))
+                                   _stream(stream, logits)))
     return loss, logp, dlogits
 
 
@@ -189,5 +207,5 @@ def token_logprobs(logits, targets, temperature=1.0, stream=None):
     ptr, size = _ids(targets, "targets", n)
     logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
     _check(lib().dmuon_token_logprobs(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size, temperature,
-                                      logp.data_ptr(), _stream(stream)))
+                                      logp.data_ptr(), _stream(stream, logits)))
     return logp
