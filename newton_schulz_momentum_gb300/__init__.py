@@ -10,7 +10,8 @@ call raises ``LibraryNotBuilt``.
 
 The pages' own names -- newton_schulz, NewtonSchulz and the Muon optimizer -- live in
 newton_schulz_momentum_gb300.optim, and the token operators (embedding, residual RMS norm, policy loss) in
-newton_schulz_momentum_gb300.token_ops; both import torch and are reachable here as attributes.
+newton_schulz_momentum_gb300.token_ops, with torch modules around them in .layers; these import torch and are
+reachable here as attributes.
 """
 
 from __future__ import annotations
@@ -489,11 +490,12 @@ def direct_flops(m, n, steps=5, dense=False):
 
 _TOKEN_OPS = ("embedding", "embedding_grad", "add_rmsnorm", "add_rmsnorm_fp8", "add_rmsnorm_grad", "policy_loss",
               "token_logprobs")
+_LAYERS = ("Embedding", "AddRMSNorm", "PolicyLoss")
 
 
 def __getattr__(name):
-    """newton_schulz, NewtonSchulz, Muon and default_muon_filter load from .optim, and the token operators from
-    .token_ops, on first use (they import torch; this module does not)."""
+    """newton_schulz, NewtonSchulz, Muon and default_muon_filter load from .optim, the token operators from .token_ops
+    and their modules from .layers, on first use (they import torch; this module does not)."""
     if name in ("newton_schulz", "NewtonSchulz", "Muon", "default_muon_filter"):
         from . import optim
         return getattr(optim, name)
@@ -501,4 +503,7 @@ def __getattr__(name):
         from . import token_ops
         globals().update((op, getattr(token_ops, op)) for op in _TOKEN_OPS)
         return globals()[name]
+    if name in _LAYERS:
+        from . import layers
+        return getattr(layers, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
