@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 256;  // of a CTA that holds short rows, and of the kernels for the longest ones
 constexpr int kMaxThreads = 1024;
+constexpr int kHugeThreads = 576;  // of two CTAs per SM that hold 16 elements of a long fp32 row in each thread
 constexpr float kFp8Max = 448.f;  // largest finite e4m3
 constexpr float kMinScale = 1.17549435e-38f;
 
@@ -122,6 +123,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return c;
 }
 
+// Within one unit of the last place, against e4m3's four significant bits.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // E elements as e4m3 bytes.
 template <int E>
 __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[E], float inv) {
@@ -136,7 +144,7 @@ __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[
 // THREADS: the most of a CTA. HELD: gains stay in registers and the next row is loaded early; without it, for
 // longer rows, a thread has fewer registers and more CTAs overlap. EDGES: rows that are not whole granules.
 template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
-__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREADS <= 320 ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
     add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   constexpr int E = kPer<T>;
   __shared__ float red[2][32][1];
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREA
         const float scale = scale_of(__float_as_uint(most[k]));
         if (p.lanes && t % p.lanes == 0) p.scales[i * parts + e0 / group] = scale;
         uint32_t w[E / 4];
-        pack_fp8(w, v[k], __frcp_rn(scale));
+        pack_fp8(w, v[k], reciprocal(scale));
         uint8_t* to = p.stage ? bytes + e0 : q + e0;
         if constexpr (E == 8)
           *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
@@ -729,13 +737,15 @@ cudaError_t launch_rows(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
-// Granules per thread: up to 64 granules a row is one warp's, so that it needs no barrier of the CTA; then CTAs of
-// 256 threads as long as that is 16 elements per thread, and 32 elements from there on.
+// Granules per thread: up to 64 granules a row is one warp's, so that it needs no barrier of the CTA (129 fp32
+// columns backward: 52 us with two warps, 31 with one); then CTAs of 256 threads as long as that is 16 elements
+// per thread. Beyond, fp32 rows of up to 2304 granules keep 16 elements per thread in CTAs of up to 576, two of
+// which fit an SM (3001 x 8200 to e4m3: 84 us with 32 elements, 76 with 16), and the rest 32 elements.
 template <typename T>
 int granules_each(int granules) {
   constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
   return granules <= 32 ? 1 : granules <= 64 ? 2 : granules <= 256 ? 1 : granules <= 512 ? 2
-       : granules <= 256 * kHeld ? kHeld : kLong;
+       : granules <= 256 * kHeld || (sizeof(T) == 4 && granules <= kHeld * kHugeThreads) ? kHeld : kLong;
 }
 
 template <typename T, bool FP8, bool EDGES>
@@ -743,6 +753,9 @@ cudaError_t launch_held_norm(RmsNormLaunch& p, int each, int sms, cudaStream_t s
   constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
   if (each == 1) return launch_rows<T, 1, FP8, 256, true, EDGES>(p, sms, stream);
   if (each == 2) return launch_rows<T, 2, FP8, 256, true, EDGES>(p, sms, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (each == kHeld && p.sum_threads > 256) return launch_rows<T, kHeld, FP8, kHugeThreads, false, EDGES>(p, sms, stream);
+  }
   if (each == kHeld) return launch_rows<T, kHeld, FP8, 256, true, EDGES>(p, sms, stream);
   if (p.sum_threads <= 320) return launch_rows<T, kLong, FP8, 320, false, EDGES>(p, sms, stream);
   return launch_rows<T, kLong, FP8, 512, false, EDGES>(p, sms, stream);
