@@ -144,7 +144,7 @@ __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[
 // THREADS: the most of a CTA. HELD: gains stay in registers and the next row is loaded early; without it, for
 // longer rows, a thread has fewer registers and more CTAs overlap. EDGES: rows that are not whole granules.
 template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
-__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 : 3) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
     add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   constexpr int E = kPer<T>;
   __shared__ float red[2][32][1];
@@ -228,19 +228,36 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREA
     if (EDGES) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (holds(k))
+        if (holds(k)) {
+          const int e0 = start(k), border = 32 - (e0 & 31);  // where a granule crosses a left-out word
+          float* to = line + e0 + (e0 >> 5);
 #pragma unroll
-          for (int j = 0; j < E; ++j) line[start(k) + j + ((start(k) + j) >> 5)] = v[k][j];
+          for (int j = 0; j < E; ++j) to[j + (j >= border ? 1 : 0)] = v[k][j];
+        }
       if (edge >= 0) line[edge + (edge >> 5)] = ve;
       __syncthreads();
-      if (t < p.sum_threads)
-        for (int e0 = t * E; e0 < dim; e0 += p.sum_threads * E)
+      // Group t + k tpr from the row's first element: tpr is sum_threads, or the row has fewer groups than either.
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int e0 = (t + k * tpr) * E;
+        const float* from = line + e0 + (e0 >> 5);
+        float u[E];
+#pragma unroll
+        for (int j = 0; j < E; ++j) u[j] = 0.f;
+        if (e0 + E <= dim) {
+#pragma unroll
+          for (int j = 0; j < E; ++j) u[j] = from[j];
+        } else {
 #pragma unroll
           for (int j = 0; j < E; ++j)
-            if (e0 + j < dim) {
-              const float a = line[e0 + j + ((e0 + j) >> 5)];
-              s[0] = fmaf(a, a, s[0]);
-            }
+            if (e0 + j < dim) u[j] = from[j];
+        }
+#pragma unroll
+        for (int j = 0; j < E; ++j) {
+          s[0] = fmaf(u[j], u[j], s[0]);
+          if (LINED) v[k][j] = u[j];
+        }
+      }
     }
     row_sum(s, tpr, red, half);
     const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
@@ -248,11 +265,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? 2 : 3) : THREA
     for (int k = 0; k < K; ++k) {
       if (!HELD) load_gain(gain[0], p.gain, first_out(k), dim);
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const int e = first_out(k) + j;
-        if (LINED) v[k][j] = e < dim ? line[e + (e >> 5)] : 0.f;
-        v[k][j] = v[k][j] * rho * gain[HELD ? k : 0][j];
-      }
+      for (int j = 0; j < E; ++j) v[k][j] = v[k][j] * rho * gain[HELD ? k : 0][j];
     }
     if constexpr (!FP8) {
       T* y = static_cast<T*>(p.y) + i * p.ldy;
