@@ -309,8 +309,8 @@ __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const Embe
 // ---------------------------------------------------------------------------- 3. sums by chunk
 
 // A group of `tpr` threads adds the rows of one chunk over tpr * kCols consecutive columns, kAhead rows loaded at a
-// time. With 16-byte rows (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise its
-// columns lie tpr apart.
+// time. With 16-byte rows (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise a warp
+// holds 32 * kCols consecutive columns and a thread every 32nd of them.
 template <typename TG, bool VEC>
 struct Columns;
 
@@ -318,9 +318,8 @@ template <typename TG>
 struct Columns<TG, true> {
   static constexpr int kCols = 16 / sizeof(TG), kAhead = 8;
   uint4 raw;
-  __device__ __forceinline__ void load(const TG* src, int64_t col, int, int64_t) {
-    raw = __ldcs(reinterpret_cast<const uint4*>(src + col));
-  }
+  // From this thread's first column on; `left` columns of the row lie there.
+  __device__ __forceinline__ void load(const TG* src, int64_t) { raw = __ldcs(reinterpret_cast<const uint4*>(src)); }
   __device__ __forceinline__ void add_to(float (&acc)[kCols]) const {
     float v[kCols];
     row::unpack16<TG>(v, raw);
@@ -331,11 +330,16 @@ struct Columns<TG, true> {
 
 template <typename TG>
 struct Columns<TG, false> {
-  static constexpr int kCols = 4, kAhead = 4;
+  static constexpr int kCols = 8, kAhead = 4;
   TG raw[kCols];
-  __device__ __forceinline__ void load(const TG* src, int64_t col, int tpr, int64_t dim) {
+  __device__ __forceinline__ void load(const TG* src, int64_t left) {
+    if (left > 32 * (kCols - 1)) {
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) raw[k] = col + k * tpr < dim ? __ldcs(src + col + k * tpr) : row::from_f<TG>(0.f);
+      for (int k = 0; k < kCols; ++k) raw[k] = __ldcs(src + 32 * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) raw[k] = 32 * k < left ? __ldcs(src + 32 * k) : row::from_f<TG>(0.f);
+    }
   }
   __device__ __forceinline__ void add_to(float (&acc)[kCols]) const {
 #pragma unroll
@@ -343,14 +347,13 @@ struct Columns<TG, false> {
   }
 };
 
-// dst = scale * acc, or dst += scale * acc.
+// dst = scale * acc, or dst += scale * acc, from this thread's first column on.
 template <bool VEC, int COLS>
-__device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COLS], float scale, bool add, int64_t col,
-                                              int tpr, int64_t dim) {
+__device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COLS], float scale, bool add, int64_t left) {
   if constexpr (VEC) {
 #pragma unroll
     for (int k = 0; k < COLS; k += 4) {
-      float4* at = reinterpret_cast<float4*>(dst + col + k);
+      float4* at = reinterpret_cast<float4*>(dst + k);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       if (add) o = *at;
       o.x = fmaf(scale, acc[k], o.x), o.y = fmaf(scale, acc[k + 1], o.y);
@@ -360,10 +363,7 @@ __device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COL
   } else {
 #pragma unroll
     for (int k = 0; k < COLS; ++k)
-      if (col + k * tpr < dim) {
-        float* at = dst + col + k * tpr;
-        *at = fmaf(scale, acc[k], add ? *at : 0.f);
-      }
+      if (32 * k < left) dst[32 * k] = fmaf(scale, acc[k], add ? dst[32 * k] : 0.f);
   }
 }
 
@@ -380,13 +380,14 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
   const int64_t chunk = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / tpr;
   if (chunk >= p.chunks) return;
   const int t = threadIdx.x % tpr;
-  const int64_t col = static_cast<int64_t>(blockIdx.y) * tpr * COLS + (VEC ? t * COLS : t);
-  const bool active = col < p.dim;
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * tpr * COLS + (VEC ? t * COLS : t / 32 * 32 * COLS + t % 32);
+  const int64_t left = p.dim - col;
+  const bool active = left > 0;
   const bool first_slice = blockIdx.y == 0 && t == 0;
   const uint2* tokens = p.sorted[0];
   const int64_t begin = chunk * p.chunk_len, end = min(begin + p.chunk_len, p.n);
   const uint32_t none = static_cast<uint32_t>(p.rows);
-  const TG* src = static_cast<const TG*>(p.grad_out);
+  const TG* src = static_cast<const TG*>(p.grad_out) + col;
   // Tokens that add nothing sort behind every row; their rows are not read.
   uint2 tok[kAhead];
   auto fetch_tokens = [&](uint2 (&to)[kAhead], int64_t i) {
@@ -409,13 +410,13 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
     if (from_before || goes_on) {
       // Head sums lie in the even rows of the workspace, tail sums in the odd ones.
       float* part = p.partials + (chunk * 2 + (from_before ? 0 : 1)) * p.ld_partials;
-      if (active) store_columns<VEC>(part, acc, 1.f, false, col, tpr, p.dim);
+      if (active) store_columns<VEC>(part + col, acc, 1.f, false, left);
       if (!from_before && key == key_far && first_slice) {
         const unsigned at = atomicAdd(p.crossing_count, 1u);
         if (dev_check(at < p.chunks, p.status)) p.crossing[at] = make_uint2(static_cast<uint32_t>(chunk), key);
       }
     } else if (active) {
-      store_columns<VEC>(p.grad + static_cast<int64_t>(key) * p.ld_grad, acc, p.scale, p.accumulate != 0, col, tpr, p.dim);
+      store_columns<VEC>(p.grad + static_cast<int64_t>(key) * p.ld_grad + col, acc, p.scale, p.accumulate != 0, left);
     }
   };
   // A chunk's length is a multiple of kAhead: only the list's last chunk has places without tokens.
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) embedding_chunk_kernel(const Embeddi
     uint2 next[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-      if (active && tok[a].x != none) val[a].load(src + tok[a].y * p.ld_grad_out, col, tpr, p.dim);
+      if (active && tok[a].x != none) val[a].load(src + tok[a].y * p.ld_grad_out, left);
     fetch_tokens(next, i + kAhead);
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
@@ -550,11 +551,11 @@ bool aligned16(const void* p, int64_t ld, size_t elem) {
 void split_tokens(EmbeddingGradLaunch& p) {
   const int cols = p.vec ? (p.grad_dtype == 1 ? Columns<__nv_bfloat16, true>::kCols : Columns<float, true>::kCols)
                          : Columns<float, false>::kCols;
-  // Slices of equal length: whole warps, or a power of two below one.
+  // Slices of equal length: whole warps, or with VEC a power of two of threads below one.
   const int64_t slices = (p.dim + kThreads * cols - 1) / (kThreads * cols);
   const int need = static_cast<int>(((p.dim + slices - 1) / slices + cols - 1) / cols);
   p.tpr = (need + 31) / 32 * 32;
-  if (need <= 16)
+  if (p.vec && need <= 16)
     for (p.tpr = 1; p.tpr < need;) p.tpr *= 2;
   const int64_t groups = kThreads / p.tpr;
   p.chunk_len = 16;
