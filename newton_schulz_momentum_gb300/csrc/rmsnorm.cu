@@ -114,6 +114,14 @@ __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[32]
     for (int k = 0; k < N; ++k) s[k] += red[half][w][k];
 }
 
+// The threads of a row meet.
+__device__ __forceinline__ void row_sync(int tpr) {
+  if (tpr <= 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
 // ---------------------------------------------------------------------------- forward
 
 // max that gives NaN for NaN.
@@ -142,9 +150,14 @@ __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[
 }
 
 // THREADS: the most of a CTA. HELD: gains stay in registers and the next row is loaded early; without it, for
-// longer rows, a thread has fewer registers and more CTAs overlap. EDGES: rows that are not whole granules.
+// longer rows, a thread has fewer registers, more CTAs overlap, and the next row is asked into L2 (16-byte
+// pieces of it, by one copy instruction; 5460 x 12289 bf16: 179 us without, 153 with; fp32 rows with edges gain
+// too, 65344 x 1027 210 -> 182 us, and all others lose, 16384 x 4096 bf16 85 -> 91). EDGES: rows that are not
+// whole granules. CTAs of 256 threads that registers leave room for: four with one aligned granule a thread
+// (1048576 x 64 bf16: 92 us with three, 84 with four), three and two where there is more to hold (65344 x 1027
+// bf16: 126 us with three, 148 with four).
 template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
-__global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 : 3) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3) : K > 1 ? 3 : 4) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
     add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   constexpr int E = kPer<T>;
   __shared__ float red[2][32][1];
@@ -218,6 +231,11 @@ __global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 :
     x += step * p.ldx;
     if (r) r += step * p.ldr;
     if (HELD && base + step < p.n) fetch(i + step);
+    if ((!HELD || (EDGES && sizeof(T) == 4 && !FP8)) && t == 0 && full > 0 && i + (HELD ? 2 : 1) * step < p.n) {
+      const int head = EDGES ? cut.head : 0;
+      ptx::prefetch_l2(x + (HELD ? step * p.ldx : 0) + head, full * 16);
+      if (r) ptx::prefetch_l2(r + (HELD ? step * p.ldr : 0) + head, full * 16);
+    }
     if (h && i < p.n) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -235,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 :
           for (int j = 0; j < E; ++j) to[j + (j >= border ? 1 : 0)] = v[k][j];
         }
       if (edge >= 0) line[edge + (edge >> 5)] = ve;
-      __syncthreads();
+      row_sync(tpr);
       // Group t + k tpr from the row's first element: tpr is sum_threads, or the row has fewer groups than either.
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 :
           atomicMax(top + first_out(k) / group, __float_as_uint(most[k]));
       }
       if (p.lanes == 0) {
-        __syncthreads();
+        row_sync(tpr);
 #pragma unroll
         for (int k = 0; k < K; ++k)
           if (first_out(k) < dim) most[k] = __uint_as_float(top[first_out(k) / group]);
@@ -324,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? ((FP8 || EDGES) && K > 1 ? 2 :
           *reinterpret_cast<uint32_t*>(to) = w[0];
       }
       if (p.stage) {
-        __syncthreads();
+        row_sync(tpr);
         // The row goes out by 16-byte addresses; what lies there begins between words of the bytes.
         const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
         if (i < p.n)
@@ -426,6 +444,14 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
     dy += step * p.lddy;
     h += step * p.ldh;
     if (dh) dh += step * p.lddh;
+    // Into L2 the row after it (16372 x 4099 fp32: 186 -> 168 us, 4194 x 16000 bf16 146 -> 116; bf16 rows that are
+    // loaded early lose, 16384 x 4096 103 -> 107).
+    if ((!AHEAD || sizeof(T) == 4) && t == 0 && i + step < p.n && full > 0) {
+      const int head = EDGES ? cut.head : 0;
+      ptx::prefetch_l2(dy + head, full * 16);
+      ptx::prefetch_l2(h + head, full * 16);
+      if (dh) ptx::prefetch_l2(dh + head, full * 16);
+    }
   };
   if (AHEAD) fetch(next, first + slot);
   int half = 0;
@@ -804,18 +830,38 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
+// A row's whole granules, K a thread, in CTAs that leave a thread the registers for them: 256 threads twice per SM,
+// then one CTA per SM whose threads are as many as the row needs, since registers are divided among them. bf16
+// (16384 x 4096, K = 2): three CTAs with the sums in shared memory 144 us, two with them in registers 100. fp32 rows
+// with edges, as of 65 granules K = 2: 65344 x 1027 225 us with one, 169 with two. Long fp32 rows with edges spill at
+// four granules in 800 threads, so eight in 416 (6099 x 11003: 240 -> 202 us), while aligned ones do not (6710 x
+// 10000: 176 us, 194 with eight), nor rows for 576 threads (8183 x 8201: 209 us, 224 with eight). bf16 rows with
+// edges of 1025 to 1280 granules: four in 320 threads 164 us, two in 640 150 (8183 x 8201).
 template <typename T, bool EDGES>
 cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
   if (granules <= 32) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
   if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, true, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 256) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 256 && !(EDGES && sizeof(T) == 4))
+    return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
   if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if (granules <= 1024) return launch_grad_rows<T, 4, 256, 2, false, false, EDGES>(p, granules, sms, stream);
+  if (granules <= 1280) {
+    if constexpr (EDGES && sizeof(T) == 2)
+      return launch_grad_rows<T, 2, 640, 1, false, false, EDGES>(p, granules, sms, stream);
+    else
+      return launch_grad_rows<T, 4, 320, 2, false, false, EDGES>(p, granules, sms, stream);
+  }
   if (granules <= 2048) return launch_grad_rows<T, 4, 512, 1, false, false, EDGES>(p, granules, sms, stream);
-  if constexpr (sizeof(T) == 4)
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (EDGES) {
+      if (granules <= 2304) return launch_grad_rows<T, 4, kHugeThreads, 1, false, false, EDGES>(p, granules, sms, stream);
+      if (granules <= 3328) return launch_grad_rows<T, 8, 416, 1, false, false, EDGES>(p, granules, sms, stream);
+    } else {
+      if (granules <= 3200) return launch_grad_rows<T, 4, 800, 1, false, false, EDGES>(p, granules, sms, stream);
+    }
     return launch_grad_rows<T, 4, 1024, 1, false, false, EDGES>(p, granules, sms, stream);
-  else
-    return cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
+  }
+  return cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
 }
 
 template <typename T>
@@ -836,7 +882,7 @@ cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
     }
     e = row::launch(add_rmsnorm_grad_kernel<T>, grid, kThreads, 0, stream, p);
   } else {
-    const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>);
+    const int granules = std::max(1, static_cast<int>(p.dim / kPer<T>));  // at most, whole ones
     e = has_edges(dy, p.n, p.dim, sizeof(T)) ? launch_held_grad<T, true>(p, granules, sms, stream)
                                              : launch_held_grad<T, false>(p, granules, sms, stream);
   }

@@ -345,6 +345,11 @@ __device__ __forceinline__ void bulk_load_hint(uint32_t smem_dst, const void* sr
       : "memory");
 }
 
+// `bytes` (a multiple of 16) of 16-byte aligned global memory into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "r"(bytes) : "memory");
+}
+
 // `bytes` (a multiple of 16) of shared memory to 16-byte aligned global memory, in the current bulk group.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t smem_src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_src), "r"(bytes)
