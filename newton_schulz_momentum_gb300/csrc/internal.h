@@ -366,7 +366,10 @@ struct RmsNormLaunch {
   int64_t group;  // columns per scale; 0: the whole row
   // Set by launch_add_rmsnorm: threads per row and those that form its sum; scales per row and the lanes that
   // share one (0: more than a warp); shared memory bytes for a row of bytes and words for a row of h (0: none).
+  // From one row of a thread to its next: rows, and elements of each array.
   int tpr, sum_threads, parts, lanes, stage, line;
+  float inv_dim;
+  int64_t step, step_x, step_r, step_h;
 };
 cudaError_t launch_add_rmsnorm(RmsNormLaunch& p, int sms, cudaStream_t stream);
 
@@ -382,7 +385,11 @@ struct RmsNormGradLaunch {
   float* dgain;  // may be null
   int accumulate;
   float *partials, *rho;  // workspace, set by rmsnorm_grad_workspace
-  int tpr, npartials;     // set by launch_add_rmsnorm_grad: threads per row, rows of partials
+  // Set by launch_add_rmsnorm_grad: threads per row, rows of partials; from one row of a thread to its next, rows and
+  // elements of each array.
+  int tpr, npartials;
+  float inv_dim;
+  int64_t step, step_dy, step_h, step_dh, step_dx;
 };
 // Workspace bytes; also places the buffers at `ws` (null when asked for the size alone).
 int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, int sms, char* ws);

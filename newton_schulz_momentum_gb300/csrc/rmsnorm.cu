@@ -95,9 +95,16 @@ __device__ __forceinline__ void load_gain(float (&g)[E], const float* gain, int 
 // per row is enough. All threads of the CTA call it.
 template <int N>
 __device__ __forceinline__ void row_sum(float (&s)[N], int tpr, float (*red)[32][N], int half) {
-  for (int o = min(tpr, 32) / 2; o > 0; o >>= 1)
+  if (tpr >= 32) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  } else {
+    for (int o = tpr / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  }
   if (tpr <= 32) {
     __syncwarp();  // as the barrier below does for wider rows: what a row left in shared memory is there for the next
     return;
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
   ptx::griddep_wait();
   const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int dim = static_cast<int>(p.dim);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  const int64_t step = p.step, first = static_cast<int64_t>(blockIdx.x) * rows;
   const T* x = static_cast<const T*>(p.x) + (first + slot) * p.ldx;
   const T* r = p.residual ? static_cast<const T*>(p.residual) + (first + slot) * p.ldr : nullptr;
   T* h = p.h ? static_cast<T*>(p.h) + (first + slot) * p.ldh : nullptr;
@@ -228,13 +235,13 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
       }
     }
     if (EDGES) ve = row::to_f(xe) + row::to_f(re);
-    x += step * p.ldx;
-    if (r) r += step * p.ldr;
+    x += p.step_x;
+    if (r) r += p.step_r;
     if (HELD && base + step < p.n) fetch(i + step);
     if ((!HELD || (EDGES && sizeof(T) == 4 && !FP8)) && t == 0 && full > 0 && i + (HELD ? 2 : 1) * step < p.n) {
       const int head = EDGES ? cut.head : 0;
-      ptx::prefetch_l2(x + (HELD ? step * p.ldx : 0) + head, full * 16);
-      if (r) ptx::prefetch_l2(r + (HELD ? step * p.ldr : 0) + head, full * 16);
+      ptx::prefetch_l2(x + (HELD ? p.step_x : 0) + head, full * 16);
+      if (r) ptx::prefetch_l2(r + (HELD ? p.step_r : 0) + head, full * 16);
     }
     if (h && i < p.n) {
 #pragma unroll
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
         if (holds(k)) store_granule(h + start(k), v[k]);
       if (edge >= 0) h[edge] = row::from_f<T>(ve);
     }
-    if (h) h += step * p.ldh;
+    if (h) h += p.step_h;
     if (EDGES) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
       }
     }
     row_sum(s, tpr, red, half);
-    const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
+    const float rho = rsqrtf(fmaf(s[0], p.inv_dim, p.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (!HELD) load_gain(gain[0], p.gain, first_out(k), dim);
@@ -376,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   ptx::griddep_wait();
   const int tpr = p.tpr, rows = blockDim.x / tpr, slot = threadIdx.x / tpr, t = threadIdx.x % tpr;
   const int dim = static_cast<int>(p.dim);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * rows, first = static_cast<int64_t>(blockIdx.x) * rows;
+  const int64_t step = p.step, first = static_cast<int64_t>(blockIdx.x) * rows;
   const T* dy = static_cast<const T*>(p.dy) + (first + slot) * p.lddy;
   const T* h = static_cast<const T*>(p.h) + (first + slot) * p.ldh;
   const T* dh = p.dh ? static_cast<const T*>(p.dh) + (first + slot) * p.lddh : nullptr;
@@ -425,28 +432,30 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
     T ye, he, te;
   };
   Row now{}, next{};
+  const bool leads = t == 0 && full > 0;
   auto fetch = [&](Row& to, int64_t i) {
+    const bool live = i < p.n;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const bool in = i < p.n && holds(k);
+      const bool in = live && holds(k);
       to.y[k] = in ? __ldcs(reinterpret_cast<const uint4*>(dy + start(k))) : make_uint4(0, 0, 0, 0);
       to.h[k] = in ? __ldcs(reinterpret_cast<const uint4*>(h + start(k))) : make_uint4(0, 0, 0, 0);
       to.t[k] = in && dh ? __ldcs(reinterpret_cast<const uint4*>(dh + start(k))) : make_uint4(0, 0, 0, 0);
     }
     if (EDGES) {
       to.ye = to.he = to.te = row::from_f<T>(0.f);
-      if (i < p.n && edge >= 0) {
+      if (live && edge >= 0) {
         to.ye = dy[edge];
         to.he = h[edge];
         if (dh) to.te = dh[edge];
       }
     }
-    dy += step * p.lddy;
-    h += step * p.ldh;
-    if (dh) dh += step * p.lddh;
+    dy += p.step_dy;
+    h += p.step_h;
+    if (dh) dh += p.step_dh;
     // Into L2 the row after it (16372 x 4099 fp32: 186 -> 168 us, 4194 x 16000 bf16 146 -> 116; bf16 rows that are
     // loaded early lose, 16384 x 4096 103 -> 107).
-    if ((!AHEAD || sizeof(T) == 4) && t == 0 && i + step < p.n && full > 0) {
+    if ((!AHEAD || sizeof(T) == 4) && leads && i + step < p.n) {
       const int head = EDGES ? cut.head : 0;
       ptx::prefetch_l2(dy + head, full * 16);
       ptx::prefetch_l2(h + head, full * 16);
@@ -457,6 +466,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   int half = 0;
   for (int64_t base = first; base < p.n; base += step, half ^= 1) {
     const int64_t i = base + slot;
+    const bool live = i < p.n;
     if (AHEAD) {
       now = next;
       if (base + step < p.n) fetch(next, i + step);
@@ -482,8 +492,9 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
       s[1] = fmaf(de, he, s[1]);
     }
     row_sum(s, tpr, red, half);
-    const float rho = rsqrtf(s[0] / static_cast<float>(dim) + p.eps);
-    const float back = s[1] / static_cast<float>(dim) * rho * rho * rho;
+    // Behind the last row everything is 0, rho too.
+    const float rho = live ? rsqrtf(fmaf(s[0], p.inv_dim, p.eps)) : 0.f;
+    const float back = s[1] * p.inv_dim * rho * rho * rho;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float a[E], b[E], c[E];
@@ -494,23 +505,24 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
       float4 sum;
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        const float term = i < p.n ? a[j] * (b[j] * rho) : 0.f;
+        const float hat = b[j] * rho;
         if (REGS) {
-          acc[k][j] += term;
+          acc[k][j] = fmaf(a[j], hat, acc[k][j]);
         } else {
           if (j % 4 == 0) sum = sums[j / 4 * granules + t + k * tpr];
-          (j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w) += term;
+          float& to = j % 4 == 0 ? sum.x : j % 4 == 1 ? sum.y : j % 4 == 2 ? sum.z : sum.w;
+          to = fmaf(a[j], hat, to);
           if (j % 4 == 3) sums[j / 4 * granules + t + k * tpr] = sum;
         }
         c[j] = fmaf(rho, a[j] * gain[REGS ? k : 0][j], fmaf(-back, b[j], c[j]));
       }
-      if (i < p.n && holds(k)) store_granule(dx + start(k), c);
+      if (live && holds(k)) store_granule(dx + start(k), c);
     }
-    if (EDGES && i < p.n && edge >= 0) {
+    if (EDGES && live && edge >= 0) {
       acc_edge = fmaf(row::to_f(now.ye), he * rho, acc_edge);
       dx[edge] = row::from_f<T>(fmaf(rho, de, fmaf(-back, he, row::to_f(now.te))));
     }
-    dx += step * p.lddx;
+    dx += p.step_dx;
   }
   if (!p.dgain) return;
   // This CTA's sums, one row of the workspace. The row slots of a CTA start at different offsets, so they join
@@ -595,7 +607,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormL
         sq[0] = fmaf(v, v, sq[0]);
       }
   row_sum(sq, threads, red, 0);
-  const float rho = rsqrtf(sq[0] / static_cast<float>(p.dim) + p.eps);
+  const float rho = rsqrtf(fmaf(sq[0], p.inv_dim, p.eps));
   auto value = [&](int64_t c) {
     const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
     return v * rho * (p.gain ? p.gain[c] : 1.f);
@@ -645,8 +657,8 @@ __global__ void __launch_bounds__(kThreads) add_rmsnorm_grad_kernel(const RmsNor
   }
   sq = row::block_sum(sq, red);
   along = row::block_sum(along, red);
-  const float rho = rsqrtf(sq / static_cast<float>(p.dim) + p.eps);
-  const float back = along / static_cast<float>(p.dim) * rho * rho * rho;
+  const float rho = rsqrtf(fmaf(sq, p.inv_dim, p.eps));
+  const float back = along * p.inv_dim * rho * rho * rho;
   if (!p.dx) {
     if (threadIdx.x == 0) p.rho[i] = rho;
     return;
@@ -773,6 +785,8 @@ cudaError_t launch_rows(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
   if (e != cudaSuccess) return e;
   p.tpr = g.tpr;
+  p.step = static_cast<int64_t>(g.ctas) * g.rows;
+  p.step_x = p.step * p.ldx, p.step_r = p.step * p.ldr, p.step_h = p.step * p.ldh;
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
 
@@ -804,6 +818,7 @@ template <typename T, bool FP8>
 cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T>(granules);
   p.sum_threads = std::min(row_threads(granules, each), kMaxThreads);
+  p.inv_dim = 1.f / static_cast<float>(p.dim);  // the mean of the squares is within two units of the last place by it
   const Array x{p.x, p.ldx};
   if (p.dim > kMaxHeld ||
       !same_offsets({x, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n, sizeof(T)))
@@ -826,6 +841,8 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
   if (e != cudaSuccess) return e;
   p.tpr = g.tpr;
+  p.step = static_cast<int64_t>(g.ctas) * g.rows;
+  p.step_dy = p.step * p.lddy, p.step_h = p.step * p.ldh, p.step_dh = p.step * p.lddh, p.step_dx = p.step * p.lddx;
   p.npartials = static_cast<int>(g.ctas);
   return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
 }
@@ -867,6 +884,7 @@ cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 template <typename T>
 cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
   const Array dy{p.dy, p.lddy};
+  p.inv_dim = 1.f / static_cast<float>(p.dim);
   cudaError_t e;
   if (p.dim > kMaxHeld || !same_offsets({dy, {p.h, p.ldh}, {p.dh, p.lddh}, {p.dx, p.lddx}}, p.n, sizeof(T))) {
     const dim3 grid(static_cast<unsigned>(p.n));
