@@ -848,12 +848,15 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 }
 
 // A row's whole granules, K a thread, in CTAs that leave a thread the registers for them: 256 threads twice per SM,
-// then one CTA per SM whose threads are as many as the row needs, since registers are divided among them. bf16
-// (16384 x 4096, K = 2): three CTAs with the sums in shared memory 144 us, two with them in registers 100. fp32 rows
-// with edges, as of 65 granules K = 2: 65344 x 1027 225 us with one, 169 with two. Long fp32 rows with edges spill at
-// four granules in 800 threads, so eight in 416 (6099 x 11003: 240 -> 202 us), while aligned ones do not (6710 x
-// 10000: 176 us, 194 with eight), nor rows for 576 threads (8183 x 8201: 209 us, 224 with eight). bf16 rows with
-// edges of 1025 to 1280 granules: four in 320 threads 164 us, two in 640 150 (8183 x 8201).
+// then one CTA per SM whose threads are as many as the row needs, since registers are divided among them. What
+// spills loses; all at 67 million elements:
+// - bf16, two granules: three CTAs with the sums in shared memory 144 us, two with them in registers 94 (dim 4096).
+// - fp32 with edges, as of 65 granules two: dim 1027 225 us with one, 169 with two.
+// - bf16 with edges, 513 to 1024 granules: four and two CTAs of 256 131 us, two in 512 and the next row ahead 112
+//   (dim 6005); aligned rows the other way, 113 and 127 (dim 5000). To 1280 granules four in 320 threads 164 us, two in
+//   640 133 (dim 8201).
+// - fp32 beyond 2048 granules: four in 576 to 768 threads while that holds them (aligned, dim 10000: 181 us, 194 with
+//   eight in 416; with edges, dim 8201: 189, 224), but with edges beyond 2304 eight (dim 11003: 240 and 202).
 template <typename T, bool EDGES>
 cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
   if (granules <= 32) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
@@ -861,12 +864,12 @@ cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   if (granules <= 256 && !(EDGES && sizeof(T) == 4))
     return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
   if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 1024) return launch_grad_rows<T, 4, 256, 2, false, false, EDGES>(p, granules, sms, stream);
-  if (granules <= 1280) {
-    if constexpr (EDGES && sizeof(T) == 2)
-      return launch_grad_rows<T, 2, 640, 1, false, false, EDGES>(p, granules, sms, stream);
-    else
-      return launch_grad_rows<T, 4, 320, 2, false, false, EDGES>(p, granules, sms, stream);
+  if constexpr (EDGES && sizeof(T) == 2) {
+    if (granules <= 1024) return launch_grad_rows<T, 2, 512, 1, false, true, EDGES>(p, granules, sms, stream);
+    if (granules <= 1280) return launch_grad_rows<T, 2, 640, 1, false, false, EDGES>(p, granules, sms, stream);
+  } else {
+    if (granules <= 1024) return launch_grad_rows<T, 4, 256, 2, false, false, EDGES>(p, granules, sms, stream);
+    if (granules <= 1280) return launch_grad_rows<T, 4, 320, 2, false, false, EDGES>(p, granules, sms, stream);
   }
   if (granules <= 2048) return launch_grad_rows<T, 4, 512, 1, false, false, EDGES>(p, granules, sms, stream);
   if constexpr (sizeof(T) == 4) {
@@ -874,7 +877,7 @@ cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaSt
       if (granules <= 2304) return launch_grad_rows<T, 4, kHugeThreads, 1, false, false, EDGES>(p, granules, sms, stream);
       if (granules <= 3328) return launch_grad_rows<T, 8, 416, 1, false, false, EDGES>(p, granules, sms, stream);
     } else {
-      if (granules <= 3200) return launch_grad_rows<T, 4, 800, 1, false, false, EDGES>(p, granules, sms, stream);
+      if (granules <= 3072) return launch_grad_rows<T, 4, 768, 1, false, false, EDGES>(p, granules, sms, stream);
     }
     return launch_grad_rows<T, 4, 1024, 1, false, false, EDGES>(p, granules, sms, stream);
   }
