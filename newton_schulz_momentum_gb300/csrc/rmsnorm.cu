@@ -555,9 +555,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   }
 }
 
-// dgain from the CTAs' sums: a CTA takes 32 columns, its warps every eighth row of the workspace.
-__global__ void __launch_bounds__(kThreads) rmsnorm_dgain_kernel(const RmsNormGradLaunch p) {
-  constexpr int kWarps = kThreads / 32;
+// dgain from the CTAs' sums: a CTA takes 32 columns, its warps every 32nd row of the workspace. Latency of the loads
+// of a warp bounds it.
+__global__ void __launch_bounds__(kMaxThreads) rmsnorm_dgain_kernel(const RmsNormGradLaunch p) {
+  constexpr int kWarps = kMaxThreads / 32;
   __shared__ float sums[kWarps][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -578,7 +579,9 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_dgain_kernel(const RmsNormGr
   sums[warp][lane] = acc;
   __syncthreads();
   if (warp == 0 && c < p.dim) {
-    for (int w = 1; w < kWarps; ++w) acc += sums[w][lane];
+    acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) acc += sums[w][lane];
     p.dgain[c] = p.accumulate ? p.dgain[c] + acc : acc;
   }
 }
@@ -908,7 +911,7 @@ cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
                                              : launch_held_grad<T, false>(p, granules, sms, stream);
   }
   if (e != cudaSuccess || !p.dgain) return e;
-  return row::launch(rmsnorm_dgain_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), kThreads, 0, stream, p);
+  return row::launch(rmsnorm_dgain_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), kMaxThreads, 0, stream, p);
 }
 
 }  // namespace
