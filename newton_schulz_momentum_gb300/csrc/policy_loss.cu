@@ -238,6 +238,38 @@ __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const
   return c * r.w * p.inv_temperature;
 }
 
+// Terms of the loss that are there; 0 between launches.
+__device__ unsigned g_terms_done;
+
+// Leaves a term of the loss; who leaves the last one adds them all, in an order that their number fixes. Called by one
+// whole warp per term. (A launch of its own for the sum: 4 more microseconds for a call of 8 rows.)
+__device__ __forceinline__ void leave_term(const PolicyLaunch& p, int64_t at, float loss) {
+  const int lane = threadIdx.x & 31;
+  unsigned before = 0;
+  if (lane == 0) {
+    p.loss_terms[at] = loss;
+    __threadfence();
+    before = atomicAdd(&g_terms_done, 1u);
+  }
+  if (__shfl_sync(0xffffffffu, before, 0) + 1 < static_cast<unsigned>(p.terms)) return;
+  __threadfence();
+  float acc = 0.f;
+  int64_t i = lane;
+  for (; i + 7 * 32 < p.terms; i += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __ldcg(p.loss_terms + i + 32 * k);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc += v[k];
+  }
+  for (; i < p.terms; i += 32) acc += __ldcg(p.loss_terms + i);
+  acc = warp_sum(acc);
+  if (lane == 0) {
+    *p.loss = acc;
+    g_terms_done = 0;
+  }
+}
+
 __device__ __forceinline__ void row_skipped(const PolicyLaunch& p, int64_t i) {
   if (p.logp) p.logp[i] = 0.f;
 }
@@ -589,8 +621,15 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
     word = word1, word1 = word2, word2 = word3, a = a1, a1 = a2;
     token_logit = token_logit1, xe = xe1, xa1 = xa2, xe1 = xe2;
   }
-  // One term per cluster or warp: its rows' in their order.
-  if (p.loss_terms && unit == 0 && lane == 0) p.loss_terms[first] = loss;
+  // One term per cluster (or CTA, its warps in their order): its rows' in their order.
+  if (SOLO && p.loss_terms) {
+    __shared__ float of_warp[R::kWarps];
+    if (lane == 0) of_warp[warp] = loss;
+    __syncthreads();
+    loss = 0.f;
+    for (int w = 0; w < R::kWarps; ++w) loss += of_warp[w];
+  }
+  if (p.loss_terms && unit == 0 && (!SOLO || warp == 0)) leave_term(p, SOLO ? blockIdx.x : first, loss);
   // Rows behind the last are never loaded, so no load is on its way here, unless a wait ran out.
   if (lane == 0) {
     if (*abort_flag)
@@ -617,10 +656,8 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
   const T* x = static_cast<const T*>(p.logits) + i * p.ld;
   T* dx = p.dlogits ? static_cast<T*>(p.dlogits) + i * p.ldd : nullptr;
   if (r.a < 0) {
-    if (threadIdx.x == 0) {
-      row_skipped(p, i);
-      if (p.loss_terms) p.loss_terms[i] = 0.f;
-    }
+    if (threadIdx.x == 0) row_skipped(p, i);
+    if (p.loss_terms && threadIdx.x < 32) leave_term(p, i, 0.f);
     if (dx)
       for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) dx[c] = row::from_f<T>(0.f);
     return;
@@ -644,7 +681,7 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
   for (int w = 1; w < kTwiceThreads / 32; ++w) t = join(t, part[w], k);
   float loss = 0.f;
   const float scale = row_end(p, i, r, xa, t, threadIdx.x == 0, loss);
-  if (threadIdx.x == 0 && p.loss_terms) p.loss_terms[i] = loss;
+  if (p.loss_terms && threadIdx.x < 32) leave_term(p, i, loss);
   if (!dx) return;
   base = finite_or_zero(t.m);
   const float per = -scale * __frcp_rn(t.s);
@@ -654,31 +691,21 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
   }
 }
 
-// ---------------------------------------------------------------------------- the loss
-
-constexpr int kSumThreads = 1024;
-
-__global__ void __launch_bounds__(kSumThreads) policy_sum_kernel(const PolicyLaunch p) {
-  __shared__ float red[32];
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  float acc = 0.f;
-  for (int64_t i = threadIdx.x; i < p.terms; i += kSumThreads) acc += __ldcg(p.loss_terms + i);
-  acc = row::block_sum(acc, red);
-  if (threadIdx.x == 0) *p.loss = acc;
-}
+// ---------------------------------------------------------------------------- launches
 
 // How many clusters of `size` CTAs of the ring kernel fit on the GPU at once. A property of the device: asked for
-// once (the caller holds the library's lock).
+// once (the caller holds the library's lock), after the kernel's attributes have been set.
 template <typename T, int MODE, bool EDGES>
-cudaError_t resident_clusters(int size, int* clusters) {
+cudaError_t resident_clusters(int dev, int size, int* clusters) {
   constexpr int kMaxDevices = 64;
   static int known[kMaxDevices][kMaxCluster + 1];  // 1 + the number
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
   int n = dev < kMaxDevices ? known[dev][size] - 1 : -1;
   if (n < 0) {
+    auto* kernel = policy_ring_kernel<T, MODE, EDGES>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<MODE>::kSmem);
+    if (e == cudaSuccess && MODE == kWide)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(size));
     cfg.blockDim = dim3(Ring<MODE>::kThreads);
@@ -689,7 +716,7 @@ cudaError_t resident_clusters(int size, int* clusters) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, policy_ring_kernel<T, MODE, EDGES>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) known[dev][size] = n + 1;
   }
@@ -712,15 +739,12 @@ cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
   // Two CTAs at least: the sums travel by asynchronous stores, which only a cluster launch has.
   const int64_t groups = (p.vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
   if (least > R::kCluster) return cudaSuccess;
-  cudaError_t e =
-      cudaFuncSetAttribute(policy_ring_kernel<T, MODE, EDGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kSmem);
-  if (e == cudaSuccess && MODE == kWide)
-    e = cudaFuncSetAttribute(policy_ring_kernel<T, MODE, EDGES>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  int best = 0;
+  int dev = 0, best = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   double most = 0.0;
   for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
     int n = 0;
-    e = resident_clusters<T, MODE, EDGES>(size, &n);
+    e = resident_clusters<T, MODE, EDGES>(dev, size, &n);
     const double rate = n / (kRowCost + static_cast<double>(groups) / (size * R::kWarps));
     if (e == cudaSuccess && rate > most) most = rate, best = n, p.cluster = size;
   }
@@ -747,7 +771,7 @@ cudaError_t launch_solo(PolicyLaunch& p, int sms, cudaStream_t stream) {
     ctas = std::min<int64_t>(ctas, static_cast<int64_t>(sms) * std::max(per_sm, 1));
   }
   if (e != cudaSuccess) return e;
-  p.terms = ctas * R::kWarps;
+  p.terms = ctas;
   return row::launch(kernel, dim3(static_cast<unsigned>(ctas)), R::kThreads, smem, stream, p);
 }
 
@@ -777,15 +801,11 @@ cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
 
 }  // namespace
 
-int64_t policy_workspace(int64_t n) { return (n + Ring<kSolo>::kWarps) * static_cast<int64_t>(sizeof(float)); }
+int64_t policy_workspace(int64_t n) { return n * static_cast<int64_t>(sizeof(float)); }
 
 cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream) {
-  p.terms = 0;
-  if (p.n > 0) {
-    const cudaError_t e = p.dtype == 0 ? launch_rows<float>(p, sms, stream) : launch_rows<__nv_bfloat16>(p, sms, stream);
-    if (e != cudaSuccess) return e;
-  }
-  return p.loss ? row::launch(policy_sum_kernel, dim3(1), kSumThreads, 0, stream, p) : cudaSuccess;
+  if (p.n == 0) return p.loss ? cudaMemsetAsync(p.loss, 0, sizeof(float), stream) : cudaSuccess;
+  return p.dtype == 0 ? launch_rows<float>(p, sms, stream) : launch_rows<__nv_bfloat16>(p, sms, stream);
 }
 
 }  // namespace dmuon
