@@ -307,8 +307,9 @@ DMUON_API int dmuon_set_graph_replay(int on);
  * Arrays are row-major with `ld` elements from one row to the next (ld >= the row length; rows of fp32 or
  * bf16 as the dtype says). Unlike the entry points above they need no more than their elements'
  * alignment; rows that are 16-byte aligned run faster. Token ids are int32 (id_bytes 4) or int64
- * (id_bytes 8). n == 0 is a call without tokens. Sums are held in fp32, in an order that depends on the
- * sizes alone: the same call gives the same bits. Offsets are 64-bit.
+ * (id_bytes 8). n == 0 is a call without tokens. Sums are held in fp32, in an order fixed by the call's
+ * sizes, strides and alignment: the same call gives the same bits. A row of dmuon_add_rmsnorm and of
+ * dmuon_policy_loss gives the same bits whatever the other rows are and wherever it lies. Offsets are 64-bit.
  */
 
 /*

@@ -9,6 +9,10 @@
 //      chunk's rows and writes each table row that begins and ends inside it; a row that crosses a chunk's
 //      border leaves its sum over the chunk in the workspace;
 //   4. the rows that cross borders are put together from their chunks' sums, in order.
+// Bound by memory where the table is large: 16384 x 4096 bf16 tokens into 128256 rows take 348 us, 2.1 GB of them
+// zeros and rows (6.4 TB/s in all). Small ones by the sort's latency, which is that of its passes and not of its
+// tokens: 20011 x 1027 fp32 into 5003 rows take 44 us, the sort (two passes) 17 of them beside the zeros, the
+// chunks' sums 19 and their joining 12. Equal ids in a row cost nothing more, nor do ids that are all the same.
 #include <algorithm>
 
 #include "row_ops.h"
@@ -56,8 +60,9 @@ __device__ __forceinline__ void source_row(const EmbeddingLaunch& p, int64_t i, 
   dst = static_cast<TO*>(p.out) + i * p.ld_out;
 }
 
-// `tpr` threads take two tokens, so that twice as much is on its way. Bound by memory: each row is read once (a
-// row that several tokens name comes from L2 again) and the output is written once.
+// `tpr` threads take two tokens, so that twice as much is on its way (16384 x 4096 fp32 to bf16: 43 us with one, 41
+// with two). Bound by memory: each row is read once (a row that several tokens name comes from L2 again) and the output
+// is written once: 16384 x 4096 bf16 out of 128256 rows 35 us, 5.4 TB/s. A single token is bound by the launch.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaunch p) {
   ptx::griddep_launch_dependents();
@@ -89,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) embedding_kernel(const EmbeddingLaun
 // Rows that do not start on 16 bytes, or are not whole granules. The output is written in 16-byte granules at
 // aligned addresses; a granule's elements begin anywhere in the table's row, so the aligned 16-byte words
 // around them are read and shifted. Where those would reach beyond the row, and in the up to 2 (E - 1) elements
-// beside the granules, single elements are read.
+// beside the granules, single elements are read. (8193 x 8191 bf16: 41 us, 4.7 TB/s; 87 with single elements.)
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kThreads) embedding_shift_kernel(const EmbeddingLaunch p) {
   constexpr int E = 16 / sizeof(TO), BYTES = E * sizeof(TI), LOADS = (BYTES + 15) / 16 + 1, WORDS = LOADS * 4;
@@ -172,7 +177,10 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
 
 // Radix sort of the tokens, least significant digit first, by the CTAs of one cluster. Every warp holds a
 // run of consecutive tokens; a token's place is the number of tokens with a smaller digit, plus those with
-// the same digit in earlier CTAs, earlier warps and earlier in its warp, so equal ids keep their order.
+// the same digit in earlier CTAs, earlier warps and earlier in its warp, so equal ids keep their order. Bound by
+// the latency of a pass, about 8 us: its tokens' loads, two barriers of the cluster, and the chains of shared
+// memory between them. Digits have up to 9 bits, as few passes as that allows and of equal width: two of 9 bits for
+// 128256 rows, two of 7 for 5003. Eight CTAs are the largest cluster of a portable size.
 __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
   const int digits = 1 << p.digit_bits;
   uint32_t* count = smem;                               // [warp][digit]
@@ -310,7 +318,8 @@ __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const Embe
 
 // A group of `tpr` threads adds the rows of one chunk over tpr * kCols consecutive columns, kAhead rows loaded at a
 // time. With 16-byte rows (VEC) a thread holds consecutive columns, one 16-byte load of a row; otherwise a warp
-// holds 32 * kCols consecutive columns and a thread every 32nd of them.
+// holds 32 * kCols consecutive columns and a thread every 32nd of them, so that a warp's loads lie side by side
+// (20011 x 1027 fp32: 44 us; with a thread's columns consecutive 61).
 template <typename TG, bool VEC>
 struct Columns;
 
@@ -367,7 +376,8 @@ __device__ __forceinline__ void store_columns(float* dst, const float (&acc)[COL
   }
 }
 
-// Rows of this many chunks' heads or more are listed, to be joined by more threads.
+// Rows of this many chunks' heads or more are listed, to be joined by more threads: a warp of the short rows' adds
+// them eight at a time, one after the other.
 constexpr int kLongSpan = 32;
 
 template <typename TG, bool VEC>
@@ -547,7 +557,9 @@ bool aligned16(const void* p, int64_t ld, size_t elem) {
 
 // How the sums by chunk are split: threads per row, and tokens per chunk. Short chunks spread few tokens over
 // many SMs; long ones leave fewer sums in the workspace (a chunk writes two fp32 rows of them at worst). So
-// chunks are 16 tokens long, and longer once that still leaves a CTA for each of 1024 places (about 7 per SM).
+// chunks are 16 tokens long, and longer once that still leaves a CTA for each of 1024 places (about 7 per SM). A
+// slice of the columns is a CTA's at most, and all slices are alike: 1027 fp32 columns, off 16 bytes, are one of 160
+// threads.
 void split_tokens(EmbeddingGradLaunch& p) {
   const int cols = p.vec ? (p.grad_dtype == 1 ? Columns<__nv_bfloat16, true>::kCols : Columns<float, true>::kCols)
                          : Columns<float, false>::kCols;

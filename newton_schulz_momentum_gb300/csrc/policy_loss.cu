@@ -7,10 +7,15 @@
 //   d(loss)/dx = c / T (onehot(a) - softmax(z)).
 // A row of weight 0 or with a negative token is not read: its terms and gradient are 0.
 //
-// Bound by memory: c needs the whole row's sum before the first element of the gradient, and a row of a large
-// vocabulary is more than an SM holds (128256 bf16: 257 KB), so the row is split over the CTAs of a cluster. It
-// waits in their shared memory while they join their sums, and is read and written once. A row of up to 18 KB is
-// one warp's; beyond the cluster's memory a row is read twice.
+// c needs the whole row's sum before the first element of the gradient, and a row of a large vocabulary is more
+// than an SM holds (128256 bf16: 257 KB), so the row is split over the CTAs of a cluster. It waits in their shared
+// memory while they join their sums, and is read and written once: 4 bytes a bf16 element, 8 an fp32 one. A row of
+// up to 18 KB is one warp's; beyond the cluster's memory a row is read twice.
+//
+// Bounds: fp32 by memory (8388 x 32001: 333 us, 6.0 TB/s), bf16 by the instructions of two exponentials and four
+// conversions per two bytes beside it (8192 x 128256: 734 us, 5.4 TB/s; 2092 x 128256 without a gradient 139 us,
+// 3.9 TB/s). Short rows by the row itself: about 500 instructions of each warp that has a share in it
+// (536870 x 500 bf16: 530 us, 2.0 TB/s). A few rows by latency: 8 x 128256 bf16 15.6 us.
 //
 // Memory is read and written in 16-byte granules at aligned addresses, wherever a row starts; the sum runs over
 // groups of as many elements counted from the row's first one. So its order goes by the vocabulary alone: a row
@@ -304,9 +309,9 @@ __device__ __forceinline__ Cut cut_row(const T* x, int vocab) {
 
 // ---------------------------------------------------------------------------- rows in shared memory
 
-constexpr int kRingSlots = 3;          // of a warp: one being loaded, one worked on, one being written
-constexpr int kBatch = 4;
-constexpr int kSlotBytes = 4608;       // of a warp that shares a row
+constexpr int kRingSlots = 3;     // of a warp: one being loaded, one worked on, one being written
+constexpr int kBatch = 4;         // granules of a lane at a time
+constexpr int kSlotBytes = 4608;  // of a warp that shares a row: two CTAs' slots fill an SM's shared memory
 constexpr int kWarpGroups = kSlotBytes / 16 - 2;  // beside the rest of the first granule, and the one read past the last
 constexpr int kMaxCluster = 16;
 // Rows whose sums are on their way or being read, of those that are read at all. A warp sends its sum of the
@@ -314,8 +319,10 @@ constexpr int kMaxCluster = 16;
 // (n - 4)-th, whose place the n-th takes.
 constexpr int kJoins = 4;
 
-// Who takes a row: one warp; a cluster of a portable size, two CTAs per SM; or, for rows beyond eight of
-// those, a cluster of CTAs twice as large.
+// Who takes a row: one warp, as long as four warps' slots fit an SM (33554 x 8000 bf16: 243 us, shared by a cluster
+// 417; 32772 x 8191: 278 and 757); a cluster of a portable size, two CTAs of 256 threads per SM (8192 x 128256 bf16:
+// 912 us when one CTA of 512 took 1135, and two of 128 952); or, for rows beyond eight of those, a cluster of CTAs
+// twice as large (1024 x 262144 bf16: 221 us, 4.9 TB/s).
 enum RingMode { kSolo, kShared, kWide };
 
 template <int MODE>
@@ -370,11 +377,11 @@ __device__ __forceinline__ int token_of(const PolicyLaunch& p, uint32_t word, in
 }
 
 // A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it (kSolo: every warp rows
-// of its own). The warps work by themselves: bulk copies bring a share's whole granules into the warp's slots and take their gradients, formed
-// in place, out; up to E - 1 elements on either side of them go through registers. Where they meet is the
-// row's sum: every warp sends its own to every CTA of the cluster, and goes on when all have arrived. (With
-// barriers over the cluster and the CTA in their place, a third of the warps' time went into those and the
-// fences they imply.)
+// of its own). The warps work by themselves: bulk copies bring a share's whole granules into the warp's slots and
+// take their gradients, formed in place, out; up to E - 1 elements on either side of them go through registers.
+// Where they meet is the row's sum: every warp sends its own to every CTA of the cluster, forms its sum of the next
+// row, and goes on when all have arrived. (With barriers over the cluster and the CTA in their place, 38% of the
+// warps' time went into those and the fences they imply.)
 // EDGES: shares that are not whole granules.
 template <typename T, int MODE, bool EDGES>
 __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) policy_ring_kernel(const PolicyLaunch p) {
@@ -645,7 +652,8 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
 
 constexpr int kTwiceThreads = 512;
 
-// One CTA per row: rows beyond a cluster's shared memory.
+// One CTA per row: rows beyond a cluster's shared memory (292000 fp32, 585000 bf16 elements). Each thread keeps its
+// own maximum and sum, element by element (256 x 600000 fp32: 804 us, 1.4 TB/s, against 4.8 for rows that fit).
 template <typename T>
 __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const PolicyLaunch p) {
   __shared__ MaxSum part[kTwiceThreads / 32];

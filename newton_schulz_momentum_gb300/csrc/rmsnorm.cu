@@ -8,8 +8,8 @@
 // Backward, for the stored h: with d = dy * gain,
 //   dx = dh + rho d - h rho^3 / dim * sum(d h),   dgain = sum over rows of dy h rho.
 //
-// Both are bound by memory: each element is read once and written once. A row is held in the registers of
-// `tpr` threads, K 16-byte granules of it in each, so one read serves the sums and the outputs. Rows need not
+// Each element is read once and written once. A row is held in the registers of `tpr` threads, K 16-byte granules
+// of it in each, so one read serves the sums and the outputs. Rows need not
 // start on 16 bytes: granules are cut where the addresses are aligned, and the up to 2 (E - 1) elements before
 // and behind them are held one per thread. CTAs stay and take every (gridDim.x * rows per CTA)-th row, a multiple
 // of 8, so all rows of a thread start at the same offset from 16 bytes whatever their length: its columns, and
@@ -18,6 +18,13 @@
 // The forward sum has one order for every layout: thread t of sum_threads adds groups of E elements t,
 // t + sum_threads, ... counted from the row's first element, then the threads join. Rows that are not whole
 // granules pass through shared memory for it, so a value's bits do not depend on where it lies.
+//
+// Bounds. Rows of whole granules: memory, forward at 16384 x 4096 bf16 85 us (6.3 TB/s), fp32 171 (6.3), backward
+// 93 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
+// 121 us (4.4 TB/s), fp32 180 (6.0), backward 116 (4.6) and 169 (6.3). 8-bit outputs: the chain from the row's sum
+// over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 100 us (4.7
+// TB/s), 3001 x 8200 fp32 72 (4.5); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
+// 219 (2.2). One row: latency, about 7 us, and the launch.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -164,7 +171,8 @@ __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[
 // (1048576 x 64 bf16: 92 us with three, 84 with four), three and two where there is more to hold (65344 x 1027
 // bf16: 126 us with three, 148 with four).
 template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
-__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3) : K > 1 ? 3 : 4) : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
+__global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3) : K > 1 ? 3 : 4)
+                                                : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
     add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   constexpr int E = kPer<T>;
   __shared__ float red[2][32][1];
@@ -395,7 +403,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E], acc_edge = 0.f;
   const float gain_edge = edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
   // Without REGS a thread's sums, then its gains: four columns at [quarter][granule], so that a warp's accesses do
-  // not conflict. Aligned gains of a small CTA are LOADED from memory at each use, which leaves L1 its space.
+  // not conflict. Aligned gains of a small CTA are LOADED from memory at each use, which leaves L1 its space: in a larger
+// one, alone on its SM, there is room for them.
   constexpr bool LOADED = !EDGES && THREADS <= 256;
   const int granules = K * tpr;
   float4* sums = reinterpret_cast<float4*>(dyn);
@@ -588,8 +597,8 @@ __global__ void __launch_bounds__(kMaxThreads) rmsnorm_dgain_kernel(const RmsNor
 
 // ---------------------------------------------------------------------------- the longest rows
 
-// One CTA per row, each element read again for every use: rows beyond what registers hold, and arrays that
-// start at different offsets from 16 bytes.
+// One CTA per row, each element read again for every use: rows beyond what registers hold (3000 x 20000 bf16: 133 us
+// forward, 427 backward), and arrays that start at different offsets from 16 bytes, whose granules no one cut fits.
 template <typename T>
 __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormLaunch p) {
   __shared__ float red[2][32][1];
@@ -698,7 +707,7 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_columns_kernel(const RmsNorm
 
 // ---------------------------------------------------------------------------- launches
 
-constexpr int kMaxHeld = 16384;  // elements of a row held in registers
+constexpr int kMaxHeld = 16384;    // elements of a row held in registers: 32 or 16 by 512 or 1024 threads
 constexpr int kColumnSplits = 32;  // stretches of rows of rmsnorm_columns_kernel
 
 // A row's arrays and their strides, to see whether their granules coincide.
@@ -813,6 +822,7 @@ cudaError_t launch_held_norm(RmsNormLaunch& p, int each, int sms, cudaStream_t s
     if (each == kHeld && p.sum_threads > 256) return launch_rows<T, kHeld, FP8, kHugeThreads, false, EDGES>(p, sms, stream);
   }
   if (each == kHeld) return launch_rows<T, kHeld, FP8, 256, true, EDGES>(p, sms, stream);
+  // Two CTAs of up to 320 threads fit an SM; rows for more are alone on it.
   if (p.sum_threads <= 320) return launch_rows<T, kLong, FP8, 320, false, EDGES>(p, sms, stream);
   return launch_rows<T, kLong, FP8, 512, false, EDGES>(p, sms, stream);
 }
@@ -835,7 +845,8 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, PER_SM, REGS, AHEAD, EDGES>;
   // Sums of long rows, or the line in which a CTA's short rows join.
   const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
-  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) : static_cast<size_t>(K) * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2);
+  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0)
+                           : static_cast<size_t>(K) * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2);
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
