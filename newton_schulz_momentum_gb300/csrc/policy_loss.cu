@@ -320,18 +320,19 @@ constexpr int kMaxCluster = 16;
 constexpr int kJoins = 4;
 
 // Who takes a row: one warp, as long as four warps' slots fit an SM (33554 x 8000 bf16: 243 us, shared by a cluster
-// 417; 32772 x 8191: 278 and 757); a cluster of a portable size, two CTAs of 256 threads per SM (8192 x 128256 bf16:
-// 912 us when one CTA of 512 took 1135, and two of 128 952); or, for rows beyond eight of those, a cluster of CTAs
+// 417; 32772 x 8191: 278 and 757); a cluster of a portable size, of CTAs of 128 threads, four per SM (33554 x 8000
+// fp32: 316 us, with 256 threads 437; 13421 x 20000 bf16 225 and 281), or of 256, two per SM (8192 x 128256 bf16: 912
+// us when one CTA of 512 took 1135, and four of 128 952); or, for rows beyond eight of those, a cluster of CTAs
 // twice as large (1024 x 262144 bf16: 221 us, 4.9 TB/s).
-enum RingMode { kSolo, kShared, kWide };
+enum RingMode { kSolo, kSmall, kShared, kWide };
 
 template <int MODE>
 struct Ring {
-  static constexpr int kThreads = MODE == kSolo ? 128 : MODE == kShared ? 256 : 512;
-  static constexpr int kPerSm = MODE == kSolo ? 4 : MODE == kShared ? 2 : 1;
+  static constexpr int kThreads = MODE == kSolo || MODE == kSmall ? 128 : MODE == kShared ? 256 : 512;
+  static constexpr int kPerSm = 512 / kThreads;
   static constexpr int kWarps = kThreads / 32;
   static constexpr int kSmem = kWarps * kRingSlots * kSlotBytes + 128;
-  static constexpr int kCluster = MODE == kSolo ? 1 : MODE == kShared ? 8 : kMaxCluster;  // CTAs per row at most
+  static constexpr int kCluster = MODE == kSolo ? 1 : MODE == kWide ? kMaxCluster : 8;  // CTAs per row at most
 };
 constexpr int kSoloSlotBytes = 18432;  // the most for which four warps' slots fit an SM
 
@@ -735,33 +736,57 @@ cudaError_t resident_clusters(int dev, int size, int* clusters) {
 // A warp's time for a row beside its granules, in granules (about 500 instructions to 65 for 32 of them).
 constexpr int kRowCost = 256;
 
-// Whether a row fits the shared memory of a cluster that fits the GPU; if so, launches. Of the cluster sizes
-// that hold a row, the one that brings the most rows through: clusters at once over time per row. (Larger ones
-// leave fewer SMs over at times, but each of their warps pays for the row again.)
+// How rows are shared among clusters: the way that brings the most of them through.
+struct RingChoice {
+  int mode = 0, cluster = 0, clusters = 0;
+  double rate = 0.0;  // clusters at once over time per row
+};
+
+// The cluster sizes of one mode that hold a row and fit the GPU. (Larger ones leave fewer SMs over at times, but each
+// of their warps pays for the row again.)
 template <typename T, int MODE, bool EDGES>
-cudaError_t launch_ring(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
+cudaError_t consider(RingChoice& best, int dev, int64_t vocab) {
   using R = Ring<MODE>;
   constexpr int E = 16 / sizeof(T);
-  *launched = false;
   constexpr int64_t per_cta = R::kWarps * kWarpGroups;
   // Two CTAs at least: the sums travel by asynchronous stores, which only a cluster launch has.
-  const int64_t groups = (p.vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
-  if (least > R::kCluster) return cudaSuccess;
-  int dev = 0, best = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  double most = 0.0;
-  for (int size = static_cast<int>(least); e == cudaSuccess && size <= R::kCluster; ++size) {
+  const int64_t groups = (vocab + E - 1) / E, least = std::max<int64_t>(2, (groups + per_cta - 1) / per_cta);
+  for (int64_t size = least; size <= R::kCluster; ++size) {
     int n = 0;
-    e = resident_clusters<T, MODE, EDGES>(dev, size, &n);
+    const cudaError_t e = resident_clusters<T, MODE, EDGES>(dev, static_cast<int>(size), &n);
+    if (e != cudaSuccess) return e;
     const double rate = n / (kRowCost + static_cast<double>(groups) / (size * R::kWarps));
-    if (e == cudaSuccess && rate > most) most = rate, best = n, p.cluster = size;
+    // Small CTAs where they gain something: more of them meet for a row (8388 x 32001 fp32: 333 us by four CTAs of 256
+    // threads, 354 by seven of 128, at almost equal rates).
+    if (rate > best.rate * (MODE == kSmall ? 1.05 : 1.0)) best = {MODE, static_cast<int>(size), n, rate};
   }
-  if (e != cudaSuccess || best == 0) return e;
-  *launched = true;
+  return cudaSuccess;
+}
+
+template <typename T, int MODE, bool EDGES>
+cudaError_t launch_ring(PolicyLaunch& p, const RingChoice& c, cudaStream_t stream) {
+  using R = Ring<MODE>;
   p.slot_bytes = kSlotBytes;
-  p.terms = std::min<int64_t>(p.n, best);
+  p.cluster = c.cluster;
+  p.terms = std::min<int64_t>(p.n, c.clusters);
   const unsigned ctas = static_cast<unsigned>(p.terms * p.cluster);
   return row::launch(policy_ring_kernel<T, MODE, EDGES>, dim3(ctas), R::kThreads, R::kSmem, stream, p, p.cluster);
+}
+
+// Whether a row fits the shared memory of a cluster; if so, launches.
+template <typename T, bool EDGES>
+cudaError_t launch_shared(PolicyLaunch& p, cudaStream_t stream, bool* launched) {
+  int dev = 0;
+  RingChoice best;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = consider<T, kShared, EDGES>(best, dev, p.vocab);
+  if (e == cudaSuccess) e = consider<T, kSmall, EDGES>(best, dev, p.vocab);
+  if (e == cudaSuccess && best.cluster == 0) e = consider<T, kWide, EDGES>(best, dev, p.vocab);
+  *launched = e == cudaSuccess && best.cluster > 0;
+  if (!*launched) return e;
+  return best.mode == kSmall ? launch_ring<T, kSmall, EDGES>(p, best, stream)
+       : best.mode == kShared ? launch_ring<T, kShared, EDGES>(p, best, stream)
+                              : launch_ring<T, kWide, EDGES>(p, best, stream);
 }
 
 template <typename T, bool EDGES>
@@ -799,9 +824,7 @@ cudaError_t launch_rows(PolicyLaunch& p, int sms, cudaStream_t stream) {
     return edges ? launch_solo<T, true>(p, sms, stream) : launch_solo<T, false>(p, sms, stream);
   }
   bool launched = false;
-  cudaError_t e = edges ? launch_ring<T, kShared, true>(p, stream, &launched) : launch_ring<T, kShared, false>(p, stream, &launched);
-  if (e == cudaSuccess && !launched)
-    e = edges ? launch_ring<T, kWide, true>(p, stream, &launched) : launch_ring<T, kWide, false>(p, stream, &launched);
+  const cudaError_t e = edges ? launch_shared<T, true>(p, stream, &launched) : launch_shared<T, false>(p, stream, &launched);
   if (e != cudaSuccess || launched) return e;
   p.terms = p.n;
   return row::launch(policy_twice_kernel<T>, dim3(static_cast<unsigned>(p.n)), kTwiceThreads, 0, stream, p);
