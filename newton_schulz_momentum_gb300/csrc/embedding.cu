@@ -1,7 +1,8 @@
 // Embedding lookup with scaling, out[i, :] = scale * table[id_i, :], and its gradient,
 // grad[v, :] = scale * sum over the tokens i with id_i = v of grad_out[i, :], added in the order of i.
 //
-// The gradient takes four launches:
+// The gradient of up to kDirectTokens tokens takes two launches: zeros, then a CTA per token that adds its row's tokens
+// unless an earlier one of them does. Of more tokens, four:
 //   1. one cluster sorts the tokens by id (stable);
 //   2. meanwhile, on the other SMs, the table is filled with zeros, which at a language model's sizes is most
 //      of the bytes (not run where the caller adds to the gradient);
@@ -292,6 +293,7 @@ constexpr int64_t kZeroBlock = int64_t(kZeroThreads) * kZeroPer * 4;  // element
 // close together: 2.1 GB take 270 us (7.8 TB/s), against 312-323 us for CTAs that stay and walk over it.
 __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const EmbeddingGradLaunch p) {
   ptx::griddep_launch_dependents();
+  if (p.direct) ptx::griddep_wait();  // no sort has waited for the work before
   // Rows that follow one another are one long row.
   const bool flat = p.ld_grad == p.dim;
   const int64_t len = flat ? p.rows * p.dim : p.dim;
@@ -310,8 +312,63 @@ __global__ void __launch_bounds__(kZeroThreads) embedding_zero_kernel(const Embe
   } else {
     for (int64_t c = begin + threadIdx.x; c < end; c += kZeroThreads) __stcs(dst + c, 0.f);
   }
-  // The next launch waits for this one, and needs the sort's result.
+  // The next launch waits for this one, and may need the sort's result.
   ptx::griddep_wait();
+}
+
+// ---------------------------------------------------------------------------- few tokens
+
+constexpr int kDirectTokens = kThreads;  // a thread looks at each
+constexpr int kDirectCols = 2;           // of a thread, kThreads apart
+constexpr int kDirectAhead = 16;         // rows loaded at a time
+
+// A CTA per token and 512 columns. The first token of an id adds that id's rows, in the tokens' order; the others'
+// CTAs end. Bound by latency: the ids, then its rows 16 at a time: 256 x 8000 fp32 into 2000 rows 26 us, 28 by the sort's
+// way; 256 x 300 bf16 18, 22; at worst, 256 tokens all alike, 23, 22.
+template <typename TG>
+__global__ void __launch_bounds__(kThreads) embedding_direct_kernel(const EmbeddingGradLaunch p) {
+  __shared__ unsigned same_of[kThreads / 32];
+  __shared__ int list[kDirectTokens];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, me = static_cast<int>(blockIdx.x);
+  const uint32_t key = sort_key(p, me);
+  const unsigned same = __ballot_sync(0xffffffffu, t < p.n && sort_key(p, t) == key);
+  if (lane == 0) same_of[warp] = same;
+  __syncthreads();
+  if (key == static_cast<uint32_t>(p.rows)) return;
+  int before = 0, count = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += __popc(same_of[w]);
+    if (w == me / 32 && same_of[w] & ((1u << (me % 32)) - 1)) return;
+    if (w < me / 32 && same_of[w]) return;
+    count += __popc(same_of[w]);
+  }
+  if ((same >> lane) & 1u) list[before + __popc(same & ((1u << lane) - 1))] = t;
+  __syncthreads();
+  const int64_t col = static_cast<int64_t>(blockIdx.y) * (kThreads * kDirectCols) + t;
+  const TG* src = static_cast<const TG*>(p.grad_out) + col;
+  float acc[kDirectCols] = {};
+  for (int i = 0; i < count; i += kDirectAhead) {
+    TG v[kDirectAhead][kDirectCols];
+#pragma unroll
+    for (int a = 0; a < kDirectAhead; ++a)
+#pragma unroll
+      for (int k = 0; k < kDirectCols; ++k)
+        v[a][k] = i + a < count && col + k * kThreads < p.dim ? __ldcs(src + list[i + a] * p.ld_grad_out + k * kThreads)
+                                                              : row::from_f<TG>(0.f);
+#pragma unroll
+    for (int a = 0; a < kDirectAhead; ++a)
+#pragma unroll
+      for (int k = 0; k < kDirectCols; ++k) acc[k] += row::to_f(v[a][k]);
+  }
+  float* dst = p.grad + static_cast<int64_t>(key) * p.ld_grad + col;
+#pragma unroll
+  for (int k = 0; k < kDirectCols; ++k)
+    if (col + k * kThreads < p.dim) {
+      float* at = dst + k * kThreads;
+      *at = fmaf(p.scale, acc[k], p.accumulate ? *at : 0.f);
+    }
 }
 
 // ---------------------------------------------------------------------------- 3. sums by chunk
@@ -597,6 +654,8 @@ cudaError_t launch_embedding(EmbeddingLaunch& p, cudaStream_t stream) {
 
 int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws) {
   p.vec_grad = aligned16(p.grad, p.ld_grad, sizeof(float));
+  p.direct = p.n <= kDirectTokens;
+  if (p.direct) return 0;
   p.vec = p.vec_grad && p.dim % (p.grad_dtype == 1 ? 8 : 4) == 0 &&
           aligned16(p.grad_out, p.ld_grad_out, p.grad_dtype == 1 ? 2 : 4);
   split_tokens(p);
@@ -615,7 +674,23 @@ int64_t embedding_grad_workspace(EmbeddingGradLaunch& p, char* ws) {
   return off;
 }
 
+cudaError_t launch_embedding_zeros(const EmbeddingGradLaunch& p, cudaStream_t stream) {
+  const bool flat = p.ld_grad == p.dim;
+  const int64_t len = flat ? p.rows * p.dim : p.dim;
+  const int64_t blocks = (len + kZeroBlock - 1) / kZeroBlock * (flat ? 1 : p.rows);
+  if (blocks >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;
+  return row::launch(embedding_zero_kernel, dim3(static_cast<unsigned>(blocks)), kZeroThreads, 0, stream, p);
+}
+
 cudaError_t launch_embedding_grad(EmbeddingGradLaunch& p, int sms, cudaStream_t stream) {
+  if (p.direct) {
+    const cudaError_t e = p.accumulate ? cudaSuccess : launch_embedding_zeros(p, stream);
+    if (e != cudaSuccess || p.n == 0) return e;
+    constexpr int64_t slice = kThreads * kDirectCols;
+    const dim3 grid(static_cast<unsigned>(p.n), static_cast<unsigned>((p.dim + slice - 1) / slice));
+    return row::launch(p.grad_dtype == 0 ? embedding_direct_kernel<float> : embedding_direct_kernel<__nv_bfloat16>, grid,
+                       kThreads, 0, stream, const_cast<const EmbeddingGradLaunch&>(p));
+  }
   int bits = 1;
   while ((int64_t(1) << bits) <= p.rows) ++bits;  // keys go up to `rows`
   p.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
@@ -625,14 +700,8 @@ cudaError_t launch_embedding_grad(EmbeddingGradLaunch& p, int sms, cudaStream_t 
   if (e != cudaSuccess) return e;
   e = row::launch(embedding_sort_kernel, dim3(kSortCtas), kSortThreads, kSortSmem, stream, p);
   if (e != cudaSuccess) return e;
-  if (!p.accumulate) {
-    const bool flat = p.ld_grad == p.dim;
-    const int64_t len = flat ? p.rows * p.dim : p.dim;
-    const int64_t blocks = (len + kZeroBlock - 1) / kZeroBlock * (flat ? 1 : p.rows);
-    if (blocks >= int64_t(1) << 31) return cudaErrorInvalidConfiguration;
-    e = row::launch(embedding_zero_kernel, dim3(static_cast<unsigned>(blocks)), kZeroThreads, 0, stream, p);
-  }
-  if (e != cudaSuccess || p.n == 0) return e;
+  if (!p.accumulate) e = launch_embedding_zeros(p, stream);
+  if (e != cudaSuccess) return e;
   if (p.grad_dtype == 0)
     e = p.vec ? launch_chunks<float, true>(p, stream) : launch_chunks<float, false>(p, stream);
   else

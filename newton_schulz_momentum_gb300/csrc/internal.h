@@ -333,7 +333,8 @@ struct EmbeddingGradLaunch {
   int64_t ld_grad;
   int accumulate;
   unsigned* status;
-  // Set by embedding_grad_workspace.
+  // Set by embedding_grad_workspace. direct: few tokens, added without a sort and without a workspace.
+  int direct;
   int64_t chunk_len, chunks;  // the sorted tokens are summed in `chunks` runs of chunk_len
   uint2* sorted[2];           // (id, position) of every token by id; the sort ends in sorted[0]
   int* chunk_state;
