@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
   // For a group that is not within a warp, the largest |y| of each (as bits, which order as the values do),
   // alternating between two halves. Then a row of bytes. Then h in the order of its elements, a word left out
   // after every 32, so that lanes E elements apart use different banks.
+  const int group_bits = p.group ? 31 - __clz(static_cast<int>(p.group)) : 30;  // log2 of a group, longer than the row without
   const int parts = FP8 ? p.parts : 0, top_bytes = FP8 && p.lanes == 0 ? (2 * rows * parts * 4 + 15) / 16 * 16 : 0;
   unsigned* tops = reinterpret_cast<unsigned*>(dyn);
   uint8_t* bytes = dyn + top_bytes + slot * p.stage;
@@ -309,7 +310,6 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
         if (edge >= 0) y[edge] = row::from_f<T>(ve * rho * gain_edge);
       }
     } else {
-      const int group = p.group ? static_cast<int>(p.group) : 1 << 30;
       unsigned* top = tops + (half * rows + slot) * parts;
       float most[K];  // of the granule, then of its group
 #pragma unroll
@@ -329,13 +329,13 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
       for (int k = 0; k < K; ++k) {
         for (int o = lanes / 2; o > 0; o >>= 1) most[k] = max_nan(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
         if (p.lanes == 0 && i < p.n && first_out(k) < dim && (threadIdx.x & 31) == 0)
-          atomicMax(top + first_out(k) / group, __float_as_uint(most[k]));
+          atomicMax(top + (first_out(k) >> group_bits), __float_as_uint(most[k]));
       }
       if (p.lanes == 0) {
         row_sync(tpr);
 #pragma unroll
         for (int k = 0; k < K; ++k)
-          if (first_out(k) < dim) most[k] = __uint_as_float(top[first_out(k) / group]);
+          if (first_out(k) < dim) most[k] = __uint_as_float(top[first_out(k) >> group_bits]);
         for (int k = t; k < parts; k += tpr) {
           if (i < p.n) p.scales[i * parts + k] = scale_of(top[k]);
           tops[((half ^ 1) * rows + slot) * parts + k] = 0;  // for the next row; its readers are a barrier behind
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
         const int e0 = first_out(k);
         if (i >= p.n || e0 >= dim) continue;
         const float scale = scale_of(__float_as_uint(most[k]));
-        if (p.lanes && t % p.lanes == 0) p.scales[i * parts + e0 / group] = scale;
+        if (p.lanes && (t & (p.lanes - 1)) == 0) p.scales[i * parts + (e0 >> group_bits)] = scale;
         uint32_t w[E / 4];
         pack_fp8(w, v[k], reciprocal(scale));
         uint8_t* to = p.stage ? bytes + e0 : q + e0;
