@@ -22,9 +22,9 @@
 // Bounds. Rows of whole granules: memory, forward at 16384 x 4096 bf16 85 us (6.3 TB/s), fp32 171 (6.3), backward
 // 93 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
 // 121 us (4.4 TB/s), fp32 180 (6.0), backward 116 (4.6) and 169 (6.3). 8-bit outputs: the chain from the row's sum
-// over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 100 us (4.7
-// TB/s), 3001 x 8200 fp32 72 (4.5); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
-// 219 (2.2). One row: latency, about 7 us, and the launch.
+// over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 85 us (5.6
+// TB/s), 3001 x 8200 fp32 59 (5.4); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
+// 185 (2.6). One row: latency, 4 us on the device, and the launch.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -324,13 +324,14 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
 #pragma unroll
         for (int k = 1; k < K; ++k) most[k] = most[0];
       }
-      const int lanes = p.lanes ? p.lanes : 32;  // a group's, or a part of it
+      for (int o = (p.lanes ? p.lanes : 32) / 2; o > 0; o >>= 1)  // a group's lanes, or a part of them
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        for (int o = lanes / 2; o > 0; o >>= 1) most[k] = max_nan(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
-        if (p.lanes == 0 && i < p.n && first_out(k) < dim && (threadIdx.x & 31) == 0)
-          atomicMax(top + (first_out(k) >> group_bits), __float_as_uint(most[k]));
-      }
+        for (int k = 0; k < K; ++k) most[k] = max_nan(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+      if (p.lanes == 0)
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+          if (i < p.n && first_out(k) < dim && (threadIdx.x & 31) == 0)
+            atomicMax(top + (first_out(k) >> group_bits), __float_as_uint(most[k]));
       if (p.lanes == 0) {
         row_sync(tpr);
 #pragma unroll
@@ -358,21 +359,24 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
       }
       if (p.stage) {
         row_sync(tpr);
-        // The row goes out by 16-byte addresses; what lies there begins between words of the bytes.
-        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q) & 15);
-        if (i < p.n)
-          for (int lo = t * 16 - at; lo < dim; lo += tpr * 16) {
-            if (lo >= 0 && lo + 16 <= dim) {
-              const uint32_t* from = reinterpret_cast<const uint32_t*>(bytes) + (lo >> 2);
-              const int bits = (lo & 3) * 8;
-              uint4 o;
-              o.x = __funnelshift_r(from[0], from[1], bits), o.y = __funnelshift_r(from[1], from[2], bits);
-              o.z = __funnelshift_r(from[2], from[3], bits), o.w = __funnelshift_r(from[3], from[4], bits);
-              __stcs(reinterpret_cast<uint4*>(q + lo), o);
-            } else {
-              for (int b = max(lo, 0); b < min(lo + 16, dim); ++b) q[b] = bytes[b];
-            }
+        // The row goes out by 16-byte addresses, what lies there beginning between words of the bytes; up to 15 bytes
+        // on either side one per thread.
+        const int head = min(static_cast<int>((0 - reinterpret_cast<uintptr_t>(q)) & 15), dim), whole = (dim - head) >> 4;
+        if (i < p.n) {
+#pragma unroll 1
+          for (int c = t; c < whole; c += tpr) {
+            const int lo = head + 16 * c, bits = (lo & 3) * 8;
+            const uint32_t* from = reinterpret_cast<const uint32_t*>(bytes) + (lo >> 2);
+            uint4 o;
+            o.x = __funnelshift_r(from[0], from[1], bits), o.y = __funnelshift_r(from[1], from[2], bits);
+            o.z = __funnelshift_r(from[2], from[3], bits), o.w = __funnelshift_r(from[3], from[4], bits);
+            __stcs(reinterpret_cast<uint4*>(q + lo), o);
           }
+#pragma unroll 1
+          for (int b = t; b < head; b += tpr) q[b] = bytes[b];
+#pragma unroll 1
+          for (int b = head + 16 * whole + t; b < dim; b += tpr) q[b] = bytes[b];
+        }
       }
     }
   }
@@ -805,10 +809,15 @@ cudaError_t launch_rows(RmsNormLaunch& p, int sms, cudaStream_t stream) {
 // Granules per thread: up to 64 granules a row is one warp's, so that it needs no barrier of the CTA (129 fp32
 // columns backward: 52 us with two warps, 31 with one); then CTAs of 256 threads as long as that is 16 elements
 // per thread. Beyond, fp32 rows of up to 2304 granules keep 16 elements per thread in CTAs of up to 576, two of
-// which fit an SM (3001 x 8200 to e4m3: 84 us with 32 elements, 76 with 16), and the rest 32 elements.
-template <typename T>
+// which fit an SM (3001 x 8200 to e4m3: 84 us with 32 elements, 76 with 16), and the rest 32 elements. 8-bit outputs
+// meet more often, so their rows are a warp's or two warps' for longer (67108 x 1000 to e4m3: bf16 95 us with one
+// granule a thread, 89 with four, fp32 173 and 139; but 65344 x 1027 bf16 200 and 236); and of fp32 rows just above
+// 128 granules a fifth warp would hold next to nothing (130308 x 515: 233 us with one, 171 with four).
+template <typename T, bool FP8>
 int granules_each(int granules) {
   constexpr int kHeld = sizeof(T) == 4 ? 4 : 2, kLong = sizeof(T) == 4 ? 8 : 4;
+  constexpr int kFours = sizeof(T) == 4 ? (FP8 ? 256 : 160) : FP8 ? 128 : 64;  // rows up to which four gain
+  if (granules > 64 && granules <= kFours) return 4;
   return granules <= 32 ? 1 : granules <= 64 ? 2 : granules <= 256 ? 1 : granules <= 512 ? 2
        : granules <= 256 * kHeld || (sizeof(T) == 4 && granules <= kHeld * kHugeThreads) ? kHeld : kLong;
 }
@@ -829,7 +838,7 @@ cudaError_t launch_held_norm(RmsNormLaunch& p, int each, int sms, cudaStream_t s
 
 template <typename T, bool FP8>
 cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
-  const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T>(granules);
+  const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T, FP8>(granules);
   p.sum_threads = std::min(row_threads(granules, each), kMaxThreads);
   p.inv_dim = 1.f / static_cast<float>(p.dim);  // the mean of the squares is within two units of the last place by it
   const Array x{p.x, p.ldx};
