@@ -169,9 +169,11 @@ __device__ __forceinline__ void pack_fp8(uint32_t (&w)[E / 4], const float (&v)[
 // too, 65344 x 1027 210 -> 182 us, and all others lose, 16384 x 4096 bf16 85 -> 91). EDGES: rows that are not
 // whole granules. CTAs of 256 threads that registers leave room for: four with one aligned granule a thread
 // (1048576 x 64 bf16: 92 us with three, 84 with four), three and two where there is more to hold (65344 x 1027
-// bf16: 126 us with three, 148 with four).
+// bf16: 126 us with three, 148 with four). Of longer rows one or two: fp32 rows with edges would spill at two (8183 x
+// 8201: 218 us with two, 192 with one; to e4m3 249 and 201).
 template <typename T, int K, bool FP8, int THREADS, bool HELD, bool EDGES>
 __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3) : K > 1 ? 3 : 4)
+                                                : EDGES && sizeof(T) == 4 ? 1
                                                 : THREADS <= 320 || THREADS == kHugeThreads ? 2 : 1)
     add_rmsnorm_rows_kernel(const RmsNormLaunch p) {
   constexpr int E = kPer<T>;
