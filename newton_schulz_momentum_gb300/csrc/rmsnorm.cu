@@ -410,10 +410,10 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   const float gain_edge = edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
   // Without REGS a thread's sums, then its gains: four columns at [quarter][granule], so that a warp's accesses do
   // not conflict. Aligned gains of a small CTA are LOADED from memory at each use, which leaves L1 its space: in a larger
-// one, alone on its SM, there is room for them.
+  // one, alone on its SM, there is room for them.
   constexpr bool LOADED = !EDGES && THREADS <= 256;
-  const int granules = K * tpr;
-  float4* sums = reinterpret_cast<float4*>(dyn);
+  const int granules = K * tpr, held = REGS ? 0 : E / 4 * granules * (LOADED ? 1 : 2);  // of a row
+  float4* sums = reinterpret_cast<float4*>(dyn) + slot * held;
   float4* gains = sums + E / 4 * granules;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   // This CTA's sums, one row of the workspace. The row slots of a CTA start at different offsets, so they join
   // by column, in their order.
   float* out = p.partials + static_cast<int64_t>(blockIdx.x) * p.dim;
-  float* line = reinterpret_cast<float*>(dyn);
+  float* line = reinterpret_cast<float*>(reinterpret_cast<float4*>(dyn) + rows * held);
   for (int turn = 0; turn < rows; ++turn) {
     if (rows > 1) __syncthreads();
     if (turn != slot) continue;
@@ -856,8 +856,8 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   auto* kernel = add_rmsnorm_grad_rows_kernel<T, K, THREADS, PER_SM, REGS, AHEAD, EDGES>;
   // Sums of long rows, or the line in which a CTA's short rows join.
   const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
-  const size_t smem = REGS ? (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0)
-                           : static_cast<size_t>(K) * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2);
+  const size_t smem = (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) +
+                      (REGS ? 0 : static_cast<size_t>(rows) * K * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2));
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -881,11 +881,13 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 //   (dim 6005); aligned rows the other way, 113 and 127 (dim 5000). To 1280 granules four in 320 threads 164 us, two in
 //   640 133 (dim 8201).
 // - fp32 beyond 2048 granules: four in 576 to 768 threads while that holds them (aligned, dim 10000: 181 us, 194 with
-//   eight in 416; with edges, dim 8201: 189, 224), but with edges beyond 2304 eight (dim 11003: 240 and 202).
+//   eight in 416; with edges, dim 8201: 189, 224), then eight in 512 (aligned, dim 16000: 175, 184 with four in 1024;
+//   with edges, dim 11003: 210, 253).
+// bf16 sums with edges lie in shared memory as of 33 granules (dim 515: 153 us in registers, 98; dim 4099 172 and 98).
 template <typename T, bool EDGES>
 cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
   if (granules <= 32) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if (granules <= 256 && !(EDGES && sizeof(T) == 4))
     return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
   if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
@@ -900,11 +902,10 @@ cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   if constexpr (sizeof(T) == 4) {
     if constexpr (EDGES) {
       if (granules <= 2304) return launch_grad_rows<T, 4, kHugeThreads, 1, false, false, EDGES>(p, granules, sms, stream);
-      if (granules <= 3328) return launch_grad_rows<T, 8, 416, 1, false, false, EDGES>(p, granules, sms, stream);
     } else {
       if (granules <= 3072) return launch_grad_rows<T, 4, 768, 1, false, false, EDGES>(p, granules, sms, stream);
     }
-    return launch_grad_rows<T, 4, 1024, 1, false, false, EDGES>(p, granules, sms, stream);
+    return launch_grad_rows<T, 8, 512, 1, false, false, EDGES>(p, granules, sms, stream);
   }
   return cudaErrorInvalidValue;  // kMaxHeld bf16 are 2048 granules
 }
