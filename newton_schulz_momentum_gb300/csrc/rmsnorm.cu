@@ -21,7 +21,7 @@
 //
 // Bounds. Rows of whole granules: memory, forward at 16384 x 4096 bf16 85 us (6.3 TB/s), fp32 171 (6.3), backward
 // 93 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
-// 121 us (4.4 TB/s), fp32 180 (6.0), backward 116 (4.6) and 169 (6.3). 8-bit outputs: the chain from the row's sum
+// 121 us (4.4 TB/s), fp32 180 (6.0), backward 111 (4.8) and 168 (6.4). 8-bit outputs: the chain from the row's sum
 // over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 85 us (5.6
 // TB/s), 3001 x 8200 fp32 59 (5.4); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
 // 185 (2.6). One row: latency, 4 us on the device, and the launch.
@@ -883,13 +883,14 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 // - fp32 beyond 2048 granules: four in 576 to 768 threads while that holds them (aligned, dim 10000: 181 us, 194 with
 //   eight in 416; with edges, dim 8201: 189, 224), then eight in 512 (aligned, dim 16000: 175, 184 with four in 1024;
 //   with edges, dim 11003: 210, 253).
-// bf16 sums with edges lie in shared memory as of 33 granules (dim 515: 153 us in registers, 98; dim 4099 172 and 98).
+// Sums of rows with edges lie in shared memory where that saves a spill or a CTA: with one granule (dim 129: bf16 110
+// us in registers, 102; fp32 183, 174) and of bf16 rows (dim 515: 153, 98; dim 4099 172, 98).
 template <typename T, bool EDGES>
 cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaStream_t stream) {
-  if (granules <= 32) return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 32) return launch_grad_rows<T, 1, 256, 3, !EDGES, true, EDGES>(p, granules, sms, stream);
   if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if (granules <= 256 && !(EDGES && sizeof(T) == 4))
-    return launch_grad_rows<T, 1, 256, EDGES ? 2 : 3, true, true, EDGES>(p, granules, sms, stream);
+    return launch_grad_rows<T, 1, 256, 3, !EDGES, true, EDGES>(p, granules, sms, stream);
   if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if constexpr (EDGES && sizeof(T) == 2) {
     if (granules <= 1024) return launch_grad_rows<T, 2, 512, 1, false, true, EDGES>(p, granules, sms, stream);
