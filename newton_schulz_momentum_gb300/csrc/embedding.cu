@@ -202,27 +202,32 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
       if (i >= p.n) return make_uint2(0xffffffffu, 0);
       return pass == 0 ? make_uint2(sort_key(p, i), static_cast<uint32_t>(i)) : __ldcg(in + i);
     };
-    // The first tokens stay in registers for the second look at them.
+    // The first tokens stay in registers for the second look at them, and which lanes have the same digit.
     uint2 held[kHeldTokens];
+    unsigned alike[kHeldTokens];
 #pragma unroll
     for (int s = 0; s < kHeldTokens; ++s) held[s] = s < steps ? token(first + s * 32 + lane) : make_uint2(0, 0);
+    auto digit = [&](int64_t i, const uint2& t) { return i < p.n ? (t.x >> shift) & (digits - 1) : 0xffffffffu; };
     auto count_one = [&](int64_t i, const uint2& t) {
-      const uint32_t d = i < p.n ? (t.x >> shift) & (digits - 1) : 0xffffffffu;
+      const uint32_t d = digit(i, t);
       const unsigned same = __match_any_sync(0xffffffffu, d);
       if (d != 0xffffffffu && lane == __ffs(same) - 1) mine[d] += __popc(same);
       __syncwarp();
+      return same;
     };
 #pragma unroll
     for (int s = 0; s < kHeldTokens; ++s)
-      if (s < steps) count_one(first + s * 32 + lane, held[s]);
+      if (s < steps) alike[s] = count_one(first + s * 32 + lane, held[s]);
     for (int64_t s = kHeldTokens; s < steps; ++s) count_one(first + s * 32 + lane, token(first + s * 32 + lane));
     __syncthreads();
     if (threadIdx.x < digits) {
-      uint32_t sum = 0;
+      uint32_t of_warp[kSortWarps], sum = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) of_warp[w] = count[w * kMaxDigits + threadIdx.x];
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const uint32_t c = count[w * kMaxDigits + threadIdx.x];
         count[w * kMaxDigits + threadIdx.x] = sum;
-        sum += c;
+        sum += of_warp[w];
       }
       total[threadIdx.x] = sum;
     }
@@ -252,9 +257,8 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
       base[threadIdx.x] = start + upto - all + before;
     }
     __syncthreads();
-    auto place_one = [&](int64_t i, const uint2& t) {
-      const uint32_t d = i < p.n ? (t.x >> shift) & (digits - 1) : 0xffffffffu;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
+    auto place_one = [&](int64_t i, const uint2& t, unsigned same) {
+      const uint32_t d = digit(i, t);
       if (d != 0xffffffffu) {
         const uint32_t at = base[d] + mine[d] + __popc(same & ((1u << lane) - 1));
         if (dev_check(at < p.n, p.status)) __stcg(out + at, t);
@@ -265,8 +269,12 @@ __device__ void sort_tokens(const EmbeddingGradLaunch& p, uint32_t* smem) {
     };
 #pragma unroll
     for (int s = 0; s < kHeldTokens; ++s)
-      if (s < steps) place_one(first + s * 32 + lane, held[s]);
-    for (int64_t s = kHeldTokens; s < steps; ++s) place_one(first + s * 32 + lane, token(first + s * 32 + lane));
+      if (s < steps) place_one(first + s * 32 + lane, held[s], alike[s]);
+    for (int64_t s = kHeldTokens; s < steps; ++s) {
+      const int64_t i = first + s * 32 + lane;
+      const uint2 t = token(i);
+      place_one(i, t, __match_any_sync(0xffffffffu, digit(i, t)));
+    }
     // The next pass reads what the whole cluster wrote, and reuses the counts others have read.
     ptx::cluster_sync_all();
   }
