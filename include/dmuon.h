@@ -432,8 +432,8 @@ DMUON_API int dmuon_selftest_bounded_wait(int64_t limit_ns, void* cuda_stream);
 /*
  * The checked build. libdmuon_checked.so is built from the same sources with device-side range checks
  * compiled in (the debugging stand-in for a memory checker): every tile's job index and position, every
- * row-wise chunk's matrix, partial-sum slot and cast tile, every AdamW chunk and every small-matrix job's
- * sizes are tested before use; a failed test skips the access and records DMUON_ERR_RANGE for
+ * row-wise chunk's matrix, partial-sum slot and cast tile, every AdamW chunk, every small-matrix job's
+ * sizes and every place in the embedding gradient's sorted and crossing lists are tested before use; a failed test skips the access and records DMUON_ERR_RANGE for
  * dmuon_check_status. The regular libdmuon.so leaves them out. dmuon_selftest_range_check launches one
  * GEMM whose only tile lies outside its (empty) product, so that in the checked build the next
  * dmuon_check_status returns DMUON_ERR_RANGE; nothing is read or written. In the regular build it returns
