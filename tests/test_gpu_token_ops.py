@@ -161,6 +161,14 @@ def test_embedding_grad_layouts(dm, dt, layout):
         assert torch.isnan(grad.as_strided((rows, 5), (dim + 5, 1), dim)).all(), "written between the rows"
 
 
+@pytest.mark.parametrize("kind", ["one", "distinct", "falling", "even"])
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n,rows,dim", [(256, 5, 1030), (255, 300, 33), (2, 1, 5)])
+def test_embedding_grad_of_few_tokens(dm, n, rows, dim, dt, kind):
+    """Up to 256 tokens are added without a sort."""
+    test_embedding_grad(dm, n, rows, dim, dt, kind)
+
+
 def test_embedding_offsets_past_32_bits(dm):
     """A table of over 2^32 elements: the last rows are looked up and receive their gradients."""
     rows, dim = (1 << 20) + 5, 4100
@@ -291,6 +299,24 @@ def test_add_rmsnorm_grad_without_rows(dm):
     assert dm.add_rmsnorm_grad(x, x, gain, dgain=keep, accumulate=True)[1].tolist() == [2.0] * 96
 
 
+# Rows of every length that has its own split among threads, and more of them than the GPU holds at a time.
+NORM_TURNS = [(4001, 300), (4001, 515), (2500, 700), (1500, 1500), (1500, 2051), (700, 5003), (700, 6005), (400, 9301),
+              (400, 12289), (400, 16000)]
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n,dim", NORM_TURNS)
+def test_add_rmsnorm_in_turns(dm, n, dim, dt):
+    test_add_rmsnorm(dm, n, dim, dt, "plain")
+    test_add_rmsnorm_fp8(dm, n, dim, dt, 128)
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n,dim", NORM_TURNS)
+def test_add_rmsnorm_grad_in_turns(dm, n, dim, dt):
+    test_add_rmsnorm_grad(dm, n, dim, dt, "plain")
+
+
 def test_norm_gradient_against_differences(dm):
     """The kernels' own forward in differences: a step of 1e-2 in fp32 values of order 1 is off by about 1e-4 (its square)
     and the rounding of a sum of 40 values, 40 u / 1e-2 = 2.4e-4; 2e-3 is asked for."""
@@ -383,6 +409,18 @@ def test_policy_loss(dm, n, vocab, dt, layout):
         got = dm.policy_loss(**s, clip_low=0.2, clip_high=0.25, kl_coef=kl, temperature=temperature,
                              dlogits=s["logits"])[2]
         assert torch.equal(got, d)
+    dm.check_status()
+
+
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n,vocab", [(400, 5003), (250, 12000), (250, 25003), (90, 50257)])
+def test_policy_in_turns(dm, n, vocab, dt):
+    """Clusters of every size of CTA, each with several rows."""
+    s = policy_inputs(n, vocab, dt, 1.0, 9)
+    loss, logp, d = check_policy(dm, s, 1.0, 0.1)
+    some = {k: v[n // 2:] for k, v in s.items()}
+    got = dm.policy_loss(**some, clip_low=0.2, clip_high=0.25, kl_coef=0.1)
+    assert torch.equal(got[1], logp[n // 2:]) and torch.equal(got[2], d[n // 2:]), "a row's bits depend on the others"
     dm.check_status()
 
 
