@@ -20,7 +20,7 @@
 // granules pass through shared memory for it, so a value's bits do not depend on where it lies.
 //
 // Bounds. Rows of whole granules: memory, forward at 16384 x 4096 bf16 85 us (6.3 TB/s), fp32 171 (6.3), backward
-// 93 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
+// 92 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
 // 121 us (4.4 TB/s), fp32 180 (6.0), backward 111 (4.8) and 168 (6.4). 8-bit outputs: the chain from the row's sum
 // over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 85 us (5.6
 // TB/s), 3001 x 8200 fp32 59 (5.4); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
@@ -386,8 +386,8 @@ __global__ void __launch_bounds__(THREADS, HELD ? (FP8 || EDGES ? (K > 1 ? 2 : 3
 
 // ---------------------------------------------------------------------------- backward
 
-// The sums for dgain of a thread's columns, and its gains, stay in registers (REGS) or, for long rows, in shared
-// memory. AHEAD: the next row is loaded early. PER_SM: CTAs that registers are to leave room for.
+// The sums for dgain of a thread's columns, and its gains, stay in registers (REGS) or in shared memory.
+// AHEAD: the next row is loaded early. PER_SM: CTAs that registers are to leave room for.
 template <typename T, int K, int THREADS, int PER_SM, bool REGS, bool AHEAD, bool EDGES>
 __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(const RmsNormGradLaunch p) {
   constexpr int E = kPer<T>;
@@ -409,10 +409,8 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   float gain[REGS ? K : 1][E], acc[REGS ? K : 1][E], acc_edge = 0.f;
   const float gain_edge = edge >= 0 && p.gain ? __ldg(p.gain + edge) : 1.f;
   // Without REGS a thread's sums, then its gains: four columns at [quarter][granule], so that a warp's accesses do
-  // not conflict. Aligned gains of a small CTA are LOADED from memory at each use, which leaves L1 its space: in a larger
-  // one, alone on its SM, there is room for them.
-  constexpr bool LOADED = !EDGES && THREADS <= 256;
-  const int granules = K * tpr, held = REGS ? 0 : E / 4 * granules * (LOADED ? 1 : 2);  // of a row
+  // not conflict. (Gains loaded from memory at each use: 8192 x 8192 bf16 107 us, 98 with them here.)
+  const int granules = K * tpr, held = REGS ? 0 : E / 4 * granules * 2;  // of a row
   float4* sums = reinterpret_cast<float4*>(dyn) + slot * held;
   float4* gains = sums + E / 4 * granules;
 #pragma unroll
@@ -426,16 +424,12 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
         acc[k][j] = 0.f;
       } else if (j % 4 == 0) {
         sums[j / 4 * granules + t + k * tpr] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!LOADED) gains[j / 4 * granules + t + k * tpr] = make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
+        gains[j / 4 * granules + t + k * tpr] = make_float4(g[j], g[j + 1], g[j + 2], g[j + 3]);
       }
     }
   }
   // Into gain[0], without REGS.
   auto gains_of = [&](int k) {
-    if (LOADED) {
-      load_gain(gain[0], p.gain, start(k), dim);
-      return;
-    }
 #pragma unroll
     for (int j = 0; j < E; j += 4) {
       const float4 u = gains[j / 4 * granules + t + k * tpr];
@@ -857,7 +851,7 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   // Sums of long rows, or the line in which a CTA's short rows join.
   const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
   const size_t smem = (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) +
-                      (REGS ? 0 : static_cast<size_t>(rows) * K * tpr * kPer<T> * 4 * (!EDGES && THREADS <= 256 ? 1 : 2));
+                      (REGS ? 0 : static_cast<size_t>(rows) * K * tpr * kPer<T> * 4 * 2);
   if (smem > kPlainSmem) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -875,10 +869,11 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
 // A row's whole granules, K a thread, in CTAs that leave a thread the registers for them: 256 threads twice per SM,
 // then one CTA per SM whose threads are as many as the row needs, since registers are divided among them. What
 // spills loses; all at 67 million elements:
-// - bf16, two granules: three CTAs with the sums in shared memory 144 us, two with them in registers 94 (dim 4096).
+// - bf16, two granules: three CTAs 122 us, two 94 (dim 4096), with the sums in shared memory; in registers 95 (and of
+//   rows up to 512 columns, a warp's, the same).
 // - fp32 with edges, as of 65 granules two: dim 1027 225 us with one, 169 with two.
 // - bf16 with edges, 513 to 1024 granules: four and two CTAs of 256 131 us, two in 512 and the next row ahead 112
-//   (dim 6005); aligned rows the other way, 113 and 127 (dim 5000). To 1280 granules four in 320 threads 164 us, two in
+//   (dim 6005); aligned rows the other way, 101 and 127 (dim 5000). To 1280 granules four in 320 threads 164 us, two in
 //   640 133 (dim 8201).
 // - fp32 beyond 2048 granules: four in 576 to 768 threads while that holds them (aligned, dim 10000: 181 us, 194 with
 //   eight in 416; with edges, dim 8201: 189, 224), then eight in 512 (aligned, dim 16000: 175, 184 with four in 1024;
@@ -891,7 +886,7 @@ cudaError_t launch_held_grad(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   if (granules <= 64) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if (granules <= 256 && !(EDGES && sizeof(T) == 4))
     return launch_grad_rows<T, 1, 256, 3, !EDGES, true, EDGES>(p, granules, sms, stream);
-  if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, !EDGES || sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
+  if (granules <= 512) return launch_grad_rows<T, 2, 256, 2, sizeof(T) == 4, true, EDGES>(p, granules, sms, stream);
   if constexpr (EDGES && sizeof(T) == 2) {
     if (granules <= 1024) return launch_grad_rows<T, 2, 512, 1, false, true, EDGES>(p, granules, sms, stream);
     if (granules <= 1280) return launch_grad_rows<T, 2, 640, 1, false, false, EDGES>(p, granules, sms, stream);
