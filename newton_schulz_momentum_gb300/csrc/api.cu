@@ -1660,95 +1660,107 @@ int dmuon_adamw_step(int count, float* const* params, const void* const* grads, 
 
 int dmuon_embedding(const void* table, int table_dtype, int64_t rows, int64_t dim, int64_t ld_table, const void* ids,
                     int id_bytes, int64_t n, float scale, void* out, int out_dtype, int64_t ld_out, void* cuda_stream) {
-  int st = check_token_sizes(n, dim, "dim");
-  if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
-  if (st == DMUON_OK) st = check_elements("table", table, table_dtype, ld_table, dim, rows);
-  if (st == DMUON_OK) st = check_elements("out", out, out_dtype, ld_out, dim, n);
-  if (st != DMUON_OK) return st;
-  if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
-  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState* ds = nullptr;
-  st = current_device(&ds);
-  if (st != DMUON_OK || n == 0) return st;
-  EmbeddingLaunch p;
-  p.table = table, p.table_dtype = table_dtype, p.out_dtype = out_dtype;
-  p.rows = rows, p.dim = dim, p.ld_table = ld_table;
-  p.ids = ids, p.id_bytes = id_bytes, p.n = n;
-  p.scale = scale, p.out = out, p.ld_out = ld_out;
-  p.status = ds->status;
-  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding(p, stream); }), "embedding launch");
-  return DMUON_OK;
+  try {
+    int st = check_token_sizes(n, dim, "dim");
+    if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("table", table, table_dtype, ld_table, dim, rows);
+    if (st == DMUON_OK) st = check_elements("out", out, out_dtype, ld_out, dim, n);
+    if (st != DMUON_OK) return st;
+    if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
+    if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    EmbeddingLaunch p;
+    p.table = table, p.table_dtype = table_dtype, p.out_dtype = out_dtype;
+    p.rows = rows, p.dim = dim, p.ld_table = ld_table;
+    p.ids = ids, p.id_bytes = id_bytes, p.n = n;
+    p.scale = scale, p.out = out, p.ld_out = ld_out;
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding(p, stream); }), "embedding launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
 }
 
 int dmuon_embedding_grad(const void* grad_out, int grad_dtype, int64_t ld_grad_out, const void* ids, int id_bytes,
                          int64_t n, int64_t rows, int64_t dim, float scale, int64_t padding_idx, float* grad,
                          int64_t ld_grad, int accumulate, void* cuda_stream) {
-  int st = check_token_sizes(n, dim, "dim");
-  if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
-  if (st == DMUON_OK) st = check_elements("grad_out", grad_out, grad_dtype, ld_grad_out, dim, n);
-  if (st == DMUON_OK) st = check_elements("grad", grad, DMUON_F32, ld_grad, dim, rows);
-  if (st != DMUON_OK) return st;
-  if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
-  if (padding_idx >= rows) return fail(DMUON_ERR_INVALID_ARG, "padding_idx must be below rows (negative: none)");
-  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState* ds = nullptr;
-  st = current_device(&ds);
-  if (st != DMUON_OK || (n == 0 && accumulate)) return st;
-  EmbeddingGradLaunch p;
-  p.grad_out = grad_out, p.grad_dtype = grad_dtype, p.ld_grad_out = ld_grad_out;
-  p.ids = ids, p.id_bytes = id_bytes;
-  p.n = n, p.rows = rows, p.dim = dim;
-  p.scale = scale, p.padding_idx = padding_idx;
-  p.grad = grad, p.ld_grad = ld_grad, p.accumulate = accumulate != 0;
-  p.status = ds->status;
-  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  char* ws = nullptr;
-  st = token_workspace(*ds, embedding_grad_workspace(p, nullptr), stream, &ws);
-  if (st != DMUON_OK) return st;
-  embedding_grad_workspace(p, ws);
-  DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding_grad(p, ds->sms, stream); }),
-          "embedding gradient launch");
-  return DMUON_OK;
+  try {
+    int st = check_token_sizes(n, dim, "dim");
+    if (st == DMUON_OK) st = check_ids(ids, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("grad_out", grad_out, grad_dtype, ld_grad_out, dim, n);
+    if (st == DMUON_OK) st = check_elements("grad", grad, DMUON_F32, ld_grad, dim, rows);
+    if (st != DMUON_OK) return st;
+    if (rows < 1 || rows > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "rows must be in [1, 2^31 - 1]");
+    if (padding_idx >= rows) return fail(DMUON_ERR_INVALID_ARG, "padding_idx must be below rows (negative: none)");
+    if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || (n == 0 && accumulate)) return st;
+    EmbeddingGradLaunch p;
+    p.grad_out = grad_out, p.grad_dtype = grad_dtype, p.ld_grad_out = ld_grad_out;
+    p.ids = ids, p.id_bytes = id_bytes;
+    p.n = n, p.rows = rows, p.dim = dim;
+    p.scale = scale, p.padding_idx = padding_idx;
+    p.grad = grad, p.ld_grad = ld_grad, p.accumulate = accumulate != 0;
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    char* ws = nullptr;
+    st = token_workspace(*ds, embedding_grad_workspace(p, nullptr), stream, &ws);
+    if (st != DMUON_OK) return st;
+    embedding_grad_workspace(p, ws);
+    DM_CUDA(timed(kClsEmbedding, stream, [&] { return launch_embedding_grad(p, ds->sms, stream); }),
+            "embedding gradient launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
 }
 
 int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int dtype, const float* gain,
                       int64_t n, int64_t dim, float eps, void* h, int64_t ldh, void* y, int y_dtype, int64_t ldy,
                       float* scales, int64_t group, void* cuda_stream) {
-  int st = check_token_sizes(n, dim, "dim");
-  if (st == DMUON_OK) st = check_elements("x", x, dtype, ldx, dim, n);
-  if (st == DMUON_OK && residual) st = check_elements("residual", residual, dtype, ldr, dim, n);
-  if (st == DMUON_OK && h) st = check_elements("h", h, dtype, ldh, dim, n);
-  if (st != DMUON_OK) return st;
-  if (y_dtype == DMUON_E4M3) {
-    if (n > 0 && (!y || !scales)) return fail(DMUON_ERR_INVALID_ARG, "y and scales must not be NULL");
-    if (ldy < dim) return fail(DMUON_ERR_INVALID_ARG, "the leading dimension of y is smaller than its row length");
-    if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
-      return fail(DMUON_ERR_INVALID_ARG, "group must be 32, 64, 128, 256 or 0 (one scale per row), got %lld",
-                  (long long)group);
-    if (!aligned_to(scales, 4)) return fail(DMUON_ERR_INVALID_ARG, "scales must be 4-byte aligned");
-  } else {
-    if (y_dtype != dtype) return fail(DMUON_ERR_INVALID_ARG, "y_dtype must be dtype or DMUON_E4M3 (2)");
-    if (scales) return fail(DMUON_ERR_INVALID_ARG, "scales must be NULL unless y_dtype is DMUON_E4M3 (2)");
-    st = check_elements("y", y, dtype, ldy, dim, n);
+  try {
+    int st = check_token_sizes(n, dim, "dim");
+    if (st == DMUON_OK) st = check_elements("x", x, dtype, ldx, dim, n);
+    if (st == DMUON_OK && residual) st = check_elements("residual", residual, dtype, ldr, dim, n);
+    if (st == DMUON_OK && h) st = check_elements("h", h, dtype, ldh, dim, n);
     if (st != DMUON_OK) return st;
+    if (y_dtype == DMUON_E4M3) {
+      if (n > 0 && (!y || !scales)) return fail(DMUON_ERR_INVALID_ARG, "y and scales must not be NULL");
+      if (ldy < dim) return fail(DMUON_ERR_INVALID_ARG, "the leading dimension of y is smaller than its row length");
+      if (group != 0 && group != 32 && group != 64 && group != 128 && group != 256)
+        return fail(DMUON_ERR_INVALID_ARG, "group must be 32, 64, 128, 256 or 0 (one scale per row), got %lld",
+                    (long long)group);
+      if (!aligned_to(scales, 4)) return fail(DMUON_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+    } else {
+      if (y_dtype != dtype) return fail(DMUON_ERR_INVALID_ARG, "y_dtype must be dtype or DMUON_E4M3 (2)");
+      if (scales) return fail(DMUON_ERR_INVALID_ARG, "scales must be NULL unless y_dtype is DMUON_E4M3 (2)");
+      st = check_elements("y", y, dtype, ldy, dim, n);
+      if (st != DMUON_OK) return st;
+    }
+    if (!aligned_to(gain, 4)) return fail(DMUON_ERR_INVALID_ARG, "gain must be 4-byte aligned");
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DMUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    RmsNormLaunch p;
+    p.x = x, p.residual = residual, p.dtype = dtype, p.ldx = ldx, p.ldr = ldr;
+    p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
+    p.h = h, p.ldh = ldh, p.y = y, p.ldy = ldy;
+    p.scales = y_dtype == DMUON_E4M3 ? scales : nullptr, p.group = group;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm(p, ds->sms, stream); }), "RMS norm launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
   }
-  if (!aligned_to(gain, 4)) return fail(DMUON_ERR_INVALID_ARG, "gain must be 4-byte aligned");
-  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DMUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState* ds = nullptr;
-  st = current_device(&ds);
-  if (st != DMUON_OK || n == 0) return st;
-  RmsNormLaunch p;
-  p.x = x, p.residual = residual, p.dtype = dtype, p.ldx = ldx, p.ldr = ldr;
-  p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
-  p.h = h, p.ldh = ldh, p.y = y, p.ldy = ldy;
-  p.scales = y_dtype == DMUON_E4M3 ? scales : nullptr, p.group = group;
-  cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-  DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm(p, ds->sms, stream); }), "RMS norm launch");
-  return DMUON_OK;
 }
 
 int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh, int64_t lddh,
@@ -1794,52 +1806,60 @@ int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int6
                       int id_bytes, const float* old_logp, const float* ref_logp, const float* advantages,
                       const float* weights, float clip_low, float clip_high, float kl_coef, float temperature,
                       float* loss, float* logp, void* dlogits, int64_t ldd, void* cuda_stream) {
-  int st = check_token_sizes(n, vocab, "vocab");
-  if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
-  if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
-  if (st == DMUON_OK && dlogits) st = check_elements("dlogits", dlogits, dtype, ldd, vocab, n);
-  if (st != DMUON_OK) return st;
-  if (!loss || (n > 0 && (!old_logp || !advantages || !weights)))
-    return fail(DMUON_ERR_INVALID_ARG, "old_logp, advantages, weights and loss must not be NULL");
-  for (const void* v : {static_cast<const void*>(old_logp), static_cast<const void*>(ref_logp),
-                        static_cast<const void*>(advantages), static_cast<const void*>(weights),
-                        static_cast<const void*>(loss), static_cast<const void*>(logp)})
-    if (!aligned_to(v, 4)) return fail(DMUON_ERR_INVALID_ARG, "fp32 vectors must be 4-byte aligned");
-  if (!(clip_low >= 0.f) || !(clip_high >= 0.f) || !std::isfinite(clip_low) || !std::isfinite(clip_high))
-    return fail(DMUON_ERR_INVALID_ARG, "clip_low and clip_high must be finite and >= 0");
-  if (!std::isfinite(kl_coef)) return fail(DMUON_ERR_INVALID_ARG, "kl_coef must be finite");
-  if (kl_coef != 0.f && n > 0 && !ref_logp)
-    return fail(DMUON_ERR_INVALID_ARG, "ref_logp must not be NULL with a kl_coef other than 0");
-  if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
-    return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
-  std::lock_guard<std::mutex> lock(g_mu);
-  PolicyLaunch p;
-  p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
-  p.targets = targets, p.id_bytes = id_bytes;
-  p.old_logp = old_logp, p.ref_logp = kl_coef != 0.f ? ref_logp : nullptr;
-  p.advantages = advantages, p.weights = weights;
-  p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.inv_temperature = 1.f / temperature;
-  p.loss = loss, p.logp = logp, p.dlogits = dlogits, p.ldd = ldd;
-  return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+  try {
+    int st = check_token_sizes(n, vocab, "vocab");
+    if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+    if (st == DMUON_OK && dlogits) st = check_elements("dlogits", dlogits, dtype, ldd, vocab, n);
+    if (st != DMUON_OK) return st;
+    if (!loss || (n > 0 && (!old_logp || !advantages || !weights)))
+      return fail(DMUON_ERR_INVALID_ARG, "old_logp, advantages, weights and loss must not be NULL");
+    for (const void* v : {static_cast<const void*>(old_logp), static_cast<const void*>(ref_logp),
+                          static_cast<const void*>(advantages), static_cast<const void*>(weights),
+                          static_cast<const void*>(loss), static_cast<const void*>(logp)})
+      if (!aligned_to(v, 4)) return fail(DMUON_ERR_INVALID_ARG, "fp32 vectors must be 4-byte aligned");
+    if (!(clip_low >= 0.f) || !(clip_high >= 0.f) || !std::isfinite(clip_low) || !std::isfinite(clip_high))
+      return fail(DMUON_ERR_INVALID_ARG, "clip_low and clip_high must be finite and >= 0");
+    if (!std::isfinite(kl_coef)) return fail(DMUON_ERR_INVALID_ARG, "kl_coef must be finite");
+    if (kl_coef != 0.f && n > 0 && !ref_logp)
+      return fail(DMUON_ERR_INVALID_ARG, "ref_logp must not be NULL with a kl_coef other than 0");
+    if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
+      return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
+    std::lock_guard<std::mutex> lock(g_mu);
+    PolicyLaunch p;
+    p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+    p.targets = targets, p.id_bytes = id_bytes;
+    p.old_logp = old_logp, p.ref_logp = kl_coef != 0.f ? ref_logp : nullptr;
+    p.advantages = advantages, p.weights = weights;
+    p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.inv_temperature = 1.f / temperature;
+    p.loss = loss, p.logp = logp, p.dlogits = dlogits, p.ldd = ldd;
+    return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
 }
 
 int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab, const void* targets,
                          int id_bytes, float temperature, float* logp, void* cuda_stream) {
-  int st = check_token_sizes(n, vocab, "vocab");
-  if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
-  if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
-  if (st != DMUON_OK) return st;
-  if (n > 0 && (!logp || !aligned_to(logp, 4)))
-    return fail(DMUON_ERR_INVALID_ARG, "logp must not be NULL and must be 4-byte aligned");
-  if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
-    return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
-  std::lock_guard<std::mutex> lock(g_mu);
-  PolicyLaunch p;
-  std::memset(&p, 0, sizeof(p));
-  p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
-  p.targets = targets, p.id_bytes = id_bytes;
-  p.inv_temperature = 1.f / temperature, p.logp = logp;
-  return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+  try {
+    int st = check_token_sizes(n, vocab, "vocab");
+    if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+    if (st != DMUON_OK) return st;
+    if (n > 0 && (!logp || !aligned_to(logp, 4)))
+      return fail(DMUON_ERR_INVALID_ARG, "logp must not be NULL and must be 4-byte aligned");
+    if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
+      return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
+    std::lock_guard<std::mutex> lock(g_mu);
+    PolicyLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+    p.targets = targets, p.id_bytes = id_bytes;
+    p.inv_temperature = 1.f / temperature, p.logp = logp;
+    return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
 }
 
 int dmuon_set_graph_replay(int on) {
