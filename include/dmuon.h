@@ -310,6 +310,11 @@ DMUON_API int dmuon_set_graph_replay(int on);
  * (id_bytes 8). n == 0 is a call without tokens. Sums are held in fp32, in an order fixed by the call's
  * sizes, strides and alignment: the same call gives the same bits. A row of dmuon_add_rmsnorm and of
  * dmuon_policy_loss gives the same bits whatever the other rows are and wherever it lies. Offsets are 64-bit.
+ *
+ * The calls may be captured into a graph of the caller's. Scratch that a captured call needs is allocated during
+ * the capture and belongs to the graph: it is kept, and counts for nothing else, until the graph and all that
+ * was instantiated from it have been destroyed, so replays stay valid whatever is called between them,
+ * dmuon_release_workspace among it.
  */
 
 /*
@@ -455,7 +460,8 @@ DMUON_API int dmuon_set_workspace_limit(size_t bytes);
 DMUON_API int dmuon_workspace_size(int count, const int64_t* rows, const int64_t* cols, int backend,
                          size_t* bytes_out);
 
-/* Synchronise the current device and free its workspace and cached descriptor tables. */
+/* Synchronise the current device and free its workspace and cached descriptor tables (not the scratch that
+ * the token operators' captured graphs hold). */
 DMUON_API int dmuon_release_workspace(void);
 
 #ifdef __cplusplus

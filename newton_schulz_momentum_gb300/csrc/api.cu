@@ -13,11 +13,13 @@
 // Direct form ("直接空间 NS（经典）"), per step: A = X X^T ; B = b A + c A^2 ; X' = B X + a X, the
 // last step writing W <- W - lr * X' instead of X'.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -184,6 +186,15 @@ struct GraphKey {
   }
 };
 
+// A block of the token operators' scratch.
+struct TokenBlock {
+  char* buf = nullptr;
+  size_t bytes = 0;
+  bool captured = false;           // by a capture, whose graph holds the block
+  unsigned long long capture = 0;  // which one
+  std::atomic<bool> dropped{false};  // that graph is gone, or never got it
+};
+
 struct DeviceState {
   bool init = false;
   int sms = 0;
@@ -210,8 +221,7 @@ struct DeviceState {
   char* gather_buf = nullptr;
   size_t gather_bytes = 0;
   int64_t gather_chunks = 0;
-  char* token_buf = nullptr;  // scratch of the token operators
-  size_t token_bytes = 0;
+  std::vector<TokenBlock*> token_blocks;  // not owned: a graph may outlive the library's own state at exit
 };
 
 std::mutex g_mu;
@@ -1241,32 +1251,111 @@ int check_elements(const char* name, const void* ptr, int dtype, int64_t ld, int
   return DMUON_OK;
 }
 
-// The token operators' scratch, `bytes` long, grown when a call needs more.
+// While it lives, this thread may allocate and free although a stream is being captured: neither is work of the capture.
+class RelaxedCapture {
+ public:
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
+
+ private:
+  cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+};
+
+// CUDA calls it, on a thread of its own, when a captured graph and all that was instantiated from it are gone.
+void CUDART_CB token_block_dropped(void* block) { static_cast<TokenBlock*>(block)->dropped.store(true); }
+
+// Makes the block part of the graph that is being captured.
+int hold_by_graph(TokenBlock& block, cudaGraph_t graph) {
+  cudaUserObject_t owner = nullptr;
+  block.dropped.store(true);  // as long as no graph holds it
+  DM_CUDA(cudaUserObjectCreate(&owner, &block, token_block_dropped, 1, cudaUserObjectNoDestructorSync),
+          "cudaUserObjectCreate");
+  const cudaError_t e = cudaGraphRetainUserObject(graph, owner, 1, cudaGraphUserObjectMove);
+  if (e != cudaSuccess) {
+    cudaUserObjectRelease(owner, 1);
+    return cuda_fail(e, "cudaGraphRetainUserObject");
+  }
+  block.dropped.store(false);
+  return DMUON_OK;
+}
+
+// Frees the blocks that `which` names. No work that uses them is left.
+template <typename F>
+void free_token_blocks(DeviceState& ds, F&& which) {
+  if (std::none_of(ds.token_blocks.begin(), ds.token_blocks.end(), [&](const TokenBlock* b) { return which(*b); })) return;
+  RelaxedCapture relaxed;
+  size_t kept = 0;
+  for (TokenBlock* b : ds.token_blocks) {
+    if (!which(*b)) {
+      ds.token_blocks[kept++] = b;
+      continue;
+    }
+    cudaFree(b->buf);
+    delete b;
+  }
+  ds.token_blocks.resize(kept);
+}
+
+// A new block of `want` bytes, or, where there is no room for what that has beyond the need, of `need`.
+int new_token_block(DeviceState& ds, size_t need, size_t want, TokenBlock** out) {
+  ds.token_blocks.reserve(ds.token_blocks.size() + 1);
+  std::unique_ptr<TokenBlock> block(new TokenBlock);
+  RelaxedCapture relaxed;
+  block->bytes = want;
+  if (cudaMalloc(&block->buf, block->bytes) != cudaSuccess) {
+    cudaGetLastError();
+    block->bytes = need;
+    if (cudaMalloc(&block->buf, block->bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return fail(DMUON_ERR_OOM, "cudaMalloc of %zu bytes of workspace failed", need);
+    }
+  }
+  *out = block.get();
+  ds.token_blocks.push_back(block.release());
+  return DMUON_OK;
+}
+
+// Scratch of the token operators, `bytes` long. Calls that run at once share a block, grown when one needs more. Calls
+// that a capture records get blocks that belong to its graph, which keeps their addresses: they stay as long as it
+// does, whatever later calls need, and may then be another graph's.
 int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** out) {
   const size_t need = static_cast<size_t>(bytes);
+  *out = nullptr;
+  if (need == 0) return DMUON_OK;
   if (g_ws_limit && need > g_ws_limit)
     return fail(DMUON_ERR_OOM, "workspace of %zu bytes exceeds the limit of %zu", need, g_ws_limit);
-  if (need > ds.token_bytes) {
-    cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-    DM_CUDA(cudaStreamIsCapturing(stream, &capturing), "cudaStreamIsCapturing");
-    if (capturing != cudaStreamCaptureStatusNone)
-      return fail(DMUON_ERR_OOM, "the workspace must grow to %zu bytes, which a capture cannot hold: make this call "
-                                 "once before capturing it", need);
-    DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize before growing the workspace");
-    if (ds.token_buf) cudaFree(ds.token_buf);
-    ds.token_buf = nullptr;
-    ds.token_bytes = 0;
-    // Half as much again, so that a slowly growing batch does not reallocate at every call.
-    size_t get = std::max<size_t>(need + need / 2, size_t(1) << 20);
-    if (g_ws_limit) get = std::min(get, g_ws_limit);
-    if (cudaMalloc(&ds.token_buf, get) != cudaSuccess) {
-      cudaGetLastError();
-      ds.token_buf = nullptr;
-      return fail(DMUON_ERR_OOM, "cudaMalloc of %zu bytes of workspace failed", get);
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  unsigned long long id = 0;
+  cudaGraph_t graph = nullptr;
+  DM_CUDA(cudaStreamGetCaptureInfo(stream, &capturing, &id, &graph), "cudaStreamGetCaptureInfo");
+  const bool captured = capturing == cudaStreamCaptureStatusActive;
+  if (!captured) free_token_blocks(ds, [](const TokenBlock& b) { return b.captured && b.dropped.load(); });
+  for (TokenBlock* b : ds.token_blocks)
+    if (b->captured == captured && !b->dropped.load() && (!captured || b->capture == id) && b->bytes >= need) {
+      *out = b->buf;
+      return DMUON_OK;
     }
-    ds.token_bytes = get;
+  TokenBlock* block = nullptr;
+  if (!captured) {
+    DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize before growing the workspace");
+    free_token_blocks(ds, [](const TokenBlock& b) { return !b.captured; });
+  } else {
+    for (TokenBlock* b : ds.token_blocks)
+      if (b->captured && b->dropped.load() && b->bytes >= need) block = b;
   }
-  *out = ds.token_buf;
+  if (!block) {
+    // Outside of captures half as much again, so that a slowly growing batch does not reallocate at every call.
+    size_t want = std::max<size_t>(need + (captured ? 0 : need / 2), size_t(1) << 20);
+    if (g_ws_limit) want = std::min(want, g_ws_limit);
+    const int st = new_token_block(ds, need, want, &block);
+    if (st != DMUON_OK) return st;
+  }
+  block->captured = captured, block->capture = id;
+  if (captured) {
+    const int st = hold_by_graph(*block, graph);
+    if (st != DMUON_OK) return st;
+  }
+  *out = block->buf;
   return DMUON_OK;
 }
 
@@ -2046,12 +2135,10 @@ int dmuon_release_workspace(void) {
   ds.gather_bytes = 0;
   ds.gather_key.clear();
   ds.gather_ok = false;
-  if (ds.token_buf) {
+  if (!ds.token_blocks.empty()) {
     DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize");
-    DM_CUDA(cudaFree(ds.token_buf), "cudaFree(token workspace)");
+    free_token_blocks(ds, [](const TokenBlock& b) { return !b.captured || b.dropped.load(); });
   }
-  ds.token_buf = nullptr;
-  ds.token_bytes = 0;
   return DMUON_OK;
 }
 
