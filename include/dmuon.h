@@ -311,6 +311,10 @@ DMUON_API int dmuon_set_graph_replay(int on);
  * sizes, strides and alignment: the same call gives the same bits. A row of dmuon_add_rmsnorm and of
  * dmuon_policy_loss gives the same bits whatever the other rows are and wherever it lies. Offsets are 64-bit.
  *
+ * These calls need not be serialised among themselves as those above: every stream has scratch of its own, so calls
+ * on different streams may overlap (where their tensors allow it). At the 65th stream, all streams' scratch is freed
+ * after a synchronisation of the device.
+ *
  * The calls may be captured into a graph of the caller's. Scratch that a captured call needs is allocated during
  * the capture and belongs to the graph: it is kept, and counts for nothing else, until the graph and all that
  * was instantiated from it have been destroyed, so replays stay valid whatever is called between them,

@@ -58,6 +58,8 @@ int cuda_fail(cudaError_t e, const char* what) {
 
 constexpr size_t kNone = ~size_t(0);
 constexpr int64_t kMaxDim = int64_t(1) << 24;
+constexpr size_t kTokenHeader = 256;  // bytes in front of a block of the token operators' scratch
+constexpr size_t kTokenStreams = 64;  // that have a block of it at a time
 constexpr int kMaxGroups = 64;  // pipeline groups of one dmuon_muon_step_host call
 // dmuon_muon_step_host gathers with one launch instead of a copy per matrix from this many matrices on,
 // when they average less than this many gradient bytes.
@@ -186,10 +188,11 @@ struct GraphKey {
   }
 };
 
-// A block of the token operators' scratch.
+// A block of the token operators' scratch: a counter, and `bytes` behind its kTokenHeader.
 struct TokenBlock {
   char* buf = nullptr;
   size_t bytes = 0;
+  unsigned long long stream = 0;   // whose calls it serves: its id, or handle during a capture
   bool captured = false;           // by a capture, whose graph holds the block
   unsigned long long capture = 0;  // which one
   std::atomic<bool> dropped{false};  // that graph is gone, or never got it
@@ -221,6 +224,7 @@ struct DeviceState {
   char* gather_buf = nullptr;
   size_t gather_bytes = 0;
   int64_t gather_chunks = 0;
+  cudaStream_t token_stream = nullptr;    // sets up the token operators' scratch
   std::vector<TokenBlock*> token_blocks;  // not owned: a graph may outlive the library's own state at exit
 };
 
@@ -1296,66 +1300,99 @@ void free_token_blocks(DeviceState& ds, F&& which) {
   ds.token_blocks.resize(kept);
 }
 
-// A new block of `want` bytes, or, where there is no room for what that has beyond the need, of `need`.
+// A new block that holds `need` bytes, and if there is room for them `want`. Its counter is 0.
 int new_token_block(DeviceState& ds, size_t need, size_t want, TokenBlock** out) {
   ds.token_blocks.reserve(ds.token_blocks.size() + 1);
   std::unique_ptr<TokenBlock> block(new TokenBlock);
   RelaxedCapture relaxed;
-  block->bytes = want;
-  if (cudaMalloc(&block->buf, block->bytes) != cudaSuccess) {
-    cudaGetLastError();
-    block->bytes = need;
-    if (cudaMalloc(&block->buf, block->bytes) != cudaSuccess) {
-      cudaGetLastError();
-      return fail(DMUON_ERR_OOM, "cudaMalloc of %zu bytes of workspace failed", need);
+  // The zero is written on a stream of the library's own, which no capture and no caller's work is on.
+  if (!ds.token_stream)
+    DM_CUDA(cudaStreamCreateWithFlags(&ds.token_stream, cudaStreamNonBlocking), "cudaStreamCreateWithFlags");
+  for (size_t bytes : {want, need}) {
+    if (cudaMalloc(&block->buf, kTokenHeader + bytes) == cudaSuccess) {
+      block->bytes = bytes;
+      break;
     }
+    cudaGetLastError();
+  }
+  if (block->bytes == 0) return fail(DMUON_ERR_OOM, "cudaMalloc of %zu bytes of workspace failed", need);
+  cudaError_t e = cudaMemsetAsync(block->buf, 0, kTokenHeader, ds.token_stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(ds.token_stream);
+  if (e != cudaSuccess) {
+    cudaFree(block->buf);
+    return cuda_fail(e, "clear the workspace's counter");
   }
   *out = block.get();
   ds.token_blocks.push_back(block.release());
   return DMUON_OK;
 }
 
-// Scratch of the token operators, `bytes` long. Calls that run at once share a block, grown when one needs more. Calls
-// that a capture records get blocks that belong to its graph, which keeps their addresses: they stay as long as it
-// does, whatever later calls need, and may then be another graph's.
-int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** out) {
+// Scratch of the token operators, `bytes` long, with a counter that is 0 between calls. A block is used in one order:
+// each stream has its own, grown when a call needs more, since calls on two streams may overlap. What a capture
+// records on a stream gets a block of its own, which belongs to its graph: the graph keeps the address, so the block
+// stays as long as it does, whatever later calls need, and may then be another graph's.
+int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** out, unsigned** counter = nullptr) {
   const size_t need = static_cast<size_t>(bytes);
   *out = nullptr;
   if (need == 0) return DMUON_OK;
   if (g_ws_limit && need > g_ws_limit)
     return fail(DMUON_ERR_OOM, "workspace of %zu bytes exceeds the limit of %zu", need, g_ws_limit);
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
-  unsigned long long id = 0;
+  unsigned long long id = 0, owner = reinterpret_cast<uintptr_t>(stream);
   cudaGraph_t graph = nullptr;
   DM_CUDA(cudaStreamGetCaptureInfo(stream, &capturing, &id, &graph), "cudaStreamGetCaptureInfo");
   const bool captured = capturing == cudaStreamCaptureStatusActive;
+  // Unlike a handle an id is never another stream's; a stream has none to give while it is captured.
+  if (!captured) DM_CUDA(cudaStreamGetId(stream, &owner), "cudaStreamGetId");
+  auto give = [&](TokenBlock& b) {
+    if (counter) *counter = reinterpret_cast<unsigned*>(b.buf);
+    *out = b.buf + kTokenHeader;
+  };
   if (!captured) free_token_blocks(ds, [](const TokenBlock& b) { return b.captured && b.dropped.load(); });
   for (TokenBlock* b : ds.token_blocks)
-    if (b->captured == captured && !b->dropped.load() && (!captured || b->capture == id) && b->bytes >= need) {
-      *out = b->buf;
+    if (b->captured == captured && b->stream == owner && !b->dropped.load() && (!captured || b->capture == id) &&
+        b->bytes >= need) {
+      give(*b);
       return DMUON_OK;
     }
   TokenBlock* block = nullptr;
-  if (!captured) {
-    DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize before growing the workspace");
-    free_token_blocks(ds, [](const TokenBlock& b) { return !b.captured; });
-  } else {
+  if (captured) {
     for (TokenBlock* b : ds.token_blocks)
       if (b->captured && b->dropped.load() && b->bytes >= need) block = b;
+  } else {
+    DM_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize before growing the workspace");
+    free_token_blocks(ds, [&](const TokenBlock& b) { return !b.captured && b.stream == owner; });
   }
   if (!block) {
     // Outside of captures half as much again, so that a slowly growing batch does not reallocate at every call.
     size_t want = std::max<size_t>(need + (captured ? 0 : need / 2), size_t(1) << 20);
-    if (g_ws_limit) want = std::min(want, g_ws_limit);
+    size_t streams = 0;
+    for (const TokenBlock* b : ds.token_blocks) streams += b->captured ? 0 : 1;
+    auto held = [&] {
+      size_t sum = 0;
+      for (const TokenBlock* b : ds.token_blocks) sum += b->bytes;
+      return sum;
+    };
+    if (!captured && (streams >= kTokenStreams || (g_ws_limit && held() + need > g_ws_limit))) {
+      // Streams that are gone have left theirs behind.
+      DM_CUDA(cudaDeviceSynchronize(), "cudaDeviceSynchronize before freeing other streams' workspace");
+      free_token_blocks(ds, [](const TokenBlock& b) { return !b.captured; });
+    }
+    if (g_ws_limit) {
+      if (held() + need > g_ws_limit)
+        return fail(DMUON_ERR_OOM, "workspace of %zu bytes beside the %zu that graphs hold exceeds the limit of %zu", need,
+                    held(), g_ws_limit);
+      want = std::min(want, g_ws_limit - held());
+    }
     const int st = new_token_block(ds, need, want, &block);
     if (st != DMUON_OK) return st;
   }
-  block->captured = captured, block->capture = id;
+  block->captured = captured, block->capture = id, block->stream = owner;
   if (captured) {
     const int st = hold_by_graph(*block, graph);
     if (st != DMUON_OK) return st;
   }
-  *out = block->buf;
+  give(*block);
   return DMUON_OK;
 }
 
@@ -1364,10 +1401,10 @@ int run_policy(PolicyLaunch& p, cudaStream_t stream) {
   DeviceState* ds = nullptr;
   int st = current_device(&ds);
   if (st != DMUON_OK || (p.n == 0 && !p.loss)) return st;
-  p.loss_terms = nullptr;
+  p.loss_terms = nullptr, p.terms_done = nullptr;
   if (p.loss) {
     char* ws = nullptr;
-    st = token_workspace(*ds, policy_workspace(p.n), stream, &ws);
+    st = token_workspace(*ds, policy_workspace(p.n), stream, &ws, &p.terms_done);
     if (st != DMUON_OK) return st;
     p.loss_terms = reinterpret_cast<float*>(ws);
   }

@@ -408,6 +408,7 @@ struct PolicyLaunch {
   float* loss;      // null: log-probabilities only
   float* loss_terms;  // workspace of policy_workspace(n) bytes: `terms` summands of the loss, set by launch_policy
   int64_t terms;
+  unsigned* terms_done;  // how many are there; 0 between launches
   float* logp;      // may be null
   void* dlogits;    // may be null
   int64_t ldd;

@@ -243,18 +243,15 @@ __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const
   return c * r.w * p.inv_temperature;
 }
 
-// Terms of the loss that are there; 0 between launches.
-__device__ unsigned g_terms_done;
-
-// Leaves a term of the loss; who leaves the last one adds them all, in an order that their number fixes. Called by one
-// whole warp per term. (A launch of its own for the sum: 4 more microseconds for a call of 8 rows.)
+// Leaves a term of the loss; who leaves the last one adds them all, in an order that their number fixes. The counter
+// lies in the call's own scratch, and its last increment sets it back to 0. Called by one whole warp per term. (A launch of its own for the sum: 4 more microseconds for a call of 8 rows.)
 __device__ __forceinline__ void leave_term(const PolicyLaunch& p, int64_t at, float loss) {
   const int lane = threadIdx.x & 31;
   unsigned before = 0;
   if (lane == 0) {
     p.loss_terms[at] = loss;
     __threadfence();
-    before = atomicAdd(&g_terms_done, 1u);
+    before = atomicInc(p.terms_done, static_cast<unsigned>(p.terms) - 1);
   }
   if (__shfl_sync(0xffffffffu, before, 0) + 1 < static_cast<unsigned>(p.terms)) return;
   __threadfence();
@@ -269,10 +266,7 @@ __device__ __forceinline__ void leave_term(const PolicyLaunch& p, int64_t at, fl
   }
   for (; i < p.terms; i += 32) acc += __ldcg(p.loss_terms + i);
   acc = warp_sum(acc);
-  if (lane == 0) {
-    *p.loss = acc;
-    g_terms_done = 0;
-  }
+  if (lane == 0) *p.loss = acc;
 }
 
 __device__ __forceinline__ void row_skipped(const PolicyLaunch& p, int64_t i) {

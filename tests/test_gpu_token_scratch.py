@@ -1,4 +1,4 @@
-"""GPU: the token operators' scratch. What a captured graph uses is its own for as long as it lives."""
+"""GPU: the token operators' scratch. What a captured graph uses is its own for as long as it lives, and so is a stream's."""
 
 import gc
 
@@ -91,6 +91,48 @@ def test_graphs_do_not_share(dm):
         got = step(dm, c)
         torch.cuda.synchronize()
         assert equal(ha, wa) and equal(hb, wb) and equal(got, wc)
+    dm.check_status()
+
+
+def test_streams_do_not_share(dm):
+    """Calls that overlap on three streams, with scratch that grows on the way, give what they give one by one, and
+    leave nothing behind for the calls that follow."""
+    sizes = [(5000, 3000, 1032), (70, 50, 128256), (900, 200, 264)]
+    some = [step_inputs(*size, seed=k) for k, size in enumerate(sizes)]
+    more = step_inputs(30000, 3000, 1032, 7)
+    want, big = [[t.clone() for t in step(dm, s)] for s in some], [t.clone() for t in step(dm, more)]
+    streams = [torch.cuda.Stream() for _ in some]
+    torch.cuda.synchronize()
+    for turn in range(30):
+        got = []
+        for s, stream in zip(some, streams):
+            with torch.cuda.stream(stream):
+                got.append(step(dm, s))
+        if turn == 15:
+            with torch.cuda.stream(streams[2]):
+                large = step(dm, more)
+        torch.cuda.synchronize()
+        assert all(equal(a, b) for a, b in zip(got, want))
+    assert equal(large, big)
+    for s, w in zip(some, want):
+        assert equal(step(dm, s), w)
+    dm.check_status()
+
+
+def test_more_streams_than_have_scratch_at_a_time(dm):
+    """Streams of the caller's own making (torch hands out the same few again and again)."""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.13")
+    s = step_inputs(600, 300, 136)
+    want = [t.clone() for t in step(dm, s)]
+    torch.cuda.synchronize()
+    for _ in range(70):
+        handle = ctypes.c_void_p()
+        assert rt.cudaStreamCreateWithFlags(ctypes.byref(handle), 1) == 0
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle.value)):
+            got = step(dm, s)
+        assert rt.cudaStreamSynchronize(handle) == 0 and equal(got, want)
+        assert rt.cudaStreamDestroy(handle) == 0
     dm.check_status()
 
 
