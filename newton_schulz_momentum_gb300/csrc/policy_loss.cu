@@ -330,10 +330,15 @@ struct Ring {
 };
 constexpr int kSoloSlotBytes = 18432;  // the most for which four warps' slots fit an SM
 
-// Writes v into a CTA of the cluster and counts its 8 bytes at that CTA's barrier (shared::cluster addresses).
+// Writes v into a CTA of the cluster and counts its bytes at that CTA's barrier (shared::cluster addresses).
 __device__ __forceinline__ void send(uint32_t addr, MaxSum v, uint32_t barrier) {
   asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(v.m),
                "f"(v.s), "r"(barrier)
+               : "memory");
+}
+
+__device__ __forceinline__ void send(uint32_t addr, float v, uint32_t barrier) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(addr), "f"(v), "r"(barrier)
                : "memory");
 }
 
@@ -385,6 +390,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
   constexpr bool SOLO = MODE == kSolo;
   extern __shared__ uint8_t dyn[];
   __shared__ MaxSum joined[kJoins][R::kCluster * R::kWarps];
+  __shared__ float joined_token[kJoins];
   __shared__ uint64_t joined_full[kJoins];
   __shared__ uint64_t slot_full[R::kWarps][kRingSlots];
   __shared__ int abort_word;
@@ -430,19 +436,20 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
     if (lane >= 16 && lane - 16 < c.tail) return c.head + c.full * E + lane - 16;
     return -1;
   };
-  // The token's logit and the edge's, as they lie in memory.
-  auto fetch = [&](T& xa, T& xe, int64_t i, int a) {
+  // The edge's logit, as it lies in memory.
+  auto fetch = [&](T& xe, int64_t i, int a) {
     if (a < 0) return;
-    const T* x = logits + i * p.ld;
-    xa = x[a - from];
     const int e = EDGES ? edge_of(cut(i)) : -1;
-    if (e >= 0) xe = x[e];
+    if (e >= 0) xe = logits[i * p.ld + e];
   };
   uint32_t parity = 0;  // bit s: of the next phase of slot s to wait for
   uint32_t sent = 0, read = 0;  // rows whose sums this warp has sent, has joined
-  MaxSum ready{};  // kSolo: the sum of the row last summed
-  // This warp's sum of row i, in slot s, to every CTA of the cluster; gives the token's logit.
-  auto sum_row = [&](int64_t i, int s, T xa, T xe) {
+  MaxSum ready{};  // kSolo: the sum of the row last summed, and its token's logit
+  float ready_token = 0.f;
+  // This warp's sum of row i, in slot s, to every CTA of the cluster; and the logit of the row's token a by the warp
+  // whose share holds it. (Not read from memory by each: the gradient may go over the logits, and the others may write
+  // theirs once they have this warp's sum. From its own slot a warp reads it before it sends anything.)
+  auto sum_row = [&](int64_t i, int s, int a, T xe) {
     const Cut c = cut(i);
     uint4* line = reinterpret_cast<uint4*>(slots + s * p.slot_bytes);
     const uint4* data = line + (c.head ? 1 : 0);
@@ -515,43 +522,47 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
       }
     }
     sum.s = warp_sum(terms.get());
-    // The token's logit has been read before this warp's sum lets the others write the row's gradient, which may
-    // go over it.
-    const float token_logit = row::to_f(xa);
-    asm volatile("" ::"f"(token_logit) : "memory");
+    const bool here = a >= from && a < from + length;
+    const T* share = reinterpret_cast<const T*>(line) + bytes / static_cast<int>(sizeof(T));
+    const float token = here ? row::to_f(share[a - from]) : 0.f;
     if (SOLO) {
       ready = sum;
-      return token_logit;
+      ready_token = token;
+      return;
     }
     const int j = sent++ % kJoins;
-    if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&joined_full[j], static_cast<uint32_t>(units * sizeof(MaxSum)));
-    if (lane < C)
-      send(ptx::map_shared(ptx::smem_u32(&joined[j][unit]), lane), sum, ptx::map_shared(ptx::smem_u32(&joined_full[j]), lane));
-    return token_logit;
+    if (threadIdx.x == 0)
+      ptx::mbar_arrive_expect_tx(&joined_full[j], static_cast<uint32_t>(units * sizeof(MaxSum) + sizeof(float)));
+    if (lane < C) {
+      const uint32_t barrier = ptx::map_shared(ptx::smem_u32(&joined_full[j]), lane);
+      if (here) send(ptx::map_shared(ptx::smem_u32(&joined_token[j]), lane), token, barrier);
+      send(ptx::map_shared(ptx::smem_u32(&joined[j][unit]), lane), sum, barrier);
+    }
   };
 
   const LaneMeta meta(p, lane);
   uint32_t word = meta.load(first, p.n), word1 = meta.load(first + step, p.n), word2 = meta.load(first + 2 * step, p.n);
   int a = token_of(p, word, first), a1 = token_of(p, word1, first + step);
-  T xa{}, xe{}, xa1{}, xe1{};
-  fetch(xa, xe, first, a);
-  fetch(xa1, xe1, first + step, a1);
+  T xe{}, xe1{};
+  fetch(xe, first, a);
+  fetch(xe1, first + step, a1);
   if (lane == 0) {
     load(first, a, 0);
     load(first + step, a1, 1);
   }
-  float token_logit = 0.f, token_logit1 = 0.f, loss = 0.f;
-  if (a >= 0) token_logit = sum_row(first, 0, xa, xe);
+  float loss = 0.f;
+  if (a >= 0) sum_row(first, 0, a, xe);
   int s = 0;
   for (int64_t i = first; i < p.n; i += step) {
     const uint32_t word3 = meta.load(i + 3 * step, p.n);
     const int s1 = s == 2 ? 0 : s + 1, s2 = s == 0 ? 2 : s - 1;
     MaxSum sum = ready;
-    if (a1 >= 0) token_logit1 = sum_row(i + step, s1, xa1, xe1);
+    float token_logit = ready_token;
+    if (a1 >= 0) sum_row(i + step, s1, a1, xe1);
     // The slot of the row before takes the row after next, once its gradient has left it.
     const int a2 = token_of(p, word2, i + 2 * step);
-    T xa2{}, xe2{};
-    fetch(xa2, xe2, i + 2 * step, a2);
+    T xe2{};
+    fetch(xe2, i + 2 * step, a2);
     if (lane == 0) {
       ptx::bulk_wait_read0();
       ptx::fence_async_smem();
@@ -567,6 +578,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
         const int j = read % kJoins;
         ptx::wait_fast(&joined_full[j], (read++ / kJoins) & 1u, abort_flag, p.status);
         sum = join_list(joined[j], units, k);
+        token_logit = __shfl_sync(0xffffffffu, joined_token[j], 0);  // so that it has been read before the next send
       }
       RowMeta now;
       now.w = __uint_as_float(__shfl_sync(0xffffffffu, word, 2));
@@ -621,7 +633,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
     }
     s = s1;
     word = word1, word1 = word2, word2 = word3, a = a1, a1 = a2;
-    token_logit = token_logit1, xe = xe1, xa1 = xa2, xe1 = xe2;
+    xe = xe1, xe1 = xe2;
   }
   // One term per cluster (or CTA, its warps in their order): its rows' in their order.
   if (SOLO && p.loss_terms) {
