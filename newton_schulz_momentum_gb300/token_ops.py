@@ -1,6 +1,6 @@
 """The token operators of libdmuon: what a language model's training step runs beside its matrix products, on
 the parameters that AdamW updates. Argument marshalling only: each function is one C call, enqueued on the current
-CUDA stream; all are reachable as attributes of the package.
+CUDA stream of its tensors' device, which is the same for all of them; all are reachable as attributes of the package.
 
     y = dm.embedding(table, ids, scale=64.0)                       # lookup
     grad = dm.embedding_grad(dy, ids, rows=table.shape[0])         # its dense fp32 gradient
@@ -24,13 +24,34 @@ _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 # The current stream's address without a Stream object around it (a third of a small call's time), where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _stream(stream, t):
-    """Address of `stream`, by default the current one of t's device."""
+def _stream(stream, dev):
+    """Address of `stream`, by default the current one of device `dev`."""
     if stream is None:
-        return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+        return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _elsewhere(call, dev, *args):
+    """call(*args) with device `dev` current: the library works on the current one."""
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _device(t, name):
+    """Index of a CUDA tensor's device."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _same_device(t, name, dev):
+    at = _device(t, name)
+    if at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, but the call's other tensors are on cuda:{dev}")
 
 
 def _code(t, name):
@@ -40,10 +61,10 @@ def _code(t, name):
     return code
 
 
-def _rows(t, name, shape=None, dtype=None):
-    """(rows, row length, row stride) of a CUDA tensor, given its expected shape and dtype."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+def _rows(t, name, dev, shape=None, dtype=None):
+    """(rows, row length, row stride) of a tensor on device `dev`, given its expected shape and dtype."""
+    if t.get_device() != dev:
+        _same_device(t, name, dev)
     size = t.shape
     if shape is not None and size != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
@@ -59,19 +80,23 @@ def _rows(t, name, shape=None, dtype=None):
     return size[0], dim, t.stride(0)
 
 
-def _vector(t, name, n, dtype=torch.float32):
-    """Device address of a contiguous CUDA tensor of n elements (None stays None)."""
+def _vector(t, name, dev, n, dtype=torch.float32):
+    """Device address of a contiguous tensor of n elements on device `dev` (None stays None)."""
     if t is None:
         return None
-    if t.numel() != n or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != dev:
+        _same_device(t, name, dev)
+    if t.numel() != n or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
     return t.data_ptr()
 
 
-def _ids(t, name, n=None):
-    """(address, bytes per id) of a list of token ids."""
+def _ids(t, name, dev, n=None):
+    """(address, bytes per id) of a list of token ids on device `dev`."""
     size = _ID_BYTES.get(t.dtype)
-    if size is None or not t.is_cuda or not t.is_contiguous():
+    if t.get_device() != dev:
+        _same_device(t, name, dev)
+    if size is None or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 or int64 CUDA tensor")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
@@ -83,71 +108,92 @@ def embedding(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     the table gives zeros, and check_status() raises ERR_INDEX."""
     if table.dim() != 2:
         raise ValueError("table must be a 2-D tensor")
-    rows, dim, ld = _rows(table, "table")
-    ptr, size = _ids(ids, "ids")
+    dev = table.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(embedding, _device(table, "table"), table, ids, scale, dtype, out, stream)
+    rows, dim, ld = _rows(table, "table", dev)
+    ptr, size = _ids(ids, "ids", dev)
     if out is None:
         out = torch.empty(ids.shape + (dim,), dtype=dtype or table.dtype, device=table.device)
         n, ldo = ids.numel(), dim
     else:
-        n, _, ldo = _rows(out, "out", ids.shape + (dim,), dtype)
-    _check(lib().dmuon_embedding(table.data_ptr(), _code(table, "table"), rows, dim, ld, ptr, size, n, scale,
-                                 out.data_ptr(), _code(out, "out"), ldo, _stream(stream, table)))
+        n, _, ldo = _rows(out, "out", dev, ids.shape + (dim,), dtype)
+    status = lib().dmuon_embedding(table.data_ptr(), _code(table, "table"), rows, dim, ld, ptr, size, n, scale,
+                                   out.data_ptr(), _code(out, "out"), ldo, _stream(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
 def embedding_grad(grad_out, ids, rows, scale=1.0, padding_idx=None, grad=None, accumulate=False, stream=None):
     """The dense fp32 gradient, rows x dim, of embedding()'s table: row v is scale times the sum of grad_out over the
     tokens of id v (none for padding_idx). Into `grad` where given: written over, or added to with accumulate."""
-    n, dim, ld = _rows(grad_out, "grad_out")
-    ptr, size = _ids(ids, "ids", n)
+    dev = grad_out.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(embedding_grad, _device(grad_out, "grad_out"), grad_out, ids, rows, scale, padding_idx,
+                          grad, accumulate, stream)
+    n, dim, ld = _rows(grad_out, "grad_out", dev)
+    ptr, size = _ids(ids, "ids", dev, n)
     if grad is None:
         if accumulate:
             raise ValueError("accumulate needs a grad to add to")
         grad = torch.empty((rows, dim), dtype=torch.float32, device=grad_out.device)
         ldg = dim
     else:
-        _, _, ldg = _rows(grad, "grad", (rows, dim), torch.float32)
-    _check(lib().dmuon_embedding_grad(grad_out.data_ptr(), _code(grad_out, "grad_out"), ld, ptr, size, n, rows, dim,
-                                      scale, -1 if padding_idx is None else padding_idx, grad.data_ptr(), ldg,
-                                      1 if accumulate else 0, _stream(stream, grad_out)))
+        _, _, ldg = _rows(grad, "grad", dev, (rows, dim), torch.float32)
+    status = lib().dmuon_embedding_grad(grad_out.data_ptr(), _code(grad_out, "grad_out"), ld, ptr, size, n, rows, dim,
+                                        scale, -1 if padding_idx is None else padding_idx, grad.data_ptr(), ldg,
+                                        1 if accumulate else 0, _stream(stream, dev))
+    if status:
+        _check(status)
     return grad
 
 
-def _norm_args(x, residual, gain, h):
-    n, dim, ldx = _rows(x, "x")
+def _norm_args(dev, x, residual, gain, h):
+    n, dim, ldx = _rows(x, "x", dev)
     ldr, ldh, hp = 0, 0, None
     if residual is not None:
-        _, _, ldr = _rows(residual, "residual", x.shape, x.dtype)
+        _, _, ldr = _rows(residual, "residual", dev, x.shape, x.dtype)
         if h is None:
             h, ldh = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
             hp = h.data_ptr()
     if hp is None and h is not None:
-        _, _, ldh = _rows(h, "h", x.shape, x.dtype)
+        _, _, ldh = _rows(h, "h", dev, x.shape, x.dtype)
         hp = h.data_ptr()
-    return (n, dim, h, (x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, _code(x, "x"),
-                        _vector(gain, "gain", dim), n, dim), (hp, ldh))
+    return (dim, h, (x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, _code(x, "x"),
+                     _vector(gain, "gain", dev, dim), n, dim), (hp, ldh))
 
 
 def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, y=None, h=None, stream=None):
     """(y, h) with h = x + residual and y = gain * h / sqrt(mean(h^2) + eps) over the last dimension, both of x's
     dtype. Without a residual h is x itself. `h` may be x or residual, to update the residual stream in place."""
-    n, dim, h, head, tail = _norm_args(x, residual, gain, h)
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(add_rmsnorm, _device(x, "x"), x, residual, gain, eps, y, h, stream)
+    dim, h, head, tail = _norm_args(dev, x, residual, gain, h)
     if y is None:
         y, ldy = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
     else:
-        _, _, ldy = _rows(y, "y", x.shape, x.dtype)
-    _check(lib().dmuon_add_rmsnorm(*head, eps, *tail, y.data_ptr(), head[4], ldy, None, 0, _stream(stream, x)))
+        _, _, ldy = _rows(y, "y", dev, x.shape, x.dtype)
+    status = lib().dmuon_add_rmsnorm(*head, eps, *tail, y.data_ptr(), head[4], ldy, None, 0, _stream(stream, dev))
+    if status:
+        _check(status)
     return y, (x if h is None else h)
 
 
 def add_rmsnorm_fp8(x, residual=None, gain=None, eps=1e-6, group=128, h=None, stream=None):
     """(q, scales, h): add_rmsnorm with y in 8 bits. Each `group` of columns (32, 64, 128 or 256; 0 for the whole row) is
     held as q = float8_e4m3fn(y / scale) with scale = max |y| / 448, fp32, shaped x.shape[:-1] + (groups,)."""
-    n, dim, h, head, tail = _norm_args(x, residual, gain, h)
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(add_rmsnorm_fp8, _device(x, "x"), x, residual, gain, eps, group, h, stream)
+    dim, h, head, tail = _norm_args(dev, x, residual, gain, h)
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty(x.shape[:-1] + (-(-dim // group) if group else 1,), dtype=torch.float32, device=x.device)
-    _check(lib().dmuon_add_rmsnorm(*head, eps, *tail, q.data_ptr(), E4M3, dim, scales.data_ptr(), group,
-                                   _stream(stream, x)))
+    status = lib().dmuon_add_rmsnorm(*head, eps, *tail, q.data_ptr(), E4M3, dim, scales.data_ptr(), group,
+                                     _stream(stream, dev))
+    if status:
+        _check(status)
     return q, scales, (x if h is None else h)
 
 
@@ -155,20 +201,26 @@ def add_rmsnorm_grad(dy, h, gain=None, dh=None, eps=1e-6, dx=None, dgain=None, a
     """(dx, dgain) of add_rmsnorm at its h: dx is the gradient of x and of residual alike, `dh` (the gradient that
     reaches h itself) included; dgain is fp32, or None without a gain. dx may be dy or dh. With accumulate the gain's
     gradient is added to `dgain`."""
-    n, dim, ldy = _rows(dy, "dy")
-    _, _, ldh = _rows(h, "h", dy.shape, dy.dtype)
-    lddh = 0 if dh is None else _rows(dh, "dh", dy.shape, dy.dtype)[2]
+    dev = dy.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(add_rmsnorm_grad, _device(dy, "dy"), dy, h, gain, dh, eps, dx, dgain, accumulate, stream)
+    n, dim, ldy = _rows(dy, "dy", dev)
+    _, _, ldh = _rows(h, "h", dev, dy.shape, dy.dtype)
+    lddh = 0 if dh is None else _rows(dh, "dh", dev, dy.shape, dy.dtype)[2]
     if dx is None:
         dx, lddx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device), dim
     else:
-        _, _, lddx = _rows(dx, "dx", dy.shape, dy.dtype)
+        _, _, lddx = _rows(dx, "dx", dev, dy.shape, dy.dtype)
     if dgain is None and gain is not None:
         if accumulate:
             raise ValueError("accumulate needs a dgain to add to")
         dgain = torch.empty(dim, dtype=torch.float32, device=dy.device)
-    _check(lib().dmuon_add_rmsnorm_grad(dy.data_ptr(), ldy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(),
-                                        lddh, _code(dy, "dy"), _vector(gain, "gain", dim), n, dim, eps, dx.data_ptr(),
-                                        lddx, _vector(dgain, "dgain", dim), 1 if accumulate else 0, _stream(stream, dy)))
+    status = lib().dmuon_add_rmsnorm_grad(dy.data_ptr(), ldy, h.data_ptr(), ldh, None if dh is None else dh.data_ptr(),
+                                          lddh, _code(dy, "dy"), _vector(gain, "gain", dev, dim), n, dim, eps,
+                                          dx.data_ptr(), lddx, _vector(dgain, "dgain", dev, dim),
+                                          1 if accumulate else 0, _stream(stream, dev))
+    if status:
+        _check(status)
     return dx, dgain
 
 
@@ -180,8 +232,12 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
     weights holds mask and mean (1 / number of tokens, and 0 for a prompt's or padding's); a row of weight 0 or with a
     negative target is not read. dlogits may be a tensor to write into (the logits themselves among them), or False
     for the loss alone."""
-    n, vocab, ld = _rows(logits, "logits")
-    ptr, size = _ids(targets, "targets", n)
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(policy_loss, _device(logits, "logits"), logits, targets, old_logp, advantages, weights,
+                          ref_logp, clip_low, clip_high, kl_coef, temperature, dlogits, stream)
+    n, vocab, ld = _rows(logits, "logits", dev)
+    ptr, size = _ids(targets, "targets", dev, n)
     ldd, dptr = 0, None
     if dlogits is None:
         dlogits, ldd = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), vocab
@@ -189,23 +245,30 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
     elif dlogits is False:
         dlogits = None
     else:
-        _, _, ldd = _rows(dlogits, "dlogits", logits.shape, logits.dtype)
+        _, _, ldd = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
         dptr = dlogits.data_ptr()
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
     logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    _check(lib().dmuon_policy_loss(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size,
-                                   _vector(old_logp, "old_logp", n), _vector(ref_logp, "ref_logp", n),
-                                   _vector(advantages, "advantages", n), _vector(weights, "weights", n), clip_low,
-                                   clip_high, kl_coef, temperature, loss.data_ptr(), logp.data_ptr(), dptr, ldd,
-                                   _stream(stream, logits)))
+    status = lib().dmuon_policy_loss(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size,
+                                     _vector(old_logp, "old_logp", dev, n), _vector(ref_logp, "ref_logp", dev, n),
+                                     _vector(advantages, "advantages", dev, n), _vector(weights, "weights", dev, n),
+                                     clip_low, clip_high, kl_coef, temperature, loss.data_ptr(), logp.data_ptr(), dptr,
+                                     ldd, _stream(stream, dev))
+    if status:
+        _check(status)
     return loss, logp, dlogits
 
 
 def token_logprobs(logits, targets, temperature=1.0, stream=None):
     """log softmax(logits / temperature)[targets], fp32, shaped like targets; 0 where a target is negative."""
-    n, vocab, ld = _rows(logits, "logits")
-    ptr, size = _ids(targets, "targets", n)
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(token_logprobs, _device(logits, "logits"), logits, targets, temperature, stream)
+    n, vocab, ld = _rows(logits, "logits", dev)
+    ptr, size = _ids(targets, "targets", dev, n)
     logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    _check(lib().dmuon_token_logprobs(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size, temperature,
-                                      logp.data_ptr(), _stream(stream, logits)))
+    status = lib().dmuon_token_logprobs(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size,
+                                        temperature, logp.data_ptr(), _stream(stream, dev))
+    if status:
+        _check(status)
     return logp

@@ -1,7 +1,9 @@
 """CPU checks of the token operators' host side: what needs no GPU to be seen."""
 
+import contextlib
 import os
 import re
+import types
 
 import pytest
 
@@ -24,3 +26,108 @@ def test_entries_let_no_exception_out(name):
     leaves a C function ends the process."""
     body = entry_body(name).strip()
     assert body.startswith("try {") and "catch (const std::exception" in body
+
+
+class Stub:
+    """What the wrappers ask of a tensor, on a device that need not exist."""
+
+    def __init__(self, *shape, dtype=None, device=0):
+        import torch
+        self.shape, self.dtype, self.index = torch.Size(shape), dtype or torch.float32, device
+        self.device, self.is_cuda = (f"cuda:{device}", True) if device >= 0 else ("cpu", False)
+
+    def get_device(self):
+        return self.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 4096
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The entry points' calls, as (name, device that was current, stream), with device 0 current at first."""
+    torch = pytest.importorskip("torch")
+    from newton_schulz_momentum_gb300 import token_ops
+    current, made = [0], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, current[0] = current[0], index
+        yield
+        current[0] = before
+
+    def entry(name):
+        def call(*args):
+            made.append((name, current[0], args[-1]))
+            return 0
+        return call
+
+    monkeypatch.setattr(token_ops, "lib", lambda: types.SimpleNamespace(**{n: entry(n) for n in ENTRIES}))
+    if hasattr(token_ops, "_current_device"):
+        monkeypatch.setattr(token_ops, "_current_device", lambda: current[0])
+    monkeypatch.setattr(token_ops, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch, "empty", lambda *shape, dtype=None, device=None: Stub(
+        *(shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape), dtype=dtype,
+        device=int(device.split(":")[1])))
+    return made
+
+
+def all_calls(at, odd=None):
+    """One call of each function with every tensor on device `at`, but for argument `odd` of (function, argument)."""
+    import torch
+    from newton_schulz_momentum_gb300 import token_ops as ops
+    i64, n, d = torch.int64, 4, 8
+    kinds = {
+        "embedding": dict(table=(9, d), ids=(n, i64), out=(n, d)),
+        "embedding_grad": dict(grad_out=(n, d), ids=(n, i64), grad=(9, d)),
+        "add_rmsnorm": dict(x=(n, d), residual=(n, d), gain=(d,), y=(n, d), h=(n, d)),
+        "add_rmsnorm_fp8": dict(x=(n, d), residual=(n, d), gain=(d,), h=(n, d)),
+        "add_rmsnorm_grad": dict(dy=(n, d), h=(n, d), gain=(d,), dh=(n, d), dx=(n, d), dgain=(d,)),
+        "policy_loss": dict(logits=(n, d), targets=(n, i64), old_logp=(n,), advantages=(n,), weights=(n,), ref_logp=(n,),
+                            dlogits=(n, d)),
+        "token_logprobs": dict(logits=(n, d), targets=(n, i64)),
+    }
+    for name, shapes in kinds.items():
+        if odd is not None and odd[0] != name:
+            continue
+        args = {}
+        for arg, shape in shapes.items():
+            dtype = shape[-1] if isinstance(shape[-1], torch.dtype) else torch.float32
+            sizes = [v for v in shape if isinstance(v, int)]
+            args[arg] = Stub(*sizes, dtype=dtype, device=odd[2] if odd is not None and odd[1] == arg else at)
+        if name == "embedding_grad":
+            args["rows"] = 9
+        yield name, args, lambda fn=getattr(ops, name), a=args: fn(**a)
+
+
+def test_calls_run_on_their_tensors_device(calls):
+    """The library launches on the current device: the tensors' device is made current around the call."""
+    for at in (0, 1):
+        for name, _, call in all_calls(at):
+            del calls[:]
+            call()
+            assert [c[1:] for c in calls] == [(at, 100 + at)], name
+
+
+def test_tensors_of_two_devices_are_refused(calls):
+    """Every tensor argument of every function is looked at; a refused call reaches no entry point."""
+    seen = 0
+    for name, args, _ in list(all_calls(1)):
+        for arg in [a for a in args if isinstance(args[a], Stub)]:
+            for where, word in ((0, "cuda"), (-1, "CUDA")):
+                ((_, _, call),) = all_calls(1, odd=(name, arg, where))
+                with pytest.raises(ValueError, match=word):
+                    call()
+                assert not calls
+                seen += 1
+    assert seen == 2 * 30
