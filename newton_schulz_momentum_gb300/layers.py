@@ -6,12 +6,14 @@ table, its norms and its loss. All arithmetic runs in libdmuon's kernels (token_
     y, h = self.norm(x, h)                     # h + x, and its norm
     loss, logp = dm.PolicyLoss(kl_coef=0.05)(logits, targets, old_logp, advantages, weights, ref_logp)
 
-Parameters are fp32, as Muon asks; activations fp32 or bf16. Muon gives all of these parameters to AdamW.
+Parameters are fp32, as Muon asks; activations fp32 or bf16. Muon gives all of these parameters to AdamW. Gradients are of
+first order: differentiating them again raises an error.
 """
 
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import token_ops
 
@@ -25,6 +27,7 @@ class _Lookup(torch.autograd.Function):
         return token_ops.embedding(table, ids, scale, dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad):
         (ids,) = ctx.saved_tensors
         return (token_ops.embedding_grad(grad.contiguous(), ids, ctx.rows, ctx.scale, ctx.padding_idx), None, None, None,
@@ -53,6 +56,7 @@ class _AddNorm(torch.autograd.Function):
         return (y, h.view_as(h)) if ctx.alone else (y, h)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh):
         h, gain = ctx.saved_tensors
         if dy is None:
@@ -84,6 +88,7 @@ class _Policy(torch.autograd.Function):
         return loss, logp
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dloss, _):
         logits, targets, old_logp, advantages, weights, ref_logp = ctx.saved_tensors
         # The gradient is linear in the weights, so what arrives from behind the loss goes into them.

@@ -131,3 +131,54 @@ def test_tensors_of_two_devices_are_refused(calls):
                 assert not calls
                 seen += 1
     assert seen == 2 * 30
+
+
+@pytest.fixture
+def plain_kernels(monkeypatch):
+    """The functions behind the modules, in torch on the CPU."""
+    torch = pytest.importorskip("torch")
+    from newton_schulz_momentum_gb300 import token_ops
+
+    def norm(x, residual, gain, eps):
+        h = x if residual is None else x + residual
+        return h * torch.rsqrt((h * h).mean(-1, keepdim=True) + eps) * gain, h
+
+    def norm_grad(dy, h, gain, dh, eps):
+        rho = torch.rsqrt((h * h).mean(-1, keepdim=True) + eps)
+        d = dy * gain
+        dx = rho * d - h * rho ** 3 * (d * h).mean(-1, keepdim=True) + (0 if dh is None else dh)
+        return dx, (dy * h * rho).sum(0)
+
+    def loss(logits, targets, old, adv, weights, ref, dlogits=None, **options):
+        p = torch.softmax(logits, 1)
+        return (p[:, 0] * weights).sum(), p[:, 0], None if dlogits is False else p * weights[:, None]
+
+    def grad(dy, ids, rows, scale, pad):
+        return torch.zeros(rows, dy.shape[-1]).index_add(0, ids, dy * scale)
+
+    for name, fn in (("embedding", lambda table, ids, scale, dtype: (scale * table[ids]).to(dtype)),
+                     ("embedding_grad", grad), ("add_rmsnorm", norm), ("add_rmsnorm_grad", norm_grad),
+                     ("policy_loss", loss)):
+        monkeypatch.setattr(token_ops, name, fn)
+    return torch
+
+
+def test_second_derivatives_raise(plain_kernels):
+    """The backward passes are not differentiable themselves: a gradient penalty gets an error, not a gradient without
+    its terms. First derivatives are as before, with create_graph too."""
+    torch = plain_kernels
+    from newton_schulz_momentum_gb300 import layers
+    torch.manual_seed(0)
+    n, d = 5, 8
+    ids = torch.tensor([0, 2, 2, 1, 0])
+    embed, norm = layers.Embedding(3, d, scale=2.0, device="cpu"), layers.AddRMSNorm(d, device="cpu")
+    x = torch.randn(n, d, requires_grad=True)
+    v = torch.rand(n) + 0.5
+    for out, by in ((embed(ids), embed.weight), (norm(x)[0], x), (norm(x, x.detach())[0], norm.weight),
+                    (layers.PolicyLoss()(x, ids, v, v, v)[0], x)):
+        total = (out.double() ** 3).sum()
+        (want,) = torch.autograd.grad(total, by, retain_graph=True)
+        (got,) = torch.autograd.grad(total, by, create_graph=True)
+        assert torch.equal(want, got.detach())
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            got.pow(2).sum().backward()
