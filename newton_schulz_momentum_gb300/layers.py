@@ -41,6 +41,16 @@ class Embedding(torch.nn.Embedding):
         super().__init__(num_embeddings, embedding_dim, padding_idx=padding_idx, device=device, dtype=torch.float32)
         self.scale, self.out_dtype = float(scale), dtype or torch.float32
 
+    @classmethod
+    def from_pretrained(cls, embeddings, freeze=True, padding_idx=None, scale=1.0, dtype=None):
+        """The module over an fp32 table of its own, which is not copied; without a gradient if `freeze`."""
+        if embeddings.dim() != 2 or embeddings.dtype != torch.float32:
+            raise ValueError("embeddings must be a 2-D float32 tensor")
+        rows, dim = embeddings.shape
+        embed = cls(rows, dim, padding_idx=padding_idx, scale=scale, dtype=dtype, device="meta")
+        embed.weight = torch.nn.Parameter(embeddings, requires_grad=not freeze)
+        return embed
+
     def forward(self, ids):
         return _Lookup.apply(self.weight, ids, self.scale, self.out_dtype, self.padding_idx)
 

@@ -182,3 +182,20 @@ def test_second_derivatives_raise(plain_kernels):
         assert torch.equal(want, got.detach())
         with pytest.raises(RuntimeError, match="once_differentiable"):
             got.pow(2).sum().backward()
+
+
+def test_embedding_from_pretrained(plain_kernels):
+    """torch.nn.Embedding's constructor from a table, with this module's own options."""
+    torch = plain_kernels
+    from newton_schulz_momentum_gb300 import layers
+    table = torch.arange(12.0).view(4, 3)
+    embed = layers.Embedding.from_pretrained(table, padding_idx=-1, scale=3.0, dtype=torch.bfloat16)
+    assert embed.weight.data_ptr() == table.data_ptr() and not embed.weight.requires_grad and embed.padding_idx == 3
+    assert torch.equal(embed(torch.tensor([2, 0])), (3.0 * table[[2, 0]]).bfloat16())
+    embed = layers.Embedding.from_pretrained(table, freeze=False)
+    assert embed.weight.requires_grad and embed.padding_idx is None and embed(torch.tensor([1])).dtype == torch.float32
+    assert (embed.num_embeddings, embed.embedding_dim) == (4, 3)
+    with pytest.raises(ValueError, match="2-D"):
+        layers.Embedding.from_pretrained(table[0])
+    with pytest.raises(ValueError, match="float32"):
+        layers.Embedding.from_pretrained(table.bfloat16())
