@@ -347,7 +347,8 @@ DMUON_API int dmuon_embedding_grad(const void* grad_out, int grad_dtype, int64_t
 /*
  * dmuon_add_rmsnorm -- h = x + residual; y = h * (mean over the row of h^2 + eps)^(-1/2) * gain.
  *   x, residual, h  device, n x dim, `dtype` (fp32 or bf16). residual NULL: h = x. h NULL: not stored. h may
- *                   be x or residual. The norm is formed from h before its rounding to `dtype`.
+ *                   be x or residual, and so may y of their type, with their leading dimension (if n > 1). The norm
+ *                   is formed from h before its rounding to `dtype`.
  *   gain            device, dim, fp32; NULL: ones
  *   y               device, n x dim, y_dtype: `dtype`, or DMUON_E4M3 with scales
  *   scales          device, n x ceil(dim / group) fp32, or NULL. Columns [k group, (k + 1) group) of a row hold
@@ -363,7 +364,8 @@ DMUON_API int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual
  * d = dy * gain,
  *   dx = dh + rho d - h rho^3 / dim * sum over the row of d h   (the gradient of x and of residual alike)
  *   dgain (+)= sum over the rows of dy h rho
- *   dy, h, dh, dx  device, n x dim, `dtype`; dh (the gradient of the stored h) may be NULL; dx may be dy or dh
+ *   dy, h, dh, dx  device, n x dim, `dtype`; dh (the gradient of the stored h) may be NULL; dx may be dy or
+ *                  dh, with its leading dimension (if n > 1)
  *   gain, dgain    device, dim, fp32; either may be NULL (ones; not wanted). accumulate != 0 adds to dgain.
  */
 DMUON_API int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t ldh, const void* dh,

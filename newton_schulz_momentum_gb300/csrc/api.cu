@@ -1255,7 +1255,16 @@ int check_elements(const char* name, const void* ptr, int dtype, int64_t ld, int
   return DMUON_OK;
 }
 
-// While it lives, this thread may allocate and free although a stream is being captured: neither is work of the capture.
+// An output may go over an input row by row: with another stride its rows would fall on rows not yet read.
+int check_in_place(const char* out_name, const void* out, int64_t ld_out, const char* in_name, const void* in,
+                   int64_t ld_in, int64_t n) {
+  if (out && out == in && ld_out != ld_in && n > 1)
+    return fail(DMUON_ERR_INVALID_ARG, "%s is written over %s, so their leading dimensions must be equal", out_name,
+                in_name);
+  return DMUON_OK;
+}
+
+// While it lives, this thread may allocate and free although a stream is being captured: neither is the capture's work.
 class RelaxedCapture {
  public:
   RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
@@ -1286,7 +1295,8 @@ int hold_by_graph(TokenBlock& block, cudaGraph_t graph) {
 // Frees the blocks that `which` names. No work that uses them is left.
 template <typename F>
 void free_token_blocks(DeviceState& ds, F&& which) {
-  if (std::none_of(ds.token_blocks.begin(), ds.token_blocks.end(), [&](const TokenBlock* b) { return which(*b); })) return;
+  const auto named = [&](const TokenBlock* b) { return which(*b); };
+  if (std::none_of(ds.token_blocks.begin(), ds.token_blocks.end(), named)) return;
   RelaxedCapture relaxed;
   size_t kept = 0;
   for (TokenBlock* b : ds.token_blocks) {
@@ -1380,8 +1390,8 @@ int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** 
     }
     if (g_ws_limit) {
       if (held() + need > g_ws_limit)
-        return fail(DMUON_ERR_OOM, "workspace of %zu bytes beside the %zu that graphs hold exceeds the limit of %zu", need,
-                    held(), g_ws_limit);
+        return fail(DMUON_ERR_OOM, "workspace of %zu bytes beside the %zu that graphs hold exceeds the limit of %zu",
+                    need, held(), g_ws_limit);
       want = std::min(want, g_ws_limit - held());
     }
     const int st = new_token_block(ds, need, want, &block);
@@ -1856,6 +1866,8 @@ int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
     if (st == DMUON_OK) st = check_elements("x", x, dtype, ldx, dim, n);
     if (st == DMUON_OK && residual) st = check_elements("residual", residual, dtype, ldr, dim, n);
     if (st == DMUON_OK && h) st = check_elements("h", h, dtype, ldh, dim, n);
+    if (st == DMUON_OK) st = check_in_place("h", h, ldh, "x", x, ldx, n);
+    if (st == DMUON_OK) st = check_in_place("h", h, ldh, "residual", residual, ldr, n);
     if (st != DMUON_OK) return st;
     if (y_dtype == DMUON_E4M3) {
       if (n > 0 && (!y || !scales)) return fail(DMUON_ERR_INVALID_ARG, "y and scales must not be NULL");
@@ -1864,10 +1876,14 @@ int dmuon_add_rmsnorm(const void* x, int64_t ldx, const void* residual, int64_t 
         return fail(DMUON_ERR_INVALID_ARG, "group must be 32, 64, 128, 256 or 0 (one scale per row), got %lld",
                     (long long)group);
       if (!aligned_to(scales, 4)) return fail(DMUON_ERR_INVALID_ARG, "scales must be 4-byte aligned");
+      if (n > 0 && (y == x || y == residual || y == h))
+        return fail(DMUON_ERR_INVALID_ARG, "y cannot go over x, residual or h with another type");
     } else {
       if (y_dtype != dtype) return fail(DMUON_ERR_INVALID_ARG, "y_dtype must be dtype or DMUON_E4M3 (2)");
       if (scales) return fail(DMUON_ERR_INVALID_ARG, "scales must be NULL unless y_dtype is DMUON_E4M3 (2)");
       st = check_elements("y", y, dtype, ldy, dim, n);
+      if (st == DMUON_OK) st = check_in_place("y", y, ldy, "x", x, ldx, n);
+      if (st == DMUON_OK) st = check_in_place("y", y, ldy, "residual", residual, ldr, n);
       if (st != DMUON_OK) return st;
     }
     if (!aligned_to(gain, 4)) return fail(DMUON_ERR_INVALID_ARG, "gain must be 4-byte aligned");
@@ -1898,6 +1914,8 @@ int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t 
     if (st == DMUON_OK) st = check_elements("h", h, dtype, ldh, dim, n);
     if (st == DMUON_OK && dh) st = check_elements("dh", dh, dtype, lddh, dim, n);
     if (st == DMUON_OK) st = check_elements("dx", dx, dtype, lddx, dim, n);
+    if (st == DMUON_OK) st = check_in_place("dx", dx, lddx, "dy", dy, lddy, n);
+    if (st == DMUON_OK) st = check_in_place("dx", dx, lddx, "dh", dh, lddh, n);
     if (st != DMUON_OK) return st;
     if (!aligned_to(gain, 4) || !aligned_to(dgain, 4))
       return fail(DMUON_ERR_INVALID_ARG, "gain and dgain must be 4-byte aligned");
@@ -1937,6 +1955,7 @@ int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int6
     if (st == DMUON_OK) st = check_ids(targets, id_bytes, n);
     if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
     if (st == DMUON_OK && dlogits) st = check_elements("dlogits", dlogits, dtype, ldd, vocab, n);
+    if (st == DMUON_OK) st = check_in_place("dlogits", dlogits, ldd, "logits", logits, ld, n);
     if (st != DMUON_OK) return st;
     if (!loss || (n > 0 && (!old_logp || !advantages || !weights)))
       return fail(DMUON_ERR_INVALID_ARG, "old_logp, advantages, weights and loss must not be NULL");

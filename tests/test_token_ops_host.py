@@ -199,3 +199,28 @@ def test_embedding_from_pretrained(plain_kernels):
         layers.Embedding.from_pretrained(table[0])
     with pytest.raises(ValueError, match="float32"):
         layers.Embedding.from_pretrained(table.bfloat16())
+
+
+A, B, C = 0x10000, 0x20000, 0x30000  # 16-byte aligned addresses, never read
+
+
+@pytest.mark.parametrize("entry,args,word", [
+    # logits, dtype, ld, n, vocab, targets, id_bytes, old, ref, adv, weights, lo, hi, kl, temp, loss, logp, dlogits, ldd
+    ("dmuon_policy_loss", (A, 1, 16, 4, 16, B, 8, C, C, C, C, 0.2, 0.2, 0.1, 1.0, C, B, A, 24), "logits"),
+    # x, ldx, residual, ldr, dtype, gain, n, dim, eps, h, ldh, y, y_dtype, ldy, scales, group
+    ("dmuon_add_rmsnorm", (A, 8, B, 8, 1, None, 4, 8, 1e-6, A, 9, C, 1, 8, None, 0), "h is written over x"),
+    ("dmuon_add_rmsnorm", (A, 8, B, 8, 1, None, 4, 8, 1e-6, B, 16, C, 1, 8, None, 0), "h is written over residual"),
+    ("dmuon_add_rmsnorm", (A, 8, B, 8, 1, None, 4, 8, 1e-6, None, 0, A, 1, 9, None, 0), "y is written over x"),
+    ("dmuon_add_rmsnorm", (A, 8, B, 16, 1, None, 4, 8, 1e-6, None, 0, B, 1, 8, None, 0), "y is written over residual"),
+    ("dmuon_add_rmsnorm", (A, 8, B, 8, 1, None, 1, 8, 1e-6, None, 0, A, 2, 8, C, 0), "another type"),
+    # dy, lddy, h, ldh, dh, lddh, dtype, gain, n, dim, eps, dx, lddx, dgain, accumulate
+    ("dmuon_add_rmsnorm_grad", (A, 8, B, 8, C, 8, 0, None, 4, 8, 1e-6, A, 12, None, 0), "dx is written over dy"),
+    ("dmuon_add_rmsnorm_grad", (A, 8, B, 8, C, 8, 0, None, 4, 8, 1e-6, C, 12, None, 0), "dx is written over dh")])
+def test_rows_in_place_with_another_stride_are_refused(entry, args, word):
+    """Rows of the output would fall on input rows that are still to be read."""
+    import newton_schulz_momentum_gb300 as dm
+    from newton_schulz_momentum_gb300 import build
+    build.build()
+    rc = getattr(dm.lib(), entry)(*args, None)
+    message = dm.lib().dmuon_last_error().decode()
+    assert rc == dm.ERR_INVALID_ARG and word in message, (rc, message)
