@@ -280,8 +280,10 @@ DMUON_API int dmuon_adamw_step(int count, float* const* params, const void* cons
  * dmuon_check_status -- synchronise `cuda_stream`, then read and clear the device status word.
  * Returns DMUON_OK, DMUON_ERR_TIMEOUT (a kernel's bounded wait gave up: its results are invalid),
  * DMUON_ERR_RANGE (checked build: an index or tile outside its table or matrix was found and skipped;
- * results are invalid), DMUON_ERR_NONFINITE (an fp16 intermediate overflowed or was NaN) or
- * DMUON_ERR_CUDA (an asynchronous CUDA error surfaced during synchronisation).
+ * results are invalid), DMUON_ERR_NONFINITE (an fp16 intermediate overflowed or was NaN), DMUON_ERR_INDEX (a
+ * token id lay outside its table or vocabulary and its row was skipped) or DMUON_ERR_CUDA (an asynchronous
+ * CUDA error surfaced during synchronisation). Of several the first in this order is returned; DMUON_ERR_INDEX
+ * then stays for the next call.
  */
 DMUON_API int dmuon_check_status(void* cuda_stream);
 

@@ -1688,14 +1688,17 @@ int dmuon_check_status(void* cuda_stream) {
   DM_CUDA(cudaStreamSynchronize(static_cast<cudaStream_t>(cuda_stream)), "cudaStreamSynchronize");
   unsigned word = 0;
   DM_CUDA(cudaMemcpy(&word, ds->status, sizeof(word), cudaMemcpyDeviceToHost), "read device status");
-  if (word) DM_CUDA(cudaMemset(ds->status, 0, sizeof(unsigned)), "clear device status");
+  // An error of the results' own comes first; the index is then left for the next check.
+  const unsigned later = word & ~kDevIndex ? word & kDevIndex : 0u;
+  if (word)
+    DM_CUDA(cudaMemcpy(ds->status, &later, sizeof(later), cudaMemcpyHostToDevice), "clear device status");
   if (word & kDevTimeout) return fail(DMUON_ERR_TIMEOUT, "a device-side bounded wait gave up; results are invalid");
   if (word & kDevRange)
     return fail(DMUON_ERR_RANGE, "a device-side range check failed (checked build): an index or tile outside its "
                                  "table or matrix was skipped; results are invalid");
+  if (word & kDevNonfinite) return fail(DMUON_ERR_NONFINITE, "an fp16 intermediate overflowed or was NaN");
   if (word & kDevIndex)
     return fail(DMUON_ERR_INDEX, "a token id lies outside its table or vocabulary; its row was skipped");
-  if (word & kDevNonfinite) return fail(DMUON_ERR_NONFINITE, "an fp16 intermediate overflowed or was NaN");
   return DMUON_OK;
 }
 
