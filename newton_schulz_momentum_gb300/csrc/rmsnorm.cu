@@ -41,9 +41,13 @@ constexpr int kHugeThreads = 576;  // of two CTAs per SM that hold 16 elements o
 constexpr float kFp8Max = 448.f;  // largest finite e4m3
 constexpr float kMinScale = 1.17549435e-38f;
 
+// top / 448, rounded once, for the bits of a group's largest |y|: the product with 1 / 448 held in two parts (Brisebarre,
+// Muller and Raina, "Accelerating correctly rounded floating-point division when the divisor is known in advance",
+// 2004; equal to the quotient for all 2^23 significands). The bound on the second part keeps an infinity one.
 __device__ __forceinline__ float scale_of(unsigned top_bits) {
-  const float top = __uint_as_float(top_bits);
-  return top == 0.f ? 1.f : (top < kFp8Max * kMinScale ? kMinScale : top * (1.f / kFp8Max));
+  constexpr float kHigh = 0x1.24924ap-9f, kLow = -0x1.b6db6ep-34f;
+  const float top = __uint_as_float(top_bits), quotient = fmaf(top, kHigh, fmaxf(top * kLow, -1e38f));
+  return top == 0.f ? 1.f : (top < kFp8Max * kMinScale ? kMinScale : quotient);
 }
 
 // Largest |y| of the block as the bits of a non-negative float; a NaN is larger than every number.
@@ -145,7 +149,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return c;
 }
 
-// Within one unit of the last place, against e4m3's four significant bits.
+// Within one unit of the last place, against e4m3's four significant bits: a quotient by the scale is within 2^-22 of
+// itself, so a value that close to a border between two e4m3 numbers may fall on its other side (__fdiv_rn for the scale
+// and __frcp_rn here, within 2^-23: 67108 x 1000 bf16 82 -> 92 us). The same for every layout, so that the bytes are.
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -642,7 +648,7 @@ __global__ void __launch_bounds__(kMaxThreads) add_rmsnorm_kernel(const RmsNormL
     unsigned top = 0;
     for (int64_t c = begin + threadIdx.x; c < end; c += threads) top = max(top, __float_as_uint(fabsf(value(c))));
     const float scale = scale_of(block_top(top, redu));
-    const float inv = __frcp_rn(scale);
+    const float inv = reciprocal(scale);
     if (threadIdx.x == 0) p.scales[i * parts + k] = scale;
     for (int64_t c = begin + threadIdx.x; c < end; c += threads) {
       const float v = row::to_f(x[c]) + (r ? row::to_f(r[c]) : 0.f);
