@@ -1939,10 +1939,13 @@ int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h, int64_t 
     p.gain = gain, p.n = n, p.dim = dim, p.eps = eps;
     p.dx = dx, p.lddx = lddx, p.dgain = dgain, p.accumulate = accumulate != 0;
     char* ws = nullptr;
-    st = token_workspace(*ds, rmsnorm_grad_workspace(p, ds->sms, nullptr), stream, &ws);
+    p.partials = p.rho = nullptr;
+    DM_CUDA(plan_add_rmsnorm_grad(p, ds->sms), "RMS norm gradient occupancy");
+    st = token_workspace(*ds, rmsnorm_grad_workspace(p, nullptr), stream, &ws);
     if (st != DMUON_OK) return st;
-    rmsnorm_grad_workspace(p, ds->sms, ws);
-    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm_grad(p, ds->sms, stream); }), "RMS norm gradient launch");
+    rmsnorm_grad_workspace(p, ws);
+    DM_CUDA(timed(kClsRmsNorm, stream, [&] { return launch_add_rmsnorm_grad(p, ds->sms, stream); }),
+            "RMS norm gradient launch");
     return DMUON_OK;
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());

@@ -386,14 +386,17 @@ struct RmsNormGradLaunch {
   float* dgain;  // may be null
   int accumulate;
   float *partials, *rho;  // workspace, set by rmsnorm_grad_workspace
-  // Set by launch_add_rmsnorm_grad: threads per row, rows of partials; from one row of a thread to its next, rows and
-  // elements of each array.
+  // Set by plan_add_rmsnorm_grad: threads per row, rows of partials and of rho; from one row of a thread to its next,
+  // rows and elements of each array.
+  int planning;
   int tpr, npartials;
   float inv_dim;
-  int64_t step, step_dy, step_h, step_dh, step_dx;
+  int64_t rhos, step, step_dy, step_h, step_dh, step_dx;
 };
-// Workspace bytes; also places the buffers at `ws` (null when asked for the size alone).
-int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, int sms, char* ws);
+// Chooses the launches, which fixes what they need of the workspace.
+cudaError_t plan_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms);
+// Workspace bytes of a planned launch; with `ws` it also places the buffers there.
+int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, char* ws);
 cudaError_t launch_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream);
 
 struct PolicyLaunch {

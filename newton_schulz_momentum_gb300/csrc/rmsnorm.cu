@@ -858,18 +858,21 @@ cudaError_t launch_grad_rows(RmsNormGradLaunch& p, int granules, int sms, cudaSt
   const int tpr = std::max(row_threads(granules, K), EDGES ? 16 : 1), rows = tpr >= kThreads ? 1 : kThreads / tpr;
   const size_t smem = (rows > 1 ? static_cast<size_t>(p.dim) * 4 : 0) +
                       (REGS ? 0 : static_cast<size_t>(rows) * K * tpr * kPer<T> * 4 * 2);
-  if (smem > kPlainSmem) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (p.planning) {
+    if (smem > kPlainSmem) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    RowGrid g;
+    const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
     if (e != cudaSuccess) return e;
+    p.tpr = tpr;
+    p.step = static_cast<int64_t>(g.ctas) * rows;
+    p.step_dy = p.step * p.lddy, p.step_h = p.step * p.ldh, p.step_dh = p.step * p.lddh, p.step_dx = p.step * p.lddx;
+    p.npartials = static_cast<int>(g.ctas);
+    return cudaSuccess;
   }
-  RowGrid g;
-  const cudaError_t e = row_grid(g, kernel, tpr, p.n, smem, sms);
-  if (e != cudaSuccess) return e;
-  p.tpr = g.tpr;
-  p.step = static_cast<int64_t>(g.ctas) * g.rows;
-  p.step_dy = p.step * p.lddy, p.step_h = p.step * p.ldh, p.step_dh = p.step * p.lddh, p.step_dx = p.step * p.lddx;
-  p.npartials = static_cast<int>(g.ctas);
-  return row::launch(kernel, dim3(g.ctas), g.threads, smem, stream, p);
+  return row::launch(kernel, dim3(static_cast<unsigned>(p.npartials)), tpr * rows, smem, stream, p);
 }
 
 // A row's whole granules, K a thread, in CTAs that leave a thread the registers for them: 256 threads twice per SM,
@@ -919,12 +922,16 @@ cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
   cudaError_t e;
   if (p.dim > kMaxHeld || !same_offsets({dy, {p.h, p.ldh}, {p.dh, p.lddh}, {p.dx, p.lddx}}, p.n, sizeof(T))) {
     const dim3 grid(static_cast<unsigned>(p.n));
+    if (p.planning) {
+      p.npartials = kColumnSplits;
+      p.rhos = p.n;
+      return cudaSuccess;
+    }
     if (p.dgain) {  // before dx, which may be written over dy
       RmsNormGradLaunch only_rho = p;
       only_rho.dx = nullptr;
       e = row::launch(add_rmsnorm_grad_kernel<T>, grid, kThreads, 0, stream, only_rho);
       if (e != cudaSuccess) return e;
-      p.npartials = kColumnSplits;
       e = row::launch(rmsnorm_columns_kernel<T>, dim3(static_cast<unsigned>((p.dim + 31) / 32), kColumnSplits), kThreads, 0,
                       stream, p);
       if (e != cudaSuccess) return e;
@@ -935,7 +942,7 @@ cudaError_t launch_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {
     e = has_edges(dy, p.n, p.dim, sizeof(T)) ? launch_held_grad<T, true>(p, granules, sms, stream)
                                              : launch_held_grad<T, false>(p, granules, sms, stream);
   }
-  if (e != cudaSuccess || !p.dgain) return e;
+  if (e != cudaSuccess || p.planning || !p.dgain) return e;
   return row::launch(rmsnorm_dgain_kernel, dim3(static_cast<unsigned>((p.dim + 31) / 32)), kMaxThreads, 0, stream, p);
 }
 
@@ -947,13 +954,22 @@ cudaError_t launch_add_rmsnorm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   return p.dtype == 0 ? launch_norm<float, false>(p, sms, stream) : launch_norm<__nv_bfloat16, false>(p, sms, stream);
 }
 
-// Rows of sums, one per resident CTA or kColumnSplits; then a rho per row for the longest rows.
-int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, int sms, char* ws) {
-  const int64_t rows = std::max<int64_t>(kColumnSplits, std::min<int64_t>(p.n, std::max(8, sms * kMaxPerSm)));
-  const int64_t sums = (rows * p.dim * 4 + 255) / 256 * 256;
-  p.partials = reinterpret_cast<float*>(ws);
-  p.rho = reinterpret_cast<float*>(ws + sums);
-  return sums + p.n * 4;
+cudaError_t plan_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms) {
+  p.planning = 1, p.rhos = 0;
+  const cudaError_t e = launch_add_rmsnorm_grad(p, sms, nullptr);
+  p.planning = 0;
+  return e;
+}
+
+// Rows of sums, one per CTA or kColumnSplits; then a rho per row for the longest rows. Both are for dgain.
+int64_t rmsnorm_grad_workspace(RmsNormGradLaunch& p, char* ws) {
+  if (!p.dgain) return 0;
+  const int64_t sums = (p.npartials * p.dim * 4 + 255) / 256 * 256;
+  if (ws) {
+    p.partials = reinterpret_cast<float*>(ws);
+    p.rho = reinterpret_cast<float*>(ws + sums);
+  }
+  return sums + p.rhos * 4;
 }
 
 cudaError_t launch_add_rmsnorm_grad(RmsNormGradLaunch& p, int sms, cudaStream_t stream) {

@@ -152,3 +152,26 @@ def test_scratch_goes_with_its_graph(dm):
         torch.cuda.empty_cache()
         left.append(torch.cuda.mem_get_info()[0])
     assert left[2] - left[-1] < 100 << 20, [v >> 20 for v in left]
+
+
+@pytest.mark.parametrize("n,dim,dt,least", [(4096, 16384, torch.bfloat16, 10), (3000, 16384, torch.float32, 10),
+                                            (4096, 65536, torch.bfloat16, 9), (65536, 128, torch.float32, 1)])
+def test_norm_gradient_asks_for_what_it_uses(dm, n, dim, dt, least):
+    """A row of gain sums per CTA that runs (152 of the longest rows', 64 KB each), or 32 of rows that no CTA holds: under a
+    limit of `least` MB and a fifth, what is given without one."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    dy, h = (torch.randn(n, dim, generator=g, device="cuda").to(dt) for _ in range(2))
+    gain = torch.randn(dim, generator=g, device="cuda")
+    want = dm.add_rmsnorm_grad(dy, h, gain)
+    torch.cuda.synchronize()
+    dm.release_workspace()
+    dm.set_workspace_limit(int(1.2e6 * least))
+    try:
+        got = dm.add_rmsnorm_grad(dy, h, gain)
+        assert equal(got, want)
+        dm.set_workspace_limit(1)  # without a gain no scratch at all
+        alone = dm.add_rmsnorm_grad(dy, h)[0]
+    finally:
+        dm.set_workspace_limit(0)
+    assert torch.equal(alone, dm.add_rmsnorm_grad(dy, h, torch.ones_like(gain))[0])
+    dm.check_status()
