@@ -61,23 +61,28 @@ def _code(t, name):
     return code
 
 
-def _rows(t, name, dev, shape=None, dtype=None):
-    """(rows, row length, row stride) of a tensor on device `dev`, given its expected shape and dtype."""
-    if t.get_device() != dev:
-        _same_device(t, name, dev)
+def _layout(t, name):
+    """(rows, row length, row stride) of a tensor."""
     size = t.shape
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(size)}")
-    if dtype is not None and t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     if not size:
         raise ValueError(f"{name} must have at least one dimension")
     dim = size[-1]
     if t.is_contiguous():
-        return (t.numel() // dim if dim else 0), dim, dim
+        return (size[0] if len(size) == 2 else t.numel() // dim if dim else 0), dim, dim
     if len(size) != 2 or t.stride(1) != 1 or t.stride(0) < dim:
         raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
     return size[0], dim, t.stride(0)
+
+
+def _rows(t, name, dev, shape, dtype):
+    """Row stride of a tensor of the given shape and dtype (None: any) on device `dev`."""
+    if t.get_device() != dev:
+        _same_device(t, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.shape[-1] if t.is_contiguous() else _layout(t, name)[2]
 
 
 def _vector(t, name, dev, n, dtype=torch.float32):
@@ -111,13 +116,13 @@ def embedding(table, ids, scale=1.0, dtype=None, out=None, stream=None):
     dev = table.get_device()
     if dev < 0 or dev != _current_device():
         return _elsewhere(embedding, _device(table, "table"), table, ids, scale, dtype, out, stream)
-    rows, dim, ld = _rows(table, "table", dev)
+    rows, dim, ld = _layout(table, "table")
     ptr, size = _ids(ids, "ids", dev)
     if out is None:
         out = torch.empty(ids.shape + (dim,), dtype=dtype or table.dtype, device=table.device)
         n, ldo = ids.numel(), dim
     else:
-        n, _, ldo = _rows(out, "out", dev, ids.shape + (dim,), dtype)
+        n, ldo = ids.numel(), _rows(out, "out", dev, ids.shape + (dim,), dtype)
     status = lib().dmuon_embedding(table.data_ptr(), _code(table, "table"), rows, dim, ld, ptr, size, n, scale,
                                    out.data_ptr(), _code(out, "out"), ldo, _stream(stream, dev))
     if status:
@@ -132,7 +137,7 @@ def embedding_grad(grad_out, ids, rows, scale=1.0, padding_idx=None, grad=None, 
     if dev < 0 or dev != _current_device():
         return _elsewhere(embedding_grad, _device(grad_out, "grad_out"), grad_out, ids, rows, scale, padding_idx,
                           grad, accumulate, stream)
-    n, dim, ld = _rows(grad_out, "grad_out", dev)
+    n, dim, ld = _layout(grad_out, "grad_out")
     ptr, size = _ids(ids, "ids", dev, n)
     if grad is None:
         if accumulate:
@@ -140,7 +145,7 @@ def embedding_grad(grad_out, ids, rows, scale=1.0, padding_idx=None, grad=None, 
         grad = torch.empty((rows, dim), dtype=torch.float32, device=grad_out.device)
         ldg = dim
     else:
-        _, _, ldg = _rows(grad, "grad", dev, (rows, dim), torch.float32)
+        ldg = _rows(grad, "grad", dev, (rows, dim), torch.float32)
     status = lib().dmuon_embedding_grad(grad_out.data_ptr(), _code(grad_out, "grad_out"), ld, ptr, size, n, rows, dim,
                                         scale, -1 if padding_idx is None else padding_idx, grad.data_ptr(), ldg,
                                         1 if accumulate else 0, _stream(stream, dev))
@@ -150,15 +155,15 @@ def embedding_grad(grad_out, ids, rows, scale=1.0, padding_idx=None, grad=None, 
 
 
 def _norm_args(dev, x, residual, gain, h):
-    n, dim, ldx = _rows(x, "x", dev)
+    n, dim, ldx = _layout(x, "x")
     ldr, ldh, hp = 0, 0, None
     if residual is not None:
-        _, _, ldr = _rows(residual, "residual", dev, x.shape, x.dtype)
+        ldr = _rows(residual, "residual", dev, x.shape, x.dtype)
         if h is None:
             h, ldh = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
             hp = h.data_ptr()
     if hp is None and h is not None:
-        _, _, ldh = _rows(h, "h", dev, x.shape, x.dtype)
+        ldh = _rows(h, "h", dev, x.shape, x.dtype)
         hp = h.data_ptr()
     return (dim, h, (x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, _code(x, "x"),
                      _vector(gain, "gain", dev, dim), n, dim), (hp, ldh))
@@ -174,7 +179,7 @@ def add_rmsnorm(x, residual=None, gain=None, eps=1e-6, y=None, h=None, stream=No
     if y is None:
         y, ldy = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
     else:
-        _, _, ldy = _rows(y, "y", dev, x.shape, x.dtype)
+        ldy = _rows(y, "y", dev, x.shape, x.dtype)
     status = lib().dmuon_add_rmsnorm(*head, eps, *tail, y.data_ptr(), head[4], ldy, None, 0, _stream(stream, dev))
     if status:
         _check(status)
@@ -204,13 +209,13 @@ def add_rmsnorm_grad(dy, h, gain=None, dh=None, eps=1e-6, dx=None, dgain=None, a
     dev = dy.get_device()
     if dev < 0 or dev != _current_device():
         return _elsewhere(add_rmsnorm_grad, _device(dy, "dy"), dy, h, gain, dh, eps, dx, dgain, accumulate, stream)
-    n, dim, ldy = _rows(dy, "dy", dev)
-    _, _, ldh = _rows(h, "h", dev, dy.shape, dy.dtype)
-    lddh = 0 if dh is None else _rows(dh, "dh", dev, dy.shape, dy.dtype)[2]
+    n, dim, ldy = _layout(dy, "dy")
+    ldh = _rows(h, "h", dev, dy.shape, dy.dtype)
+    lddh = 0 if dh is None else _rows(dh, "dh", dev, dy.shape, dy.dtype)
     if dx is None:
         dx, lddx = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device), dim
     else:
-        _, _, lddx = _rows(dx, "dx", dev, dy.shape, dy.dtype)
+        lddx = _rows(dx, "dx", dev, dy.shape, dy.dtype)
     if dgain is None and gain is not None:
         if accumulate:
             raise ValueError("accumulate needs a dgain to add to")
@@ -236,7 +241,7 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
     if dev < 0 or dev != _current_device():
         return _elsewhere(policy_loss, _device(logits, "logits"), logits, targets, old_logp, advantages, weights,
                           ref_logp, clip_low, clip_high, kl_coef, temperature, dlogits, stream)
-    n, vocab, ld = _rows(logits, "logits", dev)
+    n, vocab, ld = _layout(logits, "logits")
     ptr, size = _ids(targets, "targets", dev, n)
     ldd, dptr = 0, None
     if dlogits is None:
@@ -245,7 +250,7 @@ def policy_loss(logits, targets, old_logp, advantages, weights, ref_logp=None, c
     elif dlogits is False:
         dlogits = None
     else:
-        _, _, ldd = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
+        ldd = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
         dptr = dlogits.data_ptr()
     loss = torch.empty((), dtype=torch.float32, device=logits.device)
     logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
@@ -264,7 +269,7 @@ def token_logprobs(logits, targets, temperature=1.0, stream=None):
     dev = logits.get_device()
     if dev < 0 or dev != _current_device():
         return _elsewhere(token_logprobs, _device(logits, "logits"), logits, targets, temperature, stream)
-    n, vocab, ld = _rows(logits, "logits", dev)
+    n, vocab, ld = _layout(logits, "logits")
     ptr, size = _ids(targets, "targets", dev, n)
     logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
     status = lib().dmuon_token_logprobs(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size,
