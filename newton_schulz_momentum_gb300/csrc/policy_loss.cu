@@ -31,6 +31,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
+// The exponentials and the logarithm are the hardware's, of base 2. Beside the rounding of their own, exp(y) = 2^(y log2 e)
+// is off by about |y| 2^-24 of itself from the product's: the more, the less a logit's probability counts, or the
+// further two policies are apart. expf, expm1f and logf in a row's own terms (its ratio, its KL term, the logarithm of
+// its sum): log-probabilities of 200 x 50257 fp32 off by 1.9e-7 in the mean in place of 2.4e-7, a row's gradient by
+// 1.4e-7 in place of 1.9e-7 of itself, and 134150 x 2001 bf16 267 -> 282 us, 8192 x 128256 750 -> 764.
+
 // 2^x, within 2 units of the last place; below 2^-126 it is 0.
 __device__ __forceinline__ float pow2(float x) {
   float y;
