@@ -63,3 +63,25 @@ def test_targets_at_the_borders_of_the_shares(dm, vocab, dt):
         s["ref_logp"] = s["old_logp"] - 0.1
         check_policy(dm, s, 1.0, 0.1)
     dm.check_status()
+
+
+@pytest.mark.parametrize("layout", ["plain", "rows", "offset"])
+@pytest.mark.parametrize("dt,vocab", [(torch.float32, 292869), (torch.float32, 400001), (torch.bfloat16, 585733),
+                                      (torch.bfloat16, 700000)])
+def test_rows_beyond_the_memory_of_a_cluster(dm, dt, vocab, layout):
+    """Read twice, by a CTA each: with and without a gradient, in place, masked rows and masked logits among them."""
+    n = 7
+    s = policy_inputs(n, vocab, dt, 1.0, vocab, layout, masked=0.0)
+    s["weights"][2] = 0
+    s["targets"][4] = -1
+    s["logits"][5, vocab // 2:] = float("-inf")
+    s["targets"][5] = 3
+    s["old_logp"] = torch.log_softmax(s["logits"].double(), 1).gather(1, s["targets"].clamp(min=0)[:, None])[:, 0].float()
+    s["ref_logp"] = s["old_logp"] - 0.1
+    loss, logp, d = check_policy(dm, s, 1.0, 0.1)
+    args = dict(clip_low=0.2, clip_high=0.25, kl_coef=0.1)
+    alone = dm.policy_loss(**s, **args, dlogits=False)
+    assert torch.equal(alone[0], loss) and torch.equal(alone[1], logp)
+    got = dm.policy_loss(**s, **args, dlogits=s["logits"])
+    assert all(torch.equal(a, b) for a, b in zip(got, (loss, logp, d)))
+    dm.check_status()
