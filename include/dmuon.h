@@ -449,11 +449,11 @@ DMUON_API int dmuon_selftest_bounded_wait(int64_t limit_ns, void* cuda_stream);
  * The checked build. libdmuon_checked.so is built from the same sources with device-side range checks
  * compiled in (the debugging stand-in for a memory checker): every tile's job index and position, every
  * row-wise chunk's matrix, partial-sum slot and cast tile, every AdamW chunk, every small-matrix job's
- * sizes and every place in the embedding gradient's sorted and crossing lists are tested before use; a failed test skips the access and records DMUON_ERR_RANGE for
- * dmuon_check_status. The regular libdmuon.so leaves them out. dmuon_selftest_range_check launches one
- * GEMM whose only tile lies outside its (empty) product, so that in the checked build the next
- * dmuon_check_status returns DMUON_ERR_RANGE; nothing is read or written. In the regular build it returns
- * DMUON_ERR_UNSUPPORTED without launching. No counterpart on the pages.
+ * sizes and every place in the embedding gradient's sorted and crossing lists are tested before use; a failed
+ * test skips the access and records DMUON_ERR_RANGE for dmuon_check_status. The regular libdmuon.so leaves them
+ * out. dmuon_selftest_range_check launches one GEMM whose only tile lies outside its (empty) product, so that in
+ * the checked build the next dmuon_check_status returns DMUON_ERR_RANGE; nothing is read or written. In the
+ * regular build it returns DMUON_ERR_UNSUPPORTED without launching. No counterpart on the pages.
  */
 DMUON_API int dmuon_selftest_range_check(void* cuda_stream);
 
@@ -464,7 +464,8 @@ DMUON_API const char* dmuon_last_error(void);
 DMUON_API const char* dmuon_version(void);
 
 /* Upper bound on workspace bytes per device (0 = no limit). Calls needing more fail with
- * DMUON_ERR_OOM before launching anything. */
+ * DMUON_ERR_OOM before launching anything. It holds for the optimizer's workspace and for the token operators'
+ * scratch (of all streams and graphs together) each. */
 DMUON_API int dmuon_set_workspace_limit(size_t bytes);
 
 /* Bytes of workspace the library would need for dmuon_muon_step on these shapes (host query). */

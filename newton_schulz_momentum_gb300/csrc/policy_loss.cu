@@ -13,9 +13,10 @@
 // up to 18 KB is one warp's; beyond the cluster's memory a row is read twice.
 //
 // Bounds: fp32 by memory (8388 x 32001: 333 us, 6.0 TB/s), bf16 by the instructions of two exponentials and four
-// conversions per two bytes beside it (8192 x 128256: 734 us, 5.4 TB/s; 2092 x 128256 without a gradient 139 us,
+// conversions per two bytes beside it (8192 x 128256: 731 us, 5.3 TB/s; 2092 x 128256 without a gradient 139 us,
 // 3.9 TB/s). Short rows by the row itself: about 500 instructions of each warp that has a share in it
-// (536870 x 500 bf16: 530 us, 2.0 TB/s). A few rows by latency: 8 x 128256 bf16 15.6 us.
+// (500000 x 500 bf16: 500 us, 2.0 TB/s). A few rows by latency: 8 x 128256 bf16 10 us on the device, 16 to 18 with
+// the host's steps.
 //
 // Memory is read and written in 16-byte granules at aligned addresses, wherever a row starts; the sum runs over
 // groups of as many elements counted from the row's first one. So its order goes by the vocabulary alone: a row
@@ -250,7 +251,8 @@ __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const
 }
 
 // Leaves a term of the loss; who leaves the last one adds them all, in an order that their number fixes. The counter
-// lies in the call's own scratch, and its last increment sets it back to 0. Called by one whole warp per term. (A launch of its own for the sum: 4 more microseconds for a call of 8 rows.)
+// lies in front of the stream's or graph's scratch, and its last increment sets it back to 0. Called by one whole warp
+// per term. (A launch of its own for the sum: 4 more microseconds for a call of 8 rows.)
 __device__ __forceinline__ void leave_term(const PolicyLaunch& p, int64_t at, float loss) {
   const int lane = threadIdx.x & 31;
   unsigned before = 0;
@@ -385,8 +387,8 @@ __device__ __forceinline__ int token_of(const PolicyLaunch& p, uint32_t word, in
 // A cluster takes every gridDim.x / C-th row, and each of its warps an equal share of it (kSolo: every warp rows
 // of its own). The warps work by themselves: bulk copies bring a share's whole granules into the warp's slots and
 // take their gradients, formed in place, out; up to E - 1 elements on either side of them go through registers.
-// Where they meet is the row's sum: every warp sends its own to every CTA of the cluster, forms its sum of the next
-// row, and goes on when all have arrived. (With barriers over the cluster and the CTA in their place, 38% of the
+// Where they meet is the row's sum: every warp sends its own to every CTA of the cluster (and who has the target, its
+// logit), forms its sum of the next row, and goes on when all have arrived. (With barriers over the cluster and the CTA in their place, 38% of the
 // warps' time went into those and the fences they imply.)
 // EDGES: shares that are not whole granules.
 template <typename T, int MODE, bool EDGES>

@@ -22,9 +22,9 @@
 // Bounds. Rows of whole granules: memory, forward at 16384 x 4096 bf16 85 us (6.3 TB/s), fp32 171 (6.3), backward
 // 92 (5.8) and 168 (6.4). Rows with edges: the instructions that cut and realign them, forward at 65344 x 1027 bf16
 // 121 us (4.4 TB/s), fp32 180 (6.0), backward 111 (4.8) and 168 (6.4). 8-bit outputs: the chain from the row's sum
-// over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 85 us (5.6
-// TB/s), 3001 x 8200 fp32 59 (5.4); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
-// 185 (2.6). One row: latency, 4 us on the device, and the launch.
+// over the group's maximum to the bytes, with two or three rows at a time per SM: 16384 x 4096 bf16 83 us (5.7
+// TB/s), 3001 x 8200 fp32 60 (5.4); with edges, where groups pass through shared memory twice, 65344 x 1027 bf16
+// 187 (2.5). One row: latency, 4 us on the device, and the launch.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -842,7 +842,10 @@ template <typename T, bool FP8>
 cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T, FP8>(granules);
   p.sum_threads = std::min(row_threads(granules, each), kMaxThreads);
-  p.inv_dim = 1.f / static_cast<float>(p.dim);  // the mean of the squares is within two units of the last place by it
+  // The mean of the squares is within two units of the last place by it. (With 1 / dim in two parts, which rounds as a
+  // division does: the gains' gradient at 65537 x 129 fp32 is off by 1.80e-7 in place of 1.70e-7, dx by 5.78e-8 in
+  // place of 5.79e-8, and 520223 x 129 bf16 takes 160.4 us in place of 159.0.)
+  p.inv_dim = 1.f / static_cast<float>(p.dim);
   const Array x{p.x, p.ldx};
   if (p.dim > kMaxHeld ||
       !same_offsets({x, {p.residual, p.ldr}, {p.h, p.ldh}, {FP8 ? nullptr : p.y, p.ldy}}, p.n, sizeof(T)))
