@@ -1264,7 +1264,8 @@ int check_in_place(const char* out_name, const void* out, int64_t ld_out, const 
   return DMUON_OK;
 }
 
-// While it lives, this thread may allocate and free although a stream is being captured: neither is the capture's work.
+// While it lives, this thread may allocate, free and wait although some stream is being captured, by this thread or
+// another: none of it is the capture's work, but would end the capture with an error.
 class RelaxedCapture {
  public:
   RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode_); }
@@ -1297,7 +1298,6 @@ template <typename F>
 void free_token_blocks(DeviceState& ds, F&& which) {
   const auto named = [&](const TokenBlock* b) { return which(*b); };
   if (std::none_of(ds.token_blocks.begin(), ds.token_blocks.end(), named)) return;
-  RelaxedCapture relaxed;
   size_t kept = 0;
   for (TokenBlock* b : ds.token_blocks) {
     if (!which(*b)) {
@@ -1314,7 +1314,6 @@ void free_token_blocks(DeviceState& ds, F&& which) {
 int new_token_block(DeviceState& ds, size_t need, size_t want, TokenBlock** out) {
   ds.token_blocks.reserve(ds.token_blocks.size() + 1);
   std::unique_ptr<TokenBlock> block(new TokenBlock);
-  RelaxedCapture relaxed;
   // The zero is written on a stream of the library's own, which no capture and no caller's work is on.
   if (!ds.token_stream)
     DM_CUDA(cudaStreamCreateWithFlags(&ds.token_stream, cudaStreamNonBlocking), "cudaStreamCreateWithFlags");
@@ -1347,6 +1346,7 @@ int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** 
   if (need == 0) return DMUON_OK;
   if (g_ws_limit && need > g_ws_limit)
     return fail(DMUON_ERR_OOM, "workspace of %zu bytes exceeds the limit of %zu", need, g_ws_limit);
+  RelaxedCapture relaxed;
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   unsigned long long id = 0, owner = reinterpret_cast<uintptr_t>(stream);
   cudaGraph_t graph = nullptr;

@@ -91,7 +91,7 @@ def _vector(t, name, dev, n, dtype=torch.float32):
         return None
     if t.get_device() != dev:
         _same_device(t, name, dev)
-    if t.numel() != n or t.dtype != dtype or not t.is_contiguous():
+    if t.numel() != n or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} elements")
     return t.data_ptr()
 

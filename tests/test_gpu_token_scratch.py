@@ -175,3 +175,47 @@ def test_norm_gradient_asks_for_what_it_uses(dm, n, dim, dt, least):
         dm.set_workspace_limit(0)
     assert torch.equal(alone, dm.add_rmsnorm_grad(dy, h, torch.ones_like(gain))[0])
     dm.check_status()
+
+
+@pytest.mark.parametrize("where", ["same thread", "another thread"])
+def test_calls_beside_a_capture(dm, where):
+    """Calls that run at once on another stream while a stream is captured, with scratch that grows and scratch that is
+    there: neither they nor the capture fails."""
+    import threading
+    small, large = step_inputs(700, 300, 520), step_inputs(20000, 900, 1032, 1)
+    want, big = [t.clone() for t in step(dm, small)], [t.clone() for t in step(dm, large)]
+    side, errors = torch.cuda.Stream(), []
+    with torch.cuda.stream(side):
+        step(dm, small)
+    outs = [[torch.empty_like(t) for t in w] for w in (want, big, want)]
+    torch.cuda.synchronize()
+    dm.release_workspace()
+    with torch.cuda.stream(side):
+        dm.embedding_grad(small["dy"], small["ids"], 300)  # scratch for the small calls
+    torch.cuda.synchronize()
+
+    def beside():
+        try:
+            with torch.cuda.stream(side):
+                for s, out in zip((small, large, small), outs):
+                    dm.add_rmsnorm_grad(s["dy"], s["h"], s["gain"], dx=out[0], dgain=out[1])
+                    dm.embedding_grad(out[0], s["ids"], s["rows"], grad=out[2])
+        except Exception as e:  # noqa: BLE001 - whatever it is, it is reported
+            errors.append(e)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step(dm, small)
+        if where == "same thread":
+            beside()
+        else:
+            thread = threading.Thread(target=beside)
+            thread.start()
+            thread.join()
+        more = step(dm, small)
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for out, w in zip(outs, (want, big, want)):
+        assert equal(out[:3], w[:3])
+    assert equal(replayed(graph, held), want) and equal(more, want)
+    dm.check_status()
