@@ -69,7 +69,7 @@ def _layout(t, name):
     dim = size[-1]
     if t.is_contiguous():
         return (size[0] if len(size) == 2 else t.numel() // dim if dim else 0), dim, dim
-    if len(size) != 2 or t.stride(1) != 1 or t.stride(0) < dim:
+    if len(size) != 2 or (dim > 1 and t.stride(1) != 1) or t.stride(0) < dim:
         raise ValueError(f"{name} must be contiguous, or 2-D with contiguous rows that do not overlap")
     return size[0], dim, t.stride(0)
 

@@ -224,3 +224,16 @@ def test_rows_in_place_with_another_stride_are_refused(entry, args, word):
     rc = getattr(dm.lib(), entry)(*args, None)
     message = dm.lib().dmuon_last_error().decode()
     assert rc == dm.ERR_INVALID_ARG and word in message, (rc, message)
+
+
+def test_rows_of_one_element_have_no_stride_within():
+    """A column of a matrix: whatever lies between the elements of a row that has one does not matter."""
+    torch = pytest.importorskip("torch")
+    from newton_schulz_momentum_gb300.token_ops import _layout
+    column = torch.empty(6, 9)[:, ::4][:, 1:2]
+    assert column.stride() == (9, 4) and _layout(column, "x") == (6, 1, 9)
+    assert _layout(torch.empty(6, 9)[:, :4], "x") == (6, 4, 9) and _layout(torch.empty(2, 3, 5), "x") == (6, 5, 5)
+    assert _layout(torch.empty(0, 5), "x") == (0, 5, 5) and _layout(torch.empty(1, 9)[:, :4], "x") == (1, 4, 4)
+    for bad in (torch.empty(6, 9)[:, ::4], torch.empty(1, 9).expand(6, 9), torch.empty(4, 6, 9)[:, :, :5], torch.empty(9, 6).T):
+        with pytest.raises(ValueError, match="contiguous"):
+            _layout(bad, "x")
