@@ -570,34 +570,40 @@ __global__ void __launch_bounds__(THREADS, PER_SM) add_rmsnorm_grad_rows_kernel(
   }
 }
 
-// dgain from the CTAs' sums: a CTA takes 32 columns, its warps every 32nd row of the workspace. Latency of the loads
-// of a warp bounds it.
+// dgain from the CTAs' sums: a CTA takes 32 columns, its warps every 32nd row of the workspace, then a column each.
+// Latency of the loads of a warp bounds it. The sums are added by pairs: one after the other they were most of dgain's
+// error (65537 x 129 fp32: 1.54e-7 of itself, one after the other 1.70e-7; 16384 x 4096 fp32 1.63e-7 and 1.88e-7; 27.5 us
+// for the former's gradient, 26.5 so).
 __global__ void __launch_bounds__(kMaxThreads) rmsnorm_dgain_kernel(const RmsNormGradLaunch p) {
   constexpr int kWarps = kMaxThreads / 32;
-  __shared__ float sums[kWarps][32];
+  static_assert(kWarps == 32, "a warp's lanes are the warps' sums");
+  __shared__ float sums[kWarps][33];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * 32, c = first + lane;
   float acc = 0.f;
   if (c < p.dim) {
-    int i = warp;
-    for (; i + 7 * kWarps < p.npartials; i += 8 * kWarps) {
+    const float* from = p.partials + warp * p.dim + c;
+    const int64_t step = kWarps * p.dim;
+#pragma unroll 1
+    for (int left = p.npartials - warp; left > 0; left -= 8 * kWarps) {
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = __ldcg(p.partials + (i + k * kWarps) * p.dim + c);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc += v[k];
+      for (int k = 0; k < 8; ++k) {
+        v[k] = k * kWarps < left ? __ldcg(from) : 0.f;
+        from += step;
+      }
+      acc += ((v[0] + v[4]) + (v[1] + v[5])) + ((v[2] + v[6]) + (v[3] + v[7]));
     }
-    for (; i < p.npartials; i += kWarps) acc += __ldcg(p.partials + i * p.dim + c);
   }
   sums[warp][lane] = acc;
   __syncthreads();
-  if (warp == 0 && c < p.dim) {
-    acc = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) acc += sums[w][lane];
-    p.dgain[c] = p.accumulate ? p.dgain[c] + acc : acc;
+  acc = sums[lane][warp];
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0 && first + warp < p.dim) {
+    float* to = p.dgain + first + warp;
+    *to = p.accumulate ? *to + acc : acc;
   }
 }
 
@@ -843,8 +849,7 @@ cudaError_t launch_norm(RmsNormLaunch& p, int sms, cudaStream_t stream) {
   const int granules = static_cast<int>((p.dim + kPer<T> - 1) / kPer<T>), each = granules_each<T, FP8>(granules);
   p.sum_threads = std::min(row_threads(granules, each), kMaxThreads);
   // The mean of the squares is within two units of the last place by it. (With 1 / dim in two parts, which rounds as a
-  // division does: the gains' gradient at 65537 x 129 fp32 is off by 1.80e-7 in place of 1.70e-7, dx by 5.78e-8 in
-  // place of 5.79e-8, and 520223 x 129 bf16 takes 160.4 us in place of 159.0.)
+  // division does, no gradient's error was smaller, and 520223 x 129 bf16 took 160.4 us in place of 159.0.)
   p.inv_dim = 1.f / static_cast<float>(p.dim);
   const Array x{p.x, p.ldx};
   if (p.dim > kMaxHeld ||

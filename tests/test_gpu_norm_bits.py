@@ -59,3 +59,20 @@ def test_fp8_scales_are_rounded_once(dm, dim, dt):
             exact * (1 - 2.0 ** -22)).float().to(torch.float8_e4m3fn).float()
         assert safe.double().mean() > 0.999
         assert torch.equal(q.float()[safe], exact.float().to(torch.float8_e4m3fn).float()[safe])
+
+
+@pytest.mark.parametrize("dim", [129, 4096])
+def test_gain_sums_are_added_pairwise(dm, dim):
+    """152 rows, one per CTA, whose terms are all positive, so that the sums over the CTAs are what rounds. A rounding's
+    error has a deviation of about 0.41 u of the value (u = 2^-24). Pairwise over 2^L equal terms the last sum counts
+    in full, the two before it by half and so on: 0.41 u sqrt(2) = 0.6 u in all, and the terms' own errors average out
+    to a tenth of theirs. One after the other over 32 warps' sums it would be 0.41 u sqrt(32 / 3) = 1.35 u. The root mean
+    square over the columns has to be below 1 u."""
+    g = torch.Generator(device="cuda").manual_seed(dim)
+    h = torch.randn(152, dim, generator=g, device="cuda")
+    dy = h.sign() * (0.5 + torch.rand(152, dim, generator=g, device="cuda"))
+    _, dgain = dm.add_rmsnorm_grad(dy, h, torch.ones(dim, device="cuda"), eps=1e-6)
+    h64 = h.double()
+    want = (dy.double() * h64 * torch.rsqrt((h64 * h64).mean(1, keepdim=True) + 1e-6)).sum(0)
+    error = ((dgain.double() - want) / want).pow(2).mean().sqrt()
+    assert float(error) < 2.0 ** -24, float(error) * 2 ** 24
