@@ -387,9 +387,10 @@ DMUON_API int dmuon_add_rmsnorm_grad(const void* dy, int64_t lddy, const void* h
  * is not read: it adds nothing, its lp is given as 0 and its gradient is zeros. A target >= vocab counts
  * as one, and gives DMUON_ERR_INDEX at the next dmuon_check_status. Logits of -infinity are tokens of
  * probability 0; a row that holds NaN or +infinity, or nothing but -infinity, gives NaN.
- * Exponentials and the logarithm are taken to base 2 in fp32: beside a few roundings of 2^-24, exp(y) is within about
- * |y| 2^-24 of itself (y: a logit's distance from its row's largest, lp - old_logp, ref_logp - lp), and a
- * probability below 2^-126 of the row's largest counts as 0. lp is within a few 2^-24 of |lp| + log(vocab).
+ * Exponentials are taken to base 2 in fp32: beside a few roundings of 2^-24, exp(y) is within about |y| 2^-24 of
+ * itself (y: a logit's distance from its row's largest, lp - old_logp, ref_logp - lp), and a probability below
+ * 2^-126 of the row's largest counts as 0. lp is within a few 2^-24 of |lp| + log(vocab), and over many rows off to
+ * one side by less than 2^-23.
  */
 DMUON_API int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab,
                                 const void* targets, int id_bytes, const float* old_logp, const float* ref_logp,

@@ -1406,6 +1406,13 @@ int token_workspace(DeviceState& ds, int64_t bytes, cudaStream_t stream, char** 
   return DMUON_OK;
 }
 
+void set_temperature(PolicyLaunch& p, float temperature) {
+  const double inverse = 1.0 / static_cast<double>(temperature);
+  p.inv_temperature = static_cast<float>(inverse);
+  p.inv_temperature_low = static_cast<float>(inverse - static_cast<double>(p.inv_temperature));
+  p.log2e_over_t = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+}
+
 // The launches of dmuon_policy_loss and dmuon_token_logprobs (p.loss null). Called with g_mu held.
 int run_policy(PolicyLaunch& p, cudaStream_t stream) {
   DeviceState* ds = nullptr;
@@ -1982,7 +1989,8 @@ int dmuon_policy_loss(const void* logits, int dtype, int64_t ld, int64_t n, int6
     p.targets = targets, p.id_bytes = id_bytes;
     p.old_logp = old_logp, p.ref_logp = kl_coef != 0.f ? ref_logp : nullptr;
     p.advantages = advantages, p.weights = weights;
-    p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef, p.inv_temperature = 1.f / temperature;
+    p.clip_low = clip_low, p.clip_high = clip_high, p.kl_coef = kl_coef;
+    set_temperature(p, temperature);
     p.loss = loss, p.logp = logp, p.dlogits = dlogits, p.ldd = ldd;
     return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
   } catch (const std::exception& e) {
@@ -2006,7 +2014,8 @@ int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, i
     std::memset(&p, 0, sizeof(p));
     p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
     p.targets = targets, p.id_bytes = id_bytes;
-    p.inv_temperature = 1.f / temperature, p.logp = logp;
+    p.logp = logp;
+    set_temperature(p, temperature);
     return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());

@@ -407,7 +407,8 @@ struct PolicyLaunch {
   int id_bytes;
   const float *old_logp, *ref_logp, *advantages;  // ref_logp may be null: no KL term
   const float* weights;                           // null: log-probabilities only
-  float clip_low, clip_high, kl_coef, inv_temperature;
+  float clip_low, clip_high, kl_coef;
+  float inv_temperature, inv_temperature_low, log2e_over_t;  // 1 / T in two parts, log2(e) / T
   float* loss;      // null: log-probabilities only
   float* loss_terms;  // workspace of policy_workspace(n) bytes: `terms` summands of the loss, set by launch_policy
   int64_t terms;

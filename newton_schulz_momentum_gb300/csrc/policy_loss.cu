@@ -32,11 +32,10 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// The exponentials and the logarithm are the hardware's, of base 2. Beside the rounding of their own, exp(y) = 2^(y log2 e)
-// is off by about |y| 2^-24 of itself from the product's: the more, the less a logit's probability counts, or the
-// further two policies are apart. expf, expm1f and logf in a row's own terms (its ratio, its KL term, the logarithm of
-// its sum): log-probabilities of 200 x 50257 fp32 off by 1.9e-7 in the mean in place of 2.4e-7, a row's gradient by
-// 1.4e-7 in place of 1.9e-7 of itself, and 134150 x 2001 bf16 267 -> 282 us, 8192 x 128256 750 -> 764.
+// The exponentials are the hardware's, of base 2. Beside the rounding of their own, exp(y) = 2^(y log2 e) is off by
+// about |y| 2^-24 of itself from the product's: the more, the less a logit's probability counts, or the further two
+// policies are apart. With expf and expm1f for a row's ratio and KL term and logf for its sum, 134150 x 2001 bf16 took
+// 282 us in place of 267 and 8192 x 128256 764 in place of 750, for gradients as near as these.
 
 // 2^x, within 2 units of the last place; below 2^-126 it is 0.
 __device__ __forceinline__ float pow2(float x) {
@@ -45,11 +44,15 @@ __device__ __forceinline__ float pow2(float x) {
   return y;
 }
 
-// Within 2^-22 of itself, and of 1 for arguments around 1.
-__device__ __forceinline__ float log2_of(float x) {
+// log(x) of a sum of terms up to 1. The hardware's log2 is off by up to 2^-22 of itself, and by 2^-23 to one side in
+// the mean, which a loss would add up over its rows; one Newton step, y + (x exp(-y) - 1), leaves what 2^-y is off,
+// 2^-24 in the mean. log(1) is 0. (Log-probabilities of 1025 x 50257 bf16: off by 5e-8 in the mean and 2.6e-7 in the root
+// mean square, 1.0e-7 and 2.9e-7 without the step, at a temperature of 1.3 6e-8 and 1.9e-7, before that one's inverse
+// came in two parts; logf: 754 us for 8192 x 128256 in place of 727.)
+__device__ __forceinline__ float log_of(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  return fmaf(y, kLn2, fmaf(x, pow2(-y), -1.f));
 }
 
 // The largest logit m and s = sum of 2^((x - m) k), k = log2(e) / T. The difference is formed before the
@@ -230,8 +233,10 @@ __device__ __forceinline__ float exp_less_1(float d) {
 // Writes the row's log-probability (one thread), adds its term to `loss` and gives its gradient's scale c / T.
 __device__ __forceinline__ float row_end(const PolicyLaunch& p, int64_t i, const RowMeta& r, float xa, MaxSum t,
                                          bool writes, float& loss) {
-  // The token's distance from the maximum is exact in many cases, and log2 of a sum of 1 is 0.
-  const float logp = (xa - t.m) * p.inv_temperature - log2_of(t.s) * kLn2;
+  // The token's distance from the maximum is exact in many cases, and the logarithm of a sum of 1 is 0. A distance of
+  // -infinity stays one.
+  const float from_top = xa - t.m, low = from_top > -INFINITY ? from_top * p.inv_temperature_low : 0.f;
+  const float logp = fmaf(from_top, p.inv_temperature, low - log_of(t.s));
   float each = 0.f, c = 0.f;
   if (p.weights) {
     const float ratio = pow2((logp - r.old) * kLog2e);
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(Ring<MODE>::kThreads, Ring<MODE>::kPerSm) poli
   const int units = SOLO ? 1 : C * R::kWarps, groups_each = (vocab + units * E - 1) / (units * E);
   const int from = min(unit * groups_each * E, vocab), length = min(groups_each * E, vocab - from);
   const T* logits = static_cast<const T*>(p.logits) + from;
-  const float k = kLog2e * p.inv_temperature;
+  const float k = p.log2e_over_t;
   if (threadIdx.x == 0) {
     for (int w = 0; w < R::kWarps; ++w)
       for (int s = 0; s < kRingSlots; ++s) ptx::mbar_init(&slot_full[w][s], 1);
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(kTwiceThreads) policy_twice_kernel(const Polic
       for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) dx[c] = row::from_f<T>(0.f);
     return;
   }
-  const float k = kLog2e * p.inv_temperature;
+  const float k = p.log2e_over_t;
   MaxSum t{-INFINITY, 0.f};
   float base = 0.f;
   for (int64_t c = threadIdx.x; c < p.vocab; c += kTwiceThreads) {

@@ -85,3 +85,20 @@ def test_rows_beyond_the_memory_of_a_cluster(dm, dt, vocab, layout):
     got = dm.policy_loss(**s, **args, dlogits=s["logits"])
     assert all(torch.equal(a, b) for a, b in zip(got, (loss, logp, d)))
     dm.check_status()
+
+
+@pytest.mark.parametrize("temperature", [1.0, 1.3, 0.7])
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("vocab", [700, 50257])
+def test_log_probabilities_lean_to_no_side(dm, vocab, dt, temperature):
+    """The mean of the signed errors over 4000 rows, which a loss adds up. The exponentials are off by 2^-24 to one side in
+    the mean, in the sum and again in the logarithm's step: 2^-23. Roundings of values up to 16 (4.8e-7 at most) average
+    out to 4.8e-7 / sqrt(4000) = 8e-9, of which three are allowed. The temperature is the fp32 one of the call."""
+    g = torch.Generator(device="cuda").manual_seed(vocab)
+    n, t32 = 4000, float(torch.tensor(temperature, dtype=torch.float32))
+    logits = torch.empty(n, vocab, device="cuda").normal_(0, 2, generator=g).to(dt)
+    targets = torch.randint(0, vocab, (n,), generator=g, device="cuda")
+    got = dm.token_logprobs(logits, targets, temperature).double()
+    want = torch.cat([torch.log_softmax(part.double() / t32, 1).gather(1, at[:, None])[:, 0]
+                      for part, at in zip(logits.split(500), targets.split(500))])
+    assert abs(float((got - want).mean())) < 2.0 ** -23 + 2.4e-8, float((got - want).mean())
