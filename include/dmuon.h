@@ -303,8 +303,9 @@ DMUON_API int dmuon_check_status(void* cuda_stream);
 DMUON_API int dmuon_set_graph_replay(int on);
 
 /*
- * Token operators: what a training step of a language model runs beside its matrix products, on the
- * parameters that AdamW updates (embedding table, norm gains, output head). No counterpart on the pages.
+ * Token operators: what a training step of a language model runs beside its matrix products: on the parameters
+ * that AdamW updates (embedding table, norm gains, output head), and between the products (per-head norm with
+ * rotation, attention). No counterpart on the pages.
  *
  * Arrays are row-major with `ld` elements from one row to the next (ld >= the row length; rows of fp32 or
  * bf16 as the dtype says). Unlike the entry points above they need no more than their elements'
@@ -404,6 +405,114 @@ DMUON_API int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, in
                                    void* cuda_stream);
 
 /*
+ * dmuon_qk_norm_rotary -- the RMS norm of each head's queries and keys with the position rotation in the same pass.
+ * Per token and head: z = x * (mean over the head of x^2 + eps)^(-1/2) * gain (norm != 0; z = x otherwise); of the
+ * first rotary_dim columns the pairs (j, j + rotary_dim / 2), or (2j, 2j + 1) if interleaved, are turned by
+ * a = f_j * position:  y1 = z1 cos a - z2 sin a,  y2 = z2 cos a + z1 sin a.  The other columns pass.
+ *   q, k, q_out, k_out  device, fp32 or bf16 (`dtype`): heads (kv_heads) of `dim` columns for each of n tokens, the next
+ *                   token's and head's x_token and x_head elements away. kv_heads 0: no keys. q_out may be q and
+ *                   k_out k, with their strides. dim is even, at most 256; rotary_dim even, at most dim.
+ *   q_gain, k_gain  device, dim, fp32, for all heads alike; NULL: ones
+ *   freqs           host, rotary_dim / 2 angles per position, or NULL: f_j = base^(-2j / rotary_dim)
+ *   positions       device, int32 or int64 (id_bytes): `axes` (1 to 4) lists of n, axis_stride elements apart
+ *   sections        host, axes counts: the first sections[0] frequencies follow the first list, and so on; they add up to
+ *                   rotary_dim / 2. Not read with one axis.
+ * Angles are formed modulo a revolution in integers: positions up to 2^31 are as exact as small ones.
+ */
+DMUON_API int dmuon_qk_norm_rotary(const void* q, int64_t q_token, int64_t q_head, int64_t heads, const void* k,
+                                   int64_t k_token, int64_t k_head, int64_t kv_heads, int dtype, const float* q_gain,
+                                   const float* k_gain, int norm, float eps, int64_t n, int64_t dim, int64_t rotary_dim,
+                                   int interleaved, double base, const double* freqs, const void* positions,
+                                   int id_bytes, int axes, int64_t axis_stride, const int64_t* sections, void* q_out,
+                                   int64_t q_out_token, int64_t q_out_head, void* k_out, int64_t k_out_token,
+                                   int64_t k_out_head, void* cuda_stream);
+
+/*
+ * dmuon_qk_norm_rotary_grad -- the backward pass at the stored q and k (not read without the norm): dq and dk of
+ * their type, and dq_gain, dk_gain, fp32, summed over tokens and heads (NULL: not wanted; written over). dq may be
+ * dq_out or q, and dk dk_out or k, with their strides.
+ */
+DMUON_API int dmuon_qk_norm_rotary_grad(const void* dq_out, int64_t dq_out_token, int64_t dq_out_head, const void* q,
+                                        int64_t q_token, int64_t q_head, int64_t heads, const void* dk_out,
+                                        int64_t dk_out_token, int64_t dk_out_head, const void* k, int64_t k_token,
+                                        int64_t k_head, int64_t kv_heads, int dtype, const float* q_gain,
+                                        const float* k_gain, int norm, float eps, int64_t n, int64_t dim,
+                                        int64_t rotary_dim, int interleaved, double base, const double* freqs,
+                                        const void* positions, int id_bytes, int axes, int64_t axis_stride,
+                                        const int64_t* sections, void* dq, int64_t dq_token, int64_t dq_head, void* dk,
+                                        int64_t dk_token, int64_t dk_head, float* dq_gain, float* dk_gain,
+                                        void* cuda_stream);
+
+/*
+ * dmuon_attention -- softmax attention over whole prompts, packed one behind the other. For token i of a sequence and
+ * query head h, over the tokens j of the same sequence, up to i if causal: x_j = scale q_i . k_j of key head
+ * h / (heads / kv_heads), out_i = sum of softmax(x)_j v_j, lse_i = log of the sum of exp x_j.
+ *   q, k, v, out  device, bf16 (`dtype`), n tokens of heads (kv_heads) of `dim` columns, the next token's and head's
+ *               x_token and x_head elements away; 16-byte aligned, with strides of multiples of 8 elements. dim is a
+ *               multiple of 8, at most 128; heads a multiple of kv_heads. out must not overlap an input.
+ *   offsets     device, sequences + 1 int32 or int64 (id_bytes): sequence s is tokens offsets[s] up to, not including,
+ *               offsets[s + 1]. Sequences may be empty. NULL: `sequences` of equal length. Offsets that fall or leave
+ *               [0, n] give DMUON_ERR_INDEX at the next dmuon_check_status; what they reach inside the arrays is not
+ *               specified.
+ *   zero_outside  tokens before the first and behind the last sequence: 0 leaves their rows of out and lse as they
+ *               were, otherwise they become 0. They are not read.
+ *   lse         device, heads x n, fp32
+ * Sums, the largest and the running maximum are fp32; probabilities are rounded to bf16 for their product with v. A
+ * value that is not finite reaches no other sequence; within a causal one it may reach earlier tokens too, up to 127.
+ */
+DMUON_API int dmuon_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                              int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int dtype, int64_t n,
+                              int64_t heads, int64_t kv_heads, int64_t dim, const void* offsets, int id_bytes,
+                              int64_t sequences, int causal, float scale, int zero_outside, void* out,
+                              int64_t out_token, int64_t out_head, float* lse, void* cuda_stream);
+
+/*
+ * dmuon_attention_grad -- the backward pass at the stored out and lse. With p the softmax, D_i = dout_i . out_i,
+ * ds_ij = p_ij (dout_i . v_j - D_i):
+ *   dq_i = scale sum over j of ds_ij k_j,  dk_j = scale sum over i of ds_ij q_i,  dv_j = sum over i of p_ij dout_i,
+ * the last two over all query heads of their key head, added in a fixed order. Arrays as above; dq, dk and dv must
+ * overlap neither one another nor an input.
+ */
+DMUON_API int dmuon_attention_grad(const void* dout, int64_t dout_token, int64_t dout_head, const void* q,
+                                   int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
+                                   const void* v, int64_t v_token, int64_t v_head, const void* out, int64_t out_token,
+                                   int64_t out_head, const float* lse, int dtype, int64_t n, int64_t heads,
+                                   int64_t kv_heads, int64_t dim, const void* offsets, int id_bytes, int64_t sequences,
+                                   int causal, float scale, int zero_outside, void* dq, int64_t dq_token,
+                                   int64_t dq_head, void* dk, int64_t dk_token, int64_t dk_head, void* dv,
+                                   int64_t dv_token, int64_t dv_head, void* cuda_stream);
+
+/*
+ * dmuon_token_stats -- per row t of a model's logits, with z = logits / temperature and lp = log softmax(z):
+ * logp[t] = lp[targets[t]], entropy[t] = -sum of p lp (nats), and the `top` largest logits, the lowest column first
+ * among equals: top_ids[t, :] and their lp, top_logp[t, :].
+ *   logits    device, n x vocab, fp32 or bf16
+ *   targets   device, or NULL: every row counts and there is no logp. A row whose target is negative is not read: its
+ *             values are 0 and its ids -1. A target >= vocab counts as one, and gives DMUON_ERR_INDEX at the next
+ *             dmuon_check_status.
+ *   top       0 to 32, at most vocab; top_logp (fp32) and top_ids (int64) are n x top
+ *   norm      device, n x 2, fp32: the row's largest logit m and the sum of exp((x - m) / temperature)
+ * Logits of -infinity are tokens of probability 0. A row that holds NaN or +infinity, or nothing but -infinity, gives
+ * NaN; its ids are those of its largest numbers, -1 where there are no more of them. Exponentials as in
+ * dmuon_policy_loss.
+ */
+DMUON_API int dmuon_token_stats(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab,
+                                const void* targets, int id_bytes, int top, float temperature, float* logp,
+                                float* entropy, float* top_logp, int64_t* top_ids, float* norm, void* cuda_stream);
+
+/*
+ * dmuon_token_stats_grad -- the gradient of logp and entropy at the stored norm and entropy: with g = dlogp[t] and
+ * h = dentropy[t],
+ *   dlogits_j = 1 / temperature * (g (1[j = target] - p_j) - h p_j (lp_j + entropy))
+ *   dlogits   device, n x vocab, of the logits' type; may be logits (ldd == ld). Rows without a target become zeros.
+ * dlogp may be NULL (and targets, with it), and dentropy (and entropy, with it).
+ */
+DMUON_API int dmuon_token_stats_grad(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab,
+                                     const void* targets, int id_bytes, const float* norm, const float* entropy,
+                                     const float* dlogp, const float* dentropy, float temperature, void* dlogits,
+                                     int64_t ldd, void* cuda_stream);
+
+/*
  * Per-kernel CUDA-event timing (off by default; used by benchmarks). While enabled, the library records
  * a pair of CUDA events on the caller's stream around every kernel it launches. dmuon_timing_read
  * waits for the recorded events, writes per kernel class the summed elapsed milliseconds and the
@@ -414,9 +523,10 @@ DMUON_API int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, in
  * ms_out and launches_out must each hold DMUON_TIMING_CLASSES entries (host memory).
  */
 #define DMUON_TIMING_CLASSES 6
-/* dmuon_timing_read_launches also reports the token operators, as classes 6 embedding, 7 RMS norm and
- * 8 policy loss: one record per call. dmuon_timing_read leaves them out. */
-#define DMUON_LAUNCH_CLASSES 9
+/* dmuon_timing_read_launches also reports the token operators, as classes 6 embedding, 7 RMS norm, 8 policy loss,
+ * 9 per-head norm and rotation, 10 attention and 11 token statistics: one record per call. dmuon_timing_read leaves
+ * them out. */
+#define DMUON_LAUNCH_CLASSES 12
 DMUON_API int dmuon_timing_enable(int on);
 DMUON_API int dmuon_timing_read(double* ms_out, int64_t* launches_out);
 

@@ -9,8 +9,8 @@ call raises ``LibraryNotBuilt``.
     dm.muon_step(params, grads, momenta, lr=0.02, beta=0.95, coeffs=dm.POLAR_EXPRESS)
 
 The pages' own names -- newton_schulz, NewtonSchulz and the Muon optimizer -- live in
-newton_schulz_momentum_gb300.optim, and the token operators (embedding, residual RMS norm, policy loss) in
-newton_schulz_momentum_gb300.token_ops, with torch modules around them in .layers; these import torch and are
+newton_schulz_momentum_gb300.optim, and the token operators (embedding, residual RMS norm, policy loss,
+per-head norm with rotation, attention, token statistics) in newton_schulz_momentum_gb300.token_ops, with torch modules around them in .layers; these import torch and are
 reachable here as attributes.
 """
 
@@ -56,12 +56,14 @@ EXPORTS = (
     "dmuon_assign_owners", "dmuon_adamw_step", "dmuon_ns_tp", "dmuon_muon_step_host",
     "dmuon_timing_read_launches", "dmuon_plan_info", "dmuon_selftest_bounded_wait", "dmuon_selftest_range_check",
     "dmuon_set_graph_replay", "dmuon_embedding", "dmuon_embedding_grad", "dmuon_add_rmsnorm",
-    "dmuon_add_rmsnorm_grad", "dmuon_policy_loss", "dmuon_token_logprobs",
+    "dmuon_add_rmsnorm_grad", "dmuon_policy_loss", "dmuon_token_logprobs", "dmuon_qk_norm_rotary",
+    "dmuon_qk_norm_rotary_grad", "dmuon_attention", "dmuon_attention_grad", "dmuon_token_stats",
+    "dmuon_token_stats_grad",
 )
 COST_MODELS = {"elements": 0, "gram_flops": 1, "direct_flops": 2}
 NOALLOC_MAX_ELEMS = 268435456
 TIMING_CLASSES = ("momentum_sumsq", "finalize_norms", "normalize_cast", "gemm_tc", "adamw", "tp_reduce")
-LAUNCH_CLASSES = TIMING_CLASSES + ("embedding", "rmsnorm", "policy_loss")
+LAUNCH_CLASSES = TIMING_CLASSES + ("embedding", "rmsnorm", "policy_loss", "qk_rotary", "attention", "token_stats")
 
 
 class LibraryNotBuilt(RuntimeError):
@@ -122,6 +124,15 @@ def lib():
     L.dmuon_policy_loss.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp,
                                     i64, vp]
     L.dmuon_token_logprobs.argtypes = [vp, i32, i64, i64, i64, vp, i32, f32, vp, vp]
+    heads = [vp, i64, i64]
+    turns = [i32, vp, vp, i32, f32, i64, i64, i64, i32, f64, vp, vp, i32, i32, i64, vp]
+    L.dmuon_qk_norm_rotary.argtypes = heads + [i64] + heads + [i64] + turns + heads * 2 + [vp]
+    L.dmuon_qk_norm_rotary_grad.argtypes = (heads * 2 + [i64]) * 2 + turns + heads * 2 + [vp, vp, vp]
+    prompts = [i32, i64, i64, i64, i64, vp, i32, i64, i32, f32, i32]
+    L.dmuon_attention.argtypes = heads * 3 + prompts + heads + [vp, vp]
+    L.dmuon_attention_grad.argtypes = heads * 5 + [vp] + prompts + heads * 3 + [vp]
+    L.dmuon_token_stats.argtypes = [vp, i32, i64, i64, i64, vp, i32, i32, f32, vp, vp, vp, vp, vp, vp]
+    L.dmuon_token_stats_grad.argtypes = [vp, i32, i64, i64, i64, vp, i32, vp, vp, vp, vp, f32, vp, i64, vp]
     for name in EXPORTS:
         if name not in ("dmuon_last_error", "dmuon_version"):
             getattr(L, name).restype = ctypes.c_int
@@ -489,8 +500,9 @@ def direct_flops(m, n, steps=5, dense=False):
 
 
 _TOKEN_OPS = ("embedding", "embedding_grad", "add_rmsnorm", "add_rmsnorm_fp8", "add_rmsnorm_grad", "policy_loss",
-              "token_logprobs")
-_LAYERS = ("Embedding", "AddRMSNorm", "PolicyLoss")
+              "token_logprobs", "qk_norm_rotary", "qk_norm_rotary_grad", "attention", "attention_grad", "token_stats",
+              "token_stats_grad")
+_LAYERS = ("Embedding", "AddRMSNorm", "PolicyLoss", "QKNormRotary", "Attention", "TokenStats")
 
 
 def __getattr__(name):

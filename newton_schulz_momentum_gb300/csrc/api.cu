@@ -256,12 +256,13 @@ cudaEvent_t take_event() {
 }
 
 // Names of the launch classes (dmuon.h), also the NVTX range names of their launches.
-enum { kClsEmbedding = 6, kClsRmsNorm = 7, kClsPolicy = 8 };
+enum { kClsEmbedding = 6, kClsRmsNorm = 7, kClsPolicy = 8, kClsRotary = 9, kClsAttention = 10, kClsStats = 11 };
 const char* const kClassNames[DMUON_LAUNCH_CLASSES] = {"dmuon momentum_sumsq", "dmuon finalize_norms",
                                                         "dmuon normalize_cast", "dmuon gemm_tc",
                                                         "dmuon adamw",          "dmuon tp_reduce",
                                                         "dmuon embedding",      "dmuon rmsnorm",
-                                                        "dmuon policy_loss"};
+                                                        "dmuon policy_loss",    "dmuon qk_rotary",
+                                                        "dmuon attention",      "dmuon token_stats"};
 
 // Records events around one launch when timing is on (and an NVTX range around its host-side enqueue, for
 // a profiler's timeline); otherwise just launches.
@@ -1430,6 +1431,135 @@ int run_policy(PolicyLaunch& p, cudaStream_t stream) {
   return DMUON_OK;
 }
 
+// Heads of n tokens: element (t, h, c) lies `token` and `head` elements from the next token's and head's. An output's
+// rows must not overlap.
+int check_heads(const char* name, const void* ptr, int dtype, int64_t token, int64_t head, int64_t heads, int64_t dim,
+                int64_t n, bool output) {
+  if (n > 0 && !ptr) return fail(DMUON_ERR_INVALID_ARG, "%s must not be NULL", name);
+  if (!aligned_to(ptr, dtype == DMUON_F32 ? 4 : 2))
+    return fail(DMUON_ERR_INVALID_ARG, "%s must be aligned to its elements", name);
+  if (token < 0 || head < 0) return fail(DMUON_ERR_INVALID_ARG, "the strides of %s must not be negative", name);
+  const __int128 by_token = (heads - 1) * static_cast<__int128>(head) + dim;
+  const __int128 by_head = (std::max<int64_t>(n, 1) - 1) * static_cast<__int128>(token) + dim;
+  const bool apart = (heads == 1 || head >= dim) && (n <= 1 || token >= by_token);
+  const bool apart_by_head = (n <= 1 || token >= dim) && (heads == 1 || head >= by_head);
+  if (output && n > 0 && !apart && !apart_by_head)
+    return fail(DMUON_ERR_INVALID_ARG, "the strides of %s let its rows overlap", name);
+  return DMUON_OK;
+}
+
+// An output may go over an input head by head: with other strides its rows would fall on rows not yet read.
+int check_heads_in_place(const char* out_name, const void* out, int64_t out_token, int64_t out_head, const char* in_name,
+                         const void* in, int64_t in_token, int64_t in_head, int64_t heads, int64_t n) {
+  if (out && out == in && ((n > 1 && out_token != in_token) || (heads > 1 && out_head != in_head)))
+    return fail(DMUON_ERR_INVALID_ARG, "%s is written over %s, so their strides must be equal", out_name, in_name);
+  return DMUON_OK;
+}
+
+int check_fp32(const char* name, const void* ptr, bool needed) {
+  if (needed && !ptr) return fail(DMUON_ERR_INVALID_ARG, "%s must not be NULL", name);
+  if (!aligned_to(ptr, 4)) return fail(DMUON_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
+  return DMUON_OK;
+}
+
+int check_temperature(float temperature) {
+  if (!(temperature >= 1e-30f) || !std::isfinite(temperature))
+    return fail(DMUON_ERR_INVALID_ARG, "temperature must be finite and >= 1e-30");
+  return DMUON_OK;
+}
+
+// Checks what both passes of the per-head norm with rotation share, and fills it into the launch.
+int set_rotary(RotaryLaunch& p, int64_t heads, int64_t kv_heads, int dtype, const float* q_gain, const float* k_gain,
+               int norm, float eps, int64_t n, int64_t dim, int64_t rotary_dim, int interleaved, double base,
+               const double* freqs, const void* positions, int id_bytes, int axes, int64_t axis_stride,
+               const int64_t* sections) {
+  if (n < 0 || n > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "n must be in [0, 2^31 - 1], got %lld", (long long)n);
+  if (dtype != DMUON_F32 && dtype != DMUON_BF16)
+    return fail(DMUON_ERR_INVALID_ARG, "dtype must be DMUON_F32 (0) or DMUON_BF16 (1), got %d", dtype);
+  if (heads < 1 || kv_heads < 0 || heads > 65535 || kv_heads > 65535)
+    return fail(DMUON_ERR_INVALID_ARG, "heads must be in [1, 65535] and kv_heads in [0, 65535]");
+  if (dim < 2 || dim > 256 || dim % 2)
+    return fail(dim > 256 ? DMUON_ERR_UNSUPPORTED : DMUON_ERR_INVALID_ARG,
+                "dim must be even and in [2, 256], got %lld", (long long)dim);
+  if (rotary_dim < 0 || rotary_dim > dim || rotary_dim % 2)
+    return fail(DMUON_ERR_INVALID_ARG, "rotary_dim must be even and in [0, dim], got %lld", (long long)rotary_dim);
+  if (axes < 1 || axes > 4) return fail(DMUON_ERR_INVALID_ARG, "axes must be in [1, 4], got %d", axes);
+  int st = check_ids(positions, id_bytes, n);
+  if (st == DMUON_OK) st = check_fp32("q_gain", q_gain, false);
+  if (st == DMUON_OK) st = check_fp32("k_gain", k_gain, false);
+  if (st != DMUON_OK) return st;
+  if (axes > 1 && axis_stride < 0) return fail(DMUON_ERR_INVALID_ARG, "axis_stride must not be negative");
+  if (!norm && (q_gain || k_gain)) return fail(DMUON_ERR_INVALID_ARG, "gains need the norm");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(DMUON_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  const int half = static_cast<int>(rotary_dim / 2);
+  for (int& end : p.section_end) end = half;
+  if (axes > 1) {
+    if (!sections) return fail(DMUON_ERR_INVALID_ARG, "sections must not be NULL with several axes");
+    int64_t sum = 0;
+    for (int a = 0; a < axes; ++a) {
+      if (sections[a] < 0 || sections[a] > half) return fail(DMUON_ERR_INVALID_ARG, "sections must lie in [0, rotary_dim / 2]");
+      sum += sections[a];
+      if (a < 3) p.section_end[a] = static_cast<int>(sum);
+    }
+    if (sum != half) return fail(DMUON_ERR_INVALID_ARG, "sections must add up to rotary_dim / 2, not %lld", (long long)sum);
+  }
+  if (!freqs && (!(base > 0.0) || !std::isfinite(base)))
+    return fail(DMUON_ERR_INVALID_ARG, "base must be finite and > 0");
+  for (int j = 0; j < half; ++j) {
+    const double f = freqs ? freqs[j] : std::pow(base, -static_cast<double>(j) / half);
+    const double turns = f / 6.283185307179586476925287;  // revolutions per position
+    if (!std::isfinite(turns) || std::fabs(turns) > 1e9)
+      return fail(DMUON_ERR_INVALID_ARG, "frequency %d is not finite or beyond 1e9 revolutions", j);
+    p.freqs[j] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64) < 18446744073709551616.0
+                                           ? std::ldexp(turns - std::floor(turns), 64) : 0.0);
+  }
+  p.heads[0] = static_cast<int>(heads), p.heads[1] = static_cast<int>(kv_heads);
+  p.gain[0] = q_gain, p.gain[1] = k_gain;
+  p.dtype = dtype, p.dim = static_cast<int>(dim), p.rotary_dim = static_cast<int>(rotary_dim);
+  p.interleaved = interleaved != 0, p.norm = norm != 0, p.eps = eps, p.n = n;
+  p.positions = positions, p.id_bytes = id_bytes, p.axes = axes, p.axis_stride = axis_stride;
+  return DMUON_OK;
+}
+
+// Checks the sizes and sequences of an attention call, and fills them into the launch.
+int set_attention(AttentionLaunch& p, int dtype, int64_t n, int64_t heads, int64_t kv_heads, int64_t dim,
+                  const void* offsets, int id_bytes, int64_t sequences, int causal, float scale, int zero_outside) {
+  if (dtype != DMUON_BF16)
+    return fail(DMUON_ERR_INVALID_ARG, "attention is of DMUON_BF16 (1) alone, got dtype %d", dtype);
+  if (n < 0 || n > kMaxTokens) return fail(DMUON_ERR_INVALID_ARG, "n must be in [0, 2^31 - 1], got %lld", (long long)n);
+  if (kv_heads < 1 || heads < kv_heads || heads % kv_heads || heads > 65535)
+    return fail(DMUON_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, and at most 65535");
+  if (dim < 8 || dim % 8) return fail(DMUON_ERR_INVALID_ARG, "dim must be a multiple of 8, got %lld", (long long)dim);
+  if (dim > 128) return fail(DMUON_ERR_UNSUPPORTED, "dim must be at most 128, got %lld", (long long)dim);
+  if (n * heads > (int64_t(1) << 40)) return fail(DMUON_ERR_UNSUPPORTED, "more than 2^40 rows");
+  if (sequences < (offsets ? 0 : 1) || sequences > kMaxTokens)
+    return fail(DMUON_ERR_INVALID_ARG, "sequences must be in [1, 2^31 - 1] (0 with offsets), got %lld", (long long)sequences);
+  if (offsets) {
+    const int st = check_ids(offsets, id_bytes, 1);
+    if (st != DMUON_OK) return st;
+  } else if (n % sequences) {
+    return fail(DMUON_ERR_INVALID_ARG, "without offsets the sequences are of equal length: n must be a multiple of them");
+  }
+  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+  p.n = n, p.heads = static_cast<int>(heads), p.kv_heads = static_cast<int>(kv_heads), p.dim = static_cast<int>(dim);
+  p.offsets = offsets, p.id_bytes = id_bytes, p.sequences = sequences;
+  p.causal = causal != 0, p.scale = scale, p.zero_outside = zero_outside != 0;
+  return DMUON_OK;
+}
+
+// One array of an attention call: heads that tensor-map copies and 16-byte accesses can reach.
+int set_heads(HeadArray& a, const char* name, const void* ptr, int64_t token, int64_t head, int64_t heads,
+              const AttentionLaunch& p, bool output) {
+  const int st = check_heads(name, ptr, DMUON_BF16, token, head, heads, p.dim, p.n, output);
+  if (st != DMUON_OK) return st;
+  if (!aligned_to(ptr, 16) || token % 8 || head % 8)
+    return fail(DMUON_ERR_INVALID_ARG, "%s must be 16-byte aligned with strides of multiples of 8 elements", name);
+  if (token >= int64_t(1) << 38 || head >= int64_t(1) << 38)
+    return fail(DMUON_ERR_UNSUPPORTED, "the strides of %s are beyond 2^38 elements", name);
+  a.data = ptr, a.token = token, a.head = head;
+  return DMUON_OK;
+}
+
 }  // namespace
 
 int set_error(int status, const char* message) { return fail(status, "%s", message); }
@@ -2017,6 +2147,263 @@ int dmuon_token_logprobs(const void* logits, int dtype, int64_t ld, int64_t n, i
     p.logp = logp;
     set_temperature(p, temperature);
     return run_policy(p, static_cast<cudaStream_t>(cuda_stream));
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_qk_norm_rotary(const void* q, int64_t q_token, int64_t q_head, int64_t heads, const void* k, int64_t k_token,
+                         int64_t k_head, int64_t kv_heads, int dtype, const float* q_gain, const float* k_gain, int norm,
+                         float eps, int64_t n, int64_t dim, int64_t rotary_dim, int interleaved, double base,
+                         const double* freqs, const void* positions, int id_bytes, int axes, int64_t axis_stride,
+                         const int64_t* sections, void* q_out, int64_t q_out_token, int64_t q_out_head, void* k_out,
+                         int64_t k_out_token, int64_t k_out_head, void* cuda_stream) {
+  try {
+    RotaryLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    int st = set_rotary(p, heads, kv_heads, dtype, q_gain, k_gain, norm, eps, n, dim, rotary_dim, interleaved, base, freqs,
+                        positions, id_bytes, axes, axis_stride, sections);
+    if (st == DMUON_OK) st = check_heads("q", q, dtype, q_token, q_head, heads, dim, n, false);
+    if (st == DMUON_OK) st = check_heads("q_out", q_out, dtype, q_out_token, q_out_head, heads, dim, n, true);
+    if (st == DMUON_OK) st = check_heads_in_place("q_out", q_out, q_out_token, q_out_head, "q", q, q_token, q_head, heads, n);
+    if (st == DMUON_OK && kv_heads > 0) {
+      st = check_heads("k", k, dtype, k_token, k_head, kv_heads, dim, n, false);
+      if (st == DMUON_OK) st = check_heads("k_out", k_out, dtype, k_out_token, k_out_head, kv_heads, dim, n, true);
+      if (st == DMUON_OK)
+        st = check_heads_in_place("k_out", k_out, k_out_token, k_out_head, "k", k, k_token, k_head, kv_heads, n);
+    }
+    if (st != DMUON_OK) return st;
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    p.x[0] = q, p.x_token[0] = q_token, p.x_head[0] = q_head;
+    p.x[1] = k, p.x_token[1] = k_token, p.x_head[1] = k_head;
+    p.y[0] = q_out, p.y_token[0] = q_out_token, p.y_head[0] = q_out_head;
+    p.y[1] = k_out, p.y_token[1] = k_out_token, p.y_head[1] = k_out_head;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsRotary, stream, [&] { return launch_rotary(p, ds->sms, stream); }), "norm and rotation launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_qk_norm_rotary_grad(const void* dq_out, int64_t dq_out_token, int64_t dq_out_head, const void* q, int64_t q_token,
+                              int64_t q_head, int64_t heads, const void* dk_out, int64_t dk_out_token,
+                              int64_t dk_out_head, const void* k, int64_t k_token, int64_t k_head, int64_t kv_heads,
+                              int dtype, const float* q_gain, const float* k_gain, int norm, float eps, int64_t n,
+                              int64_t dim, int64_t rotary_dim, int interleaved, double base, const double* freqs,
+                              const void* positions, int id_bytes, int axes, int64_t axis_stride, const int64_t* sections,
+                              void* dq, int64_t dq_token, int64_t dq_head, void* dk, int64_t dk_token, int64_t dk_head,
+                              float* dq_gain, float* dk_gain, void* cuda_stream) {
+  try {
+    RotaryLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    int st = set_rotary(p, heads, kv_heads, dtype, q_gain, k_gain, norm, eps, n, dim, rotary_dim, interleaved, base, freqs,
+                        positions, id_bytes, axes, axis_stride, sections);
+    if (st == DMUON_OK) st = check_heads("dq_out", dq_out, dtype, dq_out_token, dq_out_head, heads, dim, n, false);
+    if (st == DMUON_OK && norm) st = check_heads("q", q, dtype, q_token, q_head, heads, dim, n, false);
+    if (st == DMUON_OK) st = check_heads("dq", dq, dtype, dq_token, dq_head, heads, dim, n, true);
+    if (st == DMUON_OK)
+      st = check_heads_in_place("dq", dq, dq_token, dq_head, "dq_out", dq_out, dq_out_token, dq_out_head, heads, n);
+    if (st == DMUON_OK && norm) st = check_heads_in_place("dq", dq, dq_token, dq_head, "q", q, q_token, q_head, heads, n);
+    if (st == DMUON_OK && kv_heads > 0) {
+      st = check_heads("dk_out", dk_out, dtype, dk_out_token, dk_out_head, kv_heads, dim, n, false);
+      if (st == DMUON_OK && norm) st = check_heads("k", k, dtype, k_token, k_head, kv_heads, dim, n, false);
+      if (st == DMUON_OK) st = check_heads("dk", dk, dtype, dk_token, dk_head, kv_heads, dim, n, true);
+      if (st == DMUON_OK)
+        st = check_heads_in_place("dk", dk, dk_token, dk_head, "dk_out", dk_out, dk_out_token, dk_out_head, kv_heads, n);
+      if (st == DMUON_OK && norm)
+        st = check_heads_in_place("dk", dk, dk_token, dk_head, "k", k, k_token, k_head, kv_heads, n);
+    }
+    if (st == DMUON_OK) st = check_fp32("dq_gain", dq_gain, false);
+    if (st == DMUON_OK) st = check_fp32("dk_gain", dk_gain, false);
+    if (st != DMUON_OK) return st;
+    if (!norm && (dq_gain || dk_gain)) return fail(DMUON_ERR_INVALID_ARG, "gains need the norm");
+    if (kv_heads == 0 && dk_gain) return fail(DMUON_ERR_INVALID_ARG, "dk_gain needs keys");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK) return st;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    if (n == 0) {
+      for (float* g : {dq_gain, dk_gain})
+        if (g) DM_CUDA(cudaMemsetAsync(g, 0, static_cast<size_t>(dim) * sizeof(float), stream), "zero a gain's gradient");
+      return DMUON_OK;
+    }
+    p.dy[0] = dq_out, p.dy_token[0] = dq_out_token, p.dy_head[0] = dq_out_head;
+    p.dy[1] = dk_out, p.dy_token[1] = dk_out_token, p.dy_head[1] = dk_out_head;
+    if (norm) {
+      p.x[0] = q, p.x_token[0] = q_token, p.x_head[0] = q_head;
+      p.x[1] = k, p.x_token[1] = k_token, p.x_head[1] = k_head;
+    }
+    p.y[0] = dq, p.y_token[0] = dq_token, p.y_head[0] = dq_head;
+    p.y[1] = dk, p.y_token[1] = dk_token, p.y_head[1] = dk_head;
+    p.dgain[0] = dq_gain, p.dgain[1] = dk_gain;
+    p.grad = p.planning = 1;
+    DM_CUDA(launch_rotary(p, ds->sms, stream), "norm and rotation gradient occupancy");
+    p.planning = 0;
+    char* ws = nullptr;
+    st = token_workspace(*ds, rotary_workspace(p, nullptr), stream, &ws);
+    if (st != DMUON_OK) return st;
+    rotary_workspace(p, ws);
+    DM_CUDA(timed(kClsRotary, stream, [&] { return launch_rotary(p, ds->sms, stream); }),
+            "norm and rotation gradient launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_attention(const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,
+                    const void* v, int64_t v_token, int64_t v_head, int dtype, int64_t n, int64_t heads, int64_t kv_heads,
+                    int64_t dim, const void* offsets, int id_bytes, int64_t sequences, int causal, float scale,
+                    int zero_outside, void* out, int64_t out_token, int64_t out_head, float* lse, void* cuda_stream) {
+  try {
+    AttentionLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    int st = set_attention(p, dtype, n, heads, kv_heads, dim, offsets, id_bytes, sequences, causal, scale, zero_outside);
+    if (st == DMUON_OK) st = set_heads(p.q, "q", q, q_token, q_head, heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.k, "k", k, k_token, k_head, kv_heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.v, "v", v, v_token, v_head, kv_heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.out, "out", out, out_token, out_head, heads, p, true);
+    if (st == DMUON_OK) st = check_fp32("lse", lse, n > 0);
+    if (st != DMUON_OK) return st;
+    if (n > 0 && (out == q || out == k || out == v))
+      return fail(DMUON_ERR_INVALID_ARG, "out cannot go over q, k or v, which other rows still read");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    p.lse = lse;
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention(p, ds->sms, stream); }), "attention launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_attention_grad(const void* dout, int64_t dout_token, int64_t dout_head, const void* q, int64_t q_token,
+                         int64_t q_head, const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                         int64_t v_head, const void* out, int64_t out_token, int64_t out_head, const float* lse,
+                         int dtype, int64_t n, int64_t heads, int64_t kv_heads, int64_t dim, const void* offsets,
+                         int id_bytes, int64_t sequences, int causal, float scale, int zero_outside, void* dq,
+                         int64_t dq_token, int64_t dq_head, void* dk, int64_t dk_token, int64_t dk_head, void* dv,
+                         int64_t dv_token, int64_t dv_head, void* cuda_stream) {
+  try {
+    AttentionLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    int st = set_attention(p, dtype, n, heads, kv_heads, dim, offsets, id_bytes, sequences, causal, scale, zero_outside);
+    if (st == DMUON_OK) st = set_heads(p.dout, "dout", dout, dout_token, dout_head, heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.q, "q", q, q_token, q_head, heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.k, "k", k, k_token, k_head, kv_heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.v, "v", v, v_token, v_head, kv_heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.out, "out", out, out_token, out_head, heads, p, false);
+    if (st == DMUON_OK) st = set_heads(p.dq, "dq", dq, dq_token, dq_head, heads, p, true);
+    if (st == DMUON_OK) st = set_heads(p.dk, "dk", dk, dk_token, dk_head, kv_heads, p, true);
+    if (st == DMUON_OK) st = set_heads(p.dv, "dv", dv, dv_token, dv_head, kv_heads, p, true);
+    if (st == DMUON_OK) st = check_fp32("lse", lse, n > 0);
+    if (st != DMUON_OK) return st;
+    if (n > 0)
+      for (const void* o : {dq, dk, dv})
+        for (const void* i : {dout, q, k, v, out})
+          if (o == i) return fail(DMUON_ERR_INVALID_ARG, "dq, dk and dv cannot go over an input, which other rows still read");
+    if (n > 0 && (dq == dk || dq == dv || dk == dv))
+      return fail(DMUON_ERR_INVALID_ARG, "dq, dk and dv must be different arrays");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    p.lse = const_cast<float*>(lse);
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    char* ws = nullptr;
+    st = token_workspace(*ds, attention_workspace(p, nullptr), stream, &ws);
+    if (st != DMUON_OK) return st;
+    attention_workspace(p, ws);
+    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention_grad(p, ds->sms, stream); }),
+            "attention gradient launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_token_stats(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab, const void* targets,
+                      int id_bytes, int top, float temperature, float* logp, float* entropy, float* top_logp,
+                      int64_t* top_ids, float* norm, void* cuda_stream) {
+  try {
+    int st = check_token_sizes(n, vocab, "vocab");
+    if (st == DMUON_OK && targets) st = check_ids(targets, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+    if (st == DMUON_OK) st = check_fp32("logp", logp, n > 0 && targets);
+    if (st == DMUON_OK) st = check_fp32("entropy", entropy, n > 0);
+    if (st == DMUON_OK) st = check_fp32("norm", norm, n > 0);
+    if (st == DMUON_OK) st = check_temperature(temperature);
+    if (st != DMUON_OK) return st;
+    if (top < 0 || top > kMaxAlternatives || top > vocab)
+      return fail(DMUON_ERR_INVALID_ARG, "top must be in [0, %d] and at most vocab, got %d", kMaxAlternatives, top);
+    if (top > 0 && n > 0 && (!top_logp || !top_ids || !aligned_to(top_logp, 4) || !aligned_to(top_ids, 8)))
+      return fail(DMUON_ERR_INVALID_ARG, "top_logp and top_ids must be aligned to their elements and not NULL with a top");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    StatsLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+    p.targets = targets, p.id_bytes = id_bytes, p.top = top;
+    PolicyLaunch scales;
+    set_temperature(scales, temperature);
+    p.inv_temperature = scales.inv_temperature, p.inv_temperature_low = scales.inv_temperature_low;
+    p.log2e_over_t = scales.log2e_over_t;
+    p.logp = targets ? logp : nullptr, p.entropy = entropy, p.norm = norm, p.top_logp = top_logp, p.top_ids = top_ids;
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsStats, stream, [&] { return launch_token_stats(p, ds->sms, stream); }), "token statistics launch");
+    return DMUON_OK;
+  } catch (const std::exception& e) {
+    return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
+  }
+}
+
+int dmuon_token_stats_grad(const void* logits, int dtype, int64_t ld, int64_t n, int64_t vocab, const void* targets,
+                           int id_bytes, const float* norm, const float* entropy, const float* dlogp,
+                           const float* dentropy, float temperature, void* dlogits, int64_t ldd, void* cuda_stream) {
+  try {
+    int st = check_token_sizes(n, vocab, "vocab");
+    if (st == DMUON_OK && targets) st = check_ids(targets, id_bytes, n);
+    if (st == DMUON_OK) st = check_elements("logits", logits, dtype, ld, vocab, n);
+    if (st == DMUON_OK) st = check_elements("dlogits", dlogits, dtype, ldd, vocab, n);
+    if (st == DMUON_OK) st = check_in_place("dlogits", dlogits, ldd, "logits", logits, ld, n);
+    if (st == DMUON_OK) st = check_fp32("norm", norm, n > 0);
+    if (st == DMUON_OK) st = check_fp32("dlogp", dlogp, false);
+    if (st == DMUON_OK) st = check_fp32("dentropy", dentropy, false);
+    if (st == DMUON_OK) st = check_fp32("entropy", entropy, n > 0 && dentropy);
+    if (st == DMUON_OK) st = check_temperature(temperature);
+    if (st != DMUON_OK) return st;
+    if (dlogp && !targets && n > 0) return fail(DMUON_ERR_INVALID_ARG, "dlogp needs targets");
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState* ds = nullptr;
+    st = current_device(&ds);
+    if (st != DMUON_OK || n == 0) return st;
+    StatsGradLaunch p;
+    std::memset(&p, 0, sizeof(p));
+    p.logits = logits, p.dtype = dtype, p.ld = ld, p.n = n, p.vocab = vocab;
+    p.targets = targets, p.id_bytes = id_bytes;
+    p.norm = norm, p.entropy = entropy, p.dlogp = dlogp, p.dentropy = dentropy;
+    PolicyLaunch scales;
+    set_temperature(scales, temperature);
+    p.inv_temperature = scales.inv_temperature, p.log2e_over_t = scales.log2e_over_t;
+    p.dlogits = dlogits, p.ldd = ldd;
+    p.status = ds->status;
+    cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
+    DM_CUDA(timed(kClsStats, stream, [&] { return launch_token_stats_grad(p, stream); }),
+            "token statistics gradient launch");
+    return DMUON_OK;
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
   }

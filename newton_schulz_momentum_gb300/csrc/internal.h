@@ -301,8 +301,9 @@ cudaError_t launch_normalize_cast(const RowLaunch& p, int64_t ntiles, cudaStream
 
 // ------------------------------------------------------------------------------------------------
 // Token operators: embedding lookup and gradient (embedding.cu), residual addition with RMS norm
-// (rmsnorm.cu), policy loss from logits (policy_loss.cu). Element types: 0 fp32, 1 bf16, 2 e4m3. Leading
-// dimensions count elements. Buffers need their element type's alignment only.
+// (rmsnorm.cu), policy loss from logits (policy_loss.cu), per-head norms with rotation (qk_rotary.cu), attention
+// (attention.cu), log-probabilities with entropy and alternatives (token_stats.cu). Element types: 0 fp32, 1 bf16, 2
+// e4m3. Leading dimensions count elements. Buffers need their element type's alignment only, attention's 16 bytes.
 // ------------------------------------------------------------------------------------------------
 
 struct EmbeddingLaunch {
@@ -423,6 +424,88 @@ struct PolicyLaunch {
 };
 int64_t policy_workspace(int64_t n);
 cudaError_t launch_policy(PolicyLaunch& p, int sms, cudaStream_t stream);
+
+// Heads of a token: element (t, h, c) lies at data[t * token + h * head + c].
+struct HeadArray {
+  const void* data;  // an output's is written to
+  int64_t token, head;
+};
+
+// Per-head norm with position rotation (qk_rotary.cu). Index 0 are the queries, 1 the keys (heads 0: none).
+struct RotaryLaunch {
+  const void *x[2], *dy[2];  // dy: backward only
+  void* y[2];                // backward: dx
+  int64_t x_token[2], x_head[2], dy_token[2], dy_head[2], y_token[2], y_head[2];
+  int heads[2];
+  const float* gain[2];  // may be null
+  float* dgain[2];       // backward only; may be null
+  int dtype, dim, rotary_dim, interleaved, norm, grad;
+  float eps;
+  int64_t n;
+  const void* positions;  // axes lists of n, axis_stride apart
+  int id_bytes, axes;
+  int64_t axis_stride;
+  int section_end[3];   // frequency j follows axis a where section_end[a - 1] <= j < section_end[a]
+  uint64_t freqs[128];  // share of a revolution per position, in units of 2^-64
+  // Set by launch_rotary: lanes per row, parts of a token's heads, rows of partials (workspace), 1 / dim.
+  int lanes, parts, npartials, planning;
+  float inv_dim;
+  float* partials;
+};
+// Workspace bytes of a planned backward launch (p.planning set, launch_rotary called); with `ws` it also places it.
+int64_t rotary_workspace(RotaryLaunch& p, char* ws);
+cudaError_t launch_rotary(RotaryLaunch& p, int sms, cudaStream_t stream);
+
+// Log-probabilities with entropy and alternatives (token_stats.cu).
+constexpr int kMaxAlternatives = 32;
+
+struct StatsLaunch {
+  const void* logits;
+  int dtype;
+  int64_t ld, n, vocab;
+  const void* targets;  // may be null: every row counts
+  int id_bytes, top;
+  float inv_temperature, inv_temperature_low, log2e_over_t;
+  float *logp, *entropy, *norm;  // logp null without targets; norm: largest logit and sum of each row
+  float* top_logp;               // n x top
+  int64_t* top_ids;
+  unsigned* status;
+  int cluster;  // CTAs per row, set by launch_token_stats
+};
+cudaError_t launch_token_stats(StatsLaunch& p, int sms, cudaStream_t stream);
+
+struct StatsGradLaunch {
+  const void* logits;
+  int dtype;
+  int64_t ld, n, vocab;
+  const void* targets;  // may be null with dlogp
+  int id_bytes;
+  const float *norm, *entropy, *dlogp, *dentropy;  // dlogp, or dentropy and entropy, may be null
+  float inv_temperature, log2e_over_t;
+  void* dlogits;
+  int64_t ldd;
+  unsigned* status;
+  int64_t parts;  // CTAs per row, set by launch_token_stats_grad
+};
+cudaError_t launch_token_stats_grad(StatsGradLaunch& p, cudaStream_t stream);
+
+// Attention over packed prompts (attention.cu). bf16.
+struct AttentionLaunch {
+  HeadArray q, k, v, out, dout, dq, dk, dv;
+  int64_t n;
+  int heads, kv_heads, dim;
+  const void* offsets;  // sequences + 1 of them; null: sequences of n / sequences tokens each
+  int id_bytes;
+  int64_t sequences;
+  int causal, zero_outside;
+  float scale;
+  float* lse;    // heads x n
+  float* delta;  // heads x n, workspace of the backward pass
+  unsigned* status;
+};
+int64_t attention_workspace(AttentionLaunch& p, char* ws);
+cudaError_t launch_attention(AttentionLaunch& p, int sms, cudaStream_t stream);
+cudaError_t launch_attention_grad(AttentionLaunch& p, int sms, cudaStream_t stream);
 
 // Record `message` as the calling thread's last error (returned by dmuon_last_error) and return status.
 int set_error(int status, const char* message);

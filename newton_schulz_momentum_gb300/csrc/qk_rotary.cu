@@ -1,0 +1,405 @@
+// RMS norm of each head's queries and keys with the position rotation in the same pass, and its backward pass.
+//
+// Per token and head with row x of `dim` elements: z = x rho g with rho = (mean x^2 + eps)^(-1/2) (or z = x without
+// the norm); the first rotary_dim columns are pairs, (j, j + rotary_dim / 2) or, interleaved, (2j, 2j + 1), turned by
+// the angle a_j = f_j * position:  y1 = z1 cos a - z2 sin a,  y2 = z2 cos a + z1 sin a.  With several axes frequency j
+// follows the position of the axis whose section it lies in. The other columns pass.
+//
+// Backward: d = dy turned by -a, dn = d g, dx = rho dn - x rho^3 / dim sum(dn x), dg = sum over tokens and heads of
+// d x rho.
+//
+// Angles. A frequency is held as its share of a revolution per position in units of 2^-64, so that frequency times
+// position modulo one revolution is the low half of one integer product, exact but for the frequency's own rounding
+// (2^-53 of it): positions of 2^31 are as good as small ones. fp32 angles would be off by 0.06 at position 10^6.
+//
+// Each element is read once and written once. A lane holds both ends of its pairs, so a turn needs no exchange, and a
+// row's sums are shuffles among the lanes that hold it. A warp takes a token's heads one group after another: the
+// angles, their sines and cosines are formed once for all of them. Rows whose columns come in whole 16-byte pieces are
+// read so; others element by element.
+#include <algorithm>
+
+#include "row_ops.h"
+#include "tc_ptx.h"
+
+namespace dmuon {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+// What one lane holds of a row: item i covers columns [lo, lo + V) and [hi, hi + V). z[m] of the first piece and
+// z[V + m] of the second; pair m is z[first(m)] and z[second(m)].
+template <int V, bool INTER>
+struct Pairs {
+  static __device__ __forceinline__ int first(int m) { return INTER && V > 1 ? 2 * m : m; }
+  static __device__ __forceinline__ int second(int m) { return INTER && V > 1 ? 2 * m + 1 : m + V; }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void load_piece(float* z, const T* p) {
+  if constexpr (V == 1) {
+    z[0] = row::to_f(*p);
+  } else {
+    float v[V];
+    row::unpack16<T>(v, *reinterpret_cast<const uint4*>(p));
+#pragma unroll
+    for (int m = 0; m < V; ++m) z[m] = v[m];
+  }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_piece(T* p, const float* z) {
+  if constexpr (V == 1) {
+    *p = row::from_f<T>(z[0]);
+  } else {
+    float v[V];
+#pragma unroll
+    for (int m = 0; m < V; ++m) v[m] = z[m];
+    *reinterpret_cast<uint4*>(p) = row::pack16(v);
+  }
+}
+
+// A lane's place in a row and its angles. I items per lane, `lanes` lanes per row.
+template <int V, int I, bool INTER>
+struct Place {
+  int lo[I], hi[I];
+  bool live[I];
+  uint32_t axis = 0;  // two bits per angle
+  uint64_t freq[I * V];
+
+  __device__ __forceinline__ Place(const RotaryLaunch& p, int lane_in_row) {
+    const int half = p.rotary_dim / 2, turned = half / V, items = p.dim / (2 * V);
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int it = lane_in_row + i * p.lanes;
+      live[i] = it < items;
+      if (it < turned) {
+        lo[i] = INTER ? 2 * V * it : V * it;
+        hi[i] = INTER ? lo[i] + V : lo[i] + half;
+      } else {
+        lo[i] = p.rotary_dim + (it - turned) * V;
+        hi[i] = lo[i] + (p.dim - p.rotary_dim) / 2;
+      }
+#pragma unroll
+      for (int m = 0; m < V; ++m) {
+        const int j = it * V + m;
+        freq[i * V + m] = it < turned ? p.freqs[j] : 0;
+        const uint32_t a = j >= p.section_end[0] ? (j >= p.section_end[1] ? (j >= p.section_end[2] ? 3 : 2) : 1) : 0;
+        axis |= a << (2 * (i * V + m));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void turns(const RotaryLaunch& p, int64_t token, float (&c)[I * V], float (&s)[I * V]) const {
+    int64_t pos[4];
+    pos[0] = row::load_id(p.positions, p.id_bytes, token);
+#pragma unroll
+    for (int a = 1; a < 4; ++a)
+      pos[a] = a < p.axes ? row::load_id(p.positions, p.id_bytes, a * p.axis_stride + token) : 0;
+#pragma unroll
+    for (int k = 0; k < I * V; ++k) {
+      int64_t at = pos[0];
+      if (p.axes > 1) {
+        const uint32_t a = (axis >> (2 * k)) & 3;
+        at = a == 0 ? pos[0] : a == 1 ? pos[1] : a == 2 ? pos[2] : pos[3];
+      }
+      const uint64_t share = freq[k] * static_cast<uint64_t>(at);  // of a revolution, modulo 1
+      // The nearest of 2^32 steps of a revolution, counted from -1/2 to 1/2: 2^-33 of a revolution off at most.
+      const int near = static_cast<int>(static_cast<uint32_t>((share + 0x80000000ull) >> 32));
+      sincospif(static_cast<float>(near) * 4.656612873077393e-10f, &s[k], &c[k]);  // 2^-31: halves of a revolution
+    }
+  }
+};
+
+__device__ __forceinline__ float sum_lanes(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int V, int I>
+__device__ __forceinline__ void load_row(float (&z)[I][2 * V], const T* x, const int (&lo)[I], const int (&hi)[I],
+                                         const bool (&live)[I], bool ok) {
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    if (ok && live[i]) {
+      load_piece<T, V>(z[i], x + lo[i]);
+      load_piece<T, V>(z[i] + V, x + hi[i]);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 2 * V; ++m) z[i][m] = 0.f;
+    }
+  }
+}
+
+template <int V, int I>
+__device__ __forceinline__ void load_gain(float (&g)[I][2 * V], const float* gain, const int (&lo)[I], const int (&hi)[I],
+                                          const bool (&live)[I]) {
+#pragma unroll
+  for (int i = 0; i < I; ++i)
+#pragma unroll
+    for (int m = 0; m < V; ++m) {
+      g[i][m] = gain && live[i] ? __ldg(gain + lo[i] + m) : 1.f;
+      g[i][V + m] = gain && live[i] ? __ldg(gain + hi[i] + m) : 1.f;
+    }
+}
+
+// Work of one warp: units of a token's head groups. A group is the 32 / lanes heads that a warp holds at once; groups
+// of queries come before those of keys, and part k of `parts` takes every parts-th of them.
+template <typename T, int V, int I, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p) {
+  using P = Pairs<V, INTER>;
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, sub = lane / p.lanes, per_warp = 32 / p.lanes;
+  const Place<V, I, INTER> at(p, lane % p.lanes);
+  ptx::griddep_wait();
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); unit < p.n * p.parts; unit += warps) {
+    const int64_t token = unit / p.parts;
+    const int part = static_cast<int>(unit - token * p.parts);
+    float c[I * V], s[I * V];
+    at.turns(p, token, c, s);
+    int before = 0;  // groups before this tensor's
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int heads = p.heads[w], groups = (heads + per_warp - 1) / per_warp;
+      int first = (part - before) % p.parts;
+      if (first < 0) first += p.parts;
+      before += groups;
+      if (first >= groups) continue;
+      float g[I][2 * V];
+      load_gain<V, I>(g, p.gain[w], at.lo, at.hi, at.live);
+      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
+      T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      for (int group = first; group < groups; group += p.parts) {
+        const int h = group * per_warp + sub;
+        const bool ok = h < heads;
+        float z[I][2 * V];
+        load_row<T, V, I>(z, x + h * p.x_head[w], at.lo, at.hi, at.live, ok);
+        if (p.norm) {
+          float sq = 0.f;
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int m = 0; m < 2 * V; ++m) sq = fmaf(z[i][m], z[i][m], sq);
+          const float rho = rsqrtf(fmaf(sum_lanes(sq, p.lanes), p.inv_dim, p.eps));
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int m = 0; m < 2 * V; ++m) z[i][m] = z[i][m] * rho * g[i][m];
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+#pragma unroll
+          for (int m = 0; m < V; ++m) {
+            float &a = z[i][P::first(m)], &b = z[i][P::second(m)];
+            const float ca = c[i * V + m], sa = s[i * V + m], a0 = a;
+            a = fmaf(a0, ca, -(b * sa));
+            b = fmaf(b, ca, a0 * sa);
+          }
+          if (ok && at.live[i]) {
+            store_piece<T, V>(y + h * p.y_head[w] + at.lo[i], z[i]);
+            store_piece<T, V>(y + h * p.y_head[w] + at.hi[i], z[i] + V);
+          }
+        }
+      }
+    }
+  }
+}
+
+// y holds dx and x the norm's input; dy the gradient that arrives.
+template <typename T, int V, int I, bool INTER>
+__global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_constant__ RotaryLaunch p) {
+  using P = Pairs<V, INTER>;
+  extern __shared__ float part_sums[];  // 2 x dim of each warp
+  ptx::griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / p.lanes, per_warp = 32 / p.lanes;
+  const Place<V, I, INTER> at(p, lane % p.lanes);
+  ptx::griddep_wait();
+  float sums[2][I][2 * V] = {};
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < p.n * p.parts; unit += warps) {
+    const int64_t token = unit / p.parts;
+    const int part = static_cast<int>(unit - token * p.parts);
+    float c[I * V], s[I * V];
+    at.turns(p, token, c, s);
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int heads = p.heads[w], groups = (heads + per_warp - 1) / per_warp;
+      int first = (part - before) % p.parts;
+      if (first < 0) first += p.parts;
+      before += groups;
+      if (first >= groups) continue;
+      float g[I][2 * V];
+      load_gain<V, I>(g, p.gain[w], at.lo, at.hi, at.live);
+      const T* dy = static_cast<const T*>(p.dy[w]) + token * p.dy_token[w];
+      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
+      T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      for (int group = first; group < groups; group += p.parts) {
+        const int h = group * per_warp + sub;
+        const bool ok = h < heads;
+        float d[I][2 * V], z[I][2 * V];
+        load_row<T, V, I>(d, dy + h * p.dy_head[w], at.lo, at.hi, at.live, ok);
+        if (p.norm) load_row<T, V, I>(z, x + h * p.x_head[w], at.lo, at.hi, at.live, ok);
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int m = 0; m < V; ++m) {
+            float &a = d[i][P::first(m)], &b = d[i][P::second(m)];
+            const float ca = c[i * V + m], sa = s[i * V + m], a0 = a;
+            a = fmaf(a0, ca, b * sa);
+            b = fmaf(b, ca, -(a0 * sa));
+          }
+        if (p.norm) {
+          float sq = 0.f, along = 0.f;
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int m = 0; m < 2 * V; ++m) {
+              sq = fmaf(z[i][m], z[i][m], sq);
+              along = fmaf(d[i][m] * g[i][m], z[i][m], along);
+            }
+          const float rho = rsqrtf(fmaf(sum_lanes(sq, p.lanes), p.inv_dim, p.eps));
+          const float back = rho * rho * (sum_lanes(along, p.lanes) * p.inv_dim);
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int m = 0; m < 2 * V; ++m) {
+              sums[w][i][m] = fmaf(d[i][m], z[i][m] * rho, sums[w][i][m]);
+              d[i][m] = rho * fmaf(-z[i][m], back, d[i][m] * g[i][m]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+          if (ok && at.live[i]) {
+            store_piece<T, V>(dx + h * p.y_head[w] + at.lo[i], d[i]);
+            store_piece<T, V>(dx + h * p.y_head[w] + at.hi[i], d[i] + V);
+          }
+      }
+    }
+  }
+  if (!p.partials) return;
+  // The warp's heads, then the CTA's warps, in fixed orders; the CTAs' sums are joined by rotary_gain_kernel.
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int m = 0; m < 2 * V; ++m) {
+        float v = sums[w][i][m];
+        for (int o = 16; o >= p.lanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        if (sub == 0 && at.live[i])
+          part_sums[(warp * 2 + w) * p.dim + (m < V ? at.lo[i] + m : at.hi[i] + m - V)] = v;
+      }
+  __syncthreads();
+  for (int k = threadIdx.x; k < 2 * p.dim; k += kThreads) {
+    float v = 0.f;
+    for (int q = 0; q < kWarps; ++q) v += part_sums[q * 2 * p.dim + k];
+    p.partials[static_cast<int64_t>(blockIdx.x) * 2 * p.dim + k] = v;
+  }
+}
+
+constexpr int kJoinThreads = 1024;
+
+// Sums of the gains' gradients over the CTAs of rotary_grad_kernel: 32 columns a CTA, warp q adds rows q, q + 32, ...
+__global__ void __launch_bounds__(kJoinThreads) rotary_gain_kernel(const __grid_constant__ RotaryLaunch p) {
+  __shared__ float part[32][33];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (k < 2 * p.dim)
+    for (int r = warp; r < p.npartials; r += 32) v += p.partials[static_cast<int64_t>(r) * 2 * p.dim + k];
+  part[warp][lane] = v;
+  __syncthreads();
+  if (warp != 0 || k >= 2 * p.dim) return;
+  v = 0.f;
+  for (int q = 0; q < 32; ++q) v += part[q][lane];
+  float* out = p.dgain[k / p.dim];
+  if (out) out[k % p.dim] = v;
+}
+
+bool whole_pieces(const RotaryLaunch& p, int v) {
+  const size_t size = p.dtype == 0 ? 4 : 2;
+  if (p.rotary_dim % (2 * v) != 0 || (p.dim - p.rotary_dim) % (2 * v) != 0) return false;
+  auto fits = [&](const void* ptr, int64_t token, int64_t head) {
+    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && token * size % 16 == 0 && head * size % 16 == 0;
+  };
+  for (int w = 0; w < 2; ++w) {
+    if (p.heads[w] == 0) continue;
+    if (!fits(p.y[w], p.y_token[w], p.y_head[w])) return false;
+    if (p.x[w] && !fits(p.x[w], p.x_token[w], p.x_head[w])) return false;
+    if (p.dy[w] && !fits(p.dy[w], p.dy_token[w], p.dy_head[w])) return false;
+  }
+  return true;
+}
+
+// Lanes per row for pieces of v elements: the power of two that holds a row's items, at most a warp.
+int lanes_for(const RotaryLaunch& p, int v) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * 2 * v < p.dim) lanes *= 2;
+  return lanes;
+}
+
+template <typename K>
+cudaError_t set_grid(RotaryLaunch& p, K* kernel, size_t smem, int sms, int64_t* ctas) {
+  int per_sm = 0;
+  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t resident = static_cast<int64_t>(sms) * std::max(per_sm, 1);
+  // A token's heads are shared out where there are fewer tokens than warps.
+  const int per_warp = 32 / p.lanes;
+  const int64_t groups = (p.heads[0] + per_warp - 1) / per_warp + (p.heads[1] + per_warp - 1) / per_warp;
+  p.parts = static_cast<int>(std::max<int64_t>(1, std::min(groups, resident * kWarps / p.n)));
+  *ctas = std::min(resident, (p.n * p.parts + kWarps - 1) / kWarps);
+  return cudaSuccess;
+}
+
+template <typename T, int V, int I, bool INTER>
+cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  int64_t ctas = 0;
+  if (!p.grad) {
+    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, 0, sms, &ctas);
+    if (e != cudaSuccess) return e;
+    return row::launch(rotary_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, stream, p);
+  }
+  const size_t smem = sizeof(float) * 2 * p.dim * kWarps;
+  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, smem, sms, &ctas);
+  if (e != cudaSuccess) return e;
+  p.npartials = static_cast<int>(ctas);
+  if (p.planning) return cudaSuccess;
+  e = row::launch(rotary_grad_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
+  if (e != cudaSuccess || !p.partials) return e;
+  return row::launch(rotary_gain_kernel, dim3(static_cast<unsigned>((2 * p.dim + 31) / 32)), kJoinThreads, 0, stream, p);
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_type(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  if (whole_pieces(p, V)) {
+    p.lanes = lanes_for(p, V);
+    return launch_as<T, V, 1, INTER>(p, sms, stream);  // dim <= 256: at most 32 items
+  }
+  p.lanes = lanes_for(p, 1);
+  return p.dim <= 64 ? launch_as<T, 1, 1, INTER>(p, sms, stream)
+       : p.dim <= 128 ? launch_as<T, 1, 2, INTER>(p, sms, stream)
+                      : launch_as<T, 1, 4, INTER>(p, sms, stream);
+}
+
+}  // namespace
+
+int64_t rotary_workspace(RotaryLaunch& p, char* ws) {
+  if (!p.dgain[0] && !p.dgain[1]) return 0;
+  if (ws) p.partials = reinterpret_cast<float*>(ws);
+  return static_cast<int64_t>(sizeof(float)) * p.npartials * 2 * p.dim;
+}
+
+cudaError_t launch_rotary(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  p.inv_dim = static_cast<float>(1.0 / p.dim);
+  if (p.dtype == 0)
+    return p.interleaved ? launch_type<float, true>(p, sms, stream) : launch_type<float, false>(p, sms, stream);
+  return p.interleaved ? launch_type<__nv_bfloat16, true>(p, sms, stream)
+                       : launch_type<__nv_bfloat16, false>(p, sms, stream);
+}
+
+}  // namespace dmuon

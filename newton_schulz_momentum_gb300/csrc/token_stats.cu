@@ -1,0 +1,479 @@
+// Log-probabilities of given tokens with the entropy and the most likely alternatives of their distributions, from
+// logits; and the gradient of the first two.
+//
+// Per row with logits x, token a, temperature T, z = x / T, m = max x: s = sum of exp((x - m) / T),
+//   lp_j = z_j - m / T - log s,   H = -sum of p lp = log s - sum of ((x - m) / T) exp((x - m) / T) / s,
+// and the `top` largest logits with their columns, the lowest column first among equals. Backward, for g = dL/dlp_a and
+// h = dL/dH:  dL/dx_j = 1 / T (g (1[j = a] - p_j) - h p_j (lp_j + H)).
+//
+// A row is read once for all of it. The threads of a CTA (of a cluster's CTAs where there are few rows) each keep the
+// largest logit, s and u = sum of y 2^y, y = (x - m) log2(e) / T, of their own granules, rescaled where the largest
+// logit grows, and join them at the end. The alternatives come from a bound: the threads form 64 groups (32 in a CTA
+// of one warp), at least `top` of which hold an element as large as the top-th largest of the groups' maxima, so only
+// elements that reach it can be alternatives: a few more than `top` of them as a rule, in as many threads, whose
+// granules alone are read again. Where equal logits make them more than the list holds, the row is walked once more in
+// order, the list cut down to its `top` best whenever it is full.
+#include <algorithm>
+
+#include "row_ops.h"
+#include "tc_ptx.h"
+
+namespace dmuon {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxTop = kMaxAlternatives;
+constexpr int kList = 1024;      // candidates in shared memory; at least kMaxTop and a thread's element each
+constexpr float kLowest = -1e30f;  // in place of -infinity in y: 2^y is 0 and so is y 2^y
+
+// 2^x, within 2 units of the last place; below 2^-126 it is 0.
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -INFINITY ? 0.f : m; }
+
+// Order of the alternatives: by logit, then the lower column. Zeros of both signs are equal.
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t column) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return static_cast<uint64_t>(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (0xffffffffu - column);
+}
+__device__ __forceinline__ float key_logit(uint64_t key) {
+  const uint32_t b = static_cast<uint32_t>(key >> 32);
+  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+}
+__device__ __forceinline__ uint32_t key_column(uint64_t key) { return 0xffffffffu - static_cast<uint32_t>(key); }
+
+// m: largest logit; s = sum of 2^y, u = sum of y 2^y with y = (x - m) k.
+struct Sums {
+  float m, s, u;
+};
+
+__device__ __forceinline__ void rescale(Sums& t, float m, float k) {
+  const float by = fmaxf((t.m - finite_or_zero(m)) * k, kLowest), f = pow2(by);
+  t.u = f * fmaf(by, t.s, t.u);
+  t.s *= f;
+  t.m = m;
+}
+
+__device__ __forceinline__ Sums join(Sums a, Sums b, float k) {
+  const float m = fmaxf(a.m, b.m);
+  rescale(a, m, k);
+  rescale(b, m, k);
+  return {m, a.s + b.s, a.u + b.u};
+}
+
+__device__ __forceinline__ Sums join_warp(Sums t, float k) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o),
+                 __shfl_xor_sync(0xffffffffu, t.u, o)}, k);
+  return t;
+}
+
+template <typename T>
+__device__ __forceinline__ float largest(const uint4& raw) {
+  if constexpr (sizeof(T) == 4) {
+    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)),
+                 fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+  } else {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 t = __hmax2(__hmax2(two(raw.x), two(raw.y)), __hmax2(two(raw.z), two(raw.w)));
+    return fmaxf(__low2float(t), __high2float(t));
+  }
+}
+
+// Where a row lies: `head` elements before the first 16-byte address, `full` granules, `tail` elements.
+template <typename T>
+struct RowCut {
+  static constexpr int E = 16 / sizeof(T);
+  int head, tail;
+  int64_t full;
+  __device__ __forceinline__ RowCut(const T* x, int64_t n) {
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+    head = static_cast<int>(n < ((E - off) & (E - 1)) ? n : (E - off) & (E - 1));
+    full = (n - head) / E;
+    tail = static_cast<int>(n - head - full * E);
+  }
+  // Column of the row's e-th element outside of granules.
+  __device__ __forceinline__ int64_t edge(int e) const { return e < head ? e : head + full * E + (e - head); }
+};
+
+template <int W>
+struct StatsShared {
+  Sums sums[W];
+  float group_max[64];
+  float bound;
+  int hot_count, list_count;
+  uint16_t hot[W * 32];
+  uint64_t list[kList];
+  uint64_t best[kMaxTop];  // the CTA's alternatives, best first; 0 where there are none
+  uint64_t of_cluster[8 * kMaxTop];
+  Sums total;
+};
+
+// The `top` best of the list's first `count` keys, which differ from one another, into best. All threads.
+template <int W>
+__device__ __forceinline__ void best_of(StatsShared<W>& sh, const uint64_t* list, int count, int top) {
+  for (int i = threadIdx.x; i < top; i += W * 32) sh.best[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < count; i += W * 32) {
+    const uint64_t key = list[i];
+    int rank = 0;
+    for (int j = 0; j < count; ++j) rank += list[j] > key;
+    if (rank < top) sh.best[rank] = key;
+  }
+  __syncthreads();
+}
+
+template <int W>
+__device__ __forceinline__ void push(StatsShared<W>& sh, float v, int64_t column) {
+  const int at = atomicAdd(&sh.list_count, 1);
+  if (at < kList) sh.list[at] = key_of(v, static_cast<uint32_t>(column));
+}
+
+// Alternatives of this CTA's elements into sh.best. `mine` is the thread's largest logit; its granules are those of
+// thread `thread` of `threads`, from granule `thread` on.
+template <typename T, int W>
+__device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, float mine, int top, int rank, int ctas) {
+  constexpr int E = 16 / sizeof(T), kCta = W * 32, kGroups = W == 1 ? 32 : 64, kPerGroup = kCta / kGroups;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t threads = static_cast<int64_t>(kCta) * ctas;
+  const int edges = cut.head + cut.tail;
+  const uint4* granules = reinterpret_cast<const uint4*>(x + cut.head);
+  float m = mine;
+#pragma unroll
+  for (int o = kPerGroup >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (threadIdx.x % kPerGroup == 0) sh.group_max[threadIdx.x / kPerGroup] = m;
+  if (threadIdx.x == 0) sh.hot_count = sh.list_count = 0;
+  __syncthreads();
+  if (threadIdx.x < kGroups) {
+    const float v = sh.group_max[threadIdx.x];
+    int larger = 0, before = 0;
+    for (int j = 0; j < kGroups; ++j) {
+      const float o = sh.group_max[j];
+      larger += o > v;
+      before += o == v && j < static_cast<int>(threadIdx.x);
+    }
+    if (larger + before == top - 1) sh.bound = v;
+  }
+  __syncthreads();
+  const float bound = sh.bound;
+  if (mine >= bound) sh.hot[atomicAdd(&sh.hot_count, 1)] = static_cast<uint16_t>(threadIdx.x);
+  __syncthreads();
+  const int hot = sh.hot_count;
+  // A warp reads a hot thread's granules again, a lane each.
+  for (int q = warp; q < hot; q += W) {
+    const int64_t thread = static_cast<int64_t>(rank) * kCta + sh.hot[q];
+    if (lane == 0 && thread < edges) {
+      const float v = row::to_f(x[cut.edge(static_cast<int>(thread))]);
+      if (v >= bound) push(sh, v, cut.edge(static_cast<int>(thread)));
+    }
+    for (int64_t i = thread + lane * threads; i < cut.full; i += 32 * threads) {
+      float v[E];
+      const uint4 raw = granules[i];
+      if (!(largest<T>(raw) >= bound)) continue;
+      row::unpack16<T>(v, raw);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (v[e] >= bound) push(sh, v[e], cut.head + i * E + e);
+    }
+  }
+  __syncthreads();
+  if (sh.list_count <= kList) {
+    best_of(sh, sh.list, sh.list_count, top);
+    return;
+  }
+  // Many equal logits: every element of this CTA in the order of its columns, one per thread and step. Keys above
+  // the last cut's top-th join the list; a step adds at most one per thread.
+  __syncthreads();
+  if (threadIdx.x == 0) sh.list_count = 0;
+  uint64_t least = 0;
+  const int64_t columns = cut.head + cut.full * E + cut.tail;
+  __syncthreads();
+  for (int64_t c0 = static_cast<int64_t>(rank) * kCta; c0 < columns; c0 += threads) {
+    const int64_t c = c0 + threadIdx.x;
+    if (c < columns) {
+      const float v = row::to_f(x[c]);
+      const uint64_t key = key_of(v, static_cast<uint32_t>(c));
+      if (v == v && key > least) push(sh, v, c);
+    }
+    __syncthreads();
+    const int count = sh.list_count;
+    if (count > kList - kCta || c0 + threads >= columns) {
+      best_of(sh, sh.list, count, top);
+      least = sh.best[top - 1];
+      if (static_cast<int>(threadIdx.x) < top && sh.best[threadIdx.x]) sh.list[threadIdx.x] = sh.best[threadIdx.x];
+      if (threadIdx.x == 0) {
+        int kept = 0;
+        while (kept < top && sh.best[kept]) ++kept;
+        sh.list_count = kept;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t load_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// One row per cluster of p.cluster CTAs of W warps.
+template <typename T, int W>
+__global__ void __launch_bounds__(W * 32) token_stats_kernel(const __grid_constant__ StatsLaunch p) {
+  constexpr int E = 16 / sizeof(T), kCta = W * 32, kBatch = 4;
+  __shared__ StatsShared<W> sh;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int ctas = p.cluster, rank = ctas > 1 ? static_cast<int>(ptx::cluster_ctarank()) : 0;
+  const int64_t i = blockIdx.x / ctas;
+  int64_t a = -1;
+  bool live = true;
+  if (p.targets) {
+    a = row::load_id(p.targets, p.id_bytes, i);
+    live = a >= 0 && a < p.vocab;
+    if (a >= p.vocab && threadIdx.x == 0 && rank == 0) atomicOr(p.status, kDevIndex);
+  }
+  if (!live) {  // the same for all of the cluster
+    if (rank != 0) return;
+    for (int t = threadIdx.x; t < p.top; t += kCta) p.top_logp[i * p.top + t] = 0.f, p.top_ids[i * p.top + t] = -1;
+    if (threadIdx.x == 0) {
+      p.logp[i] = 0.f;  // there are targets
+      p.entropy[i] = 0.f;
+      p.norm[2 * i] = p.norm[2 * i + 1] = 0.f;
+    }
+    return;
+  }
+  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
+  const RowCut<T> cut(x, p.vocab);
+  const float k = p.log2e_over_t;
+  const int64_t threads = static_cast<int64_t>(kCta) * ctas, thread = static_cast<int64_t>(rank) * kCta + threadIdx.x;
+  const uint4* granules = reinterpret_cast<const uint4*>(x + cut.head);
+  Sums t{-INFINITY, 0.f, 0.f};
+  auto grow = [&](float m) {
+    if (m > t.m) rescale(t, m, k);
+  };
+  auto add = [&](float v, float base) {
+    const float y = (v - base) * k, e = pow2(y);
+    t.s += e;
+    t.u = fmaf(fmaxf(y, kLowest), e, t.u);
+  };
+  if (thread < cut.head + cut.tail) {
+    const float v = row::to_f(x[cut.edge(static_cast<int>(thread))]);
+    grow(v);
+    add(v, finite_or_zero(t.m));
+  }
+  for (int64_t g = thread; g < cut.full; g += kBatch * threads) {
+    uint4 raw[kBatch];
+    // Behind the row's end the batch repeats its first granule; only its maximum is taken from there.
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) raw[b] = granules[g + b * threads < cut.full ? g + b * threads : g];
+    float m = largest<T>(raw[0]);
+#pragma unroll
+    for (int b = 1; b < kBatch; ++b) m = fmaxf(m, largest<T>(raw[b]));
+    grow(m);
+    const float base = finite_or_zero(t.m);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (g + b * threads >= cut.full) break;
+      float v[E];
+      row::unpack16<T>(v, raw[b]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) add(v[e], base);
+    }
+  }
+  const float mine = t.m;
+  t = join_warp(t, k);
+  if ((threadIdx.x & 31) == 0) sh.sums[threadIdx.x >> 5] = t;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    t = sh.sums[0];
+    for (int w = 1; w < W; ++w) t = join(t, sh.sums[w], k);
+    sh.total = t;
+  }
+  if (p.top > 0) find_top<T, W>(sh, x, cut, mine, p.top, rank, ctas);
+  else __syncthreads();
+  const uint64_t* best = sh.best;
+  if (ctas > 1) {
+    ptx::cluster_sync_all();
+    if (rank == 0) {
+      // The CTAs' sums in their order; their alternatives side by side.
+      for (int e = threadIdx.x; e < ctas * p.top; e += kCta) {
+        const uint32_t from = ptx::map_shared(ptx::smem_u32(&sh.best[e % p.top]), e / p.top);
+        sh.of_cluster[e] = static_cast<uint64_t>(load_cluster(from + 4)) << 32 | load_cluster(from);
+      }
+      if (threadIdx.x == 0) {
+        Sums all = sh.total;
+        for (int c = 1; c < ctas; ++c) {
+          const uint32_t from = ptx::map_shared(ptx::smem_u32(&sh.total), c);
+          all = join(all, {__uint_as_float(load_cluster(from)), __uint_as_float(load_cluster(from + 4)),
+                           __uint_as_float(load_cluster(from + 8))}, k);
+        }
+        sh.total = all;
+      }
+      __syncthreads();
+    }
+    ptx::cluster_sync_all();  // the other CTAs' shared memory has been read
+    if (rank != 0) return;
+    if (p.top > 0) best_of(sh, sh.of_cluster, ctas * p.top, p.top);
+  }
+  t = sh.total;
+  // Logarithm of s; a row of nothing but -infinity has no distribution: NaN.
+  const float base = finite_or_zero(t.m), log_s = t.m == -INFINITY ? NAN : logf(t.s);
+  auto logp_of = [&](float v) {
+    const float d = v - base;  // -infinity stays what it is: the inverse's second part may be 0 or negative
+    return d == -INFINITY ? d - log_s : fmaf(d, p.inv_temperature, fmaf(d, p.inv_temperature_low, -log_s));
+  };
+  if (threadIdx.x == 0) {
+    if (p.targets) p.logp[i] = logp_of(row::to_f(x[a]));
+    p.entropy[i] = fmaf(-kLn2 / t.s, t.u, log_s);
+    p.norm[2 * i] = t.m;
+    p.norm[2 * i + 1] = t.s;
+  }
+  for (int q = threadIdx.x; q < p.top; q += kCta) {
+    const uint64_t key = best[q];
+    p.top_logp[i * p.top + q] = key ? logp_of(key_logit(key)) : NAN;
+    p.top_ids[i * p.top + q] = key ? static_cast<int64_t>(key_column(key)) : -1;
+  }
+}
+
+// ---------------------------------------------------------------------------- gradient
+
+constexpr int kGradThreads = 256, kGradBatch = 4;
+
+// Each CTA takes kGradThreads * kGradBatch granules of a row (or a part of it element by element, where logits and
+// gradient start at different offsets from 16 bytes).
+template <typename T>
+__global__ void __launch_bounds__(kGradThreads) token_stats_grad_kernel(const __grid_constant__ StatsGradLaunch p) {
+  constexpr int E = 16 / sizeof(T);
+  constexpr int64_t kPart = static_cast<int64_t>(kGradThreads) * kGradBatch;
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int64_t i = blockIdx.x / p.parts, part = blockIdx.x - i * p.parts;
+  const T* x = static_cast<const T*>(p.logits) + i * p.ld;
+  T* dx = static_cast<T*>(p.dlogits) + i * p.ldd;
+  int64_t a = -1;
+  bool live = true;
+  if (p.targets) {
+    a = row::load_id(p.targets, p.id_bytes, i);
+    live = a >= 0 && a < p.vocab;
+    if (a >= p.vocab && threadIdx.x == 0 && part == 0) atomicOr(p.status, kDevIndex);
+  }
+  // With t = log2 p: dx = p (c0 + c1 t), plus the token's own term.
+  float m = 0.f, log2_s = 0.f, inv_s = 0.f, c0 = 0.f, c1 = 0.f, own = 0.f;
+  if (live) {
+    m = p.norm[2 * i];
+    const float s = p.norm[2 * i + 1], g = p.dlogp ? p.dlogp[i] : 0.f, h = p.dentropy ? p.dentropy[i] : 0.f;
+    log2_s = log2f(s);
+    inv_s = m == -INFINITY ? NAN : 1.f / s;
+    own = g * p.inv_temperature;
+    c0 = -(h != 0.f ? fmaf(h, p.entropy[i], g) : g) * p.inv_temperature;
+    c1 = -h * kLn2 * p.inv_temperature;
+  }
+  const float base = finite_or_zero(m), k = p.log2e_over_t;
+  auto value = [&](float v) {
+    const float y = (v - base) * k, e = pow2(y) * inv_s;
+    return e * fmaf(c1, fmaxf(y, kLowest) - log2_s, c0);
+  };
+  if ((reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(dx)) % 16 != 0) {
+    const int64_t end = min(p.vocab, (part + 1) * kPart * E);
+    for (int64_t c = part * kPart * E + threadIdx.x; c < end; c += kGradThreads) {
+      float v = 0.f;
+      if (live) v = value(row::to_f(x[c])) + (c == a ? own : 0.f);
+      dx[c] = row::from_f<T>(v);
+    }
+    return;
+  }
+  const RowCut<T> cut(x, p.vocab);
+  if (part == 0 && static_cast<int>(threadIdx.x) < cut.head + cut.tail) {
+    const int64_t c = cut.edge(threadIdx.x);
+    float v = 0.f;
+    if (live) v = value(row::to_f(x[c])) + (c == a ? own : 0.f);
+    dx[c] = row::from_f<T>(v);
+  }
+  const uint4* in = reinterpret_cast<const uint4*>(x + cut.head);
+  uint4* out = reinterpret_cast<uint4*>(dx + cut.head);
+  const int64_t g0 = part * kPart + threadIdx.x, ga = a >= cut.head ? (a - cut.head) / E : -1;
+  uint4 raw[kGradBatch];
+#pragma unroll
+  for (int b = 0; b < kGradBatch; ++b) {
+    const int64_t g = g0 + b * kGradThreads;
+    if (live && g < cut.full) raw[b] = __ldcs(in + g);
+  }
+#pragma unroll
+  for (int b = 0; b < kGradBatch; ++b) {
+    const int64_t g = g0 + b * kGradThreads;
+    if (g >= cut.full) break;
+    float v[E];
+    if (live) {
+      row::unpack16<T>(v, raw[b]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = value(v[e]);
+      if (g == ga) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (cut.head + g * E + e == a) v[e] += own;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+    }
+    __stcs(out + g, row::pack16(v));
+  }
+}
+
+template <typename T, int W>
+cudaError_t launch_stats(StatsLaunch& p, cudaStream_t stream) {
+  return row::launch(token_stats_kernel<T, W>, dim3(static_cast<unsigned>(p.n * p.cluster)), W * 32, 0, stream, p, p.cluster);
+}
+
+template <typename T>
+cudaError_t launch_type(StatsLaunch& p, int sms, cudaStream_t stream) {
+  constexpr int E = 16 / sizeof(T);
+  const int64_t granules = (p.vocab + E - 1) / E;
+  p.cluster = 1;
+  if (granules <= 256) return launch_stats<T, 1>(p, stream);
+  if (granules <= 2048) return launch_stats<T, 4>(p, stream);
+  // Few rows: several CTAs each, as long as a thread has a batch of granules.
+  while (p.cluster < 8 && p.n * p.cluster * 2 <= 2 * sms && granules >= 2 * p.cluster * 256 * 4) p.cluster *= 2;
+  return launch_stats<T, 8>(p, stream);
+}
+
+template <typename T>
+cudaError_t launch_grad(StatsGradLaunch& p, cudaStream_t stream) {
+  constexpr int64_t per = static_cast<int64_t>(kGradThreads) * kGradBatch * (16 / sizeof(T));
+  p.parts = (p.vocab + per - 1) / per;
+  // One dimension of the grid holds 2^31 - 1 CTAs: more rows than that allows go in several launches.
+  const int64_t rows = std::max<int64_t>(1, ((int64_t(1) << 31) - 1) / p.parts);
+  StatsGradLaunch q = p;
+  for (int64_t r = 0; r < p.n; r += rows) {
+    q.logits = static_cast<const T*>(p.logits) + r * p.ld;
+    q.dlogits = static_cast<T*>(p.dlogits) + r * p.ldd;
+    q.targets = p.targets ? static_cast<const char*>(p.targets) + r * p.id_bytes : nullptr;
+    q.norm = p.norm + 2 * r;
+    q.entropy = p.entropy ? p.entropy + r : nullptr;
+    q.dlogp = p.dlogp ? p.dlogp + r : nullptr;
+    q.dentropy = p.dentropy ? p.dentropy + r : nullptr;
+    const int64_t ctas = std::min(rows, p.n - r) * p.parts;
+    const cudaError_t e =
+        row::launch(token_stats_grad_kernel<T>, dim3(static_cast<unsigned>(ctas)), kGradThreads, 0, stream, q);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_token_stats(StatsLaunch& p, int sms, cudaStream_t stream) {
+  return p.dtype == 0 ? launch_type<float>(p, sms, stream) : launch_type<__nv_bfloat16>(p, sms, stream);
+}
+
+cudaError_t launch_token_stats_grad(StatsGradLaunch& p, cudaStream_t stream) {
+  return p.dtype == 0 ? launch_grad<float>(p, stream) : launch_grad<__nv_bfloat16>(p, stream);
+}
+
+}  // namespace dmuon

@@ -1,5 +1,5 @@
 """The token operators of libdmuon: what a language model's training step runs beside its matrix products, on
-the parameters that AdamW updates. Argument marshalling only: each function is one C call, enqueued on the current
+the parameters that AdamW updates, and between them. Argument marshalling only: each function is one C call, enqueued on the current
 CUDA stream of its tensors' device, which is the same for all of them; all are reachable as attributes of the package.
 
     y = dm.embedding(table, ids, scale=64.0)                       # lookup
@@ -9,12 +9,22 @@ CUDA stream of its tensors' device, which is the same for all of them; all are r
     dx, dgain = dm.add_rmsnorm_grad(dy, h, gain, dh=dh)
     loss, logp, dlogits = dm.policy_loss(logits, targets, old_logp, advantages, weights)
     logp = dm.token_logprobs(logits, targets)
+    q, k = dm.qk_norm_rotary(q, k, positions, q_gain, k_gain)      # norm of each head, and the position rotation
+    out, lse = dm.attention(q, k, v, offsets)                      # causal, over packed sequences
+    dq, dk, dv = dm.attention_grad(dout, q, k, v, out, lse, offsets)
+    dq, dk, dq_gain, dk_gain = dm.qk_norm_rotary_grad(dq, dk, q0, k0, positions, q_gain, k_gain)
+    stats = dm.token_stats(logits, targets, top=5)                 # logp, entropy, top_logp, top_ids, norm
+    dlogits = dm.token_stats_grad(logits, targets, stats.norm, stats.entropy, dlogp, dentropy)
 
 Activations are fp32 or bf16 CUDA tensors whose last dimension is the row; a 2-D tensor may have any row
-stride, others must be contiguous. Ids are int32 or int64. layers.py holds the autograd forms.
+stride, others must be contiguous. Heads are (..., heads, dim) with any stride from head to head and from token to
+token. Ids and positions are int32 or int64. layers.py holds the autograd forms.
 """
 
 from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -277,3 +287,254 @@ def token_logprobs(logits, targets, temperature=1.0, stream=None):
     if status:
         _check(status)
     return logp
+
+
+def _heads(t, name):
+    """(tokens, heads, head length, token stride, head stride) of a tensor (..., heads, dim)."""
+    size = t.shape
+    if len(size) < 3:
+        raise ValueError(f"{name} must have the dimensions (..., heads, dim)")
+    heads, dim = size[-2:]
+    if t.is_contiguous():
+        return (size[0] if len(size) == 3 else size[:-2].numel()), heads, dim, heads * dim, dim
+    strides = t.stride()
+    if dim > 1 and strides[-1] != 1:
+        raise ValueError(f"{name} must have contiguous heads")
+    token, n = heads * dim, 1
+    for count, stride in zip(reversed(size[:-2]), reversed(strides[:-2])):
+        if count != 1:
+            if n == 1:
+                token = stride
+            elif stride != token * n:
+                raise ValueError(f"{name} must have one stride from token to token")
+            n *= count
+    return n, heads, dim, token, strides[-2] if heads > 1 else dim
+
+
+def _head_array(t, name, dev, shape, dtype):
+    """(address, token stride, head stride) of heads of the given shape and dtype on device `dev`."""
+    if t.get_device() != dev:
+        _same_device(t, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return (t.data_ptr(),) + _heads(t, name)[3:]
+
+
+def _new(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections, interleaved, eps):
+    """(heads of k, the C calls' arguments from dtype to sections)."""
+    n, heads, dim, _, _ = _heads(q, "q")
+    if k is not None and (k.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != dim):
+        raise ValueError("k must have q's tokens and head length")
+    rotary_dim = dim if rotary_dim is None else rotary_dim
+    axes, axis_list = 1, None
+    tokens = q.shape[:-2]
+    if sections is not None:
+        axes = len(sections)
+        axis_list = (ctypes.c_int64 * axes)(*sections)
+        tokens = (axes,) + tuple(tokens)
+    pos, id_bytes = _ids(positions, "positions", dev)
+    if positions.shape != tokens:
+        raise ValueError(f"positions must have shape {tuple(tokens)}, not {tuple(positions.shape)}")
+    if freqs is not None:
+        freqs = [float(f) for f in freqs]
+        if len(freqs) != rotary_dim // 2:
+            raise ValueError(f"freqs must have rotary_dim / 2 = {rotary_dim // 2} elements, not {len(freqs)}")
+        freqs = (ctypes.c_double * max(len(freqs), 1))(*freqs)
+    return 0 if k is None else k.shape[-2], heads, (
+        _code(q, "q"), _vector(q_gain, "q_gain", dev, dim), _vector(k_gain, "k_gain", dev, dim), 1 if norm else 0, eps, n,
+        dim, rotary_dim, 1 if interleaved else 0, base, freqs, pos, id_bytes, axes, n, axis_list)
+
+
+_NO_HEADS = (None, 0, 0)
+
+
+def qk_norm_rotary(q, k, positions, q_gain=None, k_gain=None, norm=True, rotary_dim=None, base=10000.0, freqs=None,
+                   sections=None, interleaved=False, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): the RMS norm of each head of q (..., heads, dim) and k (..., kv_heads, dim; or None) over its
+    columns, times a gain that all heads share, and the position rotation of the first rotary_dim columns (all by
+    default), in pairs (j, j + rotary_dim / 2) or, interleaved, (2j, 2j + 1). norm=False rotates alone.
+
+    positions are integers, shaped like q without its last two dimensions; with sections = (s0, s1, ...), which add up to
+    rotary_dim / 2, one more dimension in front: s0 frequencies follow positions[0], the next s1 positions[1], ... The
+    angles per position are base^(-2j / rotary_dim), or `freqs` (rotary_dim / 2 numbers). q_out may be q, and k_out k."""
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(qk_norm_rotary, _device(q, "q"), q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs,
+                          sections, interleaved, eps, q_out, k_out, stream)
+    kv_heads, heads, turns = _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections,
+                                          interleaved, eps)
+    q_out = _new(q) if q_out is None else q_out
+    k_at = k_out_at = _NO_HEADS
+    if k is None:
+        k_out = None
+    else:
+        k_out = _new(k) if k_out is None else k_out
+        k_at, k_out_at = _head_array(k, "k", dev, k.shape, q.dtype), _head_array(k_out, "k_out", dev, k.shape, q.dtype)
+    status = lib().dmuon_qk_norm_rotary(*_head_array(q, "q", dev, q.shape, q.dtype), heads, *k_at, kv_heads, *turns,
+                                        *_head_array(q_out, "q_out", dev, q.shape, q.dtype), *k_out_at,
+                                        _stream(stream, dev))
+    if status:
+        _check(status)
+    return q_out, k_out
+
+
+def qk_norm_rotary_grad(dq_out, dk_out, q, k, positions, q_gain=None, k_gain=None, norm=True, rotary_dim=None,
+                        base=10000.0, freqs=None, sections=None, interleaved=False, eps=1e-6, dq=None, dk=None,
+                        stream=None):
+    """(dq, dk, dq_gain, dk_gain) of qk_norm_rotary at its q and k: the gains' gradients are fp32, None without a gain. dq
+    may be dq_out or q, and dk dk_out or k."""
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(qk_norm_rotary_grad, _device(q, "q"), dq_out, dk_out, q, k, positions, q_gain, k_gain, norm,
+                          rotary_dim, base, freqs, sections, interleaved, eps, dq, dk, stream)
+    kv_heads, heads, turns = _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections,
+                                          interleaved, eps)
+    dq = _new(q) if dq is None else dq
+    k_at = dk_out_at = dk_at = _NO_HEADS
+    if k is None:
+        dk = None
+    else:
+        dk = _new(k) if dk is None else dk
+        k_at, dk_out_at, dk_at = (_head_array(t, name, dev, k.shape, q.dtype) for t, name in
+                                  ((k, "k"), (dk_out, "dk_out"), (dk, "dk")))
+    dq_gain = None if q_gain is None else torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
+    dk_gain = None if k_gain is None or k is None else torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
+    status = lib().dmuon_qk_norm_rotary_grad(
+        *_head_array(dq_out, "dq_out", dev, q.shape, q.dtype), *_head_array(q, "q", dev, q.shape, q.dtype), heads,
+        *dk_out_at, *k_at, kv_heads, *turns, *_head_array(dq, "dq", dev, q.shape, q.dtype), *dk_at,
+        None if dq_gain is None else dq_gain.data_ptr(), None if dk_gain is None else dk_gain.data_ptr(),
+        _stream(stream, dev))
+    if status:
+        _check(status)
+    return dq, dk, dq_gain, dk_gain
+
+
+def _prompts(dev, q, k, offsets, causal, scale, zero_outside):
+    """(number of tokens, heads, the C calls' arguments from dtype to zero_outside) of an attention call."""
+    n, heads, dim, _, _ = _heads(q, "q")
+    if k.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != dim:
+        raise ValueError("k must have q's tokens and head length")
+    if q.dtype is not torch.bfloat16:
+        raise ValueError(f"q must be {torch.bfloat16}, not {q.dtype}")
+    if offsets is None:
+        at, id_bytes, sequences = None, 4, q.shape[:-3].numel() or 1
+    else:
+        at, id_bytes = _ids(offsets, "offsets", dev)
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets must be a list of one more elements than sequences")
+        sequences = offsets.numel() - 1
+    return n, heads, (BF16, n, heads, k.shape[-2], dim, at, id_bytes, sequences, 1 if causal else 0,
+                      dim ** -0.5 if scale is None else scale, 1 if zero_outside else 0)
+
+
+def attention(q, k, v, offsets=None, causal=True, scale=None, out=None, lse=None, stream=None):
+    """(out, lse): softmax attention over whole prompts. q (..., heads, dim), k and v (..., kv_heads, dim), bf16; query
+    head h reads key head h // (heads // kv_heads). `scale` is dim^-1/2 by default. out is like q; lse, (heads, tokens)
+    fp32, holds each row's log of the sum of exponentials, which attention_grad reads.
+
+    Without `offsets` the dimension in front of the heads is a sequence: (tokens, heads, dim) is one, (batch, length,
+    heads, dim) is a batch of them. `offsets`, sequences + 1 integers, packs sequences of different lengths (0 among
+    them): sequence s is tokens offsets[s] to offsets[s + 1]. Tokens of no sequence get zeros, or, where `out` is
+    given, stay as they were. dim is a multiple of 8, at most 128; addresses and strides are multiples of 16 bytes."""
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(attention, _device(q, "q"), q, k, v, offsets, causal, scale, out, lse, stream)
+    n, heads, prompts = _prompts(dev, q, k, offsets, causal, scale, out is None and lse is None)
+    given = out is not None
+    if not given:
+        out = _new(q) if lse is None else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = (torch.zeros if given else torch.empty)((heads, n), dtype=torch.float32, device=q.device)
+    status = lib().dmuon_attention(*_head_array(q, "q", dev, q.shape, q.dtype), *_head_array(k, "k", dev, k.shape, q.dtype),
+                                   *_head_array(v, "v", dev, k.shape, q.dtype), *prompts,
+                                   *_head_array(out, "out", dev, q.shape, q.dtype),
+                                   _vector(lse, "lse", dev, heads * n), _stream(stream, dev))
+    if status:
+        _check(status)
+    return out, lse
+
+
+def attention_grad(dout, q, k, v, out, lse, offsets=None, causal=True, scale=None, dq=None, dk=None, dv=None,
+                   stream=None):
+    """(dq, dk, dv) of attention at its out and lse, like q, k and v. Tokens of no sequence get zeros, or, where any of
+    the three is given, stay as they were in it."""
+    dev = q.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(attention_grad, _device(q, "q"), dout, q, k, v, out, lse, offsets, causal, scale, dq, dk, dv,
+                          stream)
+    all_new = dq is None and dk is None and dv is None
+    n, heads, prompts = _prompts(dev, q, k, offsets, causal, scale, all_new)
+    new = _new if all_new else torch.zeros_like
+    dq, dk, dv = (new(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, k)))
+    arrays = [_head_array(t, name, dev, like.shape, q.dtype) for t, name, like in (
+        (dout, "dout", q), (q, "q", q), (k, "k", k), (v, "v", k), (out, "out", q), (dq, "dq", q), (dk, "dk", k),
+        (dv, "dv", k))]
+    status = lib().dmuon_attention_grad(*arrays[0], *arrays[1], *arrays[2], *arrays[3], *arrays[4],
+                                        _vector(lse, "lse", dev, heads * n), *prompts, *arrays[5], *arrays[6],
+                                        *arrays[7], _stream(stream, dev))
+    if status:
+        _check(status)
+    return dq, dk, dv
+
+
+class TokenStats(NamedTuple):
+    """Of each row of logits: its target's log-probability (None without targets), the entropy of its distribution, the
+    log-probabilities and ids of its most likely tokens, and (largest logit, sum of exp((x - largest) / temperature))."""
+    logp: Optional[torch.Tensor]
+    entropy: torch.Tensor
+    top_logp: torch.Tensor
+    top_ids: torch.Tensor
+    norm: torch.Tensor
+
+
+def token_stats(logits, targets=None, top=0, temperature=1.0, stream=None):
+    """TokenStats(logp, entropy, top_logp, top_ids, norm) of softmax(logits / temperature), fp32 and, the ids, int64,
+    in one pass over the logits. The first three are shaped like targets (logits without their last dimension), the
+    next two with `top` (at most 32) alternatives behind, best first, the lower id among equals. A row whose target is
+    negative is not read: zeros, and ids of -1."""
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(token_stats, _device(logits, "logits"), logits, targets, top, temperature, stream)
+    n, vocab, ld = _layout(logits, "logits")
+    ptr, size = (None, 8) if targets is None else _ids(targets, "targets", dev, n)
+    shape, at = logits.shape[:-1] if targets is None else targets.shape, logits.device
+    logp = None if targets is None else torch.empty(shape, dtype=torch.float32, device=at)
+    entropy = torch.empty(shape, dtype=torch.float32, device=at)
+    top_logp = torch.empty(shape + (max(top, 0),), dtype=torch.float32, device=at)
+    top_ids = torch.empty(shape + (max(top, 0),), dtype=torch.int64, device=at)
+    norm = torch.empty(shape + (2,), dtype=torch.float32, device=at)
+    status = lib().dmuon_token_stats(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size, top, temperature,
+                                     None if logp is None else logp.data_ptr(), entropy.data_ptr(), top_logp.data_ptr(),
+                                     top_ids.data_ptr(), norm.data_ptr(), _stream(stream, dev))
+    if status:
+        _check(status)
+    return TokenStats(logp, entropy, top_logp, top_ids, norm)
+
+
+def token_stats_grad(logits, targets, norm, entropy, dlogp=None, dentropy=None, temperature=1.0, dlogits=None,
+                     stream=None):
+    """The gradient of token_stats' logp and entropy in the logits, of their dtype, at its norm and entropy. Without dlogp
+    targets may be None; without dentropy entropy may be. dlogits may be a tensor to write into, the logits among them."""
+    dev = logits.get_device()
+    if dev < 0 or dev != _current_device():
+        return _elsewhere(token_stats_grad, _device(logits, "logits"), logits, targets, norm, entropy, dlogp, dentropy,
+                          temperature, dlogits, stream)
+    n, vocab, ld = _layout(logits, "logits")
+    ptr, size = (None, 8) if targets is None else _ids(targets, "targets", dev, n)
+    if dlogits is None:
+        dlogits, ldd = _new(logits), vocab
+    else:
+        ldd = _rows(dlogits, "dlogits", dev, logits.shape, logits.dtype)
+    status = lib().dmuon_token_stats_grad(logits.data_ptr(), _code(logits, "logits"), ld, n, vocab, ptr, size,
+                                          _vector(norm, "norm", dev, 2 * n), _vector(entropy, "entropy", dev, n),
+                                          _vector(dlogp, "dlogp", dev, n), _vector(dentropy, "dentropy", dev, n),
+                                          temperature, dlogits.data_ptr(), ldd, _stream(stream, dev))
+    if status:
+        _check(status)
+    return dlogits
