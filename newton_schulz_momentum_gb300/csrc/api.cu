@@ -1531,7 +1531,7 @@ int set_attention(AttentionLaunch& p, int dtype, int64_t n, int64_t heads, int64
     return fail(DMUON_ERR_INVALID_ARG, "heads must be a multiple of kv_heads, and at most 65535");
   if (dim < 8 || dim % 8) return fail(DMUON_ERR_INVALID_ARG, "dim must be a multiple of 8, got %lld", (long long)dim);
   if (dim > 128) return fail(DMUON_ERR_UNSUPPORTED, "dim must be at most 128, got %lld", (long long)dim);
-  if (n * heads > (int64_t(1) << 40)) return fail(DMUON_ERR_UNSUPPORTED, "more than 2^40 rows");
+  if (n > int64_t(1) << 30) return fail(DMUON_ERR_UNSUPPORTED, "n must be at most 2^30, got %lld", (long long)n);
   if (sequences < (offsets ? 0 : 1) || sequences > kMaxTokens)
     return fail(DMUON_ERR_INVALID_ARG, "sequences must be in [1, 2^31 - 1] (0 with offsets), got %lld", (long long)sequences);
   if (offsets) {
@@ -1540,7 +1540,7 @@ int set_attention(AttentionLaunch& p, int dtype, int64_t n, int64_t heads, int64
   } else if (n % sequences) {
     return fail(DMUON_ERR_INVALID_ARG, "without offsets the sequences are of equal length: n must be a multiple of them");
   }
-  if (!std::isfinite(scale)) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite(scale) || scale == 0.f) return fail(DMUON_ERR_INVALID_ARG, "scale must be finite and not 0");
   p.n = n, p.heads = static_cast<int>(heads), p.kv_heads = static_cast<int>(kv_heads), p.dim = static_cast<int>(dim);
   p.offsets = offsets, p.id_bytes = id_bytes, p.sequences = sequences;
   p.causal = causal != 0, p.scale = scale, p.zero_outside = zero_outside != 0;
@@ -1554,6 +1554,8 @@ int set_heads(HeadArray& a, const char* name, const void* ptr, int64_t token, in
   if (st != DMUON_OK) return st;
   if (!aligned_to(ptr, 16) || token % 8 || head % 8)
     return fail(DMUON_ERR_INVALID_ARG, "%s must be 16-byte aligned with strides of multiples of 8 elements", name);
+  if ((p.n > 1 && token == 0) || (heads > 1 && head == 0))
+    return fail(DMUON_ERR_INVALID_ARG, "the strides of %s must not be 0", name);
   if (token >= int64_t(1) << 38 || head >= int64_t(1) << 38)
     return fail(DMUON_ERR_UNSUPPORTED, "the strides of %s are beyond 2^38 elements", name);
   a.data = ptr, a.token = token, a.head = head;

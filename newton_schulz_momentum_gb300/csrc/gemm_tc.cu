@@ -694,6 +694,29 @@ bool encode_tensor_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64
   return encode_2d(map, base, inner, outer, row_bytes, box_inner, box_outer, err, dtype, swizzle);
 }
 
+bool encode_heads(CUtensorMap* map, const HeadArray& a, int dim, int heads, int64_t n, uint32_t box_rows, const char** err) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) {
+    *err = "cuTensorMapEncodeTiled is not available from the CUDA driver";
+    return false;
+  }
+  // The stride of a dimension of one element is never used, but has to be a valid one.
+  const cuuint64_t row = static_cast<cuuint64_t>(dim) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n)};
+  const cuuint64_t strides[2] = {heads > 1 ? static_cast<cuuint64_t>(a.head) * 2 : row,
+                                 n > 1 ? static_cast<cuuint64_t>(a.token) * 2 : row * static_cast<cuuint64_t>(heads)};
+  const cuuint32_t box[3] = {64, 1, box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.data), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    *err = "cuTensorMapEncodeTiled rejected an array of heads (alignment, stride or size)";
+    return false;
+  }
+  return true;
+}
+
 bool encode_out_maps(GemmJob& job, const char** err) {
   if (job.D && !encode_2d(&job.tmD, job.D, static_cast<uint64_t>(job.N), static_cast<uint64_t>(job.M),
                           static_cast<uint64_t>(job.ldd) * 2, 32, 32, err, CU_TENSOR_MAP_DATA_TYPE_FLOAT16,

@@ -164,7 +164,7 @@ def _reachable(t):
         strides = token_ops._heads(t, "heads")[3:]
     except ValueError:
         return t.contiguous()
-    if t.data_ptr() % 16 or any(s % 8 for s in strides):
+    if t.data_ptr() % 16 or any(s % 8 or s == 0 for s in strides):
         return t.clone(memory_format=torch.contiguous_format)
     return t
 
