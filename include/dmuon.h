@@ -470,8 +470,9 @@ DMUON_API int dmuon_attention(const void* q, int64_t q_token, int64_t q_head, co
  * dmuon_attention_grad -- the backward pass at the stored out and lse. With p the softmax, D_i = dout_i . out_i,
  * ds_ij = p_ij (dout_i . v_j - D_i):
  *   dq_i = scale sum over j of ds_ij k_j,  dk_j = scale sum over i of ds_ij q_i,  dv_j = sum over i of p_ij dout_i,
- * the last two over all query heads of their key head, added in a fixed order. Arrays as above; dq, dk and dv must
- * overlap neither one another nor an input.
+ * the last two over all query heads of their key head, added in a fixed order. The sum of a row's ds is 0 but for what
+ * out lost in its rounding to bf16; it is added to D where that counts (rows of few keys, dk). p and ds are rounded to
+ * bf16 for their products. Arrays as above; dq, dk and dv must overlap neither one another nor an input.
  */
 DMUON_API int dmuon_attention_grad(const void* dout, int64_t dout_token, int64_t dout_head, const void* q,
                                    int64_t q_token, int64_t q_head, const void* k, int64_t k_token, int64_t k_head,

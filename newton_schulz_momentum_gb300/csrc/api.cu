@@ -1532,6 +1532,8 @@ int set_attention(AttentionLaunch& p, int dtype, int64_t n, int64_t heads, int64
   if (dim < 8 || dim % 8) return fail(DMUON_ERR_INVALID_ARG, "dim must be a multiple of 8, got %lld", (long long)dim);
   if (dim > 128) return fail(DMUON_ERR_UNSUPPORTED, "dim must be at most 128, got %lld", (long long)dim);
   if (n > int64_t(1) << 30) return fail(DMUON_ERR_UNSUPPORTED, "n must be at most 2^30, got %lld", (long long)n);
+  if ((n / 128 + 1 + std::min(sequences, n)) * heads > kMaxTokens)
+    return fail(DMUON_ERR_UNSUPPORTED, "more than 2^31 - 1 tiles of 128 rows");
   if (sequences < (offsets ? 0 : 1) || sequences > kMaxTokens)
     return fail(DMUON_ERR_INVALID_ARG, "sequences must be in [1, 2^31 - 1] (0 with offsets), got %lld", (long long)sequences);
   if (offsets) {
@@ -2281,7 +2283,7 @@ int dmuon_attention(const void* q, int64_t q_token, int64_t q_head, const void* 
     p.lse = lse;
     p.status = ds->status;
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);
-    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention(p, ds->sms, stream); }), "attention launch");
+    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention(p, stream); }), "attention launch");
     return DMUON_OK;
   } catch (const std::exception& e) {
     return fail(DMUON_ERR_OOM, "host exception: %s", e.what());
@@ -2326,7 +2328,7 @@ int dmuon_attention_grad(const void* dout, int64_t dout_token, int64_t dout_head
     st = token_workspace(*ds, attention_workspace(p, nullptr), stream, &ws);
     if (st != DMUON_OK) return st;
     attention_workspace(p, ws);
-    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention_grad(p, ds->sms, stream); }),
+    DM_CUDA(timed(kClsAttention, stream, [&] { return launch_attention_grad(p, stream); }),
             "attention gradient launch");
     return DMUON_OK;
   } catch (const std::exception& e) {

@@ -130,8 +130,8 @@ __device__ __forceinline__ void zero_rows_outside(const AttentionLaunch& p, cons
   const int64_t first = row::load_id(p.offsets, p.id_bytes, 0), last = row::load_id(p.offsets, p.id_bytes, p.sequences);
   const int64_t before = first < 0 ? 0 : first > p.n ? p.n : first, from = last < before ? before : last > p.n ? p.n : last;
   const int64_t rows = (before + p.n - from) * heads;
-  const int64_t thread = (static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
-  for (int64_t r = thread; r < rows; r += static_cast<int64_t>(gridDim.x) * gridDim.y * blockDim.x) {
+  const int64_t thread = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  for (int64_t r = thread; r < rows; r += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int64_t k = r / heads, head = r - k * heads, token = k < before ? k : from + (k - before);
     bf16* x = out_at(a, token, head);
     for (int c = 0; c < p.dim; c += 8) *reinterpret_cast<uint4*>(x + c) = make_uint4(0, 0, 0, 0);
@@ -166,7 +166,7 @@ __device__ __forceinline__ Unit unit_at(const AttentionLaunch& p, int64_t length
   return {static_cast<int>(kv * group + unit - back * group), static_cast<int>(p.causal ? block + 1 : blocks), block * kTile};
 }
 
-// Scores of one row times log2(e) |scale|, made probabilities; see softmax_rows.
+// A row of outputs times f.
 template <int kD>
 __device__ __forceinline__ void scale_outputs(uint32_t tmem_out, float f) {
 #pragma unroll
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   griddep_wait();
   const int group = p.heads / p.kv_heads;
   if (warp == 9) {
-    const Place found = find_place(p, blockIdx.x, [&](int64_t len) { return ((len + kTile - 1) / kTile * group + 1) / 2; });
+    const Place found = find_place(p, blockIdx.x / p.kv_heads, [&](int64_t len) { return ((len + kTile - 1) / kTile * group + 1) / 2; });
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
   }
@@ -450,148 +450,623 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
 }
 
 // ---------------------------------------------------------------------------- backward
+//
+// Two kernels, each over its own rows, so that every sum has one owner and one order (a single pass would add dq or dk
+// and dv across CTAs): scores and dout . v are formed in both, 7 products of a pair of tiles in place of 5.
+//
+// Queries (dq): a CTA has 128 queries of one head. Scores lie in one buffer of tensor memory, dout . v in two in turn,
+// so that the products for the next tile of keys run while ds of this one is formed (over its dout . v, as bf16, the left
+// operand of the product with the keys). D = dout . out is off by what out lost in its rounding, which counts where
+// rows have few keys, whose ds cancel. So the sum of ds, which is 0 but for that, is added to D: for dk in all rows
+// (delta), and for dq in rows whose keys lie in one tile.
+//
+// Keys (dk, dv): a CTA has 128 keys of a key head and meets the queries of all its query heads. Scores are formed
+// transposed, so that a thread has a key's row and p and ds are again left operands from tensor memory: scores, dout . v,
+// dv and dk fill its 512 columns. Products of one kind run while the warps work on the other:
+// dv(i), scores(i + 1), dk(i), dout . v(i + 1).
+//
+// In both, 8 warps form p and ds: each thread half of a row, 64 columns.
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kHalf = 64;
 
-// Sequence of a token: [begin, end), empty where the token lies in none.
-__device__ __forceinline__ void sequence_of(const AttentionLaunch& p, int64_t token, int64_t* begin, int64_t* end) {
-  if (!p.offsets) {
-    const int64_t len = p.n / p.sequences;
-    *begin = token / len * len;
-    *end = *begin + len;
-    return;
-  }
-  int64_t lo = 0, hi = p.sequences;  // the last offset that is not behind the token
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) / 2;
-    if (row::load_id(p.offsets, p.id_bytes, mid) <= token) lo = mid;
-    else hi = mid - 1;
-  }
-  const int64_t b = row::load_id(p.offsets, p.id_bytes, lo);
-  const int64_t e = lo < p.sequences ? row::load_id(p.offsets, p.id_bytes, lo + 1) : 0;
-  *begin = b < 0 ? 0 : b;
-  *end = token < b ? token : e > p.n ? p.n : e;
-}
-
-struct Row4 {
-  float v[4];
+template <int kD>
+struct Bwd {
+  static constexpr int kTileBytes = kTile * kD * 2;
+  static constexpr int kBoxes = kD / 64, kBoxBytes = kTile * 128;
+  static constexpr int kThreads = 352;  // warps 0-7: rows; 8: copies; 9: products; 10: what the rows need beside them
+  static constexpr uint32_t kCols = 512;
+  static constexpr int kKeySlots = 3, kValueSlots = 2;
+  static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 1024 + 256 + 1024;
+  static constexpr int kSmemKeys = 6 * kTileBytes + 4 * kTile * 4 + 256 + 1024;
 };
 
-__device__ __forceinline__ Row4 load4(const bf16* x, int dim) {
-  Row4 r;
+// One thread's copies of a tile: `row` is the first token's index in the arrays.
+template <int kD>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int64_t row, uint64_t* bar) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = (threadIdx.x & 31) + 32 * k;
-    r.v[k] = c < dim ? row::to_f(x[c]) : 0.f;
-  }
-  return r;
+  for (int b = 0; b < Bwd<kD>::kBoxes; ++b)
+    tma_load_3d(smem_u32(dst + b * Bwd<kD>::kBoxBytes), map, b * 64, head, static_cast<int>(row), bar);
 }
 
-__device__ __forceinline__ void store4(bf16* x, int dim, const Row4& r) {
+// D = A B^T of two tiles (rows of kD columns).
+template <int kD>
+__device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
+  constexpr uint32_t desc = (1u << 4) | (1u << 7) | (1u << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
+  const uint32_t a0 = smem_u32(a), b0 = smem_u32(b);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = (threadIdx.x & 31) + 32 * k;
-    if (c < dim) x[c] = row::from_f<bf16>(r.v[k]);
+  for (int s = 0; s < kD / 16; ++s) {
+    const uint32_t off = (s >> 2) * Bwd<kD>::kBoxBytes + (s & 3) * 32;
+    mma_f16(d, smem_desc(a0 + off, 16, 1024), smem_desc(b0 + off, 16, 1024), desc, s > 0);
   }
 }
 
-__device__ __forceinline__ float dot(const Row4& a, const Row4& b) {
-  float s = a.v[0] * b.v[0] + a.v[1] * b.v[1] + a.v[2] * b.v[2] + a.v[3] * b.v[3];
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
-
-// D of every row.
-__global__ void __launch_bounds__(kThreads) attention_delta_kernel(const __grid_constant__ AttentionLaunch p) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= p.n * p.heads) return;
-  const int64_t token = unit / p.heads, head = unit % p.heads;
-  const float d = dot(load4(at(p.out, token, head), p.dim), load4(at(p.dout, token, head), p.dim));
-  if ((threadIdx.x & 31) == 0) p.delta[head * p.n + token] = d;
-}
-
-__global__ void __launch_bounds__(kThreads) attention_dq_kernel(const __grid_constant__ AttentionLaunch p) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= p.n * p.heads) return;
-  const int64_t token = unit / p.heads, head = unit % p.heads, kv = head / (p.heads / p.kv_heads);
-  int64_t begin, end;
-  sequence_of(p, token, &begin, &end);
-  if (token >= end) {
-    if (p.zero_outside) store4(out_at(p.dq, token, head), p.dim, Row4{});
-    return;
-  }
-  const Row4 q = load4(at(p.q, token, head), p.dim), g = load4(at(p.dout, token, head), p.dim);
-  const float lse = p.lse[head * p.n + token], delta = p.delta[head * p.n + token];
-  Row4 d{};
-  const int64_t last = p.causal ? token + 1 : end;
-  for (int64_t j = begin; j < last; ++j) {
-    const Row4 k = load4(at(p.k, j, kv), p.dim);
-    const float e = expf(dot(q, k) * p.scale - lse);
-    const float ds = e * (dot(g, load4(at(p.v, j, kv), p.dim)) - delta) * p.scale;
+// D (+)= A B, with A (bf16) in tensor memory: the first 64 of its 128 columns in 32 from `a` on, the others in 32 from a
+// + 64 on, each half where the half row of scores was that it was made from.
+template <int kD>
+__device__ __forceinline__ void mma_halves(uint32_t d, uint32_t a, const uint8_t* b, bool add) {
+  const uint32_t desc = instr_desc_bf16<kTile, kD>(true), b0 = smem_u32(b);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) d.v[c] = fmaf(ds, k.v[c], d.v[c]);
-  }
-  store4(out_at(p.dq, token, head), p.dim, d);
+  for (int s = 0; s < kTile / 16; ++s)
+    mma_tmem_a(d, a + (s >> 2) * kHalf + (s & 3) * 8, smem_desc(b0 + s * 2048, Bwd<kD>::kBoxBytes, 1024), desc, add || s > 0);
 }
 
-__global__ void __launch_bounds__(kThreads) attention_dkv_kernel(const __grid_constant__ AttentionLaunch p) {
-  ptx::griddep_launch_dependents();
-  ptx::griddep_wait();
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= p.n * p.kv_heads) return;
-  const int64_t token = unit / p.kv_heads, kv = unit % p.kv_heads, group = p.heads / p.kv_heads;
-  int64_t begin, end;
-  sequence_of(p, token, &begin, &end);
-  if (token >= end) {
-    if (p.zero_outside) {
-      store4(out_at(p.dk, token, kv), p.dim, Row4{});
-      store4(out_at(p.dv, token, kv), p.dim, Row4{});
-    }
-    return;
-  }
-  const Row4 k = load4(at(p.k, token, kv), p.dim), v = load4(at(p.v, token, kv), p.dim);
-  Row4 dk{}, dv{};
-  for (int64_t head = kv * group; head < (kv + 1) * group; ++head)
-    for (int64_t i = p.causal ? token : begin; i < end; ++i) {
-      const Row4 q = load4(at(p.q, i, head), p.dim), g = load4(at(p.dout, i, head), p.dim);
-      const float e = expf(dot(q, k) * p.scale - p.lse[head * p.n + i]);
-      const float ds = e * (dot(g, v) - p.delta[head * p.n + i]) * p.scale;
+// Zeros in the rows from `valid` on of a tile in shared memory, by a warp, visible to the products.
+template <int kD>
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
+  for (int b = 0; b < Bwd<kD>::kBoxes; ++b)
+    for (int i = valid * 8 + (threadIdx.x & 31); i < kTile * 8; i += 32)
+      *reinterpret_cast<uint4*>(tile + b * Bwd<kD>::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_smem();
+}
+
+// 64 columns of this thread's lane.
+__device__ __forceinline__ void load_half(uint32_t taddr, float (&v)[kHalf]) {
+  uint32_t r[kHalf];
+  tmem_ld32_issue(taddr, r);
+  tmem_ld32_issue(taddr + 32, r + 32);
+  tmem_ld_wait(r);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        dv.v[c] = fmaf(e, g.v[c], dv.v[c]);
-        dk.v[c] = fmaf(ds, q.v[c], dk.v[c]);
+  for (int k = 0; k < kHalf; ++k) v[k] = __uint_as_float(r[k]);
+}
+
+// 32 columns from taddr on of an accumulator, times f, to `out` as bf16.
+__device__ __forceinline__ void store_columns(uint32_t taddr, float f, bf16* out, int columns) {
+  uint32_t r[32];
+  tmem_ld32_issue(taddr, r);
+  tmem_ld_wait(r);
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[k + e]) * f;
+    if (k < columns) *reinterpret_cast<uint4*>(out + k) = row::pack16(v);
+  }
+}
+
+template <int kD>
+__global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(const __grid_constant__ AttentionLaunch p) {
+  using F = Bwd<kD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *q_tile = smem, *do_tile = q_tile + F::kTileBytes, *keys = do_tile + F::kTileBytes,
+          *values = keys + F::kKeySlots * F::kTileBytes;
+  float* exchange = reinterpret_cast<float*>(values + F::kValueSlots * F::kTileBytes);  // 2 x 128
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(exchange + 2 * kTile);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + F::kKeySlots;
+  uint64_t* v_full = k_empty + F::kKeySlots;
+  uint64_t* v_empty = v_full + F::kValueSlots;
+  uint64_t* patched = v_empty + F::kValueSlots;
+  uint64_t* s_full = patched + 1;
+  uint64_t* s_read = s_full + 1;
+  uint64_t* dp_full = s_read + 1;  // of either buffer
+  uint64_t* ds_full = dp_full + 2;
+  uint64_t* exchanged = ds_full + 2;
+  uint64_t* done = exchanged + 1;
+  uint64_t* drain = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ Place place;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < F::kKeySlots; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
+    for (int s = 0; s < F::kValueSlots; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
+    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(s_read, 8);
+    for (int b = 0; b < 2; ++b) mbar_init(&dp_full[b], 1), mbar_init(&ds_full[b], 8);
+    mbar_init(exchanged, 8), mbar_init(done, 1), mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+  if (warp == 9) {
+    const Place found = find_place(p, blockIdx.x / p.heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
+    if (lane == 0) place = found;
+    if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
+  }
+  zero_rows_outside(p, p.dq, p.heads, nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int64_t begin = place.begin, length = place.length;
+  if (length == 0) return;
+  const uint32_t tmem = *tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dq = tmem + 3 * kTile;
+  const int64_t blocks = (length + kTile - 1) / kTile, block = blocks - 1 - place.piece, row0 = block * kTile;  // long rows first
+  const int tiles = static_cast<int>(p.causal ? block + 1 : blocks);
+  const bool patch = static_cast<int64_t>(tiles) * kTile > length;
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_fast(bar, phase & 1u, abort_flag, p.status); };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ copies
+    bool ok = true;
+    int i = 0, loaded_v = 0;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(q_full, 2 * F::kTileBytes);
+      load_tile<kD>(q_tile, &p.map_q, head, begin + row0, q_full);
+      load_tile<kD>(do_tile, &p.map_dout, head, begin + row0, q_full);
+      for (; i < tiles; ++i) {
+        const int64_t row = begin + static_cast<int64_t>(i) * kTile;
+        const int ks = i % F::kKeySlots, vs = i % F::kValueSlots;
+        if (!(ok = wait(&k_empty[ks], i / F::kKeySlots + 1))) break;
+        mbar_arrive_expect_tx(&k_full[ks], F::kTileBytes);
+        load_tile<kD>(keys + ks * F::kTileBytes, &p.map_k, kv, row, &k_full[ks]);
+        if (!(ok = wait(&v_empty[vs], i / F::kValueSlots + 1))) {
+          ++i;
+          break;
+        }
+        mbar_arrive_expect_tx(&v_full[vs], F::kTileBytes);
+        load_tile<kD>(values + vs * F::kTileBytes, &p.map_v, kv, row, &v_full[vs]);
+        ++loaded_v;
       }
     }
-  store4(out_at(p.dk, token, kv), p.dim, dk);
-  store4(out_at(p.dv, token, kv), p.dim, dv);
+    __syncwarp();
+    if (patch) {  // the keys behind the sequence meet ds of 0, and must be 0 too
+      const int last = (tiles - 1) % F::kKeySlots;
+      ok = __all_sync(0xffffffffu, ok && wait(&k_full[last], (tiles - 1) / F::kKeySlots));
+      if (ok) {
+        clear_rows<kD>(keys + last * F::kTileBytes, static_cast<int>(length - static_cast<int64_t>(tiles - 1) * kTile));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(patched);
+      }
+    }
+    if (lane == 0 && (!ok || *abort_flag)) {
+      wait_bounded(q_full, 0, abort_flag, p.status, kDrainLimitNs, false);
+      for (int t = max(0, i - F::kKeySlots); t < i; ++t)
+        wait_bounded(&k_full[t % F::kKeySlots], (t / F::kKeySlots) & 1, abort_flag, p.status, kDrainLimitNs, false);
+      for (int t = max(0, loaded_v - F::kValueSlots); t < loaded_v; ++t)
+        wait_bounded(&v_full[t % F::kValueSlots], (t / F::kValueSlots) & 1, abort_flag, p.status, kDrainLimitNs, false);
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ products
+    if (lane == 0) {
+      auto scores = [&](int i) {
+        const int ks = i % F::kKeySlots;
+        if (!wait(&k_full[ks], i / F::kKeySlots)) return false;
+        if (patch && i + 1 == tiles && !wait(patched, 0)) return false;
+        if (i > 0 && !wait(s_read, i - 1)) return false;
+        tc_fence_after();
+        mma_rows<kD>(t_s, q_tile, keys + ks * F::kTileBytes);
+        mma_commit(s_full);
+        return true;
+      };
+      auto along = [&](int i) {
+        const int vs = i % F::kValueSlots;
+        if (!wait(&v_full[vs], i / F::kValueSlots)) return false;
+        tc_fence_after();
+        mma_rows<kD>(t_dp + (i & 1) * kTile, do_tile, values + vs * F::kTileBytes);
+        mma_commit(&v_empty[vs]);
+        mma_commit(&dp_full[i & 1]);
+        return true;
+      };
+      bool ok = wait(q_full, 0) && scores(0) && along(0);
+      for (int i = 0; ok && i < tiles; ++i) {
+        if (i + 1 < tiles) ok = scores(i + 1) && along(i + 1);
+        if (!ok || !(ok = wait(&ds_full[i & 1], i >> 1))) break;
+        tc_fence_after();
+        mma_halves<kD>(t_dq, t_dp + (i & 1) * kTile, keys + (i % F::kKeySlots) * F::kTileBytes, i > 0);
+        mma_commit(&k_empty[i % F::kKeySlots]);
+      }
+      if (ok) mma_commit(done);
+      mma_commit(drain);
+      wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------ rows
+    const int side = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool live = row0 + r < length;
+    const int64_t token = begin + (live ? row0 + r : 0);
+    const float sl2 = p.scale * kLog2e, lse2 = live ? p.lse[static_cast<int64_t>(head) * p.n + token] * kLog2e : INFINITY;
+    float delta = 0.f;
+    {
+      const bf16 *o = at(p.out, token, head), *g = at(p.dout, token, head);
+      for (int c = 0; c < p.dim; c += 8) {
+        float a[8], b[8];
+        row::unpack16<bf16>(a, *reinterpret_cast<const uint4*>(o + c));
+        row::unpack16<bf16>(b, *reinterpret_cast<const uint4*>(g + c));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
+      }
+    }
+    float rest = 0.f;  // sum of ds
+    bool ok = true;
+    for (int i = 0; i < tiles; ++i) {
+      ok = __all_sync(0xffffffffu, wait(s_full, i));
+      if (!ok) break;
+      tc_fence_after();
+      float prob[kHalf];
+      load_half(t_s + lanes + side * kHalf, prob);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_read);
+      const int64_t key0 = static_cast<int64_t>(i) * kTile;
+      const bool masked = (p.causal && key0 == row0) || key0 + kTile > length;
+      const int here = masked ? static_cast<int>((p.causal && live ? row0 + r + 1 : length) - key0) - side * kHalf : kHalf;
+#pragma unroll
+      for (int k = 0; k < kHalf; k += 2) {
+        const float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(-lse2, -lse2));
+        prob[k] = pow2(y.x), prob[k + 1] = pow2(y.y);
+      }
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) prob[k] = k < here ? prob[k] : 0.f;
+      }
+      ok = __all_sync(0xffffffffu, wait(&dp_full[i & 1], i >> 1));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t = t_dp + (i & 1) * kTile + lanes + side * kHalf;
+      if (tiles == 1) {
+        // All keys of these rows are at hand: the whole D before the first ds.
+        float dp[kHalf], sum = 0.f;
+        load_half(t, dp);
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) sum += k < here ? prob[k] * (dp[k] - delta) : 0.f;
+        exchange[side * kTile + r] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(exchanged);
+        ok = __all_sync(0xffffffffu, wait(exchanged, 0));
+        if (!ok) break;
+        delta += exchange[r] + exchange[kTile + r];
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t dp[32], half[16];
+        tmem_ld32_issue(t + c, dp);
+        tmem_ld_wait(dp);
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float2 ds = add2(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), make_float2(-delta, -delta));
+          ds = mul2(ds, make_float2(prob[c + k], prob[c + k + 1]));
+          if (masked) {  // 0 whatever dout . v is there
+            ds.x = c + k < here ? ds.x : 0.f;
+            ds.y = c + k + 1 < here ? ds.y : 0.f;
+          }
+          rest += ds.x + ds.y;
+          half[k / 2] = pack_bf16(ds.x, ds.y);
+        }
+        tmem_st16(t + c / 2, half);  // over columns that have been read
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[i & 1]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
+    if (ok && tiles > 1) {
+      exchange[side * kTile + r] = rest;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(exchanged);
+      ok = __all_sync(0xffffffffu, wait(exchanged, 0));
+      if (ok) delta += exchange[r] + exchange[kTile + r];
+    }
+    if (ok) {
+      tc_fence_after();
+      if (live && side == 0) p.delta[static_cast<int64_t>(head) * p.n + token] = delta;
+      bf16* out = out_at(p.dq, token, head);
+#pragma unroll
+      for (int c = side * (kD / 2); c < (side + 1) * (kD / 2); c += 32)
+        store_columns(t_dq + lanes + c, p.scale, out + c, live ? p.dim - c : 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, F::kCols);
 }
 
-unsigned ctas_for(int64_t units) { return static_cast<unsigned>((units + kWarps - 1) / kWarps); }
+template <int kD>
+__global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(const __grid_constant__ AttentionLaunch p) {
+  using F = Bwd<kD>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *k_tile = smem, *v_tile = k_tile + F::kTileBytes, *queries = v_tile + F::kTileBytes,
+          *douts = queries + 2 * F::kTileBytes;
+  float* stats = reinterpret_cast<float*>(douts + 2 * F::kTileBytes);  // two stages of lse log2(e), D
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * kTile);
+  uint64_t* q_full = kv_full + 1;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* do_full = q_empty + 2;
+  uint64_t* do_empty = do_full + 2;
+  uint64_t* st_full = do_empty + 2;
+  uint64_t* st_empty = st_full + 2;
+  uint64_t* patched = st_empty + 2;
+  uint64_t* s_full = patched + 1;
+  uint64_t* p_full = s_full + 1;
+  uint64_t* dp_full = p_full + 1;
+  uint64_t* ds_full = dp_full + 1;
+  uint64_t* done = ds_full + 1;
+  uint64_t* drain = done + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ Place place;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1), mbar_init(&do_full[s], 1), mbar_init(&do_empty[s], 1);
+      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], 8);
+    }
+    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(p_full, 8), mbar_init(dp_full, 1), mbar_init(ds_full, 8);
+    mbar_init(done, 1), mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  griddep_wait();
+  if (warp == 9) {
+    const Place found = find_place(p, blockIdx.x / p.kv_heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
+    if (lane == 0) place = found;
+    if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
+  }
+  zero_rows_outside(p, p.dk, p.kv_heads, nullptr);
+  zero_rows_outside(p, p.dv, p.kv_heads, nullptr);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int64_t begin = place.begin, length = place.length;
+  if (length == 0) return;
+  const uint32_t tmem = *tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = tmem + 3 * kTile;
+  const int64_t blocks = (length + kTile - 1) / kTile, key0 = place.piece * kTile, first = p.causal ? place.piece : 0;
+  const int per_head = static_cast<int>(blocks - first);  // tiles of queries
+  const int64_t tiles = static_cast<int64_t>(per_head) * group;
+  const bool ragged = length % kTile != 0;  // a head's last tile of queries has rows of other sequences
+  auto wait = [&](uint64_t* bar, int64_t phase) { return wait_fast(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, p.status); };
+
+  if (warp == 8) {
+    // ------------------------------------------------------------------ copies
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * F::kTileBytes);
+      load_tile<kD>(k_tile, &p.map_k, kv, begin + key0, kv_full);
+      load_tile<kD>(v_tile, &p.map_v, kv, begin + key0, kv_full);
+      int64_t i = 0, loaded_do = 0;
+      bool ok = true;
+      for (int h = 0, b = 0; i < tiles; ++i) {
+        const int s = static_cast<int>(i & 1);
+        const int64_t row = begin + (first + b) * kTile;
+        if (!(ok = wait(&q_empty[s], (i >> 1) + 1))) break;
+        mbar_arrive_expect_tx(&q_full[s], F::kTileBytes);
+        load_tile<kD>(queries + s * F::kTileBytes, &p.map_q, kv * group + h, row, &q_full[s]);
+        if (!(ok = wait(&do_empty[s], (i >> 1) + 1))) {
+          ++i;
+          break;
+        }
+        mbar_arrive_expect_tx(&do_full[s], F::kTileBytes);
+        load_tile<kD>(douts + s * F::kTileBytes, &p.map_dout, kv * group + h, row, &do_full[s]);
+        ++loaded_do;
+        if (++b == per_head) b = 0, ++h;
+      }
+      if (!ok || *abort_flag) {
+        wait_bounded(kv_full, 0, abort_flag, p.status, kDrainLimitNs, false);
+        for (int64_t t = i > 2 ? i - 2 : 0; t < i; ++t)
+          wait_bounded(&q_full[t & 1], (t >> 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
+        for (int64_t t = loaded_do > 2 ? loaded_do - 2 : 0; t < loaded_do; ++t)
+          wait_bounded(&do_full[t & 1], (t >> 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------ products
+    if (lane == 0) {
+      int patches = 0, left = per_head;  // tiles of queries to come of the head whose scores are formed next
+      auto scores = [&](int64_t i) {
+        if (!wait(&q_full[i & 1], i >> 1)) return false;
+        if (--left == 0) {
+          left = per_head;
+          if (ragged && !wait(patched, patches++)) return false;
+        }
+        tc_fence_after();
+        mma_rows<kD>(t_s, k_tile, queries + (i & 1) * F::kTileBytes);
+        mma_commit(s_full);
+        return true;
+      };
+      auto along = [&](int64_t i) {
+        if (!wait(&do_full[i & 1], i >> 1)) return false;
+        tc_fence_after();
+        mma_rows<kD>(t_dp, v_tile, douts + (i & 1) * F::kTileBytes);
+        mma_commit(dp_full);
+        return true;
+      };
+      bool ok = wait(kv_full, 0) && scores(0) && along(0);
+      for (int64_t i = 0; ok && i < tiles; ++i) {
+        if (!(ok = wait(p_full, i))) break;
+        tc_fence_after();
+        mma_halves<kD>(t_dv, t_s, douts + (i & 1) * F::kTileBytes, i > 0);
+        mma_commit(&do_empty[i & 1]);
+        if (i + 1 < tiles && !(ok = scores(i + 1))) break;
+        if (!(ok = wait(ds_full, i))) break;
+        tc_fence_after();
+        mma_halves<kD>(t_dk, t_dp, queries + (i & 1) * F::kTileBytes, i > 0);
+        mma_commit(&q_empty[i & 1]);
+        if (i + 1 < tiles) ok = along(i + 1);
+      }
+      if (ok) mma_commit(done);
+      mma_commit(drain);
+      wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
+    }
+  } else if (warp == 10) {
+    // ------------------------------------------------------------------ the queries' lse and D; rows of other sequences
+    int64_t i = 0;
+    bool ok = true;
+    for (int h = 0; ok && h < group; ++h)
+      for (int b = 0; b < per_head; ++b, ++i) {
+        const int s = static_cast<int>(i & 1);
+        ok = __all_sync(0xffffffffu, wait(&st_empty[s], (i >> 1) + 1));
+        if (!ok) break;
+        const int64_t row = (first + b) * kTile, list = static_cast<int64_t>(kv * group + h) * p.n + begin;
+        for (int k = lane; k < kTile; k += 32) {
+          // A query behind the sequence has p = 2^(0 - infinity) = 0.
+          const bool live = row + k < length;
+          stats[s * 2 * kTile + k] = live ? p.lse[list + row + k] * kLog2e : INFINITY;
+          stats[s * 2 * kTile + kTile + k] = live ? p.delta[list + row + k] : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[s]);
+        if (ragged && b + 1 == per_head) {
+          ok = __all_sync(0xffffffffu, wait(&q_full[s], i >> 1) && wait(&do_full[s], i >> 1));
+          if (!ok) break;
+          clear_rows<kD>(queries + s * F::kTileBytes, static_cast<int>(length - row));
+          clear_rows<kD>(douts + s * F::kTileBytes, static_cast<int>(length - row));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(patched);
+        }
+      }
+  } else {
+    // ------------------------------------------------------------------ rows
+    const int side = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float sl2 = p.scale * kLog2e;
+    bool ok = true;
+    int left = 0;
+    for (int64_t i = 0; i < tiles; ++i) {
+      const bool diagonal = p.causal && left == 0;  // a head's first tile of queries is that of the keys
+      left = left == 0 ? per_head - 1 : left - 1;
+      const float* lse2 = stats + (i & 1) * 2 * kTile + side * kHalf;
+      const float* delta = lse2 + kTile;
+      ok = wait(&st_full[i & 1], i >> 1);
+      ok = __all_sync(0xffffffffu, ok && wait(s_full, i));
+      if (!ok) break;
+      tc_fence_after();
+      float prob[kHalf];
+      load_half(t_s + lanes + side * kHalf, prob);
+#pragma unroll
+      for (int k = 0; k < kHalf; k += 4) {
+        const float4 l = *reinterpret_cast<const float4*>(lse2 + k);
+        float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(-l.x, -l.y));
+        prob[k] = pow2(y.x), prob[k + 1] = pow2(y.y);
+        y = fma2(make_float2(prob[k + 2], prob[k + 3]), make_float2(sl2, sl2), make_float2(-l.z, -l.w));
+        prob[k + 2] = pow2(y.x), prob[k + 3] = pow2(y.y);
+      }
+      const int from = diagonal ? r - side * kHalf : 0;  // the queries before the key do not meet it
+      if (diagonal) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) prob[k] = k < from ? 0.f : prob[k];
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t half[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) half[k / 2] = pack_bf16(prob[c + k], prob[c + k + 1]);
+        tmem_st16(t_s + lanes + side * kHalf + c / 2, half);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+      ok = __all_sync(0xffffffffu, wait(dp_full, i));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t = t_dp + lanes + side * kHalf;
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 32) {
+        uint32_t dp[32], half[16];
+        tmem_ld32_issue(t + c, dp);
+        tmem_ld_wait(dp);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 d = *reinterpret_cast<const float4*>(delta + c + k);
+          float2 a = add2(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), make_float2(-d.x, -d.y));
+          float2 b = add2(make_float2(__uint_as_float(dp[k + 2]), __uint_as_float(dp[k + 3])), make_float2(-d.z, -d.w));
+          a = mul2(a, make_float2(prob[c + k], prob[c + k + 1]));
+          b = mul2(b, make_float2(prob[c + k + 2], prob[c + k + 3]));
+          if (diagonal) {  // 0 whatever dout . v is there
+            a.x = c + k < from ? 0.f : a.x, a.y = c + k + 1 < from ? 0.f : a.y;
+            b.x = c + k + 2 < from ? 0.f : b.x, b.y = c + k + 3 < from ? 0.f : b.y;
+          }
+          half[k / 2] = pack_bf16(a.x, a.y);
+          half[k / 2 + 1] = pack_bf16(b.x, b.y);
+        }
+        tmem_st16(t + c / 2, half);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ds_full), mbar_arrive(&st_empty[i & 1]);
+    }
+    if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
+    if (ok) {
+      tc_fence_after();
+      const bool live = key0 + r < length;
+      const int64_t token = begin + key0 + (live ? r : 0);
+      bf16* out = out_at(side ? p.dk : p.dv, token, kv);
+#pragma unroll
+      for (int c = 0; c < kD; c += 32)
+        store_columns((side ? t_dk : t_dv) + lanes + c, side ? p.scale : 1.f, out + c, live ? p.dim - c : 0);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, F::kCols);
+}
+
+// ---------------------------------------------------------------------------- launches
+
+// Pieces that the sequences have: of equal ones exactly; of others at most, each having one more than its tokens fill.
+int64_t tiles_of(const AttentionLaunch& p) {
+  if (!p.offsets) return p.sequences * ((p.n / p.sequences + kTile - 1) / kTile);
+  return std::max<int64_t>(1, p.n / kTile + std::min(p.sequences, p.n));
+}
+
+template <typename K>
+cudaError_t launch_tiles(K* kernel, AttentionLaunch& p, int64_t slots, int heads, int threads, int smem, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // Heads are neighbours in the grid: the longest rows of all of them start first.
+  return row::launch(kernel, dim3(static_cast<unsigned>(slots * heads)), threads, smem, stream, p);
+}
 
 template <int kD>
 cudaError_t launch_forward(AttentionLaunch& p, cudaStream_t stream) {
   using F = Fwd<kD>;
-  const char* why = nullptr;
-  if (!encode_heads(&p.map_q, p.q, p.dim, p.heads, p.n, kTile, &why) ||
-      !encode_heads(&p.map_k, p.k, p.dim, p.kv_heads, p.n, kTile, &why) ||
-      !encode_heads(&p.map_v, p.v, p.dim, p.kv_heads, p.n, kTile, &why))
-    return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(attention_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
-  if (e != cudaSuccess) return e;
-  const int64_t group = p.heads / p.kv_heads, filled = std::min(p.sequences, p.n);
-  // Pairs of units: of equal sequences exactly; of others at most, every sequence having one unit per head more than
-  // its tokens fill, and one unit alone.
+  const int64_t group = p.heads / p.kv_heads;
+  // Pairs of units; with offsets every sequence may leave half a pair.
   int64_t slots = 0;
   if (!p.offsets) slots = p.sequences * (((p.n / p.sequences + kTile - 1) / kTile * group + 1) / 2);
-  else slots = ((p.n / kTile + filled) * group + filled) / 2 + 1;
-  if (slots > 0x7fffffff) return cudaErrorInvalidValue;
-  return row::launch(attention_kernel<kD>, dim3(static_cast<unsigned>(slots), static_cast<unsigned>(p.kv_heads)), F::kThreads,
-                     F::kSmem, stream, p);
+  else slots = (tiles_of(p) * group + std::min(p.sequences, p.n)) / 2 + 1;
+  return launch_tiles(attention_kernel<kD>, p, slots, p.kv_heads, F::kThreads, F::kSmem, stream);
+}
+
+template <int kD>
+cudaError_t launch_backward(AttentionLaunch& p, cudaStream_t stream) {
+  using F = Bwd<kD>;
+  const cudaError_t e = launch_tiles(attention_dq_kernel<kD>, p, tiles_of(p), p.heads, F::kThreads, F::kSmemQueries, stream);
+  if (e != cudaSuccess) return e;
+  return launch_tiles(attention_dkv_kernel<kD>, p, tiles_of(p), p.kv_heads, F::kThreads, F::kSmemKeys, stream);
+}
+
+cudaError_t set_maps(AttentionLaunch& p) {
+  const char* why = nullptr;
+  p.scale_log2 = fabsf(p.scale) * kLog2e;
+  if (!encode_heads(&p.map_q, p.q, p.dim, p.heads, p.n, kTile, &why) ||
+      !encode_heads(&p.map_k, p.k, p.dim, p.kv_heads, p.n, kTile, &why) ||
+      !encode_heads(&p.map_v, p.v, p.dim, p.kv_heads, p.n, kTile, &why) ||
+      (p.dout.data && !encode_heads(&p.map_dout, p.dout, p.dim, p.heads, p.n, kTile, &why)))
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -601,16 +1076,16 @@ int64_t attention_workspace(AttentionLaunch& p, char* ws) {
   return static_cast<int64_t>(sizeof(float)) * p.n * p.heads;
 }
 
-cudaError_t launch_attention(AttentionLaunch& p, int sms, cudaStream_t stream) {
-  p.scale_log2 = fabsf(p.scale) * kLog2e;
+cudaError_t launch_attention(AttentionLaunch& p, cudaStream_t stream) {
+  const cudaError_t e = set_maps(p);
+  if (e != cudaSuccess) return e;
   return p.dim <= 64 ? launch_forward<64>(p, stream) : launch_forward<128>(p, stream);
 }
 
-cudaError_t launch_attention_grad(AttentionLaunch& p, int sms, cudaStream_t stream) {
-  cudaError_t e = row::launch(attention_delta_kernel, dim3(ctas_for(p.n * p.heads)), kThreads, 0, stream, p);
-  if (e == cudaSuccess) e = row::launch(attention_dq_kernel, dim3(ctas_for(p.n * p.heads)), kThreads, 0, stream, p);
-  if (e == cudaSuccess) e = row::launch(attention_dkv_kernel, dim3(ctas_for(p.n * p.kv_heads)), kThreads, 0, stream, p);
-  return e;
+cudaError_t launch_attention_grad(AttentionLaunch& p, cudaStream_t stream) {
+  const cudaError_t e = set_maps(p);
+  if (e != cudaSuccess) return e;
+  return p.dim <= 64 ? launch_backward<64>(p, stream) : launch_backward<128>(p, stream);
 }
 
 }  // namespace dmuon

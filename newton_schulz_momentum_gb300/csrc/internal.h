@@ -502,15 +502,15 @@ struct AttentionLaunch {
   float* lse;    // heads x n
   float* delta;  // heads x n, workspace of the backward pass
   unsigned* status;
-  // Set by launch_attention[_grad]: copies of 64 columns of 128 (forward) or 64 tokens of a head, and |scale| log2(e).
+  // Set by launch_attention[_grad]: copies of 64 columns of 128 tokens of a head, and |scale| log2(e).
   CUtensorMap map_q, map_k, map_v, map_dout;
   float scale_log2;
 };
 // Encode the tensor map of an array of heads (host): boxes of 64 columns and box_rows tokens of one head.
 bool encode_heads(CUtensorMap* map, const HeadArray& a, int dim, int heads, int64_t n, uint32_t box_rows, const char** err);
 int64_t attention_workspace(AttentionLaunch& p, char* ws);
-cudaError_t launch_attention(AttentionLaunch& p, int sms, cudaStream_t stream);
-cudaError_t launch_attention_grad(AttentionLaunch& p, int sms, cudaStream_t stream);
+cudaError_t launch_attention(AttentionLaunch& p, cudaStream_t stream);
+cudaError_t launch_attention_grad(AttentionLaunch& p, cudaStream_t stream);
 
 // Record `message` as the calling thread's last error (returned by dmuon_last_error) and return status.
 int set_error(int status, const char* message);

@@ -171,7 +171,8 @@ def attention(q, k, v, ends, causal=True, scale=None):
 
 def attention_grad(dout, q, k, v, out, lse, ends, causal=True, scale=None, p_off=0.0, dot_off=0.0):
     """(dq, dk, dv) at the stored out and lse, and the bounds of what they are off by where every p is off by p_off of
-    itself and dout . v and D by dot_off of the sum of their absolute terms."""
+    itself and dout . v and D by dot_off of the sum of their absolute terms. The sum of a row's ds, 0 but for what out
+    lost in its rounding, may be added to D, in whole or in part: it counts to the bounds."""
     n, heads, dim = q.shape
     scale = dim ** -0.5 if scale is None else scale
     group = heads // k.shape[1]
@@ -189,7 +190,7 @@ def attention_grad(dout, q, k, v, out, lse, ends, causal=True, scale=None, p_off
             delta = (do * out[b:e, h]).sum(axis=1, keepdims=True)
             ds = p * (along - delta)
             ds_off = p * (dot_off * (np.abs(do) @ np.abs(v[b:e, kv]).T + np.abs(do * out[b:e, h]).sum(axis=1, keepdims=True)))
-            ds_off += p_off * np.abs(ds)
+            ds_off += p_off * np.abs(ds) + p * np.abs(ds.sum(axis=1, keepdims=True))
             got[0][b:e, h] = scale * ds @ k[b:e, kv]
             off[0][b:e, h] = abs(scale) * ds_off @ np.abs(k[b:e, kv])
             got[1][b:e, kv] += scale * ds.T @ q[b:e, h]

@@ -6,7 +6,9 @@ taken from; the exponent's products 4 u |x| and 2^x 4 u. So p is off by x_off = 
 itself, with reach the row's largest scale sum |q k|. Forward: p is rounded to bf16 beside a sum that is not, and the sums
 over len keys are fp32: (b + x_off + 2 len u) sum p |v| + b |out|; lse: x_off + 2 len u + 4 u (1 + |lse|). Backward, at the
 stored out and lse: p and ds are rounded to bf16, dout . v and D add dim terms: p_off = 2 b + x_off, dot_off = 4 dim u, sums
-of len (times the group's heads) terms 4 len group u, and the result's own rounding b."""
+of len (times the group's heads) terms 4 len group u, and the result's own rounding b. D = dout . out has what out lost in
+its rounding; the kernel adds the sum of ds to it, which is exactly that, in some of its sums: with D + t rest, t in [0, 1],
+ds is p |rest| off at most, which the oracle adds to its bounds."""
 
 import numpy as np
 import pytest
