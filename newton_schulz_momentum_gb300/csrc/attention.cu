@@ -139,18 +139,58 @@ __device__ __forceinline__ void zero_rows_outside(const AttentionLaunch& p, cons
   }
 }
 
+// ---------------------------------------------------------------------------- tiles and products
+
+// Columns of tensor memory: a CTA takes all 512 of them, from address 0 on.
+constexpr uint32_t kCols = 512;
+
+// A tile is 128 rows of kD columns (a head's, padded with zeros to 64 or 128), as boxes of 64 columns.
+template <int kD>
+struct Tile {
+  static constexpr int kBytes = kTile * kD * 2, kBoxes = kD / 64, kBoxBytes = kTile * 128;
+};
+
+// One thread's copies of a tile: `row` is the first token's index in the arrays.
+template <int kD>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int head, int64_t row, uint64_t* bar) {
+#pragma unroll
+  for (int b = 0; b < Tile<kD>::kBoxes; ++b)
+    tma_load_3d(dst + b * Tile<kD>::kBoxBytes, map, b * 64, head, static_cast<int>(row), bar);
+}
+
+// The products below are issued by one lane of a warp that runs them as a whole, with addresses of tiles in shared
+// memory and of columns that are the warp's: operands that have to be brought into uniform registers first take longer
+// than the products (128 x 128 x 16: 150 cycles of issue, 68 like this, 64 for the product).
+
+// D = A B^T of two tiles.
+template <int kD>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  const uint32_t desc = instr_desc_bf16<kTile, kTile>(false);
+#pragma unroll
+  for (int s = 0; s < kD / 16; ++s) {
+    const uint32_t off = (s >> 2) * Tile<kD>::kBoxBytes + (s & 3) * 32;
+    mma_f16(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), desc, s > 0);
+  }
+}
+
+// D (+)= A B, A being 128 x 128 bf16 in tensor memory, two of its columns in one: the first 64 from `a` on, the others
+// `second` columns behind.
+template <int kD>
+__device__ __forceinline__ void mma_columns(uint32_t d, uint32_t a, uint32_t second, uint32_t b, bool add) {
+  const uint32_t desc = instr_desc_bf16<kTile, kD>(true);
+#pragma unroll
+  for (int s = 0; s < kTile / 16; ++s)
+    mma_tmem_a(d, a + (s >> 2) * second + (s & 3) * 8, smem_desc(b + s * 2048, Tile<kD>::kBoxBytes, 1024), desc, add || s > 0);
+}
+
 // ---------------------------------------------------------------------------- forward
 
-// kD: columns of a head, padded with zeros to 64 or 128.
 template <int kD>
-struct Fwd {
-  static constexpr int kSlots = 4;
-  static constexpr int kTileBytes = kTile * kD * 2;
-  static constexpr int kBoxes = kD / 64, kBoxBytes = kTile * 128;
+struct Fwd : Tile<kD> {
+  static constexpr int kSlots = 4, kTileBytes = Tile<kD>::kBytes;
   static constexpr int kThreads = 320;  // warps 0-3 and 4-7: a unit's rows each; 8: copies; 9: products
   static constexpr int kSmem = (2 + kSlots) * kTileBytes + 1024 + 256;
-  static constexpr uint32_t kCols = 512;
-  static constexpr uint32_t kScores = 0, kOut = 256;  // of the first unit; the second's are kTile columns behind
+  static constexpr uint32_t kScores = 0, kOut = 256;  // columns of the first unit; the second's are kTile behind
 };
 
 // How many tiles of keys the unit's rows meet, and where the unit lies.
@@ -187,6 +227,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* ring = smem + 2 * F::kTileBytes;
+  const uint32_t base = (smem_u32(smem_raw) + 1023) & ~1023u, ring_at = base + 2 * F::kTileBytes;
   uint64_t* q_full = reinterpret_cast<uint64_t*>(ring + F::kSlots * F::kTileBytes);
   uint64_t* full = q_full + 1;
   uint64_t* empty = full + F::kSlots;
@@ -199,7 +240,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -216,7 +257,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   if (warp == 9) {
     const Place found = find_place(p, blockIdx.x / p.kv_heads, [&](int64_t len) { return ((len + kTile - 1) / kTile * group + 1) / 2; });
     if (lane == 0) place = found;
-    if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
+    if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
   zero_rows_outside(p, p.out, p.heads, p.lse);
   tc_fence_before();
@@ -224,7 +265,6 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
   if (length == 0) return;
-  const uint32_t tmem = *tmem_slot;
   const Unit units[2] = {unit_at(p, length, 2 * place.piece, kv), unit_at(p, length, 2 * place.piece + 1, kv)};
   const int tiles = max(units[0].tiles, units[1].tiles);
   // Of the last tile's values the rows behind the sequence are someone else's: whatever they hold meets probabilities of
@@ -241,18 +281,15 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
       const int present = units[1].tiles > 0 ? 2 : 1;
       mbar_arrive_expect_tx(q_full, present * F::kTileBytes);
       for (int j = 0; j < present; ++j)
-        for (int b = 0; b < F::kBoxes; ++b)
-          tma_load_3d(smem_u32(smem + j * F::kTileBytes + b * F::kBoxBytes), &p.map_q, b * 64, units[j].head,
-                      static_cast<int>(begin + units[j].row), q_full);
+        load_tile<kD>(base + j * F::kTileBytes, &p.map_q, units[j].head, begin + units[j].row, q_full);
       for (int t = 0; ok && t < 2 * tiles; ++t) {  // keys and values of a tile in turn
         if (!wait_fast(&empty[slot], phase ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
         mbar_arrive_expect_tx(&full[slot], F::kTileBytes);
-        for (int b = 0; b < F::kBoxes; ++b)
-          tma_load_3d(smem_u32(ring + slot * F::kTileBytes + b * F::kBoxBytes), t & 1 ? &p.map_v : &p.map_k, b * 64, kv,
-                      static_cast<int>(begin + static_cast<int64_t>(t >> 1) * kTile), &full[slot]);
+        load_tile<kD>(ring_at + slot * F::kTileBytes, t & 1 ? &p.map_v : &p.map_k, kv,
+                      begin + static_cast<int64_t>(t >> 1) * kTile, &full[slot]);
         issued |= 1u << slot;
         parity = (parity & ~(1u << slot)) | (phase << slot);
         if (++slot == F::kSlots) slot = 0, phase ^= 1u;
@@ -280,61 +317,62 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t qk_desc = instr_desc_bf16<kTile, kTile>(false), pv_desc = instr_desc_bf16<kTile, kD>(true);
-      int slot = 0;
-      uint32_t phase = 0;
-      auto next = [&] {
-        if (++slot == F::kSlots) slot = 0, phase ^= 1u;
-      };
-      auto wait = [&](uint64_t* bar, uint32_t ph) { return wait_fast(bar, ph, abort_flag, p.status); };
-      auto scores = [&](int j, int key_slot) {
-        const uint32_t q = smem_u32(smem + j * F::kTileBytes), k = smem_u32(ring + key_slot * F::kTileBytes);
-#pragma unroll
-        for (int s = 0; s < kD / 16; ++s) {
-          const uint32_t off = (s >> 2) * F::kBoxBytes + (s & 3) * 32;
-          mma_f16(tmem + F::kScores + j * kTile, smem_desc(q + off, 16, 1024), smem_desc(k + off, 16, 1024), qk_desc, s > 0);
-        }
+    const int counts[2] = {__shfl_sync(0xffffffffu, units[0].tiles, 0), __shfl_sync(0xffffffffu, units[1].tiles, 0)};
+    const int n = max(counts[0], counts[1]);
+    const bool cut = __any_sync(0xffffffffu, patch);
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return __all_sync(0xffffffffu, wait_fast(bar, ph, abort_flag, p.status)) != 0;
+    };
+    auto scores = [&](int j, int key_slot) {
+      if (elect_one()) {
+        mma_rows<kD>(F::kScores + j * kTile, base + j * F::kTileBytes, ring_at + key_slot * F::kTileBytes);
         mma_commit(&s_full[j]);
-      };
-      bool ok = wait(q_full, 0) && wait(&full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        for (int j = 0; j < 2; ++j)
-          if (units[j].tiles > 0) scores(j, 0);
-        mma_commit(&empty[0]);
-        next();
       }
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int v_slot = slot;
-        ok = wait(&full[v_slot], phase);
-        if (ok && patch && i + 1 == tiles) ok = wait(patched, 0);
-        next();
-        const int k_slot = slot;
-        const uint32_t k_phase = phase;
-        if (i + 1 < tiles) next();
-        bool have_keys = false;
-        for (int j = 0; ok && j < 2; ++j) {
-          if (i < units[j].tiles) {
-            if (!(ok = wait(&p_full[j], i & 1))) break;
-            tc_fence_after();
-            const uint32_t v = smem_u32(ring + v_slot * F::kTileBytes);
+      __syncwarp();
+    };
+    int slot = 0;
+    uint32_t phase = 0;
+    auto next = [&] {
+      if (++slot == F::kSlots) slot = 0, phase ^= 1u;
+    };
+    bool ok = wait(q_full, 0) && wait(&full[0], 0);
+    if (ok) {
+      tc_fence_after();
 #pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              mma_tmem_a(tmem + F::kOut + j * kTile, tmem + F::kScores + j * kTile + s * 8,
-                         smem_desc(v + s * 2048, F::kBoxBytes, 1024), pv_desc, i > 0 || s > 0);
-            if (i + 1 == units[j].tiles) mma_commit(&o_full[j]);
-          }
-          if (j == 1) mma_commit(&empty[v_slot]);
-          if (i + 1 < units[j].tiles) {
-            if (!have_keys && !(ok = wait(&full[k_slot], k_phase))) break;
-            have_keys = true;
-            tc_fence_after();
-            scores(j, k_slot);
-          }
-        }
-        if (ok && i + 1 < tiles) mma_commit(&empty[k_slot]);
+      for (int j = 0; j < 2; ++j)
+        if (counts[j] > 0) scores(j, 0);
+      if (elect_one()) mma_commit(&empty[0]);
+      next();
+    }
+    for (int i = 0; ok && i < n; ++i) {
+      const int v_slot = slot;
+      ok = wait(&full[v_slot], phase) && (!cut || i + 1 < n || wait(patched, 0));
+      next();
+      const int k_slot = slot;
+      const uint32_t k_phase = phase;
+      if (ok && i + 1 < n) {
+        ok = wait(&full[k_slot], k_phase);
+        next();
       }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (ok && i < counts[j]) {
+          ok = wait(&p_full[j], i & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            mma_columns<kD>(F::kOut + j * kTile, F::kScores + j * kTile, kTile / 4, ring_at + v_slot * F::kTileBytes, i > 0);
+            if (i + 1 == counts[j]) mma_commit(&o_full[j]);
+          }
+          __syncwarp();
+        }
+        if (j == 1 && ok && elect_one()) mma_commit(&empty[v_slot]);
+        __syncwarp();
+        if (ok && i + 1 < counts[j]) scores(j, k_slot);
+      }
+      if (ok && i + 1 < n && elect_one()) mma_commit(&empty[k_slot]);
+      __syncwarp();
+    }
+    if (elect_one()) {
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
@@ -343,7 +381,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
     const int j = warp >> 2, r = (warp & 3) * 32 + lane;
     const Unit u = units[j];
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + F::kScores + j * kTile, t_o = tmem + lanes + F::kOut + j * kTile;
+    const uint32_t t_s = lanes + F::kScores + j * kTile, t_o = lanes + F::kOut + j * kTile;
     const float sl2 = p.scale_log2;
     const bool negative = p.scale < 0.f;
     float top = -INFINITY;  // the maximum in use
@@ -446,7 +484,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, F::kCols);
+  if (warp == 9) tmem_dealloc(0, kCols);
 }
 
 // ---------------------------------------------------------------------------- backward
@@ -470,52 +508,20 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
 constexpr int kHalf = 64;
 
 template <int kD>
-struct Bwd {
-  static constexpr int kTileBytes = kTile * kD * 2;
-  static constexpr int kBoxes = kD / 64, kBoxBytes = kTile * 128;
+struct Bwd : Tile<kD> {
+  static constexpr int kTileBytes = Tile<kD>::kBytes;
   static constexpr int kThreads = 352;  // warps 0-7: rows; 8: copies; 9: products; 10: what the rows need beside them
-  static constexpr uint32_t kCols = 512;
   static constexpr int kKeySlots = 3, kValueSlots = 2;
   static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 1024 + 256 + 1024;
   static constexpr int kSmemKeys = 6 * kTileBytes + 4 * kTile * 4 + 256 + 1024;
 };
 
-// One thread's copies of a tile: `row` is the first token's index in the arrays.
-template <int kD>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, int head, int64_t row, uint64_t* bar) {
-#pragma unroll
-  for (int b = 0; b < Bwd<kD>::kBoxes; ++b)
-    tma_load_3d(smem_u32(dst + b * Bwd<kD>::kBoxBytes), map, b * 64, head, static_cast<int>(row), bar);
-}
-
-// D = A B^T of two tiles (rows of kD columns).
-template <int kD>
-__device__ __forceinline__ void mma_rows(uint32_t d, const uint8_t* a, const uint8_t* b) {
-  constexpr uint32_t desc = (1u << 4) | (1u << 7) | (1u << 10) | ((kTile >> 3) << 17) | ((kTile >> 4) << 24);
-  const uint32_t a0 = smem_u32(a), b0 = smem_u32(b);
-#pragma unroll
-  for (int s = 0; s < kD / 16; ++s) {
-    const uint32_t off = (s >> 2) * Bwd<kD>::kBoxBytes + (s & 3) * 32;
-    mma_f16(d, smem_desc(a0 + off, 16, 1024), smem_desc(b0 + off, 16, 1024), desc, s > 0);
-  }
-}
-
-// D (+)= A B, with A (bf16) in tensor memory: the first 64 of its 128 columns in 32 from `a` on, the others in 32 from a
-// + 64 on, each half where the half row of scores was that it was made from.
-template <int kD>
-__device__ __forceinline__ void mma_halves(uint32_t d, uint32_t a, const uint8_t* b, bool add) {
-  const uint32_t desc = instr_desc_bf16<kTile, kD>(true), b0 = smem_u32(b);
-#pragma unroll
-  for (int s = 0; s < kTile / 16; ++s)
-    mma_tmem_a(d, a + (s >> 2) * kHalf + (s & 3) * 8, smem_desc(b0 + s * 2048, Bwd<kD>::kBoxBytes, 1024), desc, add || s > 0);
-}
-
 // Zeros in the rows from `valid` on of a tile in shared memory, by a warp, visible to the products.
 template <int kD>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
-  for (int b = 0; b < Bwd<kD>::kBoxes; ++b)
+  for (int b = 0; b < Tile<kD>::kBoxes; ++b)
     for (int i = valid * 8 + (threadIdx.x & 31); i < kTile * 8; i += 32)
-      *reinterpret_cast<uint4*>(tile + b * Bwd<kD>::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(tile + b * Tile<kD>::kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
 }
 
@@ -548,8 +554,9 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   using F = Bwd<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *q_tile = smem, *do_tile = q_tile + F::kTileBytes, *keys = do_tile + F::kTileBytes,
-          *values = keys + F::kKeySlots * F::kTileBytes;
+  uint8_t *keys = smem + 2 * F::kTileBytes, *values = keys + F::kKeySlots * F::kTileBytes;  // behind queries and dout
+  const uint32_t q_at = (smem_u32(smem_raw) + 1023) & ~1023u, do_at = q_at + F::kTileBytes, keys_at = do_at + F::kTileBytes,
+                 values_at = keys_at + F::kKeySlots * F::kTileBytes;
   float* exchange = reinterpret_cast<float*>(values + F::kValueSlots * F::kTileBytes);  // 2 x 128
   uint64_t* q_full = reinterpret_cast<uint64_t*>(exchange + 2 * kTile);
   uint64_t* k_full = q_full + 1;
@@ -568,7 +575,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -584,7 +591,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   if (warp == 9) {
     const Place found = find_place(p, blockIdx.x / p.heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
     if (lane == 0) place = found;
-    if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
+    if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
   zero_rows_outside(p, p.dq, p.heads, nullptr);
   tc_fence_before();
@@ -592,7 +599,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
   if (length == 0) return;
-  const uint32_t tmem = *tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dq = tmem + 3 * kTile;
+  constexpr uint32_t t_s = 0, t_dp = kTile, t_dq = 3 * kTile;
   const int64_t blocks = (length + kTile - 1) / kTile, block = blocks - 1 - place.piece, row0 = block * kTile;  // long rows first
   const int tiles = static_cast<int>(p.causal ? block + 1 : blocks);
   const bool patch = static_cast<int64_t>(tiles) * kTile > length;
@@ -604,20 +611,20 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     int i = 0, loaded_v = 0;
     if (lane == 0) {
       mbar_arrive_expect_tx(q_full, 2 * F::kTileBytes);
-      load_tile<kD>(q_tile, &p.map_q, head, begin + row0, q_full);
-      load_tile<kD>(do_tile, &p.map_dout, head, begin + row0, q_full);
+      load_tile<kD>(q_at, &p.map_q, head, begin + row0, q_full);
+      load_tile<kD>(do_at, &p.map_dout, head, begin + row0, q_full);
       for (; i < tiles; ++i) {
         const int64_t row = begin + static_cast<int64_t>(i) * kTile;
         const int ks = i % F::kKeySlots, vs = i % F::kValueSlots;
         if (!(ok = wait(&k_empty[ks], i / F::kKeySlots + 1))) break;
         mbar_arrive_expect_tx(&k_full[ks], F::kTileBytes);
-        load_tile<kD>(keys + ks * F::kTileBytes, &p.map_k, kv, row, &k_full[ks]);
+        load_tile<kD>(keys_at + ks * F::kTileBytes, &p.map_k, kv, row, &k_full[ks]);
         if (!(ok = wait(&v_empty[vs], i / F::kValueSlots + 1))) {
           ++i;
           break;
         }
         mbar_arrive_expect_tx(&v_full[vs], F::kTileBytes);
-        load_tile<kD>(values + vs * F::kTileBytes, &p.map_v, kv, row, &v_full[vs]);
+        load_tile<kD>(values_at + vs * F::kTileBytes, &p.map_v, kv, row, &v_full[vs]);
         ++loaded_v;
       }
     }
@@ -640,35 +647,50 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      auto scores = [&](int i) {
-        const int ks = i % F::kKeySlots;
-        if (!wait(&k_full[ks], i / F::kKeySlots)) return false;
-        if (patch && i + 1 == tiles && !wait(patched, 0)) return false;
-        if (i > 0 && !wait(s_read, i - 1)) return false;
-        tc_fence_after();
-        mma_rows<kD>(t_s, q_tile, keys + ks * F::kTileBytes);
+    const int n = __shfl_sync(0xffffffffu, tiles, 0);
+    const bool cut = __any_sync(0xffffffffu, patch);
+    auto all_wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+    int ks = 0, vs = 0, dqs = 0;  // slots of the next scores, dout . v and dq
+    uint32_t k_phase = 0, v_phase = 0;
+    auto scores = [&](int i) {
+      if (!all_wait(&k_full[ks], k_phase) || (cut && i + 1 == n && !all_wait(patched, 0)) || (i > 0 && !all_wait(s_read, i - 1)))
+        return false;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_rows<kD>(t_s, q_at, keys_at + ks * F::kTileBytes);
         mma_commit(s_full);
-        return true;
-      };
-      auto along = [&](int i) {
-        const int vs = i % F::kValueSlots;
-        if (!wait(&v_full[vs], i / F::kValueSlots)) return false;
-        tc_fence_after();
-        mma_rows<kD>(t_dp + (i & 1) * kTile, do_tile, values + vs * F::kTileBytes);
+      }
+      __syncwarp();
+      if (++ks == F::kKeySlots) ks = 0, k_phase ^= 1u;
+      return true;
+    };
+    auto along = [&](int i) {
+      if (!all_wait(&v_full[vs], v_phase)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_rows<kD>(t_dp + (i & 1) * kTile, do_at, values_at + vs * F::kTileBytes);
         mma_commit(&v_empty[vs]);
         mma_commit(&dp_full[i & 1]);
-        return true;
-      };
-      bool ok = wait(q_full, 0) && scores(0) && along(0);
-      for (int i = 0; ok && i < tiles; ++i) {
-        if (i + 1 < tiles) ok = scores(i + 1) && along(i + 1);
-        if (!ok || !(ok = wait(&ds_full[i & 1], i >> 1))) break;
-        tc_fence_after();
-        mma_halves<kD>(t_dq, t_dp + (i & 1) * kTile, keys + (i % F::kKeySlots) * F::kTileBytes, i > 0);
-        mma_commit(&k_empty[i % F::kKeySlots]);
       }
-      if (ok) mma_commit(done);
+      __syncwarp();
+      if (++vs == F::kValueSlots) vs = 0, v_phase ^= 1u;
+      return true;
+    };
+    bool ok = all_wait(q_full, 0) && scores(0) && along(0);
+    for (int i = 0; ok && i < n; ++i) {
+      if (i + 1 < n) ok = scores(i + 1) && along(i + 1);
+      ok = ok && all_wait(&ds_full[i & 1], i >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_columns<kD>(t_dq, t_dp + (i & 1) * kTile, kHalf, keys_at + dqs * F::kTileBytes, i > 0);
+        mma_commit(&k_empty[dqs]);
+        if (i + 1 == n) mma_commit(done);
+      }
+      __syncwarp();
+      if (++dqs == F::kKeySlots) dqs = 0;
+    }
+    if (elect_one()) {
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
@@ -690,7 +712,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
         for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
       }
     }
-    float rest = 0.f;  // sum of ds
+    float2 rest = make_float2(0.f, 0.f);  // sum of ds, in two parts
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
       ok = __all_sync(0xffffffffu, wait(s_full, i));
@@ -743,7 +765,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
             ds.x = c + k < here ? ds.x : 0.f;
             ds.y = c + k + 1 < here ? ds.y : 0.f;
           }
-          rest += ds.x + ds.y;
+          rest = add2(rest, ds);
           half[k / 2] = pack_bf16(ds.x, ds.y);
         }
         tmem_st16(t + c / 2, half);  // over columns that have been read
@@ -755,7 +777,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     }
     if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
     if (ok && tiles > 1) {
-      exchange[side * kTile + r] = rest;
+      exchange[side * kTile + r] = rest.x + rest.y;
       __syncwarp();
       if (lane == 0) mbar_arrive(exchanged);
       ok = __all_sync(0xffffffffu, wait(exchanged, 0));
@@ -774,7 +796,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, F::kCols);
+  if (warp == 9) tmem_dealloc(0, kCols);
 }
 
 template <int kD>
@@ -782,8 +804,9 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   using F = Bwd<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *k_tile = smem, *v_tile = k_tile + F::kTileBytes, *queries = v_tile + F::kTileBytes,
-          *douts = queries + 2 * F::kTileBytes;
+  uint8_t *queries = smem + 2 * F::kTileBytes, *douts = queries + 2 * F::kTileBytes;  // behind keys and values
+  const uint32_t k_at = (smem_u32(smem_raw) + 1023) & ~1023u, v_at = k_at + F::kTileBytes, queries_at = v_at + F::kTileBytes,
+                 douts_at = queries_at + 2 * F::kTileBytes;
   float* stats = reinterpret_cast<float*>(douts + 2 * F::kTileBytes);  // two stages of lse log2(e), D
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * kTile);
   uint64_t* q_full = kv_full + 1;
@@ -803,7 +826,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -820,7 +843,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   if (warp == 9) {
     const Place found = find_place(p, blockIdx.x / p.kv_heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
     if (lane == 0) place = found;
-    if (found.length > 0) tmem_alloc(tmem_slot, F::kCols);
+    if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
   zero_rows_outside(p, p.dk, p.kv_heads, nullptr);
   zero_rows_outside(p, p.dv, p.kv_heads, nullptr);
@@ -829,7 +852,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
   if (length == 0) return;
-  const uint32_t tmem = *tmem_slot, t_s = tmem, t_dp = tmem + kTile, t_dv = tmem + 2 * kTile, t_dk = tmem + 3 * kTile;
+  constexpr uint32_t t_s = 0, t_dp = kTile, t_dv = 2 * kTile, t_dk = 3 * kTile;
   const int64_t blocks = (length + kTile - 1) / kTile, key0 = place.piece * kTile, first = p.causal ? place.piece : 0;
   const int per_head = static_cast<int>(blocks - first);  // tiles of queries
   const int64_t tiles = static_cast<int64_t>(per_head) * group;
@@ -840,8 +863,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
       mbar_arrive_expect_tx(kv_full, 2 * F::kTileBytes);
-      load_tile<kD>(k_tile, &p.map_k, kv, begin + key0, kv_full);
-      load_tile<kD>(v_tile, &p.map_v, kv, begin + key0, kv_full);
+      load_tile<kD>(k_at, &p.map_k, kv, begin + key0, kv_full);
+      load_tile<kD>(v_at, &p.map_v, kv, begin + key0, kv_full);
       int64_t i = 0, loaded_do = 0;
       bool ok = true;
       for (int h = 0, b = 0; i < tiles; ++i) {
@@ -849,13 +872,13 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
         const int64_t row = begin + (first + b) * kTile;
         if (!(ok = wait(&q_empty[s], (i >> 1) + 1))) break;
         mbar_arrive_expect_tx(&q_full[s], F::kTileBytes);
-        load_tile<kD>(queries + s * F::kTileBytes, &p.map_q, kv * group + h, row, &q_full[s]);
+        load_tile<kD>(queries_at + s * F::kTileBytes, &p.map_q, kv * group + h, row, &q_full[s]);
         if (!(ok = wait(&do_empty[s], (i >> 1) + 1))) {
           ++i;
           break;
         }
         mbar_arrive_expect_tx(&do_full[s], F::kTileBytes);
-        load_tile<kD>(douts + s * F::kTileBytes, &p.map_dout, kv * group + h, row, &do_full[s]);
+        load_tile<kD>(douts_at + s * F::kTileBytes, &p.map_dout, kv * group + h, row, &do_full[s]);
         ++loaded_do;
         if (++b == per_head) b = 0, ++h;
       }
@@ -869,40 +892,63 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ products
-    if (lane == 0) {
-      int patches = 0, left = per_head;  // tiles of queries to come of the head whose scores are formed next
-      auto scores = [&](int64_t i) {
-        if (!wait(&q_full[i & 1], i >> 1)) return false;
-        if (--left == 0) {
-          left = per_head;
-          if (ragged && !wait(patched, patches++)) return false;
-        }
-        tc_fence_after();
-        mma_rows<kD>(t_s, k_tile, queries + (i & 1) * F::kTileBytes);
-        mma_commit(s_full);
-        return true;
-      };
-      auto along = [&](int64_t i) {
-        if (!wait(&do_full[i & 1], i >> 1)) return false;
-        tc_fence_after();
-        mma_rows<kD>(t_dp, v_tile, douts + (i & 1) * F::kTileBytes);
-        mma_commit(dp_full);
-        return true;
-      };
-      bool ok = wait(kv_full, 0) && scores(0) && along(0);
-      for (int64_t i = 0; ok && i < tiles; ++i) {
-        if (!(ok = wait(p_full, i))) break;
-        tc_fence_after();
-        mma_halves<kD>(t_dv, t_s, douts + (i & 1) * F::kTileBytes, i > 0);
-        mma_commit(&do_empty[i & 1]);
-        if (i + 1 < tiles && !(ok = scores(i + 1))) break;
-        if (!(ok = wait(ds_full, i))) break;
-        tc_fence_after();
-        mma_halves<kD>(t_dk, t_dp, queries + (i & 1) * F::kTileBytes, i > 0);
-        mma_commit(&q_empty[i & 1]);
-        if (i + 1 < tiles) ok = along(i + 1);
+    const int each = __shfl_sync(0xffffffffu, per_head, 0);
+    const int64_t n = static_cast<int64_t>(each) * group;
+    const bool cut = __any_sync(0xffffffffu, ragged);
+    auto all_wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+    int left = each;  // tiles of queries to come of the head whose scores are formed next
+    uint32_t patches = 0;
+    auto scores = [&](int s, uint32_t phase) {
+      bool there = all_wait(&q_full[s], phase);
+      if (--left == 0) {
+        left = each;
+        if (cut) there = there && all_wait(patched, patches++);
       }
-      if (ok) mma_commit(done);
+      if (!there) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
+        mma_commit(s_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    auto along = [&](int s, uint32_t phase) {
+      if (!all_wait(&do_full[s], phase)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
+        mma_commit(dp_full);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = all_wait(kv_full, 0) && scores(0, 0) && along(0, 0);
+    int s = 0;
+    uint32_t phase = 0, turn = 0;  // of the slot, of the rows' barriers
+    for (int64_t i = 0; ok && i < n; ++i) {
+      const int s1 = s ^ 1;
+      const uint32_t phase1 = s1 == 0 ? phase ^ 1u : phase;
+      if (!(ok = all_wait(p_full, turn))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_columns<kD>(t_dv, t_s, kHalf, douts_at + s * F::kTileBytes, i > 0);
+        mma_commit(&do_empty[s]);
+      }
+      __syncwarp();
+      if (i + 1 < n && !(ok = scores(s1, phase1))) break;
+      if (!(ok = all_wait(ds_full, turn))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        mma_columns<kD>(t_dk, t_dp, kHalf, queries_at + s * F::kTileBytes, i > 0);
+        mma_commit(&q_empty[s]);
+        if (i + 1 == n) mma_commit(done);
+      }
+      __syncwarp();
+      if (i + 1 < n) ok = along(s1, phase1);
+      s = s1, phase = phase1, turn ^= 1u;
+    }
+    if (elect_one()) {
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
@@ -1020,7 +1066,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, F::kCols);
+  if (warp == 9) tmem_dealloc(0, kCols);
 }
 
 // ---------------------------------------------------------------------------- launches

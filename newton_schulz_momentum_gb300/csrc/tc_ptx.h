@@ -130,6 +130,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t mbar_cluster_addr) 
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mbar_cluster_addr) : "memory");
 }
 
+// True in one lane of a warp whose lanes are all here, the same one every time. Products that one lane issues in code
+// that the whole warp runs, with addresses that are the warp's, keep their operands in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
