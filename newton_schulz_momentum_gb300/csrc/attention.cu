@@ -206,17 +206,17 @@ __device__ __forceinline__ Unit unit_at(const AttentionLaunch& p, int64_t length
   return {static_cast<int>(kv * group + unit - back * group), static_cast<int>(p.causal ? block + 1 : blocks), block * kTile};
 }
 
-// A row of outputs times f.
+// A row of outputs times f; seldom run, so a few columns at a time beside the 128 scores that the thread holds.
 template <int kD>
 __device__ __forceinline__ void scale_outputs(uint32_t tmem_out, float f) {
-#pragma unroll
-  for (int c = 0; c < kD; c += 32) {
-    uint32_t r[32];
-    tmem_ld32_issue(tmem_out + c, r);
+#pragma unroll 1
+  for (int c = 0; c < kD; c += 8) {
+    uint32_t r[8];
+    tmem_ld8_issue(tmem_out + c, r);
     tmem_ld_wait(r);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
-    tmem_st32(tmem_out + c, r);
+    for (int k = 0; k < 8; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
+    tmem_st8(tmem_out + c, r);
   }
   tmem_st_wait();
 }
@@ -396,32 +396,26 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
       const int64_t key0 = static_cast<int64_t>(i) * kTile;
       const bool masked = (p.causal && key0 == u.row) || key0 + kTile > length;
       const int keys = masked ? static_cast<int>((p.causal && u.row + r < length ? u.row + r + 1 : length) - key0) : kTile;
-      uint32_t x[2][32];
-      auto scores_of = [&](uint32_t (&v)[32], int c) {  // chunk c of the row, which has arrived
-        if (negative) {
+      // All 128 scores in registers at once: a wait for tensor memory is one for all loads under way, so pieces of a row
+      // would each take its latency.
+      uint32_t x[kTile];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] ^= 0x80000000u;
-        }
-        if (masked) {
+      for (int c = 0; c < kTile; c += 32) tmem_ld32_issue(t_s + c, x + c);
+      tmem_ld_wait(x);
+      if (negative) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = c * 32 + e < keys ? v[e] : 0xff800000u;
-        }
-      };
-      // The scores are read twice, a quarter of a row at a time and the next one under way: 128 of them and their
-      // probabilities are more registers than a thread has.
-      float m4[4] = {top, top, top, top};
-      tmem_ld32_issue(t_s, x[0]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld_wait(x[c & 1]);
-        if (c < 3) tmem_ld32_issue(t_s + (c + 1) * 32, x[(c + 1) & 1]);
-        scores_of(x[c & 1], c);
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(x[c & 1][e + 2 * q]), __uint_as_float(x[c & 1][e + 2 * q + 1])));
+        for (int c = 0; c < kTile; ++c) x[c] ^= 0x80000000u;
       }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < kTile; ++c) x[c] = c < keys ? x[c] : 0xff800000u;
+      }
+      float m4[4] = {top, top, top, top};
+#pragma unroll
+      for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(x[c + 2 * q]), __uint_as_float(x[c + 2 * q + 1])));
       const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       if (__any_sync(0xffffffffu, (m - top) * sl2 > kRaise)) {
         const float f = top == m ? 1.f : pow2((top - m) * sl2);
@@ -430,23 +424,18 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
         if (i > 0) scale_outputs<kD>(t_o, f);
       }
       const float shift = top == -INFINITY ? 0.f : -top * sl2;
-      tmem_ld32_issue(t_s, x[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld_wait(x[c & 1]);
-        if (c < 3) tmem_ld32_issue(t_s + (c + 1) * 32, x[(c + 1) & 1]);
-        scores_of(x[c & 1], c);
-        uint32_t half[16];
+      for (int c = 0; c < kTile; c += 16) {
+        uint32_t half[8];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float2 y = fma2(make_float2(__uint_as_float(x[c & 1][e]), __uint_as_float(x[c & 1][e + 1])), make_float2(sl2, sl2),
+        for (int e = 0; e < 16; e += 2) {
+          float2 y = fma2(make_float2(__uint_as_float(x[c + e]), __uint_as_float(x[c + e + 1])), make_float2(sl2, sl2),
                           make_float2(shift, shift));
           y = make_float2(pow2(y.x), pow2(y.y));
           sum = add2(sum, y);
           half[e / 2] = pack_bf16(y.x, y.y);
         }
-        // Over columns that have been read: probabilities take half of their scores' place, from its start on.
-        tmem_st16(t_s + c * 16, half);
+        tmem_st8(t_s + c / 2, half);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -739,10 +728,11 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       if (!ok) break;
       tc_fence_after();
       const uint32_t t = t_dp + (i & 1) * kTile + lanes + side * kHalf;
+      float dp[kHalf];
+      load_half(t, dp);
       if (tiles == 1) {
         // All keys of these rows are at hand: the whole D before the first ds.
-        float dp[kHalf], sum = 0.f;
-        load_half(t, dp);
+        float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kHalf; ++k) sum += k < here ? prob[k] * (dp[k] - delta) : 0.f;
         exchange[side * kTile + r] = sum;
@@ -753,13 +743,11 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
         delta += exchange[r] + exchange[kTile + r];
       }
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t dp[32], half[16];
-        tmem_ld32_issue(t + c, dp);
-        tmem_ld_wait(dp);
+      for (int c = 0; c < kHalf; c += 16) {
+        uint32_t half[8];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-          float2 ds = add2(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), make_float2(-delta, -delta));
+        for (int k = 0; k < 16; k += 2) {
+          float2 ds = add2(make_float2(dp[c + k], dp[c + k + 1]), make_float2(-delta, -delta));
           ds = mul2(ds, make_float2(prob[c + k], prob[c + k + 1]));
           if (masked) {  // 0 whatever dout . v is there
             ds.x = c + k < here ? ds.x : 0.f;
@@ -768,7 +756,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
           rest = add2(rest, ds);
           half[k / 2] = pack_bf16(ds.x, ds.y);
         }
-        tmem_st16(t + c / 2, half);  // over columns that have been read
+        tmem_st8(t + c / 2, half);  // over columns that have been read
       }
       tmem_st_wait();
       tc_fence_before();
@@ -1025,16 +1013,16 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       if (!ok) break;
       tc_fence_after();
       const uint32_t t = t_dp + lanes + side * kHalf;
+      float dp[kHalf];
+      load_half(t, dp);
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t dp[32], half[16];
-        tmem_ld32_issue(t + c, dp);
-        tmem_ld_wait(dp);
+      for (int c = 0; c < kHalf; c += 16) {
+        uint32_t half[8];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
+        for (int k = 0; k < 16; k += 4) {
           const float4 d = *reinterpret_cast<const float4*>(delta + c + k);
-          float2 a = add2(make_float2(__uint_as_float(dp[k]), __uint_as_float(dp[k + 1])), make_float2(-d.x, -d.y));
-          float2 b = add2(make_float2(__uint_as_float(dp[k + 2]), __uint_as_float(dp[k + 3])), make_float2(-d.z, -d.w));
+          float2 a = add2(make_float2(dp[c + k], dp[c + k + 1]), make_float2(-d.x, -d.y));
+          float2 b = add2(make_float2(dp[c + k + 2], dp[c + k + 3]), make_float2(-d.z, -d.w));
           a = mul2(a, make_float2(prob[c + k], prob[c + k + 1]));
           b = mul2(b, make_float2(prob[c + k + 2], prob[c + k + 3]));
           if (diagonal) {  // 0 whatever dout . v is there
@@ -1044,7 +1032,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
           half[k / 2] = pack_bf16(a.x, a.y);
           half[k / 2 + 1] = pack_bf16(b.x, b.y);
         }
-        tmem_st16(t + c / 2, half);
+        tmem_st8(t + c / 2, half);
       }
       tmem_st_wait();
       tc_fence_before();
