@@ -158,30 +158,64 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     tma_load_3d(dst + b * Tile<kD>::kBoxBytes, map, b * 64, head, static_cast<int>(row), bar);
 }
 
-// The products below are issued by one lane of a warp that runs them as a whole, with addresses of tiles in shared
-// memory and of columns that are the warp's: operands that have to be brought into uniform registers first take longer
-// than the products (128 x 128 x 16: 150 cycles of issue, 68 like this, 64 for the product).
+// The products of a tile are issued by one lane of a warp that is here as a whole, all of them in one statement: operands
+// that are brought together for one product after another, under a branch, take longer than the products (eight of
+// 128 x 128 x 16 from an idle start: 520 cycles of issue by lane 0, 340 under an elected lane's branch, 104 like this,
+// 512 for the products themselves). Offsets are in 16-byte units of a descriptor's low word.
+#define DM_SS(step, off, add)                                                                                          \
+  "add.u32 l, %1, " off ";\n\tmov.b64 a, {l, %3};\n\tadd.u32 l, %2, " off ";\n\tmov.b64 b, {l, %3};\n\t"              \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, " add ";\n\t"
+#define DM_TS(step, a_off, b_off)                                                                                      \
+  "add.u32 t, %1, " a_off ";\n\tadd.u32 l, %2, " b_off ";\n\tmov.b64 b, {l, %3};\n\t"                                  \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %4, " step ";\n\t"
+#define DM_ELECT                                                                                                       \
+  "{\n\t.reg .pred e, f, p, q;\n\t.reg .b64 a, b;\n\t.reg .b32 l, t;\n\telect.sync _|e, 0xffffffff;\n\t"              \
+  "setp.ne.u32 f, 0, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
 
 // D = A B^T of two tiles.
 template <int kD>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  static_assert(Tile<kD>::kBoxBytes >> 4 == 1024, "offsets of the second box");
   const uint32_t desc = instr_desc_bf16<kTile, kTile>(false);
-#pragma unroll
-  for (int s = 0; s < kD / 16; ++s) {
-    const uint32_t off = (s >> 2) * Tile<kD>::kBoxBytes + (s & 3) * 32;
-    mma_f16(d, smem_desc(a + off, 16, 1024), smem_desc(b + off, 16, 1024), desc, s > 0);
+  const uint64_t da = smem_desc(a, 16, 1024), db = smem_desc(b, 16, 1024);
+  const uint32_t al = static_cast<uint32_t>(da), bl = static_cast<uint32_t>(db), high = static_cast<uint32_t>(db >> 32);
+  if constexpr (kD == 64) {
+    asm volatile(DM_ELECT DM_SS(0, "0", "f") DM_SS(1, "2", "q") DM_SS(2, "4", "q") DM_SS(3, "6", "q") "}\n" ::"r"(d),
+                 "r"(al), "r"(bl), "r"(high), "r"(desc)
+                 : "memory");
+  } else {
+    asm volatile(DM_ELECT DM_SS(0, "0", "f") DM_SS(1, "2", "q") DM_SS(2, "4", "q") DM_SS(3, "6", "q")
+                     DM_SS(4, "1024", "q") DM_SS(5, "1026", "q") DM_SS(6, "1028", "q") DM_SS(7, "1030", "q") "}\n" ::"r"(d),
+                 "r"(al), "r"(bl), "r"(high), "r"(desc)
+                 : "memory");
   }
 }
 
 // D (+)= A B, A being 128 x 128 bf16 in tensor memory, two of its columns in one: the first 64 from `a` on, the others
-// `second` columns behind.
-template <int kD>
-__device__ __forceinline__ void mma_columns(uint32_t d, uint32_t a, uint32_t second, uint32_t b, bool add) {
+// kSecond columns behind.
+template <int kD, int kSecond>
+__device__ __forceinline__ void mma_columns(uint32_t d, uint32_t a, uint32_t b, bool add) {
   const uint32_t desc = instr_desc_bf16<kTile, kD>(true);
-#pragma unroll
-  for (int s = 0; s < kTile / 16; ++s)
-    mma_tmem_a(d, a + (s >> 2) * second + (s & 3) * 8, smem_desc(b + s * 2048, Tile<kD>::kBoxBytes, 1024), desc, add || s > 0);
+  const uint64_t db = smem_desc(b, Tile<kD>::kBoxBytes, 1024);
+  const uint32_t bl = static_cast<uint32_t>(db), high = static_cast<uint32_t>(db >> 32);
+  static_assert(kSecond == 32 || kSecond == 64, "offsets of the second half");
+  if constexpr (kSecond == 32) {
+    asm volatile(DM_ELECT "setp.ne.u32 p, %5, 0;\n\t" DM_TS("p", "0", "0") DM_TS("q", "8", "128") DM_TS("q", "16", "256")
+                     DM_TS("q", "24", "384") DM_TS("q", "32", "512") DM_TS("q", "40", "640") DM_TS("q", "48", "768")
+                         DM_TS("q", "56", "896") "}\n" ::"r"(d),
+                 "r"(a), "r"(bl), "r"(high), "r"(desc), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+  } else {
+    asm volatile(DM_ELECT "setp.ne.u32 p, %5, 0;\n\t" DM_TS("p", "0", "0") DM_TS("q", "8", "128") DM_TS("q", "16", "256")
+                     DM_TS("q", "24", "384") DM_TS("q", "64", "512") DM_TS("q", "72", "640") DM_TS("q", "80", "768")
+                         DM_TS("q", "88", "896") "}\n" ::"r"(d),
+                 "r"(a), "r"(bl), "r"(high), "r"(desc), "r"(static_cast<uint32_t>(add))
+                 : "memory");
+  }
 }
+#undef DM_SS
+#undef DM_TS
+#undef DM_ELECT
 
 // ---------------------------------------------------------------------------- forward
 
@@ -324,10 +358,8 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
       return __all_sync(0xffffffffu, wait_fast(bar, ph, abort_flag, p.status)) != 0;
     };
     auto scores = [&](int j, int key_slot) {
-      if (elect_one()) {
-        mma_rows<kD>(F::kScores + j * kTile, base + j * F::kTileBytes, ring_at + key_slot * F::kTileBytes);
-        mma_commit(&s_full[j]);
-      }
+      mma_rows<kD>(F::kScores + j * kTile, base + j * F::kTileBytes, ring_at + key_slot * F::kTileBytes);
+      if (elect_one()) mma_commit(&s_full[j]);
       __syncwarp();
     };
     int slot = 0;
@@ -359,11 +391,11 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
         if (ok && i < counts[j]) {
           ok = wait(&p_full[j], i & 1);
           tc_fence_after();
-          if (ok && elect_one()) {
-            mma_columns<kD>(F::kOut + j * kTile, F::kScores + j * kTile, kTile / 4, ring_at + v_slot * F::kTileBytes, i > 0);
-            if (i + 1 == counts[j]) mma_commit(&o_full[j]);
+          if (ok) {
+            mma_columns<kD, kTile / 4>(F::kOut + j * kTile, F::kScores + j * kTile, ring_at + v_slot * F::kTileBytes, i > 0);
+            if (i + 1 == counts[j] && elect_one()) mma_commit(&o_full[j]);
+            __syncwarp();
           }
-          __syncwarp();
         }
         if (j == 1 && ok && elect_one()) mma_commit(&empty[v_slot]);
         __syncwarp();
@@ -645,10 +677,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       if (!all_wait(&k_full[ks], k_phase) || (cut && i + 1 == n && !all_wait(patched, 0)) || (i > 0 && !all_wait(s_read, i - 1)))
         return false;
       tc_fence_after();
-      if (elect_one()) {
-        mma_rows<kD>(t_s, q_at, keys_at + ks * F::kTileBytes);
-        mma_commit(s_full);
-      }
+      mma_rows<kD>(t_s, q_at, keys_at + ks * F::kTileBytes);
+      if (elect_one()) mma_commit(s_full);
       __syncwarp();
       if (++ks == F::kKeySlots) ks = 0, k_phase ^= 1u;
       return true;
@@ -656,8 +686,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     auto along = [&](int i) {
       if (!all_wait(&v_full[vs], v_phase)) return false;
       tc_fence_after();
+      mma_rows<kD>(t_dp + (i & 1) * kTile, do_at, values_at + vs * F::kTileBytes);
       if (elect_one()) {
-        mma_rows<kD>(t_dp + (i & 1) * kTile, do_at, values_at + vs * F::kTileBytes);
         mma_commit(&v_empty[vs]);
         mma_commit(&dp_full[i & 1]);
       }
@@ -671,8 +701,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       ok = ok && all_wait(&ds_full[i & 1], i >> 1);
       if (!ok) break;
       tc_fence_after();
+      mma_columns<kD, kHalf>(t_dq, t_dp + (i & 1) * kTile, keys_at + dqs * F::kTileBytes, i > 0);
       if (elect_one()) {
-        mma_columns<kD>(t_dq, t_dp + (i & 1) * kTile, kHalf, keys_at + dqs * F::kTileBytes, i > 0);
         mma_commit(&k_empty[dqs]);
         if (i + 1 == n) mma_commit(done);
       }
@@ -894,20 +924,16 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       }
       if (!there) return false;
       tc_fence_after();
-      if (elect_one()) {
-        mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
-        mma_commit(s_full);
-      }
+      mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
+      if (elect_one()) mma_commit(s_full);
       __syncwarp();
       return true;
     };
     auto along = [&](int s, uint32_t phase) {
       if (!all_wait(&do_full[s], phase)) return false;
       tc_fence_after();
-      if (elect_one()) {
-        mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
-        mma_commit(dp_full);
-      }
+      mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
+      if (elect_one()) mma_commit(dp_full);
       __syncwarp();
       return true;
     };
@@ -919,16 +945,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       const uint32_t phase1 = s1 == 0 ? phase ^ 1u : phase;
       if (!(ok = all_wait(p_full, turn))) break;
       tc_fence_after();
-      if (elect_one()) {
-        mma_columns<kD>(t_dv, t_s, kHalf, douts_at + s * F::kTileBytes, i > 0);
-        mma_commit(&do_empty[s]);
-      }
+      mma_columns<kD, kHalf>(t_dv, t_s, douts_at + s * F::kTileBytes, i > 0);
+      if (elect_one()) mma_commit(&do_empty[s]);
       __syncwarp();
       if (i + 1 < n && !(ok = scores(s1, phase1))) break;
       if (!(ok = all_wait(ds_full, turn))) break;
       tc_fence_after();
+      mma_columns<kD, kHalf>(t_dk, t_dp, queries_at + s * F::kTileBytes, i > 0);
       if (elect_one()) {
-        mma_columns<kD>(t_dk, t_dp, kHalf, queries_at + s * F::kTileBytes, i > 0);
         mma_commit(&q_empty[s]);
         if (i + 1 == n) mma_commit(done);
       }
