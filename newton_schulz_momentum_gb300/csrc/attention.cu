@@ -966,31 +966,47 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     }
   } else if (warp == 10) {
     // ------------------------------------------------------------------ the queries' lse and D; rows of other sequences
-    int64_t i = 0;
+    // The values of a tile are asked for before its place is free: a wait for memory in the rows' way takes as long as
+    // half of a tile (8192 tokens: 1.91 -> 1.6 ms for both kernels).
     bool ok = true;
-    for (int h = 0; ok && h < group; ++h)
-      for (int b = 0; b < per_head; ++b, ++i) {
-        const int s = static_cast<int>(i & 1);
-        ok = __all_sync(0xffffffffu, wait(&st_empty[s], (i >> 1) + 1));
-        if (!ok) break;
-        const int64_t row = (first + b) * kTile, list = static_cast<int64_t>(kv * group + h) * p.n + begin;
-        for (int k = lane; k < kTile; k += 32) {
-          // A query behind the sequence has p = 2^(0 - infinity) = 0.
-          const bool live = row + k < length;
-          stats[s * 2 * kTile + k] = live ? p.lse[list + row + k] * kLog2e : INFINITY;
-          stats[s * 2 * kTile + kTile + k] = live ? p.delta[list + row + k] : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st_full[s]);
-        if (ragged && b + 1 == per_head) {
-          ok = __all_sync(0xffffffffu, wait(&q_full[s], i >> 1) && wait(&do_full[s], i >> 1));
-          if (!ok) break;
-          clear_rows<kD>(queries + s * F::kTileBytes, static_cast<int>(length - row));
-          clear_rows<kD>(douts + s * F::kTileBytes, static_cast<int>(length - row));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(patched);
-        }
+    float lse2[4], delta[4];
+    int h1 = 0, b1 = 0;  // the next tile
+    auto fetch = [&] {
+      const int64_t row = (first + b1) * kTile, list = static_cast<int64_t>(kv * group + h1) * p.n + begin;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // A query behind the sequence has p = 2^(0 - infinity) = 0.
+        const int64_t q = row + lane + 32 * k;
+        lse2[k] = q < length ? p.lse[list + q] : INFINITY;
+        delta[k] = q < length ? p.delta[list + q] : 0.f;
       }
+      if (++b1 == per_head) b1 = 0, ++h1;
+    };
+    fetch();
+    for (int64_t i = 0, b = 0; i < tiles; ++i) {
+      const int s = static_cast<int>(i & 1);
+      ok = __all_sync(0xffffffffu, wait(&st_empty[s], (i >> 1) + 1));
+      if (!ok) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        stats[s * 2 * kTile + lane + 32 * k] = lse2[k] * kLog2e;
+        stats[s * 2 * kTile + kTile + lane + 32 * k] = delta[k];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st_full[s]);
+      if (i + 1 < tiles) fetch();
+      const bool last = ++b == per_head;
+      if (ragged && last) {
+        ok = __all_sync(0xffffffffu, wait(&q_full[s], i >> 1) && wait(&do_full[s], i >> 1));
+        if (!ok) break;
+        const int valid = static_cast<int>(length - (blocks - 1) * kTile);
+        clear_rows<kD>(queries + s * F::kTileBytes, valid);
+        clear_rows<kD>(douts + s * F::kTileBytes, valid);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(patched);
+      }
+      if (last) b = 0;
+    }
   } else {
     // ------------------------------------------------------------------ rows
     const int side = warp >> 2, r = (warp & 3) * 32 + lane;
