@@ -191,24 +191,23 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b) {
   }
 }
 
-// D (+)= A B, A being 128 x 128 bf16 in tensor memory, two of its columns in one: the first 64 from `a` on, the others
-// kSecond columns behind.
-template <int kD, int kSecond>
+// D (+)= A B, A being 128 x 128 bf16 in tensor memory, two of its columns in one: side by side from `a` on, or kParts:
+// each 32 of them at the start of the 32 columns of the scores that they were made from.
+template <int kD, bool kParts>
 __device__ __forceinline__ void mma_columns(uint32_t d, uint32_t a, uint32_t b, bool add) {
   const uint32_t desc = instr_desc_bf16<kTile, kD>(true);
   const uint64_t db = smem_desc(b, Tile<kD>::kBoxBytes, 1024);
   const uint32_t bl = static_cast<uint32_t>(db), high = static_cast<uint32_t>(db >> 32);
-  static_assert(kSecond == 32 || kSecond == 64, "offsets of the second half");
-  if constexpr (kSecond == 32) {
+  if constexpr (!kParts) {
     asm volatile(DM_ELECT "setp.ne.u32 p, %5, 0;\n\t" DM_TS("p", "0", "0") DM_TS("q", "8", "128") DM_TS("q", "16", "256")
                      DM_TS("q", "24", "384") DM_TS("q", "32", "512") DM_TS("q", "40", "640") DM_TS("q", "48", "768")
                          DM_TS("q", "56", "896") "}\n" ::"r"(d),
                  "r"(a), "r"(bl), "r"(high), "r"(desc), "r"(static_cast<uint32_t>(add))
                  : "memory");
   } else {
-    asm volatile(DM_ELECT "setp.ne.u32 p, %5, 0;\n\t" DM_TS("p", "0", "0") DM_TS("q", "8", "128") DM_TS("q", "16", "256")
-                     DM_TS("q", "24", "384") DM_TS("q", "64", "512") DM_TS("q", "72", "640") DM_TS("q", "80", "768")
-                         DM_TS("q", "88", "896") "}\n" ::"r"(d),
+    asm volatile(DM_ELECT "setp.ne.u32 p, %5, 0;\n\t" DM_TS("p", "0", "0") DM_TS("q", "8", "128") DM_TS("q", "32", "256")
+                     DM_TS("q", "40", "384") DM_TS("q", "64", "512") DM_TS("q", "72", "640") DM_TS("q", "96", "768")
+                         DM_TS("q", "104", "896") "}\n" ::"r"(d),
                  "r"(a), "r"(bl), "r"(high), "r"(desc), "r"(static_cast<uint32_t>(add))
                  : "memory");
   }
@@ -359,8 +358,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
     };
     auto scores = [&](int j, int key_slot) {
       mma_rows<kD>(F::kScores + j * kTile, base + j * F::kTileBytes, ring_at + key_slot * F::kTileBytes);
-      if (elect_one()) mma_commit(&s_full[j]);
-      __syncwarp();
+      mma_commit_elected(&s_full[j]);
     };
     int slot = 0;
     uint32_t phase = 0;
@@ -373,7 +371,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (counts[j] > 0) scores(j, 0);
-      if (elect_one()) mma_commit(&empty[0]);
+      mma_commit_elected(&empty[0]);
       next();
     }
     for (int i = 0; ok && i < n; ++i) {
@@ -392,17 +390,14 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
           ok = wait(&p_full[j], i & 1);
           tc_fence_after();
           if (ok) {
-            mma_columns<kD, kTile / 4>(F::kOut + j * kTile, F::kScores + j * kTile, ring_at + v_slot * F::kTileBytes, i > 0);
-            if (i + 1 == counts[j] && elect_one()) mma_commit(&o_full[j]);
-            __syncwarp();
+            mma_columns<kD, false>(F::kOut + j * kTile, F::kScores + j * kTile, ring_at + v_slot * F::kTileBytes, i > 0);
+            if (i + 1 == counts[j]) mma_commit_elected(&o_full[j]);
           }
         }
-        if (j == 1 && ok && elect_one()) mma_commit(&empty[v_slot]);
-        __syncwarp();
+        if (j == 1 && ok) mma_commit_elected(&empty[v_slot]);
         if (ok && i + 1 < counts[j]) scores(j, k_slot);
       }
-      if (ok && i + 1 < n && elect_one()) mma_commit(&empty[k_slot]);
-      __syncwarp();
+      if (ok && i + 1 < n) mma_commit_elected(&empty[k_slot]);
     }
     if (elect_one()) {
       mma_commit(drain);
@@ -524,16 +519,18 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
 // dv and dk fill its 512 columns. Products of one kind run while the warps work on the other:
 // dv(i), scores(i + 1), dk(i), dout . v(i + 1).
 //
-// In both, 8 warps form p and ds: each thread half of a row, 64 columns.
+// In both, 16 warps form p and ds, each thread a quarter of a row: four warps a scheduler, since a warp alone spends most
+// of its time on latencies (8 warps with 64 columns a thread: see the table of times).
 
-constexpr int kHalf = 64;
+constexpr int kPart = 32;             // columns of a row that a thread has
+constexpr int kRowWarps = 16;
 
 template <int kD>
 struct Bwd : Tile<kD> {
   static constexpr int kTileBytes = Tile<kD>::kBytes;
-  static constexpr int kThreads = 352;  // warps 0-7: rows; 8: copies; 9: products; 10: what the rows need beside them
+  static constexpr int kThreads = 608;  // warps 0-15: rows; 16: copies; 17: products; 18: what the rows need bepart them
   static constexpr int kKeySlots = 3, kValueSlots = 2;
-  static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 1024 + 256 + 1024;
+  static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 256 + kTile * 4 + 1024;
   static constexpr int kSmemKeys = 6 * kTileBytes + 4 * kTile * 4 + 256 + 1024;
 };
 
@@ -546,14 +543,13 @@ __device__ __forceinline__ void clear_rows(uint8_t* tile, int valid) {
   fence_async_smem();
 }
 
-// 64 columns of this thread's lane.
-__device__ __forceinline__ void load_half(uint32_t taddr, float (&v)[kHalf]) {
-  uint32_t r[kHalf];
+// 32 columns of this thread's lane.
+__device__ __forceinline__ void load_part(uint32_t taddr, float (&v)[kPart]) {
+  uint32_t r[kPart];
   tmem_ld32_issue(taddr, r);
-  tmem_ld32_issue(taddr + 32, r + 32);
   tmem_ld_wait(r);
 #pragma unroll
-  for (int k = 0; k < kHalf; ++k) v[k] = __uint_as_float(r[k]);
+  for (int k = 0; k < kPart; ++k) v[k] = __uint_as_float(r[k]);
 }
 
 // 32 columns from taddr on of an accumulator, times f, to `out` as bf16.
@@ -578,8 +574,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   uint8_t *keys = smem + 2 * F::kTileBytes, *values = keys + F::kKeySlots * F::kTileBytes;  // behind queries and dout
   const uint32_t q_at = (smem_u32(smem_raw) + 1023) & ~1023u, do_at = q_at + F::kTileBytes, keys_at = do_at + F::kTileBytes,
                  values_at = keys_at + F::kKeySlots * F::kTileBytes;
-  float* exchange = reinterpret_cast<float*>(values + F::kValueSlots * F::kTileBytes);  // 2 x 128
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(exchange + 2 * kTile);
+  float* exchange = reinterpret_cast<float*>(smem);  // 4 x 128, over the queries when they are no longer needed
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(values + F::kValueSlots * F::kTileBytes);
   uint64_t* k_full = q_full + 1;
   uint64_t* k_empty = k_full + F::kKeySlots;
   uint64_t* v_full = k_empty + F::kKeySlots;
@@ -594,6 +590,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   uint64_t* drain = done + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* row_delta = reinterpret_cast<float*>(q_full + 32);
   __shared__ Place place;
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
@@ -602,14 +599,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     mbar_init(q_full, 1);
     for (int s = 0; s < F::kKeySlots; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1);
     for (int s = 0; s < F::kValueSlots; ++s) mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
-    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(s_read, 8);
-    for (int b = 0; b < 2; ++b) mbar_init(&dp_full[b], 1), mbar_init(&ds_full[b], 8);
-    mbar_init(exchanged, 8), mbar_init(done, 1), mbar_init(drain, 1);
+    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(s_read, kRowWarps);
+    for (int b = 0; b < 2; ++b) mbar_init(&dp_full[b], 1), mbar_init(&ds_full[b], kRowWarps);
+    mbar_init(exchanged, kRowWarps), mbar_init(done, 1), mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   griddep_wait();
-  if (warp == 9) {
+  if (warp == 17) {
     const Place found = find_place(p, blockIdx.x / p.heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   const bool patch = static_cast<int64_t>(tiles) * kTile > length;
   auto wait = [&](uint64_t* bar, uint32_t phase) { return wait_fast(bar, phase & 1u, abort_flag, p.status); };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------------ copies
     bool ok = true;
     int i = 0, loaded_v = 0;
@@ -666,7 +663,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       for (int t = max(0, loaded_v - F::kValueSlots); t < loaded_v; ++t)
         wait_bounded(&v_full[t % F::kValueSlots], (t / F::kValueSlots) & 1, abort_flag, p.status, kDrainLimitNs, false);
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------------ products
     const int n = __shfl_sync(0xffffffffu, tiles, 0);
     const bool cut = __any_sync(0xffffffffu, patch);
@@ -678,8 +675,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
         return false;
       tc_fence_after();
       mma_rows<kD>(t_s, q_at, keys_at + ks * F::kTileBytes);
-      if (elect_one()) mma_commit(s_full);
-      __syncwarp();
+      mma_commit_elected(s_full);
       if (++ks == F::kKeySlots) ks = 0, k_phase ^= 1u;
       return true;
     };
@@ -687,11 +683,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       if (!all_wait(&v_full[vs], v_phase)) return false;
       tc_fence_after();
       mma_rows<kD>(t_dp + (i & 1) * kTile, do_at, values_at + vs * F::kTileBytes);
-      if (elect_one()) {
-        mma_commit(&v_empty[vs]);
-        mma_commit(&dp_full[i & 1]);
-      }
-      __syncwarp();
+      mma_commit_elected(&dp_full[i & 1]);
+      mma_commit_elected(&v_empty[vs]);
       if (++vs == F::kValueSlots) vs = 0, v_phase ^= 1u;
       return true;
     };
@@ -701,93 +694,94 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
       ok = ok && all_wait(&ds_full[i & 1], i >> 1);
       if (!ok) break;
       tc_fence_after();
-      mma_columns<kD, kHalf>(t_dq, t_dp + (i & 1) * kTile, keys_at + dqs * F::kTileBytes, i > 0);
-      if (elect_one()) {
-        mma_commit(&k_empty[dqs]);
-        if (i + 1 == n) mma_commit(done);
-      }
-      __syncwarp();
+      mma_columns<kD, true>(t_dq, t_dp + (i & 1) * kTile, keys_at + dqs * F::kTileBytes, i > 0);
+      mma_commit_elected(&k_empty[dqs]);
+      if (i + 1 == n) mma_commit_elected(done);
       if (++dqs == F::kKeySlots) dqs = 0;
     }
     if (elect_one()) {
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
-  } else if (warp < 8) {
+  } else if (warp < kRowWarps) {
     // ------------------------------------------------------------------ rows
-    const int side = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int part = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const bool live = row0 + r < length;
     const int64_t token = begin + (live ? row0 + r : 0);
     const float sl2 = p.scale * kLog2e, lse2 = live ? p.lse[static_cast<int64_t>(head) * p.n + token] * kLog2e : INFINITY;
-    float delta = 0.f;
-    {
-      const bf16 *o = at(p.out, token, head), *g = at(p.dout, token, head);
-      for (int c = 0; c < p.dim; c += 8) {
+    // D of the rows, 16 lanes to one: read by a thread each, a load would touch 32 rows (16 warps: 16000 cycles).
+    for (int q = warp * 8 + (lane >> 4); q < warp * 8 + 8; q += 2) {
+      const int64_t row = begin + (row0 + q < length ? row0 + q : 0);
+      const int c = (lane & 15) * 8;
+      float d = 0.f;
+      if (c < p.dim) {
         float a[8], b[8];
-        row::unpack16<bf16>(a, *reinterpret_cast<const uint4*>(o + c));
-        row::unpack16<bf16>(b, *reinterpret_cast<const uint4*>(g + c));
+        row::unpack16<bf16>(a, *reinterpret_cast<const uint4*>(at(p.out, row, head) + c));
+        row::unpack16<bf16>(b, *reinterpret_cast<const uint4*>(at(p.dout, row, head) + c));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) delta = fmaf(a[e], b[e], delta);
+        for (int e = 0; e < 8; ++e) d = fmaf(a[e], b[e], d);
       }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if ((lane & 15) == 0) row_delta[q] = d;
     }
+    asm volatile("bar.sync 1, %0;" ::"n"(kRowWarps * 32) : "memory");  // nothing above waits: all of them come
+    float delta = row_delta[r];
     float2 rest = make_float2(0.f, 0.f);  // sum of ds, in two parts
     bool ok = true;
     for (int i = 0; i < tiles; ++i) {
       ok = __all_sync(0xffffffffu, wait(s_full, i));
       if (!ok) break;
       tc_fence_after();
-      float prob[kHalf];
-      load_half(t_s + lanes + side * kHalf, prob);
+      float prob[kPart];
+      load_part(t_s + lanes + part * kPart, prob);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_read);
       const int64_t key0 = static_cast<int64_t>(i) * kTile;
       const bool masked = (p.causal && key0 == row0) || key0 + kTile > length;
-      const int here = masked ? static_cast<int>((p.causal && live ? row0 + r + 1 : length) - key0) - side * kHalf : kHalf;
+      const int here = masked ? static_cast<int>((p.causal && live ? row0 + r + 1 : length) - key0) - part * kPart : kPart;
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 2) {
+      for (int k = 0; k < kPart; k += 2) {
         const float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(-lse2, -lse2));
         prob[k] = pow2(y.x), prob[k + 1] = pow2(y.y);
       }
       if (masked) {
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) prob[k] = k < here ? prob[k] : 0.f;
+        for (int k = 0; k < kPart; ++k) prob[k] = k < here ? prob[k] : 0.f;
       }
       ok = __all_sync(0xffffffffu, wait(&dp_full[i & 1], i >> 1));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t t = t_dp + (i & 1) * kTile + lanes + side * kHalf;
-      float dp[kHalf];
-      load_half(t, dp);
+      const uint32_t t = t_dp + (i & 1) * kTile + lanes + part * kPart;
+      float dp[kPart];
+      load_part(t, dp);
       if (tiles == 1) {
         // All keys of these rows are at hand: the whole D before the first ds.
         float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) sum += k < here ? prob[k] * (dp[k] - delta) : 0.f;
-        exchange[side * kTile + r] = sum;
+        for (int k = 0; k < kPart; ++k) sum += k < here ? prob[k] * (dp[k] - delta) : 0.f;
+        exchange[part * kTile + r] = sum;
         __syncwarp();
         if (lane == 0) mbar_arrive(exchanged);
         ok = __all_sync(0xffffffffu, wait(exchanged, 0));
         if (!ok) break;
-        delta += exchange[r] + exchange[kTile + r];
+        delta += (exchange[r] + exchange[kTile + r]) + (exchange[2 * kTile + r] + exchange[3 * kTile + r]);
       }
+      if (masked) {  // ds = 0 whatever dout . v is there
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 16) {
-        uint32_t half[8];
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          float2 ds = add2(make_float2(dp[c + k], dp[c + k + 1]), make_float2(-delta, -delta));
-          ds = mul2(ds, make_float2(prob[c + k], prob[c + k + 1]));
-          if (masked) {  // 0 whatever dout . v is there
-            ds.x = c + k < here ? ds.x : 0.f;
-            ds.y = c + k + 1 < here ? ds.y : 0.f;
-          }
-          rest = add2(rest, ds);
-          half[k / 2] = pack_bf16(ds.x, ds.y);
-        }
-        tmem_st8(t + c / 2, half);  // over columns that have been read
+        for (int k = 0; k < kPart; ++k) dp[k] = k < here ? dp[k] : delta;
       }
+      uint32_t half[16];
+#pragma unroll
+      for (int k = 0; k < kPart; k += 2) {
+        float2 ds = add2(make_float2(dp[k], dp[k + 1]), make_float2(-delta, -delta));
+        ds = mul2(ds, make_float2(prob[k], prob[k + 1]));
+        rest = add2(rest, ds);
+        half[k / 2] = pack_bf16(ds.x, ds.y);
+      }
+      tmem_st16(t, half);  // over columns that have been read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -795,18 +789,18 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     }
     if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
     if (ok && tiles > 1) {
-      exchange[side * kTile + r] = rest.x + rest.y;
+      exchange[part * kTile + r] = rest.x + rest.y;
       __syncwarp();
       if (lane == 0) mbar_arrive(exchanged);
       ok = __all_sync(0xffffffffu, wait(exchanged, 0));
-      if (ok) delta += exchange[r] + exchange[kTile + r];
+      if (ok) delta += (exchange[r] + exchange[kTile + r]) + (exchange[2 * kTile + r] + exchange[3 * kTile + r]);
     }
     if (ok) {
       tc_fence_after();
-      if (live && side == 0) p.delta[static_cast<int64_t>(head) * p.n + token] = delta;
+      if (live && part == 0) p.delta[static_cast<int64_t>(head) * p.n + token] = delta;
       bf16* out = out_at(p.dq, token, head);
 #pragma unroll
-      for (int c = side * (kD / 2); c < (side + 1) * (kD / 2); c += 32)
+      for (int c = part * kPart; c < kD; c += kTile)
         store_columns(t_dq + lanes + c, p.scale, out + c, live ? p.dim - c : 0);
     }
   }
@@ -814,7 +808,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(0, kCols);
+  if (warp == 17) tmem_dealloc(0, kCols);
 }
 
 template <int kD>
@@ -825,7 +819,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   uint8_t *queries = smem + 2 * F::kTileBytes, *douts = queries + 2 * F::kTileBytes;  // behind keys and values
   const uint32_t k_at = (smem_u32(smem_raw) + 1023) & ~1023u, v_at = k_at + F::kTileBytes, queries_at = v_at + F::kTileBytes,
                  douts_at = queries_at + 2 * F::kTileBytes;
-  float* stats = reinterpret_cast<float*>(douts + 2 * F::kTileBytes);  // two stages of lse log2(e), D
+  float* stats = reinterpret_cast<float*>(douts + 2 * F::kTileBytes);  // two stages of -lse log2(e), -D
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * kTile);
   uint64_t* q_full = kv_full + 1;
   uint64_t* q_empty = q_full + 2;
@@ -850,15 +844,15 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     mbar_init(kv_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1), mbar_init(&do_full[s], 1), mbar_init(&do_empty[s], 1);
-      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], 8);
+      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], kRowWarps);
     }
-    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(p_full, 8), mbar_init(dp_full, 1), mbar_init(ds_full, 8);
+    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(p_full, kRowWarps), mbar_init(dp_full, 1), mbar_init(ds_full, kRowWarps);
     mbar_init(done, 1), mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
   }
   griddep_wait();
-  if (warp == 9) {
+  if (warp == 17) {
     const Place found = find_place(p, blockIdx.x / p.kv_heads, [](int64_t len) { return (len + kTile - 1) / kTile; });
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
@@ -877,7 +871,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   const bool ragged = length % kTile != 0;  // a head's last tile of queries has rows of other sequences
   auto wait = [&](uint64_t* bar, int64_t phase) { return wait_fast(bar, static_cast<uint32_t>(phase) & 1u, abort_flag, p.status); };
 
-  if (warp == 8) {
+  if (warp == 16) {
     // ------------------------------------------------------------------ copies
     if (lane == 0) {
       mbar_arrive_expect_tx(kv_full, 2 * F::kTileBytes);
@@ -908,7 +902,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
           wait_bounded(&do_full[t & 1], (t >> 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ------------------------------------------------------------------ products
     const int each = __shfl_sync(0xffffffffu, per_head, 0);
     const int64_t n = static_cast<int64_t>(each) * group;
@@ -925,16 +919,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       if (!there) return false;
       tc_fence_after();
       mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
-      if (elect_one()) mma_commit(s_full);
-      __syncwarp();
+      mma_commit_elected(s_full);
       return true;
     };
     auto along = [&](int s, uint32_t phase) {
       if (!all_wait(&do_full[s], phase)) return false;
       tc_fence_after();
       mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
-      if (elect_one()) mma_commit(dp_full);
-      __syncwarp();
+      mma_commit_elected(dp_full);
       return true;
     };
     bool ok = all_wait(kv_full, 0) && scores(0, 0) && along(0, 0);
@@ -945,18 +937,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       const uint32_t phase1 = s1 == 0 ? phase ^ 1u : phase;
       if (!(ok = all_wait(p_full, turn))) break;
       tc_fence_after();
-      mma_columns<kD, kHalf>(t_dv, t_s, douts_at + s * F::kTileBytes, i > 0);
-      if (elect_one()) mma_commit(&do_empty[s]);
-      __syncwarp();
+      mma_columns<kD, true>(t_dv, t_s, douts_at + s * F::kTileBytes, i > 0);
+      mma_commit_elected(&do_empty[s]);
       if (i + 1 < n && !(ok = scores(s1, phase1))) break;
       if (!(ok = all_wait(ds_full, turn))) break;
       tc_fence_after();
-      mma_columns<kD, kHalf>(t_dk, t_dp, queries_at + s * F::kTileBytes, i > 0);
-      if (elect_one()) {
-        mma_commit(&q_empty[s]);
-        if (i + 1 == n) mma_commit(done);
-      }
-      __syncwarp();
+      mma_columns<kD, true>(t_dk, t_dp, queries_at + s * F::kTileBytes, i > 0);
+      mma_commit_elected(&q_empty[s]);
+      if (i + 1 == n) mma_commit_elected(done);
       if (i + 1 < n) ok = along(s1, phase1);
       s = s1, phase = phase1, turn ^= 1u;
     }
@@ -964,7 +952,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
-  } else if (warp == 10) {
+  } else if (warp == 18) {
     // ------------------------------------------------------------------ the queries' lse and D; rows of other sequences
     // The values of a tile are asked for before its place is free: a wait for memory in the rows' way takes as long as
     // half of a tile (8192 tokens: 1.91 -> 1.6 ms for both kernels).
@@ -989,8 +977,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       if (!ok) break;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        stats[s * 2 * kTile + lane + 32 * k] = lse2[k] * kLog2e;
-        stats[s * 2 * kTile + kTile + lane + 32 * k] = delta[k];
+        stats[s * 2 * kTile + lane + 32 * k] = lse2[k] * -kLog2e;
+        stats[s * 2 * kTile + kTile + lane + 32 * k] = -delta[k];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&st_full[s]);
@@ -1009,7 +997,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     }
   } else {
     // ------------------------------------------------------------------ rows
-    const int side = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int part = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float sl2 = p.scale * kLog2e;
     bool ok = true;
@@ -1017,34 +1005,31 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     for (int64_t i = 0; i < tiles; ++i) {
       const bool diagonal = p.causal && left == 0;  // a head's first tile of queries is that of the keys
       left = left == 0 ? per_head - 1 : left - 1;
-      const float* lse2 = stats + (i & 1) * 2 * kTile + side * kHalf;
+      const float* lse2 = stats + (i & 1) * 2 * kTile + part * kPart;
       const float* delta = lse2 + kTile;
       ok = wait(&st_full[i & 1], i >> 1);
       ok = __all_sync(0xffffffffu, ok && wait(s_full, i));
       if (!ok) break;
       tc_fence_after();
-      float prob[kHalf];
-      load_half(t_s + lanes + side * kHalf, prob);
+      float prob[kPart];
+      load_part(t_s + lanes + part * kPart, prob);
 #pragma unroll
-      for (int k = 0; k < kHalf; k += 4) {
+      for (int k = 0; k < kPart; k += 4) {
         const float4 l = *reinterpret_cast<const float4*>(lse2 + k);
-        float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(-l.x, -l.y));
+        float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(l.x, l.y));
         prob[k] = pow2(y.x), prob[k + 1] = pow2(y.y);
-        y = fma2(make_float2(prob[k + 2], prob[k + 3]), make_float2(sl2, sl2), make_float2(-l.z, -l.w));
+        y = fma2(make_float2(prob[k + 2], prob[k + 3]), make_float2(sl2, sl2), make_float2(l.z, l.w));
         prob[k + 2] = pow2(y.x), prob[k + 3] = pow2(y.y);
       }
-      const int from = diagonal ? r - side * kHalf : 0;  // the queries before the key do not meet it
+      const int from = diagonal ? r - part * kPart : 0;  // the queries before the key do not meet it
       if (diagonal) {
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) prob[k] = k < from ? 0.f : prob[k];
+        for (int k = 0; k < kPart; ++k) prob[k] = k < from ? 0.f : prob[k];
       }
+      uint32_t half[16];
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        uint32_t half[16];
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) half[k / 2] = pack_bf16(prob[c + k], prob[c + k + 1]);
-        tmem_st16(t_s + lanes + side * kHalf + c / 2, half);
-      }
+      for (int k = 0; k < kPart; k += 2) half[k / 2] = pack_bf16(prob[k], prob[k + 1]);
+      tmem_st16(t_s + lanes + part * kPart, half);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -1052,28 +1037,23 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       ok = __all_sync(0xffffffffu, wait(dp_full, i));
       if (!ok) break;
       tc_fence_after();
-      const uint32_t t = t_dp + lanes + side * kHalf;
-      float dp[kHalf];
-      load_half(t, dp);
+      const uint32_t t = t_dp + lanes + part * kPart;
+      float dp[kPart];
+      load_part(t, dp);
+      if (diagonal) {  // ds = 0 whatever dout . v is there
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 16) {
-        uint32_t half[8];
-#pragma unroll
-        for (int k = 0; k < 16; k += 4) {
-          const float4 d = *reinterpret_cast<const float4*>(delta + c + k);
-          float2 a = add2(make_float2(dp[c + k], dp[c + k + 1]), make_float2(-d.x, -d.y));
-          float2 b = add2(make_float2(dp[c + k + 2], dp[c + k + 3]), make_float2(-d.z, -d.w));
-          a = mul2(a, make_float2(prob[c + k], prob[c + k + 1]));
-          b = mul2(b, make_float2(prob[c + k + 2], prob[c + k + 3]));
-          if (diagonal) {  // 0 whatever dout . v is there
-            a.x = c + k < from ? 0.f : a.x, a.y = c + k + 1 < from ? 0.f : a.y;
-            b.x = c + k + 2 < from ? 0.f : b.x, b.y = c + k + 3 < from ? 0.f : b.y;
-          }
-          half[k / 2] = pack_bf16(a.x, a.y);
-          half[k / 2 + 1] = pack_bf16(b.x, b.y);
-        }
-        tmem_st8(t + c / 2, half);
+        for (int k = 0; k < kPart; ++k) dp[k] = k < from ? 0.f : dp[k];
       }
+#pragma unroll
+      for (int k = 0; k < kPart; k += 4) {
+        const float4 d = *reinterpret_cast<const float4*>(delta + k);
+        const float2 a = mul2(add2(make_float2(dp[k], dp[k + 1]), make_float2(d.x, d.y)), make_float2(prob[k], prob[k + 1]));
+        const float2 b =
+            mul2(add2(make_float2(dp[k + 2], dp[k + 3]), make_float2(d.z, d.w)), make_float2(prob[k + 2], prob[k + 3]));
+        half[k / 2] = pack_bf16(a.x, a.y);
+        half[k / 2 + 1] = pack_bf16(b.x, b.y);
+      }
+      tmem_st16(t, half);  // over columns that have been read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -1084,17 +1064,18 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       tc_fence_after();
       const bool live = key0 + r < length;
       const int64_t token = begin + key0 + (live ? r : 0);
-      bf16* out = out_at(side ? p.dk : p.dv, token, kv);
+      const bool keys = part >= 2;  // two parts store dv, two dk
+      bf16* out = out_at(keys ? p.dk : p.dv, token, kv);
 #pragma unroll
-      for (int c = 0; c < kD; c += 32)
-        store_columns((side ? t_dk : t_dv) + lanes + c, side ? p.scale : 1.f, out + c, live ? p.dim - c : 0);
+      for (int c = (part & 1) * kPart; c < kD; c += 2 * kPart)
+        store_columns((keys ? t_dk : t_dv) + lanes + c, keys ? p.scale : 1.f, out + c, live ? p.dim - c : 0);
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(0, kCols);
+  if (warp == 17) tmem_dealloc(0, kCols);
 }
 
 // ---------------------------------------------------------------------------- launches
