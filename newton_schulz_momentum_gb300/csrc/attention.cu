@@ -216,6 +216,27 @@ __device__ __forceinline__ void mma_columns(uint32_t d, uint32_t a, uint32_t b, 
 #undef DM_TS
 #undef DM_ELECT
 
+// D += A B^T of two strips, 128 rows of 16 columns: 8 rows of 16 bytes one after another, the second 8 columns of the same
+// rows 128 bytes behind, the next 8 rows 256.
+constexpr int kStripBytes = kTile * 32;
+__device__ __forceinline__ void mma_strips(uint32_t d, uint32_t a, uint32_t b) {
+  // No swizzle (layout 0), descriptor version 1.
+  constexpr uint64_t form = (static_cast<uint64_t>(128 >> 4) << 16) | (static_cast<uint64_t>(256 >> 4) << 32) | (1ull << 46);
+  asm volatile(
+      "{\n\t.reg .pred e, q;\n\telect.sync _|e, 0xffffffff;\n\tsetp.eq.u32 q, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}\n" ::"r"(d),
+      "l"(form | ((a & 0x3FFFFu) >> 4)), "l"(form | ((b & 0x3FFFFu) >> 4)), "r"(instr_desc_bf16<kTile, kTile>(false))
+      : "memory");
+}
+
+// x to 24 bits as three bf16 terms, in the first half of a strip's row.
+__device__ __forceinline__ void store_strip(uint8_t* strip, int row, float x) {
+  const float hi = __bfloat162float(__float2bfloat16_rn(x));
+  const float rest = isinf(x) ? 0.f : x - hi, mid = __bfloat162float(__float2bfloat16_rn(rest));
+  *reinterpret_cast<uint4*>(strip + (row >> 3) * 256 + (row & 7) * 16) =
+      make_uint4(pack_bf16(hi, mid), pack_bf16(rest - mid, 0.f), 0u, 0u);
+}
+
 // ---------------------------------------------------------------------------- forward
 
 template <int kD>
@@ -531,7 +552,7 @@ struct Bwd : Tile<kD> {
   static constexpr int kThreads = 608;  // warps 0-15: rows; 16: copies; 17: products; 18: what the rows need bepart them
   static constexpr int kKeySlots = 3, kValueSlots = 2;
   static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 256 + kTile * 4 + 1024;
-  static constexpr int kSmemKeys = 6 * kTileBytes + 4 * kTile * 4 + 256 + 1024;
+  static constexpr int kSmemKeys = 6 * kTileBytes + 5 * kStripBytes + 256 + 1024;
 };
 
 // Zeros in the rows from `valid` on of a tile in shared memory, by a warp, visible to the products.
@@ -819,8 +840,9 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   uint8_t *queries = smem + 2 * F::kTileBytes, *douts = queries + 2 * F::kTileBytes;  // behind keys and values
   const uint32_t k_at = (smem_u32(smem_raw) + 1023) & ~1023u, v_at = k_at + F::kTileBytes, queries_at = v_at + F::kTileBytes,
                  douts_at = queries_at + 2 * F::kTileBytes;
-  float* stats = reinterpret_cast<float*>(douts + 2 * F::kTileBytes);  // two stages of -lse log2(e), -D
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(stats + 4 * kTile);
+  uint8_t* strips = douts + 2 * F::kTileBytes;  // ones; two stages of -lse / scale and -D of the queries
+  const uint32_t ones_at = douts_at + 2 * F::kTileBytes;
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(strips + 5 * kStripBytes);
   uint64_t* q_full = kv_full + 1;
   uint64_t* q_empty = q_full + 2;
   uint64_t* do_full = q_empty + 2;
@@ -844,7 +866,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     mbar_init(kv_full, 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1), mbar_init(&do_full[s], 1), mbar_init(&do_empty[s], 1);
-      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], kRowWarps);
+      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], 1);
     }
     mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(p_full, kRowWarps), mbar_init(dp_full, 1), mbar_init(ds_full, kRowWarps);
     mbar_init(done, 1), mbar_init(drain, 1);
@@ -911,7 +933,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     int left = each;  // tiles of queries to come of the head whose scores are formed next
     uint32_t patches = 0;
     auto scores = [&](int s, uint32_t phase) {
-      bool there = all_wait(&q_full[s], phase);
+      bool there = all_wait(&q_full[s], phase) && all_wait(&st_full[s], phase);
       if (--left == 0) {
         left = each;
         if (cut) there = there && all_wait(patched, patches++);
@@ -919,6 +941,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       if (!there) return false;
       tc_fence_after();
       mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
+      mma_strips(t_s, ones_at, ones_at + (1 + 2 * s) * kStripBytes);
       mma_commit_elected(s_full);
       return true;
     };
@@ -926,7 +949,9 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       if (!all_wait(&do_full[s], phase)) return false;
       tc_fence_after();
       mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
+      mma_strips(t_dp, ones_at, ones_at + (2 + 2 * s) * kStripBytes);
       mma_commit_elected(dp_full);
+      mma_commit_elected(&st_empty[s]);
       return true;
     };
     bool ok = all_wait(kv_full, 0) && scores(0, 0) && along(0, 0);
@@ -954,19 +979,25 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     }
   } else if (warp == 18) {
     // ------------------------------------------------------------------ the queries' lse and D; rows of other sequences
-    // The values of a tile are asked for before its place is free: a wait for memory in the rows' way takes as long as
-    // half of a tile (8192 tokens: 1.91 -> 1.6 ms for both kernels).
+    // They enter the products as one more step of 16 columns, 1 for each key and the value in three bf16 terms for the
+    // query: a thread has a key's row, so it would have to read every query's value from shared memory, whose time the
+    // products need (1024 of 2800 cycles of a tile). The values are asked for a tile ahead.
     bool ok = true;
-    float lse2[4], delta[4];
+    float lse[4], delta[4];
+    const float by = -1.f / p.scale;
+    for (int k = lane; k < 5 * kStripBytes / 16; k += 32) {
+      const bool one = k < kStripBytes / 16 && (k & 15) < 8;
+      *reinterpret_cast<uint4*>(strips + k * 16) = make_uint4(one ? 0x3f803f80u : 0u, one ? 0x00003f80u : 0u, 0u, 0u);
+    }
     int h1 = 0, b1 = 0;  // the next tile
     auto fetch = [&] {
       const int64_t row = (first + b1) * kTile, list = static_cast<int64_t>(kv * group + h1) * p.n + begin;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        // A query behind the sequence has p = 2^(0 - infinity) = 0.
         const int64_t q = row + lane + 32 * k;
-        lse2[k] = q < length ? p.lse[list + q] : INFINITY;
-        delta[k] = q < length ? p.delta[list + q] : 0.f;
+        const bool live = q < length;
+        lse[k] = live ? p.lse[list + q] : 0.f;
+        delta[k] = live ? p.delta[list + q] : 0.f;
       }
       if (++b1 == per_head) b1 = 0, ++h1;
     };
@@ -975,19 +1006,22 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       const int s = static_cast<int>(i & 1);
       ok = __all_sync(0xffffffffu, wait(&st_empty[s], (i >> 1) + 1));
       if (!ok) break;
+      const bool last = ++b == per_head;
+      const int valid = ragged && last ? static_cast<int>(length - (blocks - 1) * kTile) : kTile;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        stats[s * 2 * kTile + lane + 32 * k] = lse2[k] * -kLog2e;
-        stats[s * 2 * kTile + kTile + lane + 32 * k] = -delta[k];
+        // A query behind the sequence has p = 2^(0 - infinity) = 0.
+        const int q = lane + 32 * k;
+        store_strip(strips + (1 + 2 * s) * kStripBytes, q, q < valid ? lse[k] * by : p.scale < 0.f ? INFINITY : -INFINITY);
+        store_strip(strips + (2 + 2 * s) * kStripBytes, q, -delta[k]);
       }
+      fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&st_full[s]);
       if (i + 1 < tiles) fetch();
-      const bool last = ++b == per_head;
       if (ragged && last) {
         ok = __all_sync(0xffffffffu, wait(&q_full[s], i >> 1) && wait(&do_full[s], i >> 1));
         if (!ok) break;
-        const int valid = static_cast<int>(length - (blocks - 1) * kTile);
         clear_rows<kD>(queries + s * F::kTileBytes, valid);
         clear_rows<kD>(douts + s * F::kTileBytes, valid);
         __syncwarp();
@@ -1005,21 +1039,15 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     for (int64_t i = 0; i < tiles; ++i) {
       const bool diagonal = p.causal && left == 0;  // a head's first tile of queries is that of the keys
       left = left == 0 ? per_head - 1 : left - 1;
-      const float* lse2 = stats + (i & 1) * 2 * kTile + part * kPart;
-      const float* delta = lse2 + kTile;
-      ok = wait(&st_full[i & 1], i >> 1);
-      ok = __all_sync(0xffffffffu, ok && wait(s_full, i));
+      ok = __all_sync(0xffffffffu, wait(s_full, i));
       if (!ok) break;
       tc_fence_after();
       float prob[kPart];
       load_part(t_s + lanes + part * kPart, prob);
 #pragma unroll
-      for (int k = 0; k < kPart; k += 4) {
-        const float4 l = *reinterpret_cast<const float4*>(lse2 + k);
-        float2 y = fma2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2), make_float2(l.x, l.y));
+      for (int k = 0; k < kPart; k += 2) {
+        const float2 y = mul2(make_float2(prob[k], prob[k + 1]), make_float2(sl2, sl2));  // (x - lse) log2(e)
         prob[k] = pow2(y.x), prob[k + 1] = pow2(y.y);
-        y = fma2(make_float2(prob[k + 2], prob[k + 3]), make_float2(sl2, sl2), make_float2(l.z, l.w));
-        prob[k + 2] = pow2(y.x), prob[k + 3] = pow2(y.y);
       }
       const int from = diagonal ? r - part * kPart : 0;  // the queries before the key do not meet it
       if (diagonal) {
@@ -1045,19 +1073,15 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
         for (int k = 0; k < kPart; ++k) dp[k] = k < from ? 0.f : dp[k];
       }
 #pragma unroll
-      for (int k = 0; k < kPart; k += 4) {
-        const float4 d = *reinterpret_cast<const float4*>(delta + k);
-        const float2 a = mul2(add2(make_float2(dp[k], dp[k + 1]), make_float2(d.x, d.y)), make_float2(prob[k], prob[k + 1]));
-        const float2 b =
-            mul2(add2(make_float2(dp[k + 2], dp[k + 3]), make_float2(d.z, d.w)), make_float2(prob[k + 2], prob[k + 3]));
-        half[k / 2] = pack_bf16(a.x, a.y);
-        half[k / 2 + 1] = pack_bf16(b.x, b.y);
+      for (int k = 0; k < kPart; k += 2) {
+        const float2 ds = mul2(make_float2(dp[k], dp[k + 1]), make_float2(prob[k], prob[k + 1]));
+        half[k / 2] = pack_bf16(ds.x, ds.y);
       }
       tmem_st16(t, half);  // over columns that have been read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ds_full), mbar_arrive(&st_empty[i & 1]);
+      if (lane == 0) mbar_arrive(ds_full);
     }
     if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
     if (ok) {
