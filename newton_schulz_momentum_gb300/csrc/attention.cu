@@ -550,7 +550,7 @@ template <int kD>
 struct Bwd : Tile<kD> {
   static constexpr int kTileBytes = Tile<kD>::kBytes;
   static constexpr int kThreads = 608;  // warps 0-15: rows; 16: copies; 17: products; 18: what the rows need bepart them
-  static constexpr int kKeySlots = 3, kValueSlots = 2;
+  static constexpr int kKeySlots = 3, kValueSlots = 2, kQuerySlots = 3;
   static constexpr int kSmemQueries = (2 + kKeySlots + kValueSlots) * kTileBytes + 256 + kTile * 4 + 1024;
   static constexpr int kSmemKeys = 6 * kTileBytes + 5 * kStripBytes + 256 + 1024;
 };
@@ -837,20 +837,19 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   using F = Bwd<kD>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *queries = smem + 2 * F::kTileBytes, *douts = queries + 2 * F::kTileBytes;  // behind keys and values
+  uint8_t *queries = smem + 2 * F::kTileBytes, *dout = queries + F::kQuerySlots * F::kTileBytes;  // behind keys and values
   const uint32_t k_at = (smem_u32(smem_raw) + 1023) & ~1023u, v_at = k_at + F::kTileBytes, queries_at = v_at + F::kTileBytes,
-                 douts_at = queries_at + 2 * F::kTileBytes;
-  uint8_t* strips = douts + 2 * F::kTileBytes;  // ones; two stages of -lse / scale and -D of the queries
-  const uint32_t ones_at = douts_at + 2 * F::kTileBytes;
+                 dout_at = queries_at + F::kQuerySlots * F::kTileBytes;
+  uint8_t* strips = dout + F::kTileBytes;  // ones; two stages of -lse / scale and -D of the queries
+  const uint32_t ones_at = dout_at + F::kTileBytes;
   uint64_t* kv_full = reinterpret_cast<uint64_t*>(strips + 5 * kStripBytes);
   uint64_t* q_full = kv_full + 1;
-  uint64_t* q_empty = q_full + 2;
-  uint64_t* do_full = q_empty + 2;
-  uint64_t* do_empty = do_full + 2;
-  uint64_t* st_full = do_empty + 2;
+  uint64_t* q_empty = q_full + F::kQuerySlots;
+  uint64_t* do_full = q_empty + F::kQuerySlots;
+  uint64_t* do_empty = do_full + 1;
+  uint64_t* st_full = do_empty + 1;
   uint64_t* st_empty = st_full + 2;
-  uint64_t* patched = st_empty + 2;
-  uint64_t* s_full = patched + 1;
+  uint64_t* s_full = st_empty + 2;
   uint64_t* p_full = s_full + 1;
   uint64_t* dp_full = p_full + 1;
   uint64_t* ds_full = dp_full + 1;
@@ -864,11 +863,10 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1), mbar_init(&do_full[s], 1), mbar_init(&do_empty[s], 1);
-      mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], 1);
-    }
-    mbar_init(patched, 1), mbar_init(s_full, 1), mbar_init(p_full, kRowWarps), mbar_init(dp_full, 1), mbar_init(ds_full, kRowWarps);
+    for (int s = 0; s < F::kQuerySlots; ++s) mbar_init(&q_full[s], 1), mbar_init(&q_empty[s], 1);
+    for (int s = 0; s < 2; ++s) mbar_init(&st_full[s], 1), mbar_init(&st_empty[s], 1);
+    mbar_init(do_full, 1), mbar_init(do_empty, 1);
+    mbar_init(s_full, 1), mbar_init(p_full, kRowWarps), mbar_init(dp_full, 1), mbar_init(ds_full, kRowWarps);
     mbar_init(done, 1), mbar_init(drain, 1);
     *abort_flag = 0;
     fence_barrier_init();
@@ -899,29 +897,33 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       mbar_arrive_expect_tx(kv_full, 2 * F::kTileBytes);
       load_tile<kD>(k_at, &p.map_k, kv, begin + key0, kv_full);
       load_tile<kD>(v_at, &p.map_v, kv, begin + key0, kv_full);
-      int64_t i = 0, loaded_do = 0;
+      // The queries of a tile are there a tile earlier than its dout, which the next one's replaces as soon as dv has it.
+      int64_t i = 0, loaded = 0;
       bool ok = true;
-      for (int h = 0, b = 0; i < tiles; ++i) {
-        const int s = static_cast<int>(i & 1);
-        const int64_t row = begin + (first + b) * kTile;
-        if (!(ok = wait(&q_empty[s], (i >> 1) + 1))) break;
-        mbar_arrive_expect_tx(&q_full[s], F::kTileBytes);
-        load_tile<kD>(queries_at + s * F::kTileBytes, &p.map_q, kv * group + h, row, &q_full[s]);
-        if (!(ok = wait(&do_empty[s], (i >> 1) + 1))) {
-          ++i;
-          break;
-        }
-        mbar_arrive_expect_tx(&do_full[s], F::kTileBytes);
-        load_tile<kD>(douts_at + s * F::kTileBytes, &p.map_dout, kv * group + h, row, &do_full[s]);
-        ++loaded_do;
+      int h = 0, b = 0, slot = 0;
+      uint32_t phase = 0;
+      auto next_queries = [&] {
+        if (loaded == tiles) return true;
+        if (!wait(&q_empty[slot], phase ^ 1u)) return false;
+        mbar_arrive_expect_tx(&q_full[slot], F::kTileBytes);
+        load_tile<kD>(queries_at + slot * F::kTileBytes, &p.map_q, kv * group + h, begin + (first + b) * kTile, &q_full[slot]);
         if (++b == per_head) b = 0, ++h;
+        if (++slot == F::kQuerySlots) slot = 0, phase ^= 1u;
+        ++loaded;
+        return true;
+      };
+      ok = next_queries();
+      for (int ho = 0, bo = 0; ok && i < tiles; ++i) {
+        if (!(ok = next_queries()) || !(ok = wait(do_empty, i + 1))) break;
+        mbar_arrive_expect_tx(do_full, F::kTileBytes);
+        load_tile<kD>(dout_at, &p.map_dout, kv * group + ho, begin + (first + bo) * kTile, do_full);
+        if (++bo == per_head) bo = 0, ++ho;
       }
       if (!ok || *abort_flag) {
         wait_bounded(kv_full, 0, abort_flag, p.status, kDrainLimitNs, false);
-        for (int64_t t = i > 2 ? i - 2 : 0; t < i; ++t)
-          wait_bounded(&q_full[t & 1], (t >> 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
-        for (int64_t t = loaded_do > 2 ? loaded_do - 2 : 0; t < loaded_do; ++t)
-          wait_bounded(&do_full[t & 1], (t >> 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
+        for (int64_t t = loaded > F::kQuerySlots ? loaded - F::kQuerySlots : 0; t < loaded; ++t)
+          wait_bounded(&q_full[t % F::kQuerySlots], (t / F::kQuerySlots) & 1, abort_flag, p.status, kDrainLimitNs, false);
+        if (i > 0) wait_bounded(do_full, (i - 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
       }
     }
   } else if (warp == 17) {
@@ -930,55 +932,65 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     const int64_t n = static_cast<int64_t>(each) * group;
     const bool cut = __any_sync(0xffffffffu, ragged);
     auto all_wait = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-    int left = each;  // tiles of queries to come of the head whose scores are formed next
-    uint32_t patches = 0;
-    auto scores = [&](int s, uint32_t phase) {
-      bool there = all_wait(&q_full[s], phase) && all_wait(&st_full[s], phase);
+    int left = each, left_do = each;  // tiles to come of the head whose scores, whose dout . v are formed next
+    // A head's last tile of queries may end in rows of other sequences: whatever they hold meets p and ds of 0, and must be
+    // 0 too.
+    const int valid = __shfl_sync(0xffffffffu, static_cast<int>(length - (blocks - 1) * kTile), 0);
+    int qs = 0;  // slot of the next scores
+    uint32_t q_phase = 0;
+    auto scores = [&](uint32_t turn, int stage) {
+      if (!all_wait(&q_full[qs], q_phase) || !all_wait(&st_full[stage], turn >> 1)) return false;
       if (--left == 0) {
         left = each;
-        if (cut) there = there && all_wait(patched, patches++);
+        if (cut) clear_rows<kD>(queries + qs * F::kTileBytes, valid);
+        __syncwarp();
       }
-      if (!there) return false;
       tc_fence_after();
-      mma_rows<kD>(t_s, k_at, queries_at + s * F::kTileBytes);
-      mma_strips(t_s, ones_at, ones_at + (1 + 2 * s) * kStripBytes);
+      mma_rows<kD>(t_s, k_at, queries_at + qs * F::kTileBytes);
+      mma_strips(t_s, ones_at, ones_at + (1 + 2 * stage) * kStripBytes);
       mma_commit_elected(s_full);
+      if (++qs == F::kQuerySlots) qs = 0, q_phase ^= 1u;
       return true;
     };
-    auto along = [&](int s, uint32_t phase) {
-      if (!all_wait(&do_full[s], phase)) return false;
+    auto along = [&](uint32_t turn, int stage) {
+      if (!all_wait(do_full, turn)) return false;
+      if (--left_do == 0) {
+        left_do = each;
+        if (cut) clear_rows<kD>(dout, valid);
+        __syncwarp();
+      }
       tc_fence_after();
-      mma_rows<kD>(t_dp, v_at, douts_at + s * F::kTileBytes);
-      mma_strips(t_dp, ones_at, ones_at + (2 + 2 * s) * kStripBytes);
+      mma_rows<kD>(t_dp, v_at, dout_at);
+      mma_strips(t_dp, ones_at, ones_at + (2 + 2 * stage) * kStripBytes);
       mma_commit_elected(dp_full);
-      mma_commit_elected(&st_empty[s]);
+      mma_commit_elected(&st_empty[stage]);
       return true;
     };
     bool ok = all_wait(kv_full, 0) && scores(0, 0) && along(0, 0);
-    int s = 0;
-    uint32_t phase = 0, turn = 0;  // of the slot, of the rows' barriers
+    int slot = 0;  // of the queries that dk takes next
+    uint32_t turn = 0;  // the tile, modulo 4
     for (int64_t i = 0; ok && i < n; ++i) {
-      const int s1 = s ^ 1;
-      const uint32_t phase1 = s1 == 0 ? phase ^ 1u : phase;
+      const uint32_t turn1 = (turn + 1) & 3;
       if (!(ok = all_wait(p_full, turn))) break;
       tc_fence_after();
-      mma_columns<kD, true>(t_dv, t_s, douts_at + s * F::kTileBytes, i > 0);
-      mma_commit_elected(&do_empty[s]);
-      if (i + 1 < n && !(ok = scores(s1, phase1))) break;
+      mma_columns<kD, true>(t_dv, t_s, dout_at, i > 0);
+      mma_commit_elected(do_empty);
+      if (i + 1 < n && !(ok = scores(turn1, turn1 & 1))) break;
       if (!(ok = all_wait(ds_full, turn))) break;
       tc_fence_after();
-      mma_columns<kD, true>(t_dk, t_dp, queries_at + s * F::kTileBytes, i > 0);
-      mma_commit_elected(&q_empty[s]);
+      mma_columns<kD, true>(t_dk, t_dp, queries_at + slot * F::kTileBytes, i > 0);
+      mma_commit_elected(&q_empty[slot]);
       if (i + 1 == n) mma_commit_elected(done);
-      if (i + 1 < n) ok = along(s1, phase1);
-      s = s1, phase = phase1, turn ^= 1u;
+      if (i + 1 < n) ok = along(turn1, turn1 & 1);
+      if (++slot == F::kQuerySlots) slot = 0;
+      turn = turn1;
     }
     if (elect_one()) {
       mma_commit(drain);
       wait_bounded(drain, 0, abort_flag, p.status, kDrainLimitNs, false);
     }
   } else if (warp == 18) {
-    // ------------------------------------------------------------------ the queries' lse and D; rows of other sequences
+    // ------------------------------------------------------------------ the queries' lse and D
     // They enter the products as one more step of 16 columns, 1 for each key and the value in three bf16 terms for the
     // query: a thread has a key's row, so it would have to read every query's value from shared memory, whose time the
     // products need (1024 of 2800 cycles of a tile). The values are asked for a tile ahead.
@@ -1019,14 +1031,6 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
       __syncwarp();
       if (lane == 0) mbar_arrive(&st_full[s]);
       if (i + 1 < tiles) fetch();
-      if (ragged && last) {
-        ok = __all_sync(0xffffffffu, wait(&q_full[s], i >> 1) && wait(&do_full[s], i >> 1));
-        if (!ok) break;
-        clear_rows<kD>(queries + s * F::kTileBytes, valid);
-        clear_rows<kD>(douts + s * F::kTileBytes, valid);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(patched);
-      }
       if (last) b = 0;
     }
   } else {
