@@ -447,8 +447,9 @@ struct RotaryLaunch {
   int64_t axis_stride;
   int section_end[3];   // frequency j follows axis a where section_end[a - 1] <= j < section_end[a]
   uint64_t freqs[128];  // share of a revolution per position, in units of 2^-64
-  // Set by launch_rotary: lanes per row, parts of a token's heads, rows of partials (workspace), 1 / dim.
-  int lanes, parts, npartials, planning;
+  // Set by launch_rotary: lanes per row, parts of a token's heads, rows of partials (workspace), whether pairs of columns
+  // are aligned, 1 / dim.
+  int lanes, parts, npartials, planning, wide;
   float inv_dim;
   float* partials;
 };

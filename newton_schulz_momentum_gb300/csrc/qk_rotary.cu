@@ -14,8 +14,8 @@
 //
 // Each element is read once and written once. A lane holds both ends of its pairs, so a turn needs no exchange, and a
 // row's sums are shuffles among the lanes that hold it. A warp takes a token's heads one group after another: the
-// angles, their sines and cosines are formed once for all of them. Rows whose columns come in whole 16-byte pieces are
-// read so; others element by element.
+// angles, their sines and cosines are formed once for all of them, and the next group's elements are on their way while
+// this one's are turned. Lanes have 8 columns of a row whose columns come in aligned fours, else single pairs.
 #include <algorithm>
 
 #include "row_ops.h"
@@ -27,35 +27,89 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// What one lane holds of a row: item i covers columns [lo, lo + V) and [hi, hi + V). z[m] of the first piece and
-// z[V + m] of the second; pair m is z[first(m)] and z[second(m)].
+// What one lane holds of a row: item i is 2 V columns, those from lo on and V more from hi on; of interleaved pairs they
+// are neighbours (hi = lo + V). Pair m of an item is z[first(m)] and z[second(m)].
 template <int V, bool INTER>
 struct Pairs {
-  static __device__ __forceinline__ int first(int m) { return INTER && V > 1 ? 2 * m : m; }
-  static __device__ __forceinline__ int second(int m) { return INTER && V > 1 ? 2 * m + 1 : m + V; }
+  static __device__ __forceinline__ int first(int m) { return INTER ? 2 * m : m; }
+  static __device__ __forceinline__ int second(int m) { return INTER ? 2 * m + 1 : m + V; }
 };
 
+// An item as it lies in memory. Of single pairs, neighbours are one access where the array allows it (`wide`).
 template <typename T, int V>
-__device__ __forceinline__ void load_piece(float* z, const T* p) {
+struct Raw {
+  static constexpr int kWords = V * 2 * static_cast<int>(sizeof(T)) / 4;  // 32-bit words; a pair of bf16 is one
+  uint32_t w[kWords];
+};
+
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ Raw<T, V> load_item(const T* x, int lo, int hi, bool wide) {
+  Raw<T, V> r;
   if constexpr (V == 1) {
-    z[0] = row::to_f(*p);
+    if (INTER && wide) {
+      if constexpr (sizeof(T) == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(x + lo);
+        r.w[0] = u.x, r.w[1] = u.y;
+      } else {
+        r.w[0] = *reinterpret_cast<const uint32_t*>(x + lo);
+      }
+    } else if constexpr (sizeof(T) == 4) {
+      r.w[0] = *reinterpret_cast<const uint32_t*>(x + lo), r.w[1] = *reinterpret_cast<const uint32_t*>(x + hi);
+    } else {
+      r.w[0] = *reinterpret_cast<const uint16_t*>(x + lo) |
+               static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(x + hi)) << 16;
+    }
+  } else if constexpr (sizeof(T) == 4) {
+    const uint4 a = *reinterpret_cast<const uint4*>(x + lo), b = *reinterpret_cast<const uint4*>(x + hi);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w, r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
   } else {
-    float v[V];
-    row::unpack16<T>(v, *reinterpret_cast<const uint4*>(p));
-#pragma unroll
-    for (int m = 0; m < V; ++m) z[m] = v[m];
+    const uint2 a = *reinterpret_cast<const uint2*>(x + lo), b = *reinterpret_cast<const uint2*>(x + hi);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = b.x, r.w[3] = b.y;
   }
+  return r;
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void store_piece(T* p, const float* z) {
-  if constexpr (V == 1) {
-    *p = row::from_f<T>(z[0]);
-  } else {
-    float v[V];
+__device__ __forceinline__ void unpack_item(float (&z)[2 * V], const Raw<T, V>& r) {
 #pragma unroll
-    for (int m = 0; m < V; ++m) v[m] = z[m];
-    *reinterpret_cast<uint4*>(p) = row::pack16(v);
+  for (int k = 0; k < Raw<T, V>::kWords; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      z[k] = __uint_as_float(r.w[k]);
+    } else {
+      z[2 * k] = __uint_as_float(r.w[k] << 16);
+      z[2 * k + 1] = __uint_as_float(r.w[k] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <typename T, int V, bool INTER>
+__device__ __forceinline__ void store_item(T* y, int lo, int hi, bool wide, const float (&z)[2 * V]) {
+  uint32_t w[Raw<T, V>::kWords];
+#pragma unroll
+  for (int k = 0; k < Raw<T, V>::kWords; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      w[k] = __float_as_uint(z[k]);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
+      w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  if constexpr (V == 1) {
+    if (INTER && wide) {
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(y + lo) = w[0];
+    } else if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<uint32_t*>(y + lo) = w[0], *reinterpret_cast<uint32_t*>(y + hi) = w[1];
+    } else {
+      *reinterpret_cast<uint16_t*>(y + lo) = static_cast<uint16_t>(w[0]);
+      *reinterpret_cast<uint16_t*>(y + hi) = static_cast<uint16_t>(w[0] >> 16);
+    }
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<uint4*>(y + lo) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(y + hi) = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    *reinterpret_cast<uint2*>(y + lo) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(y + hi) = make_uint2(w[2], w[3]);
   }
 }
 
@@ -77,8 +131,8 @@ struct Place {
         lo[i] = INTER ? 2 * V * it : V * it;
         hi[i] = INTER ? lo[i] + V : lo[i] + half;
       } else {
-        lo[i] = p.rotary_dim + (it - turned) * V;
-        hi[i] = lo[i] + (p.dim - p.rotary_dim) / 2;
+        lo[i] = p.rotary_dim + (it - turned) * (INTER ? 2 * V : V);
+        hi[i] = lo[i] + (INTER ? V : (p.dim - p.rotary_dim) / 2);
       }
 #pragma unroll
       for (int m = 0; m < V; ++m) {
@@ -116,17 +170,16 @@ __device__ __forceinline__ float sum_lanes(float v, int lanes) {
   return v;
 }
 
-template <typename T, int V, int I>
-__device__ __forceinline__ void load_row(float (&z)[I][2 * V], const T* x, const int (&lo)[I], const int (&hi)[I],
-                                         const bool (&live)[I], bool ok) {
+// A group's rows; zeros where there is no head or no item.
+template <typename T, int V, int I, bool INTER>
+__device__ __forceinline__ void load_group(Raw<T, V> (&r)[I], const T* x, const Place<V, I, INTER>& at, bool ok, bool wide) {
 #pragma unroll
   for (int i = 0; i < I; ++i) {
-    if (ok && live[i]) {
-      load_piece<T, V>(z[i], x + lo[i]);
-      load_piece<T, V>(z[i] + V, x + hi[i]);
+    if (ok && at.live[i]) {
+      r[i] = load_item<T, V, INTER>(x, at.lo[i], at.hi[i], wide);
     } else {
 #pragma unroll
-      for (int m = 0; m < 2 * V; ++m) z[i][m] = 0.f;
+      for (int k = 0; k < Raw<T, V>::kWords; ++k) r[i].w[k] = 0u;
     }
   }
 }
@@ -170,11 +223,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       load_gain<V, I>(g, p.gain[w], at.lo, at.hi, at.live);
       const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
       T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      Raw<T, V> next[I];
+      load_group<T, V, I, INTER>(next, x + (first * per_warp + sub) * p.x_head[w], at, first * per_warp + sub < heads, p.wide);
       for (int group = first; group < groups; group += p.parts) {
-        const int h = group * per_warp + sub;
+        const int h = group * per_warp + sub, h1 = h + p.parts * per_warp;
         const bool ok = h < heads;
         float z[I][2 * V];
-        load_row<T, V, I>(z, x + h * p.x_head[w], at.lo, at.hi, at.live, ok);
+#pragma unroll
+        for (int i = 0; i < I; ++i) unpack_item<T, V>(z[i], next[i]);
+        if (group + p.parts < groups) load_group<T, V, I, INTER>(next, x + h1 * p.x_head[w], at, h1 < heads, p.wide);
         if (p.norm) {
           float sq = 0.f;
 #pragma unroll
@@ -196,10 +253,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             a = fmaf(a0, ca, -(b * sa));
             b = fmaf(b, ca, a0 * sa);
           }
-          if (ok && at.live[i]) {
-            store_piece<T, V>(y + h * p.y_head[w] + at.lo[i], z[i]);
-            store_piece<T, V>(y + h * p.y_head[w] + at.hi[i], z[i] + V);
-          }
+          if (ok && at.live[i]) store_item<T, V, INTER>(y + h * p.y_head[w], at.lo[i], at.hi[i], p.wide, z[i]);
         }
       }
     }
@@ -235,12 +289,20 @@ __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_cons
       const T* dy = static_cast<const T*>(p.dy[w]) + token * p.dy_token[w];
       const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
       T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      Raw<T, V> next_d[I], next_x[I];
+      const int h0 = first * per_warp + sub;
+      load_group<T, V, I, INTER>(next_d, dy + h0 * p.dy_head[w], at, h0 < heads, p.wide);
+      load_group<T, V, I, INTER>(next_x, x + h0 * p.x_head[w], at, p.norm && h0 < heads, p.wide);
       for (int group = first; group < groups; group += p.parts) {
-        const int h = group * per_warp + sub;
+        const int h = group * per_warp + sub, h1 = h + p.parts * per_warp;
         const bool ok = h < heads;
         float d[I][2 * V], z[I][2 * V];
-        load_row<T, V, I>(d, dy + h * p.dy_head[w], at.lo, at.hi, at.live, ok);
-        if (p.norm) load_row<T, V, I>(z, x + h * p.x_head[w], at.lo, at.hi, at.live, ok);
+#pragma unroll
+        for (int i = 0; i < I; ++i) unpack_item<T, V>(d[i], next_d[i]), unpack_item<T, V>(z[i], next_x[i]);
+        if (group + p.parts < groups) {
+          load_group<T, V, I, INTER>(next_d, dy + h1 * p.dy_head[w], at, h1 < heads, p.wide);
+          load_group<T, V, I, INTER>(next_x, x + h1 * p.x_head[w], at, p.norm && h1 < heads, p.wide);
+        }
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
@@ -271,10 +333,7 @@ __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_cons
         }
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          if (ok && at.live[i]) {
-            store_piece<T, V>(dx + h * p.y_head[w] + at.lo[i], d[i]);
-            store_piece<T, V>(dx + h * p.y_head[w] + at.hi[i], d[i] + V);
-          }
+          if (ok && at.live[i]) store_item<T, V, INTER>(dx + h * p.y_head[w], at.lo[i], at.hi[i], p.wide, d[i]);
       }
     }
   }
@@ -319,11 +378,11 @@ __global__ void __launch_bounds__(kJoinThreads) rotary_gain_kernel(const __grid_
   if (out) out[k % p.dim] = v;
 }
 
-bool whole_pieces(const RotaryLaunch& p, int v) {
+// Whether every row of every array starts at a multiple of `bytes`.
+bool aligned_rows(const RotaryLaunch& p, size_t bytes) {
   const size_t size = p.dtype == 0 ? 4 : 2;
-  if (p.rotary_dim % (2 * v) != 0 || (p.dim - p.rotary_dim) % (2 * v) != 0) return false;
   auto fits = [&](const void* ptr, int64_t token, int64_t head) {
-    return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && token * size % 16 == 0 && head * size % 16 == 0;
+    return reinterpret_cast<uintptr_t>(ptr) % bytes == 0 && token * size % bytes == 0 && head * size % bytes == 0;
   };
   for (int w = 0; w < 2; ++w) {
     if (p.heads[w] == 0) continue;
@@ -334,10 +393,10 @@ bool whole_pieces(const RotaryLaunch& p, int v) {
   return true;
 }
 
-// Lanes per row for pieces of v elements: the power of two that holds a row's items, at most a warp.
-int lanes_for(const RotaryLaunch& p, int v) {
+// Lanes per row, a power of two, for `each` items a lane.
+int lanes_for(int items, int each) {
   int lanes = 1;
-  while (lanes < 32 && lanes * 2 * v < p.dim) lanes *= 2;
+  while (lanes * each < items) lanes *= 2;
   return lanes;
 }
 
@@ -375,15 +434,26 @@ cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
 
 template <typename T, bool INTER>
 cudaError_t launch_type(RotaryLaunch& p, int sms, cudaStream_t stream) {
-  constexpr int V = 16 / sizeof(T);
-  if (whole_pieces(p, V)) {
-    p.lanes = lanes_for(p, V);
-    return launch_as<T, V, 1, INTER>(p, sms, stream);  // dim <= 256: at most 32 items
+  // Fours of bf16 rather than eights: half the registers, and twice the warps (16384 x 40 x 128: forward 90 us with
+  // eights, backward 245).
+  if (p.rotary_dim % 8 == 0 && p.dim % 8 == 0 && aligned_rows(p, 4 * sizeof(T))) {
+    p.lanes = lanes_for(p.dim / 8, 1);  // dim <= 256: at most 32
+    p.wide = 1;
+    return launch_as<T, 4, 1, INTER>(p, sms, stream);
   }
-  p.lanes = lanes_for(p, 1);
-  return p.dim <= 64 ? launch_as<T, 1, 1, INTER>(p, sms, stream)
-       : p.dim <= 128 ? launch_as<T, 1, 2, INTER>(p, sms, stream)
-                      : launch_as<T, 1, 4, INTER>(p, sms, stream);
+  // Pairs: as many to a lane as leave the fewest lanes idle (78 columns: 16 lanes of 3).
+  p.wide = aligned_rows(p, 2 * sizeof(T));
+  const int items = p.dim / 2;
+  int each = 4;
+  for (int e = 3; e >= 1; --e)
+    if (lanes_for(items, e) <= 32 && lanes_for(items, e) * e <= lanes_for(items, each) * each) each = e;
+  p.lanes = lanes_for(items, each);
+  switch (each) {
+    case 1: return launch_as<T, 1, 1, INTER>(p, sms, stream);
+    case 2: return launch_as<T, 1, 2, INTER>(p, sms, stream);
+    case 3: return launch_as<T, 1, 3, INTER>(p, sms, stream);
+    default: return launch_as<T, 1, 4, INTER>(p, sms, stream);
+  }
 }
 
 }  // namespace
