@@ -28,12 +28,35 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // What one lane holds of a row: item i is 2 V columns, those from lo on and V more from hi on; of interleaved pairs they
-// are neighbours (hi = lo + V). Pair m of an item is z[first(m)] and z[second(m)].
+// are neighbours (hi = lo + V). They are held by twos, an instruction's worth of fp32 operations; partner(z, k) are the
+// other ends of the pairs whose ends are z[k].
 template <int V, bool INTER>
-struct Pairs {
-  static __device__ __forceinline__ int first(int m) { return INTER ? 2 * m : m; }
-  static __device__ __forceinline__ int second(int m) { return INTER ? 2 * m + 1 : m + V; }
-};
+__device__ __forceinline__ float2 partner(const float2 (&z)[V], int k) {
+  if constexpr (V == 1 || INTER) return make_float2(z[k].y, z[k].x);
+  else return z[k ^ (V / 2)];
+}
+// Whether element e of an item is the first end of its pair, and the pair's number.
+template <int V, bool INTER>
+__device__ __forceinline__ constexpr bool first_end(int e) { return V == 1 || INTER ? e % 2 == 0 : e < V; }
+template <int V, bool INTER>
+__device__ __forceinline__ constexpr int pair_of(int e) { return V == 1 || INTER ? e / 2 : e % V; }
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 c;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(c))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return c;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // An item as it lies in memory. Of single pairs, neighbours are one access where the array allows it (`wide`).
 template <typename T, int V>
@@ -70,27 +93,23 @@ __device__ __forceinline__ Raw<T, V> load_item(const T* x, int lo, int hi, bool 
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void unpack_item(float (&z)[2 * V], const Raw<T, V>& r) {
+__device__ __forceinline__ void unpack_item(float2 (&z)[V], const Raw<T, V>& r) {
 #pragma unroll
-  for (int k = 0; k < Raw<T, V>::kWords; ++k) {
-    if constexpr (sizeof(T) == 4) {
-      z[k] = __uint_as_float(r.w[k]);
-    } else {
-      z[2 * k] = __uint_as_float(r.w[k] << 16);
-      z[2 * k + 1] = __uint_as_float(r.w[k] & 0xFFFF0000u);
-    }
+  for (int k = 0; k < V; ++k) {
+    if constexpr (sizeof(T) == 4) z[k] = make_float2(__uint_as_float(r.w[2 * k]), __uint_as_float(r.w[2 * k + 1]));
+    else z[k] = make_float2(__uint_as_float(r.w[k] << 16), __uint_as_float(r.w[k] & 0xFFFF0000u));
   }
 }
 
 template <typename T, int V, bool INTER>
-__device__ __forceinline__ void store_item(T* y, int lo, int hi, bool wide, const float (&z)[2 * V]) {
+__device__ __forceinline__ void store_item(T* y, int lo, int hi, bool wide, const float2 (&z)[V]) {
   uint32_t w[Raw<T, V>::kWords];
 #pragma unroll
-  for (int k = 0; k < Raw<T, V>::kWords; ++k) {
+  for (int k = 0; k < V; ++k) {
     if constexpr (sizeof(T) == 4) {
-      w[k] = __float_as_uint(z[k]);
+      w[2 * k] = __float_as_uint(z[k].x), w[2 * k + 1] = __float_as_uint(z[k].y);
     } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(z[2 * k], z[2 * k + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(z[k].x, z[k].y);
       w[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
@@ -166,7 +185,9 @@ struct Place {
 };
 
 __device__ __forceinline__ float sum_lanes(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
@@ -184,15 +205,14 @@ __device__ __forceinline__ void load_group(Raw<T, V> (&r)[I], const T* x, const 
   }
 }
 
-template <int V, int I>
-__device__ __forceinline__ void load_gain(float (&g)[I][2 * V], const float* gain, const int (&lo)[I], const int (&hi)[I],
-                                          const bool (&live)[I]) {
+template <int V, int I, bool INTER>
+__device__ __forceinline__ void load_gain(float2 (&g)[I][V], const float* gain, const Place<V, I, INTER>& at) {
 #pragma unroll
   for (int i = 0; i < I; ++i)
 #pragma unroll
-    for (int m = 0; m < V; ++m) {
-      g[i][m] = gain && live[i] ? __ldg(gain + lo[i] + m) : 1.f;
-      g[i][V + m] = gain && live[i] ? __ldg(gain + hi[i] + m) : 1.f;
+    for (int k = 0; k < V; ++k) {
+      const int c = 2 * k < V || V == 1 ? at.lo[i] + 2 * k : at.hi[i] + 2 * k - V, c1 = V == 1 ? at.hi[i] : c + 1;
+      g[i][k] = gain && at.live[i] ? make_float2(__ldg(gain + c), __ldg(gain + c1)) : make_float2(1.f, 1.f);
     }
 }
 
@@ -200,7 +220,6 @@ __device__ __forceinline__ void load_gain(float (&g)[I][2 * V], const float* gai
 // of queries come before those of keys, and part k of `parts` takes every parts-th of them.
 template <typename T, int V, int I, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p) {
-  using P = Pairs<V, INTER>;
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, sub = lane / p.lanes, per_warp = 32 / p.lanes;
   const Place<V, I, INTER> at(p, lane % p.lanes);
@@ -219,42 +238,52 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       if (first < 0) first += p.parts;
       before += groups;
       if (first >= groups) continue;
-      float g[I][2 * V];
-      load_gain<V, I>(g, p.gain[w], at.lo, at.hi, at.live);
-      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
-      T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      // y = rho (x gain cos + x' gain' sin), with the sign of the pair's end: both products' factors once per token.
+      float2 g[I][V], along[I][V], across[I][V];
+      load_gain<V, I, INTER>(g, p.gain[w], at);
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const float2 other = partner<V, INTER>(g[i], k);
+          const int m0 = i * V + pair_of<V, INTER>(2 * k), m1 = i * V + pair_of<V, INTER>(2 * k + 1);
+          along[i][k] = make_float2(g[i][k].x * c[m0], g[i][k].y * c[m1]);
+          across[i][k] = make_float2(other.x * (first_end<V, INTER>(2 * k) ? -s[m0] : s[m0]),
+                                     other.y * (first_end<V, INTER>(2 * k + 1) ? -s[m1] : s[m1]));
+        }
+      const int64_t step = static_cast<int64_t>(p.parts) * per_warp, h0 = first * per_warp + sub;
+      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w] + h0 * p.x_head[w];
+      T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h0 * p.y_head[w];
+      const int64_t step_x = step * p.x_head[w], step_y = step * p.y_head[w];
       Raw<T, V> next[I];
-      load_group<T, V, I, INTER>(next, x + (first * per_warp + sub) * p.x_head[w], at, first * per_warp + sub < heads, p.wide);
+      load_group<T, V, I, INTER>(next, x, at, h0 < heads, p.wide);
+      int h = static_cast<int>(h0);
       for (int group = first; group < groups; group += p.parts) {
-        const int h = group * per_warp + sub, h1 = h + p.parts * per_warp;
         const bool ok = h < heads;
-        float z[I][2 * V];
+        h += static_cast<int>(step);
+        x += step_x;
+        float2 z[I][V];
 #pragma unroll
         for (int i = 0; i < I; ++i) unpack_item<T, V>(z[i], next[i]);
-        if (group + p.parts < groups) load_group<T, V, I, INTER>(next, x + h1 * p.x_head[w], at, h1 < heads, p.wide);
+        if (group + p.parts < groups) load_group<T, V, I, INTER>(next, x, at, h < heads, p.wide);
+        float rho = 1.f;
         if (p.norm) {
-          float sq = 0.f;
+          float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
           for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int m = 0; m < 2 * V; ++m) sq = fmaf(z[i][m], z[i][m], sq);
-          const float rho = rsqrtf(fmaf(sum_lanes(sq, p.lanes), p.inv_dim, p.eps));
-#pragma unroll
-          for (int i = 0; i < I; ++i)
-#pragma unroll
-            for (int m = 0; m < 2 * V; ++m) z[i][m] = z[i][m] * rho * g[i][m];
+            for (int k = 0; k < V; ++k) sq = fma2(z[i][k], z[i][k], sq);
+          rho = rsqrtf(fmaf(sum_lanes(sq.x + sq.y, p.lanes), p.inv_dim, p.eps));
         }
 #pragma unroll
         for (int i = 0; i < I; ++i) {
+          float2 out[V];
 #pragma unroll
-          for (int m = 0; m < V; ++m) {
-            float &a = z[i][P::first(m)], &b = z[i][P::second(m)];
-            const float ca = c[i * V + m], sa = s[i * V + m], a0 = a;
-            a = fmaf(a0, ca, -(b * sa));
-            b = fmaf(b, ca, a0 * sa);
-          }
-          if (ok && at.live[i]) store_item<T, V, INTER>(y + h * p.y_head[w], at.lo[i], at.hi[i], p.wide, z[i]);
+          for (int k = 0; k < V; ++k)
+            out[k] = mul2(fma2(z[i][k], along[i][k], mul2(partner<V, INTER>(z[i], k), across[i][k])), both(rho));
+          if (ok && at.live[i]) store_item<T, V, INTER>(y, at.lo[i], at.hi[i], p.wide, out);
         }
+        y += step_y;
       }
     }
   }
@@ -263,13 +292,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 // y holds dx and x the norm's input; dy the gradient that arrives.
 template <typename T, int V, int I, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_constant__ RotaryLaunch p) {
-  using P = Pairs<V, INTER>;
   extern __shared__ float part_sums[];  // 2 x dim of each warp
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / p.lanes, per_warp = 32 / p.lanes;
   const Place<V, I, INTER> at(p, lane % p.lanes);
   ptx::griddep_wait();
-  float sums[2][I][2 * V] = {};
+  float2 sums[2][I][V] = {};
   const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < p.n * p.parts; unit += warps) {
     const int64_t token = unit / p.parts;
@@ -284,56 +312,64 @@ __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_cons
       if (first < 0) first += p.parts;
       before += groups;
       if (first >= groups) continue;
-      float g[I][2 * V];
-      load_gain<V, I>(g, p.gain[w], at.lo, at.hi, at.live);
-      const T* dy = static_cast<const T*>(p.dy[w]) + token * p.dy_token[w];
-      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w];
-      T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w];
+      float2 g[I][V], cos2[I][V], sin2[I][V];
+      load_gain<V, I, INTER>(g, p.gain[w], at);
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int m0 = i * V + pair_of<V, INTER>(2 * k), m1 = i * V + pair_of<V, INTER>(2 * k + 1);
+          cos2[i][k] = make_float2(c[m0], c[m1]);
+          sin2[i][k] = make_float2(first_end<V, INTER>(2 * k) ? s[m0] : -s[m0], first_end<V, INTER>(2 * k + 1) ? s[m1] : -s[m1]);
+        }
+      const int64_t step = static_cast<int64_t>(p.parts) * per_warp, h0 = first * per_warp + sub;
+      const T* dy = static_cast<const T*>(p.dy[w]) + token * p.dy_token[w] + h0 * p.dy_head[w];
+      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w] + h0 * p.x_head[w];
+      T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h0 * p.y_head[w];
+      const int64_t step_dy = step * p.dy_head[w], step_x = step * p.x_head[w], step_dx = step * p.y_head[w];
       Raw<T, V> next_d[I], next_x[I];
-      const int h0 = first * per_warp + sub;
-      load_group<T, V, I, INTER>(next_d, dy + h0 * p.dy_head[w], at, h0 < heads, p.wide);
-      load_group<T, V, I, INTER>(next_x, x + h0 * p.x_head[w], at, p.norm && h0 < heads, p.wide);
+      load_group<T, V, I, INTER>(next_d, dy, at, h0 < heads, p.wide);
+      load_group<T, V, I, INTER>(next_x, x, at, p.norm && h0 < heads, p.wide);
+      int h = static_cast<int>(h0);
       for (int group = first; group < groups; group += p.parts) {
-        const int h = group * per_warp + sub, h1 = h + p.parts * per_warp;
         const bool ok = h < heads;
-        float d[I][2 * V], z[I][2 * V];
+        h += static_cast<int>(step);
+        dy += step_dy, x += step_x;
+        float2 in[I][V], z[I][V], d[I][V];
 #pragma unroll
-        for (int i = 0; i < I; ++i) unpack_item<T, V>(d[i], next_d[i]), unpack_item<T, V>(z[i], next_x[i]);
+        for (int i = 0; i < I; ++i) unpack_item<T, V>(in[i], next_d[i]), unpack_item<T, V>(z[i], next_x[i]);
         if (group + p.parts < groups) {
-          load_group<T, V, I, INTER>(next_d, dy + h1 * p.dy_head[w], at, h1 < heads, p.wide);
-          load_group<T, V, I, INTER>(next_x, x + h1 * p.x_head[w], at, p.norm && h1 < heads, p.wide);
+          load_group<T, V, I, INTER>(next_d, dy, at, h < heads, p.wide);
+          load_group<T, V, I, INTER>(next_x, x, at, p.norm && h < heads, p.wide);
         }
 #pragma unroll
         for (int i = 0; i < I; ++i)
 #pragma unroll
-          for (int m = 0; m < V; ++m) {
-            float &a = d[i][P::first(m)], &b = d[i][P::second(m)];
-            const float ca = c[i * V + m], sa = s[i * V + m], a0 = a;
-            a = fmaf(a0, ca, b * sa);
-            b = fmaf(b, ca, -(a0 * sa));
-          }
+          for (int k = 0; k < V; ++k) d[i][k] = fma2(in[i][k], cos2[i][k], mul2(partner<V, INTER>(in[i], k), sin2[i][k]));
         if (p.norm) {
-          float sq = 0.f, along = 0.f;
+          float2 sq = make_float2(0.f, 0.f), along = sq;
 #pragma unroll
           for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int m = 0; m < 2 * V; ++m) {
-              sq = fmaf(z[i][m], z[i][m], sq);
-              along = fmaf(d[i][m] * g[i][m], z[i][m], along);
+            for (int k = 0; k < V; ++k) {
+              sq = fma2(z[i][k], z[i][k], sq);
+              along = fma2(mul2(d[i][k], g[i][k]), z[i][k], along);
             }
-          const float rho = rsqrtf(fmaf(sum_lanes(sq, p.lanes), p.inv_dim, p.eps));
-          const float back = rho * rho * (sum_lanes(along, p.lanes) * p.inv_dim);
+          const float rho = rsqrtf(fmaf(sum_lanes(sq.x + sq.y, p.lanes), p.inv_dim, p.eps));
+          const float back = -rho * rho * (sum_lanes(along.x + along.y, p.lanes) * p.inv_dim);
 #pragma unroll
           for (int i = 0; i < I; ++i)
 #pragma unroll
-            for (int m = 0; m < 2 * V; ++m) {
-              sums[w][i][m] = fmaf(d[i][m], z[i][m] * rho, sums[w][i][m]);
-              d[i][m] = rho * fmaf(-z[i][m], back, d[i][m] * g[i][m]);
+            for (int k = 0; k < V; ++k) {
+              const float2 hat = mul2(z[i][k], both(rho));
+              sums[w][i][k] = fma2(d[i][k], hat, sums[w][i][k]);
+              d[i][k] = fma2(hat, both(back), mul2(mul2(d[i][k], g[i][k]), both(rho)));
             }
         }
 #pragma unroll
         for (int i = 0; i < I; ++i)
-          if (ok && at.live[i]) store_item<T, V, INTER>(dx + h * p.y_head[w], at.lo[i], at.hi[i], p.wide, d[i]);
+          if (ok && at.live[i]) store_item<T, V, INTER>(dx, at.lo[i], at.hi[i], p.wide, d[i]);
+        dx += step_dx;
       }
     }
   }
@@ -345,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_cons
     for (int i = 0; i < I; ++i)
 #pragma unroll
       for (int m = 0; m < 2 * V; ++m) {
-        float v = sums[w][i][m];
+        float v = m % 2 ? sums[w][i][m / 2].y : sums[w][i][m / 2].x;
         for (int o = 16; o >= p.lanes; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         if (sub == 0 && at.live[i])
           part_sums[(warp * 2 + w) * p.dim + (m < V ? at.lo[i] + m : at.hi[i] + m - V)] = v;
