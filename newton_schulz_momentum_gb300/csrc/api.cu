@@ -1505,13 +1505,14 @@ int set_rotary(RotaryLaunch& p, int64_t heads, int64_t kv_heads, int dtype, cons
   }
   if (!freqs && (!(base > 0.0) || !std::isfinite(base)))
     return fail(DMUON_ERR_INVALID_ARG, "base must be finite and > 0");
+  const double per_pair = freqs || half == 0 ? 0.0 : -std::log2(base) / half;
   for (int j = 0; j < half; ++j) {
-    const double f = freqs ? freqs[j] : std::pow(base, -static_cast<double>(j) / half);
-    const double turns = f / 6.283185307179586476925287;  // revolutions per position
-    if (!std::isfinite(turns) || std::fabs(turns) > 1e9)
+    const double f = freqs ? freqs[j] : std::exp2(per_pair * j);
+    const double turns = f * 0.15915494309189533577;  // revolutions per position, of 1 / (2 pi)
+    if (!(std::fabs(turns) <= 1e9))
       return fail(DMUON_ERR_INVALID_ARG, "frequency %d is not finite or beyond 1e9 revolutions", j);
-    p.freqs[j] = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64) < 18446744073709551616.0
-                                           ? std::ldexp(turns - std::floor(turns), 64) : 0.0);
+    // The share of a revolution is below 1, and as a double at most 1 - 2^-53.
+    p.freqs[j] = static_cast<uint64_t>((turns - std::floor(turns)) * 18446744073709551616.0);
   }
   p.heads[0] = static_cast<int>(heads), p.heads[1] = static_cast<int>(kv_heads);
   p.gain[0] = q_gain, p.gain[1] = k_gain;

@@ -1114,11 +1114,21 @@ int64_t tiles_of(const AttentionLaunch& p) {
   return std::max<int64_t>(1, p.n / kTile + std::min(p.sequences, p.n));
 }
 
+constexpr int kMaxDevices = 64;
+
+// Heads are neighbours in the grid: the longest rows of all of them start first. `known`: the devices on which the
+// kernel's shared memory has been asked for (the caller holds the library's lock).
 template <typename K>
-cudaError_t launch_tiles(K* kernel, AttentionLaunch& p, int64_t slots, int heads, int threads, int smem, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+cudaError_t launch_tiles(K* kernel, bool (&known)[kMaxDevices], AttentionLaunch& p, int64_t slots, int heads, int threads,
+                         int smem, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  // Heads are neighbours in the grid: the longest rows of all of them start first.
+  if (dev >= kMaxDevices || !known[dev]) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) known[dev] = true;
+  }
   return row::launch(kernel, dim3(static_cast<unsigned>(slots * heads)), threads, smem, stream, p);
 }
 
@@ -1130,15 +1140,18 @@ cudaError_t launch_forward(AttentionLaunch& p, cudaStream_t stream) {
   int64_t slots = 0;
   if (!p.offsets) slots = p.sequences * (((p.n / p.sequences + kTile - 1) / kTile * group + 1) / 2);
   else slots = (tiles_of(p) * group + std::min(p.sequences, p.n)) / 2 + 1;
-  return launch_tiles(attention_kernel<kD>, p, slots, p.kv_heads, F::kThreads, F::kSmem, stream);
+  static bool known[kMaxDevices];
+  return launch_tiles(attention_kernel<kD>, known, p, slots, p.kv_heads, F::kThreads, F::kSmem, stream);
 }
 
 template <int kD>
 cudaError_t launch_backward(AttentionLaunch& p, cudaStream_t stream) {
   using F = Bwd<kD>;
-  const cudaError_t e = launch_tiles(attention_dq_kernel<kD>, p, tiles_of(p), p.heads, F::kThreads, F::kSmemQueries, stream);
+  static bool known[2][kMaxDevices];
+  const cudaError_t e =
+      launch_tiles(attention_dq_kernel<kD>, known[0], p, tiles_of(p), p.heads, F::kThreads, F::kSmemQueries, stream);
   if (e != cudaSuccess) return e;
-  return launch_tiles(attention_dkv_kernel<kD>, p, tiles_of(p), p.kv_heads, F::kThreads, F::kSmemKeys, stream);
+  return launch_tiles(attention_dkv_kernel<kD>, known[1], p, tiles_of(p), p.kv_heads, F::kThreads, F::kSmemKeys, stream);
 }
 
 cudaError_t set_maps(AttentionLaunch& p) {

@@ -436,11 +436,21 @@ int lanes_for(int items, int each) {
   return lanes;
 }
 
+constexpr int kMaxDevices = 64;
+
+// `known` holds what a kernel's occupancy on a device was found to be, for the largest `smem` (the caller holds the
+// library's lock).
 template <typename K>
-cudaError_t set_grid(RotaryLaunch& p, K* kernel, size_t smem, int sms, int64_t* ctas) {
-  int per_sm = 0;
-  const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+cudaError_t set_grid(RotaryLaunch& p, K* kernel, int (&known)[kMaxDevices], size_t smem, int sms, int64_t* ctas) {
+  int dev = 0, per_sm = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev < kMaxDevices) per_sm = known[dev];
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) known[dev] = per_sm;
+  }
   const int64_t resident = static_cast<int64_t>(sms) * std::max(per_sm, 1);
   // A token's heads are shared out where there are fewer tokens than warps.
   const int per_warp = 32 / p.lanes;
@@ -452,14 +462,15 @@ cudaError_t set_grid(RotaryLaunch& p, K* kernel, size_t smem, int sms, int64_t* 
 
 template <typename T, int V, int I, bool INTER>
 cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  static int known[2][kMaxDevices];
   int64_t ctas = 0;
   if (!p.grad) {
-    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, 0, sms, &ctas);
+    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, known[0], 0, sms, &ctas);
     if (e != cudaSuccess) return e;
     return row::launch(rotary_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, stream, p);
   }
   const size_t smem = sizeof(float) * 2 * p.dim * kWarps;
-  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, smem, sms, &ctas);
+  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, known[1], sizeof(float) * 2 * 256 * kWarps, sms, &ctas);
   if (e != cudaSuccess) return e;
   p.npartials = static_cast<int>(ctas);
   if (p.planning) return cudaSuccess;

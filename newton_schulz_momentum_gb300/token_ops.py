@@ -319,6 +319,9 @@ def _head_array(t, name, dev, shape, dtype):
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.is_contiguous():
+        dim = shape[-1]
+        return t.data_ptr(), shape[-2] * dim, dim
     return (t.data_ptr(),) + _heads(t, name)[3:]
 
 
@@ -326,11 +329,20 @@ def _new(t):
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections, interleaved, eps):
-    """(heads of k, the C calls' arguments from dtype to sections)."""
-    n, heads, dim, _, _ = _heads(q, "q")
-    if k is not None and (k.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != dim):
+def _new_heads(t):
+    """A new tensor like t, and its (address, token stride, head stride)."""
+    new = _new(t)
+    dim = t.shape[-1]
+    return new, (new.data_ptr(), t.shape[-2] * dim, dim)
+
+
+def _like_q(k, q):
+    if k.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
         raise ValueError("k must have q's tokens and head length")
+
+
+def _rotary_args(dev, q, n, dim, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections, interleaved, eps):
+    """The C calls' arguments from dtype to sections."""
     rotary_dim = dim if rotary_dim is None else rotary_dim
     axes, axis_list = 1, None
     tokens = q.shape[:-2]
@@ -346,9 +358,8 @@ def _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, f
         if len(freqs) != rotary_dim // 2:
             raise ValueError(f"freqs must have rotary_dim / 2 = {rotary_dim // 2} elements, not {len(freqs)}")
         freqs = (ctypes.c_double * max(len(freqs), 1))(*freqs)
-    return 0 if k is None else k.shape[-2], heads, (
-        _code(q, "q"), _vector(q_gain, "q_gain", dev, dim), _vector(k_gain, "k_gain", dev, dim), 1 if norm else 0, eps, n,
-        dim, rotary_dim, 1 if interleaved else 0, base, freqs, pos, id_bytes, axes, n, axis_list)
+    return (_code(q, "q"), _vector(q_gain, "q_gain", dev, dim), _vector(k_gain, "k_gain", dev, dim), 1 if norm else 0, eps,
+            n, dim, rotary_dim, 1 if interleaved else 0, base, freqs, pos, id_bytes, axes, n, axis_list)
 
 
 _NO_HEADS = (None, 0, 0)
@@ -367,17 +378,23 @@ def qk_norm_rotary(q, k, positions, q_gain=None, k_gain=None, norm=True, rotary_
     if dev < 0 or dev != _current_device():
         return _elsewhere(qk_norm_rotary, _device(q, "q"), q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs,
                           sections, interleaved, eps, q_out, k_out, stream)
-    kv_heads, heads, turns = _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections,
-                                          interleaved, eps)
-    q_out = _new(q) if q_out is None else q_out
-    k_at = k_out_at = _NO_HEADS
+    n, heads, dim, token, head = _heads(q, "q")
+    turns = _rotary_args(dev, q, n, dim, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections, interleaved, eps)
+    if q_out is None:
+        q_out, q_out_at = _new_heads(q)
+    else:
+        q_out_at = _head_array(q_out, "q_out", dev, q.shape, q.dtype)
+    kv_heads, k_at, k_out_at = 0, _NO_HEADS, _NO_HEADS
     if k is None:
         k_out = None
     else:
-        k_out = _new(k) if k_out is None else k_out
-        k_at, k_out_at = _head_array(k, "k", dev, k.shape, q.dtype), _head_array(k_out, "k_out", dev, k.shape, q.dtype)
-    status = lib().dmuon_qk_norm_rotary(*_head_array(q, "q", dev, q.shape, q.dtype), heads, *k_at, kv_heads, *turns,
-                                        *_head_array(q_out, "q_out", dev, q.shape, q.dtype), *k_out_at,
+        _like_q(k, q)
+        kv_heads, k_at = k.shape[-2], _head_array(k, "k", dev, k.shape, q.dtype)
+        if k_out is None:
+            k_out, k_out_at = _new_heads(k)
+        else:
+            k_out_at = _head_array(k_out, "k_out", dev, k.shape, q.dtype)
+    status = lib().dmuon_qk_norm_rotary(q.data_ptr(), token, head, heads, *k_at, kv_heads, *turns, *q_out_at, *k_out_at,
                                         _stream(stream, dev))
     if status:
         _check(status)
@@ -393,33 +410,38 @@ def qk_norm_rotary_grad(dq_out, dk_out, q, k, positions, q_gain=None, k_gain=Non
     if dev < 0 or dev != _current_device():
         return _elsewhere(qk_norm_rotary_grad, _device(q, "q"), dq_out, dk_out, q, k, positions, q_gain, k_gain, norm,
                           rotary_dim, base, freqs, sections, interleaved, eps, dq, dk, stream)
-    kv_heads, heads, turns = _rotary_args(dev, q, k, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections,
-                                          interleaved, eps)
-    dq = _new(q) if dq is None else dq
-    k_at = dk_out_at = dk_at = _NO_HEADS
+    n, heads, dim, token, head = _heads(q, "q")
+    turns = _rotary_args(dev, q, n, dim, positions, q_gain, k_gain, norm, rotary_dim, base, freqs, sections, interleaved, eps)
+    if dq is None:
+        dq, dq_at = _new_heads(q)
+    else:
+        dq_at = _head_array(dq, "dq", dev, q.shape, q.dtype)
+    kv_heads, k_at, dk_out_at, dk_at = 0, _NO_HEADS, _NO_HEADS, _NO_HEADS
     if k is None:
         dk = None
     else:
-        dk = _new(k) if dk is None else dk
-        k_at, dk_out_at, dk_at = (_head_array(t, name, dev, k.shape, q.dtype) for t, name in
-                                  ((k, "k"), (dk_out, "dk_out"), (dk, "dk")))
-    dq_gain = None if q_gain is None else torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
-    dk_gain = None if k_gain is None or k is None else torch.empty(q.shape[-1], dtype=torch.float32, device=q.device)
+        _like_q(k, q)
+        kv_heads, k_at = k.shape[-2], _head_array(k, "k", dev, k.shape, q.dtype)
+        dk_out_at = _head_array(dk_out, "dk_out", dev, k.shape, q.dtype)
+        if dk is None:
+            dk, dk_at = _new_heads(k)
+        else:
+            dk_at = _head_array(dk, "dk", dev, k.shape, q.dtype)
+    dq_gain = None if q_gain is None else torch.empty(dim, dtype=torch.float32, device=q.device)
+    dk_gain = None if k_gain is None or k is None else torch.empty(dim, dtype=torch.float32, device=q.device)
     status = lib().dmuon_qk_norm_rotary_grad(
-        *_head_array(dq_out, "dq_out", dev, q.shape, q.dtype), *_head_array(q, "q", dev, q.shape, q.dtype), heads,
-        *dk_out_at, *k_at, kv_heads, *turns, *_head_array(dq, "dq", dev, q.shape, q.dtype), *dk_at,
-        None if dq_gain is None else dq_gain.data_ptr(), None if dk_gain is None else dk_gain.data_ptr(),
-        _stream(stream, dev))
+        *_head_array(dq_out, "dq_out", dev, q.shape, q.dtype), q.data_ptr(), token, head, heads, *dk_out_at, *k_at,
+        kv_heads, *turns, *dq_at, *dk_at, None if dq_gain is None else dq_gain.data_ptr(),
+        None if dk_gain is None else dk_gain.data_ptr(), _stream(stream, dev))
     if status:
         _check(status)
     return dq, dk, dq_gain, dk_gain
 
 
 def _prompts(dev, q, k, offsets, causal, scale, zero_outside):
-    """(number of tokens, heads, the C calls' arguments from dtype to zero_outside) of an attention call."""
-    n, heads, dim, _, _ = _heads(q, "q")
-    if k.dim() < 3 or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != dim:
-        raise ValueError("k must have q's tokens and head length")
+    """(number of tokens, heads, the C calls' q, their arguments from dtype to zero_outside) of an attention call."""
+    n, heads, dim, token, head = _heads(q, "q")
+    _like_q(k, q)
     if q.dtype is not torch.bfloat16:
         raise ValueError(f"q must be {torch.bfloat16}, not {q.dtype}")
     if offsets is None:
@@ -429,8 +451,9 @@ def _prompts(dev, q, k, offsets, causal, scale, zero_outside):
         if offsets.dim() != 1 or offsets.numel() < 1:
             raise ValueError("offsets must be a list of one more elements than sequences")
         sequences = offsets.numel() - 1
-    return n, heads, (BF16, n, heads, k.shape[-2], dim, at, id_bytes, sequences, 1 if causal else 0,
-                      dim ** -0.5 if scale is None else scale, 1 if zero_outside else 0)
+    return n, heads, (q.data_ptr(), token, head), (
+        BF16, n, heads, k.shape[-2], dim, at, id_bytes, sequences, 1 if causal else 0,
+        dim ** -0.5 if scale is None else scale, 1 if zero_outside else 0)
 
 
 def attention(q, k, v, offsets=None, causal=True, scale=None, out=None, lse=None, stream=None):
@@ -445,15 +468,18 @@ def attention(q, k, v, offsets=None, causal=True, scale=None, out=None, lse=None
     dev = q.get_device()
     if dev < 0 or dev != _current_device():
         return _elsewhere(attention, _device(q, "q"), q, k, v, offsets, causal, scale, out, lse, stream)
-    n, heads, prompts = _prompts(dev, q, k, offsets, causal, scale, out is None and lse is None)
+    n, heads, q_at, prompts = _prompts(dev, q, k, offsets, causal, scale, out is None and lse is None)
     given = out is not None
-    if not given:
-        out = _new(q) if lse is None else torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    if given:
+        out_at = _head_array(out, "out", dev, q.shape, q.dtype)
+    else:
+        out, out_at = _new_heads(q)
+        if lse is not None:
+            out.zero_()
     if lse is None:
         lse = (torch.zeros if given else torch.empty)((heads, n), dtype=torch.float32, device=q.device)
-    status = lib().dmuon_attention(*_head_array(q, "q", dev, q.shape, q.dtype), *_head_array(k, "k", dev, k.shape, q.dtype),
-                                   *_head_array(v, "v", dev, k.shape, q.dtype), *prompts,
-                                   *_head_array(out, "out", dev, q.shape, q.dtype),
+    status = lib().dmuon_attention(*q_at, *_head_array(k, "k", dev, k.shape, q.dtype),
+                                   *_head_array(v, "v", dev, k.shape, q.dtype), *prompts, *out_at,
                                    _vector(lse, "lse", dev, heads * n), _stream(stream, dev))
     if status:
         _check(status)
@@ -469,18 +495,25 @@ def attention_grad(dout, q, k, v, out, lse, offsets=None, causal=True, scale=Non
         return _elsewhere(attention_grad, _device(q, "q"), dout, q, k, v, out, lse, offsets, causal, scale, dq, dk, dv,
                           stream)
     all_new = dq is None and dk is None and dv is None
-    n, heads, prompts = _prompts(dev, q, k, offsets, causal, scale, all_new)
-    new = _new if all_new else torch.zeros_like
-    dq, dk, dv = (new(like) if t is None else t for t, like in ((dq, q), (dk, k), (dv, k)))
-    arrays = [_head_array(t, name, dev, like.shape, q.dtype) for t, name, like in (
-        (dout, "dout", q), (q, "q", q), (k, "k", k), (v, "v", k), (out, "out", q), (dq, "dq", q), (dk, "dk", k),
-        (dv, "dv", k))]
-    status = lib().dmuon_attention_grad(*arrays[0], *arrays[1], *arrays[2], *arrays[3], *arrays[4],
-                                        _vector(lse, "lse", dev, heads * n), *prompts, *arrays[5], *arrays[6],
-                                        *arrays[7], _stream(stream, dev))
+    n, heads, q_at, prompts = _prompts(dev, q, k, offsets, causal, scale, all_new)
+    grads, places = [], []
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+        if t is None:
+            t, at = _new_heads(like)
+            if not all_new:
+                t.zero_()
+        else:
+            at = _head_array(t, name, dev, like.shape, q.dtype)
+        grads.append(t)
+        places += at
+    status = lib().dmuon_attention_grad(*_head_array(dout, "dout", dev, q.shape, q.dtype), *q_at,
+                                        *_head_array(k, "k", dev, k.shape, q.dtype),
+                                        *_head_array(v, "v", dev, k.shape, q.dtype),
+                                        *_head_array(out, "out", dev, q.shape, q.dtype),
+                                        _vector(lse, "lse", dev, heads * n), *prompts, *places, _stream(stream, dev))
     if status:
         _check(status)
-    return dq, dk, dv
+    return tuple(grads)
 
 
 class TokenStats(NamedTuple):
