@@ -2365,6 +2365,8 @@ int dmuon_token_stats(const void* logits, int dtype, int64_t ld, int64_t n, int6
     set_temperature(scales, temperature);
     p.inv_temperature = scales.inv_temperature, p.inv_temperature_low = scales.inv_temperature_low;
     p.log2e_over_t = scales.log2e_over_t;
+    // Its product with log2(e) / T is finite.
+    p.low = -std::ldexp(1.f, 126 - std::max(0, std::ilogb(p.log2e_over_t) + 1));
     p.logp = targets ? logp : nullptr, p.entropy = entropy, p.norm = norm, p.top_logp = top_logp, p.top_ids = top_ids;
     p.status = ds->status;
     cudaStream_t stream = static_cast<cudaStream_t>(cuda_stream);

@@ -467,6 +467,7 @@ struct StatsLaunch {
   const void* targets;  // may be null: every row counts
   int id_bytes, top;
   float inv_temperature, inv_temperature_low, log2e_over_t;
+  float low;  // what smaller logits, -infinity among them, are taken as
   float *logp, *entropy, *norm;  // logp null without targets; norm: largest logit and sum of each row
   float* top_logp;               // n x top
   int64_t* top_ids;

@@ -7,12 +7,16 @@
 // h = dL/dH:  dL/dx_j = 1 / T (g (1[j = a] - p_j) - h p_j (lp_j + H)).
 //
 // A row is read once for all of it. The threads of a CTA (of a cluster's CTAs where there are few rows) each keep the
-// largest logit, s and u = sum of y 2^y, y = (x - m) log2(e) / T, of their own granules, rescaled where the largest
-// logit grows, and join them at the end. The alternatives come from a bound: the threads form 64 groups (32 in a CTA
-// of one warp), at least `top` of which hold an element as large as the top-th largest of the groups' maxima, so only
-// elements that reach it can be alternatives: a few more than `top` of them as a rule, in as many threads, whose
-// granules alone are read again. Where equal logits make them more than the list holds, the row is walked once more in
-// order, the list cut down to its `top` best whenever it is full.
+// largest logit of their own granules and, with k = log2(e) / T and c = m k as rounded, s = sum of 2^(x k - c) and
+// u = sum of (x k - c) 2^(x k - c), rescaled where the largest logit grows; they join them at the end, where what the
+// rounding of c left is taken out again (m k - c, which fma gives exactly). Logits of -infinity, and those below
+// `low` = -2^126 (T times that below T = 1.44), are taken as `low`, so that no product is infinity times 0.
+//
+// The alternatives come from a bound: the threads form 64 groups (32 in a CTA of one warp), at least `top` of which hold
+// an element as large as the top-th largest of the groups' maxima, so only elements that reach it can be alternatives: a
+// few more than `top` of them as a rule, in as many threads, whose granules alone are read again. Where equal logits make
+// them more than the list holds, the row is walked once more in order, the list cut down to its `top` best whenever it
+// is full.
 #include <algorithm>
 
 #include "row_ops.h"
@@ -23,8 +27,7 @@ namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxTop = kMaxAlternatives;
-constexpr int kList = 1024;      // candidates in shared memory; at least kMaxTop and a thread's element each
-constexpr float kLowest = -1e30f;  // in place of -infinity in y: 2^y is 0 and so is y 2^y
+constexpr float kLowest = -1e30f;  // in place of smaller exponents y: 2^y is 0 and so is y 2^y
 
 // 2^x, within 2 units of the last place; below 2^-126 it is 0.
 __device__ __forceinline__ float pow2(float x) {
@@ -46,30 +49,69 @@ __device__ __forceinline__ float key_logit(uint64_t key) {
 }
 __device__ __forceinline__ uint32_t key_column(uint64_t key) { return 0xffffffffu - static_cast<uint32_t>(key); }
 
-// m: largest logit; s = sum of 2^y, u = sum of y 2^y with y = (x - m) k.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)),
+        "l"(reinterpret_cast<const unsigned long long&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(c))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return c;
+}
+
+// The larger of two, NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
+// A granule's elements, those below `low` as `low`. (A power of two: bf16 holds it.)
+template <typename T>
+__device__ __forceinline__ void raise(uint4& raw, float low) {
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      w[k] = __float_as_uint(max_nan(__uint_as_float(w[k]), low));
+    } else {
+      const __nv_bfloat162 v = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), __float2bfloat162_rn(low));
+      w[k] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  raw = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// m: largest logit; c: what x k is taken from; s = sum of 2^y, u = sum of y 2^y with y = x k - c.
 struct Sums {
-  float m, s, u;
+  float m, c, s, u;
 };
 
-__device__ __forceinline__ void rescale(Sums& t, float m, float k) {
-  const float by = fmaxf((t.m - finite_or_zero(m)) * k, kLowest), f = pow2(by);
+__device__ __forceinline__ void rescale(Sums& t, float m, float c) {
+  const float by = fmaxf(t.c - c, kLowest), f = pow2(by);  // times s it stays finite
   t.u = f * fmaf(by, t.s, t.u);
   t.s *= f;
-  t.m = m;
+  t.m = m, t.c = c;
 }
 
-__device__ __forceinline__ Sums join(Sums a, Sums b, float k) {
-  const float m = fmaxf(a.m, b.m);
-  rescale(a, m, k);
-  rescale(b, m, k);
-  return {m, a.s + b.s, a.u + b.u};
+__device__ __forceinline__ Sums join(Sums a, Sums b) {
+  const float m = fmaxf(a.m, b.m), c = fmaxf(a.c, b.c);  // c goes with m
+  rescale(a, m, c);
+  rescale(b, m, c);
+  return {m, c, a.s + b.s, a.u + b.u};
 }
 
-__device__ __forceinline__ Sums join_warp(Sums t, float k) {
+__device__ __forceinline__ Sums join_warp(Sums t) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.s, o),
-                 __shfl_xor_sync(0xffffffffu, t.u, o)}, k);
+    t = join(t, {__shfl_xor_sync(0xffffffffu, t.m, o), __shfl_xor_sync(0xffffffffu, t.c, o),
+                 __shfl_xor_sync(0xffffffffu, t.s, o), __shfl_xor_sync(0xffffffffu, t.u, o)});
   return t;
 }
 
@@ -103,6 +145,7 @@ struct RowCut {
 
 template <int W>
 struct StatsShared {
+  static constexpr int kList = W == 1 ? 256 : 1024;  // at least kMaxTop and an element of each thread
   Sums sums[W];
   float group_max[64];
   float bound;
@@ -131,13 +174,14 @@ __device__ __forceinline__ void best_of(StatsShared<W>& sh, const uint64_t* list
 template <int W>
 __device__ __forceinline__ void push(StatsShared<W>& sh, float v, int64_t column) {
   const int at = atomicAdd(&sh.list_count, 1);
-  if (at < kList) sh.list[at] = key_of(v, static_cast<uint32_t>(column));
+  if (at < StatsShared<W>::kList) sh.list[at] = key_of(v, static_cast<uint32_t>(column));
 }
 
 // Alternatives of this CTA's elements into sh.best. `mine` is the thread's largest logit; its granules are those of
 // thread `thread` of `threads`, from granule `thread` on.
 template <typename T, int W>
-__device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, float mine, int top, int rank, int ctas) {
+__device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, float mine, float low, int top, int rank,
+                         int ctas) {
   constexpr int E = 16 / sizeof(T), kCta = W * 32, kGroups = W == 1 ? 32 : 64, kPerGroup = kCta / kGroups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t threads = static_cast<int64_t>(kCta) * ctas;
@@ -168,12 +212,13 @@ __device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, f
   for (int q = warp; q < hot; q += W) {
     const int64_t thread = static_cast<int64_t>(rank) * kCta + sh.hot[q];
     if (lane == 0 && thread < edges) {
-      const float v = row::to_f(x[cut.edge(static_cast<int>(thread))]);
+      const float v = max_nan(row::to_f(x[cut.edge(static_cast<int>(thread))]), low);
       if (v >= bound) push(sh, v, cut.edge(static_cast<int>(thread)));
     }
     for (int64_t i = thread + lane * threads; i < cut.full; i += 32 * threads) {
       float v[E];
-      const uint4 raw = granules[i];
+      uint4 raw = granules[i];
+      raise<T>(raw, low);
       if (!(largest<T>(raw) >= bound)) continue;
       row::unpack16<T>(v, raw);
 #pragma unroll
@@ -182,7 +227,7 @@ __device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, f
     }
   }
   __syncthreads();
-  if (sh.list_count <= kList) {
+  if (sh.list_count <= StatsShared<W>::kList) {
     best_of(sh, sh.list, sh.list_count, top);
     return;
   }
@@ -196,13 +241,13 @@ __device__ void find_top(StatsShared<W>& sh, const T* x, const RowCut<T>& cut, f
   for (int64_t c0 = static_cast<int64_t>(rank) * kCta; c0 < columns; c0 += threads) {
     const int64_t c = c0 + threadIdx.x;
     if (c < columns) {
-      const float v = row::to_f(x[c]);
+      const float v = max_nan(row::to_f(x[c]), low);
       const uint64_t key = key_of(v, static_cast<uint32_t>(c));
       if (v == v && key > least) push(sh, v, c);
     }
     __syncthreads();
     const int count = sh.list_count;
-    if (count > kList - kCta || c0 + threads >= columns) {
+    if (count > StatsShared<W>::kList - kCta || c0 + threads >= columns) {
       best_of(sh, sh.list, count, top);
       least = sh.best[top - 1];
       if (static_cast<int>(threadIdx.x) < top && sh.best[threadIdx.x]) sh.list[threadIdx.x] = sh.best[threadIdx.x];
@@ -250,52 +295,60 @@ __global__ void __launch_bounds__(W * 32) token_stats_kernel(const __grid_consta
   }
   const T* x = static_cast<const T*>(p.logits) + i * p.ld;
   const RowCut<T> cut(x, p.vocab);
-  const float k = p.log2e_over_t;
+  const float k = p.log2e_over_t, low = p.low;
   const int64_t threads = static_cast<int64_t>(kCta) * ctas, thread = static_cast<int64_t>(rank) * kCta + threadIdx.x;
   const uint4* granules = reinterpret_cast<const uint4*>(x + cut.head);
-  Sums t{-INFINITY, 0.f, 0.f};
+  Sums t{low, low * k, 0.f, 0.f};
   auto grow = [&](float m) {
-    if (m > t.m) rescale(t, m, k);
-  };
-  auto add = [&](float v, float base) {
-    const float y = (v - base) * k, e = pow2(y);
-    t.s += e;
-    t.u = fmaf(fmaxf(y, kLowest), e, t.u);
+    if (m > t.m) rescale(t, m, m * k);
   };
   if (thread < cut.head + cut.tail) {
-    const float v = row::to_f(x[cut.edge(static_cast<int>(thread))]);
+    const float v = max_nan(row::to_f(x[cut.edge(static_cast<int>(thread))]), low);
     grow(v);
-    add(v, finite_or_zero(t.m));
+    const float y = fmaf(v, k, -t.c), e = pow2(y);
+    t.s += e;
+    t.u = fmaf(y, e, t.u);
   }
   for (int64_t g = thread; g < cut.full; g += kBatch * threads) {
     uint4 raw[kBatch];
     // Behind the row's end the batch repeats its first granule; only its maximum is taken from there.
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) raw[b] = granules[g + b * threads < cut.full ? g + b * threads : g];
-    float m = largest<T>(raw[0]);
+    float m = low;
 #pragma unroll
-    for (int b = 1; b < kBatch; ++b) m = fmaxf(m, largest<T>(raw[b]));
+    for (int b = 0; b < kBatch; ++b) {
+      raise<T>(raw[b], low);
+      m = fmaxf(m, largest<T>(raw[b]));
+    }
     grow(m);
-    const float base = finite_or_zero(t.m);
+    const float2 k2 = make_float2(k, k), c2 = make_float2(-t.c, -t.c);
+    float2 s2 = make_float2(0.f, 0.f), u2 = s2;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (g + b * threads >= cut.full) break;
       float v[E];
       row::unpack16<T>(v, raw[b]);
 #pragma unroll
-      for (int e = 0; e < E; ++e) add(v[e], base);
+      for (int e = 0; e < E; e += 2) {
+        const float2 y = fma2(make_float2(v[e], v[e + 1]), k2, c2);
+        const float2 q = make_float2(pow2(y.x), pow2(y.y));
+        s2 = add2(s2, q);
+        u2 = fma2(y, q, u2);
+      }
     }
+    t.s += s2.x + s2.y;
+    t.u += u2.x + u2.y;
   }
   const float mine = t.m;
-  t = join_warp(t, k);
+  t = join_warp(t);
   if ((threadIdx.x & 31) == 0) sh.sums[threadIdx.x >> 5] = t;
   __syncthreads();
   if (threadIdx.x == 0) {
     t = sh.sums[0];
-    for (int w = 1; w < W; ++w) t = join(t, sh.sums[w], k);
+    for (int w = 1; w < W; ++w) t = join(t, sh.sums[w]);
     sh.total = t;
   }
-  if (p.top > 0) find_top<T, W>(sh, x, cut, mine, p.top, rank, ctas);
+  if (p.top > 0) find_top<T, W>(sh, x, cut, mine, low, p.top, rank, ctas);
   else __syncthreads();
   const uint64_t* best = sh.best;
   if (ctas > 1) {
@@ -311,7 +364,7 @@ __global__ void __launch_bounds__(W * 32) token_stats_kernel(const __grid_consta
         for (int c = 1; c < ctas; ++c) {
           const uint32_t from = ptx::map_shared(ptx::smem_u32(&sh.total), c);
           all = join(all, {__uint_as_float(load_cluster(from)), __uint_as_float(load_cluster(from + 4)),
-                           __uint_as_float(load_cluster(from + 8))}, k);
+                           __uint_as_float(load_cluster(from + 8)), __uint_as_float(load_cluster(from + 12))});
         }
         sh.total = all;
       }
@@ -322,17 +375,19 @@ __global__ void __launch_bounds__(W * 32) token_stats_kernel(const __grid_consta
     if (p.top > 0) best_of(sh, sh.of_cluster, ctas * p.top, p.top);
   }
   t = sh.total;
-  // Logarithm of s; a row of nothing but -infinity has no distribution: NaN.
-  const float base = finite_or_zero(t.m), log_s = t.m == -INFINITY ? NAN : logf(t.s);
+  // From c to m itself, and the logarithm of s. A row of nothing but -infinity has no distribution: NaN.
+  const bool none = t.m == low;
+  const float back = fmaf(t.m, k, -t.c), f = pow2(-back);
+  const float sum = t.s * f, along = f * fmaf(-back, t.s, t.u), log_s = none ? NAN : logf(sum);
   auto logp_of = [&](float v) {
-    const float d = v - base;  // -infinity stays what it is: the inverse's second part may be 0 or negative
-    return d == -INFINITY ? d - log_s : fmaf(d, p.inv_temperature, fmaf(d, p.inv_temperature_low, -log_s));
+    const float d = v - t.m;
+    return v <= low ? -INFINITY - log_s : fmaf(d, p.inv_temperature, fmaf(d, p.inv_temperature_low, -log_s));
   };
   if (threadIdx.x == 0) {
     if (p.targets) p.logp[i] = logp_of(row::to_f(x[a]));
-    p.entropy[i] = fmaf(-kLn2 / t.s, t.u, log_s);
-    p.norm[2 * i] = t.m;
-    p.norm[2 * i + 1] = t.s;
+    p.entropy[i] = fmaf(-kLn2 / sum, along, log_s);
+    p.norm[2 * i] = none ? -INFINITY : t.m;
+    p.norm[2 * i + 1] = sum;
   }
   for (int q = threadIdx.x; q < p.top; q += kCta) {
     const uint64_t key = best[q];
