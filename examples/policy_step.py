@@ -1,5 +1,5 @@
-"""Policy-gradient steps of a small language model: embedding, residual RMS norms, a clipped policy loss with a KL
-term, and the Muon optimizer, all on libdmuon's kernels; matrix products and attention are torch's.
+"""Policy-gradient steps of a small language model: embedding, residual RMS norms, rotated positions, causal attention, a
+clipped policy loss with a KL term, and the Muon optimizer, all on libdmuon's kernels; matrix products are torch's.
 
     python examples/policy_step.py [--steps 20] [--vocab 32000] [--dim 512] [--layers 4]
 
@@ -34,14 +34,16 @@ class Block(torch.nn.Module):
         super().__init__()
         self.heads = heads
         self.norm_attn, self.norm_mlp = dm.AddRMSNorm(dim), dm.AddRMSNorm(dim)
+        self.rotary, self.attention = dm.QKNormRotary(dim // heads, norm=False), dm.Attention()
         self.qkv, self.out = Linear(dim, 3 * dim), Linear(dim, dim)
         self.up, self.down = Linear(dim, 4 * dim), Linear(4 * dim, dim)
 
     def forward(self, x, h):
         y, h = self.norm_attn(x, h)
         b, t, d = y.shape
-        q, k, v = self.qkv(y).view(b, t, 3, self.heads, d // self.heads).permute(2, 0, 3, 1, 4)
-        x = self.out(F.scaled_dot_product_attention(q, k, v, is_causal=True).transpose(1, 2).reshape(b, t, d))
+        q, k, v = self.qkv(y).view(b, t, 3, self.heads, d // self.heads).unbind(2)
+        q, k = self.rotary(q, k, torch.arange(t, device="cuda").expand(b, t))
+        x = self.out(self.attention(q, k, v).view(b, t, d))
         y, h = self.norm_mlp(x, h)
         return self.down(F.gelu(self.up(y))), h
 
@@ -73,7 +75,8 @@ def train(steps=20, vocab=32000, dim=512, layers=4, batch=8, length=128, seed=0,
         with torch.no_grad():
             logits = model(prompt).view(-1, vocab)
             targets = torch.distributions.Categorical(logits=logits.float()).sample()
-            old_logp = dm.token_logprobs(logits, targets)
+            drawn = dm.token_stats(logits, targets)
+            old_logp = drawn.logp
         reward = (targets % 2 == 0).float()
         advantages = (reward - reward.mean()) / (reward.std() + 1e-6)
         weights = torch.full_like(reward, 1.0 / reward.numel())
@@ -87,7 +90,7 @@ def train(steps=20, vocab=32000, dim=512, layers=4, batch=8, length=128, seed=0,
             opt.step()
         rewards.append(reward.mean())
         report(f"step {step}: reward {float(reward.mean()):.3f}  loss {float(loss):+.4f}  "
-               f"log-ratio {float((logp - old_logp).mean()):+.4f}")
+               f"log-ratio {float((logp - old_logp).mean()):+.4f}  entropy {float(drawn.entropy.mean()):.3f}")
     dm.check_status()
     return [float(r) for r in rewards]
 
