@@ -84,9 +84,11 @@ struct Place {
   int64_t begin, length, piece;  // length 0: there are fewer pieces
 };
 
-// By one warp. Without offsets the sequences are equal; otherwise 32 of them at a time.
+// By one warp. Without offsets the sequences are equal; otherwise 128 of them at a time, four to a lane, since a look
+// at memory takes a microsecond however little is read.
 template <typename F>
 __device__ __forceinline__ Place find_place(const AttentionLaunch& p, int64_t slot, F&& per) {
+  constexpr int kEach = 4;
   const int lane = threadIdx.x & 31;
   Place at{0, 0, 0};
   if (!p.offsets) {
@@ -94,11 +96,17 @@ __device__ __forceinline__ Place find_place(const AttentionLaunch& p, int64_t sl
     if (s < p.sequences) at = {s * len, len, slot - s * pieces};
     return at;
   }
-  for (int64_t s0 = 0; s0 < p.sequences; s0 += 32) {
-    int64_t begin = 0;
-    const int64_t len = s0 + lane < p.sequences ? sequence_length(p, s0 + lane, &begin) : 0;
-    const int64_t pieces = len > 0 ? per(len) : 0;
-    int64_t sum = pieces;
+  for (int64_t s0 = 0; s0 < p.sequences; s0 += 32 * kEach) {
+    int64_t begin[kEach], len[kEach], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int64_t s = s0 + lane * kEach + k;
+      begin[k] = len[k] = 0;
+      if (s < p.sequences) len[k] = sequence_length(p, s, &begin[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) sum += len[k] > 0 ? per(len[k]) : 0;
+    const int64_t mine = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int64_t left = __shfl_up_sync(0xffffffffu, sum, o);
@@ -106,10 +114,17 @@ __device__ __forceinline__ Place find_place(const AttentionLaunch& p, int64_t sl
     }
     const unsigned behind = __ballot_sync(0xffffffffu, slot < sum);
     if (behind) {
+      int64_t piece = slot - (sum - mine);
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const int64_t pieces = len[k] > 0 ? per(len[k]) : 0;
+        if (at.length == 0 && piece < pieces) at = {begin[k], len[k], piece};
+        piece -= pieces;
+      }
       const int l = __ffs(behind) - 1;
-      at.begin = __shfl_sync(0xffffffffu, begin, l);
-      at.length = __shfl_sync(0xffffffffu, len, l);
-      at.piece = slot - __shfl_sync(0xffffffffu, sum - pieces, l);
+      at.begin = __shfl_sync(0xffffffffu, at.begin, l);
+      at.length = __shfl_sync(0xffffffffu, at.length, l);
+      at.piece = __shfl_sync(0xffffffffu, at.piece, l);
       return at;
     }
     slot -= __shfl_sync(0xffffffffu, sum, 31);
@@ -732,20 +747,30 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     const int64_t token = begin + (live ? row0 + r : 0);
     const float sl2 = p.scale * kLog2e, lse2 = live ? p.lse[static_cast<int64_t>(head) * p.n + token] * kLog2e : INFINITY;
     // D of the rows, 16 lanes to one: read by a thread each, a load would touch 32 rows (16 warps: 16000 cycles).
-    for (int q = warp * 8 + (lane >> 4); q < warp * 8 + 8; q += 2) {
-      const int64_t row = begin + (row0 + q < length ? row0 + q : 0);
+    {
+      uint4 o[4], g[4];
       const int c = (lane & 15) * 8;
-      float d = 0.f;
-      if (c < p.dim) {
-        float a[8], b[8];
-        row::unpack16<bf16>(a, *reinterpret_cast<const uint4*>(at(p.out, row, head) + c));
-        row::unpack16<bf16>(b, *reinterpret_cast<const uint4*>(at(p.dout, row, head) + c));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d = fmaf(a[e], b[e], d);
+      for (int k = 0; k < 4; ++k) {
+        const int q = warp * 8 + 2 * k + (lane >> 4);
+        const int64_t row = begin + (row0 + q < length ? row0 + q : 0);
+        o[k] = g[k] = make_uint4(0, 0, 0, 0);
+        if (c < p.dim) {
+          o[k] = *reinterpret_cast<const uint4*>(at(p.out, row, head) + c);
+          g[k] = *reinterpret_cast<const uint4*>(at(p.dout, row, head) + c);
+        }
       }
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if ((lane & 15) == 0) row_delta[q] = d;
+      for (int k = 0; k < 4; ++k) {
+        float a[8], b[8], d = 0.f;
+        row::unpack16<bf16>(a, o[k]);
+        row::unpack16<bf16>(b, g[k]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d = fmaf(a[e], b[e], d);
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        if ((lane & 15) == 0) row_delta[warp * 8 + 2 * k + (lane >> 4)] = d;
+      }
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kRowWarps * 32) : "memory");  // nothing above waits: all of them come
     float delta = row_delta[r];
