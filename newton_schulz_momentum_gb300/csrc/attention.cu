@@ -139,14 +139,14 @@ __device__ __forceinline__ bf16* out_at(const HeadArray& a, int64_t token, int64
   return static_cast<bf16*>(const_cast<void*>(a.data)) + token * a.token + head * a.head;
 }
 
-// Zeros in the rows of tokens that belong to no sequence, spread over the grid's CTAs and their threads.
+// Zeros in the rows of tokens that belong to no sequence, spread over the grid's CTAs; by a warp of each that has time.
 __device__ __forceinline__ void zero_rows_outside(const AttentionLaunch& p, const HeadArray& a, int heads, float* lse) {
   if (!p.offsets || !p.zero_outside) return;
   const int64_t first = row::load_id(p.offsets, p.id_bytes, 0), last = row::load_id(p.offsets, p.id_bytes, p.sequences);
   const int64_t before = first < 0 ? 0 : first > p.n ? p.n : first, from = last < before ? before : last > p.n ? p.n : last;
   const int64_t rows = (before + p.n - from) * heads;
-  const int64_t thread = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (int64_t r = thread; r < rows; r += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+  const int64_t lane = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+  for (int64_t r = lane; r < rows; r += static_cast<int64_t>(gridDim.x) * 32) {
     const int64_t k = r / heads, head = r - k * heads, token = k < before ? k : from + (k - before);
     bf16* x = out_at(a, token, head);
     for (int c = 0; c < p.dim; c += 8) *reinterpret_cast<uint4*>(x + c) = make_uint4(0, 0, 0, 0);
@@ -275,6 +275,38 @@ __device__ __forceinline__ Unit unit_at(const AttentionLaunch& p, int64_t length
   return {static_cast<int>(kv * group + unit - back * group), static_cast<int>(p.causal ? block + 1 : blocks), block * kTile};
 }
 
+// A warp's 32 rows of kCols columns of an accumulator from taddr on, times each lane's f, to `out` as bf16: the first
+// `rows` rows, `stride` elements apart, and `columns` columns. Through `stage` (64 kCols bytes of shared memory), so that
+// neighbouring lanes store neighbouring 16 bytes: of a row each, a store would touch 32 rows.
+template <int kCols>
+__device__ __forceinline__ void store_block(uint8_t* stage, uint32_t taddr, float f, bf16* out, int64_t stride, int rows,
+                                            int columns) {
+  constexpr int kChunks = kCols / 8;  // of 16 bytes in a row
+  constexpr int kTurn = kChunks < 8 ? kChunks - 1 : 7;
+  const int lane = threadIdx.x & 31, turn = kChunks < 8 ? (lane >> 1) & kTurn : lane & kTurn;
+#pragma unroll
+  for (int c = 0; c < kCols; c += 32) {
+    uint32_t r[32];
+    tmem_ld32_issue(taddr + c, r);
+    tmem_ld_wait(r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[8 * k + e]) * f;
+      *reinterpret_cast<uint4*>(stage + (lane * kChunks + ((c / 8 + k) ^ turn)) * 16) = row::pack16(v);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    const int id = k * 32 + lane, row = id / kChunks, chunk = id % kChunks;
+    const int at = chunk ^ (kChunks < 8 ? (row >> 1) & kTurn : row & kTurn);
+    if (row < rows && chunk * 8 < columns)
+      *reinterpret_cast<uint4*>(out + row * stride + chunk * 8) = *reinterpret_cast<uint4*>(stage + (row * kChunks + at) * 16);
+  }
+}
+
 // A row of outputs times f; seldom run, so a few columns at a time beside the 128 scores that the thread holds.
 template <int kD>
 __device__ __forceinline__ void scale_outputs(uint32_t tmem_out, float f) {
@@ -328,12 +360,14 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
-  zero_rows_outside(p, p.out, p.heads, p.lse);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
-  if (length == 0) return;
+  if (length == 0) {
+    if (warp == 0) zero_rows_outside(p, p.out, p.heads, p.lse);
+    return;
+  }
   const Unit units[2] = {unit_at(p, length, 2 * place.piece, kv), unit_at(p, length, 2 * place.piece + 1, kv)};
   const int tiles = max(units[0].tiles, units[1].tiles);
   // Of the last tile's values the rows behind the sequence are someone else's: whatever they hold meets probabilities of
@@ -379,6 +413,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
         if (lane == 0) mbar_arrive(patched);
       }
     }
+    zero_rows_outside(p, p.out, p.heads, p.lse);
     if (lane == 0 && (!ok || *abort_flag)) {
       wait_bounded(q_full, 0, abort_flag, p.status, kDrainLimitNs, false);
       for (int s = 0; s < F::kSlots; ++s)
@@ -513,20 +548,12 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
         const float total = sum.x + sum.y, inverse = 1.f / total;
         const bool live = u.row + r < length;
         const int64_t token = begin + u.row + r;
-        bf16* out = out_at(p.out, live ? token : begin, u.head);
-#pragma unroll
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32_issue(t_o + c, o);
-          tmem_ld_wait(o);
-#pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[k + e]) * inverse;
-            if (live && c + k < p.dim) *reinterpret_cast<uint4*>(out + c + k) = row::pack16(v);
-          }
-        }
+        // Over the unit's queries, which no product reads any more.
+        const int64_t left = length - u.row - (warp & 3) * 32;
+        if (left > 0)
+          store_block<kD>(smem + j * F::kTileBytes + (warp & 3) * 64 * kD, t_o, inverse,
+                          out_at(p.out, begin + u.row + (warp & 3) * 32, u.head), p.out.token,
+                          static_cast<int>(left < 32 ? left : 32), p.dim);
         if (live) p.lse[static_cast<int64_t>(u.head) * p.n + token] =
             kLn2 * ((top == -INFINITY ? 0.f : top * sl2) + log2f(total));
       }
@@ -588,20 +615,6 @@ __device__ __forceinline__ void load_part(uint32_t taddr, float (&v)[kPart]) {
   for (int k = 0; k < kPart; ++k) v[k] = __uint_as_float(r[k]);
 }
 
-// 32 columns from taddr on of an accumulator, times f, to `out` as bf16.
-__device__ __forceinline__ void store_columns(uint32_t taddr, float f, bf16* out, int columns) {
-  uint32_t r[32];
-  tmem_ld32_issue(taddr, r);
-  tmem_ld_wait(r);
-#pragma unroll
-  for (int k = 0; k < 32; k += 8) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(r[k + e]) * f;
-    if (k < columns) *reinterpret_cast<uint4*>(out + k) = row::pack16(v);
-  }
-}
-
 template <int kD>
 __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(const __grid_constant__ AttentionLaunch p) {
   using F = Bwd<kD>;
@@ -647,12 +660,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
-  zero_rows_outside(p, p.dq, p.heads, nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
-  if (length == 0) return;
+  if (length == 0) {
+    if (warp == 0) zero_rows_outside(p, p.dq, p.heads, nullptr);
+    return;
+  }
   constexpr uint32_t t_s = 0, t_dp = kTile, t_dq = 3 * kTile;
   const int64_t blocks = (length + kTile - 1) / kTile, block = blocks - 1 - place.piece, row0 = block * kTile;  // long rows first
   const int tiles = static_cast<int>(p.causal ? block + 1 : blocks);
@@ -692,6 +707,7 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
         if (lane == 0) mbar_arrive(patched);
       }
     }
+    zero_rows_outside(p, p.dq, p.heads, nullptr);
     if (lane == 0 && (!ok || *abort_flag)) {
       wait_bounded(q_full, 0, abort_flag, p.status, kDrainLimitNs, false);
       for (int t = max(0, i - F::kKeySlots); t < i; ++t)
@@ -844,10 +860,11 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
     if (ok) {
       tc_fence_after();
       if (live && part == 0) p.delta[static_cast<int64_t>(head) * p.n + token] = delta;
-      bf16* out = out_at(p.dq, token, head);
-#pragma unroll
-      for (int c = part * kPart; c < kD; c += kTile)
-        store_columns(t_dq + lanes + c, p.scale, out + c, live ? p.dim - c : 0);
+      const int64_t first = row0 + (warp & 3) * 32, left = length - first;
+      if (part * kPart < kD && left > 0)  // over keys, which no product reads any more
+        store_block<kPart>(keys + warp * 64 * kPart, t_dq + lanes + part * kPart, p.scale,
+                           out_at(p.dq, begin + first, head) + part * kPart, p.dq.token,
+                           static_cast<int>(left < 32 ? left : 32), p.dim - part * kPart);
     }
   }
   __syncwarp();
@@ -902,13 +919,14 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
-  zero_rows_outside(p, p.dk, p.kv_heads, nullptr);
-  zero_rows_outside(p, p.dv, p.kv_heads, nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const int64_t begin = place.begin, length = place.length;
-  if (length == 0) return;
+  if (length == 0) {
+    if (warp == 0) zero_rows_outside(p, p.dk, p.kv_heads, nullptr), zero_rows_outside(p, p.dv, p.kv_heads, nullptr);
+    return;
+  }
   constexpr uint32_t t_s = 0, t_dp = kTile, t_dv = 2 * kTile, t_dk = 3 * kTile;
   const int64_t blocks = (length + kTile - 1) / kTile, key0 = place.piece * kTile, first = p.causal ? place.piece : 0;
   const int per_head = static_cast<int>(blocks - first);  // tiles of queries
@@ -951,6 +969,9 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
         if (i > 0) wait_bounded(do_full, (i - 1) & 1, abort_flag, p.status, kDrainLimitNs, false);
       }
     }
+    __syncwarp();
+    zero_rows_outside(p, p.dk, p.kv_heads, nullptr);
+    zero_rows_outside(p, p.dv, p.kv_heads, nullptr);
   } else if (warp == 17) {
     // ------------------------------------------------------------------ products
     const int each = __shfl_sync(0xffffffffu, per_head, 0);
@@ -1115,13 +1136,15 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
     if (ok) ok = __all_sync(0xffffffffu, wait(done, 0));
     if (ok) {
       tc_fence_after();
-      const bool live = key0 + r < length;
-      const int64_t token = begin + key0 + (live ? r : 0);
-      const bool keys = part >= 2;  // two parts store dv, two dk
-      bf16* out = out_at(keys ? p.dk : p.dv, token, kv);
-#pragma unroll
-      for (int c = (part & 1) * kPart; c < kD; c += 2 * kPart)
-        store_columns((keys ? t_dk : t_dv) + lanes + c, keys ? p.scale : 1.f, out + c, live ? p.dim - c : 0);
+      // Two parts store dv, two dk, half of the columns each; over keys and values, which no product reads any more.
+      constexpr int kCols = kD / 2;
+      const bool is_key = part >= 2;
+      const int c = (part & 1) * kCols;
+      const int64_t first_key = key0 + (warp & 3) * 32, left_keys = length - first_key;
+      if (left_keys > 0)
+        store_block<kCols>(smem + warp * 64 * kCols, (is_key ? t_dk : t_dv) + lanes + c, is_key ? p.scale : 1.f,
+                           out_at(is_key ? p.dk : p.dv, begin + first_key, kv) + c, is_key ? p.dk.token : p.dv.token,
+                           static_cast<int>(left_keys < 32 ? left_keys : 32), p.dim - c);
     }
   }
   __syncwarp();
