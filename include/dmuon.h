@@ -457,6 +457,7 @@ DMUON_API int dmuon_qk_norm_rotary_grad(const void* dq_out, int64_t dq_out_token
  *   zero_outside  tokens before the first and behind the last sequence: 0 leaves their rows of out and lse as they
  *               were, otherwise they become 0. They are not read.
  *   lse         device, heads x n, fp32
+ * n is at most 2^30; scale is a finite number other than 0.
  * Sums, the largest and the running maximum are fp32; probabilities are rounded to bf16 for their product with v. A
  * value that is not finite reaches no other sequence; within a causal one it may reach earlier tokens too, up to 127.
  */
@@ -493,7 +494,8 @@ DMUON_API int dmuon_attention_grad(const void* dout, int64_t dout_token, int64_t
  *             dmuon_check_status.
  *   top       0 to 32, at most vocab; top_logp (fp32) and top_ids (int64) are n x top
  *   norm      device, n x 2, fp32: the row's largest logit m and the sum of exp((x - m) / temperature)
- * Logits of -infinity are tokens of probability 0. A row that holds NaN or +infinity, or nothing but -infinity, gives
+ * Logits of -infinity are tokens of probability 0, and so are those below -2^126 (times the temperature where that is
+ * below 1.44). A row that holds NaN or +infinity, or nothing but -infinity, gives
  * NaN; its ids are those of its largest numbers, -1 where there are no more of them. Exponentials as in
  * dmuon_policy_loss.
  */
