@@ -184,26 +184,172 @@ struct Place {
   }
 };
 
-__device__ __forceinline__ float sum_lanes(float v, int lanes) {
+// Each of the sums over the lanes of a row.
+template <int N>
+__device__ __forceinline__ void sum_lanes(float (&v)[N], int lanes) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < lanes) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    if (o < lanes) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
 }
 
-// A group's rows; zeros where there is no head or no item.
-template <typename T, int V, int I, bool INTER>
-__device__ __forceinline__ void load_group(Raw<T, V> (&r)[I], const T* x, const Place<V, I, INTER>& at, bool ok, bool wide) {
+// The first group of tensor w that part `part` of a token's heads has.
+__device__ __forceinline__ int first_group(const RotaryLaunch& p, int w, int part, int per_warp) {
+  if (p.parts == 1) return 0;
+  const int first = (part - (w ? (p.heads[0] + per_warp - 1) / per_warp : 0)) % p.parts;
+  return first < 0 ? first + p.parts : first;
+}
+
+// 4, 8 or 16 bytes into shared memory, asynchronously; zeros if not `ok`, whatever is at src.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(__cvta_generic_to_global(src)), "n"(kBytes),
+               "r"(ok ? kBytes : 0)
+               : "memory");
+}
+
+// The rows of `kArrays` arrays that a warp takes: batches of G groups of a tensor's heads, across tensors and tokens alike,
+// so that a token's first rows are on their way while the last of the one before are turned. They come through shared
+// memory, kStages batches ahead, every lane its own (so a lane waits for its copies alone); single pairs of bf16, whose
+// ends may be 2 bytes each, through registers, one batch ahead.
+template <typename T, int V, int I, bool INTER, int G, int kStages, int kArrays>
+struct Rows {
+  static constexpr bool kShared = V > 1 || sizeof(T) == 4;
+  static constexpr int kPiece = V * sizeof(T);                       // of a lane's item, twice
+  static constexpr int kOther = V == 1 ? 4 : kPiece * 32;            // from a lane's lower piece to its upper one
+  static constexpr int kBatch = kArrays * G * I * 2 * kPiece * 32;   // bytes of a warp's batch
+  int64_t unit;
+  int w, group, h, slot, taken;
+  const T* at[kArrays];
+  uint32_t ring;
+  Raw<T, V> next[kShared ? 1 : kArrays][kShared ? 1 : G][I];
+
+  __device__ __forceinline__ static const void* base(const RotaryLaunch& p, int a, int w) { return a ? p.x[w] : kArrays > 1 ? p.dy[w] : p.x[w]; }
+  __device__ __forceinline__ static int64_t token_stride(const RotaryLaunch& p, int a, int w) {
+    return a || kArrays == 1 ? p.x_token[w] : p.dy_token[w];
+  }
+  __device__ __forceinline__ static int64_t head_stride(const RotaryLaunch& p, int a, int w) {
+    return a || kArrays == 1 ? p.x_head[w] : p.dy_head[w];
+  }
+  // The next tensor of which this warp has groups, from w of the current unit on.
+  __device__ __forceinline__ void find(const RotaryLaunch& p, int64_t units, int64_t warps, int per_warp, int sub) {
+    for (; unit < units; unit += warps, w = 0) {
+      const int64_t token = p.parts == 1 ? unit : unit / p.parts;
+      const int part = static_cast<int>(unit - token * p.parts);
+      for (; w < 2; ++w) {
+        const int first = first_group(p, w, part, per_warp);
+        if (first * per_warp >= p.heads[w]) continue;
+        group = first, h = first * per_warp + sub;
 #pragma unroll
-  for (int i = 0; i < I; ++i) {
-    if (ok && at.live[i]) {
-      r[i] = load_item<T, V, INTER>(x, at.lo[i], at.hi[i], wide);
-    } else {
-#pragma unroll
-      for (int k = 0; k < Raw<T, V>::kWords; ++k) r[i].w[k] = 0u;
+        for (int a = 0; a < kArrays; ++a)
+          at[a] = static_cast<const T*>(base(p, a, w)) + token * token_stride(p, a, w) + h * head_stride(p, a, w);
+        return;
+      }
     }
   }
-}
+  __device__ __forceinline__ void ask(const RotaryLaunch& p, const Place<V, I, INTER>& place, int64_t units, int64_t warps,
+                                      int per_warp, int sub) {
+    if (unit < units) {
+      const int step = p.parts * per_warp;
+#pragma unroll
+      for (int u = 0; u < G; ++u) {
+        const bool ok = h + u * step < p.heads[w];
+#pragma unroll
+        for (int a = 0; a < kArrays; ++a) {
+          const bool wanted = ok && (a == 0 || p.norm);
+          const T* row = at[a] + static_cast<int64_t>(u * step) * head_stride(p, a, w);
+          if constexpr (kShared) {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+              const uint32_t dst = ring + slot * kBatch + ((a * G + u) * I + i) * 2 * kPiece * 32;
+              const bool live = wanted && place.live[i];
+              const void* lo = live ? static_cast<const void*>(row + place.lo[i]) : base(p, 0, 0);
+              if (V == 1 && INTER && p.wide) {
+                copy_async<8>(dst, lo, live);
+              } else {
+                copy_async<kPiece>(dst, lo, live);
+                copy_async<kPiece>(dst + kOther, live ? static_cast<const void*>(row + place.hi[i]) : lo, live);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+              if (wanted && place.live[i]) {
+                next[a][u][i] = load_item<T, V, INTER>(row, place.lo[i], place.hi[i], p.wide);
+              } else {
+#pragma unroll
+                for (int k = 0; k < Raw<T, V>::kWords; ++k) next[a][u][i].w[k] = 0u;
+              }
+            }
+          }
+        }
+      }
+      group += G * p.parts, h += G * step;
+      if (group * per_warp >= p.heads[w]) {
+        ++w;
+        find(p, units, warps, per_warp, sub);
+      } else {
+#pragma unroll
+        for (int a = 0; a < kArrays; ++a) at[a] += static_cast<int64_t>(G * step) * head_stride(p, a, w);
+      }
+    }
+    if constexpr (kShared) {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      if (++slot == kStages) slot = 0;
+    }
+  }
+  __device__ __forceinline__ Rows(const RotaryLaunch& p, const Place<V, I, INTER>& place, uint8_t* smem, int64_t first_unit,
+                                  int64_t units, int64_t warps, int per_warp, int sub)
+      : unit(first_unit), w(0), slot(0), taken(0) {
+    if constexpr (kShared)
+      ring = ptx::smem_u32(smem) + (threadIdx.x >> 5) * kStages * kBatch + (threadIdx.x & 31) * (V == 1 ? 8 : kPiece);
+    find(p, units, warps, per_warp, sub);
+#pragma unroll 1
+    for (int k = 0; k < (kShared ? kStages : 1); ++k) ask(p, place, units, warps, per_warp, sub);
+  }
+  // The oldest batch, as fp32; and another is asked for in its place.
+  __device__ __forceinline__ void take(float2 (&z)[kArrays][G][I][V], const RotaryLaunch& p, const Place<V, I, INTER>& place,
+                                       int64_t units, int64_t warps, int per_warp, int sub) {
+    if constexpr (kShared) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      Raw<T, V> raw[kArrays][G][I];
+#pragma unroll
+      for (int a = 0; a < kArrays; ++a)
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+#pragma unroll
+            for (int side = 0; side < (V == 1 ? 1 : 2); ++side) {
+              const uint32_t src = ring + slot * kBatch + ((a * G + u) * I + i) * 2 * kPiece * 32 + side * kOther;
+              uint32_t* to = raw[a][u][i].w + side * kPiece / 4;
+              if constexpr (V == 1 || kPiece == 8)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(to[0]), "=r"(to[1]) : "r"(src) : "memory");
+              else
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(to[0]), "=r"(to[1]), "=r"(to[2]), "=r"(to[3])
+                             : "r"(src)
+                             : "memory");
+            }
+#pragma unroll
+      for (int a = 0; a < kArrays; ++a)
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int i = 0; i < I; ++i) unpack_item<T, V>(z[a][u][i], raw[a][u][i]);
+    } else {
+#pragma unroll
+      for (int a = 0; a < kArrays; ++a)
+#pragma unroll
+        for (int u = 0; u < G; ++u)
+#pragma unroll
+          for (int i = 0; i < I; ++i) unpack_item<T, V>(z[a][u][i], next[a][u][i]);
+    }
+    ask(p, place, units, warps, per_warp, sub);
+  }
+};
 
 template <int V, int I, bool INTER>
 __device__ __forceinline__ void load_gain(float2 (&g)[I][V], const float* gain, const Place<V, I, INTER>& at) {
@@ -216,28 +362,34 @@ __device__ __forceinline__ void load_gain(float2 (&g)[I][V], const float* gain, 
     }
 }
 
+// Batches of rows in shared memory, and groups in a batch, of aligned fours; one group through registers of single pairs.
+template <typename T, int V> constexpr int kGroups = V > 1 ? 4 : sizeof(T) == 4 ? 2 : 1;
+template <typename T, int V> constexpr int kGradGroups = V > 1 ? 2 : sizeof(T) == 4 ? 2 : 1;
+constexpr int kStages = 2, kGradStages = 2;
+
 // Work of one warp: units of a token's head groups. A group is the 32 / lanes heads that a warp holds at once; groups
 // of queries come before those of keys, and part k of `parts` takes every parts-th of them.
 template <typename T, int V, int I, bool INTER>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p) {
+  constexpr int G = kGroups<T, V>;
+  extern __shared__ __align__(16) uint8_t smem[];
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, sub = lane / p.lanes, per_warp = 32 / p.lanes;
   const Place<V, I, INTER> at(p, lane % p.lanes);
   ptx::griddep_wait();
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); unit < p.n * p.parts; unit += warps) {
-    const int64_t token = unit / p.parts;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, units = p.n * p.parts;
+  int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  Rows<T, V, I, INTER, G, kStages, 1> rows(p, at, smem, unit, units, warps, per_warp, sub);
+  for (; unit < units; unit += warps) {
+    const int64_t token = p.parts == 1 ? unit : unit / p.parts;
     const int part = static_cast<int>(unit - token * p.parts);
     float c[I * V], s[I * V];
     at.turns(p, token, c, s);
-    int before = 0;  // groups before this tensor's
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int heads = p.heads[w], groups = (heads + per_warp - 1) / per_warp;
-      int first = (part - before) % p.parts;
-      if (first < 0) first += p.parts;
-      before += groups;
-      if (first >= groups) continue;
+      const int heads = p.heads[w], first = first_group(p, w, part, per_warp), step = p.parts * per_warp;
+      int h = first * per_warp + sub;
+      if (first * per_warp >= heads) continue;
       // y = rho (x gain cos + x' gain' sin), with the sign of the pair's end: both products' factors once per token.
       float2 g[I][V], along[I][V], across[I][V];
       load_gain<V, I, INTER>(g, p.gain[w], at);
@@ -251,39 +403,42 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
           across[i][k] = make_float2(other.x * (first_end<V, INTER>(2 * k) ? -s[m0] : s[m0]),
                                      other.y * (first_end<V, INTER>(2 * k + 1) ? -s[m1] : s[m1]));
         }
-      const int64_t step = static_cast<int64_t>(p.parts) * per_warp, h0 = first * per_warp + sub;
-      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w] + h0 * p.x_head[w];
-      T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h0 * p.y_head[w];
-      const int64_t step_x = step * p.x_head[w], step_y = step * p.y_head[w];
-      Raw<T, V> next[I];
-      load_group<T, V, I, INTER>(next, x, at, h0 < heads, p.wide);
-      int h = static_cast<int>(h0);
-      for (int group = first; group < groups; group += p.parts) {
-        const bool ok = h < heads;
-        h += static_cast<int>(step);
-        x += step_x;
-        float2 z[I][V];
-#pragma unroll
-        for (int i = 0; i < I; ++i) unpack_item<T, V>(z[i], next[i]);
-        if (group + p.parts < groups) load_group<T, V, I, INTER>(next, x, at, h < heads, p.wide);
-        float rho = 1.f;
+      T* y = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h * p.y_head[w];
+      const int64_t step_y = step * p.y_head[w];
+      for (int head = first * per_warp; head < heads; head += G * step) {
+        float2 z[1][G][I][V];
+        rows.take(z, p, at, units, warps, per_warp, sub);
+        float rho[G];
         if (p.norm) {
-          float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < I; ++i)
+          for (int u = 0; u < G; ++u) {
+            float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < V; ++k) sq = fma2(z[i][k], z[i][k], sq);
-          rho = rsqrtf(fmaf(sum_lanes(sq.x + sq.y, p.lanes), p.inv_dim, p.eps));
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+              for (int k = 0; k < V; ++k) sq = fma2(z[0][u][i][k], z[0][u][i][k], sq);
+            rho[u] = sq.x + sq.y;
+          }
+          sum_lanes(rho, p.lanes);
+#pragma unroll
+          for (int u = 0; u < G; ++u) rho[u] = rsqrtf(fmaf(rho[u], p.inv_dim, p.eps));
         }
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-          float2 out[V];
+        for (int u = 0; u < G; ++u) {
+          const bool ok = h + u * step < heads;
 #pragma unroll
-          for (int k = 0; k < V; ++k)
-            out[k] = mul2(fma2(z[i][k], along[i][k], mul2(partner<V, INTER>(z[i], k), across[i][k])), both(rho));
-          if (ok && at.live[i]) store_item<T, V, INTER>(y, at.lo[i], at.hi[i], p.wide, out);
+          for (int i = 0; i < I; ++i) {
+            float2 out[V];
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              out[k] = fma2(z[0][u][i][k], along[i][k], mul2(partner<V, INTER>(z[0][u][i], k), across[i][k]));
+              if (p.norm) out[k] = mul2(out[k], both(rho[u]));
+            }
+            if (ok && at.live[i]) store_item<T, V, INTER>(y + u * step_y, at.lo[i], at.hi[i], p.wide, out);
+          }
         }
-        y += step_y;
+        h += G * step;
+        y += G * step_y;
       }
     }
   }
@@ -291,27 +446,28 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
 // y holds dx and x the norm's input; dy the gradient that arrives.
 template <typename T, int V, int I, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_constant__ RotaryLaunch p) {
-  extern __shared__ float part_sums[];  // 2 x dim of each warp
+__global__ void __launch_bounds__(kThreads, 2) rotary_grad_kernel(const __grid_constant__ RotaryLaunch p) {
+  constexpr int G = kGradGroups<T, V>;
+  extern __shared__ __align__(16) uint8_t smem[];
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / p.lanes, per_warp = 32 / p.lanes;
   const Place<V, I, INTER> at(p, lane % p.lanes);
   ptx::griddep_wait();
   float2 sums[2][I][V] = {};
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < p.n * p.parts; unit += warps) {
-    const int64_t token = unit / p.parts;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps, units = p.n * p.parts;
+  int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  using Stream = Rows<T, V, I, INTER, G, kGradStages, 2>;
+  Stream rows(p, at, smem, unit, units, warps, per_warp, sub);
+  for (; unit < units; unit += warps) {
+    const int64_t token = p.parts == 1 ? unit : unit / p.parts;
     const int part = static_cast<int>(unit - token * p.parts);
     float c[I * V], s[I * V];
     at.turns(p, token, c, s);
-    int before = 0;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-      const int heads = p.heads[w], groups = (heads + per_warp - 1) / per_warp;
-      int first = (part - before) % p.parts;
-      if (first < 0) first += p.parts;
-      before += groups;
-      if (first >= groups) continue;
+      const int heads = p.heads[w], first = first_group(p, w, part, per_warp), step = p.parts * per_warp;
+      int h = first * per_warp + sub;
+      if (first * per_warp >= heads) continue;
       float2 g[I][V], cos2[I][V], sin2[I][V];
       load_gain<V, I, INTER>(g, p.gain[w], at);
 #pragma unroll
@@ -322,58 +478,61 @@ __global__ void __launch_bounds__(kThreads) rotary_grad_kernel(const __grid_cons
           cos2[i][k] = make_float2(c[m0], c[m1]);
           sin2[i][k] = make_float2(first_end<V, INTER>(2 * k) ? s[m0] : -s[m0], first_end<V, INTER>(2 * k + 1) ? s[m1] : -s[m1]);
         }
-      const int64_t step = static_cast<int64_t>(p.parts) * per_warp, h0 = first * per_warp + sub;
-      const T* dy = static_cast<const T*>(p.dy[w]) + token * p.dy_token[w] + h0 * p.dy_head[w];
-      const T* x = static_cast<const T*>(p.x[w]) + token * p.x_token[w] + h0 * p.x_head[w];
-      T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h0 * p.y_head[w];
-      const int64_t step_dy = step * p.dy_head[w], step_x = step * p.x_head[w], step_dx = step * p.y_head[w];
-      Raw<T, V> next_d[I], next_x[I];
-      load_group<T, V, I, INTER>(next_d, dy, at, h0 < heads, p.wide);
-      load_group<T, V, I, INTER>(next_x, x, at, p.norm && h0 < heads, p.wide);
-      int h = static_cast<int>(h0);
-      for (int group = first; group < groups; group += p.parts) {
-        const bool ok = h < heads;
-        h += static_cast<int>(step);
-        dy += step_dy, x += step_x;
-        float2 in[I][V], z[I][V], d[I][V];
+      T* dx = static_cast<T*>(p.y[w]) + token * p.y_token[w] + h * p.y_head[w];
+      const int64_t step_dx = step * p.y_head[w];
+      for (int head = first * per_warp; head < heads; head += G * step) {
+        float2 in[2][G][I][V], d[G][I][V];
+        rows.take(in, p, at, units, warps, per_warp, sub);
+        auto& z = in[1];
 #pragma unroll
-        for (int i = 0; i < I; ++i) unpack_item<T, V>(in[i], next_d[i]), unpack_item<T, V>(z[i], next_x[i]);
-        if (group + p.parts < groups) {
-          load_group<T, V, I, INTER>(next_d, dy, at, h < heads, p.wide);
-          load_group<T, V, I, INTER>(next_x, x, at, p.norm && h < heads, p.wide);
-        }
+        for (int u = 0; u < G; ++u)
 #pragma unroll
-        for (int i = 0; i < I; ++i)
+          for (int i = 0; i < I; ++i)
 #pragma unroll
-          for (int k = 0; k < V; ++k) d[i][k] = fma2(in[i][k], cos2[i][k], mul2(partner<V, INTER>(in[i], k), sin2[i][k]));
+            for (int k = 0; k < V; ++k)
+              d[u][i][k] = fma2(in[0][u][i][k], cos2[i][k], mul2(partner<V, INTER>(in[0][u][i], k), sin2[i][k]));
         if (p.norm) {
-          float2 sq = make_float2(0.f, 0.f), along = sq;
+          float rho[2 * G];  // the sums of squares; those of dn . x
 #pragma unroll
-          for (int i = 0; i < I; ++i)
+          for (int u = 0; u < G; ++u) {
+            float2 sq = make_float2(0.f, 0.f), along = sq;
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              sq = fma2(z[i][k], z[i][k], sq);
-              along = fma2(mul2(d[i][k], g[i][k]), z[i][k], along);
-            }
-          const float rho = rsqrtf(fmaf(sum_lanes(sq.x + sq.y, p.lanes), p.inv_dim, p.eps));
-          const float back = -rho * rho * (sum_lanes(along.x + along.y, p.lanes) * p.inv_dim);
+            for (int i = 0; i < I; ++i)
 #pragma unroll
-          for (int i = 0; i < I; ++i)
+              for (int k = 0; k < V; ++k) {
+                sq = fma2(z[u][i][k], z[u][i][k], sq);
+                along = fma2(mul2(d[u][i][k], g[i][k]), z[u][i][k], along);
+              }
+            rho[u] = sq.x + sq.y, rho[G + u] = along.x + along.y;
+          }
+          sum_lanes(rho, p.lanes);
 #pragma unroll
-            for (int k = 0; k < V; ++k) {
-              const float2 hat = mul2(z[i][k], both(rho));
-              sums[w][i][k] = fma2(d[i][k], hat, sums[w][i][k]);
-              d[i][k] = fma2(hat, both(back), mul2(mul2(d[i][k], g[i][k]), both(rho)));
-            }
+          for (int u = 0; u < G; ++u) {
+            const float r = rsqrtf(fmaf(rho[u], p.inv_dim, p.eps)), back = -r * r * (rho[G + u] * p.inv_dim);
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+              for (int k = 0; k < V; ++k) {
+                const float2 hat = mul2(z[u][i][k], both(r));
+                sums[w][i][k] = fma2(d[u][i][k], hat, sums[w][i][k]);
+                d[u][i][k] = fma2(hat, both(back), mul2(mul2(d[u][i][k], g[i][k]), both(r)));
+              }
+          }
         }
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-          if (ok && at.live[i]) store_item<T, V, INTER>(dx, at.lo[i], at.hi[i], p.wide, d[i]);
-        dx += step_dx;
+        for (int u = 0; u < G; ++u) {
+          const bool ok = h + u * step < heads;
+#pragma unroll
+          for (int i = 0; i < I; ++i)
+            if (ok && at.live[i]) store_item<T, V, INTER>(dx + u * step_dx, at.lo[i], at.hi[i], p.wide, d[u][i]);
+        }
+        h += G * step;
+        dx += G * step_dx;
       }
     }
   }
   if (!p.partials) return;
+  float* part_sums = reinterpret_cast<float*>(smem + (Stream::kShared ? kWarps * kGradStages * Stream::kBatch : 0));
   // The warp's heads, then the CTA's warps, in fixed orders; the CTAs' sums are joined by rotary_gain_kernel.
 #pragma unroll
   for (int w = 0; w < 2; ++w)
@@ -447,6 +606,8 @@ cudaError_t set_grid(RotaryLaunch& p, K* kernel, int (&known)[kMaxDevices], size
   if (e != cudaSuccess) return e;
   if (dev < kMaxDevices) per_sm = known[dev];
   if (per_sm == 0) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) known[dev] = per_sm;
@@ -465,12 +626,16 @@ cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
   static int known[2][kMaxDevices];
   int64_t ctas = 0;
   if (!p.grad) {
-    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, known[0], 0, sms, &ctas);
+    using Stream = Rows<T, V, I, INTER, kGroups<T, V>, kStages, 1>;
+    constexpr size_t smem = Stream::kShared ? kWarps * kStages * Stream::kBatch : 0;
+    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, known[0], smem, sms, &ctas);
     if (e != cudaSuccess) return e;
-    return row::launch(rotary_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, 0, stream, p);
+    return row::launch(rotary_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
   }
-  const size_t smem = sizeof(float) * 2 * p.dim * kWarps;
-  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, known[1], sizeof(float) * 2 * 256 * kWarps, sms, &ctas);
+  using Stream = Rows<T, V, I, INTER, kGradGroups<T, V>, kGradStages, 2>;
+  constexpr size_t ring = Stream::kShared ? kWarps * kGradStages * Stream::kBatch : 0;
+  const size_t smem = ring + sizeof(float) * 2 * p.dim * kWarps;
+  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, known[1], ring + sizeof(float) * 2 * 256 * kWarps, sms, &ctas);
   if (e != cudaSuccess) return e;
   p.npartials = static_cast<int>(ctas);
   if (p.planning) return cudaSuccess;
