@@ -1,6 +1,7 @@
 """The token operators of libdmuon: what a language model's training step runs beside its matrix products, on
-the parameters that AdamW updates, and between them. Argument marshalling only: each function is one C call, enqueued on the current
-CUDA stream of its tensors' device, which is the same for all of them; all are reachable as attributes of the package.
+the parameters that AdamW updates, and between them. Argument marshalling only: each function is one C call, enqueued
+on the current CUDA stream of its tensors' device, which is the same for all of them; all are reachable as attributes of
+the package.
 
     y = dm.embedding(table, ids, scale=64.0)                       # lookup
     grad = dm.embedding_grad(dy, ids, rows=table.shape[0])         # its dense fp32 gradient
@@ -326,6 +327,8 @@ def _head_array(t, name, dev, shape, dtype):
 
 
 def _new(t):
+    if t.is_contiguous():  # a quarter less time than by shape, type and device
+        return torch.empty_like(t)
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
@@ -537,8 +540,8 @@ def token_stats(logits, targets=None, top=0, temperature=1.0, stream=None):
     n, vocab, ld = _layout(logits, "logits")
     ptr, size = (None, 8) if targets is None else _ids(targets, "targets", dev, n)
     shape, at = logits.shape[:-1] if targets is None else targets.shape, logits.device
-    logp = None if targets is None else torch.empty(shape, dtype=torch.float32, device=at)
     entropy = torch.empty(shape, dtype=torch.float32, device=at)
+    logp = None if targets is None else torch.empty_like(entropy)
     top_logp = torch.empty(shape + (max(top, 0),), dtype=torch.float32, device=at)
     top_ids = torch.empty(shape + (max(top, 0),), dtype=torch.int64, device=at)
     norm = torch.empty(shape + (2,), dtype=torch.float32, device=at)

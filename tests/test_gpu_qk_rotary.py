@@ -133,6 +133,42 @@ def test_in_place_shapes_and_frequencies(dm):
     dm.check_status()
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("layout", ["plain", "qkv", "odd"])
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("hq, hk, dim, rd", [(5, 1, 64, 64), (9, 3, 78, 20), (1, 2, 128, 64), (3, 0, 250, 250), (21, 4, 32, 16)])
+def test_more_tokens_than_warps(dm, hq, hk, dim, rd, dt, layout, in_place):
+    """Warps that go through several tokens, over heads that do not fill their batches: every token's rows are those of a
+    call with few tokens, bit by bit, and the gains' sums those of the formula."""
+    n, few = 9001, 37
+    inter = dim == 78
+    q, k = heads_like(n, hq, dim, layout, dt, 1), heads_like(n, hk, dim, layout, dt, 2) if hk else None
+    qg, kg = randn((dim,), 3) + 1, randn((dim,), 4) + 1 if hk else None
+    pos = positions_for(n, 1, 100000, 5, torch.int64)
+    options = dict(rotary_dim=rd, interleaved=inter)
+    dq_out, dk_out = heads_like(n, hq, dim, layout, dt, 6), heads_like(n, hk, dim, layout, dt, 7) if hk else None
+    picks = [slice(0, few), slice(4000, 4000 + few), slice(n - few, n)]
+    part = lambda t, at: None if t is None else t[at]
+    small = [dm.qk_norm_rotary(q[at], part(k, at), pos[at], qg, kg, **options) for at in picks]
+    small_grads = [dm.qk_norm_rotary_grad(dq_out[at], part(dk_out, at), q[at], part(k, at), pos[at], qg, kg, **options)
+                   for at in picks]
+    into = dict(dq=dq_out, dk=dk_out) if in_place else {}
+    wants = []  # the gains' gradients, and what their terms add up to without their signs
+    angles = ref.turns(pos.cpu().numpy(), rd, 10000.0, None, None)
+    for t, d, g in ((q, dq_out, qg), (k, dk_out, kg)):
+        if t is not None:
+            wants.append(ref.qk_norm_rotary_grad(f64(d), f64(t), f64(g), angles, rd, inter, True, 1e-6)[1::2])
+    grads = dm.qk_norm_rotary_grad(dq_out, dk_out, q, k, pos, qg, kg, **options, **into)
+    into = dict(q_out=q, k_out=k) if in_place else {}
+    out = dm.qk_norm_rotary(q, k, pos, qg, kg, **options, **into)
+    for at, o, g in zip(picks, small, small_grads):
+        for a, b in list(zip(out, o)) + list(zip(grads[:2], g[:2])):
+            assert (a is None and b is None) or torch.equal(a[at], b)
+    for got, heads, (want, size) in zip(grads[2:], (hq, hk), wants):
+        within(got, want, (40 + n * heads) * U * size)
+    dm.check_status()
+
+
 def test_far_positions_are_as_exact_as_near_ones(dm):
     """A revolution of every frequency more or less, at positions up to 2^31: frequencies of k / 4096 revolutions, whose
     angles repeat every 4096 positions."""
