@@ -327,8 +327,6 @@ def _head_array(t, name, dev, shape, dtype):
 
 
 def _new(t):
-    if t.is_contiguous():  # a quarter less time than by shape, type and device
-        return torch.empty_like(t)
     return torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
@@ -540,8 +538,8 @@ def token_stats(logits, targets=None, top=0, temperature=1.0, stream=None):
     n, vocab, ld = _layout(logits, "logits")
     ptr, size = (None, 8) if targets is None else _ids(targets, "targets", dev, n)
     shape, at = logits.shape[:-1] if targets is None else targets.shape, logits.device
+    logp = None if targets is None else torch.empty(shape, dtype=torch.float32, device=at)
     entropy = torch.empty(shape, dtype=torch.float32, device=at)
-    logp = None if targets is None else torch.empty_like(entropy)
     top_logp = torch.empty(shape + (max(top, 0),), dtype=torch.float32, device=at)
     top_ids = torch.empty(shape + (max(top, 0),), dtype=torch.int64, device=at)
     norm = torch.empty(shape + (2,), dtype=torch.float32, device=at)
