@@ -406,7 +406,8 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int kv = blockIdx.x % p.kv_heads;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -421,7 +422,8 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
   griddep_wait();
   const int group = p.heads / p.kv_heads;
   if (warp == 9) {
-    const Place found = find_place(p, blockIdx.x / p.kv_heads, [&](int64_t len) { return ((len + kTile - 1) / kTile * group + 1) / 2; });
+    const Place found = find_place(p, blockIdx.x / p.kv_heads,
+                                   [&](int64_t len) { return ((len + kTile - 1) / kTile * group + 1) / 2; });
     if (lane == 0) place = found;
     if (found.length > 0) tmem_alloc(tmem_slot, kCols);
   }
@@ -712,7 +714,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dq_kernel(cons
   float* row_delta = reinterpret_cast<float*>(q_full + 32);
   __shared__ Place place;
 
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int head = blockIdx.x % p.heads, kv = head / (p.heads / p.kv_heads);
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
@@ -971,7 +974,8 @@ __global__ void __launch_bounds__(Bwd<kD>::kThreads, 1) attention_dkv_kernel(con
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   __shared__ Place place;
 
-  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31, kv = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int kv = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
   griddep_launch_dependents();
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);

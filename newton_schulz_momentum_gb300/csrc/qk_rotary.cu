@@ -222,16 +222,19 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool o
 template <typename T, int V, int I, bool INTER, int G, int kStages, int kArrays>
 struct Rows {
   static constexpr bool kShared = V > 1 || sizeof(T) == 4;
-  static constexpr int kPiece = V * sizeof(T);                       // of a lane's item, twice
-  static constexpr int kOther = V == 1 ? 4 : kPiece * 32;            // from a lane's lower piece to its upper one
-  static constexpr int kBatch = kArrays * G * I * 2 * kPiece * 32;   // bytes of a warp's batch
+  static constexpr int kPiece = V * sizeof(T);                      // of a lane's item, twice
+  static constexpr int kOther = V == 1 ? 4 : kPiece * 32;           // from a lane's lower piece to its upper one
+  static constexpr int kBatch = kArrays * G * I * 2 * kPiece * 32;  // bytes of a warp's batch
   int64_t unit;
-  int w, group, h, slot, taken;
+  int w, group, h, slot;
   const T* at[kArrays];
   uint32_t ring;
   Raw<T, V> next[kShared ? 1 : kArrays][kShared ? 1 : G][I];
 
-  __device__ __forceinline__ static const void* base(const RotaryLaunch& p, int a, int w) { return a ? p.x[w] : kArrays > 1 ? p.dy[w] : p.x[w]; }
+  // Array 0 of two is dy; x is the other, or the only one.
+  __device__ __forceinline__ static const void* base(const RotaryLaunch& p, int a, int w) {
+    return a || kArrays == 1 ? p.x[w] : p.dy[w];
+  }
   __device__ __forceinline__ static int64_t token_stride(const RotaryLaunch& p, int a, int w) {
     return a || kArrays == 1 ? p.x_token[w] : p.dy_token[w];
   }
@@ -307,7 +310,7 @@ struct Rows {
   }
   __device__ __forceinline__ Rows(const RotaryLaunch& p, const Place<V, I, INTER>& place, uint8_t* smem, int64_t first_unit,
                                   int64_t units, int64_t warps, int per_warp, int sub)
-      : unit(first_unit), w(0), slot(0), taken(0) {
+      : unit(first_unit), w(0), slot(0) {
     if constexpr (kShared)
       ring = ptx::smem_u32(smem) + (threadIdx.x >> 5) * kStages * kBatch + (threadIdx.x & 31) * (V == 1 ? 8 : kPiece);
     find(p, units, warps, per_warp, sub);

@@ -169,6 +169,23 @@ def test_more_tokens_than_warps(dm, hq, hk, dim, rd, dt, layout, in_place):
     dm.check_status()
 
 
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n", [3, 700, 9001])
+def test_in_place_again_and_again(dm, n, dt):
+    """Calls over their own inputs, each set up while the one before it still runs, read what that one wrote."""
+    q, k = randn((n, 5, 64), 1, dtype=dt), randn((n, 2, 64), 2, dtype=dt)
+    qg, kg = randn((64,), 3) + 1, randn((64,), 4) + 1
+    pos = positions_for(n, 1, 1000, 5, torch.int64)
+    a, b = q, k
+    for _ in range(20):
+        a, b = dm.qk_norm_rotary(a, b, pos, qg, kg)
+        torch.cuda.synchronize()
+    for _ in range(20):
+        dm.qk_norm_rotary(q, k, pos, qg, kg, q_out=q, k_out=k)
+    assert torch.equal(a, q) and torch.equal(b, k)
+    dm.check_status()
+
+
 def test_far_positions_are_as_exact_as_near_ones(dm):
     """A revolution of every frequency more or less, at positions up to 2^31: frequencies of k / 4096 revolutions, whose
     angles repeat every 4096 positions."""
