@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(Fwd<kD>::kThreads, 1) attention_kernel(const _
 // Measured, 32 heads of 128 with 8 key heads, 8192 tokens, causal: 1.31 ms, 1.05 PFLOP/s of the five products that the
 // gradient is made of and 1.47 of the seven that are formed, 0.84 of what a library product sustains for as long on the
 // same chip, whose power limit it then runs at. 37 sequences of 16001 tokens in all, 14 + 2 heads of 64: 242 us, 122 of
-// them dq, half of it CTAs that start and end (2000 of some 4 tiles each); 124 dk and dv.
+// them dq (2002 CTAs of some 4 tiles, 9 us each from the first copy to the last row), 124 dk and dv.
 
 constexpr int kPart = 32;             // columns of a row that a thread has
 constexpr int kRowWarps = 16;
