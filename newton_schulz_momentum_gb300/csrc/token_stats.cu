@@ -491,10 +491,20 @@ cudaError_t launch_type(StatsLaunch& p, int sms, cudaStream_t stream) {
   constexpr int E = 16 / sizeof(T);
   const int64_t granules = (p.vocab + E - 1) / E;
   p.cluster = 1;
-  if (granules <= 256) return launch_stats<T, 1>(p, stream);
-  if (granules <= 2048) return launch_stats<T, 4>(p, stream);
-  // Few rows: several CTAs each, as long as a thread has a batch of granules.
-  while (p.cluster < 8 && p.n * p.cluster * 2 <= 2 * sms && granules >= 2 * p.cluster * 256 * 4) p.cluster *= 2;
+  // An SM holds 4 CTAs of 8 warps, 8 of 4, 32 of one. The widest that has all rows at once; of more rows, by a row's
+  // length: a CTA's joins and barriers weigh more the shorter it is. bf16, us of 1, 4 and 8 warps: 608 rows of 3000 7.6,
+  // 7.2, 6.0, of 16000 21, 12.7, 8.8; 1216 of 1000 6.7, 7.7, 9.8, of 8000 14.1, 11.1, 12.7; 4864 of 1000 11, 22, 34, of
+  // 8000 22, 31, 42, of 16000 43, 43, 55, of 32000 86, 66, 78, of 64000 204, 120, 122, of 128256 415, 240, 223. (Two warps
+  // were never best by more than a few percent.)
+  if (p.n > 4 * sms) {
+    if (granules <= 256 || (granules <= 1024 && p.n > 8 * sms)) return launch_stats<T, 1>(p, stream);
+    if (granules <= 4096) return launch_stats<T, 4>(p, stream);
+  }
+  // Few long rows: several CTAs each, one to an SM, or two CTAs each where that makes two to an SM. bf16, us of clusters of
+  // 1, 2, 4 and 8: 8 rows of 32000 5.7, 6.4, 6.2, 6.4, of 64000 7.9, 7.6, 6.8, 6.5, of 128256 12.6, 9.8, 7.9, 7.1; 38 rows
+  // of 128256 12.6, 11.4, 9.6, 10.1; 152 of 128256 19.7, 15.3, 20.5, 25.
+  if (granules >= 6144)
+    while (p.cluster < 8 && p.n * p.cluster * 2 <= (p.cluster == 1 ? 2 : 1) * sms) p.cluster *= 2;
   return launch_stats<T, 8>(p, stream);
 }
 
