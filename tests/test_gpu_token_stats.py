@@ -91,6 +91,44 @@ def test_token_stats(dm, n, vocab, top, temp, dt, layout):
     dm.check_status()
 
 
+@pytest.mark.parametrize("layout", ["plain", "offset"])
+@pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
+@pytest.mark.parametrize("n, vocab, top", [(640, 200, 5), (700, 2600, 3), (1300, 999, 32), (1300, 5003, 5), (2500, 1, 1),
+                                           (2500, 3001, 20), (2500, 9001, 1), (1250, 17000, 2)])
+def test_many_rows(dm, n, vocab, top, dt, layout):
+    """More rows than the widest CTAs hold at once, so that a row has fewer warps: values by the formula for some of them,
+    ids for all, rows that do not count or hold no number, and the gradient."""
+    x = logits_for(n, vocab, dt, layout, vocab > 300, n + vocab)
+    x[5] = float("-inf")
+    x[6, vocab // 2] = float("nan")
+    x[7] = 1.5  # equal logits
+    targets = torch.randint(0, vocab, (n,), generator=torch.Generator().manual_seed(3))
+    targets[8:n:9] = -1
+    on_gpu = targets.cuda()
+    got = dm.token_stats(x, on_gpu, top=top, temperature=1.3)
+    parts = [dm.token_stats(x[i:i + 500], on_gpu[i:i + 500], top=top, temperature=1.3) for i in range(0, n, 500)]
+    assert torch.equal(got.top_ids, torch.cat([part.top_ids for part in parts]))
+    assert got.logp[5:7].isnan().all() and got.entropy[5:7].isnan().all()
+    picks = [0, 1, 2, 3, 4, 7, 8, 9, 17, n // 2, n - 2, n - 1]
+    some, few = torch.tensor(picks).cuda(), [targets[i].item() for i in picks]
+    x64 = f64(x[some])
+    logp, entropy, top_logp, top_ids, norm = ref.token_stats(x64, few, top, 1.3)
+    off = 8 * U * (reach(x64, 1.3) + np.log(vocab)) + sum_off(vocab)
+    assert got.top_ids[some].tolist() == top_ids.tolist()
+    finite = np.isfinite(logp)
+    within(got.logp[some][torch.from_numpy(finite).cuda()], logp[finite], (off + 8 * U * np.abs(logp))[finite])
+    within(got.entropy[some], entropy, 2 * off + 2 * (sum_off(vocab) + 8 * U * reach(x64, 1.3)) * entropy)
+    within(got.norm[some][:, 1], norm[:, 1], (sum_off(vocab) + 8 * U * reach(x64, 1.3)) * norm[:, 1])
+    g, h = randn((n,), 5), randn((n,), 6, 0.3)
+    d = dm.token_stats_grad(x, on_gpu, got.norm, got.entropy, g, h, temperature=1.3)
+    want, size = ref.token_stats_grad(x64, few, f64(g[some]), f64(h[some]), 1.3)
+    rel = 3 * off[:, None] + 3 * sum_off(vocab) + 8 * U * reach(x64, 1.3)[:, None] + 16 * U
+    more = np.exp(np.where(np.isfinite(x64), ref.log_softmax(x64, 1.3), -np.inf)) * np.abs(f64(h[some]))[:, None] / 1.3
+    within(d[some], want, rel * size + 3 * off[:, None] * more + ROUND[dt] * np.abs(want))
+    assert not d[targets.cuda() < 0].any()
+    dm.check_status()
+
+
 @pytest.mark.parametrize("dt", TYPES, ids=TYPE_IDS)
 @pytest.mark.parametrize("vocab", [40, 1111, 5000, 40000])
 def test_equal_logits(dm, vocab, dt):
