@@ -380,9 +380,8 @@ constexpr int kStages = 2, kGradStages = 2;
 
 // Work of one warp: units of a token's head groups. A group is the 32 / lanes heads that a warp holds at once; groups
 // of queries come before those of keys, and part k of `parts` takes every parts-th of them.
-template <typename T, int V, int I, bool INTER>
+template <typename T, int V, int I, bool INTER, int G>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch p) {
-  constexpr int G = kGroups<T, V>;
   extern __shared__ __align__(16) uint8_t smem[];
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, sub = lane / p.lanes, per_warp = 32 / p.lanes;
@@ -456,9 +455,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 }
 
 // y holds dx and x the norm's input; dy the gradient that arrives.
-template <typename T, int V, int I, bool INTER>
+template <typename T, int V, int I, bool INTER, int G>
 __global__ void __launch_bounds__(kThreads, 2) rotary_grad_kernel(const __grid_constant__ RotaryLaunch p) {
-  constexpr int G = kGradGroups<T, V>;
   extern __shared__ __align__(16) uint8_t smem[];
   ptx::griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / p.lanes, per_warp = 32 / p.lanes;
@@ -632,27 +630,46 @@ cudaError_t set_grid(RotaryLaunch& p, K* kernel, int (&known)[kMaxDevices], size
   return cudaSuccess;
 }
 
-template <typename T, int V, int I, bool INTER>
-cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
-  static int known[2][kMaxDevices];
+template <typename T, int V, int I, bool INTER, int G>
+cudaError_t launch_forward(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  static int known[kMaxDevices];
   int64_t ctas = 0;
-  if (!p.grad) {
-    using Stream = Rows<T, V, I, INTER, kGroups<T, V>, kStages, 1>;
-    constexpr size_t smem = Stream::kShared ? kWarps * kStages * Stream::kBatch : 0;
-    const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER>, known[0], smem, sms, &ctas);
-    if (e != cudaSuccess) return e;
-    return row::launch(rotary_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
-  }
-  using Stream = Rows<T, V, I, INTER, kGradGroups<T, V>, kGradStages, 2>;
+  using Stream = Rows<T, V, I, INTER, G, kStages, 1>;
+  constexpr size_t smem = Stream::kShared ? kWarps * kStages * Stream::kBatch : 0;
+  const cudaError_t e = set_grid(p, rotary_kernel<T, V, I, INTER, G>, known, smem, sms, &ctas);
+  if (e != cudaSuccess) return e;
+  return row::launch(rotary_kernel<T, V, I, INTER, G>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
+}
+
+template <typename T, int V, int I, bool INTER, int G>
+cudaError_t launch_backward(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  static int known[kMaxDevices];
+  int64_t ctas = 0;
+  using Stream = Rows<T, V, I, INTER, G, kGradStages, 2>;
   constexpr size_t ring = Stream::kShared ? kWarps * kGradStages * Stream::kBatch : 0;
   const size_t smem = ring + sizeof(float) * 2 * p.dim * kWarps;
-  cudaError_t e = set_grid(p, rotary_grad_kernel<T, V, I, INTER>, known[1], ring + sizeof(float) * 2 * 256 * kWarps, sms, &ctas);
+  cudaError_t e =
+      set_grid(p, rotary_grad_kernel<T, V, I, INTER, G>, known, ring + sizeof(float) * 2 * 256 * kWarps, sms, &ctas);
   if (e != cudaSuccess) return e;
   p.npartials = static_cast<int>(ctas);
   if (p.planning) return cudaSuccess;
-  e = row::launch(rotary_grad_kernel<T, V, I, INTER>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
+  e = row::launch(rotary_grad_kernel<T, V, I, INTER, G>, dim3(static_cast<unsigned>(ctas)), kThreads, smem, stream, p);
   if (e != cudaSuccess || !p.partials) return e;
   return row::launch(rotary_gain_kernel, dim3(static_cast<unsigned>((2 * p.dim + 31) / 32)), kJoinThreads, 0, stream, p);
+}
+
+template <typename T, int V, int I, bool INTER>
+cudaError_t launch_as(RotaryLaunch& p, int sms, cudaStream_t stream) {
+  // Up to three groups of a tensor's heads that a warp has of a token: batches of one, which leave none of a batch empty.
+  // 32768 tokens, bf16, us in batches of one and of more: 2 + 1 heads of 128 30.5, 46.3 (backward 40, 50), 6 + 2 45.9, 50.8
+  // (59, 66), 8 + 2 52.1, 51.7 (67, 67), 16 + 4 66, 56 (88, 79); 200 tokens of 32 + 8 5.0, 5.9 (9.3, 10.2).
+  const int per_warp = 32 / p.lanes, most = (std::max(p.heads[0], p.heads[1]) + per_warp - 1) / per_warp;
+  const int64_t warps = 16 * static_cast<int64_t>(sms), each = most * std::min(p.n, warps) / warps;
+  if (!p.grad)
+    return each <= 3 ? launch_forward<T, V, I, INTER, 1>(p, sms, stream)
+                     : launch_forward<T, V, I, INTER, kGroups<T, V>>(p, sms, stream);
+  return each <= 3 ? launch_backward<T, V, I, INTER, 1>(p, sms, stream)
+                   : launch_backward<T, V, I, INTER, kGradGroups<T, V>>(p, sms, stream);
 }
 
 template <typename T, bool INTER>
