@@ -20,7 +20,7 @@
 // What bounds it is memory, as far as enough of it is asked for ahead. Measured, 16384 tokens, 32 + 8 heads of 128 bf16
 // columns, three axes: forward 58 us, 5.8 TB/s (0.86 of a copy's rate); backward 93 us, 5.4 TB/s (0.81), where the sums
 // of the gains' gradients leave registers for 16 warps an SM. 8191 tokens, 9 + 3 heads of 78 fp32 columns of which 20
-// turn, backward: 38 us, of which the kernel is 27, instructions of 39 pairs on 16 lanes.
+// turn, backward: 35 to 39 us, of which the kernel is 27, instructions of 39 pairs on 16 lanes.
 #include <algorithm>
 
 #include "row_ops.h"
